@@ -32,13 +32,13 @@ def _case(name, op, **kw):
 def listed():
     return [
         # a decode step of 64 requests: every request gets one slot, every 16th a new block
-        _case("tables, 64 decoding", "tables", B=64, lo=16, hi=4096, nlo=1, nhi=1),
+        _case("tables 64 decoding", "tables", B=64, lo=16, hi=4096, nlo=1, nhi=1),
         # a large engine step: 4096 request slots, most decode, some admit prompts or finish
-        _case("tables, 4096 mixed", "tables", B=4096, lo=0, hi=4096, nlo=-1, nhi=2048),
+        _case("tables 4096 mixed", "tables", B=4096, lo=0, hi=4096, nlo=-1, nhi=2048),
         # the decode step's K/V rows of a 2-kv-head model into its FP8 cache
-        _case("append fp8, 64 decoding", "append", B=64, hkv=2, lo=16, hi=4096, nlo=1, nhi=1),
+        _case("append fp8 64 decoding", "append", B=64, hkv=2, lo=16, hi=4096, nlo=1, nhi=1),
         # sixteen prompts' K/V rows written in one call
-        _case("append fp8, 16 prompts", "append", B=16, hkv=8, lo=0, hi=0, nlo=3500, nhi=4500),
+        _case("append fp8 16 prompts", "append", B=16, hkv=8, lo=0, hi=0, nlo=3500, nhi=4500),
         # one decode layer of a 32/8-head model over the FP8 cache, ~4000 tokens a request
         _case("decode fp8, 32 x 4000", "decode_f8", B=32, hq=32, hkv=8, lo=3500, hi=4500),
         # four very long contexts: the split over the keys is all the parallelism there is
@@ -51,11 +51,11 @@ def listed():
         # two short requests of a small model: launch latency
         _case("decode rules, 2 x 200", "decode", B=2, hq=8, hkv=8, d=64, lo=100, hi=256, alibi=True),
         # a 4096-token chunk that ends a 16384-token prompt, capped scores
-        _case("prefill, chunk of 16384", "prefill", B=1, hq=32, hkv=8, lo=16384, hi=16384, nlo=4096, nhi=4096, cap=50.0),
+        _case("prefill chunk of 16384", "prefill", B=1, hq=32, hkv=8, lo=16384, hi=16384, nlo=4096, nhi=4096, cap=50.0),
         # a mixed step: most requests decode one token, some bring chunks; packed documents after a prefix
-        _case("prefill, mixed 24", "prefill", B=24, hq=12, hkv=2, lo=16, hi=4096, nlo=1, nhi=1024, docs=True, prefix=64),
+        _case("prefill mixed 24", "prefill", B=24, hq=12, hkv=2, lo=16, hi=4096, nlo=1, nhi=1024, docs=True, prefix=64),
         # whole prompts of a model with 64-wide heads, distance bias and a sliding window
-        _case("prefill, 4 prompts d64", "prefill", B=4, hq=8, hkv=8, d=64, lo=2001, hi=3001, nlo=3001, nhi=3001,
+        _case("prefill 4 prompts d64", "prefill", B=4, hq=8, hkv=8, d=64, lo=2001, hi=3001, nlo=3001, nhi=3001,
               alibi=True, window=1000),
     ]
 
