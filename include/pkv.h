@@ -69,7 +69,9 @@ extern "C" {
 #define PKV_DEV_WAIT_TIMEOUT 5      /* an mbarrier wait exceeded its bound (kernel gave up) */
 #define PKV_DEV_BAD_SCORE 6         /* NaN score given to top-k selection */
 #define PKV_DEV_DIRTY_WORKSPACE 7   /* decode workspace counters were not zero at the call */
-#define PKV_DEV_BAD_VALUE 8         /* non-finite K/V element given to the INT8 append */
+#define PKV_DEV_BAD_VALUE 8         /* non-finite K/V element given to the INT8 or FP8 append */
+#define PKV_DEV_NO_BLOCKS 9         /* pkv_step.h: the free stack holds too few blocks, or overflows */
+#define PKV_DEV_BAD_QUERY_RANGE 10  /* pkv_step.h: new tokens or packed query rows out of range */
 
 /*
  * Flags of the decode calls (their `flags` argument; 0 = none).

@@ -1,6 +1,6 @@
 """Paged KV-cache decode attention for GB300 (sm_103a).
 
-Python binding of libpkv (declared in include/pkv.h).  Each function checks the torch
+Python binding of libpkv (declared in include/pkv.h and include/pkv_step.h).  Each function checks the torch
 tensors it is given, builds the C shape record and calls the C-ABI entry point of the same
 name (``pkv_<name>``) on the current CUDA stream.  All computation happens in the library's
 CUDA kernels; CPU tensors are rejected, there is no fallback path.  PyTorch only provides
@@ -14,6 +14,7 @@ import ctypes
 import torch
 
 from ._lib import PkvDims, PkvError, check, header_constants, header_functions, load
+from .step import kv_append_f8, kv_step_tables
 
 __all__ = [
     "BLOCK_SIZE", "PkvError", "kv_append", "decode_workspace_bytes", "paged_decode_attention",
@@ -26,6 +27,7 @@ __all__ = [
     "prefill_window_scores",
     "paged_decode_attention_scores_q8", "kv_compact_q8", "kv_rolling_admit_q8",
     "paged_decode_attention_append_q8", "sparse_decode_attention_q8",
+    "kv_step_tables", "kv_append_f8",
 ]
 
 BLOCK_SIZE = 16

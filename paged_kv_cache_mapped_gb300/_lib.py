@@ -1,5 +1,5 @@
 """ctypes handle on libpkv.so: loads the in-tree library and declares the C signatures of
-include/pkv.h.  No arithmetic happens here."""
+include/pkv.h and include/pkv_step.h.  No arithmetic happens here."""
 from __future__ import annotations
 
 import ctypes
@@ -10,6 +10,7 @@ import threading
 PKG = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(PKG, "libpkv.so")
 HEADER = os.path.join(os.path.dirname(PKG), "include", "pkv.h")
+STEP_HEADER = os.path.join(os.path.dirname(PKG), "include", "pkv_step.h")
 
 _lock = threading.Lock()
 _lib = None
@@ -27,6 +28,16 @@ class PkvDims(ctypes.Structure):
     ]
 
 
+class PkvScoreRules(ctypes.Structure):
+    _fields_ = [
+        ("softcap", ctypes.c_float),
+        ("window", ctypes.c_int32),
+        ("alibi_slopes", ctypes.c_void_p),
+        ("doc_starts", ctypes.c_void_p),
+        ("prefix_lens", ctypes.c_void_p),
+    ]
+
+
 class PkvError(RuntimeError):
     """A call into libpkv returned a non-zero status."""
 
@@ -36,17 +47,18 @@ class PkvError(RuntimeError):
 
 
 def header_constants() -> dict:
-    """#define NAME value pairs of include/pkv.h (status and device-error codes)."""
+    """#define NAME value pairs of the public headers (status and device-error codes, flags, limits)."""
     out = {}
-    with open(HEADER) as f:
-        for m in re.finditer(r"^#define\s+(PKV_\w+)\s+([-+*() 0-9]+?)\s*(?:/\*.*)?$", f.read(), re.M):
-            out[m.group(1)] = int(eval(m.group(2), {"__builtins__": {}}, {}))  # integer literal arithmetic only
+    for path in (HEADER, STEP_HEADER):
+        with open(path) as f:
+            for m in re.finditer(r"^#define\s+(PKV_\w+)\s+([-+*() 0-9]+?)\s*(?:/\*.*)?$", f.read(), re.M):
+                out[m.group(1)] = int(eval(m.group(2), {"__builtins__": {}}, {}))  # integer literal arithmetic only
     return out
 
 
-def header_functions() -> list:
-    """Names of the functions include/pkv.h declares."""
-    with open(HEADER) as f:
+def header_functions(path: str = HEADER) -> list:
+    """Names of the functions include/pkv.h (or the header at `path`) declares."""
+    with open(path) as f:
         text = f.read()
     return sorted(set(re.findall(r"^\s*(?:const\s+)?\w+\*?\s+\*?(pkv_\w+)\s*\(", text, re.M)))
 
@@ -88,6 +100,8 @@ def load():
             "pkv_kv_select_topk": (I32, [P, P, P, I32, P, I32, I32, I32, D, U32, P, P]),
             "pkv_kv_compact": (I32, [P, P, P, I32, I32, P, P, P, P, P, P, I32, D, U32, P, P]),
             "pkv_paged_decode_attention_fixed_scratch": (I32, [P, P, P, P, P, P, F32, I32, D, P, P]),
+            "pkv_kv_step_tables": (I32, [P, P, P, P, P, P, P, P, P, P, I32, D, P, P]),
+            "pkv_kv_append_f8": (I32, [P, P, P, P, P, P, P, I64, D, P, P]),
             "pkv_read_error": (I32, [P, I32, P]),
             "pkv_device_alias": (I32, [P, ctypes.POINTER(ctypes.c_void_p)]),
             "pkv_status_string": (ctypes.c_char_p, [I32]),

@@ -85,6 +85,7 @@ const DeviceInfo* device_info(int* status) {
     {
       cudaError_t e = kvops_device_setup();
       if (e == cudaSuccess) e = prefill_device_setup();
+      if (e == cudaSuccess) e = step_device_setup();
       if (e != cudaSuccess) {
         cudaGetLastError();
         *status = PKV_ERR_CUDA_BASE + (int)e;
@@ -161,22 +162,6 @@ int encode_window_map(CUtensorMap* map, const void* base, long long rows, int nu
   return r == CUDA_SUCCESS ? PKV_OK : PKV_ERR_ARGUMENT;
 }
 
-bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
-
-int check_dims(const pkv_dims* d, bool need_q_heads) {
-  if (d == nullptr) return PKV_ERR_NULL_POINTER;
-  if (d->block_size != PKV_BLOCK_SIZE) return PKV_ERR_BLOCK_SIZE;
-  if (head_dim_index(d->head_dim) < 0) return PKV_ERR_HEAD_DIM;
-  if (d->batch < 0 || d->num_kv_heads <= 0 || d->num_blocks < 0 || d->max_blocks_per_seq < 0)
-    return PKV_ERR_DIMS;
-  if (need_q_heads) {
-    if (d->num_q_heads <= 0) return PKV_ERR_DIMS;
-    if (d->num_q_heads % d->num_kv_heads != 0) return PKV_ERR_GQA;
-  }
-  return PKV_OK;
-}
-
-int cuda_status(cudaError_t e) { return e == cudaSuccess ? PKV_OK : PKV_ERR_CUDA_BASE + (int)e; }
 
 // Merge warps per output row (log2), from an upper estimate of the partials a row has: one
 // more warp per PKV_MERGE_PARTIALS_PER_WARP partials, at most 8, and no more than the GPU holds
@@ -203,6 +188,29 @@ int merge_warps_log2(const pkv_dims* d, int max_units, long long workers, int mi
 size_t align256(size_t x) { return (x + 255) & ~size_t(255); }
 
 }  // namespace
+
+bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
+
+int check_dims(const pkv_dims* d, bool need_q_heads) {
+  if (d == nullptr) return PKV_ERR_NULL_POINTER;
+  if (d->block_size != PKV_BLOCK_SIZE) return PKV_ERR_BLOCK_SIZE;
+  if (head_dim_index(d->head_dim) < 0) return PKV_ERR_HEAD_DIM;
+  if (d->batch < 0 || d->num_kv_heads <= 0 || d->num_blocks < 0 || d->max_blocks_per_seq < 0)
+    return PKV_ERR_DIMS;
+  if (need_q_heads) {
+    if (d->num_q_heads <= 0) return PKV_ERR_DIMS;
+    if (d->num_q_heads % d->num_kv_heads != 0) return PKV_ERR_GQA;
+  }
+  return PKV_OK;
+}
+
+int cuda_status(cudaError_t e) { return e == cudaSuccess ? PKV_OK : PKV_ERR_CUDA_BASE + (int)e; }
+
+int device_ready() {
+  int st = PKV_OK;
+  (void)device_info(&st);
+  return st;
+}
 
 // Workspace layout of the decode calls (offsets 256-byte aligned):
 //   uint32 ctrl[2] | int32 layout[2B] | float2 part_ml[2 * ranges][G] | float part_o[2 * ranges][G][D]
@@ -765,7 +773,9 @@ const char* pkv_device_error_string(int code) {
     case PKV_DEV_WAIT_TIMEOUT: return "a bounded wait timed out";
     case PKV_DEV_BAD_SCORE: return "NaN score";
     case PKV_DEV_DIRTY_WORKSPACE: return "decode workspace counters were not zero (zero-fill it before first use)";
-    case PKV_DEV_BAD_VALUE: return "non-finite K/V element given to the INT8 append (token skipped)";
+    case PKV_DEV_BAD_VALUE: return "non-finite K/V element given to the INT8 or FP8 append (token skipped)";
+    case PKV_DEV_NO_BLOCKS: return "too few free blocks for the step, or a free count outside the stack";
+    case PKV_DEV_BAD_QUERY_RANGE: return "new tokens or query rows outside the packed batch";
     default: return "unknown device error";
   }
 }

@@ -256,6 +256,31 @@ size_t prefill_lse_smem_bytes(int head_dim, int max_blocks);
 cudaError_t prefill_device_setup();
 cudaError_t launch_prefill(const PrefillArgs& a, int head_dim, bool lse_given, cudaStream_t stream);
 
+// Step tables and the FP8 append (step.cu).
+struct StepArgs {
+  int32_t* block_tables;         // [B, MB]
+  int32_t* context_lens_out;     // [B]
+  int32_t* query_starts;         // [B + 1]
+  long long* slot_mapping;       // [max_tokens]
+  int32_t* positions;            // [max_tokens]
+  int32_t* free_count_out;       // [1]
+  int32_t* free_blocks;          // [NB] the free stack
+  const int32_t* free_count;     // [1]
+  const int32_t* context_lens;   // [B], may be context_lens_out
+  const int32_t* new_tokens;     // [B]
+  int32_t* err;
+  int B, MB, NB, max_tokens;
+};
+constexpr int kMaxStepBatch = 4096;
+cudaError_t step_device_setup();
+cudaError_t launch_step_tables(const StepArgs& a, cudaStream_t stream);
+
+// Host-side checks shared by the entry points (api.cu).
+int check_dims(const struct pkv_dims* d, bool need_q_heads);
+bool aligned16(const void* p);
+int cuda_status(cudaError_t e);
+int device_ready();  // one-time set-up of the current device; a PKV status
+
 // Launches `kernel` with programmatic stream serialisation (it may start before the previous
 // kernel on the stream ends; every kernel of this library waits for it before touching
 // global memory).

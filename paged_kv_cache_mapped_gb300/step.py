@@ -1,0 +1,148 @@
+"""Binding of the serving-step operators (declared in include/pkv_step.h): the step's block tables
+and slots, the FP8 cache with one scale per (block, kv head), and attention with score rules for one
+query token and for many.  As the rest of the package: argument checks and marshalling only, the
+work runs in the library's CUDA kernels on the current stream of the tensors' device."""
+from __future__ import annotations
+
+import ctypes
+import math
+
+import torch
+
+from ._lib import PkvDims, PkvScoreRules, check, header_constants, load
+
+BLOCK_SIZE = 16
+_INPUTS_READY = header_constants()["PKV_DECODE_INPUTS_READY"]
+
+
+def _need(t, name, dtype, ndim, device=None):
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name} must be a torch.Tensor")
+    if t.dtype != dtype:
+        raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
+    if not t.is_cuda:
+        raise ValueError(f"{name} must live on a CUDA device (the library has no CPU path)")
+    if not t.is_contiguous():
+        raise ValueError(f"{name} must be contiguous")
+    if t.dim() != ndim:
+        raise ValueError(f"{name} must have {ndim} dims, got shape {tuple(t.shape)}")
+    if device is not None and t.device != device:
+        raise ValueError(f"{name} is on {t.device}, expected {device}")
+    return t.data_ptr()
+
+
+def _opt(t, name, dtype, ndim, device):
+    return None if t is None else _need(t, name, dtype, ndim, device)
+
+
+def _call(name, device, stream, *args):
+    """Calls pkv_<name>(*args, stream) with `device` current."""
+    fn = getattr(load(), name)
+    if torch.cuda.current_device() == device.index:
+        s = stream if stream is not None else torch.cuda.current_stream(device)
+        check(name, fn(*args, s.cuda_stream))
+    else:
+        with torch.cuda.device(device):
+            s = stream if stream is not None else torch.cuda.current_stream(device)
+            check(name, fn(*args, s.cuda_stream))
+
+
+def _dims(batch, hq, hkv, d, nb, mb):
+    return PkvDims(batch, hq, hkv, d, BLOCK_SIZE, nb, mb)
+
+
+def _give(t, name, shape, dtype, device):
+    """The output `t` after its checks, or a new one."""
+    if t is None:
+        return torch.empty(shape, dtype=dtype, device=device)
+    _need(t, name, dtype, len(shape), device)
+    if tuple(t.shape) != tuple(shape):
+        raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
+    return t
+
+
+def kv_step_tables(block_tables, context_lens, new_tokens, free_blocks, free_count, max_new_tokens, *,
+                   context_lens_out=None, free_count_out=None, query_starts=None, slot_mapping=None, positions=None,
+                   error_word=None, stream=None):
+    """One step's block tables and slots: new_tokens[b] > 0 gives sequence b that many tokens, 0 leaves
+    it, -1 ends it and frees its blocks.  block_tables [B, MB] and the free stack free_blocks [NB]
+    (live: the first free_count [1] entries) are updated in place.  Returns (context_lens_out [B],
+    query_starts [B + 1], slot_mapping [max_new_tokens] int64, positions [max_new_tokens],
+    free_count_out [1]); rows past the step's last token have slot and position -1.  context_lens_out
+    and free_count_out may be the inputs themselves.  All or nothing on a device error (see
+    pkv_kv_step_tables)."""
+    dev = block_tables.device if isinstance(block_tables, torch.Tensor) else None
+    bt = _need(block_tables, "block_tables", torch.int32, 2)
+    lens = _need(context_lens, "context_lens", torch.int32, 1, dev)
+    new = _need(new_tokens, "new_tokens", torch.int32, 1, dev)
+    free = _need(free_blocks, "free_blocks", torch.int32, 1, dev)
+    count = _need(free_count, "free_count", torch.int32, 1, dev)
+    err = _opt(error_word, "error_word", torch.int32, 1, dev)
+    B, mb = block_tables.shape
+    if context_lens.shape[0] != B or new_tokens.shape[0] != B:
+        raise ValueError("context_lens / new_tokens batch differs from block_tables'")
+    if free_count.shape[0] != 1:
+        raise ValueError("free_count must be [1]")
+    T = int(max_new_tokens)
+    if T < 0:
+        raise ValueError("max_new_tokens must not be negative")
+    lens_out = _give(context_lens_out, "context_lens_out", (B,), torch.int32, dev)
+    count_out = _give(free_count_out, "free_count_out", (1,), torch.int32, dev)
+    starts = _give(query_starts, "query_starts", (B + 1,), torch.int32, dev)
+    slots = _give(slot_mapping, "slot_mapping", (T,), torch.int64, dev)
+    pos = _give(positions, "positions", (T,), torch.int32, dev)
+    dims = _dims(B, 1, 1, 128, free_blocks.shape[0], mb)
+    _call("pkv_kv_step_tables", dev, stream, bt, lens_out.data_ptr(), starts.data_ptr(), slots.data_ptr(), pos.data_ptr(),
+          count_out.data_ptr(), free, count, lens, new, T, ctypes.byref(dims), err)
+    return lens_out, starts, slots, pos, count_out
+
+
+def _f8_pools(k_codes, v_codes, k_scales, v_scales):
+    dev = k_codes.device if isinstance(k_codes, torch.Tensor) else None
+    _need(k_codes, "k_codes", torch.float8_e4m3fn, 4)
+    _need(v_codes, "v_codes", torch.float8_e4m3fn, 4, dev)
+    _need(k_scales, "k_scales", torch.float32, 2, dev)
+    _need(v_scales, "v_scales", torch.float32, 2, dev)
+    nb, hkv, bs, d = k_codes.shape
+    if v_codes.shape != k_codes.shape:
+        raise ValueError("k_codes and v_codes shapes differ")
+    if bs != BLOCK_SIZE:
+        raise ValueError(f"pool block size must be {BLOCK_SIZE}")
+    if k_scales.shape != (nb, hkv) or v_scales.shape != (nb, hkv):
+        raise ValueError("scale pools must be [num_blocks, num_kv_heads]")
+    return nb, hkv, d, dev
+
+
+def kv_append_f8(k_codes, v_codes, k_scales, v_scales, k, v, slot_mapping, *, error_word=None, stream=None):
+    """Write k, v [T, Hkv, d] (bf16) into FP8 pools at slot_mapping [T] (int64; < 0 skips): codes
+    [NB, Hkv, 16, d] torch.float8_e4m3fn, one power-of-two fp32 scale per (block, kv head), [NB, Hkv].
+    A block written at offset 0 starts anew; otherwise its scale only grows and its other rows move to
+    it.  The tokens of one block are adjacent in slot_mapping, slots ascending (the order of
+    kv_step_tables)."""
+    nb, hkv, d, dev = _f8_pools(k_codes, v_codes, k_scales, v_scales)
+    kp = _need(k, "k", torch.bfloat16, 3, dev)
+    vp = _need(v, "v", torch.bfloat16, 3, dev)
+    sp = _need(slot_mapping, "slot_mapping", torch.int64, 1, dev)
+    err = _opt(error_word, "error_word", torch.int32, 1, dev)
+    T = slot_mapping.shape[0]
+    if k.shape != (T, hkv, d) or v.shape != (T, hkv, d):
+        raise ValueError("k/v must be [num_tokens, num_kv_heads, head_dim]")
+    dims = _dims(0, 0, hkv, d, nb, 0)
+    _call("pkv_kv_append_f8", dev, stream, k_codes.data_ptr(), v_codes.data_ptr(), k_scales.data_ptr(), v_scales.data_ptr(),
+          kp, vp, sp, T, ctypes.byref(dims), err)
+
+
+def _rules(softcap, window, alibi_slopes, doc_starts, prefix_lens, hq, rows, batch, dev):
+    softcap = float(softcap)
+    if not (softcap >= 0.0 and math.isfinite(softcap)):
+        raise ValueError("softcap must be finite and not negative (0: none)")
+    a = _opt(alibi_slopes, "alibi_slopes", torch.float32, 1, dev)
+    ds = _opt(doc_starts, "doc_starts", torch.int32, 1, dev)
+    p = _opt(prefix_lens, "prefix_lens", torch.int32, 1, dev)
+    if a is not None and alibi_slopes.shape[0] != hq:
+        raise ValueError("alibi_slopes must be [num_q_heads]")
+    if ds is not None and doc_starts.shape[0] != rows:
+        raise ValueError("doc_starts must have one entry per query row")
+    if p is not None and prefix_lens.shape[0] != batch:
+        raise ValueError("prefix_lens must be [batch]")
+    return PkvScoreRules(softcap, int(window), a, ds, p)
