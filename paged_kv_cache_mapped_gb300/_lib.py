@@ -77,6 +77,7 @@ def load():
         P, I32, I64, SZ, F32 = ctypes.c_void_p, ctypes.c_int32, ctypes.c_int64, ctypes.c_size_t, ctypes.c_float
         U32 = ctypes.c_uint32
         D = ctypes.POINTER(PkvDims)
+        R = ctypes.POINTER(PkvScoreRules)
         sig = {
             "pkv_kv_append": (I32, [P, P, P, P, P, I64, D, P, P]),
             "pkv_kv_append_q8": (I32, [P, P, P, P, P, P, P, I64, D, P, P]),
@@ -101,6 +102,8 @@ def load():
             "pkv_kv_compact": (I32, [P, P, P, I32, I32, P, P, P, P, P, P, I32, D, U32, P, P]),
             "pkv_paged_decode_attention_fixed_scratch": (I32, [P, P, P, P, P, P, F32, I32, D, P, P]),
             "pkv_kv_step_tables": (I32, [P, P, P, P, P, P, P, P, P, P, I32, D, P, P]),
+            "pkv_paged_decode_attention_rules": (I32, [P, P, P, P, P, P, F32, R, P, SZ, D, U32, P, P]),
+            "pkv_paged_decode_attention_f8": (I32, [P, P, P, P, P, P, P, P, F32, R, P, SZ, D, U32, P, P]),
             "pkv_kv_append_f8": (I32, [P, P, P, P, P, P, P, I64, D, P, P]),
             "pkv_read_error": (I32, [P, I32, P]),
             "pkv_device_alias": (I32, [P, ctypes.POINTER(ctypes.c_void_p)]),

@@ -23,9 +23,9 @@ constexpr int kNumGroups = 1;
 struct DeviceInfo {
   bool ready = false;
   int sm_count = 0;
-  size_t max_dyn_smem[2][6] = {};  // [head_dim index][mode: dense, sparse, dense + scores,
-                                   //   dense INT8, INT8 + scores, sparse INT8]: opt-in minus static
-                                   //   shared memory
+  size_t max_dyn_smem[2][9] = {};  // [head_dim index][mode: dense, sparse, dense + scores,
+                                   //   dense INT8, INT8 + scores, sparse INT8, rules, FP8, FP8 + rules]:
+                                   //   opt-in minus static shared memory
   int merge_ctas_per_sm[2] = {};   // [head_dim index]: resident merge CTAs per SM
 };
 
@@ -56,9 +56,9 @@ const DeviceInfo* device_info(int* status) {
     }
     for (int hd = 0; hd < kNumHeadDims; ++hd) {
       for (int gi = 0; gi < kNumGroups; ++gi) {
-        for (int sp = 0; sp < 6; ++sp) {
-          const DecodeKernel k =
-              decode_kernel(hd == 0 ? 128 : 64, kGroups[gi], sp == 1 || sp == 5, sp == 2 || sp == 4, sp >= 3);
+        for (int sp = 0; sp < 9; ++sp) {
+          const DecodeKernel k = decode_kernel(hd == 0 ? 128 : 64, kGroups[gi], sp == 1 || sp == 5, sp == 2 || sp == 4,
+                                               sp >= 3 && sp != 6, sp >= 7, sp == 6 || sp == 8);
           if (k.split == nullptr) continue;
           cudaFuncAttributes fa{};
           cudaError_t e = cudaFuncGetAttributes(&fa, k.split);
@@ -204,6 +204,14 @@ int check_dims(const pkv_dims* d, bool need_q_heads) {
   return PKV_OK;
 }
 
+int check_rules(const pkv_score_rules* r) {
+  if (r->softcap != 0.f && !(r->softcap >= 1e-30f && r->softcap <= 1e30f)) return PKV_ERR_ARGUMENT;
+  if ((reinterpret_cast<uintptr_t>(r->alibi_slopes) | reinterpret_cast<uintptr_t>(r->doc_starts) |
+       reinterpret_cast<uintptr_t>(r->prefix_lens)) & 3u)
+    return PKV_ERR_ALIGNMENT;
+  return PKV_OK;
+}
+
 int cuda_status(cudaError_t e) { return e == cudaSuccess ? PKV_OK : PKV_ERR_CUDA_BASE + (int)e; }
 
 int device_ready() {
@@ -250,7 +258,7 @@ int decode_common(void* out, const void* q, const void* k_cache, const void* v_c
                   const int32_t* kept_lens, int32_t max_kept, float scale, int32_t window,
                   void* workspace, size_t workspace_bytes, const pkv_dims* dims, int32_t* err,
                   void* stream, bool sparse, const void* k_new, const void* v_new,
-                  const ScoreOutputs* score_out, const Q8Scales* q8, uint32_t flags) {
+                  const ScoreOutputs* score_out, const Q8Scales* q8, uint32_t flags, const pkv_score_rules* rules) {
   int st = check_dims(dims, true);
   if (st != PKV_OK) return st;
   if (dims->batch > kMaxBatch) return PKV_ERR_DIMS;
@@ -267,7 +275,14 @@ int decode_common(void* out, const void* q, const void* k_cache, const void* v_c
   if (q8 != nullptr) {
     if (sparse && k_new != nullptr) return PKV_ERR_ARGUMENT;
     if (!q8->k_scale || !q8->v_scale) return PKV_ERR_NULL_POINTER;
-    if (!aligned16(q8->k_scale) || !aligned16(q8->v_scale)) return PKV_ERR_ALIGNMENT;
+    if (q8->f8 ? ((reinterpret_cast<uintptr_t>(q8->k_scale) | reinterpret_cast<uintptr_t>(q8->v_scale)) & 3u) != 0
+               : !aligned16(q8->k_scale) || !aligned16(q8->v_scale))
+      return PKV_ERR_ALIGNMENT;
+  }
+  const bool f8 = q8 != nullptr && q8->f8;
+  if (rules != nullptr) {
+    st = check_rules(rules);
+    if (st != PKV_OK) return st;
   }
   if (score_out != nullptr) {
     if (sparse) return PKV_ERR_ARGUMENT;
@@ -277,7 +292,8 @@ int decode_common(void* out, const void* q, const void* k_cache, const void* v_c
          reinterpret_cast<uintptr_t>(score_out->logits)) & 3u)
       return PKV_ERR_ALIGNMENT;
   }
-  const DecodeKernel k = decode_kernel(dims->head_dim, group, sparse, score_out != nullptr, q8 != nullptr);
+  const DecodeKernel k = decode_kernel(dims->head_dim, group, sparse, score_out != nullptr, q8 != nullptr, f8,
+                                       rules != nullptr);
   if (k.split == nullptr) return PKV_ERR_GQA;
   const int max_units = sparse ? (max_kept + 15) / 16 : dims->max_blocks_per_seq;
   // the flattened unit count and the pool's row count (a TMA coordinate) must fit int32
@@ -290,8 +306,8 @@ int decode_common(void* out, const void* q, const void* k_cache, const void* v_c
   if (plan.ranges < kMaxWorkers) return PKV_ERR_WORKSPACE;
   const DeviceInfo* info = device_info(&st);
   if (!info) return st;
-  const size_t smem = decode_smem_bytes(dims->head_dim, sparse, dims->batch);
-  const int mode = sparse ? (q8 ? 5 : 1) : (q8 ? (score_out ? 4 : 3) : (score_out ? 2 : 0));
+  const size_t smem = decode_smem_bytes(dims->head_dim, sparse, dims->batch, rules != nullptr);
+  const int mode = f8 ? (rules ? 8 : 7) : rules ? 6 : sparse ? (q8 ? 5 : 1) : (q8 ? (score_out ? 4 : 3) : (score_out ? 2 : 0));
   if (smem > info->max_dyn_smem[head_dim_index(dims->head_dim)][mode])
     return PKV_ERR_DIMS;
   int per_sm = 0;
@@ -350,6 +366,15 @@ int decode_common(void* out, const void* q, const void* k_cache, const void* v_c
   a.MB = dims->max_blocks_per_seq;
   a.max_kept = sparse ? max_kept : 0;
   a.window = sparse ? 0 : window;
+  if (rules != nullptr) {
+    a.rules = 1;
+    a.window = rules->window;
+    a.slopes = rules->alibi_slopes;
+    a.doc_starts = rules->doc_starts;
+    a.prefix_lens = rules->prefix_lens;
+    a.cap_log2 = rules->softcap * 1.4426950408889634f;
+    a.cap_in = rules->softcap > 0.f ? 2.f / rules->softcap : 0.f;
+  }
   const int grid = std::min(info->sm_count * per_sm, kMaxWorkers / kDecodeWarps);
   const long long workers = (long long)grid * kDecodeWarps;
   a.workers = (int)workers;
@@ -423,6 +448,26 @@ int pkv_paged_decode_attention(void* out, const void* q, const void* k_cache, co
   return decode_common(out, q, k_cache, v_cache, block_tables, context_lens, nullptr, nullptr, 0, scale,
                        window, workspace, workspace_bytes, dims, error_word, stream, false, nullptr, nullptr,
                        nullptr, nullptr, flags);
+}
+
+int pkv_paged_decode_attention_rules(void* out, const void* q, const void* k_cache, const void* v_cache,
+                                     const int32_t* block_tables, const int32_t* context_lens, float scale,
+                                     const pkv_score_rules* rules, void* workspace, size_t workspace_bytes,
+                                     const pkv_dims* dims, uint32_t flags, int32_t* error_word, void* stream) {
+  if (rules == nullptr) return PKV_ERR_NULL_POINTER;
+  return decode_common(out, q, k_cache, v_cache, block_tables, context_lens, nullptr, nullptr, 0, scale, 0, workspace,
+                       workspace_bytes, dims, error_word, stream, false, nullptr, nullptr, nullptr, nullptr, flags,
+                       rules);
+}
+
+int pkv_paged_decode_attention_f8(void* out, const void* q, const void* k_codes, const void* v_codes,
+                                  const float* k_scales, const float* v_scales, const int32_t* block_tables,
+                                  const int32_t* context_lens, float scale, const pkv_score_rules* rules,
+                                  void* workspace, size_t workspace_bytes, const pkv_dims* dims, uint32_t flags,
+                                  int32_t* error_word, void* stream) {
+  const Q8Scales f8{k_scales, v_scales, true};
+  return decode_common(out, q, k_codes, v_codes, block_tables, context_lens, nullptr, nullptr, 0, scale, 0, workspace,
+                       workspace_bytes, dims, error_word, stream, false, nullptr, nullptr, nullptr, &f8, flags, rules);
 }
 
 int pkv_kv_append_q8(void* k_codes, void* v_codes, float* k_scales, float* v_scales, const void* k,

@@ -41,6 +41,12 @@
 //    logits and the V row scales enter P, relative to a per-segment reference scale, as one
 //    fp16 term.  Sparse rows arrive chunk by chunk as above, their scales as 4-byte copies
 //    completing on the K barrier.
+//  * FP8 pools (E4M3 codes, one fp32 scale per block and kv head): the INT8 form's tiles and products,
+//    with the codes made fp16 by the hardware conversion; the block's K scale multiplies its logits
+//    and its V scale enters P.
+//  * Score rules (capped scores, distance bias, window, documents, prefix): a sequence's units are
+//    those of its prefix and of its interval, and the logits pass through the cap and the bias in
+//    fp32 before the softmax.
 //  * Online softmax ("How KV Sparsity...", section "2. Attention modification", Fig. 7:
 //    running max, running sum, rescale, divide at the end) in base 2 with log2(e) folded
 //    into the scale; the running max only moves when a unit's max exceeds it by 2^8, so the
@@ -57,7 +63,7 @@
 namespace pkv {
 namespace {
 
-// Q8: INT8 pools, one byte per element; a tile is a single TMA box of 16 rows x D bytes.
+// Q8: INT8 or FP8 pools, one byte per element; a tile is a single TMA box of 16 rows x D bytes.
 template <int D, bool SPARSE, bool Q8 = false>
 struct Geo {
   static constexpr int kRow = Q8 ? D : D * 2;              // bytes per K/V row in HBM
@@ -211,6 +217,37 @@ struct SeqUnits {
   int err;    // PKV_DEV_* code or 0
 };
 
+// Score rules: the query at position i = L - 1 sees [lo, i] and the prefix [0, pre).  `first` is then
+// what a unit past the prefix's units adds to its index to give its block.
+struct RuleUnits {
+  SeqUnits s;
+  int pre;  // prefix tokens beside the interval (0 when the interval takes them in)
+};
+
+__device__ __forceinline__ RuleUnits rule_units(const DecodeArgs& a, int b) {
+  RuleUnits r{{0, 0, 0, 0, 0}, 0};
+  int L = a.context_lens[b];
+  if (L < 0 || L > a.MB * 16) {
+    r.s.err = PKV_DEV_BAD_CONTEXT_LEN;
+    L = 0;
+  }
+  int lo = (a.window > 0 && L > a.window) ? L - a.window : 0;
+  if (a.doc_starts != nullptr) lo = min(max(lo, a.doc_starts[b]), L);  // L: the interval is empty
+  int pre = a.prefix_lens != nullptr ? min(max(a.prefix_lens[b], 0), L) : 0;
+  if (lo <= pre) {  // the interval and the prefix meet
+    lo = 0;
+    pre = 0;
+  }
+  const int pre_units = (pre + 15) >> 4;
+  r.pre = pre;
+  r.s.lo = lo;
+  r.s.len = L;
+  const int first = max(lo >> 4, pre_units);  // the interval's first block that the prefix does not have
+  r.s.first = first - pre_units;
+  r.s.nb = pre_units + (L > lo ? max(((L - 1) >> 4) - first + 1, 0) : 0);
+  return r;
+}
+
 template <bool SPARSE>
 __device__ __forceinline__ SeqUnits seq_units(const DecodeArgs& a, int b) {
   SeqUnits s{0, 0, 0, 0, 0};
@@ -268,10 +305,12 @@ constexpr float kLog2e = 1.4426950408889634f;
 
 // SCORES (dense only): also keep every attended key's base-2 logit and write the log-sum-exp of
 // rows written out directly, for the score step (decode_score_kernel).
-template <int D, bool SPARSE, bool SCORES, bool Q8>
-__global__ void __launch_bounds__(kDecodeWarps * 32, Q8 ? PKV_Q8_MIN_CTAS : 0)
+// F8 (with Q8): the codes are E4M3 with a scale per block and kv head.  RULES (dense only): score rules.
+template <int D, bool SPARSE, bool SCORES, bool Q8, bool F8 = false, bool RULES = false>
+__global__ void __launch_bounds__(kDecodeWarps * 32, Q8 ? (F8 ? PKV_F8_MIN_CTAS : PKV_Q8_MIN_CTAS) : 0)
 decode_split_kernel(const __grid_constant__ DecodeArgs a) {
   static_assert(!(SPARSE && SCORES), "scores are emitted by the dense decode only");
+  static_assert(!(F8 && (SPARSE || SCORES || !Q8)) && !(RULES && (SPARSE || SCORES)), "dense decode only");
   using GE = Geo<D, SPARSE, Q8>;
   using WT = WarpTiles<D, SPARSE, Q8>;
   using WB = WarpSlots<D, SPARSE, Q8>;
@@ -294,6 +333,7 @@ decode_split_kernel(const __grid_constant__ DecodeArgs a) {
   int32_t* s_first = s_nb + a.B;
   int32_t* s_lo = s_first + a.B;   // dense: first attended token; sparse: context length
   int32_t* s_len = s_lo + a.B;     // dense: context length; sparse: kept count
+  int32_t* s_pre = s_len + a.B;    // score rules: prefix tokens (allocated for them only)
 
   const int warp = threadIdx.x >> 5;
   const int lane = threadIdx.x & 31;
@@ -331,7 +371,14 @@ decode_split_kernel(const __grid_constant__ DecodeArgs a) {
 
   // ---- per-sequence unit counts and partition (identical in every CTA) -------------------
   for (int b = threadIdx.x; b < a.B; b += blockDim.x) {
-    const SeqUnits su = seq_units<SPARSE>(a, b);
+    SeqUnits su;
+    if constexpr (RULES) {
+      const RuleUnits ru = rule_units(a, b);
+      su = ru.s;
+      s_pre[b] = ru.pre;
+    } else {
+      su = seq_units<SPARSE>(a, b);
+    }
     if (su.err != 0 && blockIdx.x == 0) note_error(su.err);
     if constexpr (SCORES) {  // a context longer than the score rows: its keys beyond them get no score
       if (su.len > a.score_stride && blockIdx.x == 0) note_error(PKV_DEV_BAD_CONTEXT_LEN);
@@ -387,6 +434,11 @@ decode_split_kernel(const __grid_constant__ DecodeArgs a) {
   const int tickets = s_part[kPartTickets];
   uint32_t n_taken = 0;        // tail tickets this warp took
   uint32_t t_req = kNoTicket;  // lane 0: a ticket requested before the current range ends
+  // block of unit j of sequence b
+  auto block_of = [&](int b, int j) -> int {
+    if constexpr (RULES) return j + (j * 16 >= s_pre[b] ? s_first[b] : 0);
+    return s_first[b] + j;
+  };
   // The next range from the ticket counter, or -1 (lane 0 hands the ticket over through
   // shared memory, so every lane sees the same value).
   auto take_ticket = [&]() -> int {
@@ -473,7 +525,7 @@ decode_split_kernel(const __grid_constant__ DecodeArgs a) {
     int phys = -1;
     if (first + lane < nunits) {
       const Cursor c = locate(u0 + first + lane, s_start, s_nb, a.B);
-      phys = __ldg(a.block_tables + (size_t)c.b * a.MB + s_first[c.b] + c.j);
+      phys = __ldg(a.block_tables + (size_t)c.b * a.MB + block_of(c.b, c.j));
     }
     return phys;
   };
@@ -557,7 +609,18 @@ decode_split_kernel(const __grid_constant__ DecodeArgs a) {
           const int y = (phys * a.Hkv + ic.g) * 16;  // host checks NB*Hkv*16 < 2^31
           Wb.meta[slot] = 0xffffu;
           Wb.phys[slot] = phys;
-          if constexpr (Q8) {
+          if constexpr (F8) {
+            // the block's two scales arrive as 4-byte copies that complete on the K barrier
+            auto& Ws = warps_scales[warp];
+            const size_t sc = (size_t)phys * a.Hkv + ic.g;
+            cp_async_4(Ws.k[slot], a.k_scale + sc);
+            cp_async_4(Ws.v[slot], a.v_scale + sc);
+            cp_async_mbar_arrive(&Wb.bar_k[slot]);
+            mbar_arrive_expect_tx(&Wb.bar_k[slot], GE::kTile);
+            tma_load_2d(Wt.k[slot], &a.tmap_k, 0, y, &Wb.bar_k[slot], pol);
+            mbar_arrive_expect_tx(&Wb.bar_v[slot], GE::kTile);
+            tma_load_2d(Wt.v[slot], &a.tmap_v, 0, y, &Wb.bar_v[slot], pol);
+          } else if constexpr (Q8) {
             // the K tile and both tiles' 16 row scales (64 bytes each, 64-byte aligned rows of
             // the scale pools) complete on the K barrier: the softmax needs the V scales too
             auto& Ws = warps_scales[warp];
@@ -659,6 +722,7 @@ decode_split_kernel(const __grid_constant__ DecodeArgs a) {
   int seg_slot = -1;  // partial slot of the current segment, -1: written out directly
   float* seg_logits = nullptr;  // scores mode: logit row of this lane's head h0 in the segment
   const float sl2 = a.scale_log2;
+  float slope0 = 0.f, slope1 = 0.f;  // score rules: distance slopes of heads h0, h1, times log2(e)
   // INT8 pools: q of the segment is prescaled by a power of two into fp16 range, so logits
   // use sl2q = sl2 over that power; o is kept in units of a V-scale reference vref that moves
   // (and rescales o) only when a unit's largest V scale exceeds it by kVrefSlack.
@@ -674,7 +738,7 @@ decode_split_kernel(const __grid_constant__ DecodeArgs a) {
   // rule: scale max|x| / 127, codes round-half-even of x / scale, both in IEEE fp32) and the
   // step writes codes and scale to the pool, the tile and the tile's scales; a row with a
   // non-finite value is reported and neither row is written.
-  const bool appending = !SPARSE && a.k_new != nullptr;
+  const bool appending = !SPARSE && !F8 && !RULES && a.k_new != nullptr;
   uint4 new_row = make_uint4(0u, 0u, 0u, 0u);
   const int new_chunk = lane & 15;
   const bool new_lane = new_chunk < D / 8;
@@ -744,6 +808,13 @@ decode_split_kernel(const __grid_constant__ DecodeArgs a) {
     seg_slot = (seg_begin >= u0 && seg_begin + nb <= u0 + nunits) ? -1 : 2 * ridx + (u0 >= seg_begin ? 0 : 1);
     if constexpr (SCORES)
       seg_logits = a.logits + ((size_t)c.b * a.Hq + (size_t)c.g * G + 2 * tq) * a.score_stride;
+    if constexpr (RULES) {
+      if (a.slopes != nullptr) {
+        const float* sp = a.slopes + (size_t)c.g * G;
+        slope0 = 2 * tq < G ? __ldg(sp + 2 * tq) * kLog2e : 0.f;
+        slope1 = 2 * tq + 1 < G ? __ldg(sp + 2 * tq + 1) * kLog2e : 0.f;
+      }
+    }
     if constexpr (Q8) {
       // q times 2^kq, with the segment's largest |q| brought into [2^14, 2^15): exact for
       // bf16 inputs, inside fp16 range (sign-cleared fp32 bit patterns order like the values)
@@ -756,7 +827,7 @@ decode_split_kernel(const __grid_constant__ DecodeArgs a) {
       sl2q = sl2 * __int_as_float((127 - kq) << 23);
 #pragma unroll
       for (int i = 0; i < 2 * KS; ++i) qb[i] = pack_f16x2(bf16_lo_to_f32(qraw[i]) * up, bf16_hi_to_f32(qraw[i]) * up);
-      {
+      if constexpr (!F8) {
         constexpr uint32_t kNeg1152 = 0xe480e480u;  // fp16x2 (-1152, -1152)
         const uint32_t ab[4] = {kNeg1152, kNeg1152, kNeg1152, kNeg1152};
 #pragma unroll
@@ -846,10 +917,18 @@ decode_split_kernel(const __grid_constant__ DecodeArgs a) {
     uint32_t mask = Wb.meta[slot];
     int t_new = -1;  // tile row of this step's token when the unit holds it (append mode)
     if constexpr (!SPARSE) {
-      const int tok0 = (s_first[cc.b] + cc.j) * 16;
-      const int lo = max(s_lo[cc.b] - tok0, 0);
-      const int hi = min(s_len[cc.b] - tok0, 16);
-      mask &= ((1u << hi) - 1u) & ~((1u << lo) - 1u);
+      const int tok0 = block_of(cc.b, cc.j) * 16;
+      if constexpr (RULES) {
+        // the interval's tokens of the unit and the prefix's (each may be none or all of it)
+        const int lo = min(max(s_lo[cc.b] - tok0, 0), 16);
+        const int hi = min(s_len[cc.b] - tok0, 16);
+        const int pre = min(max(s_pre[cc.b] - tok0, 0), 16);
+        mask &= (((1u << hi) - 1u) & ~((1u << lo) - 1u)) | ((1u << pre) - 1u);
+      } else {
+        const int lo = max(s_lo[cc.b] - tok0, 0);
+        const int hi = min(s_len[cc.b] - tok0, 16);
+        mask &= ((1u << hi) - 1u) & ~((1u << lo) - 1u);
+      }
       if (appending && new_ok && mask != 0u && s_len[cc.b] - 1 - tok0 < 16) {
         t_new = s_len[cc.b] - 1 - tok0;
         const size_t prow = ((size_t)Wb.phys[slot] * a.Hkv + cc.g) * 16 + t_new;  // pool row
@@ -884,7 +963,21 @@ decode_split_kernel(const __grid_constant__ DecodeArgs a) {
       float c[4] = {kbias[0], kbias[1], kbias[2], kbias[3]};  // zero but for INT8 pools
       const uint32_t kbase = smem_u32(Wt.k[slot]);
       float fk0 = sl2, fk1 = sl2;  // logit factor of tokens gq and gq + 8
-      if constexpr (Q8) {
+      if constexpr (F8) {
+        // byte rows as below, made fp16 two codes at a time
+#pragma unroll
+        for (int pp = 0; pp < KS / 2; ++pp) {
+          uint32_t r[4];
+          ldsm_x4(kbase + chunk_offset<D, SPARSE, Q8>(k_row, 2 * pp + k_half), r);
+          const uint32_t a0[4] = {e4m3x2_to_f16x2(r[0]), e4m3x2_to_f16x2(r[1]), e4m3x2_to_f16x2(r[0] >> 16),
+                                  e4m3x2_to_f16x2(r[1] >> 16)};
+          mma_f16_m16n8k16(c, a0, qb[4 * pp], qb[4 * pp + 1]);
+          const uint32_t a1[4] = {e4m3x2_to_f16x2(r[2]), e4m3x2_to_f16x2(r[3]), e4m3x2_to_f16x2(r[2] >> 16),
+                                  e4m3x2_to_f16x2(r[3] >> 16)};
+          mma_f16_m16n8k16(c, a1, qb[4 * pp + 2], qb[4 * pp + 3]);
+        }
+        fk0 = fk1 = warps_scales[warp].k[slot][0] * sl2q;
+      } else if constexpr (Q8) {
         // int8 rows: one ldmatrix yields two k-steps; each lane holds 4 consecutive columns
         // of a row per matrix, the order q was loaded in; the codes enter as 1152 + code
 #pragma unroll
@@ -913,10 +1006,26 @@ decode_split_kernel(const __grid_constant__ DecodeArgs a) {
       const bool t0 = (mask >> gq) & 1u;
       const bool t1 = (mask >> (gq + 8)) & 1u;
       const bool v0 = 2 * tq < G, v1 = 2 * tq + 1 < G;
-      const float s00 = (t0 && v0) ? c[0] * fk0 : -INFINITY;
-      const float s01 = (t0 && v1) ? c[1] * fk0 : -INFINITY;
-      const float s10 = (t1 && v0) ? c[2] * fk1 : -INFINITY;
-      const float s11 = (t1 && v1) ? c[3] * fk1 : -INFINITY;
+      float x00 = c[0] * fk0, x01 = c[1] * fk0, x10 = c[2] * fk1, x11 = c[3] * fk1;  // base-2 logits
+      if constexpr (RULES) {
+        if (a.cap_log2 > 0.f) {
+          x00 = cap_logit(x00, a.cap_log2, a.cap_in);
+          x01 = cap_logit(x01, a.cap_log2, a.cap_in);
+          x10 = cap_logit(x10, a.cap_log2, a.cap_in);
+          x11 = cap_logit(x11, a.cap_log2, a.cap_in);
+        }
+        if (a.slopes != nullptr) {
+          const float far0 = (float)(s_len[cc.b] - 1 - block_of(cc.b, cc.j) * 16 - gq), far1 = far0 - 8.f;
+          x00 = fmaf(-slope0, far0, x00);
+          x01 = fmaf(-slope1, far0, x01);
+          x10 = fmaf(-slope0, far1, x10);
+          x11 = fmaf(-slope1, far1, x11);
+        }
+      }
+      const float s00 = (t0 && v0) ? x00 : -INFINITY;
+      const float s01 = (t0 && v1) ? x01 : -INFINITY;
+      const float s10 = (t1 && v0) ? x10 : -INFINITY;
+      const float s11 = (t1 && v1) ? x11 : -INFINITY;
       if constexpr (SCORES) {  // keep the attended keys' logits for the score step
         const int tok = (s_first[cc.b] + cc.j) * 16 + gq;
         float* lg = seg_logits + tok;
@@ -936,7 +1045,9 @@ decode_split_kernel(const __grid_constant__ DecodeArgs a) {
       // INT8 pools: the V scales of the attended tokens, and their largest
       float vs0 = 0.f, vs1 = 0.f;
       float vm = 0.f;
-      if constexpr (Q8) {
+      if constexpr (F8) {
+        vs0 = vs1 = vm = warps_scales[warp].v[slot][0];
+      } else if constexpr (Q8) {
         vs0 = t0 ? warps_scales[warp].v[slot][gq] : 0.f;
         vs1 = t1 ? warps_scales[warp].v[slot][gq + 8] : 0.f;
         vm = fmaxf(vs0, vs1);
@@ -1027,6 +1138,18 @@ decode_split_kernel(const __grid_constant__ DecodeArgs a) {
         }
         __syncwarp();
       }
+      if constexpr (F8) {
+        if (mask != 0xffffu) {  // as below: E4M3 has NaN codes
+          constexpr int CPR = D / 16;  // 16-byte chunks per row
+#pragma unroll
+          for (int i = 0; i < CPR / 2; ++i) {
+            const int t = (i * 32 + lane) / CPR, ch = lane % CPR;
+            if (!((mask >> t) & 1u))
+              *reinterpret_cast<uint4*>(Wt.v[slot] + chunk_offset<D, SPARSE, Q8>(t, ch)) = make_uint4(0u, 0u, 0u, 0u);
+          }
+          __syncwarp();
+        }
+      }
       if constexpr (!Q8) {
         if (mask != 0xffffu) {
           // rows of tokens outside the attended set may hold anything (even NaN): zero them,
@@ -1043,7 +1166,23 @@ decode_split_kernel(const __grid_constant__ DecodeArgs a) {
       }
       // -- O^T += V^T P^T -------------------------------------------------------------------
       const uint32_t vbase = smem_u32(Wt.v[slot]);
-      if constexpr (Q8) {
+      if constexpr (F8) {
+        // as below, the bytes (token 2tq: columns 2gq, 2gq + 1; token 2tq + 1: the same) brought together
+        // by column before the conversion
+#pragma unroll
+        for (int pp = 0; pp < KS / 2; ++pp) {
+          uint32_t r[4];
+          ldsm_x4_trans(vbase + chunk_offset<D, SPARSE, Q8>(k_row, 2 * pp + k_half), r);
+#pragma unroll
+          for (int i = 0; i < 4; ++i) r[i] = __byte_perm(r[i], 0u, 0x3120);
+          const uint32_t a0[4] = {e4m3x2_to_f16x2(r[0]), e4m3x2_to_f16x2(r[0] >> 16), e4m3x2_to_f16x2(r[1]),
+                                  e4m3x2_to_f16x2(r[1] >> 16)};
+          mma_f16_m16n8k16(o[2 * pp], a0, bh0, bh1);
+          const uint32_t a1[4] = {e4m3x2_to_f16x2(r[2]), e4m3x2_to_f16x2(r[2] >> 16), e4m3x2_to_f16x2(r[3]),
+                                  e4m3x2_to_f16x2(r[3] >> 16)};
+          mma_f16_m16n8k16(o[2 * pp + 1], a1, bh0, bh1);
+        }
+      } else if constexpr (Q8) {
         // transposed int8 ldmatrix: each lane gets columns 2gq, 2gq + 1 of tokens 2tq, 2tq + 1;
         // columns 2gq and 2gq + 1 become accumulator rows gq and gq + 8 of the 16-column tile
 #pragma unroll
@@ -1084,7 +1223,7 @@ decode_split_kernel(const __grid_constant__ DecodeArgs a) {
   }
 
   if (aborted) {  // let the copies in flight land before the CTA's shared memory goes away
-    if constexpr (SPARSE) cp_async_wait_all();
+    if constexpr (SPARSE || F8) cp_async_wait_all();
     for (int kk = k; kk < issued; ++kk) {
       (void)mbar_wait_bounded(&Wb.bar_k[kk % R], (uint32_t)(kk / R) & 1u, a.timeout_ns);
       (void)mbar_wait_bounded(&Wb.bar_v[kk % R], (uint32_t)(kk / R) & 1u, a.timeout_ns);
@@ -1159,7 +1298,8 @@ decode_merge_kernel(const DecodeArgs a, int group, int wpr_log2) {
     for (int base = 0; base < a.B; base += 32) {
       const int bb = base + lane;
       int v = 0;
-      if (bb < a.B) v = sparse ? seq_units<true>(a, bb).nb : seq_units<false>(a, bb).nb;
+      if (bb < a.B)
+        v = sparse ? seq_units<true>(a, bb).nb : a.rules ? rule_units(a, bb).s.nb : seq_units<false>(a, bb).nb;
       const int own = __shfl_sync(kFullMask, v, (b - base) & 31);
       if (b >= base && b < base + 32) nb = own;
       int sa = v, sb = bb < b ? v : 0;
@@ -1335,34 +1475,43 @@ __global__ void __launch_bounds__(kScoreThreads) decode_score_kernel(const Decod
 
 }  // namespace
 
-DecodeKernel decode_kernel(int head_dim, int group, bool sparse, bool scores, bool q8) {
+namespace {
+
+template <int D>
+DecodeKernel kernels_of(int group, bool sparse, bool scores, bool q8, bool f8, bool rules) {
+  const void* split;
+  if (f8)
+    split = rules ? (const void*)decode_split_kernel<D, false, false, true, true, true>
+                  : (const void*)decode_split_kernel<D, false, false, true, true, false>;
+  else if (rules)
+    split = (const void*)decode_split_kernel<D, false, false, false, false, true>;
+  else if (q8)
+    split = scores   ? (const void*)decode_split_kernel<D, false, true, true>
+            : sparse ? (const void*)decode_split_kernel<D, true, false, true>
+                     : (const void*)decode_split_kernel<D, false, false, true>;
+  else
+    split = sparse   ? (const void*)decode_split_kernel<D, true, false, false>
+            : scores ? (const void*)decode_split_kernel<D, false, true, false>
+                     : (const void*)decode_split_kernel<D, false, false, false>;
+  return DecodeKernel{split, (const void*)decode_merge_kernel<D>, scores ? (const void*)decode_score_kernel : nullptr,
+                      D, group, sparse, scores, q8};
+}
+
+}  // namespace
+
+DecodeKernel decode_kernel(int head_dim, int group, bool sparse, bool scores, bool q8, bool f8, bool rules) {
   const DecodeKernel none{nullptr, nullptr, nullptr, head_dim, group, sparse, scores, q8};
-  if (group < 1 || group > kMaxGroup || (sparse && scores)) return none;
-  const void* score = scores ? (const void*)decode_score_kernel : nullptr;
-  if (head_dim == 128)
-    return DecodeKernel{q8 ? (scores   ? (const void*)decode_split_kernel<128, false, true, true>
-                              : sparse ? (const void*)decode_split_kernel<128, true, false, true>
-                                       : (const void*)decode_split_kernel<128, false, false, true>)
-                        : sparse ? (const void*)decode_split_kernel<128, true, false, false>
-                        : scores ? (const void*)decode_split_kernel<128, false, true, false>
-                                 : (const void*)decode_split_kernel<128, false, false, false>,
-                        (const void*)decode_merge_kernel<128>, score, 128, group, sparse, scores, q8};
-  if (head_dim == 64)
-    return DecodeKernel{q8 ? (scores   ? (const void*)decode_split_kernel<64, false, true, true>
-                              : sparse ? (const void*)decode_split_kernel<64, true, false, true>
-                                       : (const void*)decode_split_kernel<64, false, false, true>)
-                        : sparse ? (const void*)decode_split_kernel<64, true, false, false>
-                        : scores ? (const void*)decode_split_kernel<64, false, true, false>
-                                 : (const void*)decode_split_kernel<64, false, false, false>,
-                        (const void*)decode_merge_kernel<64>, score, 64, group, sparse, scores, q8};
+  if (group < 1 || group > kMaxGroup || (sparse && scores) || ((f8 || rules) && (sparse || scores))) return none;
+  if (head_dim == 128) return kernels_of<128>(group, sparse, scores, q8, f8, rules);
+  if (head_dim == 64) return kernels_of<64>(group, sparse, scores, q8, f8, rules);
   return none;
 }
 
-size_t decode_smem_bytes(int head_dim, bool sparse, int batch) {
+size_t decode_smem_bytes(int head_dim, bool sparse, int batch, bool rules) {
   (void)sparse;
   if (head_dim != 128 && head_dim != 64) return 0;
   // dynamic part only: the per-sequence arrays (the tile rings are static)
-  return sizeof(int32_t) * (5 * (size_t)batch + 1);
+  return sizeof(int32_t) * ((rules ? 6 : 5) * (size_t)batch + 1);
 }
 
 cudaError_t launch_decode(const DecodeKernel& k, const DecodeArgs& a, int grid, size_t smem,

@@ -8,7 +8,7 @@
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 
-#include "pkv.h"
+#include "pkv_step.h"
 
 namespace pkv {
 
@@ -39,7 +39,8 @@ struct DecodeArgs {
   float2* part_ml;               // [2 ranges, G] (running max in log2 units, running sum)
   float* part_o;                 // [2 ranges, G, D] unnormalised partial outputs
   const float* k_scale;          // INT8 pools: [NB, Hkv, 16] fp32 scale of each K row
-  const float* v_scale;          //   (likewise V); the pools then hold INT8 codes (bytes code + 128)
+  const float* v_scale;          //   (likewise V); the pools then hold INT8 codes (bytes code + 128).
+                                 //   FP8 pools: [NB, Hkv], one scale per block and kv head
   float* k_scale_out;            // INT8 append mode: the scale pools again, writable
   float* v_scale_out;
   float* logits;                 // scores mode: [B, Hq, score_stride] base-2 logits of attended keys
@@ -47,6 +48,11 @@ struct DecodeArgs {
   float* scores;                 // scores mode: [B, Hkv, score_stride] accumulated scores
   int score_stride;              // scores mode: row length of logits and scores
   int32_t* err;                  // device error word or nullptr
+  const float* slopes;           // score rules: [Hq] distance slopes or nullptr
+  const int32_t* doc_starts;     // score rules: [B] or nullptr
+  const int32_t* prefix_lens;    // score rules: [B] or nullptr
+  float cap_log2, cap_in;        // score rules: cap * log2(e) (0: no cap) and 2 / cap
+  int rules;                     // 1: score rules (the merge kernel derives the same units)
   int B, Hq, Hkv, NB, MB, max_kept, window;
   int workers;                   // worker warps of the split grid
   int min_units;                 // lower bound of the slice length P
@@ -96,6 +102,10 @@ constexpr int kPartFields = kPartOff + kMaxTailChunksLimit + 1;
 
 #ifndef PKV_Q8_MIN_CTAS
 #define PKV_Q8_MIN_CTAS 12  // INT8 decode: resident CTAs per SM the register budget must allow (0: no bound)
+#endif
+
+#ifndef PKV_F8_MIN_CTAS
+#define PKV_F8_MIN_CTAS 12  // FP8 decode: the same bound
 #endif
 
 #ifndef PKV_MIN_UNITS
@@ -172,8 +182,9 @@ struct DecodeKernel {
 
 // Returns a struct with split == nullptr when the combination is unsupported (scores mode
 // and INT8 pools exist for dense decode only, and not together).
-DecodeKernel decode_kernel(int head_dim, int group, bool sparse, bool scores = false, bool q8 = false);
-size_t decode_smem_bytes(int head_dim, bool sparse, int batch);
+DecodeKernel decode_kernel(int head_dim, int group, bool sparse, bool scores = false, bool q8 = false,
+                           bool f8 = false, bool rules = false);
+size_t decode_smem_bytes(int head_dim, bool sparse, int batch, bool rules = false);
 // merge_wpr_log2: log2 of the merge warps per output row (0..3).
 cudaError_t launch_decode(const DecodeKernel& k, const DecodeArgs& a, int grid, size_t smem,
                           int merge_wpr_log2, cudaStream_t stream);
@@ -279,6 +290,7 @@ cudaError_t launch_step_tables(const StepArgs& a, cudaStream_t stream);
 int check_dims(const struct pkv_dims* d, bool need_q_heads);
 bool aligned16(const void* p);
 int cuda_status(cudaError_t e);
+int check_rules(const struct pkv_score_rules* r);
 int device_ready();  // one-time set-up of the current device; a PKV status
 
 // Launches `kernel` with programmatic stream serialisation (it may start before the previous
@@ -318,9 +330,11 @@ struct ScoreOutputs {
 };
 
 // INT8 pools of a dense decode (pkv_paged_decode_attention_q8); nullptr: bf16 pools.
+// f8: FP8 pools with a scale per block and kv head instead.
 struct Q8Scales {
   const float* k_scale;
   const float* v_scale;
+  bool f8 = false;
 };
 
 int decode_common(void* out, const void* q, const void* k_cache, const void* v_cache,
@@ -329,6 +343,6 @@ int decode_common(void* out, const void* q, const void* k_cache, const void* v_c
                   void* workspace, size_t workspace_bytes, const struct pkv_dims* dims, int32_t* err,
                   void* stream, bool sparse, const void* k_new = nullptr, const void* v_new = nullptr,
                   const ScoreOutputs* score_out = nullptr, const Q8Scales* q8 = nullptr,
-                  uint32_t flags = 0);
+                  uint32_t flags = 0, const struct pkv_score_rules* rules = nullptr);
 
 }  // namespace pkv

@@ -338,8 +338,28 @@ __device__ __forceinline__ uint32_t i8x2_to_biased_f16x2(uint32_t w) {
   return r;
 }
 
+// Two E4M3 codes (the low 16 bits of w, low byte first) as an exact f16x2.
+__device__ __forceinline__ uint32_t e4m3x2_to_f16x2(uint32_t w) {
+  uint32_t r;
+  asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(r) : "h"((uint16_t)w));
+  return r;
+}
+
 __device__ __forceinline__ float bf16_lo_to_f32(uint32_t w) { return __uint_as_float(w << 16); }
 __device__ __forceinline__ float bf16_hi_to_f32(uint32_t w) { return __uint_as_float(w & 0xffff0000u); }
+
+// cap tanh(x / cap) of a base-2 logit x (cap2 = cap log2(e); in = 2 / cap, so y = in x has 2^y =
+// e^(2u), u the natural logit over the cap).  |u| < 0.3: the odd Taylor polynomial to u^9 (the
+// first term left out is 0.0089 u^10 of the value, 5e-8 there); beyond: 1 - 2 / (e^(2u) + 1), whose
+// absolute error of 2^-23 is then small beside the value, and whose limits are +-1.  Relative error a
+// few 2^-23 either way, so that caps far above the logits leave them as they are.
+__device__ __forceinline__ float cap_logit(float x, float cap2, float in) {
+  const float y = x * in;
+  const float u = y * 0.34657359f, w = u * u;
+  const float poly = u * fmaf(w, fmaf(w, fmaf(w, fmaf(w, 0.021869488f, -0.053968254f), 0.13333333f), -0.33333333f), 1.f);
+  const float big = 1.f - __fdividef(2.f, exp2f(y) + 1.f);
+  return cap2 * (fabsf(u) < 0.3f ? poly : big);
+}
 
 // Programmatic dependent launch.  A kernel launched with programmatic stream serialisation
 // may start while the previous kernel on its stream is still running; it must call

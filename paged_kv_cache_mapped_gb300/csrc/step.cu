@@ -193,8 +193,7 @@ __device__ __forceinline__ uint32_t pack_e4m3x2(float lo, float hi) {
 }
 
 __device__ __forceinline__ float2 e4m3x2_to_f32(uint32_t w) {
-  uint32_t h;
-  asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(h) : "h"((uint16_t)w));
+  const uint32_t h = e4m3x2_to_f16x2(w);
   return make_float2(f16_lo_to_f32(h), f16_hi_to_f32(h));
 }
 

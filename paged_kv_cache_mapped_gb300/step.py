@@ -5,7 +5,6 @@ work runs in the library's CUDA kernels on the current stream of the tensors' de
 from __future__ import annotations
 
 import ctypes
-import math
 
 import torch
 
@@ -134,8 +133,8 @@ def kv_append_f8(k_codes, v_codes, k_scales, v_scales, k, v, slot_mapping, *, er
 
 def _rules(softcap, window, alibi_slopes, doc_starts, prefix_lens, hq, rows, batch, dev):
     softcap = float(softcap)
-    if not (softcap >= 0.0 and math.isfinite(softcap)):
-        raise ValueError("softcap must be finite and not negative (0: none)")
+    if softcap != 0.0 and not 1e-30 <= softcap <= 1e30:
+        raise ValueError("softcap must be 0 (none) or within [1e-30, 1e30]")
     a = _opt(alibi_slopes, "alibi_slopes", torch.float32, 1, dev)
     ds = _opt(doc_starts, "doc_starts", torch.int32, 1, dev)
     p = _opt(prefix_lens, "prefix_lens", torch.int32, 1, dev)
@@ -146,3 +145,59 @@ def _rules(softcap, window, alibi_slopes, doc_starts, prefix_lens, hq, rows, bat
     if p is not None and prefix_lens.shape[0] != batch:
         raise ValueError("prefix_lens must be [batch]")
     return PkvScoreRules(softcap, int(window), a, ds, p)
+
+
+def _decode_common(q, nb, hkv, d, block_tables, context_lens, out, workspace, error_word, dev):
+    qp = _need(q, "q", torch.bfloat16, 3, dev)
+    bp = _need(block_tables, "block_tables", torch.int32, 2, dev)
+    lp = _need(context_lens, "context_lens", torch.int32, 1, dev)
+    err = _opt(error_word, "error_word", torch.int32, 1, dev)
+    B, hq, dq = q.shape
+    if dq != d:
+        raise ValueError("q head_dim differs from the pools'")
+    if block_tables.shape[0] != B or context_lens.shape[0] != B:
+        raise ValueError("block_tables / context_lens batch differs from q's")
+    dims = _dims(B, hq, hkv, d, nb, block_tables.shape[1])
+    out = _give(out, "out", q.shape, torch.bfloat16, dev)
+    if workspace is None:
+        workspace = torch.zeros(int(load().pkv_decode_workspace_bytes(ctypes.byref(dims))), dtype=torch.uint8, device=dev)
+    else:
+        _need(workspace, "workspace", torch.uint8, 1, dev)
+    return dims, qp, bp, lp, err, out, workspace
+
+
+def paged_decode_attention_rules(q, k_cache, v_cache, block_tables, context_lens, scale, window=0, *, softcap=0.0,
+                                 alibi_slopes=None, doc_starts=None, prefix_lens=None, out=None, workspace=None,
+                                 error_word=None, inputs_ready=False, stream=None):
+    """paged_decode_attention with score rules: scores capped to softcap * tanh(x / softcap), a distance
+    bias -alibi_slopes[h] * (L - 1 - t) (fp32 [Hq]), and the visible keys [max(0, L - window, doc_start), L)
+    and [0, prefix_len) (int32 [B] each).  Returns out [B, Hq, d] bf16; a row that sees no key is zero."""
+    dev = k_cache.device if isinstance(k_cache, torch.Tensor) else None
+    kp = _need(k_cache, "k_cache", torch.bfloat16, 4)
+    vp = _need(v_cache, "v_cache", torch.bfloat16, 4, dev)
+    nb, hkv, bs, d = k_cache.shape
+    if v_cache.shape != k_cache.shape or bs != BLOCK_SIZE:
+        raise ValueError(f"pools must have one shape [num_blocks, num_kv_heads, {BLOCK_SIZE}, head_dim]")
+    dims, qp, bp, lp, err, out, workspace = _decode_common(q, nb, hkv, d, block_tables, context_lens, out, workspace,
+                                                           error_word, dev)
+    rules = _rules(softcap, window, alibi_slopes, doc_starts, prefix_lens, dims.num_q_heads, dims.batch, dims.batch, dev)
+    _call("pkv_paged_decode_attention_rules", dev, stream, out.data_ptr(), qp, kp, vp, bp, lp, float(scale),
+          ctypes.byref(rules), workspace.data_ptr(), workspace.numel(), ctypes.byref(dims),
+          _INPUTS_READY if inputs_ready else 0, err)
+    return out
+
+
+def paged_decode_attention_f8(q, k_codes, v_codes, k_scales, v_scales, block_tables, context_lens, scale, window=0, *,
+                              softcap=0.0, alibi_slopes=None, doc_starts=None, prefix_lens=None, out=None,
+                              workspace=None, error_word=None, inputs_ready=False, stream=None):
+    """paged_decode_attention over FP8 pools (codes [NB, Hkv, 16, d] torch.float8_e4m3fn times one fp32
+    scale per (block, kv head), [NB, Hkv]), with the score rules of paged_decode_attention_rules."""
+    nb, hkv, d, dev = _f8_pools(k_codes, v_codes, k_scales, v_scales)
+    dims, qp, bp, lp, err, out, workspace = _decode_common(q, nb, hkv, d, block_tables, context_lens, out, workspace,
+                                                           error_word, dev)
+    rules = _rules(softcap, window, alibi_slopes, doc_starts, prefix_lens, dims.num_q_heads, dims.batch, dims.batch, dev)
+    plain = rules.softcap == 0 and rules.window <= 0 and alibi_slopes is None and doc_starts is None and prefix_lens is None
+    _call("pkv_paged_decode_attention_f8", dev, stream, out.data_ptr(), qp, k_codes.data_ptr(), v_codes.data_ptr(),
+          k_scales.data_ptr(), v_scales.data_ptr(), bp, lp, float(scale), None if plain else ctypes.byref(rules),
+          workspace.data_ptr(), workspace.numel(), ctypes.byref(dims), _INPUTS_READY if inputs_ready else 0, err)
+    return out
