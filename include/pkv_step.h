@@ -2,11 +2,12 @@
  * pkv_step.h -- C ABI of the serving-step operators that stand beside the calls of pkv.h: the
  * block tables and slots of a step built on the GPU, an FP8 cache with one scale per block and
  * kv head, and attention with score rules (capped scores, distance bias, sliding window,
- * documents, a prefix that stays visible).
+ * documents, a prefix that stays visible) for one query token and for many.
  *
  * One step of a serving engine: pkv_kv_step_tables gives every request the blocks and slots of
  * its new tokens, pkv_kv_append (or pkv_kv_append_f8) writes their K and V rows there, and
- * one of the decode calls attends.
+ * pkv_paged_prefill_attention (prompt chunks, mixed batches) or one of the decode calls (one token
+ * per request) attends.
  *
  * The conventions of pkv.h hold for every call here (device pointers, nothing allocated, kernels
  * enqueued on `stream` only, status codes, device errors through error_word, dense layouts).
@@ -139,6 +140,36 @@ int pkv_paged_decode_attention_f8(void* out, const void* q, const void* k_codes,
                                   const int32_t* context_lens, float scale, const pkv_score_rules* rules,
                                   void* workspace, size_t workspace_bytes, const pkv_dims* dims, uint32_t flags,
                                   int32_t* error_word, void* stream);
+
+/*
+ * pkv_prefill_workspace_bytes -- bytes of device workspace for pkv_paged_prefill_attention with these
+ * dims and at most total_tokens packed query rows.  Its contents need no preparation and nothing is
+ * kept in it between calls; calls that may overlap on the GPU (other streams, or captured graphs that
+ * run at the same time) need one each.  Returns 0 if the arguments are invalid.
+ */
+size_t pkv_prefill_workspace_bytes(const pkv_dims* dims, int32_t total_tokens);
+
+/*
+ * pkv_paged_prefill_attention -- attention of many query tokens per sequence over the paged cache:
+ * prompts, chunks of prompts and mixed steps, causal, with score rules (the prefill stage of "KV Cache
+ * primer" section 2.1 over the blocks of section 4.1).  The K and V rows of the queries' own tokens
+ * are in the cache already.
+ *   out, q        : [total_tokens, Hq, d] bf16.  Sequence b's queries are rows query_starts[b] ..
+ *                   query_starts[b+1] - 1, n_b of them, at positions L_b - n_b + r.  Rows from
+ *                   query_starts[B] on (a padded batch) are neither read nor written.
+ *   query_starts  : [B + 1] int32, ascending, query_starts[0] >= 0, query_starts[B] <= total_tokens.
+ *   context_lens  : [B] int32, L_b including the step's tokens, n_b <= L_b <= MB * 16.
+ *   total_tokens  : rows of q and out.
+ *   rules         : or NULL (causal).
+ *   error_word    : PKV_DEV_BAD_BLOCK_ID, _BAD_CONTEXT_LEN, _WAIT_TIMEOUT; _BAD_QUERY_RANGE for a
+ *                   sequence whose rows are not within the packed batch (its rows are not written).
+ * Supported: d in {64, 128}; G = Hq / Hkv in 1..8; B <= 4096; MB * 16 < 2^30.
+ */
+int pkv_paged_prefill_attention(void* out, const void* q, const void* k_cache, const void* v_cache,
+                                const int32_t* block_tables, const int32_t* context_lens,
+                                const int32_t* query_starts, int32_t total_tokens, float scale,
+                                const pkv_score_rules* rules, void* workspace, size_t workspace_bytes,
+                                const pkv_dims* dims, int32_t* error_word, void* stream);
 
 #ifdef __cplusplus
 }

@@ -14,7 +14,8 @@ import ctypes
 import torch
 
 from ._lib import PkvDims, PkvError, check, header_constants, header_functions, load
-from .step import kv_append_f8, kv_step_tables, paged_decode_attention_f8, paged_decode_attention_rules
+from .step import (kv_append_f8, kv_step_tables, paged_decode_attention_f8, paged_decode_attention_rules,
+                   paged_prefill_attention, prefill_workspace_bytes)
 
 __all__ = [
     "BLOCK_SIZE", "PkvError", "kv_append", "decode_workspace_bytes", "paged_decode_attention",
@@ -28,6 +29,7 @@ __all__ = [
     "paged_decode_attention_scores_q8", "kv_compact_q8", "kv_rolling_admit_q8",
     "paged_decode_attention_append_q8", "sparse_decode_attention_q8",
     "kv_step_tables", "kv_append_f8", "paged_decode_attention_rules", "paged_decode_attention_f8",
+    "paged_prefill_attention", "prefill_workspace_bytes",
 ]
 
 BLOCK_SIZE = 16

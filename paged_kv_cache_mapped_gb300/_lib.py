@@ -104,6 +104,8 @@ def load():
             "pkv_kv_step_tables": (I32, [P, P, P, P, P, P, P, P, P, P, I32, D, P, P]),
             "pkv_paged_decode_attention_rules": (I32, [P, P, P, P, P, P, F32, R, P, SZ, D, U32, P, P]),
             "pkv_paged_decode_attention_f8": (I32, [P, P, P, P, P, P, P, P, F32, R, P, SZ, D, U32, P, P]),
+            "pkv_prefill_workspace_bytes": (SZ, [D, I32]),
+            "pkv_paged_prefill_attention": (I32, [P, P, P, P, P, P, P, I32, F32, R, P, SZ, D, P, P]),
             "pkv_kv_append_f8": (I32, [P, P, P, P, P, P, P, I64, D, P, P]),
             "pkv_read_error": (I32, [P, I32, P]),
             "pkv_device_alias": (I32, [P, ctypes.POINTER(ctypes.c_void_p)]),

@@ -286,6 +286,25 @@ constexpr int kMaxStepBatch = 4096;
 cudaError_t step_device_setup();
 cudaError_t launch_step_tables(const StepArgs& a, cudaStream_t stream);
 
+// Attention of many query tokens per sequence (prefill_attention.cu).
+struct PrefillAttnArgs {
+  const __nv_bfloat16* q;        // [T, Hq, D] packed query rows
+  const __nv_bfloat16* k_cache;  // [NB, Hkv, 16, D]
+  const __nv_bfloat16* v_cache;
+  __nv_bfloat16* out;            // [T, Hq, D]
+  const int32_t* block_tables;   // [B, MB]
+  const int32_t* context_lens;   // [B]
+  const int32_t* query_starts;   // [B + 1]
+  const float* slopes;           // [Hq] or nullptr
+  const int32_t* doc_starts;     // [T] or nullptr
+  const int32_t* prefix_lens;    // [B] or nullptr
+  int32_t* err;
+  float scale_log2, cap_log2, cap_in;  // as DecodeArgs
+  int B, T, Hq, Hkv, NB, MB, G, window;
+};
+size_t prefill_attention_workspace(int B, int T, int G, int D);
+cudaError_t launch_prefill_attention(const PrefillAttnArgs& a, int head_dim, cudaStream_t stream);
+
 // Host-side checks shared by the entry points (api.cu).
 int check_dims(const struct pkv_dims* d, bool need_q_heads);
 bool aligned16(const void* p);

@@ -201,3 +201,49 @@ def paged_decode_attention_f8(q, k_codes, v_codes, k_scales, v_scales, block_tab
           k_scales.data_ptr(), v_scales.data_ptr(), bp, lp, float(scale), None if plain else ctypes.byref(rules),
           workspace.data_ptr(), workspace.numel(), ctypes.byref(dims), _INPUTS_READY if inputs_ready else 0, err)
     return out
+
+
+def prefill_workspace_bytes(total_tokens, batch, num_q_heads, num_kv_heads, head_dim, num_blocks, max_blocks_per_seq) -> int:
+    """Workspace of paged_prefill_attention for these sizes and at most total_tokens query rows."""
+    dims = _dims(batch, num_q_heads, num_kv_heads, head_dim, num_blocks, max_blocks_per_seq)
+    n = int(load().pkv_prefill_workspace_bytes(ctypes.byref(dims), int(total_tokens)))
+    if n == 0:
+        raise ValueError("invalid dims for paged prefill")
+    return n
+
+
+def paged_prefill_attention(q, k_cache, v_cache, block_tables, context_lens, query_starts, scale, window=0, *, softcap=0.0,
+                            alibi_slopes=None, doc_starts=None, prefix_lens=None, out=None, workspace=None,
+                            error_word=None, stream=None):
+    """Causal attention of many query tokens per sequence over the paged cache, with score rules.
+    q [T, Hq, d] bf16 packs the queries of every sequence: rows query_starts[b] .. query_starts[b+1]
+    (int32 [B + 1]) are sequence b's last positions, context_lens [B] counts its keys with the step's own.
+    The rules are those of paged_decode_attention_rules, doc_starts one int32 per packed row [T].  Returns
+    out [T, Hq, d]; rows from query_starts[B] on are left as they were (unset when `out` is made here)."""
+    dev = k_cache.device if isinstance(k_cache, torch.Tensor) else None
+    kp = _need(k_cache, "k_cache", torch.bfloat16, 4)
+    vp = _need(v_cache, "v_cache", torch.bfloat16, 4, dev)
+    nb, hkv, bs, d = k_cache.shape
+    if v_cache.shape != k_cache.shape or bs != BLOCK_SIZE:
+        raise ValueError(f"pools must have one shape [num_blocks, num_kv_heads, {BLOCK_SIZE}, head_dim]")
+    qp = _need(q, "q", torch.bfloat16, 3, dev)
+    bp = _need(block_tables, "block_tables", torch.int32, 2, dev)
+    lp = _need(context_lens, "context_lens", torch.int32, 1, dev)
+    sp = _need(query_starts, "query_starts", torch.int32, 1, dev)
+    err = _opt(error_word, "error_word", torch.int32, 1, dev)
+    T, hq, dq = q.shape
+    B = block_tables.shape[0]
+    if dq != d:
+        raise ValueError("q head_dim differs from the pools'")
+    if context_lens.shape[0] != B or query_starts.shape[0] != B + 1:
+        raise ValueError("context_lens must be [B] and query_starts [B + 1]")
+    rules = _rules(softcap, window, alibi_slopes, doc_starts, prefix_lens, hq, T, B, dev)
+    dims = _dims(B, hq, hkv, d, nb, block_tables.shape[1])
+    out = _give(out, "out", q.shape, torch.bfloat16, dev)
+    if workspace is None:
+        workspace = torch.empty(int(load().pkv_prefill_workspace_bytes(ctypes.byref(dims), T)), dtype=torch.uint8, device=dev)
+    else:
+        _need(workspace, "workspace", torch.uint8, 1, dev)
+    _call("pkv_paged_prefill_attention", dev, stream, out.data_ptr(), qp, kp, vp, bp, lp, sp, T, float(scale),
+          ctypes.byref(rules), workspace.data_ptr(), workspace.numel(), ctypes.byref(dims), err)
+    return out
