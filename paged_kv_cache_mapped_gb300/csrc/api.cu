@@ -15,7 +15,6 @@ namespace {
 
 constexpr int kMaxDevices = 64;
 constexpr int kMaxBatch = 4096;
-constexpr unsigned long long kWaitTimeoutNs = 2000000000ull;  // 2 s per mbarrier wait
 constexpr int kNumHeadDims = 2;
 constexpr int kGroups[] = {1};  // every group size shares one kernel per (head_dim, mode)
 constexpr int kNumGroups = 1;
@@ -86,6 +85,7 @@ const DeviceInfo* device_info(int* status) {
       cudaError_t e = kvops_device_setup();
       if (e == cudaSuccess) e = prefill_device_setup();
       if (e == cudaSuccess) e = step_device_setup();
+      if (e == cudaSuccess) e = prefill_attention_device_setup();
       if (e != cudaSuccess) {
         cudaGetLastError();
         *status = PKV_ERR_CUDA_BASE + (int)e;
@@ -115,21 +115,6 @@ PFN_cuTensorMapEncodeTiled_v12000 tensor_map_encoder() {
   return fn;
 }
 
-// A pool [NB, Hkv, 16, D] viewed as a 2-D bf16 tensor of NB*Hkv*16 rows of D elements, read
-// in boxes of 64 columns (128 bytes) x 16 rows with the 128-byte swizzle.
-int encode_pool_map(CUtensorMap* map, const void* base, long long rows, int head_dim) {
-  PFN_cuTensorMapEncodeTiled_v12000 enc = tensor_map_encoder();
-  if (enc == nullptr) return PKV_ERR_NO_DEVICE;
-  const cuuint64_t dims[2] = {(cuuint64_t)head_dim, (cuuint64_t)(rows > 0 ? rows : 1)};
-  const cuuint64_t strides[1] = {(cuuint64_t)head_dim * 2};
-  const cuuint32_t box[2] = {64, 16};
-  const cuuint32_t elem_strides[2] = {1, 1};
-  const CUresult r = enc(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, const_cast<void*>(base), dims, strides, box,
-                         elem_strides, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
-                         CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
-  return r == CUDA_SUCCESS ? PKV_OK : PKV_ERR_ARGUMENT;
-}
-
 // An INT8 pool [NB, Hkv, 16, D] as a 2-D byte tensor of NB*Hkv*16 rows of D bytes, read in
 // one box of D bytes x 16 rows with the swizzle of the row size (128 or 64 bytes).
 int encode_pool_map_q8(CUtensorMap* map, const void* base, long long rows, int head_dim) {
@@ -145,23 +130,6 @@ int encode_pool_map_q8(CUtensorMap* map, const void* base, long long rows, int h
                          CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
   return r == CUDA_SUCCESS ? PKV_OK : PKV_ERR_ARGUMENT;
 }
-
-// The prefill window's queries [B*alpha, Hq, D] bf16 as a 3-D tensor read in boxes of 64
-// columns x G heads x R window rows (one query chunk: G*R columns of 128 bytes each).
-int encode_window_map(CUtensorMap* map, const void* base, long long rows, int num_q_heads, int head_dim, int group,
-                      int chunk_rows) {
-  PFN_cuTensorMapEncodeTiled_v12000 enc = tensor_map_encoder();
-  if (enc == nullptr) return PKV_ERR_NO_DEVICE;
-  const cuuint64_t dims[3] = {(cuuint64_t)head_dim, (cuuint64_t)num_q_heads, (cuuint64_t)(rows > 0 ? rows : 1)};
-  const cuuint64_t strides[2] = {(cuuint64_t)head_dim * 2, (cuuint64_t)num_q_heads * head_dim * 2};
-  const cuuint32_t box[3] = {64, (cuuint32_t)group, (cuuint32_t)chunk_rows};
-  const cuuint32_t elem_strides[3] = {1, 1, 1};
-  const CUresult r = enc(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void*>(base), dims, strides, box,
-                         elem_strides, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
-                         CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
-  return r == CUDA_SUCCESS ? PKV_OK : PKV_ERR_ARGUMENT;
-}
-
 
 // Merge warps per output row (log2), from an upper estimate of the partials a row has: one
 // more warp per PKV_MERGE_PARTIALS_PER_WARP partials, at most 8, and no more than the GPU holds
@@ -189,6 +157,37 @@ size_t align256(size_t x) { return (x + 255) & ~size_t(255); }
 
 }  // namespace
 
+// A pool [NB, Hkv, 16, D] viewed as a 2-D bf16 tensor of NB*Hkv*16 rows of D elements, read
+// in boxes of 64 columns (128 bytes) x 16 rows with the 128-byte swizzle.
+int encode_pool_map(CUtensorMap* map, const void* base, long long rows, int head_dim) {
+  PFN_cuTensorMapEncodeTiled_v12000 enc = tensor_map_encoder();
+  if (enc == nullptr) return PKV_ERR_NO_DEVICE;
+  const cuuint64_t dims[2] = {(cuuint64_t)head_dim, (cuuint64_t)(rows > 0 ? rows : 1)};
+  const cuuint64_t strides[1] = {(cuuint64_t)head_dim * 2};
+  const cuuint32_t box[2] = {64, 16};
+  const cuuint32_t elem_strides[2] = {1, 1};
+  const CUresult r = enc(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, const_cast<void*>(base), dims, strides, box,
+                         elem_strides, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+                         CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  return r == CUDA_SUCCESS ? PKV_OK : PKV_ERR_ARGUMENT;
+}
+
+// The prefill window's queries [B*alpha, Hq, D] bf16 as a 3-D tensor read in boxes of 64
+// columns x G heads x R window rows (one query chunk: G*R columns of 128 bytes each).
+int encode_window_map(CUtensorMap* map, const void* base, long long rows, int num_q_heads, int head_dim, int group,
+                      int chunk_rows) {
+  PFN_cuTensorMapEncodeTiled_v12000 enc = tensor_map_encoder();
+  if (enc == nullptr) return PKV_ERR_NO_DEVICE;
+  const cuuint64_t dims[3] = {(cuuint64_t)head_dim, (cuuint64_t)num_q_heads, (cuuint64_t)(rows > 0 ? rows : 1)};
+  const cuuint64_t strides[2] = {(cuuint64_t)head_dim * 2, (cuuint64_t)num_q_heads * head_dim * 2};
+  const cuuint32_t box[3] = {64, (cuuint32_t)group, (cuuint32_t)chunk_rows};
+  const cuuint32_t elem_strides[3] = {1, 1, 1};
+  const CUresult r = enc(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void*>(base), dims, strides, box,
+                         elem_strides, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+                         CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  return r == CUDA_SUCCESS ? PKV_OK : PKV_ERR_ARGUMENT;
+}
+
 bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
 
 int check_dims(const pkv_dims* d, bool need_q_heads) {
@@ -214,9 +213,10 @@ int check_rules(const pkv_score_rules* r) {
 
 int cuda_status(cudaError_t e) { return e == cudaSuccess ? PKV_OK : PKV_ERR_CUDA_BASE + (int)e; }
 
-int device_ready() {
+int device_ready(int* sms) {
   int st = PKV_OK;
-  (void)device_info(&st);
+  const DeviceInfo* info = device_info(&st);
+  if (info != nullptr && sms != nullptr) *sms = info->sm_count;
   return st;
 }
 

@@ -288,6 +288,9 @@ cudaError_t launch_step_tables(const StepArgs& a, cudaStream_t stream);
 
 // Attention of many query tokens per sequence (prefill_attention.cu).
 struct PrefillAttnArgs {
+  CUtensorMap tmap_k;            // the K pool as [NB*Hkv*16, D] bf16, box 64 x 16, 128-byte swizzle
+  CUtensorMap tmap_v;            // the V pool likewise
+  CUtensorMap tmap_q;            // q as [T, Hq, D] bf16, box 64 x G x R, 128-byte swizzle
   const __nv_bfloat16* q;        // [T, Hq, D] packed query rows
   const __nv_bfloat16* k_cache;  // [NB, Hkv, 16, D]
   const __nv_bfloat16* v_cache;
@@ -301,16 +304,30 @@ struct PrefillAttnArgs {
   int32_t* err;
   float scale_log2, cap_log2, cap_in;  // as DecodeArgs
   int B, T, Hq, Hkv, NB, MB, G, window;
+  int R;                         // tokens of a 128-row tile (128 / G)
+  int sms, slots;                // SMs; CTAs resident at a time
+  int* plan_total;               // the plan: items in the list
+  int4* plan_items;              // (sequence, row tile group, share, shares)
+  int2* plan_seq;                // per sequence: shares, first partial row
+  float2* part_ml;               // partial rows: (running max in base 2, running sum)
+  float* part_o;                 // partial rows, unnormalised [.., D]
+  int max_items, max_rows;
+  unsigned long long timeout_ns; // bound of every mbarrier wait
 };
-size_t prefill_attention_workspace(int B, int T, int G, int D);
-cudaError_t launch_prefill_attention(const PrefillAttnArgs& a, int head_dim, cudaStream_t stream);
+size_t prefill_attention_workspace(int B, int T, int Hq, int G, int D);
+cudaError_t prefill_attention_device_setup();
+cudaError_t launch_prefill_attention(const PrefillAttnArgs& a, void* workspace, int head_dim, cudaStream_t stream);
 
 // Host-side checks shared by the entry points (api.cu).
 int check_dims(const struct pkv_dims* d, bool need_q_heads);
 bool aligned16(const void* p);
 int cuda_status(cudaError_t e);
 int check_rules(const struct pkv_score_rules* r);
-int device_ready();  // one-time set-up of the current device; a PKV status
+int device_ready(int* sms = nullptr);  // one-time set-up of the current device; a PKV status
+int encode_pool_map(CUtensorMap* map, const void* base, long long rows, int head_dim);
+int encode_window_map(CUtensorMap* map, const void* base, long long rows, int num_q_heads, int head_dim, int group,
+                      int chunk_rows);
+constexpr unsigned long long kWaitTimeoutNs = 2000000000ull;  // 2 s per mbarrier wait
 
 // Launches `kernel` with programmatic stream serialisation (it may start before the previous
 // kernel on the stream ends; every kernel of this library waits for it before touching

@@ -1,9 +1,28 @@
 // prefill_attention.cu -- attention of many query tokens per sequence over the paged cache, with
-// score rules, for sm_103a.  Declared in pkv_step.h.
+// score rules, on the 5th-generation tensor cores (sm_103a).  Declared in pkv_step.h.
 //
 // out[r, h] = sum_t p_t V_t, p = softmax over the keys t that row r sees, of
 //   x_t = cap(scale q . K_t) - slope_h |i - t|,
 // i the row's position, visible keys [lo, i] and the prefix [0, pre).
+//
+// Three kernels:
+//  * prefill_plan_kernel cuts the batch into work items -- NT row tiles of 128 rows (tokens x the G
+//    heads of a kv head) of one sequence, and, where there are fewer of those than the GPU holds, a
+//    share of their keys -- and checks every sequence.
+//  * prefill_attention_kernel runs the items, one CTA (or two) per SM, each for one kv head.  Q tiles
+//    and a ring of 128-key K and V tiles (8 cache blocks each) come by TMA.  One thread issues the
+//    MMAs: S = Q K^T into tensor memory, and O += P V with P in tensor memory where S was and V read
+//    as it lies (MN-major).  Each row tile has 4 softmax warps, a row a thread: they read S, apply the
+//    rules, keep the running maximum (moved only when exceeded by 2^8, and O rescaled then) and sum,
+//    and write P.  With two row tiles the softmax of one runs under the MMAs of the other.
+//  * prefill_merge_kernel joins the shares of split items by their maxima and sums.
+// P is rounded to bf16 for the product.  Rows over more than kTwoTermTiles key tiles take that one
+// term, and sum the rounded weights, so that the weights used still sum to one: the error beside a
+// bf16 output's own rounding is of the same size (2^-9 of each weight, independent from key to key).
+// Shorter rows, where few weights may carry the result, add the remainder as a second term.
+// Non-finite V: a masked key's weight is 0, and 0 * NaN is NaN, so V rows past the sequence are cleared,
+// and an output row that is not finite is computed again key by key over what it sees.
+// Every wait is bounded; bad block ids are cleared tiles, recorded.
 #include <algorithm>
 #include <cmath>
 
@@ -44,83 +63,761 @@ __device__ __forceinline__ int interval_start(const PrefillAttnArgs& a, int r, i
   return lo;
 }
 
-// One row, one warp: each lane holds D / 32 elements, keys one at a time, online softmax.
+constexpr int kKeys = 128;           // keys per K/V tile
+constexpr int kTileBlocks = kKeys / 16;
+constexpr int kHalf = kKeys * 128;   // bytes of one 64-element half of a tile
+constexpr float kSlack = 8.0f;       // the running maximum moves only when exceeded by this (base 2)
+constexpr int kTwoTermTiles = 4;     // rows over at most this many key tiles take P as two bf16 terms
+constexpr int kMinChunk = 4;         // key tiles of a split item at least
+
+template <int D, int NT>
+struct Geo {
+  static constexpr int kHalves = D / 64;
+  static constexpr int kTile = kHalves * kHalf;  // bytes of a Q, K or V tile
+  static constexpr int kSlots = NT == 2 ? (D == 128 ? 4 : 8) : (D == 128 ? 2 : 5);
+  static constexpr int kThreads = NT * 128 + 64;
+  static constexpr int kCtas = NT == 1 ? 2 : 1;  // per SM (shared and tensor memory allow no more)
+  static constexpr uint32_t kTmemCols = NT * (kKeys + D) <= 256 ? 256 : 512;
+  static constexpr size_t kSmem = 1024 + (size_t)(NT + kSlots) * kTile;
+};
+
+// ------------------------------------------------------------------------------------ the plan
+//
+// Sequence b has ntile_b = ceil(n_b / (NT R)) row tile groups of R = 128 / G tokens a tile, and at most
+// kt_b key tiles each.  The work of all, over twice the resident CTAs, is what an item may hold at most
+// (and kMinChunk at least); longer ones are split.  Items are listed longest rows first within a
+// sequence.
+__global__ void __launch_bounds__(1024) prefill_plan_kernel(const PrefillAttnArgs a, int tokens_per_item) {
+  __shared__ long long s_sum[33];
+  __shared__ long long s_carry[2];
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  grid_dependency_wait();
+  grid_launch_dependents();
+  // exclusive block sum; the total in s_sum[32]
+  auto scan = [&](long long v) -> long long {
+    long long x = v;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const long long t = __shfl_up_sync(kFullMask, x, o);
+      if (lane >= o) x += t;
+    }
+    if (lane == 31) s_sum[warp] = x;
+    __syncthreads();
+    if (warp == 0) {
+      const long long own = lane < (int)(blockDim.x >> 5) ? s_sum[lane] : 0;
+      long long y = own;
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) {
+        const long long t = __shfl_up_sync(kFullMask, y, o);
+        if (lane >= o) y += t;
+      }
+      __syncwarp();
+      s_sum[lane] = y - own;
+      if (lane == 31) s_sum[32] = y;
+    }
+    __syncthreads();
+    return s_sum[warp] + x - v;
+  };
+  auto shape = [&](int b, int& n, int& ntile, int& kt) {
+    const PrefillSeq s = prefill_seq(a, b);
+    n = s.n;
+    ntile = (s.n + tokens_per_item - 1) / tokens_per_item;
+    const int span = a.window > 0 ? (int)min((long long)s.L, (long long)a.window + tokens_per_item) : s.L;
+    const int blocks = min((s.L + 15) >> 4, (span >> 4) + 2 + ((s.pre + 15) >> 4));
+    kt = (blocks + kTileBlocks - 1) / kTileBlocks;
+    return s.err;
+  };
+  long long work = 0;
+  for (int base = 0; base < a.B; base += blockDim.x) {
+    int n = 0, ntile = 0, kt = 0;
+    if (base + tid < a.B) {
+      const int err = shape(base + tid, n, ntile, kt);
+      if (err != 0) record_error(a.err, err);
+    }
+    (void)scan((long long)ntile * kt * a.Hkv);
+    work += s_sum[32];
+    __syncthreads();
+  }
+  long long chunk = max((long long)kMinChunk, (work + 2 * a.slots - 1) / (2 * a.slots));
+  for (;; chunk *= 2) {  // ends: with chunk above every kt_b nothing is split
+    if (tid < 2) s_carry[tid] = 0;
+    __syncthreads();
+    for (int base = 0; base < a.B; base += blockDim.x) {
+      int n = 0, ntile = 0, kt = 0, nsplit = 1;
+      const int b = base + tid;
+      if (b < a.B) {
+        (void)shape(b, n, ntile, kt);
+        nsplit = (int)max(1ll, (kt + chunk - 1) / chunk);
+      }
+      const long long item0 = s_carry[0] + scan((long long)ntile * nsplit);
+      const long long items = s_sum[32];
+      __syncthreads();
+      const long long row0 = s_carry[1] + scan(nsplit > 1 ? (long long)n * a.Hq * nsplit : 0);
+      const long long rows = s_sum[32];
+      __syncthreads();
+      if (b < a.B) {
+        const bool fits = item0 + (long long)ntile * nsplit <= a.max_items;
+        a.plan_seq[b] = make_int2(nsplit, (int)min(row0, (long long)a.max_rows));
+        for (int k = 0; fits && k < ntile * nsplit; ++k)
+          a.plan_items[item0 + k] = make_int4(b, ntile - 1 - k / nsplit, k % nsplit, nsplit);
+      }
+      if (tid == 0) {
+        s_carry[0] += items;
+        s_carry[1] += rows;
+      }
+      __syncthreads();
+    }
+    const long long items = s_carry[0], rows = s_carry[1];
+    __syncthreads();
+    if (rows <= a.max_rows && items <= a.max_items) {
+      if (tid == 0) *a.plan_total = (int)items;
+      return;
+    }
+    if (chunk > (1ll << 31)) {  // cannot be: unsplit items are within max_items
+      if (tid == 0) *a.plan_total = 0;
+      return;
+    }
+  }
+}
+
+// --------------------------------------------------------------------------------- one row again
+//
+// The keys of list entries [e0, e1) that a row sees, one at a time by one warp (lane: D / 32 elements):
+// what the tensor cores compute for the row, without the masked keys.  Base-2 logits.
+struct Row {
+  int b, g, r, h;         // sequence, kv head, packed row, query head
+  int i, lo, pre;         // position, interval start, prefix
+  int e0, e1;             // entries of the key list
+  int pre_units, shift;   // entry e is block e, or e + shift from pre_units on
+};
+
 template <int D>
-__global__ void __launch_bounds__(256) prefill_rows_kernel(const PrefillAttnArgs a) {
+__device__ __noinline__ void exact_row(const PrefillAttnArgs& a, const Row& w, float& m, float& l, float (&o)[D / 32]) {
   constexpr int E = D / 32;
-  const long long item = ((long long)blockIdx.x * blockDim.x + threadIdx.x) >> 5;
+  const int lane = threadIdx.x & 31;
+  float q[E];
+  m = -INFINITY;
+  l = 0.f;
+#pragma unroll
+  for (int e = 0; e < E; ++e) {
+    q[e] = __bfloat162float(a.q[((size_t)w.r * a.Hq + w.h) * D + lane * E + e]);
+    o[e] = 0.f;
+  }
+  const float slope = a.slopes != nullptr ? a.slopes[w.h] * kLog2e : 0.f;
+  for (int en = w.e0; en < w.e1; ++en) {
+    const int blk = en < w.pre_units ? en : en + w.shift;
+    const int phys = a.block_tables[(size_t)w.b * a.MB + blk];
+    if (phys < 0 || phys >= a.NB) continue;
+    for (int c = 0; c < 16; ++c) {
+      const int t = blk * 16 + c;
+      if (!((t >= w.lo && t <= w.i) || t < w.pre)) continue;
+      const size_t row = (((size_t)phys * a.Hkv + w.g) * 16 + c) * D + lane * E;
+      float x = 0.f;
+#pragma unroll
+      for (int e = 0; e < E; ++e) x = fmaf(q[e], __bfloat162float(a.k_cache[row + e]), x);
+#pragma unroll
+      for (int s = 16; s > 0; s >>= 1) x += __shfl_xor_sync(kFullMask, x, s);
+      x *= a.scale_log2;
+      if (a.cap_log2 > 0.f) x = cap_logit(x, a.cap_log2, a.cap_in);
+      x -= slope * fabsf((float)(w.i - t));
+      const float top = fmaxf(m, x);
+      const float ref = top == -INFINITY ? 0.f : top;
+      const float keep = exp2f(m - ref), p = exp2f(x - ref);
+      m = top;
+      l = l * keep + p;
+#pragma unroll
+      for (int e = 0; e < E; ++e) o[e] = o[e] * keep + p * __bfloat162float(a.v_cache[row + e]);
+    }
+  }
+}
+
+// ------------------------------------------------------------------------------- the attention
+
+// The logits of a row tile's 128 keys in base 2, in place: x = cap(S sl2) - slope |i - t|, for the
+// rules that need each key's own value (otherwise the scale goes into the exponent's FMA).  dist[p] is
+// i minus the first token of the tile's block p.
+__device__ __forceinline__ void apply_rules(const PrefillAttnArgs& a, float (&v)[kKeys], float slope2, int i,
+                                            const int (&t0)[kTileBlocks]) {
+  const float sl2 = a.scale_log2;
+  if (a.cap_log2 > 0.f) {
+    // |u| of every key of the warp's rows within the polynomial's range (cap_logit): packed, no division
+    const float ku = sl2 * a.cap_in * 0.34657359f;
+    float top = 0.f;
+#pragma unroll
+    for (int c = 0; c < kKeys; ++c) top = fmaxf(top, fabsf(v[c]));
+    if (__all_sync(kFullMask, top * fabsf(ku) < 0.3f)) {
+      const uint64_t k2 = pack2(ku, ku), c2 = pack2(a.cap_log2, a.cap_log2);
+      const uint64_t p4 = pack2(0.021869488f, 0.021869488f), p3 = pack2(-0.053968254f, -0.053968254f);
+      const uint64_t p2 = pack2(0.13333333f, 0.13333333f), p1 = pack2(-0.33333333f, -0.33333333f), p0 = pack2(1.f, 1.f);
+#pragma unroll
+      for (int c = 0; c < kKeys; c += 2) {
+        const uint64_t u = fmul2(pack2(v[c], v[c + 1]), k2);
+        const uint64_t w = fmul2(u, u);
+        const uint64_t p = ffma2(ffma2(ffma2(ffma2(p4, w, p3), w, p2), w, p1), w, p0);
+        const float2 x = unpack2(fmul2(fmul2(u, c2), p));
+        v[c] = x.x;
+        v[c + 1] = x.y;
+      }
+    } else {
+#pragma unroll
+      for (int c = 0; c < kKeys; ++c) v[c] = cap_logit(v[c] * sl2, a.cap_log2, a.cap_in);
+    }
+  } else {
+#pragma unroll
+    for (int c = 0; c < kKeys; ++c) v[c] *= sl2;
+  }
+  if (a.slopes != nullptr) {
+#pragma unroll
+    for (int p = 0; p < kTileBlocks; ++p) {
+      const float d0 = (float)(i - t0[p]);
+#pragma unroll
+      for (int c = 0; c < 16; ++c) v[16 * p + c] = fmaf(-slope2, fabsf(d0 - (float)c), v[16 * p + c]);
+    }
+  }
+}
+
+template <int D, int NT>
+__global__ void __launch_bounds__(Geo<D, NT>::kThreads, Geo<D, NT>::kCtas)
+prefill_attention_kernel(const __grid_constant__ PrefillAttnArgs a) {
+  using GE = Geo<D, NT>;
+  constexpr int NS = GE::kSlots, H = GE::kHalves;
+  extern __shared__ unsigned char smem_raw[];
+  unsigned char* sq = reinterpret_cast<unsigned char*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  unsigned char* skv = sq + NT * GE::kTile;
+  __shared__ uint64_t q_full, kv_full[NS], kv_empty[NS], s_full[NT], p_full[NT], pv_done[NT];
+  __shared__ uint32_t s_tmem;
+  __shared__ int s_lo_min, s_lo_max[NT], s_abort;
+
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  constexpr int kProducer = NT * 4, kIssuer = NT * 4 + 1;
+  if (threadIdx.x == 0) {
+    mbar_init(&q_full, 1);
+    for (int s = 0; s < NS; ++s) {
+      mbar_init(&kv_full[s], 1);
+      mbar_init(&kv_empty[s], 1);
+    }
+    for (int x = 0; x < NT; ++x) {
+      mbar_init(&s_full[x], 1);
+      mbar_init(&p_full[x], 4);
+      mbar_init(&pv_done[x], 1);
+    }
+    s_abort = 0;
+    fence_mbar_init();
+  }
+  if (warp == 0) {
+    tmem_alloc(&s_tmem, GE::kTmemCols);
+    tmem_relinquish();
+  }
+  grid_dependency_wait();  // the plan
+  grid_launch_dependents();
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = s_tmem;
+  const int G = a.G, R = a.R;
+  const int total = *a.plan_total * a.Hkv;
+  const uint64_t pol_q = l2_policy_evict_first();
+
+  // softmax threads: row tile x, row r of it: token r / G, head r % G
+  const int x = warp >> 2;
+  const int r = 32 * (warp & 3) + lane;
+  const int tok = r / G, head = r - tok * G;
+  const uint32_t t_lane = tmem + ((uint32_t)(32 * (warp & 3)) << 16);
+  // running counts since the kernel's start; their low bits are the barriers' phases
+  uint32_t n_items = 0;     // items run
+  uint32_t n_kv = 0;        // K and V tiles (producer, issuer)
+  uint32_t n_tile[NT] = {}; // key tiles of each row tile (issuer; softmax threads use their own)
+
+  for (int it = blockIdx.x; it < total; it += gridDim.x) {
+    const int4 item = a.plan_items[it / a.Hkv];
+    const int g = it - (it / a.Hkv) * a.Hkv;
+    const int b = item.x;
+    const PrefillSeq s = prefill_seq(a, b);
+    const int tok0 = item.y * NT * R;
+    const int tokens = min(s.n - tok0, NT * R);
+    const int nx = NT == 2 && tokens > R ? 2 : 1;
+    const int pos0 = s.L - s.n + tok0;
+
+    // ---- what the item's rows see
+    if (threadIdx.x == 0) {
+      s_lo_min = 0x7fffffff;
+      for (int y = 0; y < NT; ++y) s_lo_max[y] = 0;
+    }
+    __syncthreads();
+    const bool softmax_warp = warp < NT * 4;
+    const bool valid = softmax_warp && tok < R && x * R + tok < tokens;
+    const int prow = s.q0 + tok0 + x * R + tok;
+    const int i = valid ? pos0 + x * R + tok : -1;
+    const int lo = valid ? interval_start(a, prow, i) : 0;
+    if (softmax_warp && x < nx) {
+      const int lo_min = __reduce_min_sync(kFullMask, valid ? lo : 0x7fffffff);
+      const int lo_max = __reduce_max_sync(kFullMask, lo);
+      if (lane == 0) {
+        atomicMin(&s_lo_min, lo_min);
+        atomicMax(&s_lo_max[x], lo_max);
+      }
+    }
+    __syncthreads();
+    const int i_max = pos0 + tokens - 1, lo_min = s_lo_min;
+    const int pre_units = (s.pre + 15) >> 4;
+    const int first = max(lo_min >> 4, pre_units);
+    const int nblk = pre_units + (lo_min <= i_max ? max((i_max >> 4) - first + 1, 0) : 0);
+    const int shift = first - pre_units;
+    const int nt_all = (nblk + kTileBlocks - 1) / kTileBlocks;
+    const int per = (nt_all + item.w - 1) / item.w;
+    const int ts = min(item.z * per, nt_all);
+    const int nt = min(ts + per, nt_all) - ts;
+    const bool two = nt_all <= kTwoTermTiles;
+    auto block_of = [&](int e) { return e < pre_units ? e : e + shift; };
+
+    if (warp == kProducer) {
+      // -------------------------------------------------------------- TMA producer
+      if (nt > 0) {
+        if (lane == 0) {
+          mbar_arrive_expect_tx(&q_full, (uint32_t)(nx * H * 128 * G * R));
+          for (int y = 0; y < nx; ++y)
+#pragma unroll
+            for (int h = 0; h < H; ++h)
+              tma_load_3d(sq + y * GE::kTile + h * kHalf, &a.tmap_q, h * 64, g * G, s.q0 + tok0 + y * R, &q_full, pol_q);
+        }
+        auto id_of = [&](int j) -> int {  // lane p < 8: the pool block of entry p of key tile j, -1: none
+          const int e = (ts + j) * kTileBlocks + lane;
+          int id = -1;
+          if (lane < kTileBlocks && j < nt && e < nblk) {
+            id = __ldg(a.block_tables + (size_t)b * a.MB + block_of(e));
+            if (id < 0 || id >= a.NB) {
+              record_error(a.err, PKV_DEV_BAD_BLOCK_ID);
+              id = -1;
+            }
+          }
+          return id;
+        };
+        int id = id_of(0);
+        bool ok = true;
+        for (int j = 0; j < nt && ok; ++j) {
+          const int next = id_of(j + 1);
+          const uint32_t have = __ballot_sync(kFullMask, id >= 0);
+          for (int kv = 0; kv < 2 && ok; ++kv, ++n_kv) {
+            const uint32_t slot = n_kv % NS;
+            if (n_kv >= NS) ok = mbar_wait_bounded(&kv_empty[slot], ((n_kv / NS) - 1) & 1u, a.timeout_ns);
+            ok = __all_sync(kFullMask, ok);
+            if (!ok) break;
+            unsigned char* dst = skv + slot * GE::kTile;
+            if (have != 0xffu) {  // blocks past the list (or refused): zeros
+              for (int p = 0; p < kTileBlocks; ++p) {
+                if ((have >> p) & 1u) continue;
+                for (int h = 0; h < H; ++h)
+#pragma unroll
+                  for (int c = 0; c < 4; ++c)
+                    *reinterpret_cast<uint4*>(dst + h * kHalf + p * 2048 + (c * 32 + lane) * 16) = make_uint4(0u, 0u, 0u, 0u);
+              }
+              fence_proxy_async_smem();
+              __syncwarp();
+            }
+            if (lane == 0) mbar_arrive_expect_tx(&kv_full[slot], (uint32_t)(__popc(have) * H * 2048));
+            __syncwarp();
+            if (id >= 0) {
+              const int y = (id * a.Hkv + g) * 16;
+#pragma unroll
+              for (int h = 0; h < H; ++h)
+                tma_load_2d(dst + h * kHalf + lane * 2048, kv == 0 ? &a.tmap_k : &a.tmap_v, h * 64, y, &kv_full[slot],
+                            l2_policy_evict_last());
+            }
+          }
+          id = next;
+        }
+        if (!ok) {
+          if (lane == 0) {
+            record_error(a.err, PKV_DEV_WAIT_TIMEOUT);
+            s_abort = 1;
+            // what is in flight lands before the CTA goes
+            (void)mbar_wait_bounded(&q_full, n_items & 1u, a.timeout_ns);
+            for (uint32_t c = n_kv > NS ? n_kv - NS : 0; c < n_kv; ++c)
+              (void)mbar_wait_bounded(&kv_full[c % NS], (c / NS) & 1u, a.timeout_ns);
+          }
+          __syncwarp();
+        }
+      }
+    } else if (warp == kIssuer) {
+      // ---------------------------------------------------------------- MMA issuer
+      if (lane == 0 && nt > 0) {
+        constexpr uint32_t id_qk = umma_idesc_bf16(128, kKeys), id_pv = umma_idesc_bf16_bmn(128, D);
+        const uint32_t q0 = smem_u32(sq), kv0 = smem_u32(skv);
+        auto qk = [&](int y, uint32_t slot) {
+          const uint32_t qa = q0 + y * GE::kTile, kb = kv0 + slot * GE::kTile;
+#pragma unroll
+          for (int k = 0; k < D / 16; ++k) {
+            const uint32_t off = (uint32_t)((k >> 2) * kHalf + (k & 3) * 32);
+            umma_bf16(tmem + y * kKeys, umma_desc_sw128(qa + off), umma_desc_sw128(kb + off), id_qk, k > 0);
+          }
+          umma_commit(&s_full[y]);
+        };
+        auto pv = [&](int y, uint32_t slot, bool first_tile) {
+          const uint32_t vb = kv0 + slot * GE::kTile, o = tmem + NT * kKeys + y * D, p = tmem + y * kKeys;
+#pragma unroll
+          for (int k = 0; k < kKeys / 16; ++k)  // chunk k / 2: first terms, then remainders, 16 columns each
+            umma_bf16_ts(o, p + 32 * (k >> 1) + 8 * (k & 1), umma_desc_mn_sw128(vb + k * 2048, kHalf), id_pv,
+                         !first_tile || k > 0);
+          if (two) {
+#pragma unroll
+            for (int k = 0; k < kKeys / 16; ++k)
+              umma_bf16_ts(o, p + 32 * (k >> 1) + 16 + 8 * (k & 1), umma_desc_mn_sw128(vb + k * 2048, kHalf), id_pv, true);
+          }
+          umma_commit(&pv_done[y]);
+        };
+        auto wait = [&](uint64_t* bar, uint32_t phase) {
+          if (mbar_wait_bounded(bar, phase & 1u, a.timeout_ns)) return true;
+          record_error(a.err, PKV_DEV_WAIT_TIMEOUT);
+          s_abort = 1;
+          return false;
+        };
+        bool ok = wait(&q_full, n_items) && wait(&kv_full[n_kv % NS], n_kv / NS);
+        if (ok) {
+          tc_fence_after();
+          for (int y = 0; y < nx; ++y) qk(y, n_kv % NS);
+          umma_commit(&kv_empty[n_kv % NS]);
+          ++n_kv;
+        }
+        for (int j = 0; j < nt && ok; ++j) {
+          const uint32_t vs = n_kv % NS, ks = (n_kv + 1) % NS;
+          ok = wait(&kv_full[vs], n_kv / NS);
+          for (int y = 0; y < nx && ok; ++y) {
+            ok = wait(&p_full[y], n_tile[y]);
+            if (ok && y == 0 && j + 1 < nt) ok = wait(&kv_full[ks], (n_kv + 1) / NS);
+            if (!ok) break;
+            tc_fence_after();
+            pv(y, vs, j == 0);
+            ++n_tile[y];
+            if (j + 1 < nt) qk(y, ks);
+          }
+          if (!ok) break;
+          umma_commit(&kv_empty[vs]);
+          if (j + 1 < nt) umma_commit(&kv_empty[ks]);
+          n_kv += j + 1 < nt ? 2 : 1;
+        }
+        if (!ok) {  // the MMAs in flight end before tensor memory goes
+          umma_commit(&kv_empty[0]);
+          (void)mbar_wait_bounded(&kv_empty[0], 0, a.timeout_ns / 64);
+          (void)mbar_wait_bounded(&kv_empty[0], 1, a.timeout_ns / 64);
+        }
+      }
+    } else if (x < nx) {
+      // ------------------------------------------------------------------ softmax
+      const float slope2 = valid && a.slopes != nullptr ? __ldg(a.slopes + g * G + head) * kLog2e : 0.f;
+      const int pre = valid ? s.pre : 0;
+      const bool own_logits = a.cap_log2 > 0.f || a.slopes != nullptr || !(a.scale_log2 > 0.f);
+      const float mul = own_logits ? 1.f : a.scale_log2;
+      const int i_min = pos0 + x * R, lo_max = s_lo_max[x];
+      // the block that ends past the sequence: its V rows there are cleared by the first row tile's warps
+      const int last_blk = (s.L - 1) >> 4;
+      const int e_last = last_blk < pre_units ? last_blk : last_blk - shift;
+      const int tail_tile = (s.L & 15) != 0 && e_last >= 0 && e_last < nblk && block_of(e_last) == last_blk
+                                ? e_last / kTileBlocks - ts : -1;
+      const uint32_t ts_addr = t_lane + x * kKeys, to_addr = t_lane + NT * kKeys + x * D;
+      float m = -INFINITY, l = 0.f;
+      bool ok = true;
+      for (int j = 0; j < nt; ++j) {
+        ok = __all_sync(kFullMask, mbar_wait_bounded(&s_full[x], n_tile[0] & 1u, a.timeout_ns));
+        if (!ok) break;
+        tc_fence_after();
+        float v[kKeys];
+#pragma unroll
+        for (int c = 0; c < kKeys / 32; ++c) tmem_ld_x32(ts_addr + 32 * c, *reinterpret_cast<float(*)[32]>(v + 32 * c));
+        tmem_wait_ld();
+        const int e0 = (ts + j) * kTileBlocks;
+        int t0[kTileBlocks];
+#pragma unroll
+        for (int p = 0; p < kTileBlocks; ++p) t0[p] = block_of(e0 + p) * 16;
+        if (own_logits) apply_rules(a, v, slope2, i, t0);
+        // all keys of the tile seen by all rows of the row tile?
+        const bool full = (e0 >= pre_units && t0[0] >= lo_max && t0[0] + kKeys - 1 <= i_min) ||
+                          (e0 + kTileBlocks <= pre_units && t0[0] + kKeys <= s.pre);
+        if (!full) {
+#pragma unroll
+          for (int p = 0; p < kTileBlocks; ++p) {
+            const int hi_c = i - t0[p], lo_c = lo - t0[p], pre_c = pre - t0[p];
+            uint32_t see = hi_c >= 15 ? 0xffffu : hi_c < 0 ? 0u : (2u << hi_c) - 1u;
+            see &= lo_c <= 0 ? 0xffffu : lo_c > 15 ? 0u : 0xffffu << lo_c;
+            see |= pre_c >= 16 ? 0xffffu : pre_c <= 0 ? 0u : (1u << pre_c) - 1u;
+#pragma unroll
+            for (int c = 0; c < 16; ++c) v[16 * p + c] = ((see >> c) & 1u) ? v[16 * p + c] : -INFINITY;
+          }
+        }
+        float mx = v[0];
+#pragma unroll
+        for (int c = 1; c < kKeys; ++c) mx = fmaxf(mx, v[c]);
+        mx *= mul;
+        const bool move = mx > m + kSlack;
+        if (__any_sync(kFullMask, move)) {
+          const float scale = move ? ex2_approx(m - mx) : 1.f;
+          if (move) m = mx;
+          l *= scale;
+          if (j > 0) {  // O moves to the new reference once the last product has ended
+            ok = __all_sync(kFullMask, mbar_wait_bounded(&pv_done[x], (n_tile[0] - 1) & 1u, a.timeout_ns));
+            if (!ok) break;
+            tc_fence_after();
+#pragma unroll
+            for (int c = 0; c < D / 32; ++c) {
+              float o[32];
+              tmem_ld_x32(to_addr + 32 * c, o);
+              tmem_wait_ld();
+#pragma unroll
+              for (int k = 0; k < 32; ++k) o[k] *= scale;
+              tmem_st_x32(to_addr + 32 * c, o);
+            }
+          }
+        }
+        const float ref = m == -INFINITY ? 0.f : m;
+        const uint64_t mul2 = pack2(mul, mul), nref2 = pack2(-ref, -ref);
+        uint64_t sum2 = pack2(0.f, 0.f);
+#pragma unroll
+        for (int c = 0; c < kKeys / 32; ++c) {
+          uint32_t hi[16];
+#pragma unroll
+          for (int k = 0; k < 16; ++k) {
+            const float2 y = unpack2(ffma2(pack2(v[32 * c + 2 * k], v[32 * c + 2 * k + 1]), mul2, nref2));
+            const float p0 = ex2_approx(y.x), p1 = ex2_approx(y.y);
+            hi[k] = pack_bf16x2(p0, p1);
+            v[32 * c + 2 * k] = p0;
+            v[32 * c + 2 * k + 1] = p1;
+            if (!two) sum2 = fadd2(sum2, bf16x2_to_f32x2(hi[k]));
+          }
+          tmem_st_x16(ts_addr + 32 * c, hi);
+          if (two) {
+#pragma unroll
+            for (int k = 0; k < 16; ++k) {
+              const float p0 = v[32 * c + 2 * k], p1 = v[32 * c + 2 * k + 1];
+              sum2 = fadd2(sum2, pack2(p0, p1));
+              hi[k] = pack_bf16x2(p0 - bf16_lo_to_f32(hi[k]), p1 - bf16_hi_to_f32(hi[k]));
+            }
+            tmem_st_x16(ts_addr + 32 * c + 16, hi);
+          }
+        }
+        const float2 sum = unpack2(sum2);
+        l += sum.x + sum.y;
+        if (x == 0 && j == tail_tile) {
+          const uint32_t vtile = n_kv + 2 * j + 1;  // this tile's V in the count of K and V tiles
+          ok = __all_sync(kFullMask, mbar_wait_bounded(&kv_full[vtile % NS], (vtile / NS) & 1u, a.timeout_ns));
+          if (!ok) break;
+          unsigned char* rows = skv + (vtile % NS) * GE::kTile + (e_last % kTileBlocks) * 2048;
+          const int gone = 16 - (s.L & 15);
+          for (int c = r; c < gone * 8 * H; c += 128)
+            *reinterpret_cast<uint4*>(rows + (c / (gone * 8)) * kHalf + (s.L & 15) * 128 + (c % (gone * 8)) * 16) =
+                make_uint4(0u, 0u, 0u, 0u);
+          fence_proxy_async_smem();
+        }
+        tmem_wait_st();
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&p_full[x]);
+        ++n_tile[0];
+      }
+      if (ok && nt > 0) {
+        ok = __all_sync(kFullMask, mbar_wait_bounded(&pv_done[x], (n_tile[0] - 1) & 1u, a.timeout_ns));
+        tc_fence_after();
+      }
+      if (!ok) {
+        if (lane == 0) {
+          record_error(a.err, PKV_DEV_WAIT_TIMEOUT);
+          s_abort = 1;
+        }
+      } else {
+        // ---- the rows out: bf16, or this share's unnormalised row with its maximum and sum
+        const bool split = item.w > 1;
+        const int h = g * G + head;
+        const long long part = split ? (long long)a.plan_seq[b].y + ((long long)item.z * s.n + (prow - s.q0)) * a.Hq + h : 0;
+        const float f = split ? 1.f : (l > 0.f ? 1.f / l : 0.f);
+        bool bad = false;
+#pragma unroll
+        for (int c = 0; c < D / 32; ++c) {
+          float o[32];
+          __syncwarp();
+          if (nt > 0) {
+            tmem_ld_x32(to_addr + 32 * c, o);
+            tmem_wait_ld();
+          }
+#pragma unroll
+          for (int k = 0; k < 32; ++k) {
+            o[k] = nt > 0 ? o[k] * f : 0.f;
+            bad |= !(fabsf(o[k]) <= 3.4028234e38f);
+          }
+          if (valid && split) {
+            float4* dst = reinterpret_cast<float4*>(a.part_o + part * D + 32 * c);
+#pragma unroll
+            for (int k = 0; k < 8; ++k) dst[k] = make_float4(o[4 * k], o[4 * k + 1], o[4 * k + 2], o[4 * k + 3]);
+          } else if (valid) {
+            uint4* dst = reinterpret_cast<uint4*>(a.out + ((size_t)prow * a.Hq + h) * D + 32 * c);
+#pragma unroll
+            for (int k = 0; k < 4; ++k)
+              dst[k] = make_uint4(pack_bf16x2(o[8 * k], o[8 * k + 1]), pack_bf16x2(o[8 * k + 2], o[8 * k + 3]),
+                                  pack_bf16x2(o[8 * k + 4], o[8 * k + 5]), pack_bf16x2(o[8 * k + 6], o[8 * k + 7]));
+          }
+        }
+        if (split && valid) a.part_ml[part] = make_float2(m, l);
+        // rows that are not finite: key by key over what they see
+        uint32_t again = __ballot_sync(kFullMask, valid && (bad || !(l <= 3.4028234e38f)));
+        __syncwarp();
+        while (again != 0u) {
+          const int src = __ffs(again) - 1;
+          again &= again - 1;
+          Row w;
+          w.b = b;
+          w.g = g;
+          w.r = __shfl_sync(kFullMask, prow, src);
+          w.h = __shfl_sync(kFullMask, h, src);
+          w.i = __shfl_sync(kFullMask, i, src);
+          w.lo = __shfl_sync(kFullMask, lo, src);
+          w.pre = __shfl_sync(kFullMask, pre, src);
+          w.e0 = ts * kTileBlocks;
+          w.e1 = min((ts + nt) * kTileBlocks, nblk);
+          w.pre_units = pre_units;
+          w.shift = shift;
+          const long long wp = __shfl_sync(kFullMask, part, src);
+          float wm, wl, wo[D / 32];
+          exact_row<D>(a, w, wm, wl, wo);
+          const float wf = split ? 1.f : (wl > 0.f ? 1.f / wl : (wl == wl ? 0.f : wl));
+#pragma unroll
+          for (int e = 0; e < D / 32; ++e) {
+            if (split) a.part_o[wp * D + lane * (D / 32) + e] = wo[e];
+            else a.out[((size_t)w.r * a.Hq + w.h) * D + lane * (D / 32) + e] = __float2bfloat16_rn(wo[e] * wf);
+          }
+          if (split && lane == 0) a.part_ml[wp] = make_float2(wm, wl);
+        }
+      }
+    }
+    // every role leaves the item together: the producer's and issuer's counts are the item's tiles
+    if (warp < NT * 4) n_kv += 2 * nt;
+    ++n_items;
+    if (nt == 0) --n_items;  // no Q was loaded
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    if (s_abort != 0) break;
+  }
+  __syncthreads();
+  if (warp == 0) tmem_dealloc(tmem, GE::kTmemCols);
+}
+
+// ------------------------------------------------------------------------------------ the merge
+
+template <int D>
+__global__ void __launch_bounds__(256) prefill_merge_kernel(const PrefillAttnArgs a) {
+  constexpr int E = D / 32;
   const int lane = threadIdx.x & 31;
   grid_dependency_wait();
   grid_launch_dependents();
-  if (item < a.B && lane == 0) {
-    const PrefillSeq s = prefill_seq(a, (int)item);
-    if (s.err != 0) record_error(a.err, s.err);
-  }
-  if (item >= (long long)a.T * a.Hq) return;
-  const int r = (int)(item / a.Hq), h = (int)(item - (long long)r * a.Hq);
-  int lo_b = 0, hi_b = a.B;
-  while (hi_b - lo_b > 1) {
-    const int mid = (lo_b + hi_b) >> 1;
-    if (a.query_starts[mid] <= r) lo_b = mid; else hi_b = mid;
-  }
-  const int b = lo_b;
-  const PrefillSeq s = prefill_seq(a, b);
-  if (r < s.q0 || r >= s.q0 + s.n) return;
-  const int i = s.L - s.n + (r - s.q0), g = h / a.G;
-  int lo = interval_start(a, r, i);
-  const int pre = s.pre;
-  float q[E], o[E], m = -INFINITY, l = 0.f;
-#pragma unroll
-  for (int e = 0; e < E; ++e) {
-    q[e] = __bfloat162float(a.q[((size_t)r * a.Hq + h) * D + lane * E + e]);
-    o[e] = 0.f;
-  }
-  const float slope = a.slopes != nullptr ? a.slopes[h] * kLog2e : 0.f;
-  for (int t = 0; t < max(pre, i + 1); ++t) {
-    if (t >= pre && t < lo) {
-      t = lo;
-      if (t > i) break;
+  const long long rows = (long long)a.T * a.Hq;
+  for (long long row = ((long long)blockIdx.x * blockDim.x + threadIdx.x) >> 5; row < rows;
+       row += ((long long)gridDim.x * blockDim.x) >> 5) {
+    const int r = (int)(row / a.Hq);
+    int lo = 0, hi = a.B;
+    while (hi - lo > 1) {
+      const int mid = (lo + hi) >> 1;
+      if (a.query_starts[mid] <= r) lo = mid; else hi = mid;
     }
-    const int phys = a.block_tables[(size_t)b * a.MB + (t >> 4)];
-    if (phys < 0 || phys >= a.NB) {
-      if (lane == 0) record_error(a.err, PKV_DEV_BAD_BLOCK_ID);
-      continue;
+    const int2 plan = a.plan_seq[lo];
+    if (plan.x <= 1) continue;
+    const PrefillSeq s = prefill_seq(a, lo);
+    if (r < s.q0 || r >= s.q0 + s.n) continue;
+    const long long per = (long long)s.n * a.Hq;
+    const long long p0 = plan.y + (long long)(r - s.q0) * a.Hq + (row - (long long)r * a.Hq);
+    float m = -INFINITY;
+    for (int k = 0; k < plan.x; ++k) m = fmaxf(m, a.part_ml[p0 + k * per].x);
+    float l = 0.f, o[E] = {};
+    if (m > -INFINITY) {
+      for (int k = 0; k < plan.x; ++k) {
+        const float2 ml = a.part_ml[p0 + k * per];
+        if (ml.x == -INFINITY && ml.y == 0.f) continue;  // a share that saw nothing
+        const float w = exp2f(ml.x - m);
+        l += w * ml.y;
+#pragma unroll
+        for (int e = 0; e < E; ++e) o[e] += w * a.part_o[(p0 + k * per) * D + lane * E + e];
+      }
     }
-    const size_t row = (((size_t)phys * a.Hkv + g) * 16 + (t & 15)) * D + lane * E;
-    float x = 0.f;
+    const float inv = l > 0.f ? 1.f / l : (l == l ? 0.f : l);
 #pragma unroll
-    for (int e = 0; e < E; ++e) x = fmaf(q[e], __bfloat162float(a.k_cache[row + e]), x);
-#pragma unroll
-    for (int w = 16; w > 0; w >>= 1) x += __shfl_xor_sync(kFullMask, x, w);
-    x *= a.scale_log2;
-    if (a.cap_log2 > 0.f) x = cap_logit(x, a.cap_log2, a.cap_in);
-    x -= slope * fabsf((float)(i - t));
-    const float top = fmaxf(m, x);
-    const float ref = top == -INFINITY ? 0.f : top;
-    const float keep = exp2f(m - ref), p = exp2f(x - ref);
-    m = top;
-    l = l * keep + p;
-#pragma unroll
-    for (int e = 0; e < E; ++e) o[e] = o[e] * keep + p * __bfloat162float(a.v_cache[row + e]);
+    for (int e = 0; e < E; ++e) a.out[row * D + lane * E + e] = __float2bfloat16_rn(o[e] * inv);
   }
-  const float inv = l > 0.f ? 1.f / l : 0.f;
-#pragma unroll
-  for (int e = 0; e < E; ++e) a.out[((size_t)r * a.Hq + h) * D + lane * E + e] = __float2bfloat16_rn(o[e] * inv);
 }
 
 }  // namespace
 
-size_t prefill_attention_workspace(int B, int T, int G, int D) {
-  (void)B; (void)T; (void)G; (void)D;
-  return 256;
+namespace {
+constexpr long long kMaxPartRows = 80000;  // split rows of one call at most (40 MB of partial rows at d = 128)
+constexpr int kMaxSlots = 512;             // resident CTAs that a plan may count on
+
+size_t align256p(size_t x) { return (x + 255) & ~size_t(255); }
+
+struct PrefillWorkspace {
+  size_t items, seq, ml, o, total;
+  long long max_items, max_rows;
+};
+
+// total | int4 items | int2 per sequence | float2 (m, l) | float o.  Items: one per row tile group of one
+// tile (the most that any variant lists) and the shares of split ones.
+PrefillWorkspace plan_prefill(long long B, long long T, int Hq, int G, int D) {
+  PrefillWorkspace w{};
+  const int R = 128 / G;
+  w.max_items = T / R + B + 4 * kMaxSlots;
+  w.max_rows = std::min(kMaxPartRows, T * Hq * 64);
+  w.items = 256;
+  w.seq = align256p(w.items + sizeof(int4) * (size_t)w.max_items);
+  w.ml = align256p(w.seq + sizeof(int2) * (size_t)B);
+  w.o = align256p(w.ml + sizeof(float2) * (size_t)w.max_rows);
+  w.total = align256p(w.o + sizeof(float) * (size_t)w.max_rows * D);
+  return w;
 }
 
-cudaError_t launch_prefill_attention(const PrefillAttnArgs& a, int head_dim, cudaStream_t stream) {
+template <int D, int NT>
+cudaError_t launch_attention(const PrefillAttnArgs& a, cudaStream_t stream) {
+  using GE = Geo<D, NT>;
   PrefillAttnArgs args = a;
+  args.slots = std::min(a.sms * GE::kCtas, kMaxSlots);
+  int per_item = NT * a.R;
+  void* plan_params[] = {&args, &per_item};
+  cudaError_t e = launch_pdl((const void*)prefill_plan_kernel, dim3(1), dim3(a.B > 256 ? 1024 : 256), 0, stream, plan_params);
+  if (e != cudaSuccess) return e;
   void* params[] = {&args};
-  const long long warps = std::max((long long)a.T * a.Hq, (long long)a.B);
-  const void* f = head_dim == 128 ? (const void*)prefill_rows_kernel<128> : (const void*)prefill_rows_kernel<64>;
-  return launch_pdl(f, dim3((unsigned)((warps + 7) / 8)), dim3(256), 0, stream, params);
+  const long long most = ((long long)a.T / per_item + a.B) * a.Hkv + 2 * args.slots;
+  e = launch_pdl((const void*)prefill_attention_kernel<D, NT>, dim3((unsigned)std::min<long long>(most, args.slots)),
+                 dim3(GE::kThreads), GE::kSmem, stream, params);
+  if (e != cudaSuccess) return e;
+  const long long warps = std::min((long long)a.T * a.Hq, 8ll * 8 * a.sms);
+  return launch_pdl((const void*)prefill_merge_kernel<D>, dim3((unsigned)((warps + 7) / 8)), dim3(256), 0, stream, params);
+}
+
+template <int D, int NT>
+cudaError_t setup_attention() {
+  return cudaFuncSetAttribute((const void*)prefill_attention_kernel<D, NT>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                              (int)Geo<D, NT>::kSmem);
+}
+}  // namespace
+
+size_t prefill_attention_workspace(int B, int T, int Hq, int G, int D) { return plan_prefill(B, T, Hq, G, D).total; }
+
+cudaError_t prefill_attention_device_setup() {
+  cudaError_t e = setup_attention<128, 1>();
+  if (e == cudaSuccess) e = setup_attention<128, 2>();
+  if (e == cudaSuccess) e = setup_attention<64, 1>();
+  if (e == cudaSuccess) e = setup_attention<64, 2>();
+  return e;
+}
+
+cudaError_t launch_prefill_attention(const PrefillAttnArgs& a, void* workspace, int head_dim, cudaStream_t stream) {
+  PrefillAttnArgs args = a;
+  const PrefillWorkspace w = plan_prefill(a.B, a.T, a.Hq, a.G, head_dim);
+  unsigned char* ws = static_cast<unsigned char*>(workspace);
+  args.plan_total = reinterpret_cast<int*>(ws);
+  args.plan_items = reinterpret_cast<int4*>(ws + w.items);
+  args.plan_seq = reinterpret_cast<int2*>(ws + w.seq);
+  args.part_ml = reinterpret_cast<float2*>(ws + w.ml);
+  args.part_o = reinterpret_cast<float*>(ws + w.o);
+  args.max_items = (int)w.max_items;
+  args.max_rows = (int)w.max_rows;
+  // two row tiles an item when the sequences fill more than one on average
+  const bool two = (long long)a.T > (long long)a.B * a.R;
+  if (head_dim == 128) return two ? launch_attention<128, 2>(args, stream) : launch_attention<128, 1>(args, stream);
+  return two ? launch_attention<64, 2>(args, stream) : launch_attention<64, 1>(args, stream);
 }
 
 }  // namespace pkv
@@ -147,7 +844,8 @@ extern "C" {
 
 size_t pkv_prefill_workspace_bytes(const pkv_dims* dims, int32_t total_tokens) {
   if (check_prefill(dims, total_tokens) != PKV_OK) return 0;
-  return prefill_attention_workspace(dims->batch, total_tokens, dims->num_q_heads / dims->num_kv_heads, dims->head_dim);
+  return prefill_attention_workspace(dims->batch, total_tokens, dims->num_q_heads,
+                                     dims->num_q_heads / dims->num_kv_heads, dims->head_dim);
 }
 
 int pkv_paged_prefill_attention(void* out, const void* q, const void* k_cache, const void* v_cache,
@@ -166,9 +864,20 @@ int pkv_paged_prefill_attention(void* out, const void* q, const void* k_cache, c
   if (!workspace || workspace_bytes < pkv_prefill_workspace_bytes(dims, total_tokens)) return PKV_ERR_WORKSPACE;
   if (!aligned16(out) || !aligned16(q) || !aligned16(k_cache) || !aligned16(v_cache) || !aligned16(workspace))
     return PKV_ERR_ALIGNMENT;
-  st = device_ready();
+  int sms = 0;
+  st = device_ready(&sms);
   if (st != PKV_OK) return st;
   PrefillAttnArgs a{};
+  const long long pool_rows = (long long)dims->num_blocks * dims->num_kv_heads * PKV_BLOCK_SIZE;
+  const int group = dims->num_q_heads / dims->num_kv_heads;
+  st = encode_pool_map(&a.tmap_k, k_cache, pool_rows, dims->head_dim);
+  if (st == PKV_OK) st = encode_pool_map(&a.tmap_v, v_cache, pool_rows, dims->head_dim);
+  if (st == PKV_OK)
+    st = encode_window_map(&a.tmap_q, q, total_tokens, dims->num_q_heads, dims->head_dim, group, 128 / group);
+  if (st != PKV_OK) return st;
+  a.sms = sms;
+  a.R = 128 / group;
+  a.timeout_ns = kWaitTimeoutNs;
   a.q = static_cast<const __nv_bfloat16*>(q);
   a.k_cache = static_cast<const __nv_bfloat16*>(k_cache);
   a.v_cache = static_cast<const __nv_bfloat16*>(v_cache);
@@ -183,7 +892,7 @@ int pkv_paged_prefill_attention(void* out, const void* q, const void* k_cache, c
   a.Hkv = dims->num_kv_heads;
   a.NB = dims->num_blocks;
   a.MB = dims->max_blocks_per_seq;
-  a.G = dims->num_q_heads / dims->num_kv_heads;
+  a.G = group;
   a.scale_log2 = scale * kLog2e;
   if (rules != nullptr) {
     a.window = rules->window;
@@ -193,7 +902,7 @@ int pkv_paged_prefill_attention(void* out, const void* q, const void* k_cache, c
     a.cap_log2 = rules->softcap * kLog2e;
     a.cap_in = rules->softcap > 0.f ? 2.f / rules->softcap : 0.f;
   }
-  return cuda_status(launch_prefill_attention(a, dims->head_dim, static_cast<cudaStream_t>(stream)));
+  return cuda_status(launch_prefill_attention(a, workspace, dims->head_dim, static_cast<cudaStream_t>(stream)));
 }
 
 }  // extern "C"

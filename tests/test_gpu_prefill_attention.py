@@ -49,7 +49,13 @@ def _rows(c, seed, most=60):
     return [(r, int(h)) for r in sorted(rows) for h in ({0, c["hq"] - 1} | set(rng.integers(0, c["hq"], 2).tolist()))]
 
 
-def _check(c, got, window=0, rows=None, weight_eps=2.0 ** -15, **r):
+def _weight_eps(L):
+    """Half a step of the weights in the product with V: two bf16 terms (2^-8 * 2^-8) over at most four
+    128-key tiles, which a sequence of up to 512 keys cannot exceed; one bf16 term (2^-8) beyond."""
+    return 2.0 ** -16 if L <= 512 else 2.0 ** -8
+
+
+def _check(c, got, window=0, rows=None, **r):
     got = got.float().cpu().double().numpy()
     g = c["hq"] // c["hkv"]
     for row, h in rows or _rows(c, 1):
@@ -61,7 +67,7 @@ def _check(c, got, window=0, rows=None, weight_eps=2.0 ** -15, **r):
             r.get("softcap", 0.0), 0.0 if r.get("alibi_slopes") is None else float(np.float32(r["alibi_slopes"][h])),
             0 if r.get("doc_starts") is None else int(r["doc_starts"][row]),
             0 if r.get("prefix_lens") is None else int(r["prefix_lens"][b]))
-        far = np.abs(got[row, h] - ref) - rules_model.bound(ref, mass, size, c["d"], weight_eps)
+        far = np.abs(got[row, h] - ref) - rules_model.bound(ref, mass, size, c["d"], _weight_eps(L))
         assert np.all(far <= 0), (row, h, b, i, float(far.max()), float(np.abs(got[row, h] - ref).max()))
 
 
@@ -179,7 +185,6 @@ def test_masked_infinities_stay_out(d):
     without them, in whatever tile they share."""
     c = _case([200, 90], [150, 90], 4, 2, d, 7)
     r = _fill_rules(c, dict(window=30, doc_starts=41, prefix_lens=12))
-    want = _call(c, **r)
     bt = c["bt"].cpu()
     at = [(0, 60, float("nan")), (0, 111, float("inf")), (0, 199, -float("inf")), (1, 33, float("nan")), (1, 89, float("nan"))]
     for b, t, x in at:
@@ -187,17 +192,16 @@ def test_masked_infinities_stay_out(d):
         c["pools"][1][blk, :, t % 16, 3:9] = x
         c["pools"][0][blk, :, t % 16, 5] = x
     got = _call(c, **r)
-    clean = 0
+    clean = []
     for row in range(240):
         b = int(row >= 150)
         i = 50 + row if b == 0 else row - 150
         lo = max(0, i - 29, int(r["doc_starts"][row]))
         if any(bb == b and (lo <= t <= i or t < r["prefix_lens"][b]) for bb, t, _ in at):
             continue
-        clean += 1
-        # the same to what another order of sums may change: an output of unit scale, one bf16 step
-        assert torch.allclose(got[row].float(), want[row].float(), rtol=2.0 ** -7, atol=1e-6), row
-    assert clean > 100
+        clean += [(row, h) for h in range(4)]
+    assert len(clean) > 400
+    _check(c, got, rows=clean, **r)  # against the keys as they were before
 
 
 @pytest.mark.gpu
@@ -220,8 +224,9 @@ def test_prefill_of_one_token_equals_the_decode_to_rounding():
     t = {n: torch.tensor(v, dtype=torch.float32 if n[0] == "a" else torch.int32, device=DEV) for n, v in r.items() if n != "softcap"}
     want = pkv.paged_decode_attention_rules(c["q"].to(DEV), *c["pools"], c["bt"], torch.tensor(lens, dtype=torch.int32, device=DEV),
                                             c["scale"], 300, softcap=9.0, **t).float()
-    # each is within half a bf16 step (2^-8 of the value) of the exact result, beside errors below 1e-3 of its size
-    assert torch.allclose(got, want, rtol=2.0 ** -6, atol=2e-3)
+    # each is within half a bf16 step (2^-8 of the value) of the exact result, and the long rows' weights are off by
+    # up to 2^-8 each: 2.1 * 2^-8 of the sum of p |v|, which is below 1.5 for normal values
+    assert torch.allclose(got, want, rtol=2.0 ** -6, atol=2.1 * 2.0 ** -8 * 1.5)
 
 
 @pytest.mark.gpu
@@ -271,7 +276,7 @@ def test_a_run_of_the_operators():
                 for h in range(hq):
                     ref, mass, size = rules_model.row(rows[0][at + j, h].double().numpy(), kk[:, h // 2], vv[:, h // 2],
                                                       len(keys[b]) - n + j, d ** -0.5, 50, 20.0)
-                    far = np.abs(got[at + j, h] - ref) - rules_model.bound(ref, mass, size, d, 2.0 ** -15)
+                    far = np.abs(got[at + j, h] - ref) - rules_model.bound(ref, mass, size, d, _weight_eps(len(keys[b])))
                     assert np.all(far <= 0), (b, j, h)
             at += max(n, 0)
 
