@@ -75,8 +75,13 @@ struct Geo {
   static constexpr int kHalves = D / 64;
   static constexpr int kTile = kHalves * kHalf;  // bytes of a Q, K or V tile
   static constexpr int kSlots = NT == 2 ? (D == 128 ? 4 : 8) : (D == 128 ? 2 : 5);
-  static constexpr int kThreads = NT * 128 + 64;
+  static constexpr int kThreads = NT * 128 + 128;  // softmax warpgroups; producer, issuer and two idle warps
   static constexpr int kCtas = NT == 1 ? 2 : 1;  // per SM (shared and tensor memory allow no more)
+  // Registers a thread: a launch gives every warp the same, which the softmax warps (a row of 128 logits
+  // in registers) then take from the others.  NT = 2: 384 x 168 = 256 x 216 + 128 x 72; NT = 1 (two CTAs):
+  // 256 x 128 = 128 x 184 + 128 x 72.
+  static constexpr int kSoftmaxRegs = NT == 2 ? 216 : 184, kOtherRegs = 72;
+  static_assert(NT * 128 * kSoftmaxRegs + 128 * kOtherRegs <= kThreads * (NT == 2 ? 168 : 128), "register split");
   static constexpr uint32_t kTmemCols = NT * (kKeys + D) <= 256 ? 256 : 512;
   static constexpr size_t kSmem = 1024 + (size_t)(NT + kSlots) * kTile;
 };
@@ -183,7 +188,8 @@ __global__ void __launch_bounds__(1024) prefill_plan_kernel(const PrefillAttnArg
 // --------------------------------------------------------------------------------- one row again
 //
 // The keys of list entries [e0, e1) that a row sees, one at a time by one warp (lane: D / 32 elements):
-// what the tensor cores compute for the row, without the masked keys.  Base-2 logits.
+// what the tensor cores compute for the row, without the masked keys.  Writes the output row, or
+// partial row `part` if that is not negative.
 struct Row {
   int b, g, r, h;         // sequence, kv head, packed row, query head
   int i, lo, pre;         // position, interval start, prefix
@@ -192,12 +198,10 @@ struct Row {
 };
 
 template <int D>
-__device__ __noinline__ void exact_row(const PrefillAttnArgs& a, const Row& w, float& m, float& l, float (&o)[D / 32]) {
+__device__ __noinline__ void exact_row(const PrefillAttnArgs& a, const Row& w, long long part) {
   constexpr int E = D / 32;
   const int lane = threadIdx.x & 31;
-  float q[E];
-  m = -INFINITY;
-  l = 0.f;
+  float q[E], o[E], m = -INFINITY, l = 0.f;
 #pragma unroll
   for (int e = 0; e < E; ++e) {
     q[e] = __bfloat162float(a.q[((size_t)w.r * a.Hq + w.h) * D + lane * E + e]);
@@ -229,15 +233,222 @@ __device__ __noinline__ void exact_row(const PrefillAttnArgs& a, const Row& w, f
       for (int e = 0; e < E; ++e) o[e] = o[e] * keep + p * __bfloat162float(a.v_cache[row + e]);
     }
   }
+  if (part >= 0) {
+#pragma unroll
+    for (int e = 0; e < E; ++e) a.part_o[part * D + lane * E + e] = o[e];
+    if (lane == 0) a.part_ml[part] = make_float2(m, l);
+  } else {
+    const float f = l > 0.f ? 1.f / l : (l == l ? 0.f : l);
+#pragma unroll
+    for (int e = 0; e < E; ++e)
+      a.out[((size_t)w.r * a.Hq + w.h) * D + lane * E + e] = __float2bfloat16_rn(o[e] * f);
+  }
 }
 
 // ------------------------------------------------------------------------------- the attention
 
-// The logits of a row tile's 128 keys in base 2, in place: x = cap(S sl2) - slope |i - t|, for the
-// rules that need each key's own value (otherwise the scale goes into the exponent's FMA).  dist[p] is
-// i minus the first token of the tile's block p.
+// One work item for one kv head, and the key list of its rows: the blocks of the prefix, then those of
+// the union of the rows' intervals, in tiles of 8.
+struct Item {
+  int b, g, split, nsplit;
+  int q0, n, L, pre;      // of the sequence
+  int tok0, tokens, nx;   // first token (of the sequence's queries), tokens, row tiles
+  int pos0;               // position of the first token
+  int pre_units, nblk, shift, nt_all, ts, nt;  // list entries, key tiles of the rows, this share's
+
+  __device__ __forceinline__ int block_of(int e) const { return e < pre_units ? e : e + shift; }
+};
+
+__device__ __forceinline__ Item load_item(const PrefillAttnArgs& a, int it, int NT) {
+  Item w;
+  const int at = it / a.Hkv;
+  const int4 p = a.plan_items[at];
+  const PrefillSeq s = prefill_seq(a, p.x);
+  w.b = p.x;
+  w.g = it - at * a.Hkv;
+  w.split = p.z;
+  w.nsplit = p.w;
+  w.q0 = s.q0;
+  w.n = s.n;
+  w.L = s.L;
+  w.pre = s.pre;
+  w.tok0 = p.y * NT * a.R;
+  w.tokens = min(s.n - w.tok0, NT * a.R);
+  w.nx = NT == 2 && w.tokens > a.R ? 2 : 1;
+  w.pos0 = s.L - s.n + w.tok0;
+  return w;
+}
+
+// lo_min: the least interval start of the item's rows.
+__device__ __forceinline__ void set_keys(Item& w, int lo_min) {
+  const int i_max = w.pos0 + w.tokens - 1;
+  w.pre_units = (w.pre + 15) >> 4;
+  const int first = max(lo_min >> 4, w.pre_units);
+  w.nblk = w.pre_units + (lo_min <= i_max ? max((i_max >> 4) - first + 1, 0) : 0);
+  w.shift = first - w.pre_units;
+  w.nt_all = (w.nblk + kTileBlocks - 1) / kTileBlocks;
+  const int per = (w.nt_all + w.nsplit - 1) / w.nsplit;
+  w.ts = min(w.split * per, w.nt_all);
+  w.nt = min(w.ts + per, w.nt_all) - w.ts;
+}
+
+template <int D, int NT>
+struct Shared {
+  uint64_t q_full, kv_full[Geo<D, NT>::kSlots], kv_empty[Geo<D, NT>::kSlots], s_full[NT], p_full[NT], pv_done[NT];
+  uint32_t tmem;
+  int lo_min, lo_max[NT], abort;
+};
+
+// Loads the item's Q tiles and its K and V tiles through the ring (one warp).  n_kv counts K and V tiles
+// since the kernel's start, n_q loaded items.
+template <int D, int NT>
+__device__ __forceinline__ void produce(const PrefillAttnArgs& a, Shared<D, NT>& sh, const Item& w, unsigned char* sq,
+                                        uint32_t& n_kv, uint32_t n_q) {
+  using GE = Geo<D, NT>;
+  constexpr int NS = GE::kSlots, H = GE::kHalves;
+  const int lane = threadIdx.x & 31;
+  unsigned char* skv = sq + NT * GE::kTile;
+  const uint64_t pol = l2_policy_evict_last();  // K and V tiles are read by every row tile of the sequence
+  if (lane == 0) {
+    const uint64_t pol_q = l2_policy_evict_first();
+    mbar_arrive_expect_tx(&sh.q_full, (uint32_t)(w.nx * H * 128 * a.G * a.R));
+    for (int y = 0; y < w.nx; ++y)
+#pragma unroll
+      for (int h = 0; h < H; ++h)
+        tma_load_3d(sq + y * GE::kTile + h * kHalf, &a.tmap_q, h * 64, w.g * a.G, w.q0 + w.tok0 + y * a.R, &sh.q_full, pol_q);
+  }
+  auto id_of = [&](int j) -> int {  // lane p < 8: the pool block of entry p of key tile j, -1: none
+    const int e = (w.ts + j) * kTileBlocks + lane;
+    int id = -1;
+    if (lane < kTileBlocks && j < w.nt && e < w.nblk) {
+      id = __ldg(a.block_tables + (size_t)w.b * a.MB + w.block_of(e));
+      if (id < 0 || id >= a.NB) {
+        record_error(a.err, PKV_DEV_BAD_BLOCK_ID);
+        id = -1;
+      }
+    }
+    return id;
+  };
+  int id = id_of(0);
+  bool ok = true;
+  for (int j = 0; j < w.nt && ok; ++j) {
+    const int next = id_of(j + 1);
+    const uint32_t have = __ballot_sync(kFullMask, id >= 0);
+    for (int kv = 0; kv < 2; ++kv, ++n_kv) {
+      const uint32_t slot = n_kv % NS;
+      if (n_kv >= NS) ok = mbar_wait_bounded(&sh.kv_empty[slot], ((n_kv / NS) - 1) & 1u, a.timeout_ns);
+      ok = __all_sync(kFullMask, ok);
+      if (!ok) break;
+      unsigned char* dst = skv + slot * GE::kTile;
+      if (have != 0xffu) {  // blocks past the list (or refused): zeros
+        for (int p = 0; p < kTileBlocks; ++p) {
+          if ((have >> p) & 1u) continue;
+          for (int h = 0; h < H; ++h)
+#pragma unroll
+            for (int c = 0; c < 4; ++c)
+              *reinterpret_cast<uint4*>(dst + h * kHalf + p * 2048 + (c * 32 + lane) * 16) = make_uint4(0u, 0u, 0u, 0u);
+        }
+        fence_proxy_async_smem();
+        __syncwarp();
+      }
+      if (lane == 0) mbar_arrive_expect_tx(&sh.kv_full[slot], (uint32_t)(__popc(have) * H * 2048));
+      __syncwarp();
+      if (id >= 0) {
+        const int y = (id * a.Hkv + w.g) * 16;
+#pragma unroll
+        for (int h = 0; h < H; ++h)
+          tma_load_2d(dst + h * kHalf + lane * 2048, kv == 0 ? &a.tmap_k : &a.tmap_v, h * 64, y, &sh.kv_full[slot], pol);
+      }
+    }
+    id = next;
+  }
+  if (!ok) {
+    if (lane == 0) {
+      record_error(a.err, PKV_DEV_WAIT_TIMEOUT);
+      sh.abort = 1;
+      // what is in flight lands before the CTA goes
+      (void)mbar_wait_bounded(&sh.q_full, n_q & 1u, a.timeout_ns);
+      for (uint32_t c = n_kv > NS ? n_kv - NS : 0; c < n_kv; ++c)
+        (void)mbar_wait_bounded(&sh.kv_full[c % NS], (c / NS) & 1u, a.timeout_ns);
+    }
+    __syncwarp();
+  }
+}
+
+// Issues the item's MMAs (one thread).  Per key tile and row tile: O += P V of the tile whose P is ready,
+// then S = Q K^T of the next one into the same columns (the tensor core runs them in the order of issue).
+template <int D, int NT>
+__device__ __forceinline__ void issue_mmas(const PrefillAttnArgs& a, Shared<D, NT>& sh, const Item& w, unsigned char* sq,
+                                           uint32_t tmem, uint32_t& n_kv, uint32_t n_q, uint32_t (&n_tile)[NT]) {
+  using GE = Geo<D, NT>;
+  constexpr int NS = GE::kSlots;
+  constexpr uint32_t id_qk = umma_idesc_bf16(128, kKeys), id_pv = umma_idesc_bf16_bmn(128, D);
+  const uint32_t q0 = smem_u32(sq), kv0 = q0 + NT * GE::kTile;
+  const bool two = w.nt_all <= kTwoTermTiles;
+  auto qk = [&](int y, uint32_t slot) {
+    const uint32_t qa = q0 + y * GE::kTile, kb = kv0 + slot * GE::kTile;
+#pragma unroll
+    for (int k = 0; k < D / 16; ++k) {
+      const uint32_t off = (uint32_t)((k >> 2) * kHalf + (k & 3) * 32);
+      umma_bf16(tmem + y * kKeys, umma_desc_sw128(qa + off), umma_desc_sw128(kb + off), id_qk, k > 0);
+    }
+    umma_commit(&sh.s_full[y]);
+  };
+  auto pv = [&](int y, uint32_t slot, bool first_tile) {
+    const uint32_t vb = kv0 + slot * GE::kTile, o = tmem + NT * kKeys + y * D, p = tmem + y * kKeys;
+#pragma unroll
+    for (int k = 0; k < kKeys / 16; ++k)  // 32 keys' first terms, then their remainders, 16 columns each
+      umma_bf16_ts(o, p + 32 * (k >> 1) + 8 * (k & 1), umma_desc_mn_sw128(vb + k * 2048, kHalf), id_pv,
+                   !first_tile || k > 0);
+    if (two) {
+#pragma unroll
+      for (int k = 0; k < kKeys / 16; ++k)
+        umma_bf16_ts(o, p + 32 * (k >> 1) + 16 + 8 * (k & 1), umma_desc_mn_sw128(vb + k * 2048, kHalf), id_pv, true);
+    }
+    umma_commit(&sh.pv_done[y]);
+  };
+  auto wait = [&](uint64_t* bar, uint32_t phase) {
+    if (mbar_wait_bounded(bar, phase & 1u, a.timeout_ns)) return true;
+    record_error(a.err, PKV_DEV_WAIT_TIMEOUT);
+    sh.abort = 1;
+    return false;
+  };
+  bool ok = wait(&sh.q_full, n_q) && wait(&sh.kv_full[n_kv % NS], n_kv / NS);
+  if (ok) {
+    tc_fence_after();
+    for (int y = 0; y < w.nx; ++y) qk(y, n_kv % NS);
+    umma_commit(&sh.kv_empty[n_kv % NS]);
+    ++n_kv;
+  }
+  for (int j = 0; j < w.nt && ok; ++j) {
+    const uint32_t vs = n_kv % NS, ks = (n_kv + 1) % NS;
+    const bool more = j + 1 < w.nt;
+    ok = wait(&sh.kv_full[vs], n_kv / NS);
+    for (int y = 0; y < w.nx && ok; ++y) {
+      ok = wait(&sh.p_full[y], n_tile[y]);
+      if (ok && y == 0 && more) ok = wait(&sh.kv_full[ks], (n_kv + 1) / NS);
+      if (!ok) break;
+      tc_fence_after();
+      pv(y, vs, j == 0);
+      ++n_tile[y];
+      if (more) qk(y, ks);
+    }
+    if (!ok) break;
+    umma_commit(&sh.kv_empty[vs]);
+    if (more) umma_commit(&sh.kv_empty[ks]);
+    n_kv += more ? 2 : 1;
+  }
+  if (!ok) {  // the MMAs in flight end before tensor memory goes
+    umma_commit(&sh.kv_empty[0]);
+    (void)mbar_wait_bounded(&sh.kv_empty[0], 0, a.timeout_ns / 64);
+    (void)mbar_wait_bounded(&sh.kv_empty[0], 1, a.timeout_ns / 64);
+  }
+}
+
+// The logits of a row's 128 keys in base 2, in place: x = cap(S sl2) - slope |i - t|, for the rules that
+// need each key's own value (otherwise the scale goes into the exponent's FMA).
 __device__ __forceinline__ void apply_rules(const PrefillAttnArgs& a, float (&v)[kKeys], float slope2, int i,
-                                            const int (&t0)[kTileBlocks]) {
+                                            const Item& w, int e0) {
   const float sl2 = a.scale_log2;
   if (a.cap_log2 > 0.f) {
     // |u| of every key of the warp's rows within the polynomial's range (cap_logit): packed, no division
@@ -252,8 +463,8 @@ __device__ __forceinline__ void apply_rules(const PrefillAttnArgs& a, float (&v)
 #pragma unroll
       for (int c = 0; c < kKeys; c += 2) {
         const uint64_t u = fmul2(pack2(v[c], v[c + 1]), k2);
-        const uint64_t w = fmul2(u, u);
-        const uint64_t p = ffma2(ffma2(ffma2(ffma2(p4, w, p3), w, p2), w, p1), w, p0);
+        const uint64_t q = fmul2(u, u);
+        const uint64_t p = ffma2(ffma2(ffma2(ffma2(p4, q, p3), q, p2), q, p1), q, p0);
         const float2 x = unpack2(fmul2(fmul2(u, c2), p));
         v[c] = x.x;
         v[c + 1] = x.y;
@@ -269,10 +480,194 @@ __device__ __forceinline__ void apply_rules(const PrefillAttnArgs& a, float (&v)
   if (a.slopes != nullptr) {
 #pragma unroll
     for (int p = 0; p < kTileBlocks; ++p) {
-      const float d0 = (float)(i - t0[p]);
+      const float d0 = (float)(i - w.block_of(e0 + p) * 16);
 #pragma unroll
       for (int c = 0; c < 16; ++c) v[16 * p + c] = fmaf(-slope2, fabsf(d0 - (float)c), v[16 * p + c]);
     }
+  }
+}
+
+// The item's softmax and output for this thread's row of row tile x: position i (-1: none), interval start
+// lo, prefix pre; prow and h name the output row.
+template <int D, int NT>
+__device__ __forceinline__ void softmax_rows(const PrefillAttnArgs& a, Shared<D, NT>& sh, const Item& w,
+                                             unsigned char* sq, uint32_t tmem, int x, int r, bool valid, int i, int lo,
+                                             int prow, int h, uint32_t n_kv, uint32_t& n_tile) {
+  using GE = Geo<D, NT>;
+  constexpr int NS = GE::kSlots, H = GE::kHalves;
+  const int lane = threadIdx.x & 31;
+  unsigned char* skv = sq + NT * GE::kTile;
+  const float slope2 = valid && a.slopes != nullptr ? __ldg(a.slopes + h) * kLog2e : 0.f;
+  const int pre = valid ? w.pre : 0;
+  const bool two = w.nt_all <= kTwoTermTiles;
+  const bool own_logits = a.cap_log2 > 0.f || a.slopes != nullptr || !(a.scale_log2 > 0.f);
+  const float mul = own_logits ? 1.f : a.scale_log2;
+  const int i_min = w.pos0 + x * a.R, lo_max = sh.lo_max[x];
+  // the block that ends past the sequence: its V rows there are cleared by the first row tile's warps
+  const int last_blk = (w.L - 1) >> 4;
+  const int e_last = last_blk < w.pre_units ? last_blk : last_blk - w.shift;
+  const int tail_tile = (w.L & 15) != 0 && e_last >= 0 && e_last < w.nblk && w.block_of(e_last) == last_blk
+                            ? e_last / kTileBlocks - w.ts : -1;
+  const uint32_t t_lane = tmem + ((uint32_t)(r & ~31) << 16);
+  const uint32_t ts_addr = t_lane + x * kKeys, to_addr = t_lane + NT * kKeys + x * D;
+  float m = -INFINITY, l = 0.f;
+  bool ok = true;
+  for (int j = 0; j < w.nt; ++j) {
+    ok = __all_sync(kFullMask, mbar_wait_bounded(&sh.s_full[x], n_tile & 1u, a.timeout_ns));
+    if (!ok) break;
+    tc_fence_after();
+    float v[kKeys];
+#pragma unroll
+    for (int c = 0; c < kKeys / 32; ++c) tmem_ld_x32(ts_addr + 32 * c, *reinterpret_cast<float(*)[32]>(v + 32 * c));
+    tmem_wait_ld();
+    const int e0 = (w.ts + j) * kTileBlocks;
+    if (own_logits) apply_rules(a, v, slope2, i, w, e0);
+    // all keys of the tile seen by all rows of the row tile?
+    const int t_first = w.block_of(e0) * 16;
+    const bool full = (e0 >= w.pre_units && t_first >= lo_max && t_first + kKeys - 1 <= i_min) ||
+                      (e0 + kTileBlocks <= w.pre_units && t_first + kKeys <= w.pre);
+    if (!full) {
+#pragma unroll
+      for (int p = 0; p < kTileBlocks; ++p) {
+        const int t0 = w.block_of(e0 + p) * 16;
+        const int hi_c = i - t0, lo_c = lo - t0, pre_c = pre - t0;
+        uint32_t see = hi_c >= 15 ? 0xffffu : hi_c < 0 ? 0u : (2u << hi_c) - 1u;
+        see &= lo_c <= 0 ? 0xffffu : lo_c > 15 ? 0u : 0xffffu << lo_c;
+        see |= pre_c >= 16 ? 0xffffu : pre_c <= 0 ? 0u : (1u << pre_c) - 1u;
+#pragma unroll
+        for (int c = 0; c < 16; ++c) v[16 * p + c] = ((see >> c) & 1u) ? v[16 * p + c] : -INFINITY;
+      }
+    }
+    float mx = v[0];
+#pragma unroll
+    for (int c = 1; c < kKeys; ++c) mx = fmaxf(mx, v[c]);
+    mx *= mul;
+    const bool move = mx > m + kSlack;
+    if (__any_sync(kFullMask, move)) {
+      const float scale = move ? ex2_approx(m - mx) : 1.f;
+      if (move) m = mx;
+      l *= scale;
+      if (j > 0) {  // O moves to the new reference once the last product has ended
+        ok = __all_sync(kFullMask, mbar_wait_bounded(&sh.pv_done[x], (n_tile - 1) & 1u, a.timeout_ns));
+        if (!ok) break;
+        tc_fence_after();
+#pragma unroll
+        for (int c = 0; c < D / 16; ++c) {
+          float o[16];
+          tmem_ld_x16(to_addr + 16 * c, o);
+          tmem_wait_ld();
+          uint32_t u[16];
+#pragma unroll
+          for (int k = 0; k < 16; ++k) u[k] = __float_as_uint(o[k] * scale);
+          tmem_st_x16(to_addr + 16 * c, u);
+        }
+      }
+    }
+    const float ref = m == -INFINITY ? 0.f : m;
+    const uint64_t mul2 = pack2(mul, mul), nref2 = pack2(-ref, -ref);
+    uint64_t sum2 = pack2(0.f, 0.f);
+#pragma unroll
+    for (int c = 0; c < kKeys / 32; ++c) {
+      uint32_t hi[16];
+#pragma unroll
+      for (int k = 0; k < 16; ++k) {
+        const float2 y = unpack2(ffma2(pack2(v[32 * c + 2 * k], v[32 * c + 2 * k + 1]), mul2, nref2));
+        const float p0 = ex2_approx(y.x), p1 = ex2_approx(y.y);
+        hi[k] = pack_bf16x2(p0, p1);
+        v[32 * c + 2 * k] = p0;
+        v[32 * c + 2 * k + 1] = p1;
+        if (!two) sum2 = fadd2(sum2, bf16x2_to_f32x2(hi[k]));
+      }
+      tmem_st_x16(ts_addr + 32 * c, hi);
+      if (two) {
+#pragma unroll
+        for (int k = 0; k < 16; ++k) {
+          const float p0 = v[32 * c + 2 * k], p1 = v[32 * c + 2 * k + 1];
+          sum2 = fadd2(sum2, pack2(p0, p1));
+          hi[k] = pack_bf16x2(p0 - bf16_lo_to_f32(hi[k]), p1 - bf16_hi_to_f32(hi[k]));
+        }
+        tmem_st_x16(ts_addr + 32 * c + 16, hi);
+      }
+    }
+    const float2 sum = unpack2(sum2);
+    l += sum.x + sum.y;
+    if (x == 0 && j == tail_tile) {
+      const uint32_t vtile = n_kv + 2 * j + 1;  // this tile's V in the count of K and V tiles
+      ok = __all_sync(kFullMask, mbar_wait_bounded(&sh.kv_full[vtile % NS], (vtile / NS) & 1u, a.timeout_ns));
+      if (!ok) break;
+      unsigned char* rows = skv + (vtile % NS) * GE::kTile + (e_last % kTileBlocks) * 2048;
+      const int gone = 16 - (w.L & 15);
+      for (int c = r; c < gone * 8 * H; c += 128)
+        *reinterpret_cast<uint4*>(rows + (c / (gone * 8)) * kHalf + (w.L & 15) * 128 + (c % (gone * 8)) * 16) =
+            make_uint4(0u, 0u, 0u, 0u);
+      fence_proxy_async_smem();
+    }
+    tmem_wait_st();
+    tc_fence_before();
+    __syncwarp();
+    if (lane == 0) mbar_arrive(&sh.p_full[x]);
+    ++n_tile;
+  }
+  if (ok && w.nt > 0) {
+    ok = __all_sync(kFullMask, mbar_wait_bounded(&sh.pv_done[x], (n_tile - 1) & 1u, a.timeout_ns));
+    tc_fence_after();
+  }
+  if (!ok) {
+    if (lane == 0) {
+      record_error(a.err, PKV_DEV_WAIT_TIMEOUT);
+      sh.abort = 1;
+    }
+    return;
+  }
+  // ---- the rows out: bf16, or this share's unnormalised row with its maximum and sum
+  const bool split = w.nsplit > 1;
+  const long long part = split ? (long long)a.plan_seq[w.b].y + ((long long)w.split * w.n + (prow - w.q0)) * a.Hq + h : 0;
+  const float f = split ? 1.f : (l > 0.f ? 1.f / l : 0.f);
+  bool bad = false;
+#pragma unroll
+  for (int c = 0; c < D / 16; ++c) {
+    float o[16];
+    __syncwarp();
+    if (w.nt > 0) {
+      tmem_ld_x16(to_addr + 16 * c, o);
+      tmem_wait_ld();
+    }
+#pragma unroll
+    for (int k = 0; k < 16; ++k) {
+      o[k] = w.nt > 0 ? o[k] * f : 0.f;
+      bad |= !(fabsf(o[k]) <= 3.4028234e38f);
+    }
+    if (valid && split) {
+      float4* dst = reinterpret_cast<float4*>(a.part_o + part * D + 16 * c);
+#pragma unroll
+      for (int k = 0; k < 4; ++k) dst[k] = make_float4(o[4 * k], o[4 * k + 1], o[4 * k + 2], o[4 * k + 3]);
+    } else if (valid) {
+      uint4* dst = reinterpret_cast<uint4*>(a.out + ((size_t)prow * a.Hq + h) * D + 16 * c);
+#pragma unroll
+      for (int k = 0; k < 2; ++k)
+        dst[k] = make_uint4(pack_bf16x2(o[8 * k], o[8 * k + 1]), pack_bf16x2(o[8 * k + 2], o[8 * k + 3]),
+                            pack_bf16x2(o[8 * k + 4], o[8 * k + 5]), pack_bf16x2(o[8 * k + 6], o[8 * k + 7]));
+    }
+  }
+  if (split && valid) a.part_ml[part] = make_float2(m, l);
+  // rows that are not finite: key by key over what they see
+  uint32_t again = __ballot_sync(kFullMask, valid && (bad || !(l <= 3.4028234e38f)));
+  while (again != 0u) {
+    const int src = __ffs(again) - 1;
+    again &= again - 1;
+    Row row;
+    row.b = w.b;
+    row.g = w.g;
+    row.r = __shfl_sync(kFullMask, prow, src);
+    row.h = __shfl_sync(kFullMask, h, src);
+    row.i = __shfl_sync(kFullMask, i, src);
+    row.lo = __shfl_sync(kFullMask, lo, src);
+    row.pre = __shfl_sync(kFullMask, pre, src);
+    row.e0 = w.ts * kTileBlocks;
+    row.e1 = min((w.ts + w.nt) * kTileBlocks, w.nblk);
+    row.pre_units = w.pre_units;
+    row.shift = w.shift;
+    exact_row<D>(a, row, split ? __shfl_sync(kFullMask, part, src) : -1);
   }
 }
 
@@ -280,32 +675,26 @@ template <int D, int NT>
 __global__ void __launch_bounds__(Geo<D, NT>::kThreads, Geo<D, NT>::kCtas)
 prefill_attention_kernel(const __grid_constant__ PrefillAttnArgs a) {
   using GE = Geo<D, NT>;
-  constexpr int NS = GE::kSlots, H = GE::kHalves;
   extern __shared__ unsigned char smem_raw[];
   unsigned char* sq = reinterpret_cast<unsigned char*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
-  unsigned char* skv = sq + NT * GE::kTile;
-  __shared__ uint64_t q_full, kv_full[NS], kv_empty[NS], s_full[NT], p_full[NT], pv_done[NT];
-  __shared__ uint32_t s_tmem;
-  __shared__ int s_lo_min, s_lo_max[NT], s_abort;
-
+  __shared__ Shared<D, NT> sh;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  constexpr int kProducer = NT * 4, kIssuer = NT * 4 + 1;
   if (threadIdx.x == 0) {
-    mbar_init(&q_full, 1);
-    for (int s = 0; s < NS; ++s) {
-      mbar_init(&kv_full[s], 1);
-      mbar_init(&kv_empty[s], 1);
+    mbar_init(&sh.q_full, 1);
+    for (int s = 0; s < GE::kSlots; ++s) {
+      mbar_init(&sh.kv_full[s], 1);
+      mbar_init(&sh.kv_empty[s], 1);
     }
     for (int x = 0; x < NT; ++x) {
-      mbar_init(&s_full[x], 1);
-      mbar_init(&p_full[x], 4);
-      mbar_init(&pv_done[x], 1);
+      mbar_init(&sh.s_full[x], 1);
+      mbar_init(&sh.p_full[x], 4);
+      mbar_init(&sh.pv_done[x], 1);
     }
-    s_abort = 0;
+    sh.abort = 0;
     fence_mbar_init();
   }
   if (warp == 0) {
-    tmem_alloc(&s_tmem, GE::kTmemCols);
+    tmem_alloc(&sh.tmem, GE::kTmemCols);
     tmem_relinquish();
   }
   grid_dependency_wait();  // the plan
@@ -313,388 +702,66 @@ prefill_attention_kernel(const __grid_constant__ PrefillAttnArgs a) {
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
-  const uint32_t tmem = s_tmem;
-  const int G = a.G, R = a.R;
+  const uint32_t tmem = sh.tmem;
   const int total = *a.plan_total * a.Hkv;
-  const uint64_t pol_q = l2_policy_evict_first();
-
-  // softmax threads: row tile x, row r of it: token r / G, head r % G
-  const int x = warp >> 2;
-  const int r = 32 * (warp & 3) + lane;
-  const int tok = r / G, head = r - tok * G;
-  const uint32_t t_lane = tmem + ((uint32_t)(32 * (warp & 3)) << 16);
-  // running counts since the kernel's start; their low bits are the barriers' phases
-  uint32_t n_items = 0;     // items run
-  uint32_t n_kv = 0;        // K and V tiles (producer, issuer)
-  uint32_t n_tile[NT] = {}; // key tiles of each row tile (issuer; softmax threads use their own)
-
-  for (int it = blockIdx.x; it < total; it += gridDim.x) {
-    const int4 item = a.plan_items[it / a.Hkv];
-    const int g = it - (it / a.Hkv) * a.Hkv;
-    const int b = item.x;
-    const PrefillSeq s = prefill_seq(a, b);
-    const int tok0 = item.y * NT * R;
-    const int tokens = min(s.n - tok0, NT * R);
-    const int nx = NT == 2 && tokens > R ? 2 : 1;
-    const int pos0 = s.L - s.n + tok0;
-
-    // ---- what the item's rows see
-    if (threadIdx.x == 0) {
-      s_lo_min = 0x7fffffff;
-      for (int y = 0; y < NT; ++y) s_lo_max[y] = 0;
-    }
-    __syncthreads();
-    const bool softmax_warp = warp < NT * 4;
-    const bool valid = softmax_warp && tok < R && x * R + tok < tokens;
-    const int prow = s.q0 + tok0 + x * R + tok;
-    const int i = valid ? pos0 + x * R + tok : -1;
-    const int lo = valid ? interval_start(a, prow, i) : 0;
-    if (softmax_warp && x < nx) {
+  // Each role has the whole item loop, so that its registers are its own.  Three block barriers an item:
+  // the shared minimum is reset, it is complete, every role has left the item.
+  uint32_t n_kv = 0, n_q = 0;  // K and V tiles, and items with tiles, since the kernel's start (barrier phases)
+  if (warp < NT * 4) {
+    setmaxnreg_inc<GE::kSoftmaxRegs>();
+    const int x = warp >> 2, r = 32 * (warp & 3) + lane;
+    const int tok = r / a.G, head = r - tok * a.G;
+    uint32_t n_tile = 0;
+    for (int it = blockIdx.x; it < total; it += gridDim.x) {
+      Item w = load_item(a, it, NT);
+      if (threadIdx.x == 0) {
+        sh.lo_min = 0x7fffffff;
+        for (int y = 0; y < NT; ++y) sh.lo_max[y] = 0;
+      }
+      __syncthreads();
+      const bool valid = tok < a.R && x * a.R + tok < w.tokens;
+      const int prow = w.q0 + w.tok0 + x * a.R + tok;
+      const int i = valid ? w.pos0 + x * a.R + tok : -1;
+      const int lo = valid ? interval_start(a, prow, i) : 0;
       const int lo_min = __reduce_min_sync(kFullMask, valid ? lo : 0x7fffffff);
       const int lo_max = __reduce_max_sync(kFullMask, lo);
       if (lane == 0) {
-        atomicMin(&s_lo_min, lo_min);
-        atomicMax(&s_lo_max[x], lo_max);
+        atomicMin(&sh.lo_min, lo_min);
+        atomicMax(&sh.lo_max[x], lo_max);
       }
+      __syncthreads();
+      set_keys(w, sh.lo_min);
+      if (x < w.nx)
+        softmax_rows<D, NT>(a, sh, w, sq, tmem, x, r, valid, i, lo, prow, w.g * a.G + head, n_kv, n_tile);
+      n_kv += 2 * w.nt;
+      tc_fence_before();
+      __syncthreads();
+      if (sh.abort != 0) break;
     }
-    __syncthreads();
-    const int i_max = pos0 + tokens - 1, lo_min = s_lo_min;
-    const int pre_units = (s.pre + 15) >> 4;
-    const int first = max(lo_min >> 4, pre_units);
-    const int nblk = pre_units + (lo_min <= i_max ? max((i_max >> 4) - first + 1, 0) : 0);
-    const int shift = first - pre_units;
-    const int nt_all = (nblk + kTileBlocks - 1) / kTileBlocks;
-    const int per = (nt_all + item.w - 1) / item.w;
-    const int ts = min(item.z * per, nt_all);
-    const int nt = min(ts + per, nt_all) - ts;
-    const bool two = nt_all <= kTwoTermTiles;
-    auto block_of = [&](int e) { return e < pre_units ? e : e + shift; };
-
-    if (warp == kProducer) {
-      // -------------------------------------------------------------- TMA producer
-      if (nt > 0) {
-        if (lane == 0) {
-          mbar_arrive_expect_tx(&q_full, (uint32_t)(nx * H * 128 * G * R));
-          for (int y = 0; y < nx; ++y)
-#pragma unroll
-            for (int h = 0; h < H; ++h)
-              tma_load_3d(sq + y * GE::kTile + h * kHalf, &a.tmap_q, h * 64, g * G, s.q0 + tok0 + y * R, &q_full, pol_q);
-        }
-        auto id_of = [&](int j) -> int {  // lane p < 8: the pool block of entry p of key tile j, -1: none
-          const int e = (ts + j) * kTileBlocks + lane;
-          int id = -1;
-          if (lane < kTileBlocks && j < nt && e < nblk) {
-            id = __ldg(a.block_tables + (size_t)b * a.MB + block_of(e));
-            if (id < 0 || id >= a.NB) {
-              record_error(a.err, PKV_DEV_BAD_BLOCK_ID);
-              id = -1;
-            }
-          }
-          return id;
-        };
-        int id = id_of(0);
-        bool ok = true;
-        for (int j = 0; j < nt && ok; ++j) {
-          const int next = id_of(j + 1);
-          const uint32_t have = __ballot_sync(kFullMask, id >= 0);
-          for (int kv = 0; kv < 2 && ok; ++kv, ++n_kv) {
-            const uint32_t slot = n_kv % NS;
-            if (n_kv >= NS) ok = mbar_wait_bounded(&kv_empty[slot], ((n_kv / NS) - 1) & 1u, a.timeout_ns);
-            ok = __all_sync(kFullMask, ok);
-            if (!ok) break;
-            unsigned char* dst = skv + slot * GE::kTile;
-            if (have != 0xffu) {  // blocks past the list (or refused): zeros
-              for (int p = 0; p < kTileBlocks; ++p) {
-                if ((have >> p) & 1u) continue;
-                for (int h = 0; h < H; ++h)
-#pragma unroll
-                  for (int c = 0; c < 4; ++c)
-                    *reinterpret_cast<uint4*>(dst + h * kHalf + p * 2048 + (c * 32 + lane) * 16) = make_uint4(0u, 0u, 0u, 0u);
-              }
-              fence_proxy_async_smem();
-              __syncwarp();
-            }
-            if (lane == 0) mbar_arrive_expect_tx(&kv_full[slot], (uint32_t)(__popc(have) * H * 2048));
-            __syncwarp();
-            if (id >= 0) {
-              const int y = (id * a.Hkv + g) * 16;
-#pragma unroll
-              for (int h = 0; h < H; ++h)
-                tma_load_2d(dst + h * kHalf + lane * 2048, kv == 0 ? &a.tmap_k : &a.tmap_v, h * 64, y, &kv_full[slot],
-                            l2_policy_evict_last());
-            }
-          }
-          id = next;
-        }
-        if (!ok) {
-          if (lane == 0) {
-            record_error(a.err, PKV_DEV_WAIT_TIMEOUT);
-            s_abort = 1;
-            // what is in flight lands before the CTA goes
-            (void)mbar_wait_bounded(&q_full, n_items & 1u, a.timeout_ns);
-            for (uint32_t c = n_kv > NS ? n_kv - NS : 0; c < n_kv; ++c)
-              (void)mbar_wait_bounded(&kv_full[c % NS], (c / NS) & 1u, a.timeout_ns);
-          }
-          __syncwarp();
-        }
-      }
-    } else if (warp == kIssuer) {
-      // ---------------------------------------------------------------- MMA issuer
-      if (lane == 0 && nt > 0) {
-        constexpr uint32_t id_qk = umma_idesc_bf16(128, kKeys), id_pv = umma_idesc_bf16_bmn(128, D);
-        const uint32_t q0 = smem_u32(sq), kv0 = smem_u32(skv);
-        auto qk = [&](int y, uint32_t slot) {
-          const uint32_t qa = q0 + y * GE::kTile, kb = kv0 + slot * GE::kTile;
-#pragma unroll
-          for (int k = 0; k < D / 16; ++k) {
-            const uint32_t off = (uint32_t)((k >> 2) * kHalf + (k & 3) * 32);
-            umma_bf16(tmem + y * kKeys, umma_desc_sw128(qa + off), umma_desc_sw128(kb + off), id_qk, k > 0);
-          }
-          umma_commit(&s_full[y]);
-        };
-        auto pv = [&](int y, uint32_t slot, bool first_tile) {
-          const uint32_t vb = kv0 + slot * GE::kTile, o = tmem + NT * kKeys + y * D, p = tmem + y * kKeys;
-#pragma unroll
-          for (int k = 0; k < kKeys / 16; ++k)  // chunk k / 2: first terms, then remainders, 16 columns each
-            umma_bf16_ts(o, p + 32 * (k >> 1) + 8 * (k & 1), umma_desc_mn_sw128(vb + k * 2048, kHalf), id_pv,
-                         !first_tile || k > 0);
-          if (two) {
-#pragma unroll
-            for (int k = 0; k < kKeys / 16; ++k)
-              umma_bf16_ts(o, p + 32 * (k >> 1) + 16 + 8 * (k & 1), umma_desc_mn_sw128(vb + k * 2048, kHalf), id_pv, true);
-          }
-          umma_commit(&pv_done[y]);
-        };
-        auto wait = [&](uint64_t* bar, uint32_t phase) {
-          if (mbar_wait_bounded(bar, phase & 1u, a.timeout_ns)) return true;
-          record_error(a.err, PKV_DEV_WAIT_TIMEOUT);
-          s_abort = 1;
-          return false;
-        };
-        bool ok = wait(&q_full, n_items) && wait(&kv_full[n_kv % NS], n_kv / NS);
-        if (ok) {
+  } else {
+    setmaxnreg_dec<GE::kOtherRegs>();
+    uint32_t n_tile[NT] = {};
+    for (int it = blockIdx.x; it < total; it += gridDim.x) {
+      Item w = load_item(a, it, NT);
+      __syncthreads();
+      __syncthreads();
+      set_keys(w, sh.lo_min);
+      if (w.nt > 0) {
+        if (warp == NT * 4) {
+          produce<D, NT>(a, sh, w, sq, n_kv, n_q);
+        } else if (warp == NT * 4 + 1 && lane == 0) {
           tc_fence_after();
-          for (int y = 0; y < nx; ++y) qk(y, n_kv % NS);
-          umma_commit(&kv_empty[n_kv % NS]);
-          ++n_kv;
+          issue_mmas<D, NT>(a, sh, w, sq, tmem, n_kv, n_q, n_tile);
         }
-        for (int j = 0; j < nt && ok; ++j) {
-          const uint32_t vs = n_kv % NS, ks = (n_kv + 1) % NS;
-          ok = wait(&kv_full[vs], n_kv / NS);
-          for (int y = 0; y < nx && ok; ++y) {
-            ok = wait(&p_full[y], n_tile[y]);
-            if (ok && y == 0 && j + 1 < nt) ok = wait(&kv_full[ks], (n_kv + 1) / NS);
-            if (!ok) break;
-            tc_fence_after();
-            pv(y, vs, j == 0);
-            ++n_tile[y];
-            if (j + 1 < nt) qk(y, ks);
-          }
-          if (!ok) break;
-          umma_commit(&kv_empty[vs]);
-          if (j + 1 < nt) umma_commit(&kv_empty[ks]);
-          n_kv += j + 1 < nt ? 2 : 1;
-        }
-        if (!ok) {  // the MMAs in flight end before tensor memory goes
-          umma_commit(&kv_empty[0]);
-          (void)mbar_wait_bounded(&kv_empty[0], 0, a.timeout_ns / 64);
-          (void)mbar_wait_bounded(&kv_empty[0], 1, a.timeout_ns / 64);
-        }
+        ++n_q;
       }
-    } else if (x < nx) {
-      // ------------------------------------------------------------------ softmax
-      const float slope2 = valid && a.slopes != nullptr ? __ldg(a.slopes + g * G + head) * kLog2e : 0.f;
-      const int pre = valid ? s.pre : 0;
-      const bool own_logits = a.cap_log2 > 0.f || a.slopes != nullptr || !(a.scale_log2 > 0.f);
-      const float mul = own_logits ? 1.f : a.scale_log2;
-      const int i_min = pos0 + x * R, lo_max = s_lo_max[x];
-      // the block that ends past the sequence: its V rows there are cleared by the first row tile's warps
-      const int last_blk = (s.L - 1) >> 4;
-      const int e_last = last_blk < pre_units ? last_blk : last_blk - shift;
-      const int tail_tile = (s.L & 15) != 0 && e_last >= 0 && e_last < nblk && block_of(e_last) == last_blk
-                                ? e_last / kTileBlocks - ts : -1;
-      const uint32_t ts_addr = t_lane + x * kKeys, to_addr = t_lane + NT * kKeys + x * D;
-      float m = -INFINITY, l = 0.f;
-      bool ok = true;
-      for (int j = 0; j < nt; ++j) {
-        ok = __all_sync(kFullMask, mbar_wait_bounded(&s_full[x], n_tile[0] & 1u, a.timeout_ns));
-        if (!ok) break;
-        tc_fence_after();
-        float v[kKeys];
-#pragma unroll
-        for (int c = 0; c < kKeys / 32; ++c) tmem_ld_x32(ts_addr + 32 * c, *reinterpret_cast<float(*)[32]>(v + 32 * c));
-        tmem_wait_ld();
-        const int e0 = (ts + j) * kTileBlocks;
-        int t0[kTileBlocks];
-#pragma unroll
-        for (int p = 0; p < kTileBlocks; ++p) t0[p] = block_of(e0 + p) * 16;
-        if (own_logits) apply_rules(a, v, slope2, i, t0);
-        // all keys of the tile seen by all rows of the row tile?
-        const bool full = (e0 >= pre_units && t0[0] >= lo_max && t0[0] + kKeys - 1 <= i_min) ||
-                          (e0 + kTileBlocks <= pre_units && t0[0] + kKeys <= s.pre);
-        if (!full) {
-#pragma unroll
-          for (int p = 0; p < kTileBlocks; ++p) {
-            const int hi_c = i - t0[p], lo_c = lo - t0[p], pre_c = pre - t0[p];
-            uint32_t see = hi_c >= 15 ? 0xffffu : hi_c < 0 ? 0u : (2u << hi_c) - 1u;
-            see &= lo_c <= 0 ? 0xffffu : lo_c > 15 ? 0u : 0xffffu << lo_c;
-            see |= pre_c >= 16 ? 0xffffu : pre_c <= 0 ? 0u : (1u << pre_c) - 1u;
-#pragma unroll
-            for (int c = 0; c < 16; ++c) v[16 * p + c] = ((see >> c) & 1u) ? v[16 * p + c] : -INFINITY;
-          }
-        }
-        float mx = v[0];
-#pragma unroll
-        for (int c = 1; c < kKeys; ++c) mx = fmaxf(mx, v[c]);
-        mx *= mul;
-        const bool move = mx > m + kSlack;
-        if (__any_sync(kFullMask, move)) {
-          const float scale = move ? ex2_approx(m - mx) : 1.f;
-          if (move) m = mx;
-          l *= scale;
-          if (j > 0) {  // O moves to the new reference once the last product has ended
-            ok = __all_sync(kFullMask, mbar_wait_bounded(&pv_done[x], (n_tile[0] - 1) & 1u, a.timeout_ns));
-            if (!ok) break;
-            tc_fence_after();
-#pragma unroll
-            for (int c = 0; c < D / 32; ++c) {
-              float o[32];
-              tmem_ld_x32(to_addr + 32 * c, o);
-              tmem_wait_ld();
-#pragma unroll
-              for (int k = 0; k < 32; ++k) o[k] *= scale;
-              tmem_st_x32(to_addr + 32 * c, o);
-            }
-          }
-        }
-        const float ref = m == -INFINITY ? 0.f : m;
-        const uint64_t mul2 = pack2(mul, mul), nref2 = pack2(-ref, -ref);
-        uint64_t sum2 = pack2(0.f, 0.f);
-#pragma unroll
-        for (int c = 0; c < kKeys / 32; ++c) {
-          uint32_t hi[16];
-#pragma unroll
-          for (int k = 0; k < 16; ++k) {
-            const float2 y = unpack2(ffma2(pack2(v[32 * c + 2 * k], v[32 * c + 2 * k + 1]), mul2, nref2));
-            const float p0 = ex2_approx(y.x), p1 = ex2_approx(y.y);
-            hi[k] = pack_bf16x2(p0, p1);
-            v[32 * c + 2 * k] = p0;
-            v[32 * c + 2 * k + 1] = p1;
-            if (!two) sum2 = fadd2(sum2, bf16x2_to_f32x2(hi[k]));
-          }
-          tmem_st_x16(ts_addr + 32 * c, hi);
-          if (two) {
-#pragma unroll
-            for (int k = 0; k < 16; ++k) {
-              const float p0 = v[32 * c + 2 * k], p1 = v[32 * c + 2 * k + 1];
-              sum2 = fadd2(sum2, pack2(p0, p1));
-              hi[k] = pack_bf16x2(p0 - bf16_lo_to_f32(hi[k]), p1 - bf16_hi_to_f32(hi[k]));
-            }
-            tmem_st_x16(ts_addr + 32 * c + 16, hi);
-          }
-        }
-        const float2 sum = unpack2(sum2);
-        l += sum.x + sum.y;
-        if (x == 0 && j == tail_tile) {
-          const uint32_t vtile = n_kv + 2 * j + 1;  // this tile's V in the count of K and V tiles
-          ok = __all_sync(kFullMask, mbar_wait_bounded(&kv_full[vtile % NS], (vtile / NS) & 1u, a.timeout_ns));
-          if (!ok) break;
-          unsigned char* rows = skv + (vtile % NS) * GE::kTile + (e_last % kTileBlocks) * 2048;
-          const int gone = 16 - (s.L & 15);
-          for (int c = r; c < gone * 8 * H; c += 128)
-            *reinterpret_cast<uint4*>(rows + (c / (gone * 8)) * kHalf + (s.L & 15) * 128 + (c % (gone * 8)) * 16) =
-                make_uint4(0u, 0u, 0u, 0u);
-          fence_proxy_async_smem();
-        }
-        tmem_wait_st();
-        tc_fence_before();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(&p_full[x]);
-        ++n_tile[0];
-      }
-      if (ok && nt > 0) {
-        ok = __all_sync(kFullMask, mbar_wait_bounded(&pv_done[x], (n_tile[0] - 1) & 1u, a.timeout_ns));
-        tc_fence_after();
-      }
-      if (!ok) {
-        if (lane == 0) {
-          record_error(a.err, PKV_DEV_WAIT_TIMEOUT);
-          s_abort = 1;
-        }
-      } else {
-        // ---- the rows out: bf16, or this share's unnormalised row with its maximum and sum
-        const bool split = item.w > 1;
-        const int h = g * G + head;
-        const long long part = split ? (long long)a.plan_seq[b].y + ((long long)item.z * s.n + (prow - s.q0)) * a.Hq + h : 0;
-        const float f = split ? 1.f : (l > 0.f ? 1.f / l : 0.f);
-        bool bad = false;
-#pragma unroll
-        for (int c = 0; c < D / 32; ++c) {
-          float o[32];
-          __syncwarp();
-          if (nt > 0) {
-            tmem_ld_x32(to_addr + 32 * c, o);
-            tmem_wait_ld();
-          }
-#pragma unroll
-          for (int k = 0; k < 32; ++k) {
-            o[k] = nt > 0 ? o[k] * f : 0.f;
-            bad |= !(fabsf(o[k]) <= 3.4028234e38f);
-          }
-          if (valid && split) {
-            float4* dst = reinterpret_cast<float4*>(a.part_o + part * D + 32 * c);
-#pragma unroll
-            for (int k = 0; k < 8; ++k) dst[k] = make_float4(o[4 * k], o[4 * k + 1], o[4 * k + 2], o[4 * k + 3]);
-          } else if (valid) {
-            uint4* dst = reinterpret_cast<uint4*>(a.out + ((size_t)prow * a.Hq + h) * D + 32 * c);
-#pragma unroll
-            for (int k = 0; k < 4; ++k)
-              dst[k] = make_uint4(pack_bf16x2(o[8 * k], o[8 * k + 1]), pack_bf16x2(o[8 * k + 2], o[8 * k + 3]),
-                                  pack_bf16x2(o[8 * k + 4], o[8 * k + 5]), pack_bf16x2(o[8 * k + 6], o[8 * k + 7]));
-          }
-        }
-        if (split && valid) a.part_ml[part] = make_float2(m, l);
-        // rows that are not finite: key by key over what they see
-        uint32_t again = __ballot_sync(kFullMask, valid && (bad || !(l <= 3.4028234e38f)));
-        __syncwarp();
-        while (again != 0u) {
-          const int src = __ffs(again) - 1;
-          again &= again - 1;
-          Row w;
-          w.b = b;
-          w.g = g;
-          w.r = __shfl_sync(kFullMask, prow, src);
-          w.h = __shfl_sync(kFullMask, h, src);
-          w.i = __shfl_sync(kFullMask, i, src);
-          w.lo = __shfl_sync(kFullMask, lo, src);
-          w.pre = __shfl_sync(kFullMask, pre, src);
-          w.e0 = ts * kTileBlocks;
-          w.e1 = min((ts + nt) * kTileBlocks, nblk);
-          w.pre_units = pre_units;
-          w.shift = shift;
-          const long long wp = __shfl_sync(kFullMask, part, src);
-          float wm, wl, wo[D / 32];
-          exact_row<D>(a, w, wm, wl, wo);
-          const float wf = split ? 1.f : (wl > 0.f ? 1.f / wl : (wl == wl ? 0.f : wl));
-#pragma unroll
-          for (int e = 0; e < D / 32; ++e) {
-            if (split) a.part_o[wp * D + lane * (D / 32) + e] = wo[e];
-            else a.out[((size_t)w.r * a.Hq + w.h) * D + lane * (D / 32) + e] = __float2bfloat16_rn(wo[e] * wf);
-          }
-          if (split && lane == 0) a.part_ml[wp] = make_float2(wm, wl);
-        }
-      }
+      __syncwarp();
+      __syncthreads();
+      if (sh.abort != 0) break;
     }
-    // every role leaves the item together: the producer's and issuer's counts are the item's tiles
-    if (warp < NT * 4) n_kv += 2 * nt;
-    ++n_items;
-    if (nt == 0) --n_items;  // no Q was loaded
-    tc_fence_before();
-    __syncthreads();
-    tc_fence_after();
-    if (s_abort != 0) break;
   }
   __syncthreads();
+  tc_fence_after();
   if (warp == 0) tmem_dealloc(tmem, GE::kTmemCols);
 }
 
