@@ -445,46 +445,88 @@ __device__ __forceinline__ void issue_mmas(const PrefillAttnArgs& a, Shared<D, N
   }
 }
 
-// The logits of a row's 128 keys in base 2, in place: x = cap(S sl2) - slope |i - t|, for the rules that
-// need each key's own value (otherwise the scale goes into the exponent's FMA).
-__device__ __forceinline__ void apply_rules(const PrefillAttnArgs& a, float (&v)[kKeys], float slope2, int i,
-                                            const Item& w, int e0) {
-  const float sl2 = a.scale_log2;
-  if (a.cap_log2 > 0.f) {
-    // |u| of every key of the warp's rows within the polynomial's range (cap_logit): packed, no division
-    const float ku = sl2 * a.cap_in * 0.34657359f;
-    float top = 0.f;
+// Largest of a row's 128 values (of their sizes when ABS), in four chains.
+template <bool ABS>
+__device__ __forceinline__ float row_max(const float (&v)[kKeys]) {
+  float t[4];
 #pragma unroll
-    for (int c = 0; c < kKeys; ++c) top = fmaxf(top, fabsf(v[c]));
-    if (__all_sync(kFullMask, top * fabsf(ku) < 0.3f)) {
-      const uint64_t k2 = pack2(ku, ku), c2 = pack2(a.cap_log2, a.cap_log2);
-      const uint64_t p4 = pack2(0.021869488f, 0.021869488f), p3 = pack2(-0.053968254f, -0.053968254f);
-      const uint64_t p2 = pack2(0.13333333f, 0.13333333f), p1 = pack2(-0.33333333f, -0.33333333f), p0 = pack2(1.f, 1.f);
+  for (int c = 0; c < 4; ++c) t[c] = ABS ? fabsf(v[c]) : v[c];
+#pragma unroll
+  for (int c = 4; c < kKeys; ++c) t[c & 3] = fmaxf(t[c & 3], ABS ? fabsf(v[c]) : v[c]);
+  return fmaxf(fmaxf(t[0], t[1]), fmaxf(t[2], t[3]));
+}
+
+// v = v * P(v^2 k^2) for the odd polynomial P of tanh (cap_logit): to u^5, or to u^9 with NINTH.
+template <bool NINTH>
+__device__ __forceinline__ void cap_poly(float (&v)[kKeys], float k) {
+  const float w = k * k;
+  const float c1 = -0.33333333f * w, c2 = 0.13333333f * w * w, c3 = -0.053968254f * w * w * w,
+              c4 = 0.021869488f * w * w * w * w;
+  const uint64_t p1 = pack2(c1, c1), p2 = pack2(c2, c2), p3 = pack2(c3, c3), p4 = pack2(c4, c4), p0 = pack2(1.f, 1.f);
+#pragma unroll
+  for (int c = 0; c < kKeys; c += 2) {
+    const uint64_t x = pack2(v[c], v[c + 1]);
+    const uint64_t q = fmul2(x, x);
+    uint64_t p = NINTH ? ffma2(ffma2(p4, q, p3), q, p2) : p2;
+    p = ffma2(ffma2(p, q, p1), q, p0);
+    const float2 y = unpack2(fmul2(x, p));
+    v[c] = y.x;
+    v[c + 1] = y.y;
+  }
+}
+
+// For the rules that need each key's own value: turns a row's 128 products S in place into numbers that
+// `return value` (> 0) times are the base-2 logits x = cap(S sl2) - slope |i - t|.  (Without such rules the
+// scale alone is that factor.)  e0: the tile's first list entry.
+__device__ __forceinline__ float apply_rules(const PrefillAttnArgs& a, float (&v)[kKeys], float slope2, int i,
+                                             const Item& w, int e0) {
+  float mul = a.scale_log2;
+  if (a.cap_log2 > 0.f) {
+    // u = S ku is the logit over the cap.  Where it is small for every key of the warp's rows the odd
+    // polynomial serves: to u^5 below 0.11 (the next term is 0.054 u^6 of the value, 2^-23 there), to u^9
+    // below 0.3; the general form costs an exponential and a reciprocal a key
+    const float ku = a.scale_log2 * a.cap_in * 0.34657359f;
+    const float far = row_max<true>(v) * fabsf(ku);
+    mul = a.cap_log2 * ku;
+    if (mul > 0.f && __all_sync(kFullMask, far < 0.11f)) {
+      cap_poly<false>(v, ku);
+    } else if (mul > 0.f && __all_sync(kFullMask, far < 0.3f)) {
+      cap_poly<true>(v, ku);
+    } else {
+#pragma unroll
+      for (int c = 0; c < kKeys; ++c) v[c] = cap_logit(v[c] * a.scale_log2, a.cap_log2, a.cap_in);
+      mul = 1.f;
+    }
+  }
+  if (a.slopes != nullptr) {
+    const uint64_t m2 = pack2(mul, mul);
+    if (e0 >= w.pre_units) {
+      // the interval's part of the list is one run of positions, and keys past i are masked: the distance
+      // is i - t, linear along the tile
+      const float b0 = -slope2 * (float)(i - w.block_of(e0) * 16);
+      const uint64_t b2 = pack2(b0, b0), s2 = pack2(slope2, slope2);
 #pragma unroll
       for (int c = 0; c < kKeys; c += 2) {
-        const uint64_t u = fmul2(pack2(v[c], v[c + 1]), k2);
-        const uint64_t q = fmul2(u, u);
-        const uint64_t p = ffma2(ffma2(ffma2(ffma2(p4, q, p3), q, p2), q, p1), q, p0);
-        const float2 x = unpack2(fmul2(fmul2(u, c2), p));
-        v[c] = x.x;
-        v[c + 1] = x.y;
+        const float2 y = unpack2(ffma2(pack2(v[c], v[c + 1]), m2, ffma2(pack2((float)c, (float)(c + 1)), s2, b2)));
+        v[c] = y.x;
+        v[c + 1] = y.y;
       }
     } else {
 #pragma unroll
-      for (int c = 0; c < kKeys; ++c) v[c] = cap_logit(v[c] * sl2, a.cap_log2, a.cap_in);
+      for (int p = 0; p < kTileBlocks; ++p) {
+        const float d0 = (float)(i - w.block_of(e0 + p) * 16);
+#pragma unroll
+        for (int c = 0; c < 16; ++c) v[16 * p + c] = fmaf(-slope2, fabsf(d0 - (float)c), v[16 * p + c] * mul);
+      }
     }
-  } else {
-#pragma unroll
-    for (int c = 0; c < kKeys; ++c) v[c] *= sl2;
+    return 1.f;
   }
-  if (a.slopes != nullptr) {
+  if (!(mul > 0.f)) {
 #pragma unroll
-    for (int p = 0; p < kTileBlocks; ++p) {
-      const float d0 = (float)(i - w.block_of(e0 + p) * 16);
-#pragma unroll
-      for (int c = 0; c < 16; ++c) v[16 * p + c] = fmaf(-slope2, fabsf(d0 - (float)c), v[16 * p + c]);
-    }
+    for (int c = 0; c < kKeys; ++c) v[c] *= mul;
+    return 1.f;
   }
+  return mul;
 }
 
 // The item's softmax and output for this thread's row of row tile x: position i (-1: none), interval start
@@ -501,7 +543,6 @@ __device__ __forceinline__ void softmax_rows(const PrefillAttnArgs& a, Shared<D,
   const int pre = valid ? w.pre : 0;
   const bool two = w.nt_all <= kTwoTermTiles;
   const bool own_logits = a.cap_log2 > 0.f || a.slopes != nullptr || !(a.scale_log2 > 0.f);
-  const float mul = own_logits ? 1.f : a.scale_log2;
   const int i_min = w.pos0 + x * a.R, lo_max = sh.lo_max[x];
   // the block that ends past the sequence: its V rows there are cleared by the first row tile's warps
   const int last_blk = (w.L - 1) >> 4;
@@ -521,7 +562,7 @@ __device__ __forceinline__ void softmax_rows(const PrefillAttnArgs& a, Shared<D,
     for (int c = 0; c < kKeys / 32; ++c) tmem_ld_x32(ts_addr + 32 * c, *reinterpret_cast<float(*)[32]>(v + 32 * c));
     tmem_wait_ld();
     const int e0 = (w.ts + j) * kTileBlocks;
-    if (own_logits) apply_rules(a, v, slope2, i, w, e0);
+    const float mul = own_logits ? apply_rules(a, v, slope2, i, w, e0) : a.scale_log2;
     // all keys of the tile seen by all rows of the row tile?
     const int t_first = w.block_of(e0) * 16;
     const bool full = (e0 >= w.pre_units && t_first >= lo_max && t_first + kKeys - 1 <= i_min) ||
@@ -538,10 +579,7 @@ __device__ __forceinline__ void softmax_rows(const PrefillAttnArgs& a, Shared<D,
         for (int c = 0; c < 16; ++c) v[16 * p + c] = ((see >> c) & 1u) ? v[16 * p + c] : -INFINITY;
       }
     }
-    float mx = v[0];
-#pragma unroll
-    for (int c = 1; c < kKeys; ++c) mx = fmaxf(mx, v[c]);
-    mx *= mul;
+    const float mx = row_max<false>(v) * mul;
     const bool move = mx > m + kSlack;
     if (__any_sync(kFullMask, move)) {
       const float scale = move ? ex2_approx(m - mx) : 1.f;
@@ -565,31 +603,38 @@ __device__ __forceinline__ void softmax_rows(const PrefillAttnArgs& a, Shared<D,
     }
     const float ref = m == -INFINITY ? 0.f : m;
     const uint64_t mul2 = pack2(mul, mul), nref2 = pack2(-ref, -ref);
-    uint64_t sum2 = pack2(0.f, 0.f);
+    uint64_t sum2[4];
 #pragma unroll
-    for (int c = 0; c < kKeys / 32; ++c) {
-      uint32_t hi[16];
+    for (int k = 0; k < 4; ++k) sum2[k] = pack2(0.f, 0.f);
+    if (!two) {
 #pragma unroll
-      for (int k = 0; k < 16; ++k) {
-        const float2 y = unpack2(ffma2(pack2(v[32 * c + 2 * k], v[32 * c + 2 * k + 1]), mul2, nref2));
-        const float p0 = ex2_approx(y.x), p1 = ex2_approx(y.y);
-        hi[k] = pack_bf16x2(p0, p1);
-        v[32 * c + 2 * k] = p0;
-        v[32 * c + 2 * k + 1] = p1;
-        if (!two) sum2 = fadd2(sum2, bf16x2_to_f32x2(hi[k]));
-      }
-      tmem_st_x16(ts_addr + 32 * c, hi);
-      if (two) {
+      for (int c = 0; c < kKeys / 32; ++c) {
+        uint32_t hi[16];
 #pragma unroll
         for (int k = 0; k < 16; ++k) {
-          const float p0 = v[32 * c + 2 * k], p1 = v[32 * c + 2 * k + 1];
-          sum2 = fadd2(sum2, pack2(p0, p1));
-          hi[k] = pack_bf16x2(p0 - bf16_lo_to_f32(hi[k]), p1 - bf16_hi_to_f32(hi[k]));
+          const float2 y = unpack2(ffma2(pack2(v[32 * c + 2 * k], v[32 * c + 2 * k + 1]), mul2, nref2));
+          hi[k] = pack_bf16x2(ex2_approx(y.x), ex2_approx(y.y));
+          sum2[k & 3] = fadd2(sum2[k & 3], bf16x2_to_f32x2(hi[k]));
         }
-        tmem_st_x16(ts_addr + 32 * c + 16, hi);
+        tmem_st_x16(ts_addr + 32 * c, hi);
+      }
+    } else {
+#pragma unroll
+      for (int c = 0; c < kKeys / 32; ++c) {
+        uint32_t hi[16], rest[16];
+#pragma unroll
+        for (int k = 0; k < 16; ++k) {
+          const float2 y = unpack2(ffma2(pack2(v[32 * c + 2 * k], v[32 * c + 2 * k + 1]), mul2, nref2));
+          const float p0 = ex2_approx(y.x), p1 = ex2_approx(y.y);
+          hi[k] = pack_bf16x2(p0, p1);
+          rest[k] = pack_bf16x2(p0 - bf16_lo_to_f32(hi[k]), p1 - bf16_hi_to_f32(hi[k]));
+          sum2[k & 3] = fadd2(sum2[k & 3], pack2(p0, p1));
+        }
+        tmem_st_x16(ts_addr + 32 * c, hi);
+        tmem_st_x16(ts_addr + 32 * c + 16, rest);
       }
     }
-    const float2 sum = unpack2(sum2);
+    const float2 sum = unpack2(fadd2(fadd2(sum2[0], sum2[1]), fadd2(sum2[2], sum2[3])));
     l += sum.x + sum.y;
     if (x == 0 && j == tail_tile) {
       const uint32_t vtile = n_kv + 2 * j + 1;  // this tile's V in the count of K and V tiles
