@@ -25,6 +25,7 @@
 // Every wait is bounded; bad block ids are cleared tiles, recorded.
 #include <algorithm>
 #include <cmath>
+#include <cstddef>
 
 #include "kernels.h"
 #include "ptx.cuh"
@@ -63,8 +64,10 @@ __device__ __forceinline__ int interval_start(const PrefillAttnArgs& a, int r, i
   return lo;
 }
 
-constexpr int kKeys = 128;           // keys per K/V tile
+constexpr int kKeys = 128;           // keys per K/V tile in shared memory
 constexpr int kTileBlocks = kKeys / 16;
+constexpr int kStep = 64;            // keys of a softmax step: half a tile
+constexpr int kStepBlocks = kStep / 16;
 constexpr int kHalf = kKeys * 128;   // bytes of one 64-element half of a tile
 constexpr float kSlack = 8.0f;       // the running maximum moves only when exceeded by this (base 2)
 constexpr int kTwoTermTiles = 4;     // rows over at most this many key tiles take P as two bf16 terms
@@ -75,14 +78,16 @@ struct Geo {
   static constexpr int kHalves = D / 64;
   static constexpr int kTile = kHalves * kHalf;  // bytes of a Q, K or V tile
   static constexpr int kSlots = NT == 2 ? (D == 128 ? 4 : 8) : (D == 128 ? 2 : 5);
-  static constexpr int kThreads = NT * 128 + 128;  // softmax warpgroups; producer, issuer and two idle warps
+  static constexpr int kSoftmaxWarps = NT * 4;           // a row a thread
+  static constexpr int kThreads = NT * 128 + 128;        // and producer, issuer, two idle warps
   static constexpr int kCtas = NT == 1 ? 2 : 1;  // per SM (shared and tensor memory allow no more)
-  // Registers a thread: a launch gives every warp the same, which the softmax warps (a row of 128 logits
-  // in registers) then take from the others.  NT = 2: 384 x 168 = 256 x 216 + 128 x 72; NT = 1 (two CTAs):
+  // Registers a thread: a launch gives every warp the same, which the softmax warps (their logits are in
+  // registers) then take from the others.  NT = 2: 384 x 168 = 256 x 216 + 128 x 72; NT = 1 (two CTAs):
   // 256 x 128 = 128 x 184 + 128 x 72.
+  static constexpr int kLaunchRegs = NT == 2 ? 168 : 128;
   static constexpr int kSoftmaxRegs = NT == 2 ? 216 : 184, kOtherRegs = 72;
-  static_assert(NT * 128 * kSoftmaxRegs + 128 * kOtherRegs <= kThreads * (NT == 2 ? 168 : 128), "register split");
-  static constexpr uint32_t kTmemCols = NT * (kKeys + D) <= 256 ? 256 : 512;
+  static_assert(kSoftmaxWarps * 32 * kSoftmaxRegs + 128 * kOtherRegs <= kThreads * kLaunchRegs, "register split");
+  static constexpr uint32_t kTmemCols = NT * (2 * kStep + D) <= 256 ? 256 : 512;
   static constexpr size_t kSmem = 1024 + (size_t)(NT + kSlots) * kTile;
 };
 
@@ -233,16 +238,14 @@ __device__ __noinline__ void exact_row(const PrefillAttnArgs& a, const Row& w, l
       for (int e = 0; e < E; ++e) o[e] = o[e] * keep + p * __bfloat162float(a.v_cache[row + e]);
     }
   }
-  if (part >= 0) {
+  const float f = part >= 0 ? 1.f : l > 0.f ? 1.f / l : (l == l ? 0.f : l);
 #pragma unroll
-    for (int e = 0; e < E; ++e) a.part_o[part * D + lane * E + e] = o[e];
-    if (lane == 0) a.part_ml[part] = make_float2(m, l);
-  } else {
-    const float f = l > 0.f ? 1.f / l : (l == l ? 0.f : l);
-#pragma unroll
-    for (int e = 0; e < E; ++e)
-      a.out[((size_t)w.r * a.Hq + w.h) * D + lane * E + e] = __float2bfloat16_rn(o[e] * f);
+  for (int e = 0; e < E; ++e) {
+    const int c = lane * E + e;
+    if (part >= 0) a.part_o[part * D + c] = o[e];
+    else a.out[((size_t)w.r * a.Hq + w.h) * D + c] = __float2bfloat16_rn(o[e] * f);
   }
+  if (part >= 0 && lane == 0) a.part_ml[part] = make_float2(m, l);
 }
 
 // ------------------------------------------------------------------------------- the attention
@@ -255,6 +258,7 @@ struct Item {
   int tok0, tokens, nx;   // first token (of the sequence's queries), tokens, row tiles
   int pos0;               // position of the first token
   int pre_units, nblk, shift, nt_all, ts, nt;  // list entries, key tiles of the rows, this share's
+  int ns;                 // steps of this share
 
   __device__ __forceinline__ int block_of(int e) const { return e < pre_units ? e : e + shift; }
 };
@@ -290,11 +294,13 @@ __device__ __forceinline__ void set_keys(Item& w, int lo_min) {
   const int per = (w.nt_all + w.nsplit - 1) / w.nsplit;
   w.ts = min(w.split * per, w.nt_all);
   w.nt = min(w.ts + per, w.nt_all) - w.ts;
+  w.ns = (min(w.nblk, (w.ts + w.nt) * kTileBlocks) - w.ts * kTileBlocks + kStepBlocks - 1) / kStepBlocks;
 }
 
 template <int D, int NT>
 struct Shared {
-  uint64_t q_full, kv_full[Geo<D, NT>::kSlots], kv_empty[Geo<D, NT>::kSlots], s_full[NT], p_full[NT], pv_done[NT];
+  uint64_t q_full, kv_full[Geo<D, NT>::kSlots], kv_empty[Geo<D, NT>::kSlots];
+  uint64_t s_full[NT][2], p_full[NT][2], pv_done[NT][2];  // by buffer: S ready, P ready, P V added
   uint32_t tmem;
   int lo_min, lo_max[NT], abort;
 };
@@ -336,7 +342,7 @@ __device__ __forceinline__ void produce(const PrefillAttnArgs& a, Shared<D, NT>&
     const uint32_t have = __ballot_sync(kFullMask, id >= 0);
     for (int kv = 0; kv < 2; ++kv, ++n_kv) {
       const uint32_t slot = n_kv % NS;
-      if (n_kv >= NS) ok = mbar_wait_bounded(&sh.kv_empty[slot], ((n_kv / NS) - 1) & 1u, a.timeout_ns);
+      if (n_kv >= NS) ok = mbar_wait_spin(&sh.kv_empty[slot], ((n_kv / NS) - 1) & 1u, a.timeout_ns);
       ok = __all_sync(kFullMask, ok);
       if (!ok) break;
       unsigned char* dst = skv + slot * GE::kTile;
@@ -367,104 +373,133 @@ __device__ __forceinline__ void produce(const PrefillAttnArgs& a, Shared<D, NT>&
       record_error(a.err, PKV_DEV_WAIT_TIMEOUT);
       sh.abort = 1;
       // what is in flight lands before the CTA goes
-      (void)mbar_wait_bounded(&sh.q_full, n_q & 1u, a.timeout_ns);
+      (void)mbar_wait_spin(&sh.q_full, n_q & 1u, a.timeout_ns);
       for (uint32_t c = n_kv > NS ? n_kv - NS : 0; c < n_kv; ++c)
-        (void)mbar_wait_bounded(&sh.kv_full[c % NS], (c / NS) & 1u, a.timeout_ns);
+        (void)mbar_wait_spin(&sh.kv_full[c % NS], (c / NS) & 1u, a.timeout_ns);
     }
     __syncwarp();
   }
 }
 
-// Issues the item's MMAs (one thread).  Per key tile and row tile: O += P V of the tile whose P is ready,
-// then S = Q K^T of the next one into the same columns (the tensor core runs them in the order of issue).
+// Issues the item's MMAs (one warp, its elected lane; what the MMAs take is the same in every lane and kept
+// in uniform registers).  S has two buffers of 64 keys a row tile in tensor memory, and P takes the place of
+// its S: while the softmax works on step t, S of step t + 1 is there.  Per step and row tile: O += P V once P
+// is ready, then S = Q K^T of two steps on into the same columns (the tensor core runs them in the order of
+// issue).  n_step counts the steps of each row tile since the kernel's start.
 template <int D, int NT>
 __device__ __forceinline__ void issue_mmas(const PrefillAttnArgs& a, Shared<D, NT>& sh, const Item& w, unsigned char* sq,
-                                           uint32_t tmem, uint32_t& n_kv, uint32_t n_q, uint32_t (&n_tile)[NT]) {
+                                           uint32_t tmem_any, uint32_t leader, uint32_t& n_kv, uint32_t n_q,
+                                           uint32_t (&n_step)[NT]) {
   using GE = Geo<D, NT>;
   constexpr int NS = GE::kSlots;
-  constexpr uint32_t id_qk = umma_idesc_bf16(128, kKeys), id_pv = umma_idesc_bf16_bmn(128, D);
-  const uint32_t q0 = smem_u32(sq), kv0 = q0 + NT * GE::kTile;
-  const bool two = w.nt_all <= kTwoTermTiles;
-  auto qk = [&](int y, uint32_t slot) {
-    const uint32_t qa = q0 + y * GE::kTile, kb = kv0 + slot * GE::kTile;
+  constexpr uint32_t id_qk = umma_idesc_bf16(128, kStep), id_pv = umma_idesc_bf16_bmn(128, D);
+  auto uniform = [](uint32_t v) { return __shfl_sync(kFullMask, v, 0); };
+  const uint32_t tmem = uniform(tmem_any);
+  const int ns = (int)uniform((uint32_t)w.ns), nx = NT == 1 ? 1 : (int)uniform((uint32_t)w.nx);
+  const bool two = uniform((uint32_t)w.nt_all) <= (uint32_t)kTwoTermTiles;
+  const uint32_t base = uniform(smem_u32(sq)), bars = uniform(smem_u32(&sh));
+  const uint32_t q0 = umma_lo_k(base), k0 = umma_lo_k(base + NT * GE::kTile);
+  const uint32_t v0 = umma_lo_mn(base + NT * GE::kTile, kHalf);
+  constexpr uint32_t kTile16 = GE::kTile / 16, kStep16 = kStep * 128 / 16;  // descriptors count 16 bytes
+  using SH = Shared<D, NT>;
+  const uint32_t kv_base = uniform(n_kv);  // K of tile t is tile kv_base + 2 t of the ring, V the next
+  uint32_t step0[NT];
+#pragma unroll
+  for (int y = 0; y < NT; ++y) step0[y] = uniform(n_step[y]);
+  auto qk = [&](int y, int t) {
+    const uint32_t buf = (step0[y] + (uint32_t)t) & 1u;
+    const uint32_t qa = q0 + y * kTile16, d = tmem + y * 2 * kStep + buf * kStep;
+    const uint32_t kb = k0 + ((kv_base + (uint32_t)(t & ~1)) % NS) * kTile16 + (t & 1) * kStep16;
 #pragma unroll
     for (int k = 0; k < D / 16; ++k) {
-      const uint32_t off = (uint32_t)((k >> 2) * kHalf + (k & 3) * 32);
-      umma_bf16(tmem + y * kKeys, umma_desc_sw128(qa + off), umma_desc_sw128(kb + off), id_qk, k > 0);
+      const uint32_t off = (uint32_t)((k >> 2) * kHalf + (k & 3) * 32) / 16;
+      umma_bf16_lo(leader, d, qa + off, kb + off, id_qk, k > 0);
     }
-    umma_commit(&sh.s_full[y]);
+    umma_commit_by(leader, bars + (uint32_t)offsetof(SH, s_full) + (y * 2 + buf) * 8);
   };
-  auto pv = [&](int y, uint32_t slot, bool first_tile) {
-    const uint32_t vb = kv0 + slot * GE::kTile, o = tmem + NT * kKeys + y * D, p = tmem + y * kKeys;
+  auto pv = [&](int y, int t) {
+    const uint32_t buf = (step0[y] + (uint32_t)t) & 1u;
+    const uint32_t vb = v0 + ((kv_base + (uint32_t)(t | 1)) % NS) * kTile16 + (t & 1) * kStep16;
+    const uint32_t o = tmem + NT * 2 * kStep + y * D, p = tmem + y * 2 * kStep + buf * kStep;
 #pragma unroll
-    for (int k = 0; k < kKeys / 16; ++k)  // 32 keys' first terms, then their remainders, 16 columns each
-      umma_bf16_ts(o, p + 32 * (k >> 1) + 8 * (k & 1), umma_desc_mn_sw128(vb + k * 2048, kHalf), id_pv,
-                   !first_tile || k > 0);
+    for (int k = 0; k < kStep / 16; ++k)  // 32 keys' first terms, then their remainders, 16 columns each
+      umma_bf16_ts_lo(leader, o, p + 32 * (k >> 1) + 8 * (k & 1), vb + k * 128, id_pv, k > 0 || t > 0);
     if (two) {
 #pragma unroll
-      for (int k = 0; k < kKeys / 16; ++k)
-        umma_bf16_ts(o, p + 32 * (k >> 1) + 16 + 8 * (k & 1), umma_desc_mn_sw128(vb + k * 2048, kHalf), id_pv, true);
+      for (int k = 0; k < kStep / 16; ++k)
+        umma_bf16_ts_lo(leader, o, p + 32 * (k >> 1) + 16 + 8 * (k & 1), vb + k * 128, id_pv, true);
     }
-    umma_commit(&sh.pv_done[y]);
+    umma_commit_by(leader, bars + (uint32_t)offsetof(SH, pv_done) + (y * 2 + buf) * 8);
   };
+  auto free_tile = [&](uint32_t c) { umma_commit_by(leader, bars + (uint32_t)offsetof(SH, kv_empty) + (c % NS) * 8); };
   auto wait = [&](uint64_t* bar, uint32_t phase) {
-    if (mbar_wait_bounded(bar, phase & 1u, a.timeout_ns)) return true;
-    record_error(a.err, PKV_DEV_WAIT_TIMEOUT);
-    sh.abort = 1;
+    if (__all_sync(kFullMask, mbar_wait_spin(bar, phase & 1u, a.timeout_ns))) return true;
+    if (leader) {
+      record_error(a.err, PKV_DEV_WAIT_TIMEOUT);
+      sh.abort = 1;
+    }
     return false;
   };
-  bool ok = wait(&sh.q_full, n_q) && wait(&sh.kv_full[n_kv % NS], n_kv / NS);
+  auto wait_kv = [&](uint32_t c) { return wait(&sh.kv_full[c % NS], c / NS); };
+  bool ok = wait(&sh.q_full, n_q) && wait_kv(kv_base);
   if (ok) {
     tc_fence_after();
-    for (int y = 0; y < w.nx; ++y) qk(y, n_kv % NS);
-    umma_commit(&sh.kv_empty[n_kv % NS]);
-    ++n_kv;
+#pragma unroll
+    for (int t = 0; t < 2; ++t)
+#pragma unroll
+      for (int y = 0; y < NT; ++y)
+        if (t < ns && y < nx) qk(y, t);
+    free_tile(kv_base);  // the first K tile has no more steps
   }
-  for (int j = 0; j < w.nt && ok; ++j) {
-    const uint32_t vs = n_kv % NS, ks = (n_kv + 1) % NS;
-    const bool more = j + 1 < w.nt;
-    ok = wait(&sh.kv_full[vs], n_kv / NS);
-    for (int y = 0; y < w.nx && ok; ++y) {
-      ok = wait(&sh.p_full[y], n_tile[y]);
-      if (ok && y == 0 && more) ok = wait(&sh.kv_full[ks], (n_kv + 1) / NS);
-      if (!ok) break;
+  for (int t = 0; t < ns && ok; ++t) {
+    const bool more = t + 2 < ns;  // a further S; its K tile arrives with its first step
+    if ((t & 1) == 0) ok = wait_kv(kv_base + t + 1) && (!more || wait_kv(kv_base + t + 2));
+#pragma unroll
+    for (int y = 0; y < NT; ++y) {
+      if (y >= nx || !ok) continue;
+      const uint32_t c = step0[y] + (uint32_t)t;
+      ok = wait(&sh.p_full[y][c & 1u], c >> 1);
+      if (!ok) continue;
       tc_fence_after();
-      pv(y, vs, j == 0);
-      ++n_tile[y];
-      if (more) qk(y, ks);
+      pv(y, t);
+      if (more) qk(y, t + 2);
     }
     if (!ok) break;
-    umma_commit(&sh.kv_empty[vs]);
-    if (more) umma_commit(&sh.kv_empty[ks]);
-    n_kv += more ? 2 : 1;
+    if ((t & 1) || t + 1 == ns) free_tile(kv_base + (uint32_t)(t | 1));  // V of this tile
+    // K of the tile two steps on: after its second step, or its first where that is the last
+    if (more && ((t & 1) || t + 3 >= ns)) free_tile(kv_base + (uint32_t)((t + 2) & ~1));
   }
   if (!ok) {  // the MMAs in flight end before tensor memory goes
-    umma_commit(&sh.kv_empty[0]);
-    (void)mbar_wait_bounded(&sh.kv_empty[0], 0, a.timeout_ns / 64);
-    (void)mbar_wait_bounded(&sh.kv_empty[0], 1, a.timeout_ns / 64);
+    free_tile(0);
+    (void)mbar_wait_spin(&sh.kv_empty[0], 0, a.timeout_ns / 64);
+    (void)mbar_wait_spin(&sh.kv_empty[0], 1, a.timeout_ns / 64);
   }
+  n_kv = kv_base + 2 * w.nt;
+#pragma unroll
+  for (int y = 0; y < NT; ++y)
+    if (y < nx) n_step[y] = step0[y] + ns;
 }
 
-// Largest of a row's 128 values (of their sizes when ABS), in four chains.
-template <bool ABS>
-__device__ __forceinline__ float row_max(const float (&v)[kKeys]) {
+// Largest of N values (of their sizes when ABS), in four chains.
+template <bool ABS, int N>
+__device__ __forceinline__ float row_max(const float (&v)[N]) {
   float t[4];
 #pragma unroll
   for (int c = 0; c < 4; ++c) t[c] = ABS ? fabsf(v[c]) : v[c];
 #pragma unroll
-  for (int c = 4; c < kKeys; ++c) t[c & 3] = fmaxf(t[c & 3], ABS ? fabsf(v[c]) : v[c]);
+  for (int c = 4; c < N; ++c) t[c & 3] = fmaxf(t[c & 3], ABS ? fabsf(v[c]) : v[c]);
   return fmaxf(fmaxf(t[0], t[1]), fmaxf(t[2], t[3]));
 }
 
 // v = v * P(v^2 k^2) for the odd polynomial P of tanh (cap_logit): to u^5, or to u^9 with NINTH.
-template <bool NINTH>
-__device__ __forceinline__ void cap_poly(float (&v)[kKeys], float k) {
+template <bool NINTH, int N>
+__device__ __forceinline__ void cap_poly(float (&v)[N], float k) {
   const float w = k * k;
   const float c1 = -0.33333333f * w, c2 = 0.13333333f * w * w, c3 = -0.053968254f * w * w * w,
               c4 = 0.021869488f * w * w * w * w;
   const uint64_t p1 = pack2(c1, c1), p2 = pack2(c2, c2), p3 = pack2(c3, c3), p4 = pack2(c4, c4), p0 = pack2(1.f, 1.f);
 #pragma unroll
-  for (int c = 0; c < kKeys; c += 2) {
+  for (int c = 0; c < N; c += 2) {
     const uint64_t x = pack2(v[c], v[c + 1]);
     const uint64_t q = fmul2(x, x);
     uint64_t p = NINTH ? ffma2(ffma2(p4, q, p3), q, p2) : p2;
@@ -475,68 +510,76 @@ __device__ __forceinline__ void cap_poly(float (&v)[kKeys], float k) {
   }
 }
 
-// For the rules that need each key's own value: turns a row's 128 products S in place into numbers that
-// `return value` (> 0) times are the base-2 logits x = cap(S sl2) - slope |i - t|.  (Without such rules the
-// scale alone is that factor.)  e0: the tile's first list entry.
-__device__ __forceinline__ float apply_rules(const PrefillAttnArgs& a, float (&v)[kKeys], float slope2, int i,
-                                             const Item& w, int e0) {
-  float mul = a.scale_log2;
+// A thread's base-2 logits are v[c] mul + base + step (c / 8), mul > 0.
+struct Logits {
+  float mul, base, step;
+};
+
+// For the rules that need each key's own value: the products S of a thread's N keys, in place, brought into
+// that form of x = cap(S sl2) - slope |i - t|.  (Without such rules v = S and mul = sl2.)  e0: the list entry of
+// its first key.
+template <int N>
+__device__ __forceinline__ Logits apply_rules(const PrefillAttnArgs& a, float (&v)[N], float slope2, int i, const Item& w,
+                                              int e0) {
+  Logits x{a.scale_log2, 0.f, 0.f};
   if (a.cap_log2 > 0.f) {
     // u = S ku is the logit over the cap.  Where it is small for every key of the warp's rows the odd
     // polynomial serves: to u^5 below 0.11 (the next term is 0.054 u^6 of the value, 2^-23 there), to u^9
     // below 0.3; the general form costs an exponential and a reciprocal a key
     const float ku = a.scale_log2 * a.cap_in * 0.34657359f;
     const float far = row_max<true>(v) * fabsf(ku);
-    mul = a.cap_log2 * ku;
-    if (mul > 0.f && __all_sync(kFullMask, far < 0.11f)) {
+    x.mul = a.cap_log2 * ku;
+    if (x.mul > 0.f && __all_sync(kFullMask, far < 0.11f)) {
       cap_poly<false>(v, ku);
-    } else if (mul > 0.f && __all_sync(kFullMask, far < 0.3f)) {
+    } else if (x.mul > 0.f && __all_sync(kFullMask, far < 0.3f)) {
       cap_poly<true>(v, ku);
     } else {
 #pragma unroll
-      for (int c = 0; c < kKeys; ++c) v[c] = cap_logit(v[c] * a.scale_log2, a.cap_log2, a.cap_in);
-      mul = 1.f;
+      for (int c = 0; c < N; ++c) v[c] = cap_logit(v[c] * a.scale_log2, a.cap_log2, a.cap_in);
+      x.mul = 1.f;
     }
   }
   if (a.slopes != nullptr) {
-    const uint64_t m2 = pack2(mul, mul);
+    const uint64_t m2 = pack2(x.mul, x.mul);
     if (e0 >= w.pre_units) {
       // the interval's part of the list is one run of positions, and keys past i are masked: the distance
-      // is i - t, linear along the tile
-      const float b0 = -slope2 * (float)(i - w.block_of(e0) * 16);
-      const uint64_t b2 = pack2(b0, b0), s2 = pack2(slope2, slope2);
+      // is i - t, linear along the tile; within eight keys it is added here, the rest goes into the exponent
+      x.base = -slope2 * (float)(i - w.block_of(e0) * 16);
+      x.step = 8.f * slope2;
+      uint64_t near[4];
 #pragma unroll
-      for (int c = 0; c < kKeys; c += 2) {
-        const float2 y = unpack2(ffma2(pack2(v[c], v[c + 1]), m2, ffma2(pack2((float)c, (float)(c + 1)), s2, b2)));
+      for (int c = 0; c < 4; ++c) near[c] = pack2(slope2 * (float)(2 * c), slope2 * (float)(2 * c + 1));
+#pragma unroll
+      for (int c = 0; c < N; c += 2) {
+        const float2 y = unpack2(ffma2(pack2(v[c], v[c + 1]), m2, near[(c >> 1) & 3]));
         v[c] = y.x;
         v[c + 1] = y.y;
       }
     } else {
 #pragma unroll
-      for (int p = 0; p < kTileBlocks; ++p) {
+      for (int p = 0; p < N / 16; ++p) {
         const float d0 = (float)(i - w.block_of(e0 + p) * 16);
 #pragma unroll
-        for (int c = 0; c < 16; ++c) v[16 * p + c] = fmaf(-slope2, fabsf(d0 - (float)c), v[16 * p + c] * mul);
+        for (int c = 0; c < 16; ++c) v[16 * p + c] = fmaf(-slope2, fabsf(d0 - (float)c), v[16 * p + c] * x.mul);
       }
     }
-    return 1.f;
-  }
-  if (!(mul > 0.f)) {
+    x.mul = 1.f;
+  } else if (!(x.mul > 0.f)) {
 #pragma unroll
-    for (int c = 0; c < kKeys; ++c) v[c] *= mul;
-    return 1.f;
+    for (int c = 0; c < N; ++c) v[c] *= x.mul;
+    x.mul = 1.f;
   }
-  return mul;
+  return x;
 }
 
-// The item's softmax and output for this thread's row of row tile x: position i (-1: none), interval start
-// lo, prefix pre; prow and h name the output row.
+// The item's softmax and output for this thread's row r of row tile x: position i (-1: none), interval start
+// lo; prow and h name the output row.
 template <int D, int NT>
 __device__ __forceinline__ void softmax_rows(const PrefillAttnArgs& a, Shared<D, NT>& sh, const Item& w,
-                                             unsigned char* sq, uint32_t tmem, int x, int r, bool valid, int i, int lo,
-                                             int prow, int h, uint32_t n_kv, uint32_t& n_tile) {
+                                             unsigned char* sq, uint32_t tmem, int x, int r, bool valid, int i,
+                                             int lo, int prow, int h, uint32_t n_kv, uint32_t& n_step) {
   using GE = Geo<D, NT>;
-  constexpr int NS = GE::kSlots, H = GE::kHalves;
+  constexpr int NS = GE::kSlots, H = GE::kHalves, N = kStep;
   const int lane = threadIdx.x & 31;
   unsigned char* skv = sq + NT * GE::kTile;
   const float slope2 = valid && a.slopes != nullptr ? __ldg(a.slopes + h) * kLog2e : 0.f;
@@ -550,26 +593,30 @@ __device__ __forceinline__ void softmax_rows(const PrefillAttnArgs& a, Shared<D,
   const int tail_tile = (w.L & 15) != 0 && e_last >= 0 && e_last < w.nblk && w.block_of(e_last) == last_blk
                             ? e_last / kTileBlocks - w.ts : -1;
   const uint32_t t_lane = tmem + ((uint32_t)(r & ~31) << 16);
-  const uint32_t ts_addr = t_lane + x * kKeys, to_addr = t_lane + NT * kKeys + x * D;
-  float m = -INFINITY, l = 0.f;
+  const uint32_t to_addr = t_lane + NT * 2 * kStep + x * D;
   bool ok = true;
-  for (int j = 0; j < w.nt; ++j) {
-    ok = __all_sync(kFullMask, mbar_wait_bounded(&sh.s_full[x], n_tile & 1u, a.timeout_ns));
+  float m = -INFINITY, l = 0.f;
+  bool tail_done = false;
+  for (int j = 0; j < w.ns; ++j) {
+    const uint32_t buf = n_step & 1u;
+    const uint32_t ts_addr = t_lane + x * 2 * kStep + buf * kStep;
+    ok = __all_sync(kFullMask, mbar_wait_spin(&sh.s_full[x][buf], (n_step >> 1) & 1u, a.timeout_ns));
     if (!ok) break;
     tc_fence_after();
-    float v[kKeys];
+    float v[N];
 #pragma unroll
-    for (int c = 0; c < kKeys / 32; ++c) tmem_ld_x32(ts_addr + 32 * c, *reinterpret_cast<float(*)[32]>(v + 32 * c));
+    for (int c = 0; c < N / 32; ++c) tmem_ld_x32(ts_addr + 32 * c, *reinterpret_cast<float(*)[32]>(v + 32 * c));
     tmem_wait_ld();
-    const int e0 = (w.ts + j) * kTileBlocks;
-    const float mul = own_logits ? apply_rules(a, v, slope2, i, w, e0) : a.scale_log2;
-    // all keys of the tile seen by all rows of the row tile?
+    const int e0 = w.ts * kTileBlocks + j * kStepBlocks;
+    Logits y{a.scale_log2, 0.f, 0.f};
+    if (own_logits) y = apply_rules(a, v, slope2, i, w, e0);
+    // all these keys seen by all rows of the row tile?
     const int t_first = w.block_of(e0) * 16;
-    const bool full = (e0 >= w.pre_units && t_first >= lo_max && t_first + kKeys - 1 <= i_min) ||
-                      (e0 + kTileBlocks <= w.pre_units && t_first + kKeys <= w.pre);
+    const bool full = (e0 >= w.pre_units && t_first >= lo_max && t_first + N - 1 <= i_min) ||
+                      (e0 + N / 16 <= w.pre_units && t_first + N <= w.pre);
     if (!full) {
 #pragma unroll
-      for (int p = 0; p < kTileBlocks; ++p) {
+      for (int p = 0; p < N / 16; ++p) {
         const int t0 = w.block_of(e0 + p) * 16;
         const int hi_c = i - t0, lo_c = lo - t0, pre_c = pre - t0;
         uint32_t see = hi_c >= 15 ? 0xffffu : hi_c < 0 ? 0u : (2u << hi_c) - 1u;
@@ -579,14 +626,26 @@ __device__ __forceinline__ void softmax_rows(const PrefillAttnArgs& a, Shared<D,
         for (int c = 0; c < 16; ++c) v[16 * p + c] = ((see >> c) & 1u) ? v[16 * p + c] : -INFINITY;
       }
     }
-    const float mx = row_max<false>(v) * mul;
+    float mx;
+    if (y.step == 0.f) {
+      mx = fmaf(row_max<false>(v), y.mul, y.base);
+    } else {
+      mx = -INFINITY;
+#pragma unroll
+      for (int g = 0; g < N / 8; ++g) {
+        float t = v[8 * g];
+#pragma unroll
+        for (int c = 1; c < 8; ++c) t = fmaxf(t, v[8 * g + c]);
+        mx = fmaxf(mx, t + fmaf(y.step, (float)g, y.base));
+      }
+    }
     const bool move = mx > m + kSlack;
     if (__any_sync(kFullMask, move)) {
       const float scale = move ? ex2_approx(m - mx) : 1.f;
       if (move) m = mx;
       l *= scale;
       if (j > 0) {  // O moves to the new reference once the last product has ended
-        ok = __all_sync(kFullMask, mbar_wait_bounded(&sh.pv_done[x], (n_tile - 1) & 1u, a.timeout_ns));
+        ok = __all_sync(kFullMask, mbar_wait_spin(&sh.pv_done[x][(n_step - 1) & 1u], ((n_step - 1) >> 1) & 1u, a.timeout_ns));
         if (!ok) break;
         tc_fence_after();
 #pragma unroll
@@ -601,31 +660,33 @@ __device__ __forceinline__ void softmax_rows(const PrefillAttnArgs& a, Shared<D,
         }
       }
     }
-    const float ref = m == -INFINITY ? 0.f : m;
-    const uint64_t mul2 = pack2(mul, mul), nref2 = pack2(-ref, -ref);
+    y.base -= m == -INFINITY ? 0.f : m;
+    const uint64_t mul2 = pack2(y.mul, y.mul);
     uint64_t sum2[4];
 #pragma unroll
     for (int k = 0; k < 4; ++k) sum2[k] = pack2(0.f, 0.f);
     if (!two) {
 #pragma unroll
-      for (int c = 0; c < kKeys / 32; ++c) {
+      for (int c = 0; c < N / 32; ++c) {
         uint32_t hi[16];
 #pragma unroll
         for (int k = 0; k < 16; ++k) {
-          const float2 y = unpack2(ffma2(pack2(v[32 * c + 2 * k], v[32 * c + 2 * k + 1]), mul2, nref2));
-          hi[k] = pack_bf16x2(ex2_approx(y.x), ex2_approx(y.y));
+          const float off = fmaf(y.step, (float)(4 * c + k / 4), y.base);
+          const float2 z = unpack2(ffma2(pack2(v[32 * c + 2 * k], v[32 * c + 2 * k + 1]), mul2, pack2(off, off)));
+          hi[k] = pack_bf16x2(ex2_approx(z.x), ex2_approx(z.y));
           sum2[k & 3] = fadd2(sum2[k & 3], bf16x2_to_f32x2(hi[k]));
         }
         tmem_st_x16(ts_addr + 32 * c, hi);
       }
     } else {
 #pragma unroll
-      for (int c = 0; c < kKeys / 32; ++c) {
+      for (int c = 0; c < N / 32; ++c) {
         uint32_t hi[16], rest[16];
 #pragma unroll
         for (int k = 0; k < 16; ++k) {
-          const float2 y = unpack2(ffma2(pack2(v[32 * c + 2 * k], v[32 * c + 2 * k + 1]), mul2, nref2));
-          const float p0 = ex2_approx(y.x), p1 = ex2_approx(y.y);
+          const float off = fmaf(y.step, (float)(4 * c + k / 4), y.base);
+          const float2 z = unpack2(ffma2(pack2(v[32 * c + 2 * k], v[32 * c + 2 * k + 1]), mul2, pack2(off, off)));
+          const float p0 = ex2_approx(z.x), p1 = ex2_approx(z.y);
           hi[k] = pack_bf16x2(p0, p1);
           rest[k] = pack_bf16x2(p0 - bf16_lo_to_f32(hi[k]), p1 - bf16_hi_to_f32(hi[k]));
           sum2[k & 3] = fadd2(sum2[k & 3], pack2(p0, p1));
@@ -636,9 +697,11 @@ __device__ __forceinline__ void softmax_rows(const PrefillAttnArgs& a, Shared<D,
     }
     const float2 sum = unpack2(fadd2(fadd2(sum2[0], sum2[1]), fadd2(sum2[2], sum2[3])));
     l += sum.x + sum.y;
-    if (x == 0 && j == tail_tile) {
-      const uint32_t vtile = n_kv + 2 * j + 1;  // this tile's V in the count of K and V tiles
-      ok = __all_sync(kFullMask, mbar_wait_bounded(&sh.kv_full[vtile % NS], (vtile / NS) & 1u, a.timeout_ns));
+    if (x == 0 && (j >> 1) == tail_tile && ((j & 1) || j + 1 == w.ns || (e_last % kTileBlocks) < kStepBlocks) &&
+        !tail_done) {
+      tail_done = true;
+      const uint32_t vtile = n_kv + 2 * (j >> 1) + 1;  // this tile's V in the count of K and V tiles
+      ok = __all_sync(kFullMask, mbar_wait_spin(&sh.kv_full[vtile % NS], (vtile / NS) & 1u, a.timeout_ns));
       if (!ok) break;
       unsigned char* rows = skv + (vtile % NS) * GE::kTile + (e_last % kTileBlocks) * 2048;
       const int gone = 16 - (w.L & 15);
@@ -650,11 +713,11 @@ __device__ __forceinline__ void softmax_rows(const PrefillAttnArgs& a, Shared<D,
     tmem_wait_st();
     tc_fence_before();
     __syncwarp();
-    if (lane == 0) mbar_arrive(&sh.p_full[x]);
-    ++n_tile;
+    if (lane == 0) mbar_arrive(&sh.p_full[x][buf]);
+    ++n_step;
   }
-  if (ok && w.nt > 0) {
-    ok = __all_sync(kFullMask, mbar_wait_bounded(&sh.pv_done[x], (n_tile - 1) & 1u, a.timeout_ns));
+  if (ok && w.ns > 0) {
+    ok = __all_sync(kFullMask, mbar_wait_spin(&sh.pv_done[x][(n_step - 1) & 1u], ((n_step - 1) >> 1) & 1u, a.timeout_ns));
     tc_fence_after();
   }
   if (!ok) {
@@ -668,18 +731,18 @@ __device__ __forceinline__ void softmax_rows(const PrefillAttnArgs& a, Shared<D,
   const bool split = w.nsplit > 1;
   const long long part = split ? (long long)a.plan_seq[w.b].y + ((long long)w.split * w.n + (prow - w.q0)) * a.Hq + h : 0;
   const float f = split ? 1.f : (l > 0.f ? 1.f / l : 0.f);
-  bool bad = false;
+  bool bad = !(l <= 3.4028234e38f);
 #pragma unroll
   for (int c = 0; c < D / 16; ++c) {
     float o[16];
     __syncwarp();
-    if (w.nt > 0) {
+    if (w.ns > 0) {
       tmem_ld_x16(to_addr + 16 * c, o);
       tmem_wait_ld();
     }
 #pragma unroll
     for (int k = 0; k < 16; ++k) {
-      o[k] = w.nt > 0 ? o[k] * f : 0.f;
+      o[k] = w.ns > 0 ? o[k] * f : 0.f;
       bad |= !(fabsf(o[k]) <= 3.4028234e38f);
     }
     if (valid && split) {
@@ -696,7 +759,7 @@ __device__ __forceinline__ void softmax_rows(const PrefillAttnArgs& a, Shared<D,
   }
   if (split && valid) a.part_ml[part] = make_float2(m, l);
   // rows that are not finite: key by key over what they see
-  uint32_t again = __ballot_sync(kFullMask, valid && (bad || !(l <= 3.4028234e38f)));
+  uint32_t again = __ballot_sync(kFullMask, valid && bad);
   while (again != 0u) {
     const int src = __ffs(again) - 1;
     again &= again - 1;
@@ -731,9 +794,11 @@ prefill_attention_kernel(const __grid_constant__ PrefillAttnArgs a) {
       mbar_init(&sh.kv_empty[s], 1);
     }
     for (int x = 0; x < NT; ++x) {
-      mbar_init(&sh.s_full[x], 1);
-      mbar_init(&sh.p_full[x], 4);
-      mbar_init(&sh.pv_done[x], 1);
+      for (int q = 0; q < 2; ++q) {
+        mbar_init(&sh.s_full[x][q], 1);
+        mbar_init(&sh.p_full[x][q], 4);
+        mbar_init(&sh.pv_done[x][q], 1);
+      }
     }
     sh.abort = 0;
     fence_mbar_init();
@@ -752,11 +817,12 @@ prefill_attention_kernel(const __grid_constant__ PrefillAttnArgs a) {
   // Each role has the whole item loop, so that its registers are its own.  Three block barriers an item:
   // the shared minimum is reset, it is complete, every role has left the item.
   uint32_t n_kv = 0, n_q = 0;  // K and V tiles, and items with tiles, since the kernel's start (barrier phases)
-  if (warp < NT * 4) {
+  if (warp < GE::kSoftmaxWarps) {
     setmaxnreg_inc<GE::kSoftmaxRegs>();
+    // a warp reaches the tensor memory lanes of its number mod 4
     const int x = warp >> 2, r = 32 * (warp & 3) + lane;
     const int tok = r / a.G, head = r - tok * a.G;
-    uint32_t n_tile = 0;
+    uint32_t n_step = 0;
     for (int it = blockIdx.x; it < total; it += gridDim.x) {
       Item w = load_item(a, it, NT);
       if (threadIdx.x == 0) {
@@ -777,7 +843,7 @@ prefill_attention_kernel(const __grid_constant__ PrefillAttnArgs a) {
       __syncthreads();
       set_keys(w, sh.lo_min);
       if (x < w.nx)
-        softmax_rows<D, NT>(a, sh, w, sq, tmem, x, r, valid, i, lo, prow, w.g * a.G + head, n_kv, n_tile);
+        softmax_rows<D, NT>(a, sh, w, sq, tmem, x, r, valid, i, lo, prow, w.g * a.G + head, n_kv, n_step);
       n_kv += 2 * w.nt;
       tc_fence_before();
       __syncthreads();
@@ -785,18 +851,19 @@ prefill_attention_kernel(const __grid_constant__ PrefillAttnArgs a) {
     }
   } else {
     setmaxnreg_dec<GE::kOtherRegs>();
-    uint32_t n_tile[NT] = {};
+    uint32_t n_step[NT] = {};
+    const uint32_t leader = elect_one();
     for (int it = blockIdx.x; it < total; it += gridDim.x) {
       Item w = load_item(a, it, NT);
       __syncthreads();
       __syncthreads();
       set_keys(w, sh.lo_min);
       if (w.nt > 0) {
-        if (warp == NT * 4) {
+        if (warp == GE::kSoftmaxWarps) {
           produce<D, NT>(a, sh, w, sq, n_kv, n_q);
-        } else if (warp == NT * 4 + 1 && lane == 0) {
+        } else if (warp == GE::kSoftmaxWarps + 1) {
           tc_fence_after();
-          issue_mmas<D, NT>(a, sh, w, sq, tmem, n_kv, n_q, n_tile);
+          issue_mmas<D, NT>(a, sh, w, sq, tmem, leader, n_kv, n_q, n_step);
         }
         ++n_q;
       }

@@ -69,6 +69,20 @@ __device__ __forceinline__ bool mbar_wait_bounded(uint64_t* bar, uint32_t parity
   }
 }
 
+// The same for waits on a critical path: the clock is read only once in 256 tries (reading it takes longer
+// than most waits).
+__device__ __forceinline__ bool mbar_wait_spin(uint64_t* bar, uint32_t parity, uint64_t limit_ns) {
+  uint64_t t0 = 0;
+  for (uint32_t n = 0;; ++n) {
+    if (mbar_try_wait(bar, parity)) return true;
+    if ((n & 255u) == 255u) {
+      const uint64_t t = global_timer_ns();
+      if (t0 == 0) t0 = t;
+      else if (t - t0 > limit_ns) return false;
+    }
+  }
+}
+
 // ------------------------------------------------------------------------------ bulk copies
 
 // L2 policy: streamed K/V tiles are read once per step; evict them first.
@@ -186,24 +200,56 @@ __device__ __forceinline__ void umma_bf16(uint32_t d_tmem, uint64_t a_desc, uint
       : "memory");
 }
 
-// Descriptor of an MN-major operand (rows along K: the contraction's index) with the 128-byte swizzle:
-// each K row holds 64 elements of the M or N index in 128 bytes, 8 rows are 1024 bytes, and the next 64
-// elements of M or N start `mn_stride` bytes on.
-__device__ __forceinline__ uint64_t umma_desc_mn_sw128(uint32_t saddr, uint32_t mn_stride) {
-  return (uint64_t)((saddr & 0x3FFFFu) >> 4) | ((uint64_t)(mn_stride >> 4) << 16) | ((uint64_t)(1024 >> 4) << 32) |
-         ((uint64_t)1 << 46) | ((uint64_t)2 << 61);
+// The same descriptors as a low word, which alone depends on the address (adding bytes / 16 to it moves
+// the operand), and the high word common to both.
+constexpr uint32_t kUmmaDescHi = (1024u >> 4) | (1u << 14) | (2u << 29);
+__device__ __forceinline__ uint32_t umma_lo_k(uint32_t saddr) { return ((saddr & 0x3FFFFu) >> 4) | (1u << 16); }
+// MN-major operand (rows along K, the contraction's index): each K row holds 64 elements of the M or N index
+// in 128 bytes, 8 rows are 1024 bytes, and the next 64 elements of M or N start `mn_stride` bytes on.
+__device__ __forceinline__ uint32_t umma_lo_mn(uint32_t saddr, uint32_t mn_stride) {
+  return ((saddr & 0x3FFFFu) >> 4) | ((mn_stride >> 4) << 16);
+}
+
+// 1 in one lane of a converged warp, 0 in the others.
+__device__ __forceinline__ uint32_t elect_one() {
+  uint32_t leader;
+  asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(leader));
+  return leader;
 }
 
 // As umma_idesc_bf16, B MN-major.
 __host__ __device__ constexpr uint32_t umma_idesc_bf16_bmn(int m, int n) { return umma_idesc_bf16(m, n) | (1u << 16); }
 
-// D = A * B^T (+ D when accumulate) with A (M x 16 bf16, two to a 32-bit column) in tensor memory.
-__device__ __forceinline__ void umma_bf16_ts(uint32_t d_tmem, uint32_t a_tmem, uint64_t b_desc, uint32_t idesc,
+// D = A * B^T (+ D when accumulate), operands by their descriptors' low words.  Executed by a whole warp with
+// the same arguments, issued by its lane with leader != 0: the operands then stay in uniform registers, which
+// the instruction needs (a single diverged thread moves each of them there first, ~90 cycles an MMA).
+__device__ __forceinline__ void umma_bf16_lo(uint32_t leader, uint32_t d_tmem, uint32_t a_lo, uint32_t b_lo, uint32_t idesc,
                                              bool accumulate) {
   asm volatile(
-      "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
-      "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d_tmem),
-      "r"(a_tmem), "l"(b_desc), "r"(idesc), "r"((uint32_t)accumulate)
+      "{\n\t.reg .pred p, q;\n\t.reg .b64 da, db;\n\tsetp.ne.b32 p, %4, 0;\n\tsetp.ne.b32 q, %6, 0;\n\t"
+      "mov.b64 da, {%1, %5};\n\tmov.b64 db, {%2, %5};\n\t"
+      "@q tcgen05.mma.cta_group::1.kind::f16 [%0], da, db, %3, p;\n\t}" ::"r"(d_tmem),
+      "r"(a_lo), "r"(b_lo), "r"(idesc), "r"((uint32_t)accumulate), "n"(kUmmaDescHi), "r"(leader)
+      : "memory");
+}
+
+// The same with A (M x 16 bf16, two to a 32-bit column) in tensor memory.
+__device__ __forceinline__ void umma_bf16_ts_lo(uint32_t leader, uint32_t d_tmem, uint32_t a_tmem, uint32_t b_lo,
+                                                uint32_t idesc, bool accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p, q;\n\t.reg .b64 db;\n\tsetp.ne.b32 p, %4, 0;\n\tsetp.ne.b32 q, %6, 0;\n\t"
+      "mov.b64 db, {%2, %5};\n\t"
+      "@q tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], db, %3, p;\n\t}" ::"r"(d_tmem),
+      "r"(a_tmem), "r"(b_lo), "r"(idesc), "r"((uint32_t)accumulate), "n"(kUmmaDescHi), "r"(leader)
+      : "memory");
+}
+
+// umma_commit by the lane that issued (leader != 0) of a whole warp.
+__device__ __forceinline__ void umma_commit_by(uint32_t leader, uint32_t bar_smem) {
+  asm volatile(
+      "{\n\t.reg .pred q;\n\tsetp.ne.b32 q, %1, 0;\n\t"
+      "@q tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n\t}" ::"r"(bar_smem),
+      "r"(leader)
       : "memory");
 }
 
