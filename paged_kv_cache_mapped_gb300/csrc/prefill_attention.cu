@@ -79,7 +79,7 @@ struct Geo {
   static constexpr int kTile = kHalves * kHalf;  // bytes of a Q, K or V tile
   static constexpr int kSlots = NT == 2 ? (D == 128 ? 4 : 8) : (D == 128 ? 2 : 5);
   static constexpr int kSoftmaxWarps = NT * 4;           // a row a thread
-  static constexpr int kThreads = NT * 128 + 128;        // and producer, issuer, two idle warps
+  static constexpr int kThreads = NT * 128 + 128;        // and producer, issuers, idle warps
   static constexpr int kCtas = NT == 1 ? 2 : 1;  // per SM (shared and tensor memory allow no more)
   // Registers a thread: a launch gives every warp the same, which the softmax warps (their logits are in
   // registers) then take from the others.  NT = 2: 384 x 168 = 256 x 216 + 128 x 72; NT = 1 (two CTAs):
@@ -301,6 +301,7 @@ template <int D, int NT>
 struct Shared {
   uint64_t q_full, kv_full[Geo<D, NT>::kSlots], kv_empty[Geo<D, NT>::kSlots];
   uint64_t s_full[NT][2], p_full[NT][2], pv_done[NT][2];  // by buffer: S ready, P ready, P V added
+  uint64_t drained[NT];  // after a timeout: the MMAs issued have ended
   uint32_t tmem;
   int lo_min, lo_max[NT], abort;
 };
@@ -381,56 +382,23 @@ __device__ __forceinline__ void produce(const PrefillAttnArgs& a, Shared<D, NT>&
   }
 }
 
-// Issues the item's MMAs (one warp, its elected lane; what the MMAs take is the same in every lane and kept
-// in uniform registers).  S has two buffers of 64 keys a row tile in tensor memory, and P takes the place of
-// its S: while the softmax works on step t, S of step t + 1 is there.  Per step and row tile: O += P V once P
-// is ready, then S = Q K^T of two steps on into the same columns (the tensor core runs them in the order of
-// issue).  n_step counts the steps of each row tile since the kernel's start.
+// Issues the MMAs of the item's row tile y (a warp for each row tile, its elected lane; what the MMAs take is the
+// same in every lane and kept in uniform registers).  S has two buffers of 64 keys in tensor memory, and P
+// takes the place of its S: while the softmax works on step t, S of step t + 1 is there.  Per step: O += P V
+// once P is ready, then S = Q K^T of two steps on into the same columns (the tensor core runs one thread's
+// MMAs in the order of issue).  With a warp for each row tile, what one spends on its barriers passes under the
+// other's MMAs.  A ring tile is free once both have read it; a row tile that the item does not have only says so.
 template <int D, int NT>
 __device__ __forceinline__ void issue_mmas(const PrefillAttnArgs& a, Shared<D, NT>& sh, const Item& w, unsigned char* sq,
-                                           uint32_t tmem_any, uint32_t leader, uint32_t& n_kv, uint32_t n_q,
-                                           uint32_t (&n_step)[NT]) {
+                                           uint32_t tmem_any, uint32_t leader, int y, uint32_t& n_kv, uint32_t n_q,
+                                           uint32_t& n_step) {
   using GE = Geo<D, NT>;
+  using SH = Shared<D, NT>;
   constexpr int NS = GE::kSlots;
   constexpr uint32_t id_qk = umma_idesc_bf16(128, kStep), id_pv = umma_idesc_bf16_bmn(128, D);
   auto uniform = [](uint32_t v) { return __shfl_sync(kFullMask, v, 0); };
-  const uint32_t tmem = uniform(tmem_any);
-  const int ns = (int)uniform((uint32_t)w.ns), nx = NT == 1 ? 1 : (int)uniform((uint32_t)w.nx);
-  const bool two = uniform((uint32_t)w.nt_all) <= (uint32_t)kTwoTermTiles;
   const uint32_t base = uniform(smem_u32(sq)), bars = uniform(smem_u32(&sh));
-  const uint32_t q0 = umma_lo_k(base), k0 = umma_lo_k(base + NT * GE::kTile);
-  const uint32_t v0 = umma_lo_mn(base + NT * GE::kTile, kHalf);
-  constexpr uint32_t kTile16 = GE::kTile / 16, kStep16 = kStep * 128 / 16;  // descriptors count 16 bytes
-  using SH = Shared<D, NT>;
   const uint32_t kv_base = uniform(n_kv);  // K of tile t is tile kv_base + 2 t of the ring, V the next
-  uint32_t step0[NT];
-#pragma unroll
-  for (int y = 0; y < NT; ++y) step0[y] = uniform(n_step[y]);
-  auto qk = [&](int y, int t) {
-    const uint32_t buf = (step0[y] + (uint32_t)t) & 1u;
-    const uint32_t qa = q0 + y * kTile16, d = tmem + y * 2 * kStep + buf * kStep;
-    const uint32_t kb = k0 + ((kv_base + (uint32_t)(t & ~1)) % NS) * kTile16 + (t & 1) * kStep16;
-#pragma unroll
-    for (int k = 0; k < D / 16; ++k) {
-      const uint32_t off = (uint32_t)((k >> 2) * kHalf + (k & 3) * 32) / 16;
-      umma_bf16_lo(leader, d, qa + off, kb + off, id_qk, k > 0);
-    }
-    umma_commit_by(leader, bars + (uint32_t)offsetof(SH, s_full) + (y * 2 + buf) * 8);
-  };
-  auto pv = [&](int y, int t) {
-    const uint32_t buf = (step0[y] + (uint32_t)t) & 1u;
-    const uint32_t vb = v0 + ((kv_base + (uint32_t)(t | 1)) % NS) * kTile16 + (t & 1) * kStep16;
-    const uint32_t o = tmem + NT * 2 * kStep + y * D, p = tmem + y * 2 * kStep + buf * kStep;
-#pragma unroll
-    for (int k = 0; k < kStep / 16; ++k)  // 32 keys' first terms, then their remainders, 16 columns each
-      umma_bf16_ts_lo(leader, o, p + 32 * (k >> 1) + 8 * (k & 1), vb + k * 128, id_pv, k > 0 || t > 0);
-    if (two) {
-#pragma unroll
-      for (int k = 0; k < kStep / 16; ++k)
-        umma_bf16_ts_lo(leader, o, p + 32 * (k >> 1) + 16 + 8 * (k & 1), vb + k * 128, id_pv, true);
-    }
-    umma_commit_by(leader, bars + (uint32_t)offsetof(SH, pv_done) + (y * 2 + buf) * 8);
-  };
   auto free_tile = [&](uint32_t c) { umma_commit_by(leader, bars + (uint32_t)offsetof(SH, kv_empty) + (c % NS) * 8); };
   auto wait = [&](uint64_t* bar, uint32_t phase) {
     if (__all_sync(kFullMask, mbar_wait_spin(bar, phase & 1u, a.timeout_ns))) return true;
@@ -441,43 +409,71 @@ __device__ __forceinline__ void issue_mmas(const PrefillAttnArgs& a, Shared<D, N
     return false;
   };
   auto wait_kv = [&](uint32_t c) { return wait(&sh.kv_full[c % NS], c / NS); };
-  bool ok = wait(&sh.q_full, n_q) && wait_kv(kv_base);
+  n_kv = kv_base + 2 * w.nt;
+  bool ok = true;
+  if (y >= w.nx) {
+    for (uint32_t c = kv_base; c < kv_base + 2 * (uint32_t)w.nt && ok; ++c) {
+      ok = wait_kv(c);
+      if (ok) free_tile(c);
+    }
+    return;
+  }
+  const int ns = (int)uniform((uint32_t)w.ns);
+  const bool two = uniform((uint32_t)w.nt_all) <= (uint32_t)kTwoTermTiles;
+  const uint32_t step0 = uniform(n_step);
+  const uint32_t s0 = uniform(tmem_any) + y * 2 * kStep, o = uniform(tmem_any) + NT * 2 * kStep + y * D;
+  constexpr uint32_t kTile16 = GE::kTile / 16, kStep16 = kStep * 128 / 16;  // descriptors count 16 bytes
+  const uint32_t qa = umma_lo_k(base) + y * kTile16, k0 = umma_lo_k(base + NT * GE::kTile);
+  const uint32_t v0 = umma_lo_mn(base + NT * GE::kTile, kHalf);
+  auto qk = [&](int t) {
+    const uint32_t buf = (step0 + (uint32_t)t) & 1u;
+    const uint32_t kb = k0 + ((kv_base + (uint32_t)(t & ~1)) % NS) * kTile16 + (t & 1) * kStep16;
+#pragma unroll
+    for (int k = 0; k < D / 16; ++k) {
+      const uint32_t off = (uint32_t)((k >> 2) * kHalf + (k & 3) * 32) / 16;
+      umma_bf16_lo(leader, s0 + buf * kStep, qa + off, kb + off, id_qk, k > 0);
+    }
+    umma_commit_by(leader, bars + (uint32_t)offsetof(SH, s_full) + (y * 2 + buf) * 8);
+  };
+  auto pv = [&](int t) {
+    const uint32_t buf = (step0 + (uint32_t)t) & 1u;
+    const uint32_t vb = v0 + ((kv_base + (uint32_t)(t | 1)) % NS) * kTile16 + (t & 1) * kStep16;
+    const uint32_t p = s0 + buf * kStep;
+#pragma unroll
+    for (int k = 0; k < kStep / 16; ++k)  // 32 keys' first terms, then their remainders, 16 columns each
+      umma_bf16_ts_lo(leader, o, p + 32 * (k >> 1) + 8 * (k & 1), vb + k * 128, id_pv, k > 0 || t > 0);
+    if (two) {
+#pragma unroll
+      for (int k = 0; k < kStep / 16; ++k)
+        umma_bf16_ts_lo(leader, o, p + 32 * (k >> 1) + 16 + 8 * (k & 1), vb + k * 128, id_pv, true);
+    }
+    umma_commit_by(leader, bars + (uint32_t)offsetof(SH, pv_done) + (y * 2 + buf) * 8);
+  };
+  ok = wait(&sh.q_full, n_q) && wait_kv(kv_base);
   if (ok) {
     tc_fence_after();
-#pragma unroll
-    for (int t = 0; t < 2; ++t)
-#pragma unroll
-      for (int y = 0; y < NT; ++y)
-        if (t < ns && y < nx) qk(y, t);
+    qk(0);
+    if (ns > 1) qk(1);
     free_tile(kv_base);  // the first K tile has no more steps
   }
   for (int t = 0; t < ns && ok; ++t) {
     const bool more = t + 2 < ns;  // a further S; its K tile arrives with its first step
     if ((t & 1) == 0) ok = wait_kv(kv_base + t + 1) && (!more || wait_kv(kv_base + t + 2));
-#pragma unroll
-    for (int y = 0; y < NT; ++y) {
-      if (y >= nx || !ok) continue;
-      const uint32_t c = step0[y] + (uint32_t)t;
-      ok = wait(&sh.p_full[y][c & 1u], c >> 1);
-      if (!ok) continue;
-      tc_fence_after();
-      pv(y, t);
-      if (more) qk(y, t + 2);
-    }
+    const uint32_t c = step0 + (uint32_t)t;
+    ok = ok && wait(&sh.p_full[y][c & 1u], c >> 1);
     if (!ok) break;
+    tc_fence_after();
+    pv(t);
+    if (more) qk(t + 2);
     if ((t & 1) || t + 1 == ns) free_tile(kv_base + (uint32_t)(t | 1));  // V of this tile
     // K of the tile two steps on: after its second step, or its first where that is the last
     if (more && ((t & 1) || t + 3 >= ns)) free_tile(kv_base + (uint32_t)((t + 2) & ~1));
   }
   if (!ok) {  // the MMAs in flight end before tensor memory goes
-    free_tile(0);
-    (void)mbar_wait_spin(&sh.kv_empty[0], 0, a.timeout_ns / 64);
-    (void)mbar_wait_spin(&sh.kv_empty[0], 1, a.timeout_ns / 64);
+    umma_commit_by(leader, bars + (uint32_t)offsetof(SH, drained) + y * 8);
+    (void)mbar_wait_spin(&sh.drained[y], 0, a.timeout_ns);
   }
-  n_kv = kv_base + 2 * w.nt;
-#pragma unroll
-  for (int y = 0; y < NT; ++y)
-    if (y < nx) n_step[y] = step0[y] + ns;
+  n_step = step0 + ns;
 }
 
 // Largest of N values (of their sizes when ABS), in four chains.
@@ -587,7 +583,8 @@ __device__ __forceinline__ void softmax_rows(const PrefillAttnArgs& a, Shared<D,
   const bool two = w.nt_all <= kTwoTermTiles;
   const bool own_logits = a.cap_log2 > 0.f || a.slopes != nullptr || !(a.scale_log2 > 0.f);
   const int i_min = w.pos0 + x * a.R, lo_max = sh.lo_max[x];
-  // the block that ends past the sequence: its V rows there are cleared by the first row tile's warps
+  // the block that ends past the sequence: its V rows there are cleared, by the warps of each row tile before
+  // they hand over the step's P (both write the same zeros)
   const int last_blk = (w.L - 1) >> 4;
   const int e_last = last_blk < w.pre_units ? last_blk : last_blk - w.shift;
   const int tail_tile = (w.L & 15) != 0 && e_last >= 0 && e_last < w.nblk && w.block_of(e_last) == last_blk
@@ -697,7 +694,7 @@ __device__ __forceinline__ void softmax_rows(const PrefillAttnArgs& a, Shared<D,
     }
     const float2 sum = unpack2(fadd2(fadd2(sum2[0], sum2[1]), fadd2(sum2[2], sum2[3])));
     l += sum.x + sum.y;
-    if (x == 0 && (j >> 1) == tail_tile && ((j & 1) || j + 1 == w.ns || (e_last % kTileBlocks) < kStepBlocks) &&
+    if ((j >> 1) == tail_tile && ((j & 1) || j + 1 == w.ns || (e_last % kTileBlocks) < kStepBlocks) &&
         !tail_done) {
       tail_done = true;
       const uint32_t vtile = n_kv + 2 * (j >> 1) + 1;  // this tile's V in the count of K and V tiles
@@ -791,9 +788,10 @@ prefill_attention_kernel(const __grid_constant__ PrefillAttnArgs a) {
     mbar_init(&sh.q_full, 1);
     for (int s = 0; s < GE::kSlots; ++s) {
       mbar_init(&sh.kv_full[s], 1);
-      mbar_init(&sh.kv_empty[s], 1);
+      mbar_init(&sh.kv_empty[s], NT);
     }
     for (int x = 0; x < NT; ++x) {
+      mbar_init(&sh.drained[x], 1);
       for (int q = 0; q < 2; ++q) {
         mbar_init(&sh.s_full[x][q], 1);
         mbar_init(&sh.p_full[x][q], 4);
@@ -851,7 +849,7 @@ prefill_attention_kernel(const __grid_constant__ PrefillAttnArgs a) {
     }
   } else {
     setmaxnreg_dec<GE::kOtherRegs>();
-    uint32_t n_step[NT] = {};
+    uint32_t n_step = 0;
     const uint32_t leader = elect_one();
     for (int it = blockIdx.x; it < total; it += gridDim.x) {
       Item w = load_item(a, it, NT);
@@ -861,9 +859,9 @@ prefill_attention_kernel(const __grid_constant__ PrefillAttnArgs a) {
       if (w.nt > 0) {
         if (warp == GE::kSoftmaxWarps) {
           produce<D, NT>(a, sh, w, sq, n_kv, n_q);
-        } else if (warp == GE::kSoftmaxWarps + 1) {
+        } else if (warp <= GE::kSoftmaxWarps + NT) {
           tc_fence_after();
-          issue_mmas<D, NT>(a, sh, w, sq, tmem, leader, n_kv, n_q, n_step);
+          issue_mmas<D, NT>(a, sh, w, sq, tmem, leader, warp - GE::kSoftmaxWarps - 1, n_kv, n_q, n_step);
         }
         ++n_q;
       }
