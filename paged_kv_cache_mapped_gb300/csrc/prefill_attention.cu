@@ -16,10 +16,10 @@
 //    rules, keep the running maximum (moved only when exceeded by 2^8, and O rescaled then) and sum,
 //    and write P.  With two row tiles the softmax of one runs under the MMAs of the other.
 //  * prefill_merge_kernel joins the shares of split items by their maxima and sums.
-// P is rounded to bf16 for the product.  Rows over more than kTwoTermTiles key tiles take that one
-// term, and sum the rounded weights, so that the weights used still sum to one: the error beside a
-// bf16 output's own rounding is of the same size (2^-9 of each weight, independent from key to key).
-// Shorter rows, where few weights may carry the result, add the remainder as a second term.
+// P is rounded to bf16 for the product (the sum takes it in fp32).  Rows over more than kTwoTermTiles key
+// tiles take that one term: its error, at most 2^-8 of each weight and independent from key to key, is of the
+// size of a bf16 output's own rounding.  Shorter rows, where few weights may carry the result, add the
+// remainder as a second term, which costs half as many MMAs again.
 // Non-finite V: a masked key's weight is 0, and 0 * NaN is NaN, so V rows past the sequence are cleared,
 // and an output row that is not finite is computed again key by key over what it sees.
 // Every wait is bounded; bad block ids are cleared tiles, recorded.
@@ -458,13 +458,17 @@ __device__ __forceinline__ void issue_mmas(const PrefillAttnArgs& a, Shared<D, N
   }
   for (int t = 0; t < ns && ok; ++t) {
     const bool more = t + 2 < ns;  // a further S; its K tile arrives with its first step
-    if ((t & 1) == 0) ok = wait_kv(kv_base + t + 1) && (!more || wait_kv(kv_base + t + 2));
+    if ((t & 1) == 0) ok = wait_kv(kv_base + t + 1);
     const uint32_t c = step0 + (uint32_t)t;
     ok = ok && wait(&sh.p_full[y][c & 1u], c >> 1);
     if (!ok) break;
     tc_fence_after();
     pv(t);
-    if (more) qk(t + 2);
+    if (more) {
+      if ((t & 1) == 0) ok = wait_kv(kv_base + t + 2);
+      if (!ok) break;
+      qk(t + 2);
+    }
     if ((t & 1) || t + 1 == ns) free_tile(kv_base + (uint32_t)(t | 1));  // V of this tile
     // K of the tile two steps on: after its second step, or its first where that is the last
     if (more && ((t & 1) || t + 3 >= ns)) free_tile(kv_base + (uint32_t)((t + 2) & ~1));
@@ -476,15 +480,17 @@ __device__ __forceinline__ void issue_mmas(const PrefillAttnArgs& a, Shared<D, N
   n_step = step0 + ns;
 }
 
-// Largest of N values (of their sizes when ABS), in four chains.
+// Largest of N values (of their sizes when ABS), in four chains of three-operand maxima.
 template <bool ABS, int N>
 __device__ __forceinline__ float row_max(const float (&v)[N]) {
+  static_assert(N % 8 == 4 || N % 8 == 0, "pairs for four chains");
   float t[4];
 #pragma unroll
-  for (int c = 0; c < 4; ++c) t[c] = ABS ? fabsf(v[c]) : v[c];
+  for (int c = 0; c < 4; ++c) t[c] = fmax3(ABS ? fabsf(v[2 * c]) : v[2 * c], ABS ? fabsf(v[2 * c + 1]) : v[2 * c + 1], -INFINITY);
 #pragma unroll
-  for (int c = 4; c < N; ++c) t[c & 3] = fmaxf(t[c & 3], ABS ? fabsf(v[c]) : v[c]);
-  return fmaxf(fmaxf(t[0], t[1]), fmaxf(t[2], t[3]));
+  for (int c = 8; c < N; c += 2)
+    t[(c >> 1) & 3] = fmax3(t[(c >> 1) & 3], ABS ? fabsf(v[c]) : v[c], ABS ? fabsf(v[c + 1]) : v[c + 1]);
+  return fmaxf(fmax3(t[0], t[1], t[2]), t[3]);
 }
 
 // v = v * P(v^2 k^2) for the odd polynomial P of tanh (cap_logit): to u^5, or to u^9 with NINTH.
@@ -582,18 +588,24 @@ __device__ __forceinline__ void softmax_rows(const PrefillAttnArgs& a, Shared<D,
   const int pre = valid ? w.pre : 0;
   const bool two = w.nt_all <= kTwoTermTiles;
   const bool own_logits = a.cap_log2 > 0.f || a.slopes != nullptr || !(a.scale_log2 > 0.f);
-  const int i_min = w.pos0 + x * a.R, lo_max = sh.lo_max[x];
+  // steps whose keys all rows of the row tile see: a range of the interval's part of the list, and one of the
+  // prefix's.  The list's position of entry e is 16 (e + shift) there.
+  const int e_base = w.ts * kTileBlocks;
+  int full0 = (max(w.pre_units, ((sh.lo_max[x] + 15) >> 4) - w.shift) - e_base + kStepBlocks - 1) >> 2;
+  const int full1 = (((w.pos0 + x * a.R + 1) >> 4) - w.shift - e_base) >> 2;  // whole blocks up to the first row's position
+  full0 = max(full0, 0);
+  const int full_pre = ((w.pre >> 4) - e_base) >> 2;
+  static_assert(kStepBlocks == 4, "steps of four blocks");
   // the block that ends past the sequence: its V rows there are cleared, by the warps of each row tile before
   // they hand over the step's P (both write the same zeros)
   const int last_blk = (w.L - 1) >> 4;
   const int e_last = last_blk < w.pre_units ? last_blk : last_blk - w.shift;
-  const int tail_tile = (w.L & 15) != 0 && e_last >= 0 && e_last < w.nblk && w.block_of(e_last) == last_blk
-                            ? e_last / kTileBlocks - w.ts : -1;
+  const int tail_step = (w.L & 15) != 0 && e_last >= 0 && e_last < w.nblk && w.block_of(e_last) == last_blk
+                            ? (e_last - e_base) >> 2 : -1;
   const uint32_t t_lane = tmem + ((uint32_t)(r & ~31) << 16);
   const uint32_t to_addr = t_lane + NT * 2 * kStep + x * D;
   bool ok = true;
   float m = -INFINITY, l = 0.f;
-  bool tail_done = false;
   for (int j = 0; j < w.ns; ++j) {
     const uint32_t buf = n_step & 1u;
     const uint32_t ts_addr = t_lane + x * 2 * kStep + buf * kStep;
@@ -604,13 +616,10 @@ __device__ __forceinline__ void softmax_rows(const PrefillAttnArgs& a, Shared<D,
 #pragma unroll
     for (int c = 0; c < N / 32; ++c) tmem_ld_x32(ts_addr + 32 * c, *reinterpret_cast<float(*)[32]>(v + 32 * c));
     tmem_wait_ld();
-    const int e0 = w.ts * kTileBlocks + j * kStepBlocks;
+    const int e0 = e_base + j * kStepBlocks;
     Logits y{a.scale_log2, 0.f, 0.f};
     if (own_logits) y = apply_rules(a, v, slope2, i, w, e0);
-    // all these keys seen by all rows of the row tile?
-    const int t_first = w.block_of(e0) * 16;
-    const bool full = (e0 >= w.pre_units && t_first >= lo_max && t_first + N - 1 <= i_min) ||
-                      (e0 + N / 16 <= w.pre_units && t_first + N <= w.pre);
+    const bool full = (j >= full0 && j < full1) || j < full_pre;
     if (!full) {
 #pragma unroll
       for (int p = 0; p < N / 16; ++p) {
@@ -670,8 +679,9 @@ __device__ __forceinline__ void softmax_rows(const PrefillAttnArgs& a, Shared<D,
         for (int k = 0; k < 16; ++k) {
           const float off = fmaf(y.step, (float)(4 * c + k / 4), y.base);
           const float2 z = unpack2(ffma2(pack2(v[32 * c + 2 * k], v[32 * c + 2 * k + 1]), mul2, pack2(off, off)));
-          hi[k] = pack_bf16x2(ex2_approx(z.x), ex2_approx(z.y));
-          sum2[k & 3] = fadd2(sum2[k & 3], bf16x2_to_f32x2(hi[k]));
+          const float p0 = ex2_approx(z.x), p1 = ex2_approx(z.y);
+          hi[k] = pack_bf16x2(p0, p1);
+          sum2[k & 3] = fadd2(sum2[k & 3], pack2(p0, p1));
         }
         tmem_st_x16(ts_addr + 32 * c, hi);
       }
@@ -694,9 +704,7 @@ __device__ __forceinline__ void softmax_rows(const PrefillAttnArgs& a, Shared<D,
     }
     const float2 sum = unpack2(fadd2(fadd2(sum2[0], sum2[1]), fadd2(sum2[2], sum2[3])));
     l += sum.x + sum.y;
-    if ((j >> 1) == tail_tile && ((j & 1) || j + 1 == w.ns || (e_last % kTileBlocks) < kStepBlocks) &&
-        !tail_done) {
-      tail_done = true;
+    if (j == tail_step) {
       const uint32_t vtile = n_kv + 2 * (j >> 1) + 1;  // this tile's V in the count of K and V tiles
       ok = __all_sync(kFullMask, mbar_wait_spin(&sh.kv_full[vtile % NS], (vtile / NS) & 1u, a.timeout_ns));
       if (!ok) break;

@@ -468,6 +468,13 @@ __device__ __forceinline__ float cap_logit(float x, float cap2, float in) {
   return cap2 * (fabsf(u) < 0.3f ? poly : big);
 }
 
+// Largest of three (a NaN operand is passed over).
+__device__ __forceinline__ float fmax3(float a, float b, float c) {
+  float d;
+  asm("max.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
+  return d;
+}
+
 // 2^x by the hardware approximation (relative error ~2^-22, results below 2^-126 flushed to zero).
 __device__ __forceinline__ float ex2_approx(float x) {
   float y;
