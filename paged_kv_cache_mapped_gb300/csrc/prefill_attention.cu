@@ -261,6 +261,11 @@ struct Item {
   int ns;                 // steps of this share
 
   __device__ __forceinline__ int block_of(int e) const { return e < pre_units ? e : e + shift; }
+  // Key tiles run from the last one back, so that with a distance bias the nearest keys set the maximum.  Step t
+  // is half `half(t)` of the share's tile nt - 1 - order(t); the last tile may have its first half alone.
+  __device__ __forceinline__ int at(int t) const { return t + (ns & 1); }  // odd: the tile's last step
+  __device__ __forceinline__ int order(int t) const { return at(t) >> 1; }
+  __device__ __forceinline__ int half(int t) const { return t == 0 && (ns & 1) ? 0 : at(t) & 1; }
 };
 
 __device__ __forceinline__ Item load_item(const PrefillAttnArgs& a, int it, int NT) {
@@ -324,8 +329,8 @@ __device__ __forceinline__ void produce(const PrefillAttnArgs& a, Shared<D, NT>&
       for (int h = 0; h < H; ++h)
         tma_load_3d(sq + y * GE::kTile + h * kHalf, &a.tmap_q, h * 64, w.g * a.G, w.q0 + w.tok0 + y * a.R, &sh.q_full, pol_q);
   }
-  auto id_of = [&](int j) -> int {  // lane p < 8: the pool block of entry p of key tile j, -1: none
-    const int e = (w.ts + j) * kTileBlocks + lane;
+  auto id_of = [&](int j) -> int {  // lane p < 8: the pool block of entry p of the j-th key tile, -1: none
+    const int e = (w.ts + w.nt - 1 - j) * kTileBlocks + lane;
     int id = -1;
     if (lane < kTileBlocks && j < w.nt && e < w.nblk) {
       id = __ldg(a.block_tables + (size_t)w.b * a.MB + w.block_of(e));
@@ -418,26 +423,31 @@ __device__ __forceinline__ void issue_mmas(const PrefillAttnArgs& a, Shared<D, N
     }
     return;
   }
-  const int ns = (int)uniform((uint32_t)w.ns);
+  const int ns = (int)uniform((uint32_t)w.ns), odd = ns & 1;  // (Item::at and half, of uniform values)
   const bool two = uniform((uint32_t)w.nt_all) <= (uint32_t)kTwoTermTiles;
   const uint32_t step0 = uniform(n_step);
   const uint32_t s0 = uniform(tmem_any) + y * 2 * kStep, o = uniform(tmem_any) + NT * 2 * kStep + y * D;
   constexpr uint32_t kTile16 = GE::kTile / 16, kStep16 = kStep * 128 / 16;  // descriptors count 16 bytes
   const uint32_t qa = umma_lo_k(base) + y * kTile16, k0 = umma_lo_k(base + NT * GE::kTile);
   const uint32_t v0 = umma_lo_mn(base + NT * GE::kTile, kHalf);
+  // S of step t, with its tile's K awaited before the first step and freed after the last
   auto qk = [&](int t) {
-    const uint32_t buf = (step0 + (uint32_t)t) & 1u;
-    const uint32_t kb = k0 + ((kv_base + (uint32_t)(t & ~1)) % NS) * kTile16 + (t & 1) * kStep16;
+    const uint32_t buf = (step0 + (uint32_t)t) & 1u, u = (uint32_t)(t + odd), tile = kv_base + (u & ~1u);
+    if ((t == 0 || (u & 1u) == 0) && !wait_kv(tile)) return false;
+    if (t == 0) tc_fence_after();
+    const uint32_t kb = k0 + (tile % NS) * kTile16 + (t == 0 && odd ? 0 : (u & 1u) * kStep16);
 #pragma unroll
     for (int k = 0; k < D / 16; ++k) {
       const uint32_t off = (uint32_t)((k >> 2) * kHalf + (k & 3) * 32) / 16;
       umma_bf16_lo(leader, s0 + buf * kStep, qa + off, kb + off, id_qk, k > 0);
     }
     umma_commit_by(leader, bars + (uint32_t)offsetof(SH, s_full) + (y * 2 + buf) * 8);
+    if (u & 1u) free_tile(tile);
+    return true;
   };
   auto pv = [&](int t) {
-    const uint32_t buf = (step0 + (uint32_t)t) & 1u;
-    const uint32_t vb = v0 + ((kv_base + (uint32_t)(t | 1)) % NS) * kTile16 + (t & 1) * kStep16;
+    const uint32_t buf = (step0 + (uint32_t)t) & 1u, u = (uint32_t)(t + odd), tile = kv_base + (u | 1u);
+    const uint32_t vb = v0 + (tile % NS) * kTile16 + (t == 0 && odd ? 0 : (u & 1u) * kStep16);
     const uint32_t p = s0 + buf * kStep;
 #pragma unroll
     for (int k = 0; k < kStep / 16; ++k)  // 32 keys' first terms, then their remainders, 16 columns each
@@ -448,30 +458,17 @@ __device__ __forceinline__ void issue_mmas(const PrefillAttnArgs& a, Shared<D, N
         umma_bf16_ts_lo(leader, o, p + 32 * (k >> 1) + 16 + 8 * (k & 1), vb + k * 128, id_pv, true);
     }
     umma_commit_by(leader, bars + (uint32_t)offsetof(SH, pv_done) + (y * 2 + buf) * 8);
+    if (u & 1u) free_tile(tile);
   };
-  ok = wait(&sh.q_full, n_q) && wait_kv(kv_base);
-  if (ok) {
-    tc_fence_after();
-    qk(0);
-    if (ns > 1) qk(1);
-    free_tile(kv_base);  // the first K tile has no more steps
-  }
+  ok = wait(&sh.q_full, n_q) && qk(0) && (ns < 2 || qk(1));
   for (int t = 0; t < ns && ok; ++t) {
-    const bool more = t + 2 < ns;  // a further S; its K tile arrives with its first step
-    if ((t & 1) == 0) ok = wait_kv(kv_base + t + 1);
-    const uint32_t c = step0 + (uint32_t)t;
+    const uint32_t c = step0 + (uint32_t)t, u = (uint32_t)(t + odd);
+    ok = (t > 0 && (u & 1u)) || wait_kv(kv_base + (u | 1u));  // V of a tile's first step
     ok = ok && wait(&sh.p_full[y][c & 1u], c >> 1);
     if (!ok) break;
     tc_fence_after();
     pv(t);
-    if (more) {
-      if ((t & 1) == 0) ok = wait_kv(kv_base + t + 2);
-      if (!ok) break;
-      qk(t + 2);
-    }
-    if ((t & 1) || t + 1 == ns) free_tile(kv_base + (uint32_t)(t | 1));  // V of this tile
-    // K of the tile two steps on: after its second step, or its first where that is the last
-    if (more && ((t & 1) || t + 3 >= ns)) free_tile(kv_base + (uint32_t)((t + 2) & ~1));
+    if (t + 2 < ns) ok = qk(t + 2);
   }
   if (!ok) {  // the MMAs in flight end before tensor memory goes
     umma_commit_by(leader, bars + (uint32_t)offsetof(SH, drained) + y * 8);
@@ -574,6 +571,46 @@ __device__ __forceinline__ Logits apply_rules(const PrefillAttnArgs& a, float (&
   return x;
 }
 
+// One step's weights for a thread's 64 unmasked keys in one pass: p = 2^(logit - ref), written as bf16 pairs
+// over S, and their sum.  CAP: the logit is S P(S^2) with P = c0 + c1 S^2 + c2 S^4, tanh's polynomial to u^5
+// with the scales folded in; otherwise S c0.  BIAS: plus base + slope2 c for key c of the step.
+template <bool CAP, bool BIAS>
+__device__ __forceinline__ float step_weights(const float (&v)[kStep], uint32_t ts_addr, float c0, float c1, float c2,
+                                              float base, float slope2) {
+  const uint64_t k0 = pack2(c0, c0), k1 = pack2(c1, c1), k2 = pack2(c2, c2);
+  uint64_t near[4], sum[4];
+#pragma unroll
+  for (int k = 0; k < 4; ++k) {
+    near[k] = BIAS ? pack2(fmaf(slope2, (float)(2 * k), base), fmaf(slope2, (float)(2 * k + 1), base)) : pack2(base, base);
+    sum[k] = pack2(0.f, 0.f);
+  }
+#pragma unroll
+  for (int c = 0; c < kStep / 32; ++c) {
+    uint32_t hi[16];
+#pragma unroll
+    for (int k = 0; k < 16; ++k) {
+      const uint64_t x = pack2(v[32 * c + 2 * k], v[32 * c + 2 * k + 1]);
+      uint64_t b = near[k & 3];
+      if constexpr (BIAS) {
+        const float far = slope2 * (float)(32 * c + 8 * (k >> 2));
+        if (c > 0 || k >= 4) b = fadd2(b, pack2(far, far));
+      }
+      uint64_t f = k0;
+      if constexpr (CAP) {
+        const uint64_t q = fmul2(x, x);
+        f = ffma2(ffma2(k2, q, k1), q, k0);
+      }
+      const float2 z = unpack2(ffma2(x, f, b));
+      const float p0 = ex2_approx(z.x), p1 = ex2_approx(z.y);
+      hi[k] = pack_bf16x2(p0, p1);
+      sum[k & 3] = fadd2(sum[k & 3], pack2(p0, p1));
+    }
+    tmem_st_x16(ts_addr + 32 * c, hi);
+  }
+  const float2 t = unpack2(fadd2(fadd2(sum[0], sum[1]), fadd2(sum[2], sum[3])));
+  return t.x + t.y;
+}
+
 // The item's softmax and output for this thread's row r of row tile x: position i (-1: none), interval start
 // lo; prow and h name the output row.
 template <int D, int NT>
@@ -587,6 +624,9 @@ __device__ __forceinline__ void softmax_rows(const PrefillAttnArgs& a, Shared<D,
   const float slope2 = valid && a.slopes != nullptr ? __ldg(a.slopes + h) * kLog2e : 0.f;
   const int pre = valid ? w.pre : 0;
   const bool two = w.nt_all <= kTwoTermTiles;
+  // the cap as a polynomial of S (cap_logit's u = S ku): cap0 S + cap1 S^3 + cap2 S^5
+  const float ku = a.scale_log2 * a.cap_in * 0.34657359f, ku_size = a.cap_log2 > 0.f ? fabsf(ku) : 0.f;
+  const float cap0 = a.cap_log2 * ku, cap1 = -0.33333333f * cap0 * ku * ku, cap2 = 0.13333333f * cap0 * ku * ku * ku * ku;
   const bool own_logits = a.cap_log2 > 0.f || a.slopes != nullptr || !(a.scale_log2 > 0.f);
   // steps whose keys all rows of the row tile see: a range of the interval's part of the list, and one of the
   // prefix's.  The list's position of entry e is 16 (e + shift) there.
@@ -616,33 +656,52 @@ __device__ __forceinline__ void softmax_rows(const PrefillAttnArgs& a, Shared<D,
 #pragma unroll
     for (int c = 0; c < N / 32; ++c) tmem_ld_x32(ts_addr + 32 * c, *reinterpret_cast<float(*)[32]>(v + 32 * c));
     tmem_wait_ld();
-    const int e0 = e_base + j * kStepBlocks;
+    const int js = 2 * (w.nt - 1 - w.order(j)) + w.half(j);  // the step's place in the share's list
+    const int e0 = e_base + js * kStepBlocks;
+    const bool full = (js >= full0 && js < full1) || js < full_pre;
+    // Steps without a mask take one pass over the row.  With a cap or a bias, the products' largest size bounds
+    // the logits: the step's nearest key lies within twice that below the bound, so where that is 2^80 or less
+    // the bound serves as the maximum (the weights stay within fp32 and bf16 range), and the cap and the bias
+    // are part of the exponent's FMAs
+    bool fast = full && !two;
+    float mx = -INFINITY, base = 0.f;
     Logits y{a.scale_log2, 0.f, 0.f};
-    if (own_logits) y = apply_rules(a, v, slope2, i, w, e0);
-    const bool full = (j >= full0 && j < full1) || j < full_pre;
-    if (!full) {
-#pragma unroll
-      for (int p = 0; p < N / 16; ++p) {
-        const int t0 = w.block_of(e0 + p) * 16;
-        const int hi_c = i - t0, lo_c = lo - t0, pre_c = pre - t0;
-        uint32_t see = hi_c >= 15 ? 0xffffu : hi_c < 0 ? 0u : (2u << hi_c) - 1u;
-        see &= lo_c <= 0 ? 0xffffu : lo_c > 15 ? 0u : 0xffffu << lo_c;
-        see |= pre_c >= 16 ? 0xffffu : pre_c <= 0 ? 0u : (1u << pre_c) - 1u;
-#pragma unroll
-        for (int c = 0; c < 16; ++c) v[16 * p + c] = ((see >> c) & 1u) ? v[16 * p + c] : -INFINITY;
+    if (fast && !own_logits) {
+      mx = row_max<false>(v) * a.scale_log2;
+    } else if (fast) {
+      const float far = row_max<true>(v);
+      const float size = far * fabsf(a.scale_log2);
+      mx = size;
+      if (slope2 != 0.f) {
+        base = -slope2 * (float)(i - w.block_of(e0) * 16);
+        mx += fmaxf(base, fmaf(slope2, (float)(kStep - 1), base));
       }
+      fast = __all_sync(kFullMask, 2.f * size <= 80.f && far * ku_size < 0.11f && (slope2 == 0.f || js >= full_pre));
     }
-    float mx;
-    if (y.step == 0.f) {
-      mx = fmaf(row_max<false>(v), y.mul, y.base);
-    } else {
-      mx = -INFINITY;
+    if (!fast) {
+      if (own_logits) y = apply_rules(a, v, slope2, i, w, e0);
+      if (!full) {
 #pragma unroll
-      for (int g = 0; g < N / 8; ++g) {
-        float t = v[8 * g];
+        for (int p = 0; p < N / 16; ++p) {
+          const int t0 = w.block_of(e0 + p) * 16;
+          const int hi_c = i - t0, lo_c = lo - t0, pre_c = pre - t0;
+          uint32_t see = hi_c >= 15 ? 0xffffu : hi_c < 0 ? 0u : (2u << hi_c) - 1u;
+          see &= lo_c <= 0 ? 0xffffu : lo_c > 15 ? 0u : 0xffffu << lo_c;
+          see |= pre_c >= 16 ? 0xffffu : pre_c <= 0 ? 0u : (1u << pre_c) - 1u;
 #pragma unroll
-        for (int c = 1; c < 8; ++c) t = fmaxf(t, v[8 * g + c]);
-        mx = fmaxf(mx, t + fmaf(y.step, (float)g, y.base));
+          for (int c = 0; c < 16; ++c) v[16 * p + c] = ((see >> c) & 1u) ? v[16 * p + c] : -INFINITY;
+        }
+      }
+      if (y.step == 0.f) {
+        mx = fmaf(row_max<false>(v), y.mul, y.base);
+      } else {
+        mx = -INFINITY;
+#pragma unroll
+        for (int g = 0; g < N / 8; ++g) {
+          const float* t = v + 8 * g;
+          const float top = fmax3(fmax3(t[0], t[1], t[2]), fmax3(t[3], t[4], t[5]), fmaxf(t[6], t[7]));
+          mx = fmaxf(mx, top + fmaf(y.step, (float)g, y.base));
+        }
       }
     }
     const bool move = mx > m + kSlack;
@@ -666,46 +725,58 @@ __device__ __forceinline__ void softmax_rows(const PrefillAttnArgs& a, Shared<D,
         }
       }
     }
-    y.base -= m == -INFINITY ? 0.f : m;
-    const uint64_t mul2 = pack2(y.mul, y.mul);
-    uint64_t sum2[4];
-#pragma unroll
-    for (int k = 0; k < 4; ++k) sum2[k] = pack2(0.f, 0.f);
-    if (!two) {
-#pragma unroll
-      for (int c = 0; c < N / 32; ++c) {
-        uint32_t hi[16];
-#pragma unroll
-        for (int k = 0; k < 16; ++k) {
-          const float off = fmaf(y.step, (float)(4 * c + k / 4), y.base);
-          const float2 z = unpack2(ffma2(pack2(v[32 * c + 2 * k], v[32 * c + 2 * k + 1]), mul2, pack2(off, off)));
-          const float p0 = ex2_approx(z.x), p1 = ex2_approx(z.y);
-          hi[k] = pack_bf16x2(p0, p1);
-          sum2[k & 3] = fadd2(sum2[k & 3], pack2(p0, p1));
-        }
-        tmem_st_x16(ts_addr + 32 * c, hi);
+    const float ref = m == -INFINITY ? 0.f : m;
+    if (fast) {
+      base -= ref;
+      if (a.slopes == nullptr) {
+        l += a.cap_log2 > 0.f ? step_weights<true, false>(v, ts_addr, cap0, cap1, cap2, base, 0.f)
+                              : step_weights<false, false>(v, ts_addr, a.scale_log2, 0.f, 0.f, base, 0.f);
+      } else {
+        l += a.cap_log2 > 0.f ? step_weights<true, true>(v, ts_addr, cap0, cap1, cap2, base, slope2)
+                              : step_weights<false, true>(v, ts_addr, a.scale_log2, 0.f, 0.f, base, slope2);
       }
     } else {
+      y.base -= ref;
+      const uint64_t mul2 = pack2(y.mul, y.mul);
+      uint64_t sum2[4];
 #pragma unroll
-      for (int c = 0; c < N / 32; ++c) {
-        uint32_t hi[16], rest[16];
+      for (int k = 0; k < 4; ++k) sum2[k] = pack2(0.f, 0.f);
+      if (!two) {
 #pragma unroll
-        for (int k = 0; k < 16; ++k) {
-          const float off = fmaf(y.step, (float)(4 * c + k / 4), y.base);
-          const float2 z = unpack2(ffma2(pack2(v[32 * c + 2 * k], v[32 * c + 2 * k + 1]), mul2, pack2(off, off)));
-          const float p0 = ex2_approx(z.x), p1 = ex2_approx(z.y);
-          hi[k] = pack_bf16x2(p0, p1);
-          rest[k] = pack_bf16x2(p0 - bf16_lo_to_f32(hi[k]), p1 - bf16_hi_to_f32(hi[k]));
-          sum2[k & 3] = fadd2(sum2[k & 3], pack2(p0, p1));
+        for (int c = 0; c < N / 32; ++c) {
+          uint32_t hi[16];
+#pragma unroll
+          for (int k = 0; k < 16; ++k) {
+            const float off = fmaf(y.step, (float)(4 * c + k / 4), y.base);
+            const float2 z = unpack2(ffma2(pack2(v[32 * c + 2 * k], v[32 * c + 2 * k + 1]), mul2, pack2(off, off)));
+            const float p0 = ex2_approx(z.x), p1 = ex2_approx(z.y);
+            hi[k] = pack_bf16x2(p0, p1);
+            sum2[k & 3] = fadd2(sum2[k & 3], pack2(p0, p1));
+          }
+          tmem_st_x16(ts_addr + 32 * c, hi);
         }
-        tmem_st_x16(ts_addr + 32 * c, hi);
-        tmem_st_x16(ts_addr + 32 * c + 16, rest);
+      } else {
+#pragma unroll
+        for (int c = 0; c < N / 32; ++c) {
+          uint32_t hi[16], rest[16];
+#pragma unroll
+          for (int k = 0; k < 16; ++k) {
+            const float off = fmaf(y.step, (float)(4 * c + k / 4), y.base);
+            const float2 z = unpack2(ffma2(pack2(v[32 * c + 2 * k], v[32 * c + 2 * k + 1]), mul2, pack2(off, off)));
+            const float p0 = ex2_approx(z.x), p1 = ex2_approx(z.y);
+            hi[k] = pack_bf16x2(p0, p1);
+            rest[k] = pack_bf16x2(p0 - bf16_lo_to_f32(hi[k]), p1 - bf16_hi_to_f32(hi[k]));
+            sum2[k & 3] = fadd2(sum2[k & 3], pack2(p0, p1));
+          }
+          tmem_st_x16(ts_addr + 32 * c, hi);
+          tmem_st_x16(ts_addr + 32 * c + 16, rest);
+        }
       }
+      const float2 sum = unpack2(fadd2(fadd2(sum2[0], sum2[1]), fadd2(sum2[2], sum2[3])));
+      l += sum.x + sum.y;
     }
-    const float2 sum = unpack2(fadd2(fadd2(sum2[0], sum2[1]), fadd2(sum2[2], sum2[3])));
-    l += sum.x + sum.y;
-    if (j == tail_step) {
-      const uint32_t vtile = n_kv + 2 * (j >> 1) + 1;  // this tile's V in the count of K and V tiles
+    if (js == tail_step) {
+      const uint32_t vtile = n_kv + 2 * w.order(j) + 1;  // this tile's V in the count of K and V tiles
       ok = __all_sync(kFullMask, mbar_wait_spin(&sh.kv_full[vtile % NS], (vtile / NS) & 1u, a.timeout_ns));
       if (!ok) break;
       unsigned char* rows = skv + (vtile % NS) * GE::kTile + (e_last % kTileBlocks) * 2048;
