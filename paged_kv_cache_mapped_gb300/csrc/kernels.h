@@ -306,12 +306,12 @@ struct PrefillAttnArgs {
   int B, T, Hq, Hkv, NB, MB, G, window;
   int R;                         // tokens of a 128-row tile (128 / G)
   int sms, slots;                // SMs; CTAs resident at a time
-  int* plan_total;               // the plan: items in the list
-  int4* plan_items;              // (sequence, row tile group, share, shares)
-  int2* plan_seq;                // per sequence: shares, first partial row
+  int* plan_head;                // the plan: items in the list, ticket counter
+  int4* plan_items;              // (sequence, row tile group, share | shares << 16, first partial row)
+  int2* plan_tiles;              // per row tile group: shares, first partial row
+  int* plan_seq;                 // per sequence: its first row tile group
   float2* part_ml;               // partial rows: (running max in base 2, running sum)
   float* part_o;                 // partial rows, unnormalised [.., D]
-  int max_items, max_rows;
   unsigned long long timeout_ns; // bound of every mbarrier wait
 };
 size_t prefill_attention_workspace(int B, int T, int Hq, int G, int D);

@@ -57,6 +57,17 @@ __device__ __forceinline__ PrefillSeq prefill_seq(const PrefillAttnArgs& a, int 
   return s;
 }
 
+// The largest i < n with start[i] <= x (start ascending, start[0] <= x; of equal starts the last one has the
+// items).
+__device__ __forceinline__ int owner_of(const int* start, int n, int x) {
+  int lo = 0, hi = n;
+  while (hi - lo > 1) {
+    const int mid = (lo + hi) >> 1;
+    if (start[mid] <= x) lo = mid; else hi = mid;
+  }
+  return lo;
+}
+
 // First key of the interval that packed row r at position i sees (i + 1: none).
 __device__ __forceinline__ int interval_start(const PrefillAttnArgs& a, int r, int i) {
   int lo = a.window > 0 && i >= a.window ? i - a.window + 1 : 0;
@@ -93,17 +104,54 @@ struct Geo {
 
 // ------------------------------------------------------------------------------------ the plan
 //
-// Sequence b has ntile_b = ceil(n_b / (NT R)) row tile groups of R = 128 / G tokens a tile, and at most
-// kt_b key tiles each.  The work of all, over twice the resident CTAs, is what an item may hold at most
-// (and kMinChunk at least); longer ones are split.  Items are listed longest rows first within a
-// sequence.
-__global__ void __launch_bounds__(1024) prefill_plan_kernel(const PrefillAttnArgs a, int tokens_per_item) {
-  __shared__ long long s_sum[33];
-  __shared__ long long s_carry[2];
-  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+// Sequence b has ceil(n_b / (NT R)) row tile groups ("entries") of R = 128 / G tokens a tile; entry e has kt_e key
+// tiles (an upper bound where documents hide some), and Hkv items of it make P = entries * Hkv.  `slots` CTAs
+// run at a time.
+//  * P < slots: every entry is cut into shares of at most c key tiles, c chosen among ktmax / s, s = 1, 2, ..., for
+//    the least of max(c, ..) estimates of the end: c where all shares run at once, else the smaller of
+//    W / slots + c (any list schedule) and the rounds times c.
+//  * P >= slots: entries above one and a half times the fair share W / slots are cut to that.  If there are none, the last P mod slots
+//    items, which would leave most CTAs idle for a whole item, are cut in s shares each (chunk of 4096 on 16384,
+//    512 items on 152 CTAs: 56 items in two shares, 0.99 -> @@ ms capped).
+// The shares of split entries number at most 2 slots, which bounds the partial rows.  The list has the entries
+// with more than half of ktmax first, a sequence's last rows first within either part.
+struct Entry {
+  int b, tile, ntile, tokens, n, kt;
+};
+
+__device__ __forceinline__ Entry plan_entry(const PrefillAttnArgs& a, const int* base, int e, int per_item) {
+  Entry x;
+  x.b = owner_of(base, a.B, e);
+  const PrefillSeq s = prefill_seq(a, x.b);
+  x.n = s.n;
+  x.ntile = base[x.b + 1] - base[x.b];
+  x.tile = x.ntile - 1 - (e - base[x.b]);
+  x.tokens = min(s.n - x.tile * per_item, per_item);
+  const int i0 = s.L - s.n + x.tile * per_item, i1 = i0 + x.tokens - 1;
+  const int lo = a.window > 0 && i0 >= a.window ? i0 - a.window + 1 : 0;
+  const int pre_units = (s.pre + 15) >> 4;
+  const int nblk = pre_units + max((i1 >> 4) - max(lo >> 4, pre_units) + 1, 0);
+  x.kt = (nblk + kTileBlocks - 1) / kTileBlocks;
+  return x;
+}
+
+constexpr int kPlanEntries = 512;  // entries kept in shared memory: the most that the first rule meets
+
+__global__ void __launch_bounds__(1024) prefill_plan_kernel(const PrefillAttnArgs a, int per_item) {
+  extern __shared__ int s_base[];  // [B + 1] first entry of each sequence
+  __shared__ long long s_sum[34];
+  __shared__ int s_kt[kPlanEntries];
+  __shared__ int s_max;
+  __shared__ unsigned long long s_best;
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, warps = blockDim.x >> 5;
+  if (tid == 0) {
+    s_max = 0;
+    s_best = ~0ull;
+    s_base[0] = 0;
+  }
   grid_dependency_wait();
   grid_launch_dependents();
-  // exclusive block sum; the total in s_sum[32]
+  // exclusive block sum of v; the total in s_sum[32]
   auto scan = [&](long long v) -> long long {
     long long x = v;
 #pragma unroll
@@ -111,10 +159,11 @@ __global__ void __launch_bounds__(1024) prefill_plan_kernel(const PrefillAttnArg
       const long long t = __shfl_up_sync(kFullMask, x, o);
       if (lane >= o) x += t;
     }
+    __syncthreads();  // the sums of the scan before have been read
     if (lane == 31) s_sum[warp] = x;
     __syncthreads();
     if (warp == 0) {
-      const long long own = lane < (int)(blockDim.x >> 5) ? s_sum[lane] : 0;
+      const long long own = lane < warps ? s_sum[lane] : 0;
       long long y = own;
 #pragma unroll
       for (int o = 1; o < 32; o <<= 1) {
@@ -128,65 +177,102 @@ __global__ void __launch_bounds__(1024) prefill_plan_kernel(const PrefillAttnArg
     __syncthreads();
     return s_sum[warp] + x - v;
   };
-  auto shape = [&](int b, int& n, int& ntile, int& kt) {
-    const PrefillSeq s = prefill_seq(a, b);
-    n = s.n;
-    ntile = (s.n + tokens_per_item - 1) / tokens_per_item;
-    const int span = a.window > 0 ? (int)min((long long)s.L, (long long)a.window + tokens_per_item) : s.L;
-    const int blocks = min((s.L + 15) >> 4, (span >> 4) + 2 + ((s.pre + 15) >> 4));
-    kt = (blocks + kTileBlocks - 1) / kTileBlocks;
-    return s.err;
-  };
-  long long work = 0;
+  int carry = 0;
   for (int base = 0; base < a.B; base += blockDim.x) {
-    int n = 0, ntile = 0, kt = 0;
+    int ntile = 0;
     if (base + tid < a.B) {
-      const int err = shape(base + tid, n, ntile, kt);
-      if (err != 0) record_error(a.err, err);
+      const PrefillSeq s = prefill_seq(a, base + tid);
+      if (s.err != 0) record_error(a.err, s.err);
+      ntile = (s.n + per_item - 1) / per_item;
     }
-    (void)scan((long long)ntile * kt * a.Hkv);
-    work += s_sum[32];
-    __syncthreads();
+    const int at = carry + (int)scan(ntile);
+    if (base + tid < a.B) s_base[base + tid + 1] = at + ntile;
+    carry += (int)s_sum[32];
   }
-  long long chunk = max((long long)kMinChunk, (work + 2 * a.slots - 1) / (2 * a.slots));
-  for (;; chunk *= 2) {  // ends: with chunk above every kt_b nothing is split
-    if (tid < 2) s_carry[tid] = 0;
+  __syncthreads();
+  const int entries = carry;
+  long long work = 0;
+  int most = 0;
+  for (int e = tid; e < entries; e += blockDim.x) {
+    const int kt = plan_entry(a, s_base, e, per_item).kt;
+    if (e < kPlanEntries) s_kt[e] = kt;
+    work += kt;
+    most = max(most, kt);
+  }
+  most = __reduce_max_sync(kFullMask, most);
+  if (lane == 0) atomicMax(&s_max, most);
+  (void)scan(work);
+  const long long W = s_sum[32] * a.Hkv, P = (long long)entries * a.Hkv;
+  const int ktmax = max(s_max, 1);
+  int chunk, tail = entries, tail_split = 1;
+  if (P < a.slots && entries <= kPlanEntries) {
+    const int smax = P > 0 ? (int)min(64ll, 2 * a.slots / P) : 1;
+    for (int sp = warp + 1; sp <= smax; sp += warps) {
+      const int c = max(kMinChunk, (ktmax + sp - 1) / sp);
+      int shares = 0;
+      for (int e = lane; e < entries; e += 32) shares += max(1, (s_kt[e] + c - 1) / c);
+      shares = __reduce_add_sync(kFullMask, shares);
+      const long long items = (long long)shares * a.Hkv;
+      long long end = c;
+      if (items > a.slots) end = min(W / a.slots + c, (items + a.slots - 1) / a.slots * c);
+      const unsigned long long cost = (unsigned long long)(end * 64 + (c < ktmax ? 32 : 0) + sp);
+      if (lane == 0) atomicMin(&s_best, cost << 32 | (unsigned)c);
+    }
     __syncthreads();
-    for (int base = 0; base < a.B; base += blockDim.x) {
-      int n = 0, ntile = 0, kt = 0, nsplit = 1;
-      const int b = base + tid;
-      if (b < a.B) {
-        (void)shape(b, n, ntile, kt);
-        nsplit = (int)max(1ll, (kt + chunk - 1) / chunk);
+    chunk = (int)(unsigned)(s_best & 0xffffffffull);
+  } else {
+    chunk = (int)max((long long)kMinChunk, (W + W / 2) / a.slots);
+    if (ktmax <= chunk) {
+      const int t = (int)(P % a.slots) / a.Hkv * a.Hkv;  // whole entries
+      float best = 2.f;
+      for (int sp = 1; sp <= 8 && t > 0 && (long long)t * sp <= 2 * a.slots; ++sp) {
+        const float end = (float)((t * sp + a.slots - 1) / a.slots) / (float)sp + 0.03f * (float)sp;
+        if (end < best) {
+          best = end;
+          tail_split = sp;
+        }
       }
-      const long long item0 = s_carry[0] + scan((long long)ntile * nsplit);
-      const long long items = s_sum[32];
-      __syncthreads();
-      const long long row0 = s_carry[1] + scan(nsplit > 1 ? (long long)n * a.Hq * nsplit : 0);
-      const long long rows = s_sum[32];
-      __syncthreads();
-      if (b < a.B) {
-        const bool fits = item0 + (long long)ntile * nsplit <= a.max_items;
-        a.plan_seq[b] = make_int2(nsplit, (int)min(row0, (long long)a.max_rows));
-        for (int k = 0; fits && k < ntile * nsplit; ++k)
-          a.plan_items[item0 + k] = make_int4(b, ntile - 1 - k / nsplit, k % nsplit, nsplit);
-      }
-      if (tid == 0) {
-        s_carry[0] += items;
-        s_carry[1] += rows;
-      }
-      __syncthreads();
+      if (tail_split > 1) tail = entries - t / a.Hkv;
     }
-    const long long items = s_carry[0], rows = s_carry[1];
-    __syncthreads();
-    if (rows <= a.max_rows && items <= a.max_items) {
-      if (tid == 0) *a.plan_total = (int)items;
-      return;
+  }
+  auto shares_of = [&](int e, int kt) {
+    if (e >= tail) return min(tail_split, max(1, kt / kMinChunk));
+    return max(1, (kt + chunk - 1) / chunk);
+  };
+  // places in the list: the long entries' shares, then the others'; partial rows of the split ones
+  long long first = 0;
+  for (int e = tid; e < entries; e += blockDim.x) {
+    const int kt = e < kPlanEntries ? s_kt[e] : plan_entry(a, s_base, e, per_item).kt;
+    if (2 * kt > ktmax) first += shares_of(e, kt);
+  }
+  (void)scan(first);
+  long long at[2] = {0, s_sum[32]};
+  long long row = 0;
+  for (int base = 0; base < entries; base += blockDim.x) {
+    const int e = base + tid;
+    Entry x{};
+    int shares = 0, part = 1;
+    if (e < entries) {
+      x = plan_entry(a, s_base, e, per_item);
+      shares = shares_of(e, x.kt);
+      part = 2 * x.kt > ktmax ? 0 : 1;
     }
-    if (chunk > (1ll << 31)) {  // cannot be: unsplit items are within max_items
-      if (tid == 0) *a.plan_total = 0;
-      return;
+    const long long both = scan(part == 0 ? (long long)shares << 32 : shares);
+    const long long both_all = s_sum[32];
+    const long long row0 = row + scan(shares > 1 ? (long long)x.tokens * a.Hq * shares : 0);
+    row += s_sum[32];
+    if (e < entries) {
+      const long long item0 = at[part] + (part == 0 ? both >> 32 : both & 0xffffffffll);
+      a.plan_tiles[s_base[x.b] + x.tile] = make_int2(shares, (int)row0);
+      for (int k = 0; k < shares; ++k) a.plan_items[item0 + k] = make_int4(x.b, x.tile, k | shares << 16, (int)row0);
     }
+    at[0] += both_all >> 32;
+    at[1] += both_all & 0xffffffffll;
+  }
+  for (int b = tid; b < a.B; b += blockDim.x) a.plan_seq[b] = s_base[b];
+  if (tid == 0) {
+    a.plan_head[0] = (int)at[1];  // items
+    a.plan_head[1] = 0;           // the ticket counter
   }
 }
 
@@ -253,7 +339,7 @@ __device__ __noinline__ void exact_row(const PrefillAttnArgs& a, const Row& w, l
 // One work item for one kv head, and the key list of its rows: the blocks of the prefix, then those of
 // the union of the rows' intervals, in tiles of 8.
 struct Item {
-  int b, g, split, nsplit;
+  int b, g, split, nsplit, part;  // part: first partial row of the entry
   int q0, n, L, pre;      // of the sequence
   int tok0, tokens, nx;   // first token (of the sequence's queries), tokens, row tiles
   int pos0;               // position of the first token
@@ -275,8 +361,9 @@ __device__ __forceinline__ Item load_item(const PrefillAttnArgs& a, int it, int 
   const PrefillSeq s = prefill_seq(a, p.x);
   w.b = p.x;
   w.g = it - at * a.Hkv;
-  w.split = p.z;
-  w.nsplit = p.w;
+  w.split = p.z & 0xffff;
+  w.nsplit = p.z >> 16;
+  w.part = p.w;
   w.q0 = s.q0;
   w.n = s.n;
   w.L = s.L;
@@ -308,7 +395,7 @@ struct Shared {
   uint64_t s_full[NT][2], p_full[NT][2], pv_done[NT][2];  // by buffer: S ready, P ready, P V added
   uint64_t drained[NT];  // after a timeout: the MMAs issued have ended
   uint32_t tmem;
-  int lo_min, lo_max[NT], abort;
+  int lo_min, lo_max[NT], abort, next;
 };
 
 // Loads the item's Q tiles and its K and V tiles through the ring (one warp).  n_kv counts K and V tiles
@@ -805,7 +892,8 @@ __device__ __forceinline__ void softmax_rows(const PrefillAttnArgs& a, Shared<D,
   }
   // ---- the rows out: bf16, or this share's unnormalised row with its maximum and sum
   const bool split = w.nsplit > 1;
-  const long long part = split ? (long long)a.plan_seq[w.b].y + ((long long)w.split * w.n + (prow - w.q0)) * a.Hq + h : 0;
+  const long long part =
+      split ? (long long)w.part + ((long long)w.split * w.tokens + (prow - w.q0 - w.tok0)) * a.Hq + h : 0;
   const float f = split ? 1.f : (l > 0.f ? 1.f / l : 0.f);
   bool bad = !(l <= 3.4028234e38f);
 #pragma unroll
@@ -890,7 +978,7 @@ prefill_attention_kernel(const __grid_constant__ PrefillAttnArgs a) {
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = sh.tmem;
-  const int total = *a.plan_total * a.Hkv;
+  const int total = a.plan_head[0] * a.Hkv;
   // Each role has the whole item loop, so that its registers are its own.  Three block barriers an item:
   // the shared minimum is reset, it is complete, every role has left the item.
   uint32_t n_kv = 0, n_q = 0;  // K and V tiles, and items with tiles, since the kernel's start (barrier phases)
@@ -900,7 +988,7 @@ prefill_attention_kernel(const __grid_constant__ PrefillAttnArgs a) {
     const int x = warp >> 2, r = 32 * (warp & 3) + lane;
     const int tok = r / a.G, head = r - tok * a.G;
     uint32_t n_step = 0;
-    for (int it = blockIdx.x; it < total; it += gridDim.x) {
+    for (int it = blockIdx.x; it < total; it = sh.next) {
       Item w = load_item(a, it, NT);
       if (threadIdx.x == 0) {
         sh.lo_min = 0x7fffffff;
@@ -930,7 +1018,7 @@ prefill_attention_kernel(const __grid_constant__ PrefillAttnArgs a) {
     setmaxnreg_dec<GE::kOtherRegs>();
     uint32_t n_step = 0;
     const uint32_t leader = elect_one();
-    for (int it = blockIdx.x; it < total; it += gridDim.x) {
+    for (int it = blockIdx.x; it < total; it = sh.next) {
       Item w = load_item(a, it, NT);
       __syncthreads();
       __syncthreads();
@@ -944,6 +1032,8 @@ prefill_attention_kernel(const __grid_constant__ PrefillAttnArgs a) {
         }
         ++n_q;
       }
+      // an idle warp takes the next item's ticket meanwhile
+      if (warp == GE::kSoftmaxWarps + 1 + NT && lane == 0) sh.next = (int)gridDim.x + atomicAdd(a.plan_head + 1, 1);
       __syncwarp();
       __syncthreads();
       if (sh.abort != 0) break;
@@ -957,7 +1047,7 @@ prefill_attention_kernel(const __grid_constant__ PrefillAttnArgs a) {
 // ------------------------------------------------------------------------------------ the merge
 
 template <int D>
-__global__ void __launch_bounds__(256) prefill_merge_kernel(const PrefillAttnArgs a) {
+__global__ void __launch_bounds__(256) prefill_merge_kernel(const PrefillAttnArgs a, int per_item) {
   constexpr int E = D / 32;
   const int lane = threadIdx.x & 31;
   grid_dependency_wait();
@@ -966,17 +1056,14 @@ __global__ void __launch_bounds__(256) prefill_merge_kernel(const PrefillAttnArg
   for (long long row = ((long long)blockIdx.x * blockDim.x + threadIdx.x) >> 5; row < rows;
        row += ((long long)gridDim.x * blockDim.x) >> 5) {
     const int r = (int)(row / a.Hq);
-    int lo = 0, hi = a.B;
-    while (hi - lo > 1) {
-      const int mid = (lo + hi) >> 1;
-      if (a.query_starts[mid] <= r) lo = mid; else hi = mid;
-    }
-    const int2 plan = a.plan_seq[lo];
-    if (plan.x <= 1) continue;
-    const PrefillSeq s = prefill_seq(a, lo);
+    const int b = owner_of(a.query_starts, a.B, r);
+    const PrefillSeq s = prefill_seq(a, b);
     if (r < s.q0 || r >= s.q0 + s.n) continue;
-    const long long per = (long long)s.n * a.Hq;
-    const long long p0 = plan.y + (long long)(r - s.q0) * a.Hq + (row - (long long)r * a.Hq);
+    const int tile = (r - s.q0) / per_item;
+    const int2 plan = a.plan_tiles[a.plan_seq[b] + tile];
+    if (plan.x <= 1) continue;
+    const long long per = (long long)min(s.n - tile * per_item, per_item) * a.Hq;
+    const long long p0 = plan.y + (long long)(r - s.q0 - tile * per_item) * a.Hq + (row - (long long)r * a.Hq);
     float m = -INFINITY;
     for (int k = 0; k < plan.x; ++k) m = fmaxf(m, a.part_ml[p0 + k * per].x);
     float l = 0.f, o[E] = {};
@@ -999,28 +1086,26 @@ __global__ void __launch_bounds__(256) prefill_merge_kernel(const PrefillAttnArg
 }  // namespace
 
 namespace {
-constexpr long long kMaxPartRows = 80000;  // split rows of one call at most (40 MB of partial rows at d = 128)
-constexpr int kMaxSlots = 512;             // resident CTAs that a plan may count on
-
+constexpr int kMaxSms = 160;                             // CTAs a plan counts on: at most kCtas on each of these
+constexpr long long kMaxPartRows = 2ll * kMaxSms * 256;  // rows of 2 slots shares (43 MB of partial rows at d = 128)
 size_t align256p(size_t x) { return (x + 255) & ~size_t(255); }
 
 struct PrefillWorkspace {
-  size_t items, seq, ml, o, total;
-  long long max_items, max_rows;
+  size_t items, tiles, seq, ml, o, total;
 };
 
-// total | int4 items | int2 per sequence | float2 (m, l) | float o.  Items: one per row tile group of one
-// tile (the most that any variant lists) and the shares of split ones.
+// head | int4 items | int2 per entry | int per sequence | float2 (m, l) | float o.  Entries: at most one per 128
+// rows, and one more per sequence; items: those and the shares of split ones.
 PrefillWorkspace plan_prefill(long long B, long long T, int Hq, int G, int D) {
   PrefillWorkspace w{};
-  const int R = 128 / G;
-  w.max_items = T / R + B + 4 * kMaxSlots;
-  w.max_rows = std::min(kMaxPartRows, T * Hq * 64);
+  const long long entries = T / (128 / G) + B;
+  const long long rows = std::min(kMaxPartRows, T * Hq * 64);  // an entry has at most 64 shares
   w.items = 256;
-  w.seq = align256p(w.items + sizeof(int4) * (size_t)w.max_items);
-  w.ml = align256p(w.seq + sizeof(int2) * (size_t)B);
-  w.o = align256p(w.ml + sizeof(float2) * (size_t)w.max_rows);
-  w.total = align256p(w.o + sizeof(float) * (size_t)w.max_rows * D);
+  w.tiles = align256p(w.items + sizeof(int4) * (size_t)(entries + 4 * kMaxSms));
+  w.seq = align256p(w.tiles + sizeof(int2) * (size_t)entries);
+  w.ml = align256p(w.seq + sizeof(int) * (size_t)B);
+  w.o = align256p(w.ml + sizeof(float2) * (size_t)rows);
+  w.total = align256p(w.o + sizeof(float) * (size_t)rows * D);
   return w;
 }
 
@@ -1028,10 +1113,11 @@ template <int D, int NT>
 cudaError_t launch_attention(const PrefillAttnArgs& a, cudaStream_t stream) {
   using GE = Geo<D, NT>;
   PrefillAttnArgs args = a;
-  args.slots = std::min(a.sms * GE::kCtas, kMaxSlots);
+  args.slots = std::min(a.sms, kMaxSms) * GE::kCtas;
   int per_item = NT * a.R;
   void* plan_params[] = {&args, &per_item};
-  cudaError_t e = launch_pdl((const void*)prefill_plan_kernel, dim3(1), dim3(a.B > 256 ? 1024 : 256), 0, stream, plan_params);
+  cudaError_t e = launch_pdl((const void*)prefill_plan_kernel, dim3(1),
+                             dim3(a.B > 256 || a.T > 16384 ? 1024 : 256), sizeof(int) * ((size_t)a.B + 1), stream, plan_params);
   if (e != cudaSuccess) return e;
   void* params[] = {&args};
   const long long most = ((long long)a.T / per_item + a.B) * a.Hkv + 2 * args.slots;
@@ -1039,7 +1125,7 @@ cudaError_t launch_attention(const PrefillAttnArgs& a, cudaStream_t stream) {
                  dim3(GE::kThreads), GE::kSmem, stream, params);
   if (e != cudaSuccess) return e;
   const long long warps = std::min((long long)a.T * a.Hq, 8ll * 8 * a.sms);
-  return launch_pdl((const void*)prefill_merge_kernel<D>, dim3((unsigned)((warps + 7) / 8)), dim3(256), 0, stream, params);
+  return launch_pdl((const void*)prefill_merge_kernel<D>, dim3((unsigned)((warps + 7) / 8)), dim3(256), 0, stream, plan_params);
 }
 
 template <int D, int NT>
@@ -1063,13 +1149,12 @@ cudaError_t launch_prefill_attention(const PrefillAttnArgs& a, void* workspace, 
   PrefillAttnArgs args = a;
   const PrefillWorkspace w = plan_prefill(a.B, a.T, a.Hq, a.G, head_dim);
   unsigned char* ws = static_cast<unsigned char*>(workspace);
-  args.plan_total = reinterpret_cast<int*>(ws);
+  args.plan_head = reinterpret_cast<int*>(ws);
   args.plan_items = reinterpret_cast<int4*>(ws + w.items);
-  args.plan_seq = reinterpret_cast<int2*>(ws + w.seq);
+  args.plan_tiles = reinterpret_cast<int2*>(ws + w.tiles);
+  args.plan_seq = reinterpret_cast<int*>(ws + w.seq);
   args.part_ml = reinterpret_cast<float2*>(ws + w.ml);
   args.part_o = reinterpret_cast<float*>(ws + w.o);
-  args.max_items = (int)w.max_items;
-  args.max_rows = (int)w.max_rows;
   // two row tiles an item when the sequences fill more than one on average
   const bool two = (long long)a.T > (long long)a.B * a.R;
   if (head_dim == 128) return two ? launch_attention<128, 2>(args, stream) : launch_attention<128, 1>(args, stream);
