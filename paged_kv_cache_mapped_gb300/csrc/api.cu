@@ -4,6 +4,7 @@
 #include <cudaTypedefs.h>
 
 #include <algorithm>
+#include <atomic>
 #include <cstring>
 #include <mutex>
 
@@ -151,6 +152,22 @@ int merge_warps_log2(const pkv_dims* d, int max_units, long long workers, int mi
   const long long rows = (long long)d->batch * d->num_q_heads;
   while (lg > 0 && (rows << lg) > resident_warps) --lg;
   return lg;
+}
+
+// Resident split CTAs per SM for this kernel and dynamic shared memory: the answer of the last query per
+// kernel is kept (a program's steps repeat their batch size), packed with its question in one word.
+int decode_ctas_per_sm(const DeviceInfo* info, const void* kernel, int hd, int mode, size_t smem, int* per_sm) {
+  static std::atomic<unsigned long long> last[kMaxDevices][2][9];
+  std::atomic<unsigned long long>& at = last[info - g_devices][hd][mode];
+  const unsigned long long known = at.load(std::memory_order_relaxed);
+  if (known != 0 && (known >> 8) == smem + 1) {
+    *per_sm = (int)(known & 255u);
+    return PKV_OK;
+  }
+  const cudaError_t e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(per_sm, kernel, kDecodeWarps * 32, smem);
+  if (e != cudaSuccess) return PKV_ERR_CUDA_BASE + (int)e;
+  at.store(((unsigned long long)(smem + 1) << 8) | (unsigned)(*per_sm & 255), std::memory_order_relaxed);
+  return PKV_OK;
 }
 
 size_t align256(size_t x) { return (x + 255) & ~size_t(255); }
@@ -311,8 +328,8 @@ int decode_common(void* out, const void* q, const void* k_cache, const void* v_c
   if (smem > info->max_dyn_smem[head_dim_index(dims->head_dim)][mode])
     return PKV_ERR_DIMS;
   int per_sm = 0;
-  cudaError_t e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per_sm, k.split, kDecodeWarps * 32, smem);
-  if (e != cudaSuccess) return cuda_status(e);
+  st = decode_ctas_per_sm(info, k.split, head_dim_index(dims->head_dim), mode, smem, &per_sm);
+  if (st != PKV_OK) return st;
   if (per_sm < 1) return PKV_ERR_DIMS;
 
   DecodeArgs a{};

@@ -281,6 +281,7 @@ struct StepArgs {
   const int32_t* new_tokens;     // [B]
   int32_t* err;
   int B, MB, NB, max_tokens;
+  int wide;                      // 1: slot_mapping and positions take 16-byte stores
 };
 constexpr int kMaxStepBatch = 4096;
 cudaError_t step_device_setup();

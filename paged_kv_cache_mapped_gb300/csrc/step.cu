@@ -17,9 +17,13 @@ namespace {
 // Three exclusive sums over the sequences (new tokens, blocks to take, blocks given back) decide
 // everything: the place of each token in the packed batch, of each taken block on the free stack
 // and of each pushed block.  The kernel reads a few bytes per sequence and writes 12 per token, so
-// its floor is the launch and a chain of dependent loads; one CTA runs it, and the checks of all
-// inputs come before the first write.
+// its floor is the launch and a chain of dependent loads.  One cluster runs it, of one CTA or (large steps) of
+// eight: every CTA has all the sums, the tokens and blocks are dealt out, and the cluster's barriers put the
+// checks of all inputs before the first write without a word of workspace.
 constexpr int kStepThreads = 1024;
+constexpr int kStepRunMost = kMaxStepBatch / kStepThreads;
+constexpr int kStepCluster = 8;
+constexpr int kStepLarge = 2048;  // more tokens or sequences than this are for eight CTAs
 
 // The largest i < n with start[i] <= x (start ascending, start[0] = 0, x below the total, so that
 // entry owns x: of equal starts the last one has the items).
@@ -32,12 +36,18 @@ __device__ __forceinline__ int owner_of(const int* start, int n, int x) {
   return lo;
 }
 
+// kStepRun: sequences of a thread.  CLUSTER: eight CTAs, or one (whose barriers are the block's, 1.7 us less).
+template <int kStepRun, bool CLUSTER>
 __global__ void __launch_bounds__(kStepThreads) step_tables_kernel(const StepArgs a) {
   namespace cg = cooperative_groups;
   cg::cluster_group cluster = cg::this_cluster();
-  const int rank = (int)cluster.block_rank();
+  const int rank = CLUSTER ? (int)cluster.block_rank() : 0;
+  auto sync_all = [&] {
+    if constexpr (CLUSTER) cluster.sync();
+    else __syncthreads();
+  };
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  const int gtid = rank * blockDim.x + tid, gsize = (int)cluster.num_blocks() * blockDim.x;
+  const int gtid = rank * blockDim.x + tid, gsize = (CLUSTER ? kStepCluster : 1) * (int)blockDim.x;
   const int warps = blockDim.x >> 5;
   extern __shared__ int s_dyn[];
   int* s_tok = s_dyn;             // [B + 1] exclusive sum of the new tokens
@@ -48,65 +58,76 @@ __global__ void __launch_bounds__(kStepThreads) step_tables_kernel(const StepArg
   __shared__ int s_carry[3];
   __shared__ int s_err;           // rank 0's copy collects the cluster's errors
   if (tid == 0) s_err = PKV_DEV_OK;
-  if (tid < 3) s_carry[tid] = 0;
   grid_dependency_wait();
   grid_launch_dependents();
-  cluster.sync();
-  int* err0 = cluster.map_shared_rank(&s_err, 0);
+  sync_all();
+  int* err0 = CLUSTER ? cluster.map_shared_rank(&s_err, 0) : &s_err;
   auto fail = [&](int code) { atomicCAS(err0, PKV_DEV_OK, code); };
 
-  for (int base = 0; base < a.B; base += blockDim.x) {
-    const int b = base + tid;
-    int v[3] = {0, 0, 0};
-    int c = 0;
+  // a thread's run of up to kStepRun sequences, summed here, then across the block
+  int v[3][kStepRun], sum[3] = {0, 0, 0};
+  const int run0 = tid * kStepRun;
+#pragma unroll
+  for (int k = 0; k < kStepRun; ++k) {
+    const int b = run0 + k;
+#pragma unroll
+    for (int q = 0; q < 3; ++q) v[q][k] = 0;
     if (b < a.B) {
-      c = a.context_lens[b];
-      const int n = a.new_tokens[b];
+      const int c = a.context_lens[b], n = a.new_tokens[b];
       const long long cap = (long long)a.MB * 16;
       if (c < 0 || c > cap || (n > 0 && (long long)c + n > cap)) fail(PKV_DEV_BAD_CONTEXT_LEN);
       else if (n < -1) fail(PKV_DEV_BAD_QUERY_RANGE);
       else {
         // more tokens than the step holds are an error below; the cut keeps the sums in 32 bits
         const int m = min(n, a.max_tokens + 1);
-        v[0] = max(m, 0);
-        v[1] = m > 0 ? ((c + m + 15) >> 4) - ((c + 15) >> 4) : 0;
-        v[2] = n < 0 ? (c + 15) >> 4 : 0;
+        v[0][k] = max(m, 0);
+        v[1][k] = m > 0 ? ((c + m + 15) >> 4) - ((c + 15) >> 4) : 0;
+        v[2][k] = n < 0 ? (c + 15) >> 4 : 0;
       }
-    }
-    int incl[3];
-#pragma unroll
-    for (int q = 0; q < 3; ++q) {
-      int x = v[q];
-#pragma unroll
-      for (int o = 1; o < 32; o <<= 1) {
-        const int t = __shfl_up_sync(kFullMask, x, o);
-        if (lane >= o) x += t;
-      }
-      incl[q] = x;
-      if (lane == 31) s_warp[q][warp] = x;
-    }
-    __syncthreads();
-    if (warp < 3) {
-      const int own = lane < warps ? s_warp[warp][lane] : 0;
-      int x = own;
-#pragma unroll
-      for (int o = 1; o < 32; o <<= 1) {
-        const int t = __shfl_up_sync(kFullMask, x, o);
-        if (lane >= o) x += t;
-      }
-      const int carry = s_carry[warp];
-      s_warp[warp][lane] = carry + x - own;
-      __syncwarp();
-      if (lane == 31) s_carry[warp] = carry + x;
-    }
-    __syncthreads();
-    if (b < a.B) {
-      s_tok[b] = s_warp[0][warp] + incl[0] - v[0];
-      s_take[b] = s_warp[1][warp] + incl[1] - v[1];
-      s_push[b] = s_warp[2][warp] + incl[2] - v[2];
       s_len[b] = c;
     }
-    __syncthreads();
+#pragma unroll
+    for (int q = 0; q < 3; ++q) sum[q] += v[q][k];
+  }
+  int incl[3];
+#pragma unroll
+  for (int q = 0; q < 3; ++q) {
+    int x = sum[q];
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int t = __shfl_up_sync(kFullMask, x, o);
+      if (lane >= o) x += t;
+    }
+    incl[q] = x;
+    if (lane == 31) s_warp[q][warp] = x;
+  }
+  __syncthreads();
+  if (warp < 3) {
+    const int own = lane < warps ? s_warp[warp][lane] : 0;
+    int x = own;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int t = __shfl_up_sync(kFullMask, x, o);
+      if (lane >= o) x += t;
+    }
+    s_warp[warp][lane] = x - own;
+    if (lane == 31) s_carry[warp] = x;
+  }
+  __syncthreads();
+  {
+    int at[3];
+#pragma unroll
+    for (int q = 0; q < 3; ++q) at[q] = s_warp[q][warp] + incl[q] - sum[q];
+#pragma unroll
+    for (int k = 0; k < kStepRun; ++k) {
+      if (run0 + k < a.B) {
+        s_tok[run0 + k] = at[0];
+        s_take[run0 + k] = at[1];
+        s_push[run0 + k] = at[2];
+      }
+#pragma unroll
+      for (int q = 0; q < 3; ++q) at[q] += v[q][k];
+    }
   }
   const int T = s_carry[0], A = s_carry[1], R = s_carry[2];
   const int count = a.free_count[0];
@@ -115,7 +136,7 @@ __global__ void __launch_bounds__(kStepThreads) step_tables_kernel(const StepArg
     if (T > a.max_tokens) fail(PKV_DEV_BAD_QUERY_RANGE);
     else if (count < 0 || count > a.NB || R > a.NB - count || A > count + R) fail(PKV_DEV_NO_BLOCKS);
   }
-  cluster.sync();
+  sync_all();
   const int top = count + R;
   bool ok = *err0 == PKV_DEV_OK;
   if (ok) {
@@ -136,14 +157,14 @@ __global__ void __launch_bounds__(kStepThreads) step_tables_kernel(const StepArg
     }
   }
   __threadfence();
-  cluster.sync();
+  sync_all();
   if (ok) {
     for (int p = gtid; p < A; p += gsize) {
       const int id = __ldcg(a.free_blocks + top - 1 - p);
       if (id < 0 || id >= a.NB) fail(PKV_DEV_BAD_BLOCK_ID);
     }
   }
-  cluster.sync();
+  sync_all();
   const int code = *err0;
   ok = code == PKV_DEV_OK;
   for (int b = gtid; b <= a.B; b += gsize) {
@@ -154,20 +175,44 @@ __global__ void __launch_bounds__(kStepThreads) step_tables_kernel(const StepArg
     const bool ended = (b + 1 < a.B ? s_push[b + 1] : R) > s_push[b];
     a.context_lens_out[b] = ok ? (ended ? 0 : s_len[b] + n) : s_len[b];
   }
-  for (int i = gtid; i < a.max_tokens; i += gsize) {
-    long long slot = -1;
-    int pos = -1;
-    if (ok && i < T) {
-      const int b = owner_of(s_tok, a.B, i);
-      const int c = s_len[b], held = (c + 15) >> 4;
-      pos = c + i - s_tok[b];
-      const int j = pos >> 4;
-      const int id = j < held ? a.block_tables[(size_t)b * a.MB + j]
-                              : __ldcg(a.free_blocks + top - 1 - (s_take[b] + j - held));
-      slot = (long long)id * 16 + (pos & 15);
+  // four tokens a thread: one search, then along; 16-byte stores
+  for (int i0 = 4 * gtid; i0 < a.max_tokens; i0 += 4 * gsize) {
+    long long slot[4];
+    int pos[4];
+    int b = 0, block_j = -1, id = 0;
+    if (ok && i0 < T) b = owner_of(s_tok, a.B, i0);
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      slot[k] = -1;
+      pos[k] = -1;
+      if (ok && i0 + k < T) {
+        while (s_tok[b + 1] <= i0 + k) {
+          ++b;
+          block_j = -1;
+        }
+        const int c = s_len[b], held = (c + 15) >> 4;
+        pos[k] = c + i0 + k - s_tok[b];
+        const int j = pos[k] >> 4;
+        if (j != block_j) {
+          id = j < held ? a.block_tables[(size_t)b * a.MB + j]
+                        : __ldcg(a.free_blocks + top - 1 - (s_take[b] + j - held));
+          block_j = j;
+        }
+        slot[k] = (long long)id * 16 + (pos[k] & 15);
+      }
     }
-    a.slot_mapping[i] = slot;
-    a.positions[i] = pos;
+    if (a.wide && i0 + 4 <= a.max_tokens) {
+      *reinterpret_cast<longlong2*>(a.slot_mapping + i0) = make_longlong2(slot[0], slot[1]);
+      *reinterpret_cast<longlong2*>(a.slot_mapping + i0 + 2) = make_longlong2(slot[2], slot[3]);
+      *reinterpret_cast<int4*>(a.positions + i0) = make_int4(pos[0], pos[1], pos[2], pos[3]);
+    } else {
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        if (i0 + k >= a.max_tokens) break;
+        a.slot_mapping[i0 + k] = slot[k];
+        a.positions[i0 + k] = pos[k];
+      }
+    }
   }
   if (ok) {
     for (int p = gtid; p < A; p += gsize) {
@@ -180,7 +225,7 @@ __global__ void __launch_bounds__(kStepThreads) step_tables_kernel(const StepArg
     a.free_count_out[0] = ok ? top - A : count;
     if (!ok) record_error(a.err, code);
   }
-  cluster.sync();  // rank 0's error word is read by all until here
+  sync_all();  // rank 0's error word is read by all until here
 }
 
 // --------------------------------------------------------------------------------- FP8 append
@@ -206,39 +251,16 @@ __device__ __forceinline__ float needed_scale(float amax) {
   return __int_as_float((e + 127) << 23);
 }
 
-// One warp per (token, kv head); the first token of a block in the call leads the block's run of
-// adjacent tokens and the warps of the others end at once, so a block's scale has one writer.
-// Lanes 0-15 hold the K rows, lanes 16-31 the V rows, D / 16 elements each.
+// One run for one kv head: `tok` leads it.
 template <int D>
-__global__ void __launch_bounds__(256) kv_append_f8_kernel(uint8_t* __restrict__ kq, uint8_t* __restrict__ vq,
-                                                           float* __restrict__ ks, float* __restrict__ vs,
-                                                           const __nv_bfloat16* __restrict__ k,
-                                                           const __nv_bfloat16* __restrict__ v,
-                                                           const int64_t* __restrict__ slots, int64_t T,
-                                                           int Hkv, int NB, int32_t* err) {
+__device__ __forceinline__ void append_run(uint8_t* kq, uint8_t* vq, float* ks, float* vs, const __nv_bfloat16* k,
+                                           const __nv_bfloat16* v, const int64_t* slots, int64_t T, int Hkv,
+                                           int64_t tok, int g, int32_t* err) {
   constexpr int E = D / 16;   // elements per lane
   constexpr int W = E / 2;    // words of two bf16
-  const int64_t item = ((int64_t)blockIdx.x * blockDim.x + threadIdx.x) >> 5;
   const int lane = threadIdx.x & 31;
-  grid_dependency_wait();
-  grid_launch_dependents();
-  if (item >= T * Hkv) return;
-  const int64_t tok = item / Hkv;
-  const int g = (int)(item - tok * Hkv);
   const int64_t slot = __ldg(slots + tok);
-  if (slot < 0) return;
-  if (slot >= (int64_t)NB * 16) {
-    if (lane == 0) record_error(err, PKV_DEV_BAD_SLOT);
-    return;
-  }
   const int64_t blk = slot >> 4;
-  if (tok > 0) {
-    const int64_t before = __ldg(slots + tok - 1);
-    if (before >= 0 && (before >> 4) == blk) {
-      if (before >= slot && lane == 0) record_error(err, PKV_DEV_BAD_SLOT);
-      return;
-    }
-  }
   // the run: lane l looks at token tok + l, which belongs while every one up to it is in the block
   // and above the one before
   int off = -1;
@@ -256,7 +278,7 @@ __global__ void __launch_bounds__(256) kv_append_f8_kernel(uint8_t* __restrict__
   const __nv_bfloat16* src = (lane < 16 ? k : v) + ((size_t)tok * Hkv + g) * D + h * E;
   uint32_t x[16][W];
   uint32_t good = 0;  // tokens of the run whose K and V rows are finite
-  float amax = 0.f;
+  uint32_t most = 0;  // largest |x| so far as bf16 bits, a pair of 16-bit numbers (sign cleared they order like the values)
 #pragma unroll
   for (int r = 0; r < 16; ++r) {
     if (r >= run) break;
@@ -272,24 +294,21 @@ __global__ void __launch_bounds__(256) kv_append_f8_kernel(uint8_t* __restrict__
 #pragma unroll
   for (int r = 0; r < 16; ++r) {
     if (r >= run) break;
-    float m = 0.f;
-    bool finite = true;
+    uint32_t m = x[r][0] & 0x7fff7fffu;
 #pragma unroll
-    for (int i = 0; i < W; ++i) {
-      const float lo = bf16_lo_to_f32(x[r][i]), hi = bf16_hi_to_f32(x[r][i]);
-      finite &= isfinite(lo) && isfinite(hi);
-      m = fmaxf(m, fmaxf(fabsf(lo), fabsf(hi)));
-    }
+    for (int i = 1; i < W; ++i) m = __vmaxu2(m, x[r][i] & 0x7fff7fffu);
+    const bool finite = (m & 0xffffu) < 0x7f80u && (m >> 16) < 0x7f80u;
     if (__all_sync(kFullMask, finite)) {
       good |= 1u << r;
-      amax = fmaxf(amax, m);
+      most = __vmaxu2(most, m);
     } else if (lane == 0) {
       record_error(err, PKV_DEV_BAD_VALUE);
     }
   }
   if (good == 0) return;
 #pragma unroll
-  for (int m = 1; m < 16; m <<= 1) amax = fmaxf(amax, __shfl_xor_sync(kFullMask, amax, m));  // the half-warp
+  for (int m = 1; m < 16; m <<= 1) most = __vmaxu2(most, __shfl_xor_sync(kFullMask, most, m));  // the half-warp
+  const float amax = __uint_as_float(max(most & 0xffffu, most >> 16) << 16);
   float* scale_at = (lane < 16 ? ks : vs) + (size_t)blk * Hkv + g;
   uint8_t* codes = (lane < 16 ? kq : vq) + row0 * D + h * E;
   const bool anew = (slot & 15) == 0;
@@ -325,13 +344,20 @@ __global__ void __launch_bounds__(256) kv_append_f8_kernel(uint8_t* __restrict__
     const int o = __shfl_sync(kFullMask, off, r);
     if (!((good >> r) & 1u)) continue;
     uint32_t out[E / 4];
+    if (pow2) {
+      const uint64_t inv2 = pack2(inv, inv);
 #pragma unroll
-    for (int i = 0; i < E / 4; ++i) {
-      float f[4] = {bf16_lo_to_f32(x[r][2 * i]), bf16_hi_to_f32(x[r][2 * i]), bf16_lo_to_f32(x[r][2 * i + 1]),
-                    bf16_hi_to_f32(x[r][2 * i + 1])};
+      for (int i = 0; i < E / 4; ++i) {
+        const float2 a = unpack2(fmul2(bf16x2_to_f32x2(x[r][2 * i]), inv2));
+        const float2 b = unpack2(fmul2(bf16x2_to_f32x2(x[r][2 * i + 1]), inv2));
+        out[i] = pack_e4m3x2(a.x, a.y) | (pack_e4m3x2(b.x, b.y) << 16);
+      }
+    } else {
 #pragma unroll
-      for (int e = 0; e < 4; ++e) f[e] = pow2 ? f[e] * inv : __fdiv_rn(f[e], now);
-      out[i] = pack_e4m3x2(f[0], f[1]) | (pack_e4m3x2(f[2], f[3]) << 16);
+      for (int i = 0; i < E / 4; ++i)
+        out[i] = pack_e4m3x2(__fdiv_rn(bf16_lo_to_f32(x[r][2 * i]), now), __fdiv_rn(bf16_hi_to_f32(x[r][2 * i]), now)) |
+                 (pack_e4m3x2(__fdiv_rn(bf16_lo_to_f32(x[r][2 * i + 1]), now),
+                              __fdiv_rn(bf16_hi_to_f32(x[r][2 * i + 1]), now)) << 16);
     }
     if constexpr (E == 8)
       *reinterpret_cast<uint2*>(codes + o * D) = make_uint2(out[0], out[1]);
@@ -341,28 +367,91 @@ __global__ void __launch_bounds__(256) kv_append_f8_kernel(uint8_t* __restrict__
   if (h == 0 && now != old) *scale_at = now;
 }
 
+// The first token of a block in the call leads the block's run of adjacent tokens, and one warp takes the run
+// for one kv head, so a block's scale has one writer.  Lanes 0-15 hold the K rows, lanes 16-31 the V rows,
+// D / 16 elements each; all rows of a run are loaded before any is used.  A CTA has a window of up to 32 tokens,
+// whose leaders times kv heads its warps share: with a window of 1 (few tokens) every run has its own CTA, with
+// 16 (prompts) a CTA has one or two runs of 16 tokens instead of 16 CTAs of which 15 end at once.  The bytes
+// bound it (16 prompts of ~4000, 8 heads, d 128, 388 MB: 288 -> @@ us).
+constexpr int kAppendWarps = 8;
+
+template <int D>
+__global__ void __launch_bounds__(kAppendWarps * 32, 2)
+kv_append_f8_kernel(uint8_t* __restrict__ kq, uint8_t* __restrict__ vq, float* __restrict__ ks, float* __restrict__ vs,
+                    const __nv_bfloat16* __restrict__ k, const __nv_bfloat16* __restrict__ v,
+                    const int64_t* __restrict__ slots, int64_t T, int Hkv, int NB, int window, int32_t* err) {
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  grid_dependency_wait();
+  grid_launch_dependents();
+  const int64_t tok0 = (int64_t)blockIdx.x * window;
+  uint32_t leaders;
+  {
+    int code = 0;
+    bool leads = false;
+    const int64_t t = tok0 + lane;
+    if (lane < window && t < T) {
+      const int64_t slot = __ldg(slots + t);
+      const int64_t before = t > 0 ? __ldg(slots + t - 1) : -1;
+      if (slot >= (int64_t)NB * 16) code = PKV_DEV_BAD_SLOT;
+      else if (slot >= 0) {
+        leads = before < 0 || (before >> 4) != (slot >> 4);
+        if (!leads && before >= slot) code = PKV_DEV_BAD_SLOT;  // not above the one before
+      }
+    }
+    if (warp == 0 && code != 0) record_error(err, code);
+    leaders = __ballot_sync(kFullMask, leads);
+  }
+  const int runs = __popc(leaders);
+  for (int item = warp; item < runs * Hkv; item += kAppendWarps) {
+    const int nth = item / Hkv, g = item - nth * Hkv;
+    const int64_t tok = tok0 + (int)__fns(leaders, 0, nth + 1);
+    append_run<D>(kq, vq, ks, vs, k, v, slots, T, Hkv, tok, g, err);
+  }
+}
+
 }  // namespace
 
 size_t step_smem_bytes(int batch) { return sizeof(int) * (4 * (size_t)batch + 1); }
 
 cudaError_t step_device_setup() {
-  return cudaFuncSetAttribute((const void*)step_tables_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+  return cudaFuncSetAttribute((const void*)step_tables_kernel<kStepRunMost, true>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                               (int)step_smem_bytes(kMaxStepBatch));
 }
 
 cudaError_t launch_step_tables(const StepArgs& a, cudaStream_t stream) {
   StepArgs args = a;
+  args.wide = ((reinterpret_cast<uintptr_t>(a.slot_mapping) | reinterpret_cast<uintptr_t>(a.positions)) & 15u) == 0;
   void* params[] = {&args};
-  return launch_pdl((const void*)step_tables_kernel, dim3(1), dim3(kStepThreads), step_smem_bytes(a.B), stream, params);
+  const bool large = a.max_tokens > kStepLarge || a.B > kStepLarge;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(large ? kStepCluster : 1);
+  cfg.blockDim = dim3(a.B <= 512 && !large ? 256 : kStepThreads);
+  cfg.dynamicSmemBytes = step_smem_bytes(a.B);
+  cfg.stream = stream;
+  cudaLaunchAttribute attr[2];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  attr[1].id = cudaLaunchAttributeClusterDimension;
+  attr[1].val.clusterDim.x = large ? kStepCluster : 1;
+  attr[1].val.clusterDim.y = 1;
+  attr[1].val.clusterDim.z = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = large ? 2 : 1;
+  const void* f = !large              ? (const void*)step_tables_kernel<2, false>
+                  : a.B <= kStepThreads ? (const void*)step_tables_kernel<1, true>
+                                        : (const void*)step_tables_kernel<kStepRunMost, true>;
+  return cudaLaunchKernelExC(&cfg, f, params);
 }
 
 cudaError_t launch_kv_append_f8(void* kq, void* vq, float* ks, float* vs, const void* k, const void* v,
                                 const int64_t* slots, int64_t T, int Hkv, int D, int NB, int32_t* err,
                                 cudaStream_t stream) {
-  const int64_t blocks = (T * Hkv + 7) / 8;
-  void* params[] = {&kq, &vq, &ks, &vs, &k, &v, &slots, &T, &Hkv, &NB, &err};
+  // the window: as many tokens as leave about two CTAs for each place on the GPU (two of 152 SMs)
+  int window = (int)std::min<int64_t>(16, std::max<int64_t>(1, T * Hkv / (kAppendWarps * 2 * 304)));
+  const int64_t blocks = (T + window - 1) / window;
+  void* params[] = {&kq, &vq, &ks, &vs, &k, &v, &slots, &T, &Hkv, &NB, &window, &err};
   const void* f = D == 128 ? (const void*)kv_append_f8_kernel<128> : (const void*)kv_append_f8_kernel<64>;
-  return launch_pdl(f, dim3((unsigned)blocks), dim3(256), 0, stream, params);
+  return launch_pdl(f, dim3((unsigned)blocks), dim3(kAppendWarps * 32), 0, stream, params);
 }
 
 }  // namespace pkv
@@ -415,7 +504,7 @@ int pkv_kv_append_f8(void* k_codes, void* v_codes, float* k_scales, float* v_sca
                      void* stream) {
   int st = check_dims(dims, false);
   if (st != PKV_OK) return st;
-  if (num_tokens < 0 || num_tokens * dims->num_kv_heads >= (1ll << 33)) return PKV_ERR_DIMS;
+  if (num_tokens < 0 || num_tokens >= (1ll << 33) / dims->num_kv_heads) return PKV_ERR_DIMS;
   if (num_tokens == 0) return PKV_OK;
   if (!k_codes || !v_codes || !k_scales || !v_scales || !k || !v || !slot_mapping) return PKV_ERR_NULL_POINTER;
   if (!aligned16(k_codes) || !aligned16(v_codes) || !aligned16(k) || !aligned16(v) ||

@@ -5,6 +5,7 @@ work runs in the library's CUDA kernels on the current stream of the tensors' de
 from __future__ import annotations
 
 import ctypes
+import functools
 
 import torch
 
@@ -14,10 +15,15 @@ BLOCK_SIZE = 16
 _INPUTS_READY = header_constants()["PKV_DECODE_INPUTS_READY"]
 
 
-def _need(t, name, dtype, ndim, device=None):
-    if not isinstance(t, torch.Tensor):
-        raise TypeError(f"{name} must be a torch.Tensor")
-    if t.dtype != dtype:
+def _need(t, name, dtype, ndim, device=-1):
+    """The tensor's address, once it is what the kernels take: on CUDA device number `device` (-1: any)."""
+    try:
+        if (t.dtype is dtype and t.is_cuda and t.is_contiguous() and t.dim() == ndim
+                and (device < 0 or t.get_device() == device)):
+            return t.data_ptr()
+    except AttributeError:
+        raise TypeError(f"{name} must be a torch.Tensor") from None
+    if t.dtype is not dtype:
         raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
     if not t.is_cuda:
         raise ValueError(f"{name} must live on a CUDA device (the library has no CPU path)")
@@ -25,39 +31,48 @@ def _need(t, name, dtype, ndim, device=None):
         raise ValueError(f"{name} must be contiguous")
     if t.dim() != ndim:
         raise ValueError(f"{name} must have {ndim} dims, got shape {tuple(t.shape)}")
-    if device is not None and t.device != device:
-        raise ValueError(f"{name} is on {t.device}, expected {device}")
-    return t.data_ptr()
+    raise ValueError(f"{name} is on {t.device}, expected cuda:{device}")
 
 
 def _opt(t, name, dtype, ndim, device):
     return None if t is None else _need(t, name, dtype, ndim, device)
 
 
+_functions = {}
+
+
 def _call(name, device, stream, *args):
-    """Calls pkv_<name>(*args, stream) with `device` current."""
-    fn = getattr(load(), name)
-    if torch.cuda.current_device() == device.index:
-        s = stream if stream is not None else torch.cuda.current_stream(device)
-        check(name, fn(*args, s.cuda_stream))
+    """Calls pkv_<name>(*args, stream) with CUDA device number `device` current."""
+    fn = _functions.get(name)
+    if fn is None:
+        fn = _functions[name] = getattr(load(), name)
+    if torch._C._cuda_getDevice() == device:
+        s = torch._C._cuda_getCurrentRawStream(device) if stream is None else stream.cuda_stream
+        status = fn(*args, s)
     else:
         with torch.cuda.device(device):
-            s = stream if stream is not None else torch.cuda.current_stream(device)
-            check(name, fn(*args, s.cuda_stream))
+            s = torch._C._cuda_getCurrentRawStream(device) if stream is None else stream.cuda_stream
+            status = fn(*args, s)
+    if status:
+        check(name, status)
 
 
+@functools.lru_cache(maxsize=256)
 def _dims(batch, hq, hkv, d, nb, mb):
-    return PkvDims(batch, hq, hkv, d, BLOCK_SIZE, nb, mb)
+    """The shape record's address (records of the same sizes are one)."""
+    r = PkvDims(batch, hq, hkv, d, BLOCK_SIZE, nb, mb)
+    return ctypes.pointer(r)
 
 
-def _give(t, name, shape, dtype, device):
-    """The output `t` after its checks, or a new one."""
+def _give(t, name, shape, dtype, like, device):
+    """The output `t` after its checks, or a new one on `like`'s device; with its address."""
     if t is None:
-        return torch.empty(shape, dtype=dtype, device=device)
-    _need(t, name, dtype, len(shape), device)
+        t = torch.empty(shape, dtype=dtype, device=like.device)
+        return t, t.data_ptr()
+    ptr = _need(t, name, dtype, len(shape), device)
     if tuple(t.shape) != tuple(shape):
         raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
-    return t
+    return t, ptr
 
 
 def kv_step_tables(block_tables, context_lens, new_tokens, free_blocks, free_count, max_new_tokens, *,
@@ -70,8 +85,8 @@ def kv_step_tables(block_tables, context_lens, new_tokens, free_blocks, free_cou
     free_count_out [1]); rows past the step's last token have slot and position -1.  context_lens_out
     and free_count_out may be the inputs themselves.  All or nothing on a device error (see
     pkv_kv_step_tables)."""
-    dev = block_tables.device if isinstance(block_tables, torch.Tensor) else None
     bt = _need(block_tables, "block_tables", torch.int32, 2)
+    dev = block_tables.get_device()
     lens = _need(context_lens, "context_lens", torch.int32, 1, dev)
     new = _need(new_tokens, "new_tokens", torch.int32, 1, dev)
     free = _need(free_blocks, "free_blocks", torch.int32, 1, dev)
@@ -85,31 +100,41 @@ def kv_step_tables(block_tables, context_lens, new_tokens, free_blocks, free_cou
     T = int(max_new_tokens)
     if T < 0:
         raise ValueError("max_new_tokens must not be negative")
-    lens_out = _give(context_lens_out, "context_lens_out", (B,), torch.int32, dev)
-    count_out = _give(free_count_out, "free_count_out", (1,), torch.int32, dev)
-    starts = _give(query_starts, "query_starts", (B + 1,), torch.int32, dev)
-    slots = _give(slot_mapping, "slot_mapping", (T,), torch.int64, dev)
-    pos = _give(positions, "positions", (T,), torch.int32, dev)
-    dims = _dims(B, 1, 1, 128, free_blocks.shape[0], mb)
-    _call("pkv_kv_step_tables", dev, stream, bt, lens_out.data_ptr(), starts.data_ptr(), slots.data_ptr(), pos.data_ptr(),
-          count_out.data_ptr(), free, count, lens, new, T, ctypes.byref(dims), err)
+    lens_out, lp = _give(context_lens_out, "context_lens_out", (B,), torch.int32, block_tables, dev)
+    count_out, cp = _give(free_count_out, "free_count_out", (1,), torch.int32, block_tables, dev)
+    starts, qp = _give(query_starts, "query_starts", (B + 1,), torch.int32, block_tables, dev)
+    slots, sp = _give(slot_mapping, "slot_mapping", (T,), torch.int64, block_tables, dev)
+    pos, pp = _give(positions, "positions", (T,), torch.int32, block_tables, dev)
+    _call("pkv_kv_step_tables", dev, stream, bt, lp, qp, sp, pp, cp, free, count, lens, new, T,
+          _dims(B, 1, 1, 128, free_blocks.shape[0], mb), err)
     return lens_out, starts, slots, pos, count_out
 
 
 def _f8_pools(k_codes, v_codes, k_scales, v_scales):
-    dev = k_codes.device if isinstance(k_codes, torch.Tensor) else None
-    _need(k_codes, "k_codes", torch.float8_e4m3fn, 4)
-    _need(v_codes, "v_codes", torch.float8_e4m3fn, 4, dev)
-    _need(k_scales, "k_scales", torch.float32, 2, dev)
-    _need(v_scales, "v_scales", torch.float32, 2, dev)
-    nb, hkv, bs, d = k_codes.shape
-    if v_codes.shape != k_codes.shape:
+    kp = _need(k_codes, "k_codes", torch.float8_e4m3fn, 4)
+    dev = k_codes.get_device()
+    vp = _need(v_codes, "v_codes", torch.float8_e4m3fn, 4, dev)
+    ksp = _need(k_scales, "k_scales", torch.float32, 2, dev)
+    vsp = _need(v_scales, "v_scales", torch.float32, 2, dev)
+    shape = k_codes.shape
+    nb, hkv, bs, d = shape
+    if v_codes.shape != shape:
         raise ValueError("k_codes and v_codes shapes differ")
     if bs != BLOCK_SIZE:
         raise ValueError(f"pool block size must be {BLOCK_SIZE}")
     if k_scales.shape != (nb, hkv) or v_scales.shape != (nb, hkv):
         raise ValueError("scale pools must be [num_blocks, num_kv_heads]")
-    return nb, hkv, d, dev
+    return nb, hkv, d, dev, kp, vp, ksp, vsp
+
+
+def _bf16_pools(k_cache, v_cache):
+    kp = _need(k_cache, "k_cache", torch.bfloat16, 4)
+    dev = k_cache.get_device()
+    vp = _need(v_cache, "v_cache", torch.bfloat16, 4, dev)
+    nb, hkv, bs, d = k_cache.shape
+    if v_cache.shape != k_cache.shape or bs != BLOCK_SIZE:
+        raise ValueError(f"pools must have one shape [num_blocks, num_kv_heads, {BLOCK_SIZE}, head_dim]")
+    return nb, hkv, d, dev, kp, vp
 
 
 def kv_append_f8(k_codes, v_codes, k_scales, v_scales, k, v, slot_mapping, *, error_word=None, stream=None):
@@ -118,7 +143,7 @@ def kv_append_f8(k_codes, v_codes, k_scales, v_scales, k, v, slot_mapping, *, er
     A block written at offset 0 starts anew; otherwise its scale only grows and its other rows move to
     it.  The tokens of one block are adjacent in slot_mapping, slots ascending (the order of
     kv_step_tables)."""
-    nb, hkv, d, dev = _f8_pools(k_codes, v_codes, k_scales, v_scales)
+    nb, hkv, d, dev, kc, vc, ks, vs = _f8_pools(k_codes, v_codes, k_scales, v_scales)
     kp = _need(k, "k", torch.bfloat16, 3, dev)
     vp = _need(v, "v", torch.bfloat16, 3, dev)
     sp = _need(slot_mapping, "slot_mapping", torch.int64, 1, dev)
@@ -126,9 +151,7 @@ def kv_append_f8(k_codes, v_codes, k_scales, v_scales, k, v, slot_mapping, *, er
     T = slot_mapping.shape[0]
     if k.shape != (T, hkv, d) or v.shape != (T, hkv, d):
         raise ValueError("k/v must be [num_tokens, num_kv_heads, head_dim]")
-    dims = _dims(0, 0, hkv, d, nb, 0)
-    _call("pkv_kv_append_f8", dev, stream, k_codes.data_ptr(), v_codes.data_ptr(), k_scales.data_ptr(), v_scales.data_ptr(),
-          kp, vp, sp, T, ctypes.byref(dims), err)
+    _call("pkv_kv_append_f8", dev, stream, kc, vc, ks, vs, kp, vp, sp, T, _dims(0, 0, hkv, d, nb, 0), err)
 
 
 def _rules(softcap, window, alibi_slopes, doc_starts, prefix_lens, hq, rows, batch, dev):
@@ -153,17 +176,17 @@ def _decode_common(q, nb, hkv, d, block_tables, context_lens, out, workspace, er
     lp = _need(context_lens, "context_lens", torch.int32, 1, dev)
     err = _opt(error_word, "error_word", torch.int32, 1, dev)
     B, hq, dq = q.shape
+    rows, mb = block_tables.shape
     if dq != d:
         raise ValueError("q head_dim differs from the pools'")
-    if block_tables.shape[0] != B or context_lens.shape[0] != B:
+    if rows != B or context_lens.shape[0] != B:
         raise ValueError("block_tables / context_lens batch differs from q's")
-    dims = _dims(B, hq, hkv, d, nb, block_tables.shape[1])
-    out = _give(out, "out", q.shape, torch.bfloat16, dev)
+    dims = _dims(B, hq, hkv, d, nb, mb)
+    out, op = _give(out, "out", (B, hq, d), torch.bfloat16, q, dev)
     if workspace is None:
-        workspace = torch.zeros(int(load().pkv_decode_workspace_bytes(ctypes.byref(dims))), dtype=torch.uint8, device=dev)
-    else:
-        _need(workspace, "workspace", torch.uint8, 1, dev)
-    return dims, qp, bp, lp, err, out, workspace
+        workspace = torch.zeros(int(load().pkv_decode_workspace_bytes(dims)), dtype=torch.uint8, device=q.device)
+    wp = _need(workspace, "workspace", torch.uint8, 1, dev)
+    return B, hq, dims, qp, bp, lp, err, out, op, wp, workspace.numel()
 
 
 def paged_decode_attention_rules(q, k_cache, v_cache, block_tables, context_lens, scale, window=0, *, softcap=0.0,
@@ -172,18 +195,12 @@ def paged_decode_attention_rules(q, k_cache, v_cache, block_tables, context_lens
     """paged_decode_attention with score rules: scores capped to softcap * tanh(x / softcap), a distance
     bias -alibi_slopes[h] * (L - 1 - t) (fp32 [Hq]), and the visible keys [max(0, L - window, doc_start), L)
     and [0, prefix_len) (int32 [B] each).  Returns out [B, Hq, d] bf16; a row that sees no key is zero."""
-    dev = k_cache.device if isinstance(k_cache, torch.Tensor) else None
-    kp = _need(k_cache, "k_cache", torch.bfloat16, 4)
-    vp = _need(v_cache, "v_cache", torch.bfloat16, 4, dev)
-    nb, hkv, bs, d = k_cache.shape
-    if v_cache.shape != k_cache.shape or bs != BLOCK_SIZE:
-        raise ValueError(f"pools must have one shape [num_blocks, num_kv_heads, {BLOCK_SIZE}, head_dim]")
-    dims, qp, bp, lp, err, out, workspace = _decode_common(q, nb, hkv, d, block_tables, context_lens, out, workspace,
-                                                           error_word, dev)
-    rules = _rules(softcap, window, alibi_slopes, doc_starts, prefix_lens, dims.num_q_heads, dims.batch, dims.batch, dev)
-    _call("pkv_paged_decode_attention_rules", dev, stream, out.data_ptr(), qp, kp, vp, bp, lp, float(scale),
-          ctypes.byref(rules), workspace.data_ptr(), workspace.numel(), ctypes.byref(dims),
-          _INPUTS_READY if inputs_ready else 0, err)
+    nb, hkv, d, dev, kp, vp = _bf16_pools(k_cache, v_cache)
+    B, hq, dims, qp, bp, lp, err, out, op, wp, ws_bytes = _decode_common(q, nb, hkv, d, block_tables, context_lens, out,
+                                                                         workspace, error_word, dev)
+    rules = _rules(softcap, window, alibi_slopes, doc_starts, prefix_lens, hq, B, B, dev)
+    _call("pkv_paged_decode_attention_rules", dev, stream, op, qp, kp, vp, bp, lp, scale, ctypes.byref(rules), wp, ws_bytes,
+          dims, _INPUTS_READY if inputs_ready else 0, err)
     return out
 
 
@@ -192,21 +209,21 @@ def paged_decode_attention_f8(q, k_codes, v_codes, k_scales, v_scales, block_tab
                               workspace=None, error_word=None, inputs_ready=False, stream=None):
     """paged_decode_attention over FP8 pools (codes [NB, Hkv, 16, d] torch.float8_e4m3fn times one fp32
     scale per (block, kv head), [NB, Hkv]), with the score rules of paged_decode_attention_rules."""
-    nb, hkv, d, dev = _f8_pools(k_codes, v_codes, k_scales, v_scales)
-    dims, qp, bp, lp, err, out, workspace = _decode_common(q, nb, hkv, d, block_tables, context_lens, out, workspace,
-                                                           error_word, dev)
-    rules = _rules(softcap, window, alibi_slopes, doc_starts, prefix_lens, dims.num_q_heads, dims.batch, dims.batch, dev)
-    plain = rules.softcap == 0 and rules.window <= 0 and alibi_slopes is None and doc_starts is None and prefix_lens is None
-    _call("pkv_paged_decode_attention_f8", dev, stream, out.data_ptr(), qp, k_codes.data_ptr(), v_codes.data_ptr(),
-          k_scales.data_ptr(), v_scales.data_ptr(), bp, lp, float(scale), None if plain else ctypes.byref(rules),
-          workspace.data_ptr(), workspace.numel(), ctypes.byref(dims), _INPUTS_READY if inputs_ready else 0, err)
+    nb, hkv, d, dev, kp, vp, ks, vs = _f8_pools(k_codes, v_codes, k_scales, v_scales)
+    B, hq, dims, qp, bp, lp, err, out, op, wp, ws_bytes = _decode_common(q, nb, hkv, d, block_tables, context_lens, out,
+                                                                         workspace, error_word, dev)
+    rules = None
+    if softcap != 0 or window > 0 or alibi_slopes is not None or doc_starts is not None or prefix_lens is not None:
+        rules = ctypes.byref(_rules(softcap, window, alibi_slopes, doc_starts, prefix_lens, hq, B, B, dev))
+    _call("pkv_paged_decode_attention_f8", dev, stream, op, qp, kp, vp, ks, vs, bp, lp, scale, rules, wp, ws_bytes, dims,
+          _INPUTS_READY if inputs_ready else 0, err)
     return out
 
 
 def prefill_workspace_bytes(total_tokens, batch, num_q_heads, num_kv_heads, head_dim, num_blocks, max_blocks_per_seq) -> int:
     """Workspace of paged_prefill_attention for these sizes and at most total_tokens query rows."""
     dims = _dims(batch, num_q_heads, num_kv_heads, head_dim, num_blocks, max_blocks_per_seq)
-    n = int(load().pkv_prefill_workspace_bytes(ctypes.byref(dims), int(total_tokens)))
+    n = int(load().pkv_prefill_workspace_bytes(dims, int(total_tokens)))
     if n == 0:
         raise ValueError("invalid dims for paged prefill")
     return n
@@ -220,30 +237,24 @@ def paged_prefill_attention(q, k_cache, v_cache, block_tables, context_lens, que
     (int32 [B + 1]) are sequence b's last positions, context_lens [B] counts its keys with the step's own.
     The rules are those of paged_decode_attention_rules, doc_starts one int32 per packed row [T].  Returns
     out [T, Hq, d]; rows from query_starts[B] on are left as they were (unset when `out` is made here)."""
-    dev = k_cache.device if isinstance(k_cache, torch.Tensor) else None
-    kp = _need(k_cache, "k_cache", torch.bfloat16, 4)
-    vp = _need(v_cache, "v_cache", torch.bfloat16, 4, dev)
-    nb, hkv, bs, d = k_cache.shape
-    if v_cache.shape != k_cache.shape or bs != BLOCK_SIZE:
-        raise ValueError(f"pools must have one shape [num_blocks, num_kv_heads, {BLOCK_SIZE}, head_dim]")
+    nb, hkv, d, dev, kp, vp = _bf16_pools(k_cache, v_cache)
     qp = _need(q, "q", torch.bfloat16, 3, dev)
     bp = _need(block_tables, "block_tables", torch.int32, 2, dev)
     lp = _need(context_lens, "context_lens", torch.int32, 1, dev)
     sp = _need(query_starts, "query_starts", torch.int32, 1, dev)
     err = _opt(error_word, "error_word", torch.int32, 1, dev)
     T, hq, dq = q.shape
-    B = block_tables.shape[0]
+    B, mb = block_tables.shape
     if dq != d:
         raise ValueError("q head_dim differs from the pools'")
     if context_lens.shape[0] != B or query_starts.shape[0] != B + 1:
         raise ValueError("context_lens must be [B] and query_starts [B + 1]")
     rules = _rules(softcap, window, alibi_slopes, doc_starts, prefix_lens, hq, T, B, dev)
-    dims = _dims(B, hq, hkv, d, nb, block_tables.shape[1])
-    out = _give(out, "out", q.shape, torch.bfloat16, dev)
+    dims = _dims(B, hq, hkv, d, nb, mb)
+    out, op = _give(out, "out", (T, hq, d), torch.bfloat16, q, dev)
     if workspace is None:
-        workspace = torch.empty(int(load().pkv_prefill_workspace_bytes(ctypes.byref(dims), T)), dtype=torch.uint8, device=dev)
-    else:
-        _need(workspace, "workspace", torch.uint8, 1, dev)
-    _call("pkv_paged_prefill_attention", dev, stream, out.data_ptr(), qp, kp, vp, bp, lp, sp, T, float(scale),
-          ctypes.byref(rules), workspace.data_ptr(), workspace.numel(), ctypes.byref(dims), err)
+        workspace = torch.empty(int(load().pkv_prefill_workspace_bytes(dims, T)), dtype=torch.uint8, device=q.device)
+    wp = _need(workspace, "workspace", torch.uint8, 1, dev)
+    _call("pkv_paged_prefill_attention", dev, stream, op, qp, kp, vp, bp, lp, sp, T, scale, ctypes.byref(rules), wp,
+          workspace.numel(), dims, err)
     return out
