@@ -396,6 +396,7 @@ int decode_common(void* out, const void* q, const void* k_cache, const void* v_c
   const long long workers = (long long)grid * kDecodeWarps;
   a.workers = (int)workers;
   const int ring = (sparse && dims->head_dim == 128) ? PKV_RING_SPARSE_D128
+                   : f8 ? (dims->head_dim == 128 ? PKV_RING_F8_D128 : PKV_RING_F8_D64)
                    : q8 != nullptr ? (dims->head_dim == 128 ? PKV_RING_Q8_D128 : PKV_RING_Q8_D64)
                                    : (dims->head_dim == 128 ? PKV_RING_D128 : PKV_RING_D64);
   // Partition settings by form (kernels.h has the measurements): the bf16 decode and its
@@ -406,7 +407,7 @@ int decode_common(void* out, const void* q, const void* k_cache, const void* v_c
   const int busy_pct = sparse ? (q8 != nullptr ? PKV_MIN_BUSY_PCT_SPARSE_Q8 : PKV_MIN_BUSY_PCT_SPARSE)
                        : dense_q8 ? PKV_MIN_BUSY_PCT_Q8 : PKV_MIN_BUSY_PCT;
   a.min_busy_pct = std::min(std::max(busy_pct, 0), 100);
-  a.tail_pct = std::min(std::max(sparse ? PKV_TAIL_PCT_SPARSE : dense_q8 ? PKV_TAIL_PCT_Q8 : PKV_TAIL_PCT, 0), 50);
+  a.tail_pct = std::min(std::max(sparse ? PKV_TAIL_PCT_SPARSE : f8 ? PKV_TAIL_PCT_F8 : dense_q8 ? PKV_TAIL_PCT_Q8 : PKV_TAIL_PCT, 0), 50);
   a.chunk_min = std::max(dense_q8 ? PKV_CHUNK_MIN_Q8 : PKV_CHUNK_MIN, ring);  // never ends inside the tile ring
   a.cpw_cap = (int)std::min<long long>(std::min(PKV_MAX_TAIL_CHUNKS, kMaxTailChunksLimit),
                                        plan.ranges / workers - 1);

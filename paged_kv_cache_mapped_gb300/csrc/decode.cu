@@ -64,13 +64,14 @@ namespace pkv {
 namespace {
 
 // Q8: INT8 or FP8 pools, one byte per element; a tile is a single TMA box of 16 rows x D bytes.
-template <int D, bool SPARSE, bool Q8 = false>
+template <int D, bool SPARSE, bool Q8 = false, bool F8 = false>
 struct Geo {
   static constexpr int kRow = Q8 ? D : D * 2;              // bytes per K/V row in HBM
   static constexpr int kBoxes = Q8 ? 1 : D / 64;           // dense: 128-byte column boxes per row
   static constexpr int kTile = 16 * kRow;                  // bytes per tile
   static constexpr int kKSteps = D / 16;                   // k-steps of q.K, m-tiles of P.V
   static constexpr int kRing = (SPARSE && D == 128) ? PKV_RING_SPARSE_D128
+                               : F8 ? ((D == 128) ? PKV_RING_F8_D128 : PKV_RING_F8_D64)
                                : Q8 ? ((D == 128) ? PKV_RING_Q8_D128 : PKV_RING_Q8_D64)
                                     : ((D == 128) ? PKV_RING_D128 : PKV_RING_D64);
   static_assert((Q8 || kBoxes * 128 == kRow) && kRing >= 2, "head_dim must be a multiple of 64");
@@ -103,18 +104,18 @@ constexpr float kRescaleSlack = 8.0f;
 // factor, so P times scale / reference stays below 2^8 * 64 (inside fp16).
 constexpr float kVrefSlack = 64.0f;
 
-template <int D, bool SPARSE, bool Q8 = false>
+template <int D, bool SPARSE, bool Q8 = false, bool F8 = false>
 struct WarpTiles {
-  alignas(1024) unsigned char k[Geo<D, SPARSE, Q8>::kRing][Geo<D, SPARSE, Q8>::kTile];
-  alignas(1024) unsigned char v[Geo<D, SPARSE, Q8>::kRing][Geo<D, SPARSE, Q8>::kTile];
+  alignas(1024) unsigned char k[Geo<D, SPARSE, Q8, F8>::kRing][Geo<D, SPARSE, Q8, F8>::kTile];
+  alignas(1024) unsigned char v[Geo<D, SPARSE, Q8, F8>::kRing][Geo<D, SPARSE, Q8, F8>::kTile];
 };
 
-template <int D, bool SPARSE, bool Q8 = false>
+template <int D, bool SPARSE, bool Q8 = false, bool F8 = false>
 struct WarpSlots {
-  uint64_t bar_k[Geo<D, SPARSE, Q8>::kRing];  // K rows of the slot landed
-  uint64_t bar_v[Geo<D, SPARSE, Q8>::kRing];  // V rows of the slot landed
-  uint32_t meta[Geo<D, SPARSE, Q8>::kRing];   // rows of the unit that were copied (bit t = token t)
-  int32_t phys[Geo<D, SPARSE, Q8>::kRing];    // dense: physical block of the unit in the slot
+  uint64_t bar_k[Geo<D, SPARSE, Q8, F8>::kRing];  // K rows of the slot landed
+  uint64_t bar_v[Geo<D, SPARSE, Q8, F8>::kRing];  // V rows of the slot landed
+  uint32_t meta[Geo<D, SPARSE, Q8, F8>::kRing];   // rows of the unit that were copied (bit t = token t)
+  int32_t phys[Geo<D, SPARSE, Q8, F8>::kRing];    // dense: physical block of the unit in the slot
 };
 
 // INT8 pools: the row scales of the K and V tiles of each slot, copied with the K tile.
@@ -311,9 +312,9 @@ __global__ void __launch_bounds__(kDecodeWarps * 32, Q8 ? (F8 ? PKV_F8_MIN_CTAS 
 decode_split_kernel(const __grid_constant__ DecodeArgs a) {
   static_assert(!(SPARSE && SCORES), "scores are emitted by the dense decode only");
   static_assert(!(F8 && (SPARSE || SCORES || !Q8)) && !(RULES && (SPARSE || SCORES)), "dense decode only");
-  using GE = Geo<D, SPARSE, Q8>;
-  using WT = WarpTiles<D, SPARSE, Q8>;
-  using WB = WarpSlots<D, SPARSE, Q8>;
+  using GE = Geo<D, SPARSE, Q8, F8>;
+  using WT = WarpTiles<D, SPARSE, Q8, F8>;
+  using WB = WarpSlots<D, SPARSE, Q8, F8>;
   constexpr int R = GE::kRing;
   constexpr int KS = GE::kKSteps;
 

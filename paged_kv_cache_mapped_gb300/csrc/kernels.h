@@ -96,6 +96,13 @@ constexpr int kPartFields = kPartOff + kMaxTailChunksLimit + 1;
 #define PKV_RING_Q8_D64 4
 #endif
 
+#ifndef PKV_RING_F8_D128
+#define PKV_RING_F8_D128 2  // FP8 pools: the same (3 and 4 are no faster, 32 x ~4000 tokens: 49.1, 49.6, 50.5 us)
+#endif
+#ifndef PKV_RING_F8_D64
+#define PKV_RING_F8_D64 4
+#endif
+
 #ifndef PKV_RING_SPARSE_D128
 #define PKV_RING_SPARSE_D128 2  // gather form of the sparse decode (bf16 and INT8) at head_dim 128
 #endif
@@ -105,7 +112,7 @@ constexpr int kPartFields = kPartOff + kMaxTailChunksLimit + 1;
 #endif
 
 #ifndef PKV_F8_MIN_CTAS
-#define PKV_F8_MIN_CTAS 12  // FP8 decode: the same bound
+#define PKV_F8_MIN_CTAS 12  // FP8 decode: the same bound (14: 53.6 us against 49.1 for 32 x ~4000 tokens)
 #endif
 
 #ifndef PKV_MIN_UNITS
@@ -130,6 +137,11 @@ constexpr int kPartFields = kPartOff + kMaxTailChunksLimit + 1;
 // 7-unit chunk each).
 #ifndef PKV_TAIL_PCT_Q8
 #define PKV_TAIL_PCT_Q8 10
+#endif
+// FP8 pools: no tail at all (4 x 131072 tokens: 174.0 us with 10 %, 178.3 with 20 %, 170.4 without; 32 x ~4000:
+// 49.0, 52.8 and 49.0 us).
+#ifndef PKV_TAIL_PCT_F8
+#define PKV_TAIL_PCT_F8 0
 #endif
 #ifndef PKV_CHUNK_MIN_Q8
 #define PKV_CHUNK_MIN_Q8 6

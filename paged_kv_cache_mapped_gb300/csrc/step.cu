@@ -372,7 +372,7 @@ __device__ __forceinline__ void append_run(uint8_t* kq, uint8_t* vq, float* ks, 
 // D / 16 elements each; all rows of a run are loaded before any is used.  A CTA has a window of up to 32 tokens,
 // whose leaders times kv heads its warps share: with a window of 1 (few tokens) every run has its own CTA, with
 // 16 (prompts) a CTA has one or two runs of 16 tokens instead of 16 CTAs of which 15 end at once.  The bytes
-// bound it (16 prompts of ~4000, 8 heads, d 128, 388 MB: 288 -> @@ us).
+// bound it (16 prompts of ~4000, 8 heads, d 128, 388 MB: 288 -> 80.6 us, 71 % of the copy rate; three CTAs an SM spill and are no faster).
 constexpr int kAppendWarps = 8;
 
 template <int D>
