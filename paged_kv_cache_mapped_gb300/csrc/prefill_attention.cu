@@ -116,14 +116,14 @@ struct Geo {
 // The shares of split entries number at most 2 slots, which bounds the partial rows.  The list has the entries
 // with more than half of ktmax first, a sequence's last rows first within either part.
 struct Entry {
-  int b, tile, ntile, tokens, n, kt;
+  int b, tile, ntile, tokens, kt;
 };
 
-__device__ __forceinline__ Entry plan_entry(const PrefillAttnArgs& a, const int* base, int e, int per_item) {
+// seq: (queries, keys, prefix) of each sequence.
+__device__ __forceinline__ Entry plan_entry(const PrefillAttnArgs& a, const int* base, const int* seq, int e, int per_item) {
   Entry x;
   x.b = owner_of(base, a.B, e);
-  const PrefillSeq s = prefill_seq(a, x.b);
-  x.n = s.n;
+  const struct { int n, L, pre; } s = {seq[3 * x.b], seq[3 * x.b + 1], seq[3 * x.b + 2]};
   x.ntile = base[x.b + 1] - base[x.b];
   x.tile = x.ntile - 1 - (e - base[x.b]);
   x.tokens = min(s.n - x.tile * per_item, per_item);
@@ -135,10 +135,13 @@ __device__ __forceinline__ Entry plan_entry(const PrefillAttnArgs& a, const int*
   return x;
 }
 
+constexpr int kMaxShares = 64;     // of an entry
 constexpr int kPlanEntries = 512;  // entries kept in shared memory: the most that the first rule meets
 
 __global__ void __launch_bounds__(1024) prefill_plan_kernel(const PrefillAttnArgs a, int per_item) {
-  extern __shared__ int s_base[];  // [B + 1] first entry of each sequence
+  extern __shared__ int s_base[];  // [B + 1] first entry of each sequence, then [B] (queries, keys, prefix)
+  int* s_seq = s_base + a.B + 1;
+  __shared__ int s_split;
   __shared__ long long s_sum[34];
   __shared__ int s_kt[kPlanEntries];
   __shared__ int s_max;
@@ -146,6 +149,7 @@ __global__ void __launch_bounds__(1024) prefill_plan_kernel(const PrefillAttnArg
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, warps = blockDim.x >> 5;
   if (tid == 0) {
     s_max = 0;
+    s_split = 0;
     s_best = ~0ull;
     s_base[0] = 0;
   }
@@ -184,6 +188,9 @@ __global__ void __launch_bounds__(1024) prefill_plan_kernel(const PrefillAttnArg
       const PrefillSeq s = prefill_seq(a, base + tid);
       if (s.err != 0) record_error(a.err, s.err);
       ntile = (s.n + per_item - 1) / per_item;
+      s_seq[3 * (base + tid)] = s.n;
+      s_seq[3 * (base + tid) + 1] = s.L;
+      s_seq[3 * (base + tid) + 2] = s.pre;
     }
     const int at = carry + (int)scan(ntile);
     if (base + tid < a.B) s_base[base + tid + 1] = at + ntile;
@@ -194,7 +201,7 @@ __global__ void __launch_bounds__(1024) prefill_plan_kernel(const PrefillAttnArg
   long long work = 0;
   int most = 0;
   for (int e = tid; e < entries; e += blockDim.x) {
-    const int kt = plan_entry(a, s_base, e, per_item).kt;
+    const int kt = plan_entry(a, s_base, s_seq, e, per_item).kt;
     if (e < kPlanEntries) s_kt[e] = kt;
     work += kt;
     most = max(most, kt);
@@ -206,13 +213,13 @@ __global__ void __launch_bounds__(1024) prefill_plan_kernel(const PrefillAttnArg
   const int ktmax = max(s_max, 1);
   int chunk, tail = entries, tail_split = 1;
   if (P < a.slots && entries <= kPlanEntries) {
-    const int smax = P > 0 ? (int)min(64ll, 2 * a.slots / P) : 1;
-    for (int sp = warp + 1; sp <= smax; sp += warps) {
+    for (int sp = warp + 1; sp <= kMaxShares; sp += warps) {
       const int c = max(kMinChunk, (ktmax + sp - 1) / sp);
       int shares = 0;
       for (int e = lane; e < entries; e += 32) shares += max(1, (s_kt[e] + c - 1) / c);
       shares = __reduce_add_sync(kFullMask, shares);
       const long long items = (long long)shares * a.Hkv;
+      if (sp > 1 && (items > 2 * a.slots)) continue;
       long long end = c;
       if (items > a.slots) end = min(W / a.slots + c, (items + a.slots - 1) / a.slots * c);
       const unsigned long long cost = (unsigned long long)(end * 64 + (c < ktmax ? 32 : 0) + sp);
@@ -237,12 +244,12 @@ __global__ void __launch_bounds__(1024) prefill_plan_kernel(const PrefillAttnArg
   }
   auto shares_of = [&](int e, int kt) {
     if (e >= tail) return min(tail_split, max(1, kt / kMinChunk));
-    return max(1, (kt + chunk - 1) / chunk);
+    return min(kMaxShares, max(1, (kt + chunk - 1) / chunk));
   };
   // places in the list: the long entries' shares, then the others'; partial rows of the split ones
   long long first = 0;
   for (int e = tid; e < entries; e += blockDim.x) {
-    const int kt = e < kPlanEntries ? s_kt[e] : plan_entry(a, s_base, e, per_item).kt;
+    const int kt = e < kPlanEntries ? s_kt[e] : plan_entry(a, s_base, s_seq, e, per_item).kt;
     if (2 * kt > ktmax) first += shares_of(e, kt);
   }
   (void)scan(first);
@@ -253,7 +260,7 @@ __global__ void __launch_bounds__(1024) prefill_plan_kernel(const PrefillAttnArg
     Entry x{};
     int shares = 0, part = 1;
     if (e < entries) {
-      x = plan_entry(a, s_base, e, per_item);
+      x = plan_entry(a, s_base, s_seq, e, per_item);
       shares = shares_of(e, x.kt);
       part = 2 * x.kt > ktmax ? 0 : 1;
     }
@@ -263,16 +270,17 @@ __global__ void __launch_bounds__(1024) prefill_plan_kernel(const PrefillAttnArg
     row += s_sum[32];
     if (e < entries) {
       const long long item0 = at[part] + (part == 0 ? both >> 32 : both & 0xffffffffll);
-      a.plan_tiles[s_base[x.b] + x.tile] = make_int2(shares, (int)row0);
+      if (shares > 1) a.plan_split[atomicAdd(&s_split, 1)] = make_int4(x.b, x.tile, shares, (int)row0);
       for (int k = 0; k < shares; ++k) a.plan_items[item0 + k] = make_int4(x.b, x.tile, k | shares << 16, (int)row0);
     }
     at[0] += both_all >> 32;
     at[1] += both_all & 0xffffffffll;
   }
-  for (int b = tid; b < a.B; b += blockDim.x) a.plan_seq[b] = s_base[b];
+  __syncthreads();
   if (tid == 0) {
     a.plan_head[0] = (int)at[1];  // items
     a.plan_head[1] = 0;           // the ticket counter
+    a.plan_head[2] = s_split;     // split entries
   }
 }
 
@@ -347,11 +355,13 @@ struct Item {
   int ns;                 // steps of this share
 
   __device__ __forceinline__ int block_of(int e) const { return e < pre_units ? e : e + shift; }
-  // Key tiles run from the last one back, so that with a distance bias the nearest keys set the maximum.  Step t
-  // is half `half(t)` of the share's tile nt - 1 - order(t); the last tile may have its first half alone.
-  __device__ __forceinline__ int at(int t) const { return t + (ns & 1); }  // odd: the tile's last step
-  __device__ __forceinline__ int order(int t) const { return at(t) >> 1; }
-  __device__ __forceinline__ int half(int t) const { return t == 0 && (ns & 1) ? 0 : at(t) & 1; }
+};
+
+// Steps run from the last one back, so that with a distance bias the nearest keys set the maximum.  Row tile x
+// runs those from hi down to lo: later ones lie past its last row, earlier ones before its first interval.
+// Step j is half j & 1 of the share's tile j >> 1, which is the (nt - 1 - (j >> 1))-th to be loaded.
+struct Steps {
+  int hi, lo;
 };
 
 __device__ __forceinline__ Item load_item(const PrefillAttnArgs& a, int it, int NT) {
@@ -389,13 +399,21 @@ __device__ __forceinline__ void set_keys(Item& w, int lo_min) {
   w.ns = (min(w.nblk, (w.ts + w.nt) * kTileBlocks) - w.ts * kTileBlocks + kStepBlocks - 1) / kStepBlocks;
 }
 
+// lo_least: the least interval start of row tile x.
+__device__ __forceinline__ Steps steps_of(const PrefillAttnArgs& a, const Item& w, int x, int lo_least) {
+  const int e_base = w.ts * kTileBlocks;
+  const int i_last = w.pos0 + min(w.tokens, (x + 1) * a.R) - 1;
+  const int e_last = max((i_last >> 4) - w.shift, w.pre_units - 1), e_first = w.pre_units > 0 ? 0 : (lo_least >> 4) - w.shift;
+  return Steps{min(w.ns - 1, (e_last - e_base) >> 2), max(0, (e_first - e_base) >> 2)};
+}
+
 template <int D, int NT>
 struct Shared {
   uint64_t q_full, kv_full[Geo<D, NT>::kSlots], kv_empty[Geo<D, NT>::kSlots];
   uint64_t s_full[NT][2], p_full[NT][2], pv_done[NT][2];  // by buffer: S ready, P ready, P V added
   uint64_t drained[NT];  // after a timeout: the MMAs issued have ended
   uint32_t tmem;
-  int lo_min, lo_max[NT], abort, next;
+  int lo_least[NT], lo_most[NT], abort, next;  // interval starts of the row tiles' rows
 };
 
 // Loads the item's Q tiles and its K and V tiles through the ring (one warp).  n_kv counts K and V tiles
@@ -503,65 +521,73 @@ __device__ __forceinline__ void issue_mmas(const PrefillAttnArgs& a, Shared<D, N
   auto wait_kv = [&](uint32_t c) { return wait(&sh.kv_full[c % NS], c / NS); };
   n_kv = kv_base + 2 * w.nt;
   bool ok = true;
-  if (y >= w.nx) {
-    for (uint32_t c = kv_base; c < kv_base + 2 * (uint32_t)w.nt && ok; ++c) {
-      ok = wait_kv(c);
-      if (ok) free_tile(c);
+  const int nt = (int)uniform((uint32_t)w.nt);
+  const Steps range = y < w.nx ? steps_of(a, w, y, sh.lo_least[y]) : Steps{-1, 0};
+  const int hi = (int)uniform((uint32_t)range.hi), lo = (int)uniform((uint32_t)range.lo);
+  auto pass = [&](int from, int to) {  // the loads [from, to) that this row tile does not read
+    for (int c = 2 * from; c < 2 * to && ok; ++c) {
+      ok = wait_kv(kv_base + c);
+      if (ok) free_tile(kv_base + c);
     }
+  };
+  if (hi < lo) {
+    pass(0, nt);
     return;
   }
-  const int ns = (int)uniform((uint32_t)w.ns), odd = ns & 1;  // (Item::at and half, of uniform values)
   const bool two = uniform((uint32_t)w.nt_all) <= (uint32_t)kTwoTermTiles;
   const uint32_t step0 = uniform(n_step);
   const uint32_t s0 = uniform(tmem_any) + y * 2 * kStep, o = uniform(tmem_any) + NT * 2 * kStep + y * D;
   constexpr uint32_t kTile16 = GE::kTile / 16, kStep16 = kStep * 128 / 16;  // descriptors count 16 bytes
   const uint32_t qa = umma_lo_k(base) + y * kTile16, k0 = umma_lo_k(base + NT * GE::kTile);
   const uint32_t v0 = umma_lo_mn(base + NT * GE::kTile, kHalf);
-  // S of step t, with its tile's K awaited before the first step and freed after the last
-  auto qk = [&](int t) {
-    const uint32_t buf = (step0 + (uint32_t)t) & 1u, u = (uint32_t)(t + odd), tile = kv_base + (u & ~1u);
-    if ((t == 0 || (u & 1u) == 0) && !wait_kv(tile)) return false;
-    if (t == 0) tc_fence_after();
-    const uint32_t kb = k0 + (tile % NS) * kTile16 + (t == 0 && odd ? 0 : (u & 1u) * kStep16);
+  // S of step j, with its tile's K awaited before the first step and freed after the last
+  auto qk = [&](int j) {
+    const uint32_t buf = (step0 + (uint32_t)(hi - j)) & 1u, tile = kv_base + 2u * (uint32_t)(nt - 1 - (j >> 1));
+    if ((j == hi || (j & 1)) && !wait_kv(tile)) return false;
+    if (j == hi) tc_fence_after();
+    const uint32_t kb = k0 + (tile % NS) * kTile16 + (j & 1) * kStep16;
 #pragma unroll
     for (int k = 0; k < D / 16; ++k) {
       const uint32_t off = (uint32_t)((k >> 2) * kHalf + (k & 3) * 32) / 16;
       umma_bf16_lo(leader, s0 + buf * kStep, qa + off, kb + off, id_qk, k > 0);
     }
     umma_commit_by(leader, bars + (uint32_t)offsetof(SH, s_full) + (y * 2 + buf) * 8);
-    if (u & 1u) free_tile(tile);
+    if (!(j & 1) || j == lo) free_tile(tile);
     return true;
   };
-  auto pv = [&](int t) {
-    const uint32_t buf = (step0 + (uint32_t)t) & 1u, u = (uint32_t)(t + odd), tile = kv_base + (u | 1u);
-    const uint32_t vb = v0 + (tile % NS) * kTile16 + (t == 0 && odd ? 0 : (u & 1u) * kStep16);
+  auto pv = [&](int j) {
+    const uint32_t buf = (step0 + (uint32_t)(hi - j)) & 1u, tile = kv_base + 2u * (uint32_t)(nt - 1 - (j >> 1)) + 1u;
+    const uint32_t vb = v0 + (tile % NS) * kTile16 + (j & 1) * kStep16;
     const uint32_t p = s0 + buf * kStep;
 #pragma unroll
     for (int k = 0; k < kStep / 16; ++k)  // 32 keys' first terms, then their remainders, 16 columns each
-      umma_bf16_ts_lo(leader, o, p + 32 * (k >> 1) + 8 * (k & 1), vb + k * 128, id_pv, k > 0 || t > 0);
+      umma_bf16_ts_lo(leader, o, p + 32 * (k >> 1) + 8 * (k & 1), vb + k * 128, id_pv, k > 0 || j < hi);
     if (two) {
 #pragma unroll
       for (int k = 0; k < kStep / 16; ++k)
         umma_bf16_ts_lo(leader, o, p + 32 * (k >> 1) + 16 + 8 * (k & 1), vb + k * 128, id_pv, true);
     }
     umma_commit_by(leader, bars + (uint32_t)offsetof(SH, pv_done) + (y * 2 + buf) * 8);
-    if (u & 1u) free_tile(tile);
+    if (!(j & 1) || j == lo) free_tile(tile);
   };
-  ok = wait(&sh.q_full, n_q) && qk(0) && (ns < 2 || qk(1));
-  for (int t = 0; t < ns && ok; ++t) {
-    const uint32_t c = step0 + (uint32_t)t, u = (uint32_t)(t + odd);
-    ok = (t > 0 && (u & 1u)) || wait_kv(kv_base + (u | 1u));  // V of a tile's first step
+  ok = wait(&sh.q_full, n_q);
+  pass(0, nt - 1 - (hi >> 1));
+  ok = ok && qk(hi) && (hi - 1 < lo || qk(hi - 1));
+  for (int j = hi; j >= lo && ok; --j) {
+    const uint32_t c = step0 + (uint32_t)(hi - j);
+    if (j == hi || (j & 1)) ok = wait_kv(kv_base + 2u * (uint32_t)(nt - 1 - (j >> 1)) + 1u);
     ok = ok && wait(&sh.p_full[y][c & 1u], c >> 1);
     if (!ok) break;
     tc_fence_after();
-    pv(t);
-    if (t + 2 < ns) ok = qk(t + 2);
+    pv(j);
+    if (j - 2 >= lo) ok = qk(j - 2);
   }
+  pass(nt - (lo >> 1), nt);
   if (!ok) {  // the MMAs in flight end before tensor memory goes
     umma_commit_by(leader, bars + (uint32_t)offsetof(SH, drained) + y * 8);
     (void)mbar_wait_spin(&sh.drained[y], 0, a.timeout_ns);
   }
-  n_step = step0 + ns;
+  n_step = step0 + (uint32_t)(hi - lo + 1);
 }
 
 // Largest of N values (of their sizes when ABS), in four chains of three-operand maxima.
@@ -715,10 +741,11 @@ __device__ __forceinline__ void softmax_rows(const PrefillAttnArgs& a, Shared<D,
   const float ku = a.scale_log2 * a.cap_in * 0.34657359f, ku_size = a.cap_log2 > 0.f ? fabsf(ku) : 0.f;
   const float cap0 = a.cap_log2 * ku, cap1 = -0.33333333f * cap0 * ku * ku, cap2 = 0.13333333f * cap0 * ku * ku * ku * ku;
   const bool own_logits = a.cap_log2 > 0.f || a.slopes != nullptr || !(a.scale_log2 > 0.f);
+  const Steps range = steps_of(a, w, x, sh.lo_least[x]);
   // steps whose keys all rows of the row tile see: a range of the interval's part of the list, and one of the
   // prefix's.  The list's position of entry e is 16 (e + shift) there.
   const int e_base = w.ts * kTileBlocks;
-  int full0 = (max(w.pre_units, ((sh.lo_max[x] + 15) >> 4) - w.shift) - e_base + kStepBlocks - 1) >> 2;
+  int full0 = (max(w.pre_units, ((sh.lo_most[x] + 15) >> 4) - w.shift) - e_base + kStepBlocks - 1) >> 2;
   const int full1 = (((w.pos0 + x * a.R + 1) >> 4) - w.shift - e_base) >> 2;  // whole blocks up to the first row's position
   full0 = max(full0, 0);
   const int full_pre = ((w.pre >> 4) - e_base) >> 2;
@@ -733,7 +760,7 @@ __device__ __forceinline__ void softmax_rows(const PrefillAttnArgs& a, Shared<D,
   const uint32_t to_addr = t_lane + NT * 2 * kStep + x * D;
   bool ok = true;
   float m = -INFINITY, l = 0.f;
-  for (int j = 0; j < w.ns; ++j) {
+  for (int j = range.hi; j >= range.lo; --j) {
     const uint32_t buf = n_step & 1u;
     const uint32_t ts_addr = t_lane + x * 2 * kStep + buf * kStep;
     ok = __all_sync(kFullMask, mbar_wait_spin(&sh.s_full[x][buf], (n_step >> 1) & 1u, a.timeout_ns));
@@ -743,9 +770,8 @@ __device__ __forceinline__ void softmax_rows(const PrefillAttnArgs& a, Shared<D,
 #pragma unroll
     for (int c = 0; c < N / 32; ++c) tmem_ld_x32(ts_addr + 32 * c, *reinterpret_cast<float(*)[32]>(v + 32 * c));
     tmem_wait_ld();
-    const int js = 2 * (w.nt - 1 - w.order(j)) + w.half(j);  // the step's place in the share's list
-    const int e0 = e_base + js * kStepBlocks;
-    const bool full = (js >= full0 && js < full1) || js < full_pre;
+    const int e0 = e_base + j * kStepBlocks;
+    const bool full = (j >= full0 && j < full1) || j < full_pre;
     // Steps without a mask take one pass over the row.  With a cap or a bias, the products' largest size bounds
     // the logits: the step's nearest key lies within twice that below the bound, so where that is 2^80 or less
     // the bound serves as the maximum (the weights stay within fp32 and bf16 range), and the cap and the bias
@@ -763,7 +789,7 @@ __device__ __forceinline__ void softmax_rows(const PrefillAttnArgs& a, Shared<D,
         base = -slope2 * (float)(i - w.block_of(e0) * 16);
         mx += fmaxf(base, fmaf(slope2, (float)(kStep - 1), base));
       }
-      fast = __all_sync(kFullMask, 2.f * size <= 80.f && far * ku_size < 0.11f && (slope2 == 0.f || js >= full_pre));
+      fast = __all_sync(kFullMask, 2.f * size <= 80.f && far * ku_size < 0.11f && (slope2 == 0.f || j >= full_pre));
     }
     if (!fast) {
       if (own_logits) y = apply_rules(a, v, slope2, i, w, e0);
@@ -796,7 +822,7 @@ __device__ __forceinline__ void softmax_rows(const PrefillAttnArgs& a, Shared<D,
       const float scale = move ? ex2_approx(m - mx) : 1.f;
       if (move) m = mx;
       l *= scale;
-      if (j > 0) {  // O moves to the new reference once the last product has ended
+      if (j < range.hi) {  // O moves to the new reference once the last product has ended
         ok = __all_sync(kFullMask, mbar_wait_spin(&sh.pv_done[x][(n_step - 1) & 1u], ((n_step - 1) >> 1) & 1u, a.timeout_ns));
         if (!ok) break;
         tc_fence_after();
@@ -862,8 +888,8 @@ __device__ __forceinline__ void softmax_rows(const PrefillAttnArgs& a, Shared<D,
       const float2 sum = unpack2(fadd2(fadd2(sum2[0], sum2[1]), fadd2(sum2[2], sum2[3])));
       l += sum.x + sum.y;
     }
-    if (js == tail_step) {
-      const uint32_t vtile = n_kv + 2 * w.order(j) + 1;  // this tile's V in the count of K and V tiles
+    if (j == tail_step) {
+      const uint32_t vtile = n_kv + 2 * (w.nt - 1 - (j >> 1)) + 1;  // this tile's V in the count of K and V tiles
       ok = __all_sync(kFullMask, mbar_wait_spin(&sh.kv_full[vtile % NS], (vtile / NS) & 1u, a.timeout_ns));
       if (!ok) break;
       unsigned char* rows = skv + (vtile % NS) * GE::kTile + (e_last % kTileBlocks) * 2048;
@@ -879,7 +905,8 @@ __device__ __forceinline__ void softmax_rows(const PrefillAttnArgs& a, Shared<D,
     if (lane == 0) mbar_arrive(&sh.p_full[x][buf]);
     ++n_step;
   }
-  if (ok && w.ns > 0) {
+  const bool some = range.hi >= range.lo;
+  if (ok && some) {
     ok = __all_sync(kFullMask, mbar_wait_spin(&sh.pv_done[x][(n_step - 1) & 1u], ((n_step - 1) >> 1) & 1u, a.timeout_ns));
     tc_fence_after();
   }
@@ -900,13 +927,13 @@ __device__ __forceinline__ void softmax_rows(const PrefillAttnArgs& a, Shared<D,
   for (int c = 0; c < D / 16; ++c) {
     float o[16];
     __syncwarp();
-    if (w.ns > 0) {
+    if (some) {
       tmem_ld_x16(to_addr + 16 * c, o);
       tmem_wait_ld();
     }
 #pragma unroll
     for (int k = 0; k < 16; ++k) {
-      o[k] = w.ns > 0 ? o[k] * f : 0.f;
+      o[k] = some ? o[k] * f : 0.f;
       bad |= !(fabsf(o[k]) <= 3.4028234e38f);
     }
     if (valid && split) {
@@ -991,22 +1018,24 @@ prefill_attention_kernel(const __grid_constant__ PrefillAttnArgs a) {
     for (int it = blockIdx.x; it < total; it = sh.next) {
       Item w = load_item(a, it, NT);
       if (threadIdx.x == 0) {
-        sh.lo_min = 0x7fffffff;
-        for (int y = 0; y < NT; ++y) sh.lo_max[y] = 0;
+        for (int y = 0; y < NT; ++y) {
+          sh.lo_least[y] = 0x7fffffff;
+          sh.lo_most[y] = 0;
+        }
       }
       __syncthreads();
       const bool valid = tok < a.R && x * a.R + tok < w.tokens;
       const int prow = w.q0 + w.tok0 + x * a.R + tok;
       const int i = valid ? w.pos0 + x * a.R + tok : -1;
       const int lo = valid ? interval_start(a, prow, i) : 0;
-      const int lo_min = __reduce_min_sync(kFullMask, valid ? lo : 0x7fffffff);
-      const int lo_max = __reduce_max_sync(kFullMask, lo);
+      const int least = __reduce_min_sync(kFullMask, valid ? lo : 0x7fffffff);
+      const int most = __reduce_max_sync(kFullMask, lo);
       if (lane == 0) {
-        atomicMin(&sh.lo_min, lo_min);
-        atomicMax(&sh.lo_max[x], lo_max);
+        atomicMin(&sh.lo_least[x], least);
+        atomicMax(&sh.lo_most[x], most);
       }
       __syncthreads();
-      set_keys(w, sh.lo_min);
+      set_keys(w, min(sh.lo_least[0], sh.lo_least[NT - 1]));
       if (x < w.nx)
         softmax_rows<D, NT>(a, sh, w, sq, tmem, x, r, valid, i, lo, prow, w.g * a.G + head, n_kv, n_step);
       n_kv += 2 * w.nt;
@@ -1022,7 +1051,7 @@ prefill_attention_kernel(const __grid_constant__ PrefillAttnArgs a) {
       Item w = load_item(a, it, NT);
       __syncthreads();
       __syncthreads();
-      set_keys(w, sh.lo_min);
+      set_keys(w, min(sh.lo_least[0], sh.lo_least[NT - 1]));
       if (w.nt > 0) {
         if (warp == GE::kSoftmaxWarps) {
           produce<D, NT>(a, sh, w, sq, n_kv, n_q);
@@ -1046,40 +1075,64 @@ prefill_attention_kernel(const __grid_constant__ PrefillAttnArgs a) {
 
 // ------------------------------------------------------------------------------------ the merge
 
+// A warp a row of a split entry: lane k has the (maximum, sum) of shares k and k + 32, then the rows of all
+// shares are added, four loads in flight.
 template <int D>
 __global__ void __launch_bounds__(256) prefill_merge_kernel(const PrefillAttnArgs a, int per_item) {
   constexpr int E = D / 32;
   const int lane = threadIdx.x & 31;
   grid_dependency_wait();
   grid_launch_dependents();
-  const long long rows = (long long)a.T * a.Hq;
+  const int per_entry = per_item * a.Hq;
+  const long long rows = (long long)a.plan_head[2] * per_entry;
   for (long long row = ((long long)blockIdx.x * blockDim.x + threadIdx.x) >> 5; row < rows;
        row += ((long long)gridDim.x * blockDim.x) >> 5) {
-    const int r = (int)(row / a.Hq);
-    const int b = owner_of(a.query_starts, a.B, r);
-    const PrefillSeq s = prefill_seq(a, b);
-    if (r < s.q0 || r >= s.q0 + s.n) continue;
-    const int tile = (r - s.q0) / per_item;
-    const int2 plan = a.plan_tiles[a.plan_seq[b] + tile];
-    if (plan.x <= 1) continue;
-    const long long per = (long long)min(s.n - tile * per_item, per_item) * a.Hq;
-    const long long p0 = plan.y + (long long)(r - s.q0 - tile * per_item) * a.Hq + (row - (long long)r * a.Hq);
+    const int k = (int)(row / per_entry), in = (int)(row - (long long)k * per_entry);
+    const int4 split = a.plan_split[k];  // (sequence, row tile group, shares, first partial row)
+    const PrefillSeq s = prefill_seq(a, split.x);
+    const int tok0 = split.y * per_item, per = min(s.n - tok0, per_item) * a.Hq;
+    if (in >= per) continue;
+    const long long p0 = (long long)split.w + in;
+    float2 ml[2];
     float m = -INFINITY;
-    for (int k = 0; k < plan.x; ++k) m = fmaxf(m, a.part_ml[p0 + k * per].x);
-    float l = 0.f, o[E] = {};
-    if (m > -INFINITY) {
-      for (int k = 0; k < plan.x; ++k) {
-        const float2 ml = a.part_ml[p0 + k * per];
-        if (ml.x == -INFINITY && ml.y == 0.f) continue;  // a share that saw nothing
-        const float w = exp2f(ml.x - m);
-        l += w * ml.y;
 #pragma unroll
-        for (int e = 0; e < E; ++e) o[e] += w * a.part_o[(p0 + k * per) * D + lane * E + e];
+    for (int q = 0; q < 2; ++q) {
+      const int sh = lane + 32 * q;
+      ml[q] = sh < split.z ? __ldcg(a.part_ml + p0 + (long long)sh * per) : make_float2(-INFINITY, 0.f);
+      m = fmaxf(m, ml[q].x);
+    }
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(kFullMask, m, o));
+    const float ref = m == -INFINITY ? 0.f : m;
+    float w[2], l = 0.f;
+#pragma unroll
+    for (int q = 0; q < 2; ++q) {
+      w[q] = exp2f(ml[q].x - ref);  // 0 for a share that saw nothing
+      l += w[q] * ml[q].y;
+    }
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) l += __shfl_xor_sync(kFullMask, l, o);
+    float o[E] = {};
+#pragma unroll 4
+    for (int sh = 0; sh < split.z; ++sh) {
+      const float f = __shfl_sync(kFullMask, sh < 32 ? w[0] : w[1], sh & 31);
+      const float* src = a.part_o + (p0 + (long long)sh * per) * D + lane * E;
+      float x[E];
+      if constexpr (E == 4) {
+        const float4 t = __ldcg(reinterpret_cast<const float4*>(src));
+        x[0] = t.x; x[1] = t.y; x[2] = t.z; x[3] = t.w;
+      } else {
+        const float2 t = __ldcg(reinterpret_cast<const float2*>(src));
+        x[0] = t.x; x[1] = t.y;
       }
+#pragma unroll
+      for (int e = 0; e < E; ++e) o[e] = f == 0.f ? o[e] : fmaf(f, x[e], o[e]);
     }
     const float inv = l > 0.f ? 1.f / l : (l == l ? 0.f : l);
+    __nv_bfloat16* dst = a.out + ((long long)(s.q0 + tok0) * a.Hq + in) * D + lane * E;
 #pragma unroll
-    for (int e = 0; e < E; ++e) a.out[row * D + lane * E + e] = __float2bfloat16_rn(o[e] * inv);
+    for (int e = 0; e < E; e += 2)
+      *reinterpret_cast<uint32_t*>(dst + e) = pack_bf16x2(o[e] * inv, o[e + 1] * inv);
   }
 }
 
@@ -1091,23 +1144,24 @@ constexpr long long kMaxPartRows = 2ll * kMaxSms * 256;  // rows of 2 slots shar
 size_t align256p(size_t x) { return (x + 255) & ~size_t(255); }
 
 struct PrefillWorkspace {
-  size_t items, tiles, seq, ml, o, total;
+  size_t items, split, ml, o, total;
 };
 
-// head | int4 items | int2 per entry | int per sequence | float2 (m, l) | float o.  Entries: at most one per 128
-// rows, and one more per sequence; items: those and the shares of split ones.
+// head | int4 items | int4 split entries | float2 (m, l) | float o.  Entries: at most one per 128 rows, and one
+// more per sequence; items: those and the shares of split ones.
 PrefillWorkspace plan_prefill(long long B, long long T, int Hq, int G, int D) {
   PrefillWorkspace w{};
   const long long entries = T / (128 / G) + B;
-  const long long rows = std::min(kMaxPartRows, T * Hq * 64);  // an entry has at most 64 shares
+  const long long rows = std::min(kMaxPartRows, T * Hq * kMaxShares);
   w.items = 256;
-  w.tiles = align256p(w.items + sizeof(int4) * (size_t)(entries + 4 * kMaxSms));
-  w.seq = align256p(w.tiles + sizeof(int2) * (size_t)entries);
-  w.ml = align256p(w.seq + sizeof(int) * (size_t)B);
+  w.split = align256p(w.items + sizeof(int4) * (size_t)(entries + 4 * kMaxSms));
+  w.ml = align256p(w.split + sizeof(int4) * (size_t)std::min<long long>(entries, 4 * kMaxSms));
   w.o = align256p(w.ml + sizeof(float2) * (size_t)rows);
   w.total = align256p(w.o + sizeof(float) * (size_t)rows * D);
   return w;
 }
+
+size_t plan_smem_bytes(int B) { return sizeof(int) * (4 * (size_t)B + 1); }
 
 template <int D, int NT>
 cudaError_t launch_attention(const PrefillAttnArgs& a, cudaStream_t stream) {
@@ -1117,7 +1171,7 @@ cudaError_t launch_attention(const PrefillAttnArgs& a, cudaStream_t stream) {
   int per_item = NT * a.R;
   void* plan_params[] = {&args, &per_item};
   cudaError_t e = launch_pdl((const void*)prefill_plan_kernel, dim3(1),
-                             dim3(a.B > 256 || a.T > 16384 ? 1024 : 256), sizeof(int) * ((size_t)a.B + 1), stream, plan_params);
+                             dim3(a.B > 256 || a.T > 16384 ? 1024 : 256), plan_smem_bytes(a.B), stream, plan_params);
   if (e != cudaSuccess) return e;
   void* params[] = {&args};
   const long long most = ((long long)a.T / per_item + a.B) * a.Hkv + 2 * args.slots;
@@ -1138,7 +1192,9 @@ cudaError_t setup_attention() {
 size_t prefill_attention_workspace(int B, int T, int Hq, int G, int D) { return plan_prefill(B, T, Hq, G, D).total; }
 
 cudaError_t prefill_attention_device_setup() {
-  cudaError_t e = setup_attention<128, 1>();
+  cudaError_t e = cudaFuncSetAttribute((const void*)prefill_plan_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                       (int)plan_smem_bytes(kMaxStepBatch));
+  if (e == cudaSuccess) e = setup_attention<128, 1>();
   if (e == cudaSuccess) e = setup_attention<128, 2>();
   if (e == cudaSuccess) e = setup_attention<64, 1>();
   if (e == cudaSuccess) e = setup_attention<64, 2>();
@@ -1151,12 +1207,12 @@ cudaError_t launch_prefill_attention(const PrefillAttnArgs& a, void* workspace, 
   unsigned char* ws = static_cast<unsigned char*>(workspace);
   args.plan_head = reinterpret_cast<int*>(ws);
   args.plan_items = reinterpret_cast<int4*>(ws + w.items);
-  args.plan_tiles = reinterpret_cast<int2*>(ws + w.tiles);
-  args.plan_seq = reinterpret_cast<int*>(ws + w.seq);
+  args.plan_split = reinterpret_cast<int4*>(ws + w.split);
   args.part_ml = reinterpret_cast<float2*>(ws + w.ml);
   args.part_o = reinterpret_cast<float*>(ws + w.o);
-  // two row tiles an item when the sequences fill more than one on average
-  const bool two = (long long)a.T > (long long)a.B * a.R;
+  // two row tiles an item when the sequences fill more than one on average and the row tiles would not all run
+  // at once by themselves
+  const bool two = (long long)a.T > (long long)a.B * a.R && (long long)a.T / a.R * a.Hkv >= 2 * a.sms;
   if (head_dim == 128) return two ? launch_attention<128, 2>(args, stream) : launch_attention<128, 1>(args, stream);
   return two ? launch_attention<64, 2>(args, stream) : launch_attention<64, 1>(args, stream);
 }
