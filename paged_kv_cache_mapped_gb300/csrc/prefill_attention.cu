@@ -89,8 +89,10 @@ struct Geo {
   static constexpr int kHalves = D / 64;
   static constexpr int kTile = kHalves * kHalf;  // bytes of a Q, K or V tile
   static constexpr int kSlots = NT == 2 ? (D == 128 ? 4 : 8) : (D == 128 ? 2 : 5);
-  static constexpr int kSoftmaxWarps = NT * 4;           // a row a thread
-  static constexpr int kThreads = NT * 128 + 128;        // and producer, issuers, idle warps
+  static constexpr int kSoftmaxWarps = NT * 4;  // a row a thread
+  // and a producer, two issuers (one for each row tile, or for each product of the one), the ticket taker
+  static constexpr int kThreads = NT * 128 + 128;
+  static constexpr int kProducer = kSoftmaxWarps, kIssuer = kProducer + 1, kTicket = kIssuer + 2;
   static constexpr int kCtas = NT == 1 ? 2 : 1;  // per SM (shared and tensor memory allow no more)
   // Registers a thread: a launch gives every warp the same, which the softmax warps (their logits are in
   // registers) then take from the others.  NT = 2: 384 x 168 = 256 x 216 + 128 x 72; NT = 1 (two CTAs):
@@ -411,7 +413,7 @@ template <int D, int NT>
 struct Shared {
   uint64_t q_full, kv_full[Geo<D, NT>::kSlots], kv_empty[Geo<D, NT>::kSlots];
   uint64_t s_full[NT][2], p_full[NT][2], pv_done[NT][2];  // by buffer: S ready, P ready, P V added
-  uint64_t drained[NT];  // after a timeout: the MMAs issued have ended
+  uint64_t drained[2];  // after a timeout: an issuer's MMAs have ended
   uint32_t tmem;
   int lo_least[NT], lo_most[NT], abort, next;  // interval starts of the row tiles' rows
 };
@@ -492,13 +494,17 @@ __device__ __forceinline__ void produce(const PrefillAttnArgs& a, Shared<D, NT>&
   }
 }
 
-// Issues the MMAs of the item's row tile y (a warp for each row tile, its elected lane; what the MMAs take is the
-// same in every lane and kept in uniform registers).  S has two buffers of 64 keys in tensor memory, and P
-// takes the place of its S: while the softmax works on step t, S of step t + 1 is there.  Per step: O += P V
-// once P is ready, then S = Q K^T of two steps on into the same columns (the tensor core runs one thread's
-// MMAs in the order of issue).  With a warp for each row tile, what one spends on its barriers passes under the
-// other's MMAs.  A ring tile is free once both have read it; a row tile that the item does not have only says so.
-template <int D, int NT>
+// Issues MMAs of the item's row tile y: QK the products S = Q K^T, PV the products O += P V (a warp's elected
+// lane; what the MMAs take is the same in every lane and kept in uniform registers).  S has two buffers of 64
+// keys in tensor memory, and P takes the place of its S: while the softmax works on a step, S of the next one
+// is there, and that of the step after follows the product that reads P from its columns (the tensor core runs
+// one thread's MMAs in the order of issue).
+// Beside the softmax warps a thread needs 60 to 120 cycles an MMA and a hundred or more for each barrier: one
+// issuer for two row tiles leaves the tensor core idle (chunk of 4096 on 16384, plain, 1.07 ms; one for each
+// 0.92; one for each product of each 0.75 against 0.72, its warps taking issue slots from the softmax).  With
+// one row tile and two CTAs an SM the products have an issuer each (64 tokens on 2000 keys each: 129 -> 112 us).
+// A ring tile is free once both row tiles have read it; a row tile that does not read it only says so.
+template <int D, int NT, bool QK, bool PV>
 __device__ __forceinline__ void issue_mmas(const PrefillAttnArgs& a, Shared<D, NT>& sh, const Item& w, unsigned char* sq,
                                            uint32_t tmem_any, uint32_t leader, int y, uint32_t& n_kv, uint32_t n_q,
                                            uint32_t& n_step) {
@@ -508,7 +514,7 @@ __device__ __forceinline__ void issue_mmas(const PrefillAttnArgs& a, Shared<D, N
   constexpr uint32_t id_qk = umma_idesc_bf16(128, kStep), id_pv = umma_idesc_bf16_bmn(128, D);
   auto uniform = [](uint32_t v) { return __shfl_sync(kFullMask, v, 0); };
   const uint32_t base = uniform(smem_u32(sq)), bars = uniform(smem_u32(&sh));
-  const uint32_t kv_base = uniform(n_kv);  // K of tile t is tile kv_base + 2 t of the ring, V the next
+  const uint32_t kv_base = uniform(n_kv);  // K of the i-th tile loaded is tile kv_base + 2 i of the ring, V the next
   auto free_tile = [&](uint32_t c) { umma_commit_by(leader, bars + (uint32_t)offsetof(SH, kv_empty) + (c % NS) * 8); };
   auto wait = [&](uint64_t* bar, uint32_t phase) {
     if (__all_sync(kFullMask, mbar_wait_spin(bar, phase & 1u, a.timeout_ns))) return true;
@@ -525,10 +531,11 @@ __device__ __forceinline__ void issue_mmas(const PrefillAttnArgs& a, Shared<D, N
   const Steps range = y < w.nx ? steps_of(a, w, y, sh.lo_least[y]) : Steps{-1, 0};
   const int hi = (int)uniform((uint32_t)range.hi), lo = (int)uniform((uint32_t)range.lo);
   auto pass = [&](int from, int to) {  // the loads [from, to) that this row tile does not read
-    for (int c = 2 * from; c < 2 * to && ok; ++c) {
-      ok = wait_kv(kv_base + c);
-      if (ok) free_tile(kv_base + c);
-    }
+    for (int i = from; i < to && ok; ++i)
+      for (int v = QK ? 0 : 1; v < (PV ? 2 : 1) && ok; ++v) {
+        ok = wait_kv(kv_base + 2 * i + v);
+        if (ok) free_tile(kv_base + 2 * i + v);
+      }
   };
   if (hi < lo) {
     pass(0, nt);
@@ -540,23 +547,21 @@ __device__ __forceinline__ void issue_mmas(const PrefillAttnArgs& a, Shared<D, N
   constexpr uint32_t kTile16 = GE::kTile / 16, kStep16 = kStep * 128 / 16;  // descriptors count 16 bytes
   const uint32_t qa = umma_lo_k(base) + y * kTile16, k0 = umma_lo_k(base + NT * GE::kTile);
   const uint32_t v0 = umma_lo_mn(base + NT * GE::kTile, kHalf);
-  // S of step j, with its tile's K awaited before the first step and freed after the last
+  auto k_tile = [&](int j) { return kv_base + 2u * (uint32_t)(nt - 1 - (j >> 1)); };
+  // S of step j; its tile's K is awaited before the tile's first step and freed after the last
+  auto wait_k = [&](int j) { return (j != hi && !(j & 1)) || wait_kv(k_tile(j)); };
   auto qk = [&](int j) {
-    const uint32_t buf = (step0 + (uint32_t)(hi - j)) & 1u, tile = kv_base + 2u * (uint32_t)(nt - 1 - (j >> 1));
-    if ((j == hi || (j & 1)) && !wait_kv(tile)) return false;
-    if (j == hi) tc_fence_after();
-    const uint32_t kb = k0 + (tile % NS) * kTile16 + (j & 1) * kStep16;
+    const uint32_t buf = (step0 + (uint32_t)(hi - j)) & 1u, kb = k0 + (k_tile(j) % NS) * kTile16 + (j & 1) * kStep16;
 #pragma unroll
     for (int k = 0; k < D / 16; ++k) {
       const uint32_t off = (uint32_t)((k >> 2) * kHalf + (k & 3) * 32) / 16;
       umma_bf16_lo(leader, s0 + buf * kStep, qa + off, kb + off, id_qk, k > 0);
     }
     umma_commit_by(leader, bars + (uint32_t)offsetof(SH, s_full) + (y * 2 + buf) * 8);
-    if (!(j & 1) || j == lo) free_tile(tile);
-    return true;
+    if (!(j & 1) || j == lo) free_tile(k_tile(j));
   };
   auto pv = [&](int j) {
-    const uint32_t buf = (step0 + (uint32_t)(hi - j)) & 1u, tile = kv_base + 2u * (uint32_t)(nt - 1 - (j >> 1)) + 1u;
+    const uint32_t buf = (step0 + (uint32_t)(hi - j)) & 1u, tile = k_tile(j) + 1u;
     const uint32_t vb = v0 + (tile % NS) * kTile16 + (j & 1) * kStep16;
     const uint32_t p = s0 + buf * kStep;
 #pragma unroll
@@ -570,22 +575,40 @@ __device__ __forceinline__ void issue_mmas(const PrefillAttnArgs& a, Shared<D, N
     umma_commit_by(leader, bars + (uint32_t)offsetof(SH, pv_done) + (y * 2 + buf) * 8);
     if (!(j & 1) || j == lo) free_tile(tile);
   };
-  ok = wait(&sh.q_full, n_q);
+  if constexpr (QK) ok = wait(&sh.q_full, n_q);
   pass(0, nt - 1 - (hi >> 1));
-  ok = ok && qk(hi) && (hi - 1 < lo || qk(hi - 1));
+  if constexpr (QK) {
+    for (int j = hi; j >= max(lo, hi - 1) && ok; --j) {  // (the second tile may need the first one's place)
+      ok = wait_k(j);
+      if (!ok) break;
+      tc_fence_after();
+      qk(j);
+    }
+  }
   for (int j = hi; j >= lo && ok; --j) {
     const uint32_t c = step0 + (uint32_t)(hi - j);
-    if (j == hi || (j & 1)) ok = wait_kv(kv_base + 2u * (uint32_t)(nt - 1 - (j >> 1)) + 1u);
-    ok = ok && wait(&sh.p_full[y][c & 1u], c >> 1);
-    if (!ok) break;
-    tc_fence_after();
-    pv(j);
-    if (j - 2 >= lo) ok = qk(j - 2);
+    if constexpr (PV) {
+      if (j == hi || (j & 1)) ok = wait_kv(k_tile(j) + 1u);  // V of the tile's first step
+      ok = ok && wait(&sh.p_full[y][c & 1u], c >> 1);
+      if (!ok) break;
+      tc_fence_after();
+      pv(j);
+    }
+    if (QK && j - 2 >= lo) {
+      ok = wait_k(j - 2);
+      if constexpr (!PV) {  // the product has read P from the columns
+        ok = ok && wait(&sh.pv_done[y][c & 1u], c >> 1);
+        tc_fence_after();
+      }
+      if (!ok) break;
+      qk(j - 2);
+    }
   }
   pass(nt - (lo >> 1), nt);
   if (!ok) {  // the MMAs in flight end before tensor memory goes
-    umma_commit_by(leader, bars + (uint32_t)offsetof(SH, drained) + y * 8);
-    (void)mbar_wait_spin(&sh.drained[y], 0, a.timeout_ns);
+    const uint32_t at = NT == 2 ? (uint32_t)y : (PV ? 1u : 0u);
+    umma_commit_by(leader, bars + (uint32_t)offsetof(SH, drained) + at * 8);
+    (void)mbar_wait_spin(&sh.drained[at], 0, a.timeout_ns);
   }
   n_step = step0 + (uint32_t)(hi - lo + 1);
 }
@@ -985,13 +1008,14 @@ prefill_attention_kernel(const __grid_constant__ PrefillAttnArgs a) {
       mbar_init(&sh.kv_empty[s], NT);
     }
     for (int x = 0; x < NT; ++x) {
-      mbar_init(&sh.drained[x], 1);
       for (int q = 0; q < 2; ++q) {
         mbar_init(&sh.s_full[x][q], 1);
         mbar_init(&sh.p_full[x][q], 4);
         mbar_init(&sh.pv_done[x][q], 1);
       }
     }
+    mbar_init(&sh.drained[0], 1);
+    mbar_init(&sh.drained[1], 1);
     sh.abort = 0;
     fence_mbar_init();
   }
@@ -1053,16 +1077,22 @@ prefill_attention_kernel(const __grid_constant__ PrefillAttnArgs a) {
       __syncthreads();
       set_keys(w, min(sh.lo_least[0], sh.lo_least[NT - 1]));
       if (w.nt > 0) {
-        if (warp == GE::kSoftmaxWarps) {
+        if (warp == GE::kProducer) {
           produce<D, NT>(a, sh, w, sq, n_kv, n_q);
-        } else if (warp <= GE::kSoftmaxWarps + NT) {
+        } else if (warp < GE::kTicket) {
           tc_fence_after();
-          issue_mmas<D, NT>(a, sh, w, sq, tmem, leader, warp - GE::kSoftmaxWarps - 1, n_kv, n_q, n_step);
+          const int k = warp - GE::kIssuer;
+          if constexpr (NT == 2) {
+            issue_mmas<D, NT, true, true>(a, sh, w, sq, tmem, leader, k, n_kv, n_q, n_step);
+          } else {
+            if (k == 0) issue_mmas<D, NT, true, false>(a, sh, w, sq, tmem, leader, 0, n_kv, n_q, n_step);
+            else issue_mmas<D, NT, false, true>(a, sh, w, sq, tmem, leader, 0, n_kv, n_q, n_step);
+          }
         }
         ++n_q;
       }
-      // an idle warp takes the next item's ticket meanwhile
-      if (warp == GE::kSoftmaxWarps + 1 + NT && lane == 0) sh.next = (int)gridDim.x + atomicAdd(a.plan_head + 1, 1);
+      // the next item's ticket is taken meanwhile
+      if (warp == GE::kTicket && lane == 0) sh.next = (int)gridDim.x + atomicAdd(a.plan_head + 1, 1);
       __syncwarp();
       __syncthreads();
       if (sh.abort != 0) break;
