@@ -320,8 +320,9 @@ struct PrefillAttnArgs {
   int R;                         // tokens of a 128-row tile (128 / G)
   int sms, slots;                // SMs; CTAs resident at a time
   int* plan_head;                // the plan: items in the list, ticket counter, split entries
-  int4* plan_items;              // (sequence, row tile group, share | shares << 16, first partial row)
-  int4* plan_split;              // split row tile groups: (sequence, group, shares, first partial row)
+  int4* plan_items;              // two each: (sequence, first packed row, tokens, position of the first), (keys,
+                                 //   prefix, share | shares << 16, first partial row)
+  int4* plan_split;              // split row tile groups: (first packed row, tokens, shares, first partial row)
   float2* part_ml;               // partial rows: (running max in base 2, running sum)
   float* part_o;                 // partial rows, unnormalised [.., D]
   unsigned long long timeout_ns; // bound of every mbarrier wait

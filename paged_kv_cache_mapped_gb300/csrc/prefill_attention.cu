@@ -109,12 +109,14 @@ struct Geo {
 // Sequence b has ceil(n_b / (NT R)) row tile groups ("entries") of R = 128 / G tokens a tile; entry e has kt_e key
 // tiles (an upper bound where documents hide some), and Hkv items of it make P = entries * Hkv.  `slots` CTAs
 // run at a time.
-//  * P < slots: every entry is cut into shares of at most c key tiles, c chosen among ktmax / s, s = 1, 2, ..., for
-//    the least of max(c, ..) estimates of the end: c where all shares run at once, else the smaller of
-//    W / slots + c (any list schedule) and the rounds times c.
+//  * P < slots: every entry is cut into shares of at most c key tiles, c chosen among ktmax / s for a few s for
+//    the least estimate of the end, an item costing a tile beside its own: c + 1 where all shares run at once,
+//    else the smaller of the mean + c (any list schedule) and the rounds times c + 1; and 4 tiles' time plus one
+//    for 2000 rows where rows have to be merged (2 x 300 tokens of 1000, 19200 rows: 31 us whole, 51 us in two
+//    shares; 4 single tokens of 131072 keys: 361 us in 19 shares each, 379 in 16).
 //  * P >= slots: entries above one and a half times the fair share W / slots are cut to that.  If there are none, the last P mod slots
 //    items, which would leave most CTAs idle for a whole item, are cut in s shares each (chunk of 4096 on 16384,
-//    512 items on 152 CTAs: 56 items in two shares, 0.99 -> @@ ms capped).
+//    512 items on 152 CTAs: 56 items in two shares, capped 0.99 -> 0.87 ms).
 // The shares of split entries number at most 2 slots, which bounds the partial rows.  The list has the entries
 // with more than half of ktmax first, a sequence's last rows first within either part.
 struct Entry {
@@ -146,6 +148,7 @@ __global__ void __launch_bounds__(1024) prefill_plan_kernel(const PrefillAttnArg
   __shared__ int s_split;
   __shared__ long long s_sum[34];
   __shared__ int s_kt[kPlanEntries];
+  __shared__ short s_tokens[kPlanEntries];
   __shared__ int s_max;
   __shared__ unsigned long long s_best;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, warps = blockDim.x >> 5;
@@ -203,10 +206,13 @@ __global__ void __launch_bounds__(1024) prefill_plan_kernel(const PrefillAttnArg
   long long work = 0;
   int most = 0;
   for (int e = tid; e < entries; e += blockDim.x) {
-    const int kt = plan_entry(a, s_base, s_seq, e, per_item).kt;
-    if (e < kPlanEntries) s_kt[e] = kt;
-    work += kt;
-    most = max(most, kt);
+    const Entry x = plan_entry(a, s_base, s_seq, e, per_item);
+    if (e < kPlanEntries) {
+      s_kt[e] = x.kt;
+      s_tokens[e] = (short)x.tokens;
+    }
+    work += x.kt;
+    most = max(most, x.kt);
   }
   most = __reduce_max_sync(kFullMask, most);
   if (lane == 0) atomicMax(&s_max, most);
@@ -215,20 +221,30 @@ __global__ void __launch_bounds__(1024) prefill_plan_kernel(const PrefillAttnArg
   const int ktmax = max(s_max, 1);
   int chunk, tail = entries, tail_split = 1;
   if (P < a.slots && entries <= kPlanEntries) {
-    for (int sp = warp + 1; sp <= kMaxShares; sp += warps) {
+    for (int q = warp; q < 16; q += warps) {
+      // 1 .. 6, 8, 10, 16, .., 64, and what fills the CTAs once and twice if all entries are alike
+      const int once = (int)(a.slots / P);
+      const int sp = q < 6    ? q + 1
+                     : q < 13 ? (q & 1) ? 5 << ((q >> 1) - 2) : 4 << ((q >> 1) - 2)
+                              : min(kMaxShares, q == 13 ? once : q == 14 ? 2 * once : (int)(2 * a.slots / P));
       const int c = max(kMinChunk, (ktmax + sp - 1) / sp);
-      int shares = 0;
-      for (int e = lane; e < entries; e += 32) shares += max(1, (s_kt[e] + c - 1) / c);
+      int shares = 0, rows = 0;
+      for (int e = lane; e < entries; e += 32) {
+        const int n = min(kMaxShares, max(1, (s_kt[e] + c - 1) / c));
+        shares += n;
+        rows += n > 1 ? s_tokens[e] : 0;
+      }
       shares = __reduce_add_sync(kFullMask, shares);
+      rows = __reduce_add_sync(kFullMask, rows);
       const long long items = (long long)shares * a.Hkv;
-      if (sp > 1 && (items > 2 * a.slots)) continue;
-      long long end = c;
-      if (items > a.slots) end = min(W / a.slots + c, (items + a.slots - 1) / a.slots * c);
-      const unsigned long long cost = (unsigned long long)(end * 64 + (c < ktmax ? 32 : 0) + sp);
-      if (lane == 0) atomicMin(&s_best, cost << 32 | (unsigned)c);
+      if (sp > 1 && items > 2 * a.slots) continue;
+      long long end = c + 1;
+      if (items > a.slots) end = min((W + items) / a.slots + c, (items + a.slots - 1) / a.slots * end);
+      if (rows > 0) end += 4 + (long long)rows * a.Hq / 2000;
+      if (lane == 0) atomicMin(&s_best, (unsigned long long)end << 32 | (0xffffffffu - (unsigned)c));
     }
     __syncthreads();
-    chunk = (int)(unsigned)(s_best & 0xffffffffull);
+    chunk = (int)(0xffffffffu - (unsigned)(s_best & 0xffffffffull));  // of equal ends the fewest shares
   } else {
     chunk = (int)max((long long)kMinChunk, (W + W / 2) / a.slots);
     if (ktmax <= chunk) {
@@ -272,8 +288,13 @@ __global__ void __launch_bounds__(1024) prefill_plan_kernel(const PrefillAttnArg
     row += s_sum[32];
     if (e < entries) {
       const long long item0 = at[part] + (part == 0 ? both >> 32 : both & 0xffffffffll);
-      if (shares > 1) a.plan_split[atomicAdd(&s_split, 1)] = make_int4(x.b, x.tile, shares, (int)row0);
-      for (int k = 0; k < shares; ++k) a.plan_items[item0 + k] = make_int4(x.b, x.tile, k | shares << 16, (int)row0);
+      const int q0 = a.query_starts[x.b] + x.tile * per_item, L = s_seq[3 * x.b + 1];
+      if (shares > 1) a.plan_split[atomicAdd(&s_split, 1)] = make_int4(q0, x.tokens, shares, (int)row0);
+      const int4 where = make_int4(x.b, q0, x.tokens, L - s_seq[3 * x.b] + x.tile * per_item);
+      for (int k = 0; k < shares; ++k) {
+        a.plan_items[2 * (item0 + k)] = where;
+        a.plan_items[2 * (item0 + k) + 1] = make_int4(L, s_seq[3 * x.b + 2], k | shares << 16, (int)row0);
+      }
     }
     at[0] += both_all >> 32;
     at[1] += both_all & 0xffffffffll;
@@ -350,9 +371,9 @@ __device__ __noinline__ void exact_row(const PrefillAttnArgs& a, const Row& w, l
 // the union of the rows' intervals, in tiles of 8.
 struct Item {
   int b, g, split, nsplit, part;  // part: first partial row of the entry
-  int q0, n, L, pre;      // of the sequence
-  int tok0, tokens, nx;   // first token (of the sequence's queries), tokens, row tiles
-  int pos0;               // position of the first token
+  int L, pre;                     // of the sequence
+  int row0, tokens, nx;           // first packed row, tokens, row tiles
+  int pos0;                       // position of the first token
   int pre_units, nblk, shift, nt_all, ts, nt;  // list entries, key tiles of the rows, this share's
   int ns;                 // steps of this share
 
@@ -369,21 +390,18 @@ struct Steps {
 __device__ __forceinline__ Item load_item(const PrefillAttnArgs& a, int it, int NT) {
   Item w;
   const int at = it / a.Hkv;
-  const int4 p = a.plan_items[at];
-  const PrefillSeq s = prefill_seq(a, p.x);
+  const int4 p = a.plan_items[2 * at], q = a.plan_items[2 * at + 1];
   w.b = p.x;
   w.g = it - at * a.Hkv;
-  w.split = p.z & 0xffff;
-  w.nsplit = p.z >> 16;
-  w.part = p.w;
-  w.q0 = s.q0;
-  w.n = s.n;
-  w.L = s.L;
-  w.pre = s.pre;
-  w.tok0 = p.y * NT * a.R;
-  w.tokens = min(s.n - w.tok0, NT * a.R);
+  w.row0 = p.y;
+  w.tokens = p.z;
+  w.pos0 = p.w;
+  w.L = q.x;
+  w.pre = q.y;
+  w.split = q.z & 0xffff;
+  w.nsplit = q.z >> 16;
+  w.part = q.w;
   w.nx = NT == 2 && w.tokens > a.R ? 2 : 1;
-  w.pos0 = s.L - s.n + w.tok0;
   return w;
 }
 
@@ -434,7 +452,7 @@ __device__ __forceinline__ void produce(const PrefillAttnArgs& a, Shared<D, NT>&
     for (int y = 0; y < w.nx; ++y)
 #pragma unroll
       for (int h = 0; h < H; ++h)
-        tma_load_3d(sq + y * GE::kTile + h * kHalf, &a.tmap_q, h * 64, w.g * a.G, w.q0 + w.tok0 + y * a.R, &sh.q_full, pol_q);
+        tma_load_3d(sq + y * GE::kTile + h * kHalf, &a.tmap_q, h * 64, w.g * a.G, w.row0 + y * a.R, &sh.q_full, pol_q);
   }
   auto id_of = [&](int j) -> int {  // lane p < 8: the pool block of entry p of the j-th key tile, -1: none
     const int e = (w.ts + w.nt - 1 - j) * kTileBlocks + lane;
@@ -943,7 +961,7 @@ __device__ __forceinline__ void softmax_rows(const PrefillAttnArgs& a, Shared<D,
   // ---- the rows out: bf16, or this share's unnormalised row with its maximum and sum
   const bool split = w.nsplit > 1;
   const long long part =
-      split ? (long long)w.part + ((long long)w.split * w.tokens + (prow - w.q0 - w.tok0)) * a.Hq + h : 0;
+      split ? (long long)w.part + ((long long)w.split * w.tokens + (prow - w.row0)) * a.Hq + h : 0;
   const float f = split ? 1.f : (l > 0.f ? 1.f / l : 0.f);
   bool bad = !(l <= 3.4028234e38f);
 #pragma unroll
@@ -1001,6 +1019,11 @@ prefill_attention_kernel(const __grid_constant__ PrefillAttnArgs a) {
   unsigned char* sq = reinterpret_cast<unsigned char*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   __shared__ Shared<D, NT> sh;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  if (threadIdx.x == 32) {
+    prefetch_tensor_map(&a.tmap_q);
+    prefetch_tensor_map(&a.tmap_k);
+    prefetch_tensor_map(&a.tmap_v);
+  }
   if (threadIdx.x == 0) {
     mbar_init(&sh.q_full, 1);
     for (int s = 0; s < GE::kSlots; ++s) {
@@ -1049,7 +1072,7 @@ prefill_attention_kernel(const __grid_constant__ PrefillAttnArgs a) {
       }
       __syncthreads();
       const bool valid = tok < a.R && x * a.R + tok < w.tokens;
-      const int prow = w.q0 + w.tok0 + x * a.R + tok;
+      const int prow = w.row0 + x * a.R + tok;
       const int i = valid ? w.pos0 + x * a.R + tok : -1;
       const int lo = valid ? interval_start(a, prow, i) : 0;
       const int least = __reduce_min_sync(kFullMask, valid ? lo : 0x7fffffff);
@@ -1118,9 +1141,8 @@ __global__ void __launch_bounds__(256) prefill_merge_kernel(const PrefillAttnArg
   for (long long row = ((long long)blockIdx.x * blockDim.x + threadIdx.x) >> 5; row < rows;
        row += ((long long)gridDim.x * blockDim.x) >> 5) {
     const int k = (int)(row / per_entry), in = (int)(row - (long long)k * per_entry);
-    const int4 split = a.plan_split[k];  // (sequence, row tile group, shares, first partial row)
-    const PrefillSeq s = prefill_seq(a, split.x);
-    const int tok0 = split.y * per_item, per = min(s.n - tok0, per_item) * a.Hq;
+    const int4 split = a.plan_split[k];  // (first packed row, tokens, shares, first partial row)
+    const int per = split.y * a.Hq;
     if (in >= per) continue;
     const long long p0 = (long long)split.w + in;
     float2 ml[2];
@@ -1159,7 +1181,7 @@ __global__ void __launch_bounds__(256) prefill_merge_kernel(const PrefillAttnArg
       for (int e = 0; e < E; ++e) o[e] = f == 0.f ? o[e] : fmaf(f, x[e], o[e]);
     }
     const float inv = l > 0.f ? 1.f / l : (l == l ? 0.f : l);
-    __nv_bfloat16* dst = a.out + ((long long)(s.q0 + tok0) * a.Hq + in) * D + lane * E;
+    __nv_bfloat16* dst = a.out + ((long long)split.x * a.Hq + in) * D + lane * E;
 #pragma unroll
     for (int e = 0; e < E; e += 2)
       *reinterpret_cast<uint32_t*>(dst + e) = pack_bf16x2(o[e] * inv, o[e + 1] * inv);
@@ -1177,14 +1199,14 @@ struct PrefillWorkspace {
   size_t items, split, ml, o, total;
 };
 
-// head | int4 items | int4 split entries | float2 (m, l) | float o.  Entries: at most one per 128 rows, and one
+// head | int4[2] items | int4 split entries | float2 (m, l) | float o.  Entries: at most one per 128 rows, and one
 // more per sequence; items: those and the shares of split ones.
 PrefillWorkspace plan_prefill(long long B, long long T, int Hq, int G, int D) {
   PrefillWorkspace w{};
   const long long entries = T / (128 / G) + B;
   const long long rows = std::min(kMaxPartRows, T * Hq * kMaxShares);
   w.items = 256;
-  w.split = align256p(w.items + sizeof(int4) * (size_t)(entries + 4 * kMaxSms));
+  w.split = align256p(w.items + 2 * sizeof(int4) * (size_t)(entries + 4 * kMaxSms));
   w.ml = align256p(w.split + sizeof(int4) * (size_t)std::min<long long>(entries, 4 * kMaxSms));
   w.o = align256p(w.ml + sizeof(float2) * (size_t)rows);
   w.total = align256p(w.o + sizeof(float) * (size_t)rows * D);
@@ -1240,9 +1262,10 @@ cudaError_t launch_prefill_attention(const PrefillAttnArgs& a, void* workspace, 
   args.plan_split = reinterpret_cast<int4*>(ws + w.split);
   args.part_ml = reinterpret_cast<float2*>(ws + w.ml);
   args.part_o = reinterpret_cast<float*>(ws + w.o);
-  // two row tiles an item when the sequences fill more than one on average and the row tiles would not all run
-  // at once by themselves
-  const bool two = (long long)a.T > (long long)a.B * a.R && (long long)a.T / a.R * a.Hkv >= 2 * a.sms;
+  // two row tiles an item when the sequences fill more than one on average (64 single tokens on 2000 keys, d 128:
+  // 110 us with one, 149 with two; 8 x 16 on 5000 52 and 64; 4 x 2048 prompts 205 and 163; 4 x 512 on 4096 with
+  // one head a kv head 62 and 56)
+  const bool two = (long long)a.T > (long long)a.B * a.R;
   if (head_dim == 128) return two ? launch_attention<128, 2>(args, stream) : launch_attention<128, 1>(args, stream);
   return two ? launch_attention<64, 2>(args, stream) : launch_attention<64, 1>(args, stream);
 }

@@ -131,6 +131,11 @@ __device__ __forceinline__ void tma_load_3d(void* dst_smem, const void* tmap, in
       : "memory");
 }
 
+// Brings a kernel parameter's tensor map into the descriptor cache.
+__device__ __forceinline__ void prefetch_tensor_map(const void* tmap) {
+  asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(tmap)) : "memory");
+}
+
 // Asynchronous 4-byte copy global -> shared (cp.async); an mbarrier tracks it through
 // cp_async_mbar_arrive.
 __device__ __forceinline__ void cp_async_4(void* dst_smem, const void* src_gmem) {
