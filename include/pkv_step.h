@@ -53,6 +53,7 @@ extern "C" {
  *                      all), PKV_DEV_NO_BLOCKS (too few free blocks; a free count outside the stack
  *                      or one that the pushed blocks would take past it), PKV_DEV_BAD_BLOCK_ID (a
  *                      held, pushed or taken block outside the pool).
+ * Arrays are aligned to their elements (slot_mapping to 8 bytes).
  * All or nothing: on an error the lengths and the count are passed through unchanged, the tables
  * and the stack's live entries stay as they were, every query_starts entry is 0 and every slot and
  * position -1.
@@ -88,7 +89,7 @@ int pkv_kv_step_tables(int32_t* block_tables, int32_t* context_lens_out, int32_t
  *                        holds a non-finite value (it is left unwritten and does not count), or a
  *                        (block, kv head) whose old scale is negative or not finite (nothing of it
  *                        is written).
- * Code pools, k and v 16-byte aligned; scales 4-byte aligned.
+ * Code pools, k and v 16-byte aligned; scales 4-byte, slot_mapping 8-byte aligned.
  */
 int pkv_kv_append_f8(void* k_codes, void* v_codes, float* k_scales, float* v_scales, const void* k,
                      const void* v, const int64_t* slot_mapping, int64_t num_tokens, const pkv_dims* dims,
@@ -162,7 +163,9 @@ size_t pkv_prefill_workspace_bytes(const pkv_dims* dims, int32_t total_tokens);
  *   total_tokens  : rows of q and out.
  *   rules         : or NULL (causal).
  *   error_word    : PKV_DEV_BAD_BLOCK_ID, _BAD_CONTEXT_LEN, _WAIT_TIMEOUT; _BAD_QUERY_RANGE for a
- *                   sequence whose rows are not within the packed batch (its rows are not written).
+ *                   sequence whose rows are not within the packed batch or which starts below a start
+ *                   before its own.  Rows of a refused sequence are not written.
+ * Arrays of int32 are 4-byte aligned, the others 16-byte.
  * Supported: d in {64, 128}; G = Hq / Hkv in 1..8; B <= 4096; MB * 16 < 2^30.
  */
 int pkv_paged_prefill_attention(void* out, const void* q, const void* k_cache, const void* v_cache,

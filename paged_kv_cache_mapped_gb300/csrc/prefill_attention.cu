@@ -6,16 +6,21 @@
 // i the row's position, visible keys [lo, i] and the prefix [0, pre).
 //
 // Three kernels:
-//  * prefill_plan_kernel cuts the batch into work items -- NT row tiles of 128 rows (tokens x the G
-//    heads of a kv head) of one sequence, and, where there are fewer of those than the GPU holds, a
-//    share of their keys -- and checks every sequence.
-//  * prefill_attention_kernel runs the items, one CTA (or two) per SM, each for one kv head.  Q tiles
-//    and a ring of 128-key K and V tiles (8 cache blocks each) come by TMA.  One thread issues the
-//    MMAs: S = Q K^T into tensor memory, and O += P V with P in tensor memory where S was and V read
-//    as it lies (MN-major).  Each row tile has 4 softmax warps, a row a thread: they read S, apply the
+//  * prefill_plan_kernel (one CTA) checks every sequence and cuts the batch into work items: one or two row
+//    tiles of 128 rows (tokens x the G heads of a kv head) of one sequence, and, where there are fewer of
+//    those than the GPU holds, a share of their keys.
+//  * prefill_attention_kernel runs the items, each for one kv head, taken by ticket by one CTA (two row tiles
+//    an item) or two CTAs (one) per SM.  Q tiles and a ring of 128-key K and V tiles (8 cache blocks each) come by TMA.
+//    S = Q K^T goes into tensor memory, 64 keys a step, and O += P V takes P from where S was and V as it
+//    lies (MN-major).  Each row tile has 4 softmax warps, a row a thread: they read S, apply the
 //    rules, keep the running maximum (moved only when exceeded by 2^8, and O rescaled then) and sum,
-//    and write P.  With two row tiles the softmax of one runs under the MMAs of the other.
+//    and write P.  The softmax of one step runs under the products of the next, and of the other row tile.
 //  * prefill_merge_kernel joins the shares of split items by their maxima and sums.
+// What bounds it: long chunks the MMAs' issue and rate and the exponentials together (4096 tokens on 16384 keys, 32 / 8 heads,
+// d 128: 719 us, 1340 TFLOP/s, 70 % of the measured bf16 rate; capped 840 us, with a distance bias 800); many
+// single tokens the bytes (64 on 2000 keys each 109 us, 4.8 TB/s; 4 on 131072 361 us, 5.9 TB/s); small batches the
+// chain of plan, first loads and merge (one token on 200 keys 19 us).  A CTA holds two row tiles
+// because every K and V tile that comes into shared memory then serves 256 rows.
 // P is rounded to bf16 for the product (the sum takes it in fp32).  Rows over more than kTwoTermTiles key
 // tiles take that one term: its error, at most 2^-8 of each weight and independent from key to key, is of the
 // size of a bf16 output's own rounding.  Shorter rows, where few weights may carry the result, add the
@@ -81,8 +86,8 @@ constexpr int kStep = 64;            // keys of a softmax step: half a tile
 constexpr int kStepBlocks = kStep / 16;
 constexpr int kHalf = kKeys * 128;   // bytes of one 64-element half of a tile
 constexpr float kSlack = 8.0f;       // the running maximum moves only when exceeded by this (base 2)
-constexpr int kTwoTermTiles = 4;     // rows over at most this many key tiles take P as two bf16 terms
-constexpr int kMinChunk = 4;         // key tiles of a split item at least
+constexpr int kTwoTermTiles = 4;     // rows over at most this many key tiles take P as two bf16 terms (above)
+constexpr int kMinChunk = 4;         // key tiles of a split item at least (with 2: mixed 24 36 -> 52 us)
 
 template <int D, int NT>
 struct Geo {
@@ -114,8 +119,8 @@ struct Geo {
 //    else the smaller of the mean + c (any list schedule) and the rounds times c + 1; and 4 tiles' time plus one
 //    for 2000 rows where rows have to be merged (2 x 300 tokens of 1000, 19200 rows: 31 us whole, 51 us in two
 //    shares; 4 single tokens of 131072 keys: 361 us in 19 shares each, 379 in 16).
-//  * P >= slots: entries above one and a half times the fair share W / slots are cut to that.  If there are none, the last P mod slots
-//    items, which would leave most CTAs idle for a whole item, are cut in s shares each (chunk of 4096 on 16384,
+//  * P >= slots: entries above one and a half times the fair share W / slots are cut to that.  If there are
+//    none, the last P mod slots items, which would leave most CTAs idle for a whole item, are cut in s shares each (chunk of 4096 on 16384,
 //    512 items on 152 CTAs: 56 items in two shares, capped 0.99 -> 0.87 ms).
 // The shares of split entries number at most 2 slots, which bounds the partial rows.  The list has the entries
 // with more than half of ktmax first, a sequence's last rows first within either part.
@@ -187,10 +192,20 @@ __global__ void __launch_bounds__(1024) prefill_plan_kernel(const PrefillAttnArg
     return s_sum[warp] + x - v;
   };
   int carry = 0;
+  bool unordered = false;
   for (int base = 0; base < a.B; base += blockDim.x) {
     int ntile = 0;
+    PrefillSeq s{0, 0, 0, 0, 0};
+    if (base + tid < a.B) s = prefill_seq(a, base + tid);
+    // Ascending starts make the sequences' rows disjoint, which bounds the entries (and gives each row one
+    // writer).  Where some are not, a sequence is refused that starts below any start before its own.
+    unordered = __syncthreads_or(s.err == PKV_DEV_BAD_QUERY_RANGE) != 0 || unordered;
+    if (unordered && base + tid < a.B && s.err == 0) {
+      int most = 0;
+      for (int k = 0; k < base + tid; ++k) most = max(most, a.query_starts[k]);
+      if (s.q0 < most) s = PrefillSeq{0, 0, 0, 0, PKV_DEV_BAD_QUERY_RANGE};
+    }
     if (base + tid < a.B) {
-      const PrefillSeq s = prefill_seq(a, base + tid);
       if (s.err != 0) record_error(a.err, s.err);
       ntile = (s.n + per_item - 1) / per_item;
       s_seq[3 * (base + tid)] = s.n;
@@ -375,7 +390,7 @@ struct Item {
   int row0, tokens, nx;           // first packed row, tokens, row tiles
   int pos0;                       // position of the first token
   int pre_units, nblk, shift, nt_all, ts, nt;  // list entries, key tiles of the rows, this share's
-  int ns;                 // steps of this share
+  int ns;                                      // steps of this share
 
   __device__ __forceinline__ int block_of(int e) const { return e < pre_units ? e : e + shift; }
 };
@@ -1312,7 +1327,9 @@ int pkv_paged_prefill_attention(void* out, const void* q, const void* k_cache, c
   if (dims->batch == 0 || total_tokens == 0) return PKV_OK;
   if (!out || !q || !k_cache || !v_cache || !block_tables || !context_lens || !query_starts) return PKV_ERR_NULL_POINTER;
   if (!workspace || workspace_bytes < pkv_prefill_workspace_bytes(dims, total_tokens)) return PKV_ERR_WORKSPACE;
-  if (!aligned16(out) || !aligned16(q) || !aligned16(k_cache) || !aligned16(v_cache) || !aligned16(workspace))
+  if (!aligned16(out) || !aligned16(q) || !aligned16(k_cache) || !aligned16(v_cache) || !aligned16(workspace) ||
+      ((reinterpret_cast<uintptr_t>(block_tables) | reinterpret_cast<uintptr_t>(context_lens) |
+        reinterpret_cast<uintptr_t>(query_starts) | reinterpret_cast<uintptr_t>(error_word)) & 3u))
     return PKV_ERR_ALIGNMENT;
   int sms = 0;
   st = device_ready(&sms);

@@ -478,6 +478,13 @@ int pkv_kv_step_tables(int32_t* block_tables, int32_t* context_lens_out, int32_t
   if (dims->batch > 0 && dims->max_blocks_per_seq > 0 && !block_tables) return PKV_ERR_NULL_POINTER;
   if (max_new_tokens > 0 && (!slot_mapping || !positions)) return PKV_ERR_NULL_POINTER;
   if (dims->num_blocks > 0 && !free_blocks) return PKV_ERR_NULL_POINTER;
+  uintptr_t words = reinterpret_cast<uintptr_t>(slot_mapping) & 4u;
+  for (const void* p : {(const void*)block_tables, (const void*)context_lens_out, (const void*)query_starts,
+                        (const void*)slot_mapping, (const void*)positions, (const void*)free_count_out,
+                        (const void*)free_blocks, (const void*)free_count, (const void*)context_lens,
+                        (const void*)new_tokens, (const void*)error_word})
+    words |= reinterpret_cast<uintptr_t>(p) & 3u;
+  if (words != 0) return PKV_ERR_ALIGNMENT;
   const int st = device_ready();
   if (st != PKV_OK) return st;
   StepArgs a{};
@@ -508,7 +515,8 @@ int pkv_kv_append_f8(void* k_codes, void* v_codes, float* k_scales, float* v_sca
   if (num_tokens == 0) return PKV_OK;
   if (!k_codes || !v_codes || !k_scales || !v_scales || !k || !v || !slot_mapping) return PKV_ERR_NULL_POINTER;
   if (!aligned16(k_codes) || !aligned16(v_codes) || !aligned16(k) || !aligned16(v) ||
-      ((reinterpret_cast<uintptr_t>(k_scales) | reinterpret_cast<uintptr_t>(v_scales)) & 3u))
+      ((reinterpret_cast<uintptr_t>(k_scales) | reinterpret_cast<uintptr_t>(v_scales) |
+        reinterpret_cast<uintptr_t>(error_word)) & 3u) || (reinterpret_cast<uintptr_t>(slot_mapping) & 7u))
     return PKV_ERR_ALIGNMENT;
   st = device_ready();
   if (st != PKV_OK) return st;

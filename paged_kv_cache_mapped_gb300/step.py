@@ -64,10 +64,19 @@ def _dims(batch, hq, hkv, d, nb, mb):
     return ctypes.pointer(r)
 
 
-def _give(t, name, shape, dtype, like, device):
+def _new(shape, dtype, like, stream, make=torch.empty):
+    """A new tensor on `like`'s device, made (and zeroed) in the order of the call's own stream: a caching
+    allocator may hand its memory out again once it is freed there."""
+    if stream is None:
+        return make(shape, dtype=dtype, device=like.device)
+    with torch.cuda.stream(stream):
+        return make(shape, dtype=dtype, device=like.device)
+
+
+def _give(t, name, shape, dtype, like, device, stream):
     """The output `t` after its checks, or a new one on `like`'s device; with its address."""
     if t is None:
-        t = torch.empty(shape, dtype=dtype, device=like.device)
+        t = _new(shape, dtype, like, stream)
         return t, t.data_ptr()
     ptr = _need(t, name, dtype, len(shape), device)
     if tuple(t.shape) != tuple(shape):
@@ -100,11 +109,11 @@ def kv_step_tables(block_tables, context_lens, new_tokens, free_blocks, free_cou
     T = int(max_new_tokens)
     if T < 0:
         raise ValueError("max_new_tokens must not be negative")
-    lens_out, lp = _give(context_lens_out, "context_lens_out", (B,), torch.int32, block_tables, dev)
-    count_out, cp = _give(free_count_out, "free_count_out", (1,), torch.int32, block_tables, dev)
-    starts, qp = _give(query_starts, "query_starts", (B + 1,), torch.int32, block_tables, dev)
-    slots, sp = _give(slot_mapping, "slot_mapping", (T,), torch.int64, block_tables, dev)
-    pos, pp = _give(positions, "positions", (T,), torch.int32, block_tables, dev)
+    lens_out, lp = _give(context_lens_out, "context_lens_out", (B,), torch.int32, block_tables, dev, stream)
+    count_out, cp = _give(free_count_out, "free_count_out", (1,), torch.int32, block_tables, dev, stream)
+    starts, qp = _give(query_starts, "query_starts", (B + 1,), torch.int32, block_tables, dev, stream)
+    slots, sp = _give(slot_mapping, "slot_mapping", (T,), torch.int64, block_tables, dev, stream)
+    pos, pp = _give(positions, "positions", (T,), torch.int32, block_tables, dev, stream)
     _call("pkv_kv_step_tables", dev, stream, bt, lp, qp, sp, pp, cp, free, count, lens, new, T,
           _dims(B, 1, 1, 128, free_blocks.shape[0], mb), err)
     return lens_out, starts, slots, pos, count_out
@@ -167,10 +176,10 @@ def _rules(softcap, window, alibi_slopes, doc_starts, prefix_lens, hq, rows, bat
         raise ValueError("doc_starts must have one entry per query row")
     if p is not None and prefix_lens.shape[0] != batch:
         raise ValueError("prefix_lens must be [batch]")
-    return PkvScoreRules(softcap, int(window), a, ds, p)
+    return PkvScoreRules(softcap, max(0, min(int(window), 2**31 - 1)), a, ds, p)
 
 
-def _decode_common(q, nb, hkv, d, block_tables, context_lens, out, workspace, error_word, dev):
+def _decode_common(q, nb, hkv, d, block_tables, context_lens, out, workspace, error_word, dev, stream):
     qp = _need(q, "q", torch.bfloat16, 3, dev)
     bp = _need(block_tables, "block_tables", torch.int32, 2, dev)
     lp = _need(context_lens, "context_lens", torch.int32, 1, dev)
@@ -182,9 +191,9 @@ def _decode_common(q, nb, hkv, d, block_tables, context_lens, out, workspace, er
     if rows != B or context_lens.shape[0] != B:
         raise ValueError("block_tables / context_lens batch differs from q's")
     dims = _dims(B, hq, hkv, d, nb, mb)
-    out, op = _give(out, "out", (B, hq, d), torch.bfloat16, q, dev)
+    out, op = _give(out, "out", (B, hq, d), torch.bfloat16, q, dev, stream)
     if workspace is None:
-        workspace = torch.zeros(int(load().pkv_decode_workspace_bytes(dims)), dtype=torch.uint8, device=q.device)
+        workspace = _new((int(load().pkv_decode_workspace_bytes(dims)),), torch.uint8, q, stream, torch.zeros)
     wp = _need(workspace, "workspace", torch.uint8, 1, dev)
     return B, hq, dims, qp, bp, lp, err, out, op, wp, workspace.numel()
 
@@ -197,7 +206,7 @@ def paged_decode_attention_rules(q, k_cache, v_cache, block_tables, context_lens
     and [0, prefix_len) (int32 [B] each).  Returns out [B, Hq, d] bf16; a row that sees no key is zero."""
     nb, hkv, d, dev, kp, vp = _bf16_pools(k_cache, v_cache)
     B, hq, dims, qp, bp, lp, err, out, op, wp, ws_bytes = _decode_common(q, nb, hkv, d, block_tables, context_lens, out,
-                                                                         workspace, error_word, dev)
+                                                                         workspace, error_word, dev, stream)
     rules = _rules(softcap, window, alibi_slopes, doc_starts, prefix_lens, hq, B, B, dev)
     _call("pkv_paged_decode_attention_rules", dev, stream, op, qp, kp, vp, bp, lp, scale, ctypes.byref(rules), wp, ws_bytes,
           dims, _INPUTS_READY if inputs_ready else 0, err)
@@ -211,7 +220,7 @@ def paged_decode_attention_f8(q, k_codes, v_codes, k_scales, v_scales, block_tab
     scale per (block, kv head), [NB, Hkv]), with the score rules of paged_decode_attention_rules."""
     nb, hkv, d, dev, kp, vp, ks, vs = _f8_pools(k_codes, v_codes, k_scales, v_scales)
     B, hq, dims, qp, bp, lp, err, out, op, wp, ws_bytes = _decode_common(q, nb, hkv, d, block_tables, context_lens, out,
-                                                                         workspace, error_word, dev)
+                                                                         workspace, error_word, dev, stream)
     rules = None
     if softcap != 0 or window > 0 or alibi_slopes is not None or doc_starts is not None or prefix_lens is not None:
         rules = ctypes.byref(_rules(softcap, window, alibi_slopes, doc_starts, prefix_lens, hq, B, B, dev))
@@ -251,9 +260,9 @@ def paged_prefill_attention(q, k_cache, v_cache, block_tables, context_lens, que
         raise ValueError("context_lens must be [B] and query_starts [B + 1]")
     rules = _rules(softcap, window, alibi_slopes, doc_starts, prefix_lens, hq, T, B, dev)
     dims = _dims(B, hq, hkv, d, nb, mb)
-    out, op = _give(out, "out", (T, hq, d), torch.bfloat16, q, dev)
+    out, op = _give(out, "out", (T, hq, d), torch.bfloat16, q, dev, stream)
     if workspace is None:
-        workspace = torch.empty(int(load().pkv_prefill_workspace_bytes(dims, T)), dtype=torch.uint8, device=q.device)
+        workspace = _new((int(load().pkv_prefill_workspace_bytes(dims, T)),), torch.uint8, q, stream)
     wp = _need(workspace, "workspace", torch.uint8, 1, dev)
     _call("pkv_paged_prefill_attention", dev, stream, op, qp, kp, vp, bp, lp, sp, T, scale, ctypes.byref(rules), wp,
           workspace.numel(), dims, err)
