@@ -1212,7 +1212,8 @@ def run_reference(args):
 
 # ------------------------------------------------------------------- small profiling cases
 
-CASES = ("q8", "gather", "gather_q8", "prefill", "kvops", "layers", "append", "qwen8", "qwen8_plain")
+CASES = ("q8", "gather", "gather_q8", "prefill", "kvops", "layers", "append", "qwen8", "qwen8_plain",
+         "chunk", "step")
 
 
 def run_case(name: str, calls: int = 3):
@@ -1230,6 +1231,10 @@ def run_case(name: str, calls: int = 3):
       qwen8    eight qwen1p5b layers (each with its own pools: append + decode, the calls declaring
                their inputs ready) captured in one CUDA graph and replayed `calls` times
       qwen8_plain  the same graph with calls that do not declare their inputs ready
+      chunk    a sparse layer's first sequence, its last 4096 of 16384 tokens: paged_prefill_attention,
+               plain, then with capped scores
+      step     llama8b-shaped prompts into FP8 pools: kv_step_tables, kv_append_f8, then one token a
+               sequence by paged_decode_attention_f8, and over bf16 pools by paged_decode_attention_rules
     """
     import paged_kv_cache_mapped_gb300 as pkv
     from paged_kv_cache_mapped_gb300 import inputs as W
@@ -1368,6 +1373,33 @@ def run_case(name: str, calls: int = 3):
                 graph.replay()
             torch.cuda.synchronize(dev)
             torch.cuda.cudart().cudaProfilerStop()
+    elif name == "chunk":
+        wl = W.WORKLOADS["sparse"]
+        c = W.make_layer(wl, device=dev, device_rng=True)
+        n = 4096
+        g = torch.Generator(device=dev).manual_seed(61)
+        q = torch.randn((n, wl.num_q_heads, wl.head_dim), generator=g, device=dev).to(torch.bfloat16)
+        starts = torch.tensor([0, n], dtype=torch.int32, device=dev)
+        for cap in (0.0, 30.0):
+            pkv.paged_prefill_attention(q, c["k_cache"], c["v_cache"], c["block_tables"][:1].contiguous(),
+                                        c["context_lens"][:1].contiguous(), starts, wl.scale, softcap=cap)
+    elif name == "step":
+        wl = W.WORKLOADS["llama8b"]
+        c = W.make_layer(wl, device=dev, device_rng=True)
+        B, (nb, hkv, _, d) = wl.batch, c["k_cache"].shape
+        T = int(c["context_lens"].sum())
+        bt = torch.full_like(c["block_tables"], -1)
+        free, count = torch.randperm(nb, dtype=torch.int32, device=dev), torch.tensor([nb], dtype=torch.int32, device=dev)
+        lens, _, slots, _, _ = pkv.kv_step_tables(bt, torch.zeros_like(c["context_lens"]), c["context_lens"], free, count, T)
+        g = torch.Generator(device=dev).manual_seed(62)
+        k, v = (torch.randn((T, hkv, d), generator=g, device=dev).to(torch.bfloat16) for _ in range(2))
+        kq, vq = (torch.zeros((nb, hkv, 16, d), dtype=torch.uint8, device=dev).view(torch.float8_e4m3fn) for _ in range(2))
+        ks, vs = (torch.zeros((nb, hkv), device=dev) for _ in range(2))
+        for _ in range(calls):
+            pkv.kv_append_f8(kq, vq, ks, vs, k, v, slots)
+            pkv.paged_decode_attention_f8(c["q"], kq, vq, ks, vs, bt, lens, c["scale"])
+            pkv.paged_decode_attention_rules(c["q"], c["k_cache"], c["v_cache"], c["block_tables"], c["context_lens"],
+                                             c["scale"], softcap=30.0)
     else:
         raise SystemExit(f"unknown case {name!r}; one of {', '.join(CASES)}")
     torch.cuda.synchronize(dev)

@@ -17,7 +17,8 @@
 //    and write P.  The softmax of one step runs under the products of the next, and of the other row tile.
 //  * prefill_merge_kernel joins the shares of split items by their maxima and sums.
 // What bounds it: long chunks the MMAs' issue and rate and the exponentials together (4096 tokens on 16384 keys, 32 / 8 heads,
-// d 128: 719 us, 1340 TFLOP/s, 70 % of the measured bf16 rate; capped 840 us, with a distance bias 800); many
+// d 128: 720-730 us, 1320-1340 TFLOP/s, 69 % of the measured bf16 rate; with a distance bias 810; capped 841 where
+// the scores stay below a fifth of the cap, 1045 below 0.8 of it, 1520 beyond); many
 // single tokens the bytes (64 on 2000 keys each 109 us, 4.8 TB/s; 4 on 131072 361 us, 5.9 TB/s); small batches the
 // chain of plan, first loads and merge (one token on 200 keys 19 us).  A CTA holds two row tiles
 // because every K and V tile that comes into shared memory then serves 256 rows.
@@ -31,6 +32,7 @@
 #include <algorithm>
 #include <cmath>
 #include <cstddef>
+#include <type_traits>
 
 #include "kernels.h"
 #include "ptx.cuh"
@@ -659,20 +661,28 @@ __device__ __forceinline__ float row_max(const float (&v)[N]) {
   return fmaxf(fmax3(t[0], t[1], t[2]), t[3]);
 }
 
-// v = v * P(v^2 k^2) for the odd polynomial P of tanh (cap_logit): to u^5, or to u^9 with NINTH.
-template <bool NINTH, int N>
+// tanh(u) / u as a polynomial of u^2, of the least largest relative error on |u| <= kCapNear (degree 2, 1.1e-7)
+// and on |u| <= kCapFar (degree 5, 5.8e-8), found by Remez' exchange in 40 digits; 2.0e-7 and 1.5e-7 in fp32
+// steps.
+constexpr float kCapNear = 0.2f, kCapFar = 0.8f;
+__device__ constexpr float kCap2[3] = {0.99999988f, -0.3332859f, 0.13015407f};
+__device__ constexpr float kCap5[6] = {0.99999994f, -0.33332676f, 0.13321048f, -0.053114317f, 0.019093301f, -0.0043552998f};
+
+// v = v P(v^2 k^2) with P = tanh(u) / u, for |v k| <= kCapFar.
+template <int N>
 __device__ __forceinline__ void cap_poly(float (&v)[N], float k) {
-  const float w = k * k;
-  const float c1 = -0.33333333f * w, c2 = 0.13333333f * w * w, c3 = -0.053968254f * w * w * w,
-              c4 = 0.021869488f * w * w * w * w;
-  const uint64_t p1 = pack2(c1, c1), p2 = pack2(c2, c2), p3 = pack2(c3, c3), p4 = pack2(c4, c4), p0 = pack2(1.f, 1.f);
+  uint64_t p[6];
+  float w = 1.f;
+#pragma unroll
+  for (int n = 0; n < 6; ++n, w *= k * k) p[n] = pack2(kCap5[n] * w, kCap5[n] * w);
 #pragma unroll
   for (int c = 0; c < N; c += 2) {
     const uint64_t x = pack2(v[c], v[c + 1]);
     const uint64_t q = fmul2(x, x);
-    uint64_t p = NINTH ? ffma2(ffma2(p4, q, p3), q, p2) : p2;
-    p = ffma2(ffma2(p, q, p1), q, p0);
-    const float2 y = unpack2(fmul2(x, p));
+    uint64_t f = p[5];
+#pragma unroll
+    for (int n = 4; n >= 0; --n) f = ffma2(f, q, p[n]);
+    const float2 y = unpack2(fmul2(x, f));
     v[c] = y.x;
     v[c + 1] = y.y;
   }
@@ -687,27 +697,33 @@ struct Logits {
 // that form of x = cap(S sl2) - slope |i - t|.  (Without such rules v = S and mul = sl2.)  e0: the list entry of
 // its first key.
 template <int N>
-__device__ __forceinline__ Logits apply_rules(const PrefillAttnArgs& a, float (&v)[N], float slope2, int i, const Item& w,
+__device__ __forceinline__ Logits apply_rules(const PrefillAttnArgs& a, bool cap, bool bias, float (&v)[N], float slope2, int i, const Item& w,
                                               int e0) {
   Logits x{a.scale_log2, 0.f, 0.f};
-  if (a.cap_log2 > 0.f) {
-    // u = S ku is the logit over the cap.  Where it is small for every key of the warp's rows the odd
-    // polynomial serves: to u^5 below 0.11 (the next term is 0.054 u^6 of the value, 2^-23 there), to u^9
-    // below 0.3; the general form costs an exponential and a reciprocal a key
+  if (cap) {
+    // u = S ku is the logit over the cap.  Up to kCapFar for every key of the warp's rows the polynomial serves.
+    // Else 1 - 2 / (e^2u + 1), an exponential and a reciprocal a key: for a small u beside large ones its error is
+    // that of the cap's last bits, as the rounding of the large ones' is
     const float ku = a.scale_log2 * a.cap_in * 0.34657359f;
     const float far = row_max<true>(v) * fabsf(ku);
     x.mul = a.cap_log2 * ku;
-    if (x.mul > 0.f && __all_sync(kFullMask, far < 0.11f)) {
-      cap_poly<false>(v, ku);
-    } else if (x.mul > 0.f && __all_sync(kFullMask, far < 0.3f)) {
-      cap_poly<true>(v, ku);
+    if (x.mul > 0.f && __all_sync(kFullMask, far < kCapFar && fabsf(ku) < 1e3f)) {
+      cap_poly(v, ku);
     } else {
+      const float k = ku * (2.f * kLog2e), twice = -2.f * a.cap_log2;
+      const uint64_t k2 = pack2(k, k), one = pack2(1.f, 1.f), top = pack2(a.cap_log2, a.cap_log2), m2 = pack2(twice, twice);
 #pragma unroll
-      for (int c = 0; c < N; ++c) v[c] = cap_logit(v[c] * a.scale_log2, a.cap_log2, a.cap_in);
+      for (int c = 0; c < N; c += 2) {
+        const float2 z = unpack2(fmul2(pack2(v[c], v[c + 1]), k2));
+        const float2 e = unpack2(fadd2(pack2(ex2_approx(z.x), ex2_approx(z.y)), one));
+        const float2 y = unpack2(ffma2(pack2(rcp_approx(e.x), rcp_approx(e.y)), m2, top));
+        v[c] = y.x;
+        v[c + 1] = y.y;
+      }
       x.mul = 1.f;
     }
   }
-  if (a.slopes != nullptr) {
+  if (bias && a.slopes != nullptr) {
     const uint64_t m2 = pack2(x.mul, x.mul);
     if (e0 >= w.pre_units) {
       // the interval's part of the list is one run of positions, and keys past i are masked: the distance
@@ -741,12 +757,24 @@ __device__ __forceinline__ Logits apply_rules(const PrefillAttnArgs& a, float (&
 }
 
 // One step's weights for a thread's 64 unmasked keys in one pass: p = 2^(logit - ref), written as bf16 pairs
-// over S, and their sum.  CAP: the logit is S P(S^2) with P = c0 + c1 S^2 + c2 S^4, tanh's polynomial to u^5
-// with the scales folded in; otherwise S c0.  BIAS: plus base + slope2 c for key c of the step.
-template <bool CAP, bool BIAS>
-__device__ __forceinline__ float step_weights(const float (&v)[kStep], uint32_t ts_addr, float c0, float c1, float c2,
-                                              float base, float slope2) {
-  const uint64_t k0 = pack2(c0, c0), k1 = pack2(c1, c1), k2 = pack2(c2, c2);
+// over S, and their sum.  The logit is S c0, or with CAP S c0 P(S^2 ku^2), P of that degree with the scales folded
+// into its coefficients (here at each step: kept over the steps they cost the registers of the logits, capped
+// 0.89 -> 0.93 ms).  BIAS: plus base + slope2 c for key c of the step.
+template <int CAP, bool BIAS>
+__device__ __forceinline__ float step_weights(const float (&v)[kStep], uint32_t ts_addr, float c0, float ku, float base,
+                                              float slope2) {
+  uint64_t kc[CAP + 1];
+  if constexpr (CAP == 0) {
+    kc[0] = pack2(c0, c0);
+  } else {
+    asm volatile("" : "+f"(ku));
+    const float w = ku * ku;
+#pragma unroll
+    for (int n = 0; n <= CAP; ++n, c0 *= w) {
+      const float k = c0 * (CAP == 2 ? kCap2[n] : kCap5[n]);
+      kc[n] = pack2(k, k);
+    }
+  }
   uint64_t near[4], sum[4];
 #pragma unroll
   for (int k = 0; k < 4; ++k) {
@@ -764,10 +792,11 @@ __device__ __forceinline__ float step_weights(const float (&v)[kStep], uint32_t 
         const float far = slope2 * (float)(32 * c + 8 * (k >> 2));
         if (c > 0 || k >= 4) b = fadd2(b, pack2(far, far));
       }
-      uint64_t f = k0;
-      if constexpr (CAP) {
+      uint64_t f = kc[CAP];
+      if constexpr (CAP > 0) {
         const uint64_t q = fmul2(x, x);
-        f = ffma2(ffma2(k2, q, k1), q, k0);
+#pragma unroll
+        for (int n = CAP - 1; n >= 0; --n) f = ffma2(f, q, kc[n]);
       }
       const float2 z = unpack2(ffma2(x, f, b));
       const float p0 = ex2_approx(z.x), p1 = ex2_approx(z.y);
@@ -782,7 +811,9 @@ __device__ __forceinline__ float step_weights(const float (&v)[kStep], uint32_t 
 
 // The item's softmax and output for this thread's row r of row tile x: position i (-1: none), interval start
 // lo; prow and h name the output row.
-template <int D, int NT>
+// MODE: the rules that need each key's own logit, 1 a cap and 2 a distance bias (or a scale that is not positive),
+// 4: asked of the arguments at each step.
+template <int D, int NT, int MODE>
 __device__ __forceinline__ void softmax_rows(const PrefillAttnArgs& a, Shared<D, NT>& sh, const Item& w,
                                              unsigned char* sq, uint32_t tmem, int x, int r, bool valid, int i,
                                              int lo, int prow, int h, uint32_t n_kv, uint32_t& n_step) {
@@ -790,13 +821,13 @@ __device__ __forceinline__ void softmax_rows(const PrefillAttnArgs& a, Shared<D,
   constexpr int NS = GE::kSlots, H = GE::kHalves, N = kStep;
   const int lane = threadIdx.x & 31;
   unsigned char* skv = sq + NT * GE::kTile;
-  const float slope2 = valid && a.slopes != nullptr ? __ldg(a.slopes + h) * kLog2e : 0.f;
+  const bool cap = MODE == 4 ? a.cap_log2 > 0.f : (MODE & 1) != 0;
+  const bool bias = MODE == 4 ? a.slopes != nullptr || !(a.scale_log2 > 0.f) : (MODE & 2) != 0;
+  const float slope2 = bias && valid && a.slopes != nullptr ? __ldg(a.slopes + h) * kLog2e : 0.f;
   const int pre = valid ? w.pre : 0;
   const bool two = w.nt_all <= kTwoTermTiles;
-  // the cap as a polynomial of S (cap_logit's u = S ku): cap0 S + cap1 S^3 + cap2 S^5
-  const float ku = a.scale_log2 * a.cap_in * 0.34657359f, ku_size = a.cap_log2 > 0.f ? fabsf(ku) : 0.f;
-  const float cap0 = a.cap_log2 * ku, cap1 = -0.33333333f * cap0 * ku * ku, cap2 = 0.13333333f * cap0 * ku * ku * ku * ku;
-  const bool own_logits = a.cap_log2 > 0.f || a.slopes != nullptr || !(a.scale_log2 > 0.f);
+  // the cap as a polynomial of S: u = S ku, the logit cap_log2 u P(u^2)
+  const float ku = a.scale_log2 * a.cap_in * 0.34657359f, ku_size = fabsf(ku) < 1e3f ? fabsf(ku) : INFINITY;
   const Steps range = steps_of(a, w, x, sh.lo_least[x]);
   // steps whose keys all rows of the row tile see: a range of the interval's part of the list, and one of the
   // prefix's.  The list's position of entry e is 16 (e + shift) there.
@@ -816,6 +847,7 @@ __device__ __forceinline__ void softmax_rows(const PrefillAttnArgs& a, Shared<D,
   const uint32_t to_addr = t_lane + NT * 2 * kStep + x * D;
   bool ok = true;
   float m = -INFINITY, l = 0.f;
+  float reach = kCapNear;  // of the polynomial tried for the cap
   for (int j = range.hi; j >= range.lo; --j) {
     const uint32_t buf = n_step & 1u;
     const uint32_t ts_addr = t_lane + x * 2 * kStep + buf * kStep;
@@ -835,20 +867,27 @@ __device__ __forceinline__ void softmax_rows(const PrefillAttnArgs& a, Shared<D,
     bool fast = full && !two;
     float mx = -INFINITY, base = 0.f;
     Logits y{a.scale_log2, 0.f, 0.f};
-    if (fast && !own_logits) {
+    if (fast && !cap && !bias) {
       mx = row_max<false>(v) * a.scale_log2;
     } else if (fast) {
       const float far = row_max<true>(v);
       const float size = far * fabsf(a.scale_log2);
       mx = size;
-      if (slope2 != 0.f) {
+      if (bias && slope2 != 0.f) {
         base = -slope2 * (float)(i - w.block_of(e0) * 16);
         mx += fmaxf(base, fmaf(slope2, (float)(kStep - 1), base));
       }
-      fast = __all_sync(kFullMask, 2.f * size <= 80.f && far * ku_size < 0.11f && (slope2 == 0.f || j >= full_pre));
+      const bool in = 2.f * size <= 80.f && (!bias || slope2 == 0.f || j >= full_pre);
+      const float u = cap ? far * ku_size : 0.f;
+      fast = __all_sync(kFullMask, in && u < reach);
+      if (cap && (!fast || reach != kCapNear)) {  // the other polynomial, here and from here on
+        const bool near = fast && __all_sync(kFullMask, u < kCapNear);
+        reach = near ? kCapNear : kCapFar;
+        fast = fast || __all_sync(kFullMask, in && u < reach);
+      }
     }
     if (!fast) {
-      if (own_logits) y = apply_rules(a, v, slope2, i, w, e0);
+      if (cap || bias) y = apply_rules(a, cap, bias, v, slope2, i, w, e0);
       if (!full) {
 #pragma unroll
         for (int p = 0; p < N / 16; ++p) {
@@ -897,12 +936,15 @@ __device__ __forceinline__ void softmax_rows(const PrefillAttnArgs& a, Shared<D,
     const float ref = m == -INFINITY ? 0.f : m;
     if (fast) {
       base -= ref;
-      if (a.slopes == nullptr) {
-        l += a.cap_log2 > 0.f ? step_weights<true, false>(v, ts_addr, cap0, cap1, cap2, base, 0.f)
-                              : step_weights<false, false>(v, ts_addr, a.scale_log2, 0.f, 0.f, base, 0.f);
+      const float c0 = cap ? a.cap_log2 * ku : a.scale_log2;
+      if (!bias) {
+        if (!cap) l += step_weights<0, false>(v, ts_addr, c0, 0.f, base, 0.f);
+        else if (reach == kCapNear) l += step_weights<2, false>(v, ts_addr, c0, ku, base, 0.f);
+        else l += step_weights<5, false>(v, ts_addr, c0, ku, base, 0.f);
       } else {
-        l += a.cap_log2 > 0.f ? step_weights<true, true>(v, ts_addr, cap0, cap1, cap2, base, slope2)
-                              : step_weights<false, true>(v, ts_addr, a.scale_log2, 0.f, 0.f, base, slope2);
+        if (!cap) l += step_weights<0, true>(v, ts_addr, c0, 0.f, base, slope2);
+        else if (reach == kCapNear) l += step_weights<2, true>(v, ts_addr, c0, ku, base, slope2);
+        else l += step_weights<5, true>(v, ts_addr, c0, ku, base, slope2);
       }
     } else {
       y.base -= ref;
@@ -1077,6 +1119,7 @@ prefill_attention_kernel(const __grid_constant__ PrefillAttnArgs a) {
     const int x = warp >> 2, r = 32 * (warp & 3) + lane;
     const int tok = r / a.G, head = r - tok * a.G;
     uint32_t n_step = 0;
+    const int mode = (a.cap_log2 > 0.f ? 1 : 0) | (a.slopes != nullptr || !(a.scale_log2 > 0.f) ? 2 : 0);
     for (int it = blockIdx.x; it < total; it = sh.next) {
       Item w = load_item(a, it, NT);
       if (threadIdx.x == 0) {
@@ -1098,8 +1141,23 @@ prefill_attention_kernel(const __grid_constant__ PrefillAttnArgs a) {
       }
       __syncthreads();
       set_keys(w, min(sh.lo_least[0], sh.lo_least[NT - 1]));
-      if (x < w.nx)
-        softmax_rows<D, NT>(a, sh, w, sq, tmem, x, r, valid, i, lo, prow, w.g * a.G + head, n_kv, n_step);
+      if (x < w.nx) {
+        const int h = w.g * a.G + head;
+        auto rows = [&](auto m) {
+          softmax_rows<D, NT, decltype(m)::value>(a, sh, w, sq, tmem, x, r, valid, i, lo, prow, h, n_kv, n_step);
+        };
+        // a loop for each set of rules: one for all is 3 to 5 % slower with a cap (0.88 against 0.84 ms, a chunk
+        // of 4096 on 16384 keys).  One row tile has the registers of half the threads: there the loop for all
+        // serves (64 tokens on 2000 keys 109 us, 114 with four loops, which spill)
+        if constexpr (NT == 1) {
+          rows(std::integral_constant<int, 4>{});
+        } else {
+          if (mode == 0) rows(std::integral_constant<int, 0>{});
+          else if (mode == 1) rows(std::integral_constant<int, 1>{});
+          else if (mode == 2) rows(std::integral_constant<int, 2>{});
+          else rows(std::integral_constant<int, 3>{});
+        }
+      }
       n_kv += 2 * w.nt;
       tc_fence_before();
       __syncthreads();

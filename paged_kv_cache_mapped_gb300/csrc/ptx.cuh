@@ -480,6 +480,13 @@ __device__ __forceinline__ float fmax3(float a, float b, float c) {
   return d;
 }
 
+// 1 / x by the hardware approximation (relative error ~2^-23; 0 for infinity).
+__device__ __forceinline__ float rcp_approx(float x) {
+  float y;
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+
 // 2^x by the hardware approximation (relative error ~2^-22, results below 2^-126 flushed to zero).
 __device__ __forceinline__ float ex2_approx(float x) {
   float y;

@@ -236,3 +236,15 @@ def test_addresses_are_aligned_to_their_elements():
                                                None, P(0x1000), 1 << 40, ctypes.byref(d), None, None)
 
     assert attend(lens=0x1002) == C["PKV_ERR_ALIGNMENT"]
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("new", [[400, 130], [3, 1]], ids=["chunks", "few tokens"])
+@pytest.mark.parametrize("d", [64, 128])
+def test_caps_around_the_scores(d, new):
+    """Scores (normal, up to about 4) far below, near and above the cap, alone and with a distance bias and a
+    prefix: the cap's short and long polynomials and its general form."""
+    c = prefill._case([1700, 900], new, 4, 2, d, 30)
+    for softcap in (60.0, 14.0, 5.0, 1.0, 0.1):
+        prefill._run(c, softcap=softcap)
+        prefill._run(c, softcap=softcap, alibi_slopes=prefill._slopes(4), prefix_lens=[200, 0])
