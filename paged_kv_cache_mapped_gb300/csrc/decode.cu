@@ -728,6 +728,10 @@ decode_split_kernel(const __grid_constant__ DecodeArgs a) {
   // use sl2q = sl2 over that power; o is kept in units of a V-scale reference vref that moves
   // (and rescales o) only when a unit's largest V scale exceeds it by kVrefSlack.
   float sl2q = sl2, vref = 0.f, inv_vref = 0.f;
+  // FP8 pools: the blocks' V scales may be far apart, and a large one may come with weights that are next to
+  // nothing, so o of head h is kept in units of 2^vr, vr a running reference of logit + log2(scale) that moves as
+  // the maximum does (only when exceeded by 2^8); vc = 2^(mr - vr) brings a weight into that unit.
+  float vr0 = -INFINITY, vr1 = -INFINITY, vc0 = 0.f, vc1 = 0.f;
   // INT8 pools: K codes enter q.K as the fp16 numbers 1152 + code (no subtraction per element);
   // each unit's S accumulator starts at -1152 sum_k q'_k of its head instead of 0, computed once
   // per segment by the tensor core from the same q fragments (accumulator layout: rows gq, gq + 8,
@@ -753,6 +757,11 @@ decode_split_kernel(const __grid_constant__ DecodeArgs a) {
       l0 += __shfl_xor_sync(kFullMask, l0, m);
       l1 += __shfl_xor_sync(kFullMask, l1, m);
     }
+    // FP8: what a weight of 2^(logit - mr) counts in o's unit, 2^(vr - mr)
+    auto unit = [&](int hh) {
+      const float m = hh ? mr1 : mr0, vr = hh ? vr1 : vr0;
+      return vr == -INFINITY ? 0.f : exp2f(fminf(vr - m, 127.f));
+    };
 #pragma unroll
     for (int hh = 0; hh < 2; ++hh) {
       const int head = 2 * tq + hh;
@@ -766,7 +775,8 @@ decode_split_kernel(const __grid_constant__ DecodeArgs a) {
         }
         const float inv = l > 0.f ? 1.f / l : 0.f;
         if constexpr (Q8) {  // accumulator rows gq, gq + 8 are columns 2gq, 2gq + 1 of each 16
-          const float f = inv * vref;
+          float f = inv * vref;
+          if constexpr (F8) f = inv * unit(hh);
           __nv_bfloat16* dst = a.out + row * D + 2 * gq;
 #pragma unroll
           for (int mt = 0; mt < KS; ++mt)
@@ -783,9 +793,10 @@ decode_split_kernel(const __grid_constant__ DecodeArgs a) {
         const size_t e = (size_t)seg_slot * G + head;  // a flush writes G adjacent entries
         if constexpr (Q8) {
           float* dst = a.part_o + e * D + 2 * gq;
+          const float f = F8 ? unit(hh) : vref;
 #pragma unroll
           for (int mt = 0; mt < KS; ++mt)
-            *reinterpret_cast<float2*>(dst + mt * 16) = make_float2(o[mt][hh] * vref, o[mt][2 + hh] * vref);
+            *reinterpret_cast<float2*>(dst + mt * 16) = make_float2(o[mt][hh] * f, o[mt][2 + hh] * f);
         } else {
           float* dst = a.part_o + e * D + gq;
 #pragma unroll
@@ -838,6 +849,8 @@ decode_split_kernel(const __grid_constant__ DecodeArgs a) {
       }
       vref = 0.f;
       inv_vref = 0.f;
+      vr0 = vr1 = -INFINITY;
+      vc0 = vc1 = 0.f;
     } else {
 #pragma unroll
       for (int i = 0; i < 2 * KS; ++i) qb[i] = qraw[i];
@@ -1047,14 +1060,15 @@ decode_split_kernel(const __grid_constant__ DecodeArgs a) {
       float vs0 = 0.f, vs1 = 0.f;
       float vm = 0.f;
       if constexpr (F8) {
-        vs0 = vs1 = vm = warps_scales[warp].v[slot][0];
+        vs0 = warps_scales[warp].v[slot][0];
+        vm = fmaxf((float)((__float_as_int(vs0) >> 23) - 127), -100.f);  // log2 of the block's scale, rounded down
       } else if constexpr (Q8) {
         vs0 = t0 ? warps_scales[warp].v[slot][gq] : 0.f;
         vs1 = t1 ? warps_scales[warp].v[slot][gq + 8] : 0.f;
         vm = fmaxf(vs0, vs1);
       }
       bool g0 = mx0 > mr0 + kRescaleSlack, g1 = mx1 > mr1 + kRescaleSlack;
-      bool gv = Q8 && vm > vref * kVrefSlack;
+      bool gv = F8 ? mx0 + vm > vr0 + kRescaleSlack || mx1 + vm > vr1 + kRescaleSlack : Q8 && vm > vref * kVrefSlack;
       if (__any_sync(kFullMask, g0 || g1 || gv)) {
 #pragma unroll
         for (int m = 4; m <= 16; m <<= 1) {
@@ -1063,7 +1077,7 @@ decode_split_kernel(const __grid_constant__ DecodeArgs a) {
         }
         g0 = mx0 > mr0 + kRescaleSlack;
         g1 = mx1 > mr1 + kRescaleSlack;
-        if constexpr (Q8) {  // warp-uniform: the scales of a token are the same in its 4 lanes
+        if constexpr (Q8 && !F8) {  // warp-uniform: the scales of a token are the same in its 4 lanes
 #pragma unroll
           for (int m = 4; m <= 16; m <<= 1) vm = fmaxf(vm, __shfl_xor_sync(kFullMask, vm, m));
           gv = vm > vref * kVrefSlack;
@@ -1079,7 +1093,19 @@ decode_split_kernel(const __grid_constant__ DecodeArgs a) {
         }
         l0 *= al0;
         l1 *= al1;
-        if constexpr (Q8) {
+        if constexpr (F8) {
+          al0 = al1 = 1.f;
+          if (mx0 + vm > vr0 + kRescaleSlack) {
+            al0 = exp2f(vr0 - (mx0 + vm));
+            vr0 = mx0 + vm;
+          }
+          if (mx1 + vm > vr1 + kRescaleSlack) {
+            al1 = exp2f(vr1 - (mx1 + vm));
+            vr1 = mx1 + vm;
+          }
+          vc0 = vr0 == -INFINITY ? 0.f : exp2f(mr0 - vr0);
+          vc1 = vr1 == -INFINITY ? 0.f : exp2f(mr1 - vr1);
+        } else if constexpr (Q8) {
           if (gv) {  // o moves to the new V reference (o is zero while vref is)
             const float fv = vref > 0.f ? vref / vm : 0.f;
             al0 *= fv;
@@ -1104,10 +1130,15 @@ decode_split_kernel(const __grid_constant__ DecodeArgs a) {
       l1 += p01 + p11;
       // -- P^T as B fragments (tokens x heads -> heads x tokens) ---------------------------
       // INT8 pools: P times each token's V scale over vref (at most 2^8 * slack) as one fp16
-      // term (11 significant bits, below the bf16 output's rounding);
+      // term (11 significant bits, below the bf16 output's rounding); FP8: P times the block's V scale over 2^vr (at
+      // most 2^9), likewise;
       // bf16: a hi + lo pair of bf16 terms (8 bits alone would not be)
       uint32_t hA, hB, lA = 0u, lB = 0u;
-      if constexpr (Q8) {
+      if constexpr (F8) {
+        const float r0 = vs0 * vc0, r1 = vs0 * vc1;
+        hA = pack_f16x2(p00 * r0, p01 * r1);
+        hB = pack_f16x2(p10 * r0, p11 * r1);
+      } else if constexpr (Q8) {
         const float r0 = vs0 * inv_vref, r1 = vs1 * inv_vref;
         hA = pack_f16x2(p00 * r0, p01 * r0);
         hB = pack_f16x2(p10 * r1, p11 * r1);

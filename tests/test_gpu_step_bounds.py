@@ -9,6 +9,7 @@ import pytest
 import torch
 
 import paged_kv_cache_mapped_gb300 as pkv
+import test_gpu_decode_rules as decode
 import test_gpu_prefill_attention as prefill
 from helpers import paged_from_contiguous, rand_bf16
 from paged_kv_cache_mapped_gb300 import _lib, header_constants
@@ -248,3 +249,14 @@ def test_caps_around_the_scores(d, new):
     for softcap in (60.0, 14.0, 5.0, 1.0, 0.1):
         prefill._run(c, softcap=softcap)
         prefill._run(c, softcap=softcap, alibi_slopes=prefill._slopes(4), prefix_lens=[200, 0])
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("slope", [-1.5, 0.25, 3.0])
+@pytest.mark.parametrize("d", [64, 128])
+def test_fp8_blocks_of_large_values_under_small_weights(d, slope):
+    """V scales up to 2^40 apart with a distance bias that leaves the large blocks of some rows next to no
+    weight: the small blocks that carry those rows keep their digits."""
+    c = decode._case([300, 40, 17, 1700], 8, 2, d, 8, True, vscale=40)
+    decode._check(c, decode._call(c, alibi_slopes=[slope] * 8), alibi_slopes=[slope] * 8)
+    decode._check(c, decode._call(c, softcap=3.0, alibi_slopes=[slope] * 8), softcap=3.0, alibi_slopes=[slope] * 8)
