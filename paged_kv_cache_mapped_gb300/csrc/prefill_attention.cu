@@ -533,7 +533,9 @@ __device__ __forceinline__ void produce(const PrefillAttnArgs& a, Shared<D, NT>&
 // lane; what the MMAs take is the same in every lane and kept in uniform registers).  S has two buffers of 64
 // keys in tensor memory, and P takes the place of its S: while the softmax works on a step, S of the next one
 // is there, and that of the step after follows the product that reads P from its columns (the tensor core runs
-// one thread's MMAs in the order of issue).
+// one thread's MMAs in the order of issue).  One product for a whole 128-key tile, a third fewer MMAs and a
+// quarter less tensor time, leaves no room for the second buffer and is slower (chunk of 4096 on 16384: 863
+// against 720 us): the softmax then waits out every product.
 // Beside the softmax warps a thread needs 60 to 120 cycles an MMA and a hundred or more for each barrier: one
 // issuer for two row tiles leaves the tensor core idle (chunk of 4096 on 16384, plain, 1.07 ms; one for each
 // 0.92; one for each product of each 0.75 against 0.72, its warps taking issue slots from the softmax).  With
