@@ -17,13 +17,16 @@ namespace {
 // Three exclusive sums over the sequences (new tokens, blocks to take, blocks given back) decide
 // everything: the place of each token in the packed batch, of each taken block on the free stack
 // and of each pushed block.  The kernel reads a few bytes per sequence and writes 12 per token, so
-// its floor is the launch and a chain of dependent loads.  One cluster runs it, of one CTA or (large steps) of
-// eight: every CTA has all the sums, the tokens and blocks are dealt out, and the cluster's barriers put the
-// checks of all inputs before the first write without a word of workspace.
+// its floor is the launch and a chain of dependent loads (64 decoding sequences 4.4 us, 4096 with prompts among
+// them 17 us on the GPU).  One cluster runs it, of one CTA or (large steps) of eight: every CTA has all the
+// sums, the tokens and blocks are dealt out, and the cluster's barriers put the checks of all inputs before the
+// first write without a word of workspace.
 constexpr int kStepThreads = 1024;
 constexpr int kStepRunMost = kMaxStepBatch / kStepThreads;
 constexpr int kStepCluster = 8;
-constexpr int kStepLarge = 2048;  // more tokens or sequences than this are for eight CTAs
+// More tokens or sequences than this are for eight CTAs (us with one and with eight: 64 tokens 4.4, 5.8; 2048 of
+// as many sequences 8.2, 8.6; 4096 of 16 sequences 6.4, 6.3; 4096 of as many 12.4, 10.3; 64000 61.7, 8.5).
+constexpr int kStepLarge = 2048;
 
 // The largest i < n with start[i] <= x (start ascending, start[0] = 0, x below the total, so that
 // entry owns x: of equal starts the last one has the items).
@@ -36,7 +39,7 @@ __device__ __forceinline__ int owner_of(const int* start, int n, int x) {
   return lo;
 }
 
-// kStepRun: sequences of a thread.  CLUSTER: eight CTAs, or one (whose barriers are the block's, 1.7 us less).
+// kStepRun: sequences of a thread.  CLUSTER: eight CTAs, or one (whose barriers are the block's).
 template <int kStepRun, bool CLUSTER>
 __global__ void __launch_bounds__(kStepThreads) step_tables_kernel(const StepArgs a) {
   namespace cg = cooperative_groups;
@@ -369,10 +372,12 @@ __device__ __forceinline__ void append_run(uint8_t* kq, uint8_t* vq, float* ks, 
 
 // The first token of a block in the call leads the block's run of adjacent tokens, and one warp takes the run
 // for one kv head, so a block's scale has one writer.  Lanes 0-15 hold the K rows, lanes 16-31 the V rows,
-// D / 16 elements each; all rows of a run are loaded before any is used.  A CTA has a window of up to 32 tokens,
-// whose leaders times kv heads its warps share: with a window of 1 (few tokens) every run has its own CTA, with
-// 16 (prompts) a CTA has one or two runs of 16 tokens instead of 16 CTAs of which 15 end at once.  The bytes
-// bound it (16 prompts of ~4000, 8 heads, d 128, 388 MB: 288 -> 80.6 us, 71 % of the copy rate; three CTAs an SM spill and are no faster).
+// D / 16 elements each; all rows of a run are loaded before any is used.  A CTA has a window of tokens, whose
+// leaders times kv heads its warps share: one token where there are few (64 decoding sequences, 8 heads, 2.5 us;
+// in windows of 16 one CTA would have 128 runs, 18.9 us), 16 where there are many (64000 tokens of prompts 79.5 us;
+// a CTA a token, of which 15 of 16 end at once, 221 us), between them by what fills the GPU.  The bytes bound it (16
+// prompts of ~4000, 8 heads, d 128, 388 MB: 80 us, 71 % of the copy rate; three CTAs an SM spill and are no
+// faster).
 constexpr int kAppendWarps = 8;
 
 template <int D>
