@@ -260,3 +260,51 @@ def test_fp8_blocks_of_large_values_under_small_weights(d, slope):
     c = decode._case([300, 40, 17, 1700], 8, 2, d, 8, True, vscale=40)
     decode._check(c, decode._call(c, alibi_slopes=[slope] * 8), alibi_slopes=[slope] * 8)
     decode._check(c, decode._call(c, softcap=3.0, alibi_slopes=[slope] * 8), softcap=3.0, alibi_slopes=[slope] * 8)
+
+
+@pytest.mark.gpu
+def test_blocks_past_32_bits():
+    """Pools of more than 2^32 bytes: sequences at the far end give what the same rows give in a small pool, and
+    the append writes its codes and scales there."""
+    hq, hkv, d, B = 8, 8, 128, 2
+    lens, new = [300, 77], [40, 1]
+    c = prefill._case(lens, new, hq, hkv, d, 31, fill=0.0)
+    small, bt = c["pools"], c["bt"]
+    n = small[0].shape[0]
+    q, starts, ld = c["q"].to(DEV), torch.from_numpy(c["starts"]).to(DEV), _i32(lens)
+    r = dict(softcap=5.0, prefix_lens=_i32([9, 0]))
+    want = pkv.paged_prefill_attention(q, *small, bt, ld, starts, c["scale"], 200, **r)
+    want_d = pkv.paged_decode_attention_rules(q[:B], *small, bt, ld, c["scale"], 200, **r)
+    nb = (1 << 32) // (hkv * 16 * d) + 2 * n
+    far = torch.where(bt >= 0, bt + nb - n, bt)
+    big = []
+    for p in small:
+        t = torch.empty((nb, hkv, 16, d), dtype=torch.bfloat16, device=DEV)
+        t[nb - n:] = p
+        big.append(t)
+    err = pkv.new_error_word(DEV)
+    assert torch.equal(pkv.paged_prefill_attention(q, *big, far, ld, starts, c["scale"], 200, error_word=err, **r), want)
+    assert torch.equal(pkv.paged_decode_attention_rules(q[:B], *big, far, ld, c["scale"], 200, error_word=err, **r), want_d)
+    rows = [big[0][nb - n:].transpose(1, 2).reshape(n * 16, hkv, d).clone(), big[1][nb - n:].transpose(1, 2).reshape(n * 16, hkv, d).clone()]
+    del big
+    got = []
+    for first, total in ((0, n), (nb - n, nb)):
+        codes = [torch.zeros((total, hkv, 16, d), dtype=torch.uint8, device=DEV).view(torch.float8_e4m3fn) for _ in range(2)]
+        scales = [torch.zeros((total, hkv), device=DEV) for _ in range(2)]
+        pkv.kv_append_f8(*codes, *scales, *rows, torch.arange(n * 16, device=DEV) + first * 16, error_word=err)
+        out = pkv.paged_decode_attention_f8(q[:B], *codes, *scales, far if first else bt, ld, c["scale"], 200, error_word=err, **r)
+        got.append([x[first:].view(torch.uint8).clone() for x in codes] + [x[first:].clone() for x in scales] + [out])
+        del codes, scales
+    assert pkv.read_error(err) == 0
+    assert all(torch.equal(x, y) for x, y in zip(*got))
+
+
+@pytest.mark.gpu
+def test_a_prompt_of_131072_tokens():
+    """The plan's lists far past its shared memory, and rows at both ends of a long prompt."""
+    n = 131072
+    c = prefill._case([n], [n], 4, 1, 64, 32)
+    err = pkv.new_error_word(DEV)
+    got = prefill._call(c, error_word=err, window=5000, prefix_lens=[100])
+    assert pkv.read_error(err) == 0
+    prefill._check(c, got, rows=[(x, x % 4) for x in (0, 1, 127, 4999, 5000, 65535, 100001, n - 2, n - 1)], window=5000, prefix_lens=[100])
