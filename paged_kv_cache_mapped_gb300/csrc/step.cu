@@ -254,24 +254,19 @@ __device__ __forceinline__ float needed_scale(float amax) {
   return __int_as_float((e + 127) << 23);
 }
 
-// One run for one kv head: `tok` leads it.
+// One run for one kv head: `tok` leads it; lane l has the slot of token tok + l (l < 16; -1 past the last).
 template <int D>
 __device__ __forceinline__ void append_run(uint8_t* kq, uint8_t* vq, float* ks, float* vs, const __nv_bfloat16* k,
-                                           const __nv_bfloat16* v, const int64_t* slots, int64_t T, int Hkv,
-                                           int64_t tok, int g, int32_t* err) {
+                                           const __nv_bfloat16* v, int64_t lane_slot, int Hkv, int64_t tok, int g,
+                                           int32_t* err) {
   constexpr int E = D / 16;   // elements per lane
   constexpr int W = E / 2;    // words of two bf16
+  constexpr int kRows = 8;    // in registers at a time
   const int lane = threadIdx.x & 31;
-  const int64_t slot = __ldg(slots + tok);
+  const int64_t slot = __shfl_sync(kFullMask, lane_slot, 0);
   const int64_t blk = slot >> 4;
-  // the run: lane l looks at token tok + l, which belongs while every one up to it is in the block
-  // and above the one before
-  int off = -1;
-  {
-    int64_t s = -1;
-    if (lane < 16 && tok + lane < T) s = __ldg(slots + tok + lane);
-    if (s >= 0 && (s >> 4) == blk) off = (int)(s & 15);
-  }
+  // the run: token tok + l belongs while every one up to it is in the block and above the one before
+  const int off = lane < 16 && lane_slot >= 0 && (lane_slot >> 4) == blk ? (int)(lane_slot & 15) : -1;
   const int prev = __shfl_up_sync(kFullMask, off, 1);
   const uint32_t in_run = __ballot_sync(kFullMask, off >= 0 && (lane == 0 || off > prev));
   const int run = __ffs(~in_run) - 1;
@@ -279,33 +274,48 @@ __device__ __forceinline__ void append_run(uint8_t* kq, uint8_t* vq, float* ks, 
 
   const int h = lane & 15;
   const __nv_bfloat16* src = (lane < 16 ? k : v) + ((size_t)tok * Hkv + g) * D + h * E;
-  uint32_t x[16][W];
-  uint32_t good = 0;  // tokens of the run whose K and V rows are finite
+  uint32_t bad = 0;
   uint32_t most = 0;  // largest |x| so far as bf16 bits, a pair of 16-bit numbers (sign cleared they order like the values)
+  uint32_t x[kRows][W];
+  auto load = [&](int r0) {
 #pragma unroll
-  for (int r = 0; r < 16; ++r) {
-    if (r >= run) break;
-    const __nv_bfloat16* p = src + (size_t)r * Hkv * D;
-    if constexpr (W == 4) {
-      const uint4 w = __ldg(reinterpret_cast<const uint4*>(p));
-      x[r][0] = w.x; x[r][1] = w.y; x[r][2] = w.z; x[r][3] = w.w;
-    } else {
-      const uint2 w = __ldg(reinterpret_cast<const uint2*>(p));
-      x[r][0] = w.x; x[r][1] = w.y;
+    for (int r = 0; r < kRows; ++r) {
+      if (r0 + r >= run) break;
+      const __nv_bfloat16* p = src + (size_t)(r0 + r) * Hkv * D;
+      if constexpr (W == 4) {
+        const uint4 w = __ldg(reinterpret_cast<const uint4*>(p));
+        x[r][0] = w.x; x[r][1] = w.y; x[r][2] = w.z; x[r][3] = w.w;
+      } else {
+        const uint2 w = __ldg(reinterpret_cast<const uint2*>(p));
+        x[r][0] = w.x; x[r][1] = w.y;
+      }
+    }
+  };
+  for (int r0 = 0; r0 < run; r0 += kRows) {
+    load(r0);
+#pragma unroll
+    for (int r = 0; r < kRows; ++r) {
+      if (r0 + r >= run) break;
+      uint32_t m = x[r][0] & 0x7fff7fffu;
+#pragma unroll
+      for (int i = 1; i < W; ++i) m = __vmaxu2(m, x[r][i] & 0x7fff7fffu);
+      if ((m & 0xffffu) >= 0x7f80u || (m >> 16) >= 0x7f80u) bad |= 1u << (r0 + r);
+      most = __vmaxu2(most, m);
     }
   }
+  bad = __reduce_or_sync(kFullMask, bad);  // tokens of the run with a non-finite element in their K or V row
+  const uint32_t good = ((1u << run) - 1u) & ~bad;
+  if (bad != 0) {  // the other rows' largest, once more
+    if (lane == 0) record_error(err, PKV_DEV_BAD_VALUE);
+    most = 0;
+    for (int r0 = 0; r0 < run; r0 += kRows) {
+      load(r0);
 #pragma unroll
-  for (int r = 0; r < 16; ++r) {
-    if (r >= run) break;
-    uint32_t m = x[r][0] & 0x7fff7fffu;
+      for (int r = 0; r < kRows; ++r) {
+        if (!((good >> (r0 + r)) & 1u)) continue;
 #pragma unroll
-    for (int i = 1; i < W; ++i) m = __vmaxu2(m, x[r][i] & 0x7fff7fffu);
-    const bool finite = (m & 0xffffu) < 0x7f80u && (m >> 16) < 0x7f80u;
-    if (__all_sync(kFullMask, finite)) {
-      good |= 1u << r;
-      most = __vmaxu2(most, m);
-    } else if (lane == 0) {
-      record_error(err, PKV_DEV_BAD_VALUE);
+        for (int i = 0; i < W; ++i) most = __vmaxu2(most, x[r][i] & 0x7fff7fffu);
+      }
     }
   }
   if (good == 0) return;
@@ -337,51 +347,58 @@ __device__ __forceinline__ void append_run(uint8_t* kq, uint8_t* vq, float* ks, 
       }
     }
   }
+  // the run's offsets, four bits each
+  const uint32_t own = lane < run ? (uint32_t)off << (4 * (lane & 7)) : 0u;
+  const uint32_t offs0 = __reduce_or_sync(kFullMask, lane < 8 ? own : 0u), offs1 = __reduce_or_sync(kFullMask, lane < 8 ? 0u : own);
   // x / scale: by the exact reciprocal where the scale is a power of two (every scale that the append
   // makes), by a division where the caller's own scale is not
   const bool pow2 = (__float_as_int(now) & 0x7fffff) == 0 && now >= 1.1754944e-38f;
   const float inv = pow2 ? __frcp_rn(now) : 0.f;
+  for (int r0 = 0; r0 < run; r0 += kRows) {
+    load(r0);
 #pragma unroll
-  for (int r = 0; r < 16; ++r) {
-    if (r >= run) break;
-    const int o = __shfl_sync(kFullMask, off, r);
-    if (!((good >> r) & 1u)) continue;
-    uint32_t out[E / 4];
-    if (pow2) {
-      const uint64_t inv2 = pack2(inv, inv);
+    for (int r = 0; r < kRows; ++r) {
+      if (!((good >> (r0 + r)) & 1u)) continue;
+      const int o = (int)(((r0 + r < 8 ? offs0 : offs1) >> (4 * ((r0 + r) & 7))) & 15u);
+      uint32_t out[E / 4];
+      if (pow2) {
+        const uint64_t inv2 = pack2(inv, inv);
 #pragma unroll
-      for (int i = 0; i < E / 4; ++i) {
-        const float2 a = unpack2(fmul2(bf16x2_to_f32x2(x[r][2 * i]), inv2));
-        const float2 b = unpack2(fmul2(bf16x2_to_f32x2(x[r][2 * i + 1]), inv2));
-        out[i] = pack_e4m3x2(a.x, a.y) | (pack_e4m3x2(b.x, b.y) << 16);
+        for (int i = 0; i < E / 4; ++i) {
+          const float2 a = unpack2(fmul2(bf16x2_to_f32x2(x[r][2 * i]), inv2));
+          const float2 b = unpack2(fmul2(bf16x2_to_f32x2(x[r][2 * i + 1]), inv2));
+          out[i] = pack_e4m3x2(a.x, a.y) | (pack_e4m3x2(b.x, b.y) << 16);
+        }
+      } else {
+#pragma unroll
+        for (int i = 0; i < E / 4; ++i)
+          out[i] = pack_e4m3x2(__fdiv_rn(bf16_lo_to_f32(x[r][2 * i]), now), __fdiv_rn(bf16_hi_to_f32(x[r][2 * i]), now)) |
+                   (pack_e4m3x2(__fdiv_rn(bf16_lo_to_f32(x[r][2 * i + 1]), now),
+                                __fdiv_rn(bf16_hi_to_f32(x[r][2 * i + 1]), now)) << 16);
       }
-    } else {
-#pragma unroll
-      for (int i = 0; i < E / 4; ++i)
-        out[i] = pack_e4m3x2(__fdiv_rn(bf16_lo_to_f32(x[r][2 * i]), now), __fdiv_rn(bf16_hi_to_f32(x[r][2 * i]), now)) |
-                 (pack_e4m3x2(__fdiv_rn(bf16_lo_to_f32(x[r][2 * i + 1]), now),
-                              __fdiv_rn(bf16_hi_to_f32(x[r][2 * i + 1]), now)) << 16);
+      if constexpr (E == 8)
+        *reinterpret_cast<uint2*>(codes + o * D) = make_uint2(out[0], out[1]);
+      else
+        *reinterpret_cast<uint32_t*>(codes + o * D) = out[0];
     }
-    if constexpr (E == 8)
-      *reinterpret_cast<uint2*>(codes + o * D) = make_uint2(out[0], out[1]);
-    else
-      *reinterpret_cast<uint32_t*>(codes + o * D) = out[0];
   }
   if (h == 0 && now != old) *scale_at = now;
 }
 
 // The first token of a block in the call leads the block's run of adjacent tokens, and one warp takes the run
-// for one kv head, so a block's scale has one writer.  Lanes 0-15 hold the K rows, lanes 16-31 the V rows,
-// D / 16 elements each; all rows of a run are loaded before any is used.  A CTA has a window of tokens, whose
-// leaders times kv heads its warps share: one token where there are few (64 decoding sequences, 8 heads, 2.5 us;
-// in windows of 16 one CTA would have 128 runs, 18.9 us), 16 where there are many (64000 tokens of prompts 79.5 us;
-// a CTA a token, of which 15 of 16 end at once, 221 us), between them by what fills the GPU.  The bytes bound it (16
-// prompts of ~4000, 8 heads, d 128, 388 MB: 80 us, 71 % of the copy rate; three CTAs an SM spill and are no
-// faster).
+// for one kv head, so a block's scale has one writer.  Lanes 0-15 have the K rows, lanes 16-31 the V rows,
+// D / 16 elements each, eight rows at a time: once for the maxima, and again (from L1) for the codes, which leaves
+// registers for four CTAs an SM (all 16 rows kept: two, 69.0 against 59.6 us for 64000 tokens).  A CTA has a
+// window of tokens, whose leaders times kv heads its warps share, and brings the window's rows into L2 while its
+// slots are read (80.1 -> 73.2 us then).  The window is one token where there are few (64 decoding sequences, 8
+// heads, 2.5 us; in windows of 16 one CTA would have 128 runs, 18.9 us), 16 where there are many (64000 tokens; a CTA
+// a token, of which 15 of 16 end at once, 225 us), between them what lets all CTAs run at once (4096 tokens of
+// prompts 8.6 us and of as many sequences 15.1; with half as many CTAs 7.5 and 19.9).  The bytes bound it: 64000
+// tokens, 8 heads, d 128, 393 MB, 6.6 TB/s.
 constexpr int kAppendWarps = 8;
 
 template <int D>
-__global__ void __launch_bounds__(kAppendWarps * 32, 2)
+__global__ void __launch_bounds__(kAppendWarps * 32, 4)
 kv_append_f8_kernel(uint8_t* __restrict__ kq, uint8_t* __restrict__ vq, float* __restrict__ ks, float* __restrict__ vs,
                     const __nv_bfloat16* __restrict__ k, const __nv_bfloat16* __restrict__ v,
                     const int64_t* __restrict__ slots, int64_t T, int Hkv, int NB, int window, int32_t* err) {
@@ -389,13 +406,19 @@ kv_append_f8_kernel(uint8_t* __restrict__ kq, uint8_t* __restrict__ vq, float* _
   grid_dependency_wait();
   grid_launch_dependents();
   const int64_t tok0 = (int64_t)blockIdx.x * window;
+  if (window > 1 && threadIdx.x == 0) {  // the window's rows on their way while its slots are read
+    const uint32_t bytes = (uint32_t)(min((int64_t)window, T - tok0) * Hkv * D * 2);
+    prefetch_l2(k + tok0 * Hkv * D, bytes);
+    prefetch_l2(v + tok0 * Hkv * D, bytes);
+  }
   uint32_t leaders;
+  int64_t slot = -1;  // of token tok0 + lane: the window's, and 15 more for the run of its last
   {
     int code = 0;
     bool leads = false;
     const int64_t t = tok0 + lane;
+    if (t < T) slot = __ldg(slots + t);
     if (lane < window && t < T) {
-      const int64_t slot = __ldg(slots + t);
       const int64_t before = t > 0 ? __ldg(slots + t - 1) : -1;
       if (slot >= (int64_t)NB * 16) code = PKV_DEV_BAD_SLOT;
       else if (slot >= 0) {
@@ -409,8 +432,9 @@ kv_append_f8_kernel(uint8_t* __restrict__ kq, uint8_t* __restrict__ vq, float* _
   const int runs = __popc(leaders);
   for (int item = warp; item < runs * Hkv; item += kAppendWarps) {
     const int nth = item / Hkv, g = item - nth * Hkv;
-    const int64_t tok = tok0 + (int)__fns(leaders, 0, nth + 1);
-    append_run<D>(kq, vq, ks, vs, k, v, slots, T, Hkv, tok, g, err);
+    const int at = (int)__fns(leaders, 0, nth + 1);
+    const int64_t lane_slot = __shfl_sync(kFullMask, slot, (at + lane) & 31);
+    append_run<D>(kq, vq, ks, vs, k, v, lane_slot, Hkv, tok0 + at, g, err);
   }
 }
 
@@ -451,8 +475,8 @@ cudaError_t launch_step_tables(const StepArgs& a, cudaStream_t stream) {
 cudaError_t launch_kv_append_f8(void* kq, void* vq, float* ks, float* vs, const void* k, const void* v,
                                 const int64_t* slots, int64_t T, int Hkv, int D, int NB, int32_t* err,
                                 cudaStream_t stream) {
-  // the window: as many tokens as leave about two CTAs for each place on the GPU (two of 152 SMs)
-  int window = (int)std::min<int64_t>(16, std::max<int64_t>(1, T * Hkv / (kAppendWarps * 2 * 304)));
+  // the window: as many tokens as let all CTAs run at once (four on each of 152 SMs)
+  int window = (int)std::min<int64_t>(16, (T + 607) / 608);
   const int64_t blocks = (T + window - 1) / window;
   void* params[] = {&kq, &vq, &ks, &vs, &k, &v, &slots, &T, &Hkv, &NB, &window, &err};
   const void* f = D == 128 ? (const void*)kv_append_f8_kernel<128> : (const void*)kv_append_f8_kernel<64>;
