@@ -25,7 +25,8 @@
 // P is rounded to bf16 for the product (the sum takes it in fp32).  Rows over more than kTwoTermTiles key
 // tiles take that one term: its error, at most 2^-8 of each weight and independent from key to key, is of the
 // size of a bf16 output's own rounding.  Shorter rows, where few weights may carry the result, add the
-// remainder as a second term, which costs half as many MMAs again.
+// remainder as a second term, which costs half as many MMAs again (all rows in two terms: chunk of 4096 on 16384
+// 937 us against 730; none: 24 mixed sequences 26.3 against 28.5).
 // Non-finite V: a masked key's weight is 0, and 0 * NaN is NaN, so V rows past the sequence are cleared,
 // and an output row that is not finite is computed again key by key over what it sees.
 // Every wait is bounded; bad block ids are cleared tiles, recorded.
@@ -1297,8 +1298,10 @@ cudaError_t launch_attention(const PrefillAttnArgs& a, cudaStream_t stream) {
   args.slots = std::min(a.sms, kMaxSms) * GE::kCtas;
   int per_item = NT * a.R;
   void* plan_params[] = {&args, &per_item};
-  cudaError_t e = launch_pdl((const void*)prefill_plan_kernel, dim3(1),
-                             dim3(a.B > 256 || a.T > 16384 ? 1024 : 256), plan_smem_bytes(a.B), stream, plan_params);
+  // a whole call with a plan of 512 and of 1024 threads, us: one token 19.1, 20.0; 24 mixed sequences 28.1, 28.9; 300
+  // sequences 39.1, 40.3; 1000 37.6, 36.5; 4000 114, 106 (256 threads: 19.3, 28.5, 41.2, 42.4, 140)
+  cudaError_t e = launch_pdl((const void*)prefill_plan_kernel, dim3(1), dim3(a.B > 512 ? 1024 : 512), plan_smem_bytes(a.B),
+                             stream, plan_params);
   if (e != cudaSuccess) return e;
   void* params[] = {&args};
   const long long most = ((long long)a.T / per_item + a.B) * a.Hkv + 2 * args.slots;
