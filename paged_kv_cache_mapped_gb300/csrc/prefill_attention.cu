@@ -405,12 +405,11 @@ struct Steps {
   int hi, lo;
 };
 
-__device__ __forceinline__ Item load_item(const PrefillAttnArgs& a, int it, int NT) {
+// p, q: the record of item it.
+__device__ __forceinline__ Item item_of(const PrefillAttnArgs& a, int it, int4 p, int4 q, int NT) {
   Item w;
-  const int at = it / a.Hkv;
-  const int4 p = a.plan_items[2 * at], q = a.plan_items[2 * at + 1];
   w.b = p.x;
-  w.g = it - at * a.Hkv;
+  w.g = it % a.Hkv;
   w.row0 = p.y;
   w.tokens = p.z;
   w.pos0 = p.w;
@@ -451,6 +450,7 @@ struct Shared {
   uint64_t s_full[NT][2], p_full[NT][2], pv_done[NT][2];  // by buffer: S ready, P ready, P V added
   uint64_t drained[2];  // after a timeout: an issuer's MMAs have ended
   uint32_t tmem;
+  int4 record[2];                       // of the next item
   int lo_least[NT], lo_most[NT], abort, next;  // interval starts of the row tiles' rows
 };
 
@@ -1112,6 +1112,9 @@ prefill_attention_kernel(const __grid_constant__ PrefillAttnArgs a) {
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = sh.tmem;
+  // (a CTA without an item reads past the list's end, inside the workspace)
+  const int4* first = a.plan_items + 2 * ((int)blockIdx.x / a.Hkv);
+  int4 rec0 = first[0], rec1 = first[1];
   const int total = a.plan_head[0] * a.Hkv;
   // Each role has the whole item loop, so that its registers are its own.  Three block barriers an item:
   // the shared minimum is reset, it is complete, every role has left the item.
@@ -1123,8 +1126,8 @@ prefill_attention_kernel(const __grid_constant__ PrefillAttnArgs a) {
     const int tok = r / a.G, head = r - tok * a.G;
     uint32_t n_step = 0;
     const int mode = (a.cap_log2 > 0.f ? 1 : 0) | (a.slopes != nullptr || !(a.scale_log2 > 0.f) ? 2 : 0);
-    for (int it = blockIdx.x; it < total; it = sh.next) {
-      Item w = load_item(a, it, NT);
+    for (int it = blockIdx.x; it < total; it = sh.next, rec0 = sh.record[0], rec1 = sh.record[1]) {
+      Item w = item_of(a, it, rec0, rec1, NT);
       if (threadIdx.x == 0) {
         for (int y = 0; y < NT; ++y) {
           sh.lo_least[y] = 0x7fffffff;
@@ -1170,8 +1173,8 @@ prefill_attention_kernel(const __grid_constant__ PrefillAttnArgs a) {
     setmaxnreg_dec<GE::kOtherRegs>();
     uint32_t n_step = 0;
     const uint32_t leader = elect_one();
-    for (int it = blockIdx.x; it < total; it = sh.next) {
-      Item w = load_item(a, it, NT);
+    for (int it = blockIdx.x; it < total; it = sh.next, rec0 = sh.record[0], rec1 = sh.record[1]) {
+      Item w = item_of(a, it, rec0, rec1, NT);
       __syncthreads();
       __syncthreads();
       set_keys(w, min(sh.lo_least[0], sh.lo_least[NT - 1]));
@@ -1190,8 +1193,15 @@ prefill_attention_kernel(const __grid_constant__ PrefillAttnArgs a) {
         }
         ++n_q;
       }
-      // the next item's ticket is taken meanwhile
-      if (warp == GE::kTicket && lane == 0) sh.next = (int)gridDim.x + atomicAdd(a.plan_head + 1, 1);
+      // meanwhile the next item's ticket is taken, its record read
+      if (warp == GE::kTicket && lane == 0) {
+        const int next = (int)gridDim.x + atomicAdd(a.plan_head + 1, 1);
+        sh.next = next;
+        if (next < total) {
+          sh.record[0] = a.plan_items[2 * (next / a.Hkv)];
+          sh.record[1] = a.plan_items[2 * (next / a.Hkv) + 1];
+        }
+      }
       __syncwarp();
       __syncthreads();
       if (sh.abort != 0) break;
