@@ -19,7 +19,7 @@
 // What bounds it: long chunks the MMAs' issue and rate and the exponentials together (4096 tokens on 16384 keys, 32 / 8 heads,
 // d 128: 720-730 us, 1320-1340 TFLOP/s, 69 % of the measured bf16 rate; with a distance bias 810; capped 841 where
 // the scores stay below a fifth of the cap, 1045 below 0.8 of it, 1520 beyond); many
-// single tokens the bytes (64 on 2000 keys each 109 us, 4.8 TB/s; 4 on 131072 361 us, 5.9 TB/s); small batches the
+// single tokens the bytes (64 on 2000 keys each 109 us, 4.8 TB/s; 4 on 131072 338 us, 6.4 TB/s); small batches the
 // chain of plan, first loads and merge (one token on 200 keys 19 us).  A CTA holds two row tiles
 // because every K and V tile that comes into shared memory then serves 256 rows.
 // P is rounded to bf16 for the product (the sum takes it in fp32).  Rows over more than kTwoTermTiles key
@@ -90,7 +90,7 @@ constexpr int kStepBlocks = kStep / 16;
 constexpr int kHalf = kKeys * 128;   // bytes of one 64-element half of a tile
 constexpr float kSlack = 8.0f;       // the running maximum moves only when exceeded by this (base 2)
 constexpr int kTwoTermTiles = 4;     // rows over at most this many key tiles take P as two bf16 terms (above)
-constexpr int kMinChunk = 4;         // key tiles of a split item at least (with 2: mixed 24 36 -> 52 us)
+constexpr int kMinChunk = 4;         // key tiles of a share at least where items outnumber the CTAs
 
 template <int D, int NT>
 struct Geo {
@@ -119,9 +119,10 @@ struct Geo {
 // run at a time.
 //  * P < slots: every entry is cut into shares of at most c key tiles, c chosen among ktmax / s for a few s for
 //    the least estimate of the end, an item costing a tile beside its own: c + 1 where all shares run at once,
-//    else the smaller of the mean + c (any list schedule) and the rounds times c + 1; and 4 tiles' time plus one
+//    else the smaller of the mean + c (any list schedule) and the rounds times c + 1; and a tile's time plus one
 //    for 2000 rows where rows have to be merged (2 x 300 tokens of 1000, 19200 rows: 31 us whole, 51 us in two
-//    shares; 4 single tokens of 131072 keys: 361 us in 19 shares each, 379 in 16).
+//    shares; 4 single tokens of 131072 keys: 342 us in 19 shares each, 359 in 16; 3 sequences of ~500 keys, 12 tokens:
+//    18.4 us in shares of a tile, 24.8 whole).
 //  * P >= slots: entries above one and a half times the fair share W / slots are cut to that.  If there are
 //    none, the last P mod slots items, which would leave most CTAs idle for a whole item, are cut in s shares each (chunk of 4096 on 16384,
 //    512 items on 152 CTAs: 56 items in two shares, capped 0.99 -> 0.87 ms).
@@ -245,7 +246,7 @@ __global__ void __launch_bounds__(1024) prefill_plan_kernel(const PrefillAttnArg
       const int sp = q < 6    ? q + 1
                      : q < 13 ? (q & 1) ? 5 << ((q >> 1) - 2) : 4 << ((q >> 1) - 2)
                               : min(kMaxShares, q == 13 ? once : q == 14 ? 2 * once : (int)(2 * a.slots / P));
-      const int c = max(kMinChunk, (ktmax + sp - 1) / sp);
+      const int c = (ktmax + sp - 1) / sp;
       int shares = 0, rows = 0;
       for (int e = lane; e < entries; e += 32) {
         const int n = min(kMaxShares, max(1, (s_kt[e] + c - 1) / c));
@@ -258,7 +259,7 @@ __global__ void __launch_bounds__(1024) prefill_plan_kernel(const PrefillAttnArg
       if (sp > 1 && items > 2 * a.slots) continue;
       long long end = c + 1;
       if (items > a.slots) end = min((W + items) / a.slots + c, (items + a.slots - 1) / a.slots * end);
-      if (rows > 0) end += 4 + (long long)rows * a.Hq / 2000;
+      if (rows > 0) end += 1 + (long long)rows * a.Hq / 2000;
       if (lane == 0) atomicMin(&s_best, (unsigned long long)end << 32 | (0xffffffffu - (unsigned)c));
     }
     __syncthreads();
@@ -1222,7 +1223,7 @@ __global__ void __launch_bounds__(256) prefill_merge_kernel(const PrefillAttnArg
   const int lane = threadIdx.x & 31;
   grid_dependency_wait();
   grid_launch_dependents();
-  const int per_entry = per_item * a.Hq;
+  const int per_entry = min(per_item, a.T) * a.Hq;  // rows at most
   const long long rows = (long long)a.plan_head[2] * per_entry;
   for (long long row = ((long long)blockIdx.x * blockDim.x + threadIdx.x) >> 5; row < rows;
        row += ((long long)gridDim.x * blockDim.x) >> 5) {
@@ -1318,7 +1319,8 @@ cudaError_t launch_attention(const PrefillAttnArgs& a, cudaStream_t stream) {
   e = launch_pdl((const void*)prefill_attention_kernel<D, NT>, dim3((unsigned)std::min<long long>(most, args.slots)),
                  dim3(GE::kThreads), GE::kSmem, stream, params);
   if (e != cudaSuccess) return e;
-  const long long warps = std::min((long long)a.T * a.Hq, 8ll * 8 * a.sms);
+  const long long entries = (long long)a.T / per_item + a.B;  // at most
+  const long long warps = std::min(entries * std::min(per_item, a.T) * a.Hq, 8ll * 8 * a.sms);
   return launch_pdl((const void*)prefill_merge_kernel<D>, dim3((unsigned)((warps + 7) / 8)), dim3(256), 0, stream, plan_params);
 }
 
