@@ -120,8 +120,8 @@ struct Geo {
 //  * P < slots: every entry is cut into shares of at most c key tiles, c chosen among ktmax / s for a few s for
 //    the least estimate of the end, an item costing a tile beside its own: c + 1 where all shares run at once,
 //    else the smaller of the mean + c (any list schedule) and the rounds times c + 1; and a tile's time plus one
-//    for 2000 rows where rows have to be merged (2 x 300 tokens of 1000, 19200 rows: 31 us whole, 51 us in two
-//    shares; 4 single tokens of 131072 keys: 342 us in 19 shares each, 359 in 16; 3 sequences of ~500 keys, 12 tokens:
+//    for 4000 rows where rows have to be merged (2 x 300 tokens of 1000, 19200 rows: 30 us whole, 43 us in
+//    shares; 2 x 114 tokens of ~1550, 12768 rows: 35.9 us in shares, 38.5 whole; 4 single tokens of 131072 keys: 342 us in 19 shares each, 359 in 16; 3 sequences of ~500 keys, 12 tokens:
 //    18.4 us in shares of a tile, 24.8 whole).
 //  * P >= slots: entries above one and a half times the fair share W / slots are cut to that.  If there are
 //    none, the last P mod slots items, which would leave most CTAs idle for a whole item, are cut in s shares each (chunk of 4096 on 16384,
@@ -259,7 +259,7 @@ __global__ void __launch_bounds__(1024) prefill_plan_kernel(const PrefillAttnArg
       if (sp > 1 && items > 2 * a.slots) continue;
       long long end = c + 1;
       if (items > a.slots) end = min((W + items) / a.slots + c, (items + a.slots - 1) / a.slots * end);
-      if (rows > 0) end += 1 + (long long)rows * a.Hq / 2000;
+      if (rows > 0) end += 1 + (long long)rows * a.Hq / 4000;
       if (lane == 0) atomicMin(&s_best, (unsigned long long)end << 32 | (0xffffffffu - (unsigned)c));
     }
     __syncthreads();
