@@ -666,9 +666,10 @@ __device__ __forceinline__ float row_max(const float (&v)[N]) {
 }
 
 // tanh(u) / u as a polynomial of u^2, of the least largest relative error on |u| <= kCapNear (degree 2, 1.1e-7)
-// and on |u| <= kCapFar (degree 5, 5.8e-8), found by Remez' exchange in 40 digits; 2.0e-7 and 1.5e-7 in fp32
-// steps.
+// and on |u| <= kCapFar (degree 5, 5.8e-8), found by Remez' exchange in 40 digits; as stored 1.2e-7 and 6.8e-8, in
+// fp32 steps 1.5e-7 and 1.1e-7.
 constexpr float kCapNear = 0.2f, kCapFar = 0.8f;
+constexpr float kCapWide = 256.f;  // caps (base 2) whose last bits are more than 2^-14, a 64th of a bf16 output's half step
 __device__ constexpr float kCap2[3] = {0.99999988f, -0.3332859f, 0.13015407f};
 __device__ constexpr float kCap5[6] = {0.99999994f, -0.33332676f, 0.13321048f, -0.053114317f, 0.019093301f, -0.0043552998f};
 
@@ -692,6 +693,22 @@ __device__ __forceinline__ void cap_poly(float (&v)[N], float k) {
   }
 }
 
+// v = cap2 tanh(v ku), each key by the polynomial or the exponential form as its own u = v ku asks (an infinite u
+// gives +-cap2, NaN stays).  Both forms a key, in place of one: for caps above 177 whose scores, or a masked key beside
+// them, come near the cap (chunk of 4096 on 16384, 2.84 against 1.51 ms).
+template <int N>
+__device__ __forceinline__ void cap_each(float (&v)[N], float ku, float cap2) {
+#pragma unroll
+  for (int c = 0; c < N; ++c) {
+    const float u = v[c] * ku, w = u * u;
+    float f = kCap5[5];
+#pragma unroll
+    for (int n = 4; n >= 0; --n) f = fmaf(f, w, kCap5[n]);
+    const float big = 1.f - 2.f * rcp_approx(ex2_approx(u * (2.f * kLog2e)) + 1.f);
+    v[c] = cap2 * (fabsf(u) < kCapFar ? u * f : big);
+  }
+}
+
 // A thread's base-2 logits are v[c] mul + base + step (c / 8), mul > 0.
 struct Logits {
   float mul, base, step;
@@ -706,13 +723,17 @@ __device__ __forceinline__ Logits apply_rules(const PrefillAttnArgs& a, bool cap
   Logits x{a.scale_log2, 0.f, 0.f};
   if (cap) {
     // u = S ku is the logit over the cap.  Up to kCapFar for every key of the warp's rows the polynomial serves.
-    // Else 1 - 2 / (e^2u + 1), an exponential and a reciprocal a key: for a small u beside large ones its error is
-    // that of the cap's last bits, as the rounding of the large ones' is
+    // Else 1 - 2 / (e^2u + 1), an exponential and a reciprocal a key, whose error for a small u is that of the
+    // cap's last bits, about 2^-22 cap_log2.  The large u beside it may be a masked key's or another row's, so a
+    // cap above kCapWide takes the form of each key's own u
     const float ku = a.scale_log2 * a.cap_in * 0.34657359f;
     const float far = row_max<true>(v) * fabsf(ku);
     x.mul = a.cap_log2 * ku;
     if (x.mul > 0.f && __all_sync(kFullMask, far < kCapFar && fabsf(ku) < 1e3f)) {
       cap_poly(v, ku);
+    } else if (a.cap_log2 > kCapWide) {
+      cap_each(v, ku, a.cap_log2);
+      x.mul = 1.f;
     } else {
       const float k = ku * (2.f * kLog2e), twice = -2.f * a.cap_log2;
       const uint64_t k2 = pack2(k, k), one = pack2(1.f, 1.f), top = pack2(a.cap_log2, a.cap_log2), m2 = pack2(twice, twice);
