@@ -73,10 +73,10 @@ int pkv_kv_step_tables(int32_t* block_tables, int32_t* context_lens_out, int32_t
  * pkv_kv_append_f8 -- pkv_kv_append into FP8 pools.  Per (block, kv head) that receives rows, for K
  * and for V on their own: the needed scale is the smallest power of two s with max|x| / s <= 448
  * over the call's rows of the block (exponent kept in [-120, 119]).  A block whose offset 0 is
- * written starts anew with the needed scale; otherwise its scale becomes the larger of the old and
- * the needed one, and if it grew, the codes c of the rows that this call does not write become
- * rne(c * (old / new)) (exact but for results below the smallest normal number).  Rows become
- * rne(x / scale), saturated at 448.
+ * written (not one whose row there is refused) starts anew with the needed scale; otherwise its scale
+ * becomes the larger of the old and the needed one, and if it grew, the codes c of the rows that this
+ * call does not write become rne(c * (old / new)) (exact but for results below the smallest normal
+ * number).  Rows become rne(x / scale), saturated at 448.
  *   k_codes, v_codes   : [NB, Hkv, 16, d] E4M3, updated in place.
  *   k_scales, v_scales : [NB, Hkv] fp32, updated in place.
  *   k, v, slot_mapping, num_tokens, dims : as pkv_kv_append, and the tokens of one block are

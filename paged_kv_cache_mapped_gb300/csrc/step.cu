@@ -324,7 +324,7 @@ __device__ __forceinline__ void append_run(uint8_t* kq, uint8_t* vq, float* ks, 
   const float amax = __uint_as_float(max(most & 0xffffu, most >> 16) << 16);
   float* scale_at = (lane < 16 ? ks : vs) + (size_t)blk * Hkv + g;
   uint8_t* codes = (lane < 16 ? kq : vq) + row0 * D + h * E;
-  const bool anew = (slot & 15) == 0;
+  const bool anew = (slot & 15) == 0 && (good & 1u) != 0;  // offset 0 is written, not only asked for
   const float old = anew ? 0.f : *scale_at;
   if (!__all_sync(kFullMask, old >= 0.f && old <= 3.4028234e38f)) {
     if (lane == 0) record_error(err, PKV_DEV_BAD_VALUE);

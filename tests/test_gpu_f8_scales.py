@@ -1,0 +1,55 @@
+"""The FP8 cache's block scales where they decide: a refused row at the start of a block in the append."""
+import numpy as np
+import pytest
+import torch
+
+import f8_model
+import paged_kv_cache_mapped_gb300 as pkv
+import test_gpu_f8_append as append
+from paged_kv_cache_mapped_gb300 import header_constants
+
+C = header_constants()
+DEV = torch.device("cuda:0")
+
+
+def _append(pools, k, v, slots):
+    dev = [t.to(DEV) for t in pools]
+    err = pkv.new_error_word(DEV)
+    pkv.kv_append_f8(dev[0], dev[2], dev[1], dev[3], k.to(DEV), v.to(DEV), torch.tensor(slots, device=DEV), error_word=err)
+    return dev, pkv.read_error(err)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("in_k", [False, True], ids=["V", "K"])
+@pytest.mark.parametrize("spread", [0.0, 5.0], ids=["alike", "apart"])
+@pytest.mark.parametrize("slots", [[32], [32, 33], [32, 35, 47], list(range(32, 48)), [16, 17, 32, 33]], ids=str)
+def test_a_refused_row_at_offset_0_does_not_start_the_block(slots, spread, in_k):
+    """Head 0's row at the block's offset 0 is not finite: it is not written, so the block keeps its scale or
+    moves to a larger one with all that it holds; head 1's block starts anew."""
+    nb, hkv, d = 4, 2, 64
+    k, v = append._rows(len(slots), hkv, d, 21, spread)
+    first = slots.index(32)
+    (k if in_k else v)[first, 0, 5] = float("nan")
+    pools = append._pools(nb, hkv, d, 22)
+    dev, code = _append(pools, k, v, slots)
+    assert code == C["PKV_DEV_BAD_VALUE"]
+    for codes, scales, rows, gc, gs in ((pools[0], pools[1], k, dev[0], dev[1]), (pools[2], pools[3], v, dev[2], dev[3])):
+        for h in (0, 1):
+            at = [-1 if h == 0 and i == first else s for i, s in enumerate(slots)]
+            r = np.nan_to_num(rows[:, h:h + 1].double().numpy())
+            wc, ws = f8_model.append(append._vals(codes[:, h:h + 1]), scales[:, h:h + 1].numpy(), r, at)
+            assert np.array_equal(gs[:, h:h + 1].cpu().double().numpy(), ws), h
+            assert np.array_equal(append._vals(gc[:, h:h + 1]), wc), h
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("bad", [-1.0, float("nan"), float("inf")])
+def test_a_refused_row_at_offset_0_leaves_the_old_scale_to_be_checked(bad):
+    """The block does not start anew, so an old scale that is no scale refuses the block's other rows."""
+    k, v = append._rows(2, 1, 128, 23)
+    k[0, 0, 0] = float("inf")
+    pools = append._pools(4, 1, 128, 24)
+    pools[3][2, 0] = bad
+    dev, code = _append(pools, k, v, [32, 33])
+    assert code == C["PKV_DEV_BAD_VALUE"]
+    assert all(torch.equal(a.cpu().view(torch.uint8), b.view(torch.uint8)) for a, b in zip(dev, pools))
