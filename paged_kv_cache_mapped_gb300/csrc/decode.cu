@@ -107,6 +107,9 @@ constexpr float kRescaleSlack = 8.0f;
 // INT8 pools: the V-scale reference moves when a unit's largest V scale exceeds it by this
 // factor, so P times scale / reference stays below 2^8 * 64 (inside fp16).
 constexpr float kVrefSlack = 64.0f;
+// FP8 pools: P times scale is below 2^9 in the unit of its reference; times 2^6 it takes fp16's range up to 2^15, so
+// that a weight keeps its 11 bits down to 2^-20 of the largest and a step of 2^-30 of it below.
+constexpr float kF8Up = 6.0f;
 
 template <int D, bool SPARSE, bool Q8 = false, bool F8 = false>
 struct WarpTiles {
@@ -733,8 +736,8 @@ decode_split_kernel(const __grid_constant__ DecodeArgs a) {
   // (and rescales o) only when a unit's largest V scale exceeds it by kVrefSlack.
   float sl2q = sl2, vref = 0.f, inv_vref = 0.f;
   // FP8 pools: the blocks' V scales may be far apart, and a large one may come with weights that are next to
-  // nothing, so o of head h is kept in units of 2^vr, vr a running reference of logit + log2(scale) that moves as
-  // the maximum does (only when exceeded by 2^8); vc = 2^(mr - vr) brings a weight into that unit.
+  // nothing, so o of head h is kept in units of 2^(vr - kF8Up), vr a running reference of logit + log2(scale) that
+  // moves as the maximum does (only when exceeded by 2^8); vc = 2^(mr - vr + kF8Up) brings a weight into that unit.
   float vr0 = -INFINITY, vr1 = -INFINITY, vc0 = 0.f, vc1 = 0.f;
   // INT8 pools: K codes enter q.K as the fp16 numbers 1152 + code (no subtraction per element);
   // each unit's S accumulator starts at -1152 sum_k q'_k of its head instead of 0, computed once
@@ -761,10 +764,10 @@ decode_split_kernel(const __grid_constant__ DecodeArgs a) {
       l0 += __shfl_xor_sync(kFullMask, l0, m);
       l1 += __shfl_xor_sync(kFullMask, l1, m);
     }
-    // FP8: what a weight of 2^(logit - mr) counts in o's unit, 2^(vr - mr)
+    // FP8: what one of o's units is in weights of 2^(logit - mr), 2^(vr - kF8Up - mr)
     auto unit = [&](int hh) {
       const float m = hh ? mr1 : mr0, vr = hh ? vr1 : vr0;
-      return vr == -INFINITY ? 0.f : exp2f(fminf(vr - m, 127.f));
+      return vr == -INFINITY ? 0.f : exp2f(fminf(vr - kF8Up - m, 127.f));
     };
 #pragma unroll
     for (int hh = 0; hh < 2; ++hh) {
@@ -1107,8 +1110,8 @@ decode_split_kernel(const __grid_constant__ DecodeArgs a) {
             al1 = exp2f(vr1 - (mx1 + vm));
             vr1 = mx1 + vm;
           }
-          vc0 = vr0 == -INFINITY ? 0.f : exp2f(mr0 - vr0);
-          vc1 = vr1 == -INFINITY ? 0.f : exp2f(mr1 - vr1);
+          vc0 = vr0 == -INFINITY ? 0.f : exp2f(mr0 - vr0 + kF8Up);
+          vc1 = vr1 == -INFINITY ? 0.f : exp2f(mr1 - vr1 + kF8Up);
         } else if constexpr (Q8) {
           if (gv) {  // o moves to the new V reference (o is zero while vref is)
             const float fv = vref > 0.f ? vref / vm : 0.f;
@@ -1134,8 +1137,8 @@ decode_split_kernel(const __grid_constant__ DecodeArgs a) {
       l1 += p01 + p11;
       // -- P^T as B fragments (tokens x heads -> heads x tokens) ---------------------------
       // INT8 pools: P times each token's V scale over vref (at most 2^8 * slack) as one fp16
-      // term (11 significant bits, below the bf16 output's rounding); FP8: P times the block's V scale over 2^vr (at
-      // most 2^9), likewise;
+      // term (11 significant bits, below the bf16 output's rounding); FP8: P times the block's V scale over o's unit
+      // (at most 2^15), likewise;
       // bf16: a hi + lo pair of bf16 terms (8 bits alone would not be)
       uint32_t hA, hB, lA = 0u, lB = 0u;
       if constexpr (F8) {

@@ -1,10 +1,13 @@
-"""The FP8 cache's block scales where they decide: a refused row at the start of a block in the append."""
+"""The FP8 cache's block scales where they decide: a refused row at the start of a block in the append, and
+decodes over blocks of far apart weights and scales."""
 import numpy as np
 import pytest
 import torch
 
 import f8_model
 import paged_kv_cache_mapped_gb300 as pkv
+import rules_model
+import test_gpu_decode_rules as decode
 import test_gpu_f8_append as append
 from paged_kv_cache_mapped_gb300 import header_constants
 
@@ -53,3 +56,31 @@ def test_a_refused_row_at_offset_0_leaves_the_old_scale_to_be_checked(bad):
     dev, code = _append(pools, k, v, [32, 33])
     assert code == C["PKV_DEV_BAD_VALUE"]
     assert all(torch.equal(a.cpu().view(torch.uint8), b.view(torch.uint8)) for a, b in zip(dev, pools))
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("a", [1.703125, 1.6953125])
+@pytest.mark.parametrize("d", [64, 128])
+def test_light_keys_keep_their_digits_beside_heavy_ones(d, a):
+    """The first block's keys weigh 2^19.6 times the others' and have V = 0, so the others, all alike, make the
+    output; 2000 copies, so that most lie whole in one warp's share, where fp16's smallest step of 2^-24 is not to be
+    counted from the heavy keys' weight (it would be 1.5 % of a light one)."""
+    c = decode._case([64], 8, 2, d, 51, True)
+    kc, ks, vc, vs = c["pools"]
+    first = int(c["bt"][0, 0])
+    c["q"] = torch.full((1, 8, d), a).bfloat16()
+    c["scale"] = 8.0 / d  # logits 8 a in the first block, 0 in the others
+    for t, x in ((kc, 0.0), (vc, 3.0), (ks, 1.0), (vs, 0.25)):
+        t.copy_(torch.full(t.shape, x).to(t.dtype))
+    kc[first] = torch.ones_like(kc[first].float()).to(kc.dtype)
+    vc[first] = torch.zeros_like(vc[first].float()).to(vc.dtype)
+    n = 2000
+    many = dict(c, q=c["q"].repeat(n, 1, 1), bt=c["bt"].repeat(n, 1), lens=c["lens"] * n)
+    err = pkv.new_error_word(DEV)
+    got = decode._call(many, err=err).double().cpu().numpy()
+    assert pkv.read_error(err) == 0
+    k, v = np.zeros((64, d)), np.full((64, d), 0.75)
+    k[:16], v[:16] = 1.0, 0.0
+    ref, mass, size = rules_model.row(np.full(d, a), k, v, 63, c["scale"])
+    far = np.abs(got - ref) - rules_model.bound(ref, mass, size, d, 2.0 ** -11)
+    assert float(far.max()) <= 0
