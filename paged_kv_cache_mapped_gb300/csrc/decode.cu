@@ -1142,9 +1142,10 @@ decode_split_kernel(const __grid_constant__ DecodeArgs a) {
       // bf16: a hi + lo pair of bf16 terms (8 bits alone would not be)
       uint32_t hA, hB, lA = 0u, lB = 0u;
       if constexpr (F8) {
-        const float r0 = vs0 * vc0, r1 = vs0 * vc1;
-        hA = pack_f16x2(p00 * r0, p01 * r1);
-        hB = pack_f16x2(p10 * r0, p11 * r1);
+        // (in this order: vc alone is at most 2^114 and the result at most 2^15, where vc times the scale of a block under
+        // weights next to nothing can be past fp32, and a weight of 0 times that NaN)
+        hA = pack_f16x2(p00 * vc0 * vs0, p01 * vc1 * vs0);
+        hB = pack_f16x2(p10 * vc0 * vs0, p11 * vc1 * vs0);
       } else if constexpr (Q8) {
         const float r0 = vs0 * inv_vref, r1 = vs1 * inv_vref;
         hA = pack_f16x2(p00 * r0, p01 * r0);

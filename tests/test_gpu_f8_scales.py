@@ -84,3 +84,71 @@ def test_light_keys_keep_their_digits_beside_heavy_ones(d, a):
     ref, mass, size = rules_model.row(np.full(d, a), k, v, 63, c["scale"])
     far = np.abs(got - ref) - rules_model.bound(ref, mass, size, d, 2.0 ** -11)
     assert float(far.max()) <= 0
+
+
+ENDS = [(-120, 40, -9.0), (-100, 60, -6.07), (-120, 119, -9.0), (-120, 119, -7.0), (0, 119, -6.0), (-30, 119, -9.5), (119, -120, -9.0),
+        (-100, 100, -0.1)]
+
+
+def _far_scales(e0, e1, slope, zero, d):
+    """Two sequences whose first block has V scale 2^e0 and the largest weights, the others 2^e1 and weights of
+    2^(23 slope) a block less, so that either may carry the row; as all zeros the first block is what the append
+    makes of a block of zero rows.  Also each row's exact output, its bound, and Σ |v|.  The bound takes, beside
+    the half step of 2^-11 of each weight, that of fp16's smallest numbers: 2^-25 in units of 2^-6 of the largest weight
+    times scale (no scale counting less than 2^-100 there), for each code."""
+    c = decode._case([64, 41], 8, 2, d, 50, True)
+    c["q"].zero_()  # the logits are the distance bias alone
+    vc, vs = c["pools"][2], c["pools"][3]
+    vs.fill_(2.0 ** e1)
+    first = c["bt"][:, 0].long()
+    vs[first] = 2.0 ** e0
+    if zero:
+        vc.view(torch.uint8)[first] = 0
+    x = vc.float().cpu().double().numpy() * vs.cpu().double().numpy()[:, :, None, None]
+    ref, bound, size = (np.zeros((2, 8, d)) for _ in range(3))
+    for b, L in enumerate(c["lens"]):
+        for t in range(L):
+            c["v"][b, t] = x[int(c["bt"][b, t // 16]), :, t % 16]
+        for h in range(8):
+            v = c["v"][b, :L, h // 4]
+            ref[b, h], mass, top = rules_model.row(np.zeros(d), c["k"][b, :L, h // 4], v, L - 1, 1.0, slope=float(np.float32(slope)))
+            bound[b, h] = rules_model.bound(ref[b, h], mass, top, d, 2.0 ** -11)
+            size[b, h] = np.abs(v).sum(0)
+            s = np.array([float(vs[int(c["bt"][b, t // 16]), h // 4]) for t in range(L)])
+            p = np.exp(slope * np.arange(L) - max(0.0, slope * (L - 1)))
+            bound[b, h] += 2.0 ** -31 * (p * np.maximum(s, 2.0 ** -100)).max() * (np.abs(v) / s[:, None]).sum(0)
+    return c, ref, bound, size
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("e0,e1,slope", ENDS)
+@pytest.mark.parametrize("zero", [False, True], ids=["values", "zeros"])
+@pytest.mark.parametrize("d", [64, 128])
+def test_v_scales_at_both_ends_of_their_range(d, zero, e0, e1, slope):
+    """Two sequences, every block in a share of its own.  Shares are joined by fp32 weights relative to the
+    largest: one is off by up to 2^-148 (two steps of the smallest numbers), and a share holds its keys by
+    weights of up to 2^8 in that unit, over a sum of at least 1: 2^-140 of Σ |v|."""
+    c, ref, bound, size = _far_scales(e0, e1, slope, zero, d)
+    err = pkv.new_error_word(DEV)
+    got = decode._call(c, err=err, alibi_slopes=[slope] * 8).double().cpu().numpy()
+    assert pkv.read_error(err) == 0
+    assert float((np.abs(got - ref) - bound - 2.0 ** -140 * size).max()) <= 0
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("e0,e1,slope", ENDS)
+@pytest.mark.parametrize("zero", [False, True], ids=["values", "zeros"])
+@pytest.mark.parametrize("d", [64, 128])
+def test_v_scales_far_apart_within_a_share(d, zero, e0, e1, slope):
+    """2000 copies of each sequence, 14000 units and more for some 1800 warps: shares of 8 units and more, in which
+    most sequences (of 3 and 4 units) lie whole.  Each key's weight is an fp32 number relative to the largest, off
+    by up to 2^-148 where it is one of the smallest, 2^-148 of Σ |v|: half of the copies at least meet that."""
+    c, ref, bound, size = _far_scales(e0, e1, slope, zero, d)
+    n = 2000
+    many = dict(c, q=c["q"].repeat(n, 1, 1), bt=c["bt"].repeat(n, 1), lens=c["lens"] * n)
+    err = pkv.new_error_word(DEV)
+    got = decode._call(many, err=err, alibi_slopes=[slope] * 8).double().cpu().numpy().reshape(n, 2, 8, d)
+    assert pkv.read_error(err) == 0
+    far = np.abs(got - ref) - bound
+    assert float((far - 2.0 ** -140 * size).max()) <= 0
+    assert float(np.mean(far <= 2.0 ** -148 * size, axis=0).min()) >= 0.5
