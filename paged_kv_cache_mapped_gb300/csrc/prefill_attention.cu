@@ -222,6 +222,10 @@ __global__ void __launch_bounds__(1024) prefill_plan_kernel(const PrefillAttnArg
   }
   __syncthreads();
   const int entries = carry;
+  if (entries == 0) {  // every sequence idle or refused: nothing to share out
+    if (tid < 3) a.plan_head[tid] = 0;
+    return;
+  }
   long long work = 0;
   int most = 0;
   for (int e = tid; e < entries; e += blockDim.x) {
