@@ -1076,7 +1076,8 @@ __device__ __forceinline__ void softmax_rows(const PrefillAttnArgs& a, Shared<D,
     }
   }
   if (split && valid) a.part_ml[part] = make_float2(m, l);
-  // rows that are not finite: key by key over what they see
+  // rows that are not finite: key by key over what they see, stored by other lanes after this one's stores
+  __syncwarp();
   uint32_t again = __ballot_sync(kFullMask, valid && bad);
   while (again != 0u) {
     const int src = __ffs(again) - 1;

@@ -43,3 +43,33 @@ def test_steps_without_an_entry(what, B, hkv):
     assert pkv.read_error(err) == 0
     # bit for bit: a length past the sequence's own reads the pools' NaN fill
     assert torch.equal(out.t[:9].view(torch.int16), want.view(torch.int16)) and bool((out.t[9:] == 3.0).all())
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("lens,new", [([3000, 2500], [2, 1]), ([900, 700], [400, 130]), ([300, 90], [20, 90])],
+                         ids=["in shares", "chunks", "short"])
+@pytest.mark.parametrize("d", [64, 128])
+def test_rows_computed_again_are_the_ones_kept(d, lens, new):
+    """NaN and infinities in V rows before the windows, in blocks that the windows share: every row that has such
+    a block is computed again, and its second result stands, the same in every one of 40 calls."""
+    c = prefill._case(lens, new, 8, 2, d, 61)
+    for b, (L, n) in enumerate(zip(lens, new)):
+        for row in range(n):
+            t = L - n + row - 40  # the first key that the row does not see
+            if t >= 0 and row % 97 == 0:
+                blk = int(c["bt"][b, t // 16])
+                c["pools"][1][blk, :, t % 16, ::3] = (float("nan"), float("inf"), -float("inf"))[row % 3]
+    clean = []
+    for r in range(int(c["starts"][-1])):
+        b = int(np.searchsorted(c["starts"], r, side="right") - 1)
+        n, row = new[b], r - int(c["starts"][b])
+        # sees [i - 39, i]: no key i' - 40 of a poisoned row i' of its sequence
+        if not any(0 <= lens[b] - n + k - 40 and row - 39 <= k - 40 <= row for k in range(0, n, 97)):
+            clean += [(r, 0), (r, 5)]
+    assert len(clean) >= 4
+    err = pkv.new_error_word(DEV)
+    first = prefill._call(c, window=40, error_word=err)
+    prefill._check(c, first, window=40, rows=clean[:200])
+    for _ in range(40):
+        assert torch.equal(prefill._call(c, window=40, error_word=err).view(torch.int16), first.view(torch.int16))
+    assert pkv.read_error(err) == 0
