@@ -28,7 +28,7 @@
 // remainder as a second term, which costs half as many MMAs again (all rows in two terms: chunk of 4096 on 16384
 // 937 us against 730; none: 24 mixed sequences 26.3 against 28.5).
 // Non-finite V: a masked key's weight is 0, and 0 * NaN is NaN, so V rows past the sequence are cleared,
-// and an output row that is not finite is computed again key by key over what it sees.
+// and an output row that owes a NaN to a masked key is computed again over what it sees.
 // Every wait is bounded; bad block ids are cleared tiles, recorded.
 #include <algorithm>
 #include <cmath>
@@ -330,54 +330,168 @@ __global__ void __launch_bounds__(1024) prefill_plan_kernel(const PrefillAttnArg
   }
 }
 
-// --------------------------------------------------------------------------------- one row again
+// --------------------------------------------------------------------------------- rows again
 //
-// The keys of list entries [e0, e1) that a row sees, one at a time by one warp (lane: D / 32 elements):
-// what the tensor cores compute for the row, without the masked keys.  Writes the output row, or
-// partial row `part` if that is not negative.
+// A row that is not finite comes from what it sees, or from a masked key: its weight is 0, and 0 times a V of NaN or
+// infinity is NaN.  Only the second is wrong, and masked_non_finite looks for such a key; a row that has one is
+// computed again without it, 5 us for 32 keys with the row's warp alone.  A V of NaN that every row of its row tile
+// sees costs the search (chunk of 4096 on 16384: 742 us with one that the last 64 rows see, 789 that all do, against
+// 733; all rows computed again, 911 ms); rows before it in its own tile are computed again (a NaN at 16382: 86 ms),
+// as are rows of up to 512 keys (2.3 ms in all).
+
+// A row: sequence, kv head, packed row, query head; position, interval start, prefix; entries [e0, e1) of the key
+// list, of which entry e is block e, or e + shift from pre_units on.
 struct Row {
-  int b, g, r, h;         // sequence, kv head, packed row, query head
-  int i, lo, pre;         // position, interval start, prefix
-  int e0, e1;             // entries of the key list
-  int pre_units, shift;   // entry e is block e, or e + shift from pre_units on
+  int b, g, r, h;
+  int i, lo, pre;
+  int e0, e1;
+  int pre_units, shift;
 };
 
+// The keys of block `blk` that the row sees, a bit each.
+__device__ __forceinline__ uint32_t seen_keys(int i, int lo, int pre, int blk) {
+  const int hi_c = i - blk * 16, lo_c = lo - blk * 16, pre_c = pre - blk * 16;
+  uint32_t see = hi_c >= 15 ? 0xffffu : hi_c < 0 ? 0u : (2u << hi_c) - 1u;
+  see &= lo_c <= 0 ? 0xffffu : lo_c > 15 ? 0u : 0xffffu << lo_c;
+  return see | (pre_c >= 16 ? 0xffffu : pre_c <= 0 ? 0u : (1u << pre_c) - 1u);
+}
+
+// Whether a key that this lane's row (i, lo, pre; the other fields are the warp's) does not see has a non-finite V
+// in list entries [e0, e1), by one warp.  L: the sequence's keys (V rows past it were cleared).
 template <int D>
-__device__ __noinline__ void exact_row(const PrefillAttnArgs& a, const Row& w, long long part) {
-  constexpr int E = D / 32;
+__device__ __noinline__ bool masked_non_finite(const PrefillAttnArgs& a, const Row& w, int L) {
   const int lane = threadIdx.x & 31;
-  float q[E], o[E], m = -INFINITY, l = 0.f;
-#pragma unroll
-  for (int e = 0; e < E; ++e) {
-    q[e] = __bfloat162float(a.q[((size_t)w.r * a.Hq + w.h) * D + lane * E + e]);
-    o[e] = 0.f;
-  }
-  const float slope = a.slopes != nullptr ? a.slopes[w.h] * kLog2e : 0.f;
+  bool found = false;
   for (int en = w.e0; en < w.e1; ++en) {
     const int blk = en < w.pre_units ? en : en + w.shift;
     const int phys = a.block_tables[(size_t)w.b * a.MB + blk];
     if (phys < 0 || phys >= a.NB) continue;
-    for (int c = 0; c < 16; ++c) {
-      const int t = blk * 16 + c;
-      if (!((t >= w.lo && t <= w.i) || t < w.pre)) continue;
-      const size_t row = (((size_t)phys * a.Hkv + w.g) * 16 + c) * D + lane * E;
-      float x = 0.f;
+    // lanes 2c and 2c + 1 have the halves of row c
+    const uint4* v = reinterpret_cast<const uint4*>(a.v_cache + (((size_t)phys * a.Hkv + w.g) * 16 + (lane >> 1)) * D) +
+                     (lane & 1) * (D / 16);
+    bool bad = false;
 #pragma unroll
-      for (int e = 0; e < E; ++e) x = fmaf(q[e], __bfloat162float(a.k_cache[row + e]), x);
+    for (int k = 0; k < D / 16; ++k) {
+      const uint4 x = v[k];
+      for (const uint32_t p : {x.x, x.y, x.z, x.w}) bad |= (p & 0x7f80u) == 0x7f80u || (p & 0x7f800000u) == 0x7f800000u;
+    }
+    uint32_t rows = __ballot_sync(kFullMask, bad);
+    if (rows == 0u) continue;
+    rows = (rows | rows >> 1) & 0x55555555u;  // a bit in two, brought together
+    rows = (rows | rows >> 1) & 0x33333333u;
+    rows = (rows | rows >> 2) & 0x0f0f0f0fu;
+    rows = (rows | rows >> 4) & 0x00ff00ffu;
+    rows = (rows | rows >> 8) & 0xffffu;
+    if (L - blk * 16 < 16) rows &= (1u << (L - blk * 16)) - 1u;
+    found |= (rows & ~seen_keys(w.i, w.lo, w.pre, blk)) != 0u;
+  }
+  return found;
+}
+
+// What the tensor cores compute for the row, without the masked keys, by one warp, 32 keys at a time: eight lanes
+// a K row for the products, then a key a lane, then D / 32 elements of the output a lane.  Writes the output row, or
+// partial row `part` if that is not negative.  A sum that is no number stays so, and ends it.
+template <int D>
+__device__ __noinline__ void exact_row(const PrefillAttnArgs& a, const Row& w, long long part) {
+  constexpr int E = D / 32, H = D / 64;
+  const int lane = threadIdx.x & 31, sub = lane & 7;
+  const int key = (lane >> 3) + 4 * sub;  // of the 32: lanes 8 g .. 8 g + 7 read the rows of keys g + 4 n
+  float o[E], m = -INFINITY, l = 0.f;
 #pragma unroll
-      for (int s = 16; s > 0; s >>= 1) x += __shfl_xor_sync(kFullMask, x, s);
-      x *= a.scale_log2;
-      if (a.cap_log2 > 0.f) x = cap_logit(x, a.cap_log2, a.cap_in);
-      x -= slope * fabsf((float)(w.i - t));
-      const float top = fmaxf(m, x);
-      const float ref = top == -INFINITY ? 0.f : top;
-      const float keep = exp2f(m - ref), p = exp2f(x - ref);
-      m = top;
-      l = l * keep + p;
+  for (int e = 0; e < E; ++e) o[e] = 0.f;
+  uint32_t q[H][4];
 #pragma unroll
-      for (int e = 0; e < E; ++e) o[e] = o[e] * keep + p * __bfloat162float(a.v_cache[row + e]);
+  for (int h = 0; h < H; ++h) {
+    const uint4 u = *reinterpret_cast<const uint4*>(a.q + ((size_t)w.r * a.Hq + w.h) * D + h * 64 + sub * 8);
+    q[h][0] = u.x; q[h][1] = u.y; q[h][2] = u.z; q[h][3] = u.w;
+  }
+  const float slope = a.slopes != nullptr ? a.slopes[w.h] * kLog2e : 0.f;
+  auto block_of = [&](int e) { return e < w.pre_units ? e : e + w.shift; };
+  auto id_of = [&](int en) {  // the pool block of the lane's key, of entries en and en + 1; -1: none
+    const int e = en + (key >> 4);
+    const int id = e < w.e1 ? a.block_tables[(size_t)w.b * a.MB + block_of(e)] : -1;
+    return id < a.NB ? id : -1;
+  };
+  int next = id_of(w.e0);
+  for (int en = w.e0; en < w.e1; en += 2) {
+    const int phys = next, blk = block_of(en + (key >> 4)), c = key & 15;
+    next = id_of(en + 2);
+    const bool see = phys >= 0 && ((seen_keys(w.i, w.lo, w.pre, blk) >> c) & 1u);
+    const uint32_t seen = __ballot_sync(kFullMask, see);
+    const long long row = ((long long)phys * a.Hkv + w.g) * 16 + c;
+    uint32_t v[16][E / 2];  // V of half of the keys, the first half's on their way while the logits are worked out
+    auto load_v = [&](int s0) {
+#pragma unroll
+      for (int s = 0; s < 16; ++s) {
+        const long long at = __shfl_sync(kFullMask, row, s0 + s);
+        const uint32_t* src = reinterpret_cast<const uint32_t*>(a.v_cache + at * D + lane * E);
+#pragma unroll
+        for (int k = 0; k < E / 2; ++k) v[s][k] = ((seen >> (s0 + s)) & 1u) ? src[k] : 0u;
+      }
+    };
+    load_v(0);
+    float x = 0.f;
+#pragma unroll 1
+    for (int n0 = 0; n0 < 8; n0 += 4) {
+      uint4 t[4][H];
+#pragma unroll
+      for (int n = 0; n < 4; ++n) {
+        const int from = (lane & 24) | (n0 + n);
+        const long long at = __shfl_sync(kFullMask, row, from);
+#pragma unroll
+        for (int h = 0; h < H; ++h)
+          t[n][h] = ((seen >> from) & 1u) ? *reinterpret_cast<const uint4*>(a.k_cache + at * D + h * 64 + sub * 8)
+                                          : make_uint4(0u, 0u, 0u, 0u);
+      }
+#pragma unroll
+      for (int n = 0; n < 4; ++n) {
+        float y = 0.f;
+#pragma unroll
+        for (int h = 0; h < H; ++h) {
+          const uint32_t ts[4] = {t[n][h].x, t[n][h].y, t[n][h].z, t[n][h].w};
+#pragma unroll
+          for (int k = 0; k < 4; ++k) {
+            y = fmaf(bf16_lo_to_f32(q[h][k]), bf16_lo_to_f32(ts[k]), y);
+            y = fmaf(bf16_hi_to_f32(q[h][k]), bf16_hi_to_f32(ts[k]), y);
+          }
+        }
+#pragma unroll
+        for (int s = 4; s > 0; s >>= 1) y += __shfl_xor_sync(kFullMask, y, s);
+        if (n0 + n == sub) x = y;
+      }
+    }
+    x *= a.scale_log2;
+    if (a.cap_log2 > 0.f) x = cap_logit(x, a.cap_log2, a.cap_in);
+    x -= slope * fabsf((float)(w.i - (blk * 16 + c)));
+    if (!see) x = -INFINITY;
+    float top = x;
+#pragma unroll
+    for (int s = 16; s > 0; s >>= 1) top = fmaxf(top, __shfl_xor_sync(kFullMask, top, s));
+    top = fmaxf(m, top);
+    const float ref = top == -INFINITY ? 0.f : top;
+    const float keep = exp2f(m - ref), p = exp2f(x - ref);
+    m = top;
+    l = l * keep + p;
+    if (__any_sync(kFullMask, l != l)) {
+      l = __int_as_float(0x7fffffff);
+      break;
+    }
+#pragma unroll
+    for (int k = 0; k < E; ++k) o[k] *= keep;
+#pragma unroll
+    for (int half = 0; half < 2; ++half) {
+      if (half == 1) load_v(16);
+#pragma unroll
+      for (int s = 0; s < 16; ++s) {
+        const float ps = __shfl_sync(kFullMask, p, 16 * half + s);
+#pragma unroll
+        for (int k = 0; k < E; ++k)
+          o[k] = fmaf(ps, (k & 1) ? bf16_hi_to_f32(v[s][k >> 1]) : bf16_lo_to_f32(v[s][k >> 1]), o[k]);
+      }
     }
   }
+#pragma unroll
+  for (int s = 16; s > 0; s >>= 1) l += __shfl_xor_sync(kFullMask, l, s);
   const float f = part >= 0 ? 1.f : l > 0.f ? 1.f / l : (l == l ? 0.f : l);
 #pragma unroll
   for (int e = 0; e < E; ++e) {
@@ -920,11 +1034,7 @@ __device__ __forceinline__ void softmax_rows(const PrefillAttnArgs& a, Shared<D,
       if (!full) {
 #pragma unroll
         for (int p = 0; p < N / 16; ++p) {
-          const int t0 = w.block_of(e0 + p) * 16;
-          const int hi_c = i - t0, lo_c = lo - t0, pre_c = pre - t0;
-          uint32_t see = hi_c >= 15 ? 0xffffu : hi_c < 0 ? 0u : (2u << hi_c) - 1u;
-          see &= lo_c <= 0 ? 0xffffu : lo_c > 15 ? 0u : 0xffffu << lo_c;
-          see |= pre_c >= 16 ? 0xffffu : pre_c <= 0 ? 0u : (1u << pre_c) - 1u;
+          const uint32_t see = seen_keys(i, lo, pre, w.block_of(e0 + p));
 #pragma unroll
           for (int c = 0; c < 16; ++c) v[16 * p + c] = ((see >> c) & 1u) ? v[16 * p + c] : -INFINITY;
         }
@@ -1076,25 +1186,39 @@ __device__ __forceinline__ void softmax_rows(const PrefillAttnArgs& a, Shared<D,
     }
   }
   if (split && valid) a.part_ml[part] = make_float2(m, l);
-  // rows that are not finite: key by key over what they see, stored by other lanes after this one's stores
-  __syncwarp();
+  // Rows that are not finite and may owe it to a masked key, which steps without a mask do not have.  (Rows of two
+  // terms, at most 512 keys long, are all taken: an infinite V times the terms may be NaN.)
   uint32_t again = __ballot_sync(kFullMask, valid && bad);
-  while (again != 0u) {
-    const int src = __ffs(again) - 1;
-    again &= again - 1;
+  if (again != 0u) {
     Row row;
     row.b = w.b;
     row.g = w.g;
-    row.r = __shfl_sync(kFullMask, prow, src);
-    row.h = __shfl_sync(kFullMask, h, src);
-    row.i = __shfl_sync(kFullMask, i, src);
-    row.lo = __shfl_sync(kFullMask, lo, src);
-    row.pre = __shfl_sync(kFullMask, pre, src);
-    row.e0 = w.ts * kTileBlocks;
-    row.e1 = min((w.ts + w.nt) * kTileBlocks, w.nblk);
     row.pre_units = w.pre_units;
     row.shift = w.shift;
-    exact_row<D>(a, row, split ? __shfl_sync(kFullMask, part, src) : -1);
+    bool owes = two || !(l <= 3.4028234e38f);
+    for (int j = range.lo; j <= range.hi && !two; ++j) {
+      if ((j >= full0 && j < full1) || j < full_pre) continue;
+      row.i = i;
+      row.lo = lo;
+      row.pre = pre;
+      row.e0 = e_base + j * kStepBlocks;
+      row.e1 = min(row.e0 + kStepBlocks, w.nblk);
+      owes = masked_non_finite<D>(a, row, w.L) || owes;
+    }
+    again = __ballot_sync(kFullMask, valid && bad && owes);
+    __syncwarp();  // the rows are stored by other lanes after this one's stores
+    while (again != 0u) {
+      const int src = __ffs(again) - 1;
+      again &= again - 1;
+      row.r = __shfl_sync(kFullMask, prow, src);
+      row.h = __shfl_sync(kFullMask, h, src);
+      row.i = __shfl_sync(kFullMask, i, src);
+      row.lo = __shfl_sync(kFullMask, lo, src);
+      row.pre = __shfl_sync(kFullMask, pre, src);
+      row.e0 = w.ts * kTileBlocks;
+      row.e1 = min((w.ts + w.nt) * kTileBlocks, w.nblk);
+      exact_row<D>(a, row, split ? __shfl_sync(kFullMask, part, src) : -1);
+    }
   }
 }
 

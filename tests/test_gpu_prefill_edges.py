@@ -4,6 +4,7 @@ import pytest
 import torch
 
 import paged_kv_cache_mapped_gb300 as pkv
+import rules_model
 import test_gpu_prefill_attention as prefill
 from paged_kv_cache_mapped_gb300 import header_constants
 from test_gpu_guard_bands import Guarded, _check
@@ -73,3 +74,59 @@ def test_rows_computed_again_are_the_ones_kept(d, lens, new):
     for _ in range(40):
         assert torch.equal(prefill._call(c, window=40, error_word=err).view(torch.int16), first.view(torch.int16))
     assert pkv.read_error(err) == 0
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("rule", ["causal", "prefix and window", "documents"])
+@pytest.mark.parametrize("lens,new", [([3000, 2500], [2, 1]), ([1900, 700], [400, 130])], ids=["in shares", "chunks"])
+@pytest.mark.parametrize("d", [64, 128])
+def test_a_value_that_is_no_number_stays_with_its_columns(d, lens, new, rule):
+    """NaN in some columns of a few V rows: NaN in those columns of the rows that see one, the other columns and
+    the other rows as without them."""
+    c = prefill._case(lens, new, 8, 2, d, 62)
+    r = prefill._fill_rules(c, {"causal": {}, "prefix and window": dict(window=300, prefix_lens=200),
+                                "documents": dict(doc_starts=90, prefix_lens=40)}[rule])
+    at = {0: [3, lens[0] - new[0] // 2, lens[0] - 250], 1: [lens[1] - 90, 190, lens[1] - 1]}
+    for b in at:
+        for t in at[b]:
+            c["pools"][1][int(c["bt"][b, t // 16]), :, t % 16, 3:9] = float("nan")
+    err = pkv.new_error_word(DEV)
+    got = prefill._call(c, error_word=err, **r)
+    assert pkv.read_error(err) == 0
+    nan = torch.isnan(got.float()).cpu().numpy()
+    assert not nan[:, :, :3].any() and not nan[:, :, 9:].any()
+    for row in range(int(c["starts"][-1])):
+        b = int(np.searchsorted(c["starts"], row, side="right") - 1)
+        i = lens[b] - new[b] + row - int(c["starts"][b])
+        lo = max(0, i - r["window"] + 1 if r.get("window") else 0, int(r["doc_starts"][row]) if "doc_starts" in r else 0)
+        sees = any(lo <= t <= i or t < (r["prefix_lens"][b] if "prefix_lens" in r else 0) for t in at[b])
+        assert nan[row, :, 3:9].all() if sees else not nan[row].any(), (row, i)
+    got = got.double().cpu().numpy()
+    for row, h in prefill._rows(c, 3):
+        b = int(np.searchsorted(c["starts"], row, side="right") - 1)
+        L, i = lens[b], lens[b] - new[b] + row - int(c["starts"][b])
+        ref, mass, size = rules_model.row(c["q"][row, h].double().numpy(), c["k"][b, :L, h // 4], c["v"][b, :L, h // 4], i, c["scale"],
+                                          r.get("window", 0), 0.0, 0.0, int(r["doc_starts"][row]) if "doc_starts" in r else 0,
+                                          int(r["prefix_lens"][b]) if "prefix_lens" in r else 0)
+        far = np.abs(got[row, h] - ref) - rules_model.bound(ref, mass, size, d, prefill._weight_eps(L))
+        assert float(far[~nan[row, h]].max()) <= 0, (row, h)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("t,most_ms", [(0, 5.0), (4032, 5.0), (4046, 20.0)])
+def test_cost_of_a_value_that_is_no_number(t, most_ms):
+    """A prompt of 4096 tokens (0.1 ms) with a NaN in the first V row, which all rows see, or in the first of the last
+    64-token tile, which all its rows see: the result is NaN there by right and not worked out twice but for the rows of
+    at most 512 keys (computing every such row again took some 70 ms).  In the middle of that tile the rows before it
+    are computed again.  The limits are two to four times what the calls take."""
+    c = prefill._case([4096], [4096], 8, 2, 128, 63)
+    ins = [c["q"].to(DEV), *c["pools"], c["bt"], torch.tensor([4096], dtype=torch.int32, device=DEV), torch.from_numpy(c["starts"]).to(DEV)]
+    c["pools"][1][int(c["bt"][0, t // 16]), :, t % 16] = float("nan")
+    pkv.paged_prefill_attention(*ins, c["scale"])
+    a, b = torch.cuda.Event(enable_timing=True), torch.cuda.Event(enable_timing=True)
+    a.record()
+    got = pkv.paged_prefill_attention(*ins, c["scale"])
+    b.record()
+    torch.cuda.synchronize()
+    assert torch.isnan(got[t:]).all() and not torch.isnan(got[:t]).any()
+    assert a.elapsed_time(b) < most_ms
