@@ -59,7 +59,10 @@ def _call(name, device, stream, *args):
 
 @functools.lru_cache(maxsize=256)
 def _dims(batch, hq, hkv, d, nb, mb):
-    """The shape record's address (records of the same sizes are one)."""
+    """The shape record's address (records of the same sizes are one; ctypes would cut a size to 32 bits)."""
+    for x in (batch, hq, hkv, d, nb, mb):
+        if not 0 <= x < 2**31:
+            raise ValueError(f"sizes must be within [0, 2**31), got {x}")
     r = PkvDims(batch, hq, hkv, d, BLOCK_SIZE, nb, mb)
     return ctypes.pointer(r)
 
@@ -94,6 +97,9 @@ def kv_step_tables(block_tables, context_lens, new_tokens, free_blocks, free_cou
     free_count_out [1]); rows past the step's last token have slot and position -1.  context_lens_out
     and free_count_out may be the inputs themselves.  All or nothing on a device error (see
     pkv_kv_step_tables)."""
+    T = int(max_new_tokens)
+    if not 0 <= T < 2**31:  # (the library refuses what is past its own limit)
+        raise ValueError(f"max_new_tokens must be within [0, 2**31), got {T}")
     bt = _need(block_tables, "block_tables", torch.int32, 2)
     dev = block_tables.get_device()
     lens = _need(context_lens, "context_lens", torch.int32, 1, dev)
@@ -106,9 +112,6 @@ def kv_step_tables(block_tables, context_lens, new_tokens, free_blocks, free_cou
         raise ValueError("context_lens / new_tokens batch differs from block_tables'")
     if free_count.shape[0] != 1:
         raise ValueError("free_count must be [1]")
-    T = int(max_new_tokens)
-    if T < 0:
-        raise ValueError("max_new_tokens must not be negative")
     lens_out, lp = _give(context_lens_out, "context_lens_out", (B,), torch.int32, block_tables, dev, stream)
     count_out, cp = _give(free_count_out, "free_count_out", (1,), torch.int32, block_tables, dev, stream)
     starts, qp = _give(query_starts, "query_starts", (B + 1,), torch.int32, block_tables, dev, stream)
@@ -232,7 +235,8 @@ def paged_decode_attention_f8(q, k_codes, v_codes, k_scales, v_scales, block_tab
 def prefill_workspace_bytes(total_tokens, batch, num_q_heads, num_kv_heads, head_dim, num_blocks, max_blocks_per_seq) -> int:
     """Workspace of paged_prefill_attention for these sizes and at most total_tokens query rows."""
     dims = _dims(batch, num_q_heads, num_kv_heads, head_dim, num_blocks, max_blocks_per_seq)
-    n = int(load().pkv_prefill_workspace_bytes(dims, int(total_tokens)))
+    T = int(total_tokens)
+    n = int(load().pkv_prefill_workspace_bytes(dims, T)) if 0 <= T < 2**31 else 0
     if n == 0:
         raise ValueError("invalid dims for paged prefill")
     return n
