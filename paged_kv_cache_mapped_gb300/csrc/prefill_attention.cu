@@ -332,12 +332,13 @@ __global__ void __launch_bounds__(1024) prefill_plan_kernel(const PrefillAttnArg
 
 // --------------------------------------------------------------------------------- rows again
 //
-// A row that is not finite comes from what it sees, or from a masked key: its weight is 0, and 0 times a V of NaN or
-// infinity is NaN.  Only the second is wrong, and masked_non_finite looks for such a key; a row that has one is
-// computed again without it, 5 us for 32 keys with the row's warp alone.  A V of NaN that every row of its row tile
-// sees costs the search (chunk of 4096 on 16384: 742 us with one that the last 64 rows see, 789 that all do, against
-// 733; all rows computed again, 911 ms); rows before it in its own tile are computed again (a NaN at 16382: 86 ms),
-// as are rows of up to 512 keys (2.3 ms in all).
+// A row that is not finite comes from a V that it sees, from a masked key, whose weight is 0, and 0 times a V of NaN or
+// infinity is NaN, or (V of 2^119 and more) from weights of up to 2^8 where those of at most 1 would do.  Only the
+// first is its own.  non_finite_v looks for the others; a row that has a masked key that is not finite, or whose keys
+// all are, is computed again, 5 us for 32 keys with the row's warp alone.  A V of NaN that every row of its row tile
+// sees costs the search, from the last step back (chunk of 4096 on 16384: 761 us with one that the last 64 rows see, 2.65 ms
+// with one at 8192, 4.66 with one at 0, against 746 us; all such rows computed again, 911 ms); rows before it in its
+// own tile are computed again (a NaN at 16382: 90 ms), as are rows of up to 512 keys (2.4 ms in all).
 
 // A row: sequence, kv head, packed row, query head; position, interval start, prefix; entries [e0, e1) of the key
 // list, of which entry e is block e, or e + shift from pre_units on.
@@ -356,12 +357,13 @@ __device__ __forceinline__ uint32_t seen_keys(int i, int lo, int pre, int blk) {
   return see | (pre_c >= 16 ? 0xffffu : pre_c <= 0 ? 0u : (1u << pre_c) - 1u);
 }
 
-// Whether a key that this lane's row (i, lo, pre; the other fields are the warp's) does not see has a non-finite V
-// in list entries [e0, e1), by one warp.  L: the sequence's keys (V rows past it were cleared).
+// Whether a key in list entries [e0, e1) has a non-finite V (1), and (2) whether there is one that this lane's row
+// (i, lo, pre; the other fields are the warp's) does not see, by one warp.  L: the sequence's keys (V rows past it
+// were cleared).
 template <int D>
-__device__ __noinline__ bool masked_non_finite(const PrefillAttnArgs& a, const Row& w, int L) {
+__device__ __noinline__ int non_finite_v(const PrefillAttnArgs& a, const Row& w, int L) {
   const int lane = threadIdx.x & 31;
-  bool found = false;
+  int found = 0;
   for (int en = w.e0; en < w.e1; ++en) {
     const int blk = en < w.pre_units ? en : en + w.shift;
     const int phys = a.block_tables[(size_t)w.b * a.MB + blk];
@@ -383,7 +385,7 @@ __device__ __noinline__ bool masked_non_finite(const PrefillAttnArgs& a, const R
     rows = (rows | rows >> 4) & 0x00ff00ffu;
     rows = (rows | rows >> 8) & 0xffffu;
     if (L - blk * 16 < 16) rows &= (1u << (L - blk * 16)) - 1u;
-    found |= (rows & ~seen_keys(w.i, w.lo, w.pre, blk)) != 0u;
+    found |= ((rows & ~seen_keys(w.i, w.lo, w.pre, blk)) != 0u ? 2 : 0) | (rows != 0u ? 1 : 0);
   }
   return found;
 }
@@ -1186,8 +1188,8 @@ __device__ __forceinline__ void softmax_rows(const PrefillAttnArgs& a, Shared<D,
     }
   }
   if (split && valid) a.part_ml[part] = make_float2(m, l);
-  // Rows that are not finite and may owe it to a masked key, which steps without a mask do not have.  (Rows of two
-  // terms, at most 512 keys long, are all taken: an infinite V times the terms may be NaN.)
+  // Rows that are not finite and may owe it to other than a V that they see.  (Rows of two terms, at most 512 keys
+  // long, are all taken: an infinite V times the terms may be NaN.)
   uint32_t again = __ballot_sync(kFullMask, valid && bad);
   if (again != 0u) {
     Row row;
@@ -1195,16 +1197,19 @@ __device__ __forceinline__ void softmax_rows(const PrefillAttnArgs& a, Shared<D,
     row.g = w.g;
     row.pre_units = w.pre_units;
     row.shift = w.shift;
-    bool owes = two || !(l <= 3.4028234e38f);
-    for (int j = range.lo; j <= range.hi && !two; ++j) {
-      if ((j >= full0 && j < full1) || j < full_pre) continue;
-      row.i = i;
-      row.lo = lo;
-      row.pre = pre;
-      row.e0 = e_base + j * kStepBlocks;
-      row.e1 = min(row.e0 + kStepBlocks, w.nblk);
-      owes = masked_non_finite<D>(a, row, w.L) || owes;
+    row.i = i;
+    row.lo = lo;
+    row.pre = pre;
+    int found = 0;
+    for (int full = 0; full < 2; ++full) {  // (a masked key is in a step with a mask; in the others one key is enough)
+      for (int j = range.hi; j >= range.lo && !two && !(full && (found & 1)); --j) {
+        if (((j >= full0 && j < full1) || j < full_pre) != (full != 0)) continue;
+        row.e0 = e_base + j * kStepBlocks;
+        row.e1 = min(row.e0 + kStepBlocks, w.nblk);
+        found |= non_finite_v<D>(a, row, w.L);
+      }
     }
+    const bool owes = two || !(l <= 3.4028234e38f) || found != 1;
     again = __ballot_sync(kFullMask, valid && bad && owes);
     __syncwarp();  // the rows are stored by other lanes after this one's stores
     while (again != 0u) {

@@ -130,3 +130,21 @@ def test_cost_of_a_value_that_is_no_number(t, most_ms):
     torch.cuda.synchronize()
     assert torch.isnan(got[t:]).all() and not torch.isnan(got[:t]).any()
     assert a.elapsed_time(b) < most_ms
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("window", [0, 300])
+@pytest.mark.parametrize("lens,new", [([3000, 2500], [2, 1]), ([1900, 700], [400, 130])], ids=["in shares", "chunks"])
+@pytest.mark.parametrize("d", [64, 128])
+def test_large_finite_values(d, lens, new, window):
+    """V of some 2^120, of either sign: a weight of up to 2^8 times that is past fp32, the output is not.  (Relative
+    to the largest, 3000 weights 2^x of normal scores make sums of some 2^120 sqrt(3000 E 4^(x - 4)), below 2^124.)"""
+    c = prefill._case(lens, new, 8, 2, d, 64)
+    big = 2.0 ** 120
+    c["pools"][1].mul_(big)
+    c["v"] = c["v"] * big
+    err = pkv.new_error_word(DEV)
+    got = prefill._call(c, window=window, error_word=err)
+    assert pkv.read_error(err) == 0
+    assert bool(torch.isfinite(got.float()).all())
+    prefill._check(c, got, window=window)
