@@ -83,8 +83,9 @@ int pkv_kv_step_tables(int32_t* block_tables, int32_t* context_lens_out, int32_t
  *                        adjacent in slot_mapping with ascending slots (the order of
  *                        pkv_kv_step_tables).  A token whose slot is in the block of the token
  *                        before it but not above that token's is reported (PKV_DEV_BAD_SLOT), and
- *                        neither it nor the tokens of that block adjacent to it are written.  The
- *                        same block in two places that are not adjacent is invalid input.
+ *                        neither it nor the tokens of that block that follow on it are written; those
+ *                        before it are.  The same block in two places that are not adjacent is
+ *                        invalid input.
  *   error_word         : PKV_DEV_BAD_SLOT; PKV_DEV_BAD_VALUE for a (token, kv head) whose K or V row
  *                        holds a non-finite value (it is left unwritten and does not count), or a
  *                        (block, kv head) whose old scale is negative or not finite (nothing of it

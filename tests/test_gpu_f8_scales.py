@@ -59,6 +59,20 @@ def test_a_refused_row_at_offset_0_leaves_the_old_scale_to_be_checked(bad):
 
 
 @pytest.mark.gpu
+@pytest.mark.parametrize("slots,written", [([9, 12, 11, 13, 40], [9, 12, -1, -1, 40]), ([16, 17, 17, 18, 19], [16, 17, -1, -1, -1]),
+                                           ([3, 2, 1, 0, 16], [3, -1, -1, -1, 16]), ([40, 41, 40, -1, 9], [40, 41, -1, -1, 9])])
+def test_tokens_after_a_descending_one_are_left_out(slots, written):
+    """What a block's tokens before the refused one write stands, with the scale of those alone."""
+    k, v = append._rows(len(slots), 2, 128, 25)
+    pools = append._pools(4, 2, 128, 26)
+    dev, code = _append(pools, k, v, slots)
+    assert code == C["PKV_DEV_BAD_SLOT"]
+    for codes, scales, rows, gc, gs in ((pools[0], pools[1], k, dev[0], dev[1]), (pools[2], pools[3], v, dev[2], dev[3])):
+        wc, ws = f8_model.append(append._vals(codes), scales.numpy(), rows.double().numpy(), written)
+        assert np.array_equal(gs.cpu().double().numpy(), ws) and np.array_equal(append._vals(gc), wc)
+
+
+@pytest.mark.gpu
 @pytest.mark.parametrize("a", [1.703125, 1.6953125])
 @pytest.mark.parametrize("d", [64, 128])
 def test_light_keys_keep_their_digits_beside_heavy_ones(d, a):
