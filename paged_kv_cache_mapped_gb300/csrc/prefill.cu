@@ -58,14 +58,6 @@ __device__ __forceinline__ unsigned char* align1024(unsigned char* p) {
 
 __device__ __forceinline__ uint32_t ld_u32(const __nv_bfloat16* p) { return __ldg(reinterpret_cast<const uint32_t*>(p)); }
 
-// 2^x by the hardware approximation (the PTX ex2 instruction; relative error ~2^-22, results
-// below 2^-126 flushed to zero).
-__device__ __forceinline__ float ex2(float x) {
-  float y;
-  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
-  return y;
-}
-
 // -------------------------------------------------------------------------- score kernel
 
 template <int D>
@@ -243,7 +235,7 @@ __global__ void __launch_bounds__(kScoreWarps * 32) prefill_score_kernel(const _
         for (int mt = 0; mt < 2; ++mt)
 #pragma unroll
           for (int rr = 0; rr < 2; ++rr) {
-            const float e = ex2(fmaf(c[mt][2 * rr], sl2, -l0)) + ex2(fmaf(c[mt][2 * rr + 1], sl2, -l1));
+            const float e = ex2_approx(fmaf(c[mt][2 * rr], sl2, -l0)) + ex2_approx(fmaf(c[mt][2 * rr + 1], sl2, -l1));
             acc[mt][rr] = fmaf(kf[mt][rr], e, acc[mt][rr]);
           }
       } else {
@@ -258,8 +250,8 @@ __global__ void __launch_bounds__(kScoreWarps * 32) prefill_score_kernel(const _
             const int k = key[mt][rr];
             const bool a0 = kval[mt][rr] && cv0 && k <= j0;
             const bool a1 = kval[mt][rr] && cv1 && k <= j1;
-            const float e0 = ex2(fmaf(c[mt][2 * rr], sl2, -l0));
-            const float e1 = ex2(fmaf(c[mt][2 * rr + 1], sl2, -l1));
+            const float e0 = ex2_approx(fmaf(c[mt][2 * rr], sl2, -l0));
+            const float e1 = ex2_approx(fmaf(c[mt][2 * rr + 1], sl2, -l1));
             acc[mt][rr] += (a0 ? e0 : 0.f) + (a1 ? e1 : 0.f);
           }
       }
@@ -520,8 +512,8 @@ __global__ void __launch_bounds__(kTcThreads, PKV_TC_MINB) prefill_score_tc_kern
               const float4 l = *reinterpret_cast<const float4*>(l2c + 32 * q + 4 * c4);
               const float2 x01 = unpack2(ffma2(pack2(v[4 * c4], v[4 * c4 + 1]), s2, pack2(l.x, l.y)));
               const float2 x23 = unpack2(ffma2(pack2(v[4 * c4 + 2], v[4 * c4 + 3]), s2, pack2(l.z, l.w)));
-              acc2 = fadd2(acc2, pack2(ex2(x01.x), ex2(x01.y)));
-              acc2 = fadd2(acc2, pack2(ex2(x23.x), ex2(x23.y)));
+              acc2 = fadd2(acc2, pack2(ex2_approx(x01.x), ex2_approx(x01.y)));
+              acc2 = fadd2(acc2, pack2(ex2_approx(x23.x), ex2_approx(x23.y)));
             }
             const float2 a2 = unpack2(acc2);
             sum += a2.x + a2.y;
@@ -529,7 +521,7 @@ __global__ void __launch_bounds__(kTcThreads, PKV_TC_MINB) prefill_score_tc_kern
 #pragma unroll
             for (int c = 0; c < 32; ++c) {
               const int cc = 32 * q + c;
-              if (cc < ncols && key <= jbase + (cc >> log2g)) sum += ex2(fmaf(v[c], sl2, l2c[cc]));
+              if (cc < ncols && key <= jbase + (cc >> log2g)) sum += ex2_approx(fmaf(v[c], sl2, l2c[cc]));
             }
           }
         }
@@ -742,7 +734,7 @@ __global__ void __launch_bounds__(kLtThreads, 2) prefill_lse_tc_kernel(const __g
         for (int c = 1; c < 32; ++c) mx = fmaxf(mx, v[c]);
         mx *= sl2;  // sl2 > 0 keeps the order
         if (mx > m + kLseSlack) {
-          l *= ex2(m - mx);
+          l *= ex2_approx(m - mx);
           m = mx;
         }
         if (m != -INFINITY) {  // packed fp32 pairs: one FMA and one add per two terms
@@ -751,7 +743,7 @@ __global__ void __launch_bounds__(kLtThreads, 2) prefill_lse_tc_kernel(const __g
 #pragma unroll
           for (int c = 0; c < 32; c += 2) {
             const float2 x = unpack2(ffma2(pack2(v[c], v[c + 1]), s2, nm2));
-            e2 = fadd2(e2, pack2(ex2(x.x), ex2(x.y)));
+            e2 = fadd2(e2, pack2(ex2_approx(x.x), ex2_approx(x.y)));
           }
           const float2 e = unpack2(e2);
           l += e.x + e.y;
@@ -922,12 +914,12 @@ __global__ void __launch_bounds__(kLseWarps * 32) prefill_lse_kernel(const __gri
           float& mr = m[mt][rr];
           float& lr = l[mt][rr];
           if (mx > mr + kLseSlack) {
-            lr *= ex2(mr - mx);
+            lr *= ex2_approx(mr - mx);
             mr = mx;
           }
           if (mr != -INFINITY)
-            lr += ex2(fmaf(x[0], sl2, -mr)) + ex2(fmaf(x[1], sl2, -mr)) + ex2(fmaf(x[2], sl2, -mr)) +
-                  ex2(fmaf(x[3], sl2, -mr));
+            lr += ex2_approx(fmaf(x[0], sl2, -mr)) + ex2_approx(fmaf(x[1], sl2, -mr)) + ex2_approx(fmaf(x[2], sl2, -mr)) +
+                  ex2_approx(fmaf(x[3], sl2, -mr));
         }
     }
     __syncwarp();

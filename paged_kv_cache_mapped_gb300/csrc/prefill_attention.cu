@@ -65,17 +65,6 @@ __device__ __forceinline__ PrefillSeq prefill_seq(const PrefillAttnArgs& a, int 
   return s;
 }
 
-// The largest i < n with start[i] <= x (start ascending, start[0] <= x; of equal starts the last one has the
-// items).
-__device__ __forceinline__ int owner_of(const int* start, int n, int x) {
-  int lo = 0, hi = n;
-  while (hi - lo > 1) {
-    const int mid = (lo + hi) >> 1;
-    if (start[mid] <= x) lo = mid; else hi = mid;
-  }
-  return lo;
-}
-
 // First key of the interval that packed row r at position i sees (i + 1: none).
 __device__ __forceinline__ int interval_start(const PrefillAttnArgs& a, int r, int i) {
   int lo = a.window > 0 && i >= a.window ? i - a.window + 1 : 0;
@@ -1470,9 +1459,8 @@ cudaError_t launch_attention(const PrefillAttnArgs& a, cudaStream_t stream) {
                              stream, plan_params);
   if (e != cudaSuccess) return e;
   void* params[] = {&args};
-  const long long most = ((long long)a.T / per_item + a.B) * a.Hkv + 2 * args.slots;
-  e = launch_pdl((const void*)prefill_attention_kernel<D, NT>, dim3((unsigned)std::min<long long>(most, args.slots)),
-                 dim3(GE::kThreads), GE::kSmem, stream, params);
+  // a CTA for every slot: even one token's keys are cut into shares for all of them
+  e = launch_pdl((const void*)prefill_attention_kernel<D, NT>, dim3((unsigned)args.slots), dim3(GE::kThreads), GE::kSmem, stream, params);
   if (e != cudaSuccess) return e;
   const long long entries = (long long)a.T / per_item + a.B;  // at most
   const long long warps = std::min(entries * std::min(per_item, a.T) * a.Hq, 8ll * 8 * a.sms);

@@ -499,6 +499,17 @@ __device__ __forceinline__ float ex2_approx(float x) {
   return y;
 }
 
+// The largest i < n with start[i] <= x (start ascending, start[0] <= x: entry i has the items from start[i] on; of
+// equal starts the last one has them).
+__device__ __forceinline__ int owner_of(const int* start, int n, int x) {
+  int lo = 0, hi = n;
+  while (hi - lo > 1) {
+    const int mid = (lo + hi) >> 1;
+    if (start[mid] <= x) lo = mid; else hi = mid;
+  }
+  return lo;
+}
+
 // Programmatic dependent launch.  A kernel launched with programmatic stream serialisation
 // may start while the previous kernel on its stream is still running; it must call
 // grid_dependency_wait() before touching global memory that kernel may produce or read.

@@ -28,17 +28,6 @@ constexpr int kStepCluster = 8;
 // as many sequences 8.2, 8.6; 4096 of 16 sequences 6.4, 6.3; 4096 of as many 12.4, 10.3; 64000 61.7, 8.5).
 constexpr int kStepLarge = 2048;
 
-// The largest i < n with start[i] <= x (start ascending, start[0] = 0, x below the total, so that
-// entry owns x: of equal starts the last one has the items).
-__device__ __forceinline__ int owner_of(const int* start, int n, int x) {
-  int lo = 0, hi = n;
-  while (hi - lo > 1) {
-    const int mid = (lo + hi) >> 1;
-    if (start[mid] <= x) lo = mid; else hi = mid;
-  }
-  return lo;
-}
-
 // kStepRun: sequences of a thread.  CLUSTER: eight CTAs, or one (whose barriers are the block's).
 template <int kStepRun, bool CLUSTER>
 __global__ void __launch_bounds__(kStepThreads) step_tables_kernel(const StepArgs a) {
@@ -473,10 +462,10 @@ cudaError_t launch_step_tables(const StepArgs& a, cudaStream_t stream) {
 }
 
 cudaError_t launch_kv_append_f8(void* kq, void* vq, float* ks, float* vs, const void* k, const void* v,
-                                const int64_t* slots, int64_t T, int Hkv, int D, int NB, int32_t* err,
+                                const int64_t* slots, int64_t T, int Hkv, int D, int NB, int32_t* err, int sms,
                                 cudaStream_t stream) {
-  // the window: as many tokens as let all CTAs run at once (four on each of 152 SMs)
-  int window = (int)std::min<int64_t>(16, (T + 607) / 608);
+  // the window: as many tokens as let all CTAs run at once (four on each SM)
+  int window = (int)std::min<int64_t>(16, (T + 4 * sms - 1) / (4 * sms));
   const int64_t blocks = (T + window - 1) / window;
   void* params[] = {&kq, &vq, &ks, &vs, &k, &v, &slots, &T, &Hkv, &NB, &window, &err};
   const void* f = D == 128 ? (const void*)kv_append_f8_kernel<128> : (const void*)kv_append_f8_kernel<64>;
@@ -547,10 +536,11 @@ int pkv_kv_append_f8(void* k_codes, void* v_codes, float* k_scales, float* v_sca
       ((reinterpret_cast<uintptr_t>(k_scales) | reinterpret_cast<uintptr_t>(v_scales) |
         reinterpret_cast<uintptr_t>(error_word)) & 3u) || (reinterpret_cast<uintptr_t>(slot_mapping) & 7u))
     return PKV_ERR_ALIGNMENT;
-  st = device_ready();
+  int sms = 0;
+  st = device_ready(&sms);
   if (st != PKV_OK) return st;
   return cuda_status(launch_kv_append_f8(k_codes, v_codes, k_scales, v_scales, k, v, slot_mapping, num_tokens,
-                                         dims->num_kv_heads, dims->head_dim, dims->num_blocks, error_word,
+                                         dims->num_kv_heads, dims->head_dim, dims->num_blocks, error_word, sms,
                                          static_cast<cudaStream_t>(stream)));
 }
 
