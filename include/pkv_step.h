@@ -129,7 +129,8 @@ int pkv_paged_decode_attention_rules(void* out, const void* q, const void* k_cac
 
 /*
  * pkv_paged_decode_attention_f8 -- pkv_paged_decode_attention over FP8 pools (value = code * scale of
- * the key's block), with score rules.
+ * the key's block), with score rules.  Weights are fp32 numbers relative to the row's largest, and enter
+ * the product with V times their block's scale as one fp16 term (11 bits).
  *   k_codes, v_codes   : [NB, Hkv, 16, d] E4M3, 16-byte aligned.
  *   k_scales, v_scales : [NB, Hkv] fp32, finite and >= 0.
  *   rules              : or NULL (plain softmax over all keys).
@@ -155,7 +156,9 @@ size_t pkv_prefill_workspace_bytes(const pkv_dims* dims, int32_t total_tokens);
  * pkv_paged_prefill_attention -- attention of many query tokens per sequence over the paged cache:
  * prompts, chunks of prompts and mixed steps, causal, with score rules (the prefill stage of "KV Cache
  * primer" section 2.1 over the blocks of section 4.1).  The K and V rows of the queries' own tokens
- * are in the cache already.
+ * are in the cache already.  bf16 pools only: a prompt over an FP8 cache is not offered.  Weights enter
+ * the product with V as two bf16 terms in sequences of at most 512 keys, as one (8 bits) in longer ones;
+ * their sum is fp32.
  *   out, q        : [total_tokens, Hq, d] bf16.  Sequence b's queries are rows query_starts[b] ..
  *                   query_starts[b+1] - 1, n_b of them, at positions L_b - n_b + r.  Rows from
  *                   query_starts[B] on (a padded batch) are neither read nor written.

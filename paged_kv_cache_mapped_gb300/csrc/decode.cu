@@ -45,7 +45,8 @@
 //    with the codes made fp16 by the hardware conversion; the block's K scale multiplies its logits
 //    and its V scale enters P, relative to a reference of each head that follows logit and scale
 //    together.  Half the bytes of bf16 at the same instructions a unit and more: issue and bytes bound it
-//    together (32 sequences of ~4000 tokens, 32 / 8 heads, d 128: 49.0 us, 5.3 TB/s; 4 of 131072: 171 us, 6.3 TB/s).
+//    together (32 sequences of ~4000 tokens, 32 / 8 heads, d 128: 49.2 us, 5.3 TB/s; 4 of 131072: 172 us, 6.3 TB/s).  Score
+//    rules add to the issue: 55.8 us with a cap, 61.6 with a distance bias, 65.4 with both (4 of 131072: 196, 217, 233).
 //  * Score rules (capped scores, distance bias, window, documents, prefix): a sequence's units are
 //    those of its prefix and of its interval, so masked blocks are not read, and the logits pass through
 //    the cap and the bias in fp32 before the softmax.  Bytes bound it as the plain form (32 of ~4000, capped

@@ -16,15 +16,17 @@
 //    rules, keep the running maximum (moved only when exceeded by 2^8, and O rescaled then) and sum,
 //    and write P.  The softmax of one step runs under the products of the next, and of the other row tile.
 //  * prefill_merge_kernel joins the shares of split items by their maxima and sums.
-// What bounds it: long chunks the MMAs' issue and rate and the exponentials together (4096 tokens on 16384 keys, 32 / 8 heads,
-// d 128: 720-730 us, 1320-1340 TFLOP/s, 69 % of the measured bf16 rate; with a distance bias 810; capped 841 where
-// the scores stay below a fifth of the cap, 1045 below 0.8 of it, 1520 beyond); many
-// single tokens the bytes (64 on 2000 keys each 109 us, 4.8 TB/s; 4 on 131072 338 us, 6.4 TB/s); small batches the
-// chain of plan, first loads and merge (one token on 200 keys 19 us).  A CTA holds two row tiles
-// because every K and V tile that comes into shared memory then serves 256 rows.
+// What bounds it: long chunks the chain of a step (products, load, maximum, exponentials, store) at two softmax warps a
+// scheduler, no unit being full (4096 tokens on 16384 keys, 32 / 8 heads, d 128: 720-750 us, 1290-1340 TFLOP/s, 67-70 % of
+// the measured bf16 rate; tensor pipe 56 %, issue 47 %, exponentials 28 %; with a distance bias 810 us; capped 836-871 where the
+// scores stay below a fifth of the cap, 1020-1045 below 0.8 of it, 1490-1520 beyond); d 64 the same chain, its
+// products halved (4 prompts of 3000, 8 heads, bias and a window of 1000: 57-59 us, tensor pipe 16 %, issue 36 %); many single
+// tokens the loads in flight, a K and a V tile a CTA (64 on 2000 keys each 110 us, 4.8 TB/s, DRAM at 62 % of its peak; 4
+// on 131072 336-338 us, 6.4 TB/s); small batches the chain of plan, first loads and merge (one token on 200 keys 19 us).
+// A CTA holds two row tiles because every K and V tile that comes into shared memory then serves 256 rows.
 // P is rounded to bf16 for the product (the sum takes it in fp32).  Rows over more than kTwoTermTiles key
-// tiles take that one term: its error, at most 2^-8 of each weight and independent from key to key, is of the
-// size of a bf16 output's own rounding.  Shorter rows, where few weights may carry the result, add the
+// tiles take that one term: its error, at most 2^-8 of each weight, is of the size of a bf16 output's own rounding
+// where a few keys or equal weights carry a row, and averages out where many unequal ones do.  Shorter rows, where few weights may carry the result, add the
 // remainder as a second term, which costs half as many MMAs again (all rows in two terms: chunk of 4096 on 16384
 // 937 us against 730; none: 24 mixed sequences 26.3 against 28.5).
 // Non-finite V: a masked key's weight is 0, and 0 * NaN is NaN, so V rows past the sequence are cleared,

@@ -248,7 +248,8 @@ def paged_prefill_attention(q, k_cache, v_cache, block_tables, context_lens, que
     """Causal attention of many query tokens per sequence over the paged cache, with score rules.
     q [T, Hq, d] bf16 packs the queries of every sequence: rows query_starts[b] .. query_starts[b+1]
     (int32 [B + 1]) are sequence b's last positions, context_lens [B] counts its keys with the step's own.
-    The rules are those of paged_decode_attention_rules, doc_starts one int32 per packed row [T].  Returns
+    The pools are bf16 (there is no form over the FP8 cache).  The rules are those of
+    paged_decode_attention_rules, doc_starts one int32 per packed row [T].  Returns
     out [T, Hq, d]; rows from query_starts[B] on are left as they were (unset when `out` is made here)."""
     nb, hkv, d, dev, kp, vp = _bf16_pools(k_cache, v_cache)
     qp = _need(q, "q", torch.bfloat16, 3, dev)
