@@ -52,7 +52,8 @@ extern "C" {
  *                      table), PKV_DEV_BAD_QUERY_RANGE (n_b < -1, or more than max_new_tokens in
  *                      all), PKV_DEV_NO_BLOCKS (too few free blocks; a free count outside the stack
  *                      or one that the pushed blocks would take past it), PKV_DEV_BAD_BLOCK_ID (a
- *                      held, pushed or taken block outside the pool).
+ *                      block outside the pool among those pushed, taken, or part filled and written on;
+ *                      a sequence's other blocks are not looked at).
  * Arrays are aligned to their elements (slot_mapping to 8 bytes).
  * All or nothing: on an error the lengths and the count are passed through unchanged, the tables
  * and the stack's live entries stay as they were, every query_starts entry is 0 and every slot and
