@@ -1,6 +1,6 @@
 """Paged KV-cache decode attention for GB300 (sm_103a).
 
-Python binding of libpkv (declared in include/pkv.h and include/pkv_step.h).  Each function checks the torch
+Python binding of libpkv (declared in the headers of include/).  Each function checks the torch
 tensors it is given, builds the C shape record and calls the C-ABI entry point of the same
 name (``pkv_<name>``) on the current CUDA stream.  All computation happens in the library's
 CUDA kernels; CPU tensors are rejected, there is no fallback path.  PyTorch only provides
@@ -14,6 +14,7 @@ import ctypes
 import torch
 
 from ._lib import PkvDims, PkvError, check, header_constants, header_functions, load
+from .evict import evict_workspace_bytes, kv_evict, kv_evict_q8
 from .step import (kv_append_f8, kv_step_tables, paged_decode_attention_f8, paged_decode_attention_rules,
                    paged_prefill_attention, prefill_workspace_bytes)
 
@@ -30,6 +31,7 @@ __all__ = [
     "paged_decode_attention_append_q8", "sparse_decode_attention_q8",
     "kv_step_tables", "kv_append_f8", "paged_decode_attention_rules", "paged_decode_attention_f8",
     "paged_prefill_attention", "prefill_workspace_bytes",
+    "kv_evict", "kv_evict_q8", "evict_workspace_bytes",
 ]
 
 BLOCK_SIZE = 16

@@ -1,5 +1,5 @@
 """ctypes handle on libpkv.so: loads the in-tree library and declares the C signatures of
-include/pkv.h and include/pkv_step.h.  No arithmetic happens here."""
+include/pkv.h, include/pkv_step.h and include/pkv_evict.h.  No arithmetic happens here."""
 from __future__ import annotations
 
 import ctypes
@@ -11,6 +11,7 @@ PKG = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(PKG, "libpkv.so")
 HEADER = os.path.join(os.path.dirname(PKG), "include", "pkv.h")
 STEP_HEADER = os.path.join(os.path.dirname(PKG), "include", "pkv_step.h")
+EVICT_HEADER = os.path.join(os.path.dirname(PKG), "include", "pkv_evict.h")
 
 _lock = threading.Lock()
 _lib = None
@@ -35,6 +36,27 @@ class PkvScoreRules(ctypes.Structure):
         ("alibi_slopes", ctypes.c_void_p),
         ("doc_starts", ctypes.c_void_p),
         ("prefix_lens", ctypes.c_void_p),
+    ]
+
+
+class PkvEvictRules(ctypes.Structure):
+    _fields_ = [
+        ("n_sink", ctypes.c_int32),
+        ("k_top", ctypes.c_int32),
+        ("n_recent", ctypes.c_int32),
+        ("trigger", ctypes.c_int32),
+    ]
+
+
+class PkvEvictState(ctypes.Structure):
+    _fields_ = [
+        ("scores", ctypes.c_void_p),
+        ("scores_out", ctypes.c_void_p),
+        ("slot_pos", ctypes.c_void_p),
+        ("slot_pos_out", ctypes.c_void_p),
+        ("dropped", ctypes.c_void_p),
+        ("dropped_out", ctypes.c_void_p),
+        ("stride", ctypes.c_int32),
     ]
 
 
@@ -78,6 +100,7 @@ def load():
         U32 = ctypes.c_uint32
         D = ctypes.POINTER(PkvDims)
         R = ctypes.POINTER(PkvScoreRules)
+        ER, ES = ctypes.POINTER(PkvEvictRules), ctypes.POINTER(PkvEvictState)
         sig = {
             "pkv_kv_append": (I32, [P, P, P, P, P, I64, D, P, P]),
             "pkv_kv_append_q8": (I32, [P, P, P, P, P, P, P, I64, D, P, P]),
@@ -107,6 +130,9 @@ def load():
             "pkv_prefill_workspace_bytes": (SZ, [D, I32]),
             "pkv_paged_prefill_attention": (I32, [P, P, P, P, P, P, P, I32, F32, R, P, SZ, D, P, P]),
             "pkv_kv_append_f8": (I32, [P, P, P, P, P, P, P, I64, D, P, P]),
+            "pkv_evict_workspace_bytes": (SZ, [D, ER]),
+            "pkv_kv_evict": (I32, [P, P, P, P, P, ES, ER, P, P, P, P, SZ, D, P, P]),
+            "pkv_kv_evict_q8": (I32, [P, P, P, P, P, P, P, ES, ER, P, P, P, P, SZ, D, P, P]),
             "pkv_read_error": (I32, [P, I32, P]),
             "pkv_device_alias": (I32, [P, ctypes.POINTER(ctypes.c_void_p)]),
             "pkv_status_string": (ctypes.c_char_p, [I32]),

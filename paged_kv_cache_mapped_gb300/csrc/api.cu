@@ -87,6 +87,7 @@ const DeviceInfo* device_info(int* status) {
       if (e == cudaSuccess) e = prefill_device_setup();
       if (e == cudaSuccess) e = step_device_setup();
       if (e == cudaSuccess) e = prefill_attention_device_setup();
+      if (e == cudaSuccess) e = evict_device_setup();
       if (e != cudaSuccess) {
         cudaGetLastError();
         *status = PKV_ERR_CUDA_BASE + (int)e;

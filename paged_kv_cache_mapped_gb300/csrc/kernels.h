@@ -331,6 +331,9 @@ size_t prefill_attention_workspace(int B, int T, int Hq, int G, int D);
 cudaError_t prefill_attention_device_setup();
 cudaError_t launch_prefill_attention(const PrefillAttnArgs& a, void* workspace, int head_dim, cudaStream_t stream);
 
+// Eviction (evict.cu).
+cudaError_t evict_device_setup();
+
 // Host-side checks shared by the entry points (api.cu).
 int check_dims(const struct pkv_dims* d, bool need_q_heads);
 bool aligned16(const void* p);
