@@ -1,5 +1,5 @@
 """ctypes handle on libpkv.so: loads the in-tree library and declares the C signatures of
-include/pkv.h, include/pkv_step.h and include/pkv_evict.h.  No arithmetic happens here."""
+include/pkv.h, pkv_step.h, pkv_evict.h and pkv_diff.h.  No arithmetic happens here."""
 from __future__ import annotations
 
 import ctypes
@@ -12,6 +12,7 @@ LIB_PATH = os.path.join(PKG, "libpkv.so")
 HEADER = os.path.join(os.path.dirname(PKG), "include", "pkv.h")
 STEP_HEADER = os.path.join(os.path.dirname(PKG), "include", "pkv_step.h")
 EVICT_HEADER = os.path.join(os.path.dirname(PKG), "include", "pkv_evict.h")
+DIFF_HEADER = os.path.join(os.path.dirname(PKG), "include", "pkv_diff.h")
 
 _lock = threading.Lock()
 _lib = None
@@ -36,6 +37,15 @@ class PkvScoreRules(ctypes.Structure):
         ("alibi_slopes", ctypes.c_void_p),
         ("doc_starts", ctypes.c_void_p),
         ("prefix_lens", ctypes.c_void_p),
+    ]
+
+
+class PkvDiffParams(ctypes.Structure):
+    _fields_ = [
+        ("lambdas", ctypes.c_void_p),
+        ("lambda_rows", ctypes.c_int32),
+        ("norm_eps", ctypes.c_float),
+        ("norm_weight", ctypes.c_void_p),
     ]
 
 
@@ -100,6 +110,7 @@ def load():
         U32 = ctypes.c_uint32
         D = ctypes.POINTER(PkvDims)
         R = ctypes.POINTER(PkvScoreRules)
+        DP = ctypes.POINTER(PkvDiffParams)
         ER, ES = ctypes.POINTER(PkvEvictRules), ctypes.POINTER(PkvEvictState)
         sig = {
             "pkv_kv_append": (I32, [P, P, P, P, P, I64, D, P, P]),
@@ -130,6 +141,10 @@ def load():
             "pkv_prefill_workspace_bytes": (SZ, [D, I32]),
             "pkv_paged_prefill_attention": (I32, [P, P, P, P, P, P, P, I32, F32, R, P, SZ, D, P, P]),
             "pkv_kv_append_f8": (I32, [P, P, P, P, P, P, P, I64, D, P, P]),
+            "pkv_diff_decode_workspace_bytes": (SZ, [D, I32]),
+            "pkv_paged_diff_decode_attention": (I32, [P, P, P, P, P, P, F32, DP, R, P, SZ, D, U32, P, P]),
+            "pkv_paged_diff_decode_attention_scores": (I32, [P, P, P, I32, P, P, P, P, P, F32, DP, R, P, SZ, D, U32, P,
+                                                             P]),
             "pkv_evict_workspace_bytes": (SZ, [D, ER]),
             "pkv_kv_evict": (I32, [P, P, P, P, P, ES, ER, P, P, P, P, SZ, D, P, P]),
             "pkv_kv_evict_q8": (I32, [P, P, P, P, P, P, P, ES, ER, P, P, P, P, SZ, D, P, P]),

@@ -5,6 +5,7 @@
 
 #include <algorithm>
 #include <atomic>
+#include <cmath>
 #include <cstring>
 #include <mutex>
 
@@ -20,13 +21,17 @@ constexpr int kNumHeadDims = 2;
 constexpr int kGroups[] = {1};  // every group size shares one kernel per (head_dim, mode)
 constexpr int kNumGroups = 1;
 
+constexpr int kNumModes = 11;
+
 struct DeviceInfo {
   bool ready = false;
   int sm_count = 0;
-  size_t max_dyn_smem[2][9] = {};  // [head_dim index][mode: dense, sparse, dense + scores,
-                                   //   dense INT8, INT8 + scores, sparse INT8, rules, FP8, FP8 + rules]:
+  size_t max_dyn_smem[2][kNumModes] = {};  // [head_dim index][mode: dense, sparse, dense + scores,
+                                   //   dense INT8, INT8 + scores, sparse INT8, rules, FP8, FP8 + rules,
+                                   //   differential, differential + scores]:
                                    //   opt-in minus static shared memory
   int merge_ctas_per_sm[2] = {};   // [head_dim index]: resident merge CTAs per SM
+  int diff_merge_ctas_per_sm[2] = {};  // likewise, of the differential form
 };
 
 std::mutex g_mutex;
@@ -56,9 +61,11 @@ const DeviceInfo* device_info(int* status) {
     }
     for (int hd = 0; hd < kNumHeadDims; ++hd) {
       for (int gi = 0; gi < kNumGroups; ++gi) {
-        for (int sp = 0; sp < 9; ++sp) {
-          const DecodeKernel k = decode_kernel(hd == 0 ? 128 : 64, kGroups[gi], sp == 1 || sp == 5, sp == 2 || sp == 4,
-                                               sp >= 3 && sp != 6, sp >= 7, sp == 6 || sp == 8);
+        for (int sp = 0; sp < kNumModes; ++sp) {
+          const bool diff = sp >= 9;
+          const DecodeKernel k =
+              decode_kernel(hd == 0 ? 128 : 64, kGroups[gi], sp == 1 || sp == 5, sp == 2 || sp == 4 || sp == 10,
+                            sp >= 3 && sp != 6 && !diff, sp >= 7 && !diff, sp == 6 || sp == 8 || diff, diff);
           if (k.split == nullptr) continue;
           cudaFuncAttributes fa{};
           cudaError_t e = cudaFuncGetAttributes(&fa, k.split);
@@ -78,7 +85,7 @@ const DeviceInfo* device_info(int* status) {
             *status = PKV_ERR_CUDA_BASE + (int)e;
             return nullptr;
           }
-          info.merge_ctas_per_sm[hd] = per_sm > 0 ? per_sm : 1;
+          (diff ? info.diff_merge_ctas_per_sm : info.merge_ctas_per_sm)[hd] = per_sm > 0 ? per_sm : 1;
         }
       }
     }
@@ -158,7 +165,7 @@ int merge_warps_log2(const pkv_dims* d, int max_units, long long workers, int mi
 // Resident split CTAs per SM for this kernel and dynamic shared memory: the answer of the last query per
 // kernel is kept (a program's steps repeat their batch size), packed with its question in one word.
 int decode_ctas_per_sm(const DeviceInfo* info, const void* kernel, int hd, int mode, size_t smem, int* per_sm) {
-  static std::atomic<unsigned long long> last[kMaxDevices][2][9];
+  static std::atomic<unsigned long long> last[kMaxDevices][2][kNumModes];
   std::atomic<unsigned long long>& at = last[info - g_devices][hd][mode];
   const unsigned long long known = at.load(std::memory_order_relaxed);
   if (known != 0 && (known >> 8) == smem + 1) {
@@ -269,18 +276,38 @@ WorkspacePlan fit_workspace(const pkv_dims* d, size_t bytes) {
 
 namespace {
 
+// The score step of a differential decode: fp32 log-sum-exps [B, Hq, 2] | logits [B, Hq, 2, stride].
+size_t diff_score_bytes(const pkv_dims* d, int stride) {
+  if (stride <= 0) return 0;
+  const size_t maps = 2 * (size_t)d->batch * d->num_q_heads;
+  return align256(sizeof(float) * maps) + align256(sizeof(float) * maps * stride);
+}
+
 }  // namespace
+
+int check_diff(const pkv_diff_params* p) {
+  if (p == nullptr || p->lambdas == nullptr) return PKV_ERR_NULL_POINTER;
+  if (p->lambda_rows != 0 && p->lambda_rows != 1) return PKV_ERR_ARGUMENT;
+  if (p->norm_weight != nullptr && !(p->norm_eps > 0.f && p->norm_eps < INFINITY)) return PKV_ERR_ARGUMENT;
+  if ((reinterpret_cast<uintptr_t>(p->lambdas) | reinterpret_cast<uintptr_t>(p->norm_weight)) & 3u) return PKV_ERR_ALIGNMENT;
+  return PKV_OK;
+}
 
 int decode_common(void* out, const void* q, const void* k_cache, const void* v_cache,
                   const int32_t* block_tables, const int32_t* context_lens, const int32_t* kept,
                   const int32_t* kept_lens, int32_t max_kept, float scale, int32_t window,
                   void* workspace, size_t workspace_bytes, const pkv_dims* dims, int32_t* err,
                   void* stream, bool sparse, const void* k_new, const void* v_new,
-                  const ScoreOutputs* score_out, const Q8Scales* q8, uint32_t flags, const pkv_score_rules* rules) {
+                  const ScoreOutputs* score_out, const Q8Scales* q8, uint32_t flags, const pkv_score_rules* rules,
+                  const DiffDecode* diff) {
   int st = check_dims(dims, true);
   if (st != PKV_OK) return st;
   if (dims->batch > kMaxBatch) return PKV_ERR_DIMS;
   if ((flags & ~(uint32_t)PKV_DECODE_INPUTS_READY) != 0) return PKV_ERR_ARGUMENT;
+  if (diff != nullptr) {
+    st = check_diff(diff->params);
+    if (st != PKV_OK) return st;
+  }
   if (dims->batch == 0) return PKV_OK;
   if (!out || !q || !k_cache || !v_cache || !block_tables || !context_lens || !workspace)
     return (!workspace) ? PKV_ERR_WORKSPACE : PKV_ERR_NULL_POINTER;
@@ -310,8 +337,11 @@ int decode_common(void* out, const void* q, const void* k_cache, const void* v_c
          reinterpret_cast<uintptr_t>(score_out->logits)) & 3u)
       return PKV_ERR_ALIGNMENT;
   }
-  const DecodeKernel k = decode_kernel(dims->head_dim, group, sparse, score_out != nullptr, q8 != nullptr, f8,
-                                       rules != nullptr);
+  const bool diff_scores = diff != nullptr && diff->scores_out != nullptr;
+  const pkv_score_rules no_rules{};
+  if (diff != nullptr && rules == nullptr) rules = &no_rules;  // (one form serves both)
+  const DecodeKernel k = decode_kernel(dims->head_dim, group, sparse, score_out != nullptr || diff_scores, q8 != nullptr, f8,
+                                       rules != nullptr, diff != nullptr);
   if (k.split == nullptr) return PKV_ERR_GQA;
   const int max_units = sparse ? (max_kept + 15) / 16 : dims->max_blocks_per_seq;
   // the flattened unit count and the pool's row count (a TMA coordinate) must fit int32
@@ -320,12 +350,19 @@ int decode_common(void* out, const void* q, const void* k_cache, const void* v_c
   const long long pool_rows = (long long)dims->num_blocks * dims->num_kv_heads * PKV_BLOCK_SIZE;
   if (pool_rows >= (1ll << 31)) return PKV_ERR_DIMS;
   // partial slots for at least the static ranges of the largest grid
-  const WorkspacePlan plan = fit_workspace(dims, workspace_bytes);
+  pkv_dims rows = *dims;  // whose query heads are the rows with partials: a differential head has two
+  size_t extra = 0;       // and the logits and log-sum-exps of its score step stand behind them
+  if (diff != nullptr) {
+    if (dims->num_q_heads >= (1 << 30)) return PKV_ERR_DIMS;
+    rows.num_q_heads = 2 * dims->num_q_heads;
+    extra = diff_score_bytes(dims, diff->stride);
+  }
+  const WorkspacePlan plan = fit_workspace(&rows, workspace_bytes > extra ? workspace_bytes - extra : 0);
   if (plan.ranges < kMaxWorkers) return PKV_ERR_WORKSPACE;
   const DeviceInfo* info = device_info(&st);
   if (!info) return st;
   const size_t smem = decode_smem_bytes(dims->head_dim, sparse, dims->batch, rules != nullptr);
-  const int mode = f8 ? (rules ? 8 : 7) : rules ? 6 : sparse ? (q8 ? 5 : 1) : (q8 ? (score_out ? 4 : 3) : (score_out ? 2 : 0));
+  const int mode = diff ? (diff_scores ? 10 : 9) : f8 ? (rules ? 8 : 7) : rules ? 6 : sparse ? (q8 ? 5 : 1) : (q8 ? (score_out ? 4 : 3) : (score_out ? 2 : 0));
   if (smem > info->max_dyn_smem[head_dim_index(dims->head_dim)][mode])
     return PKV_ERR_DIMS;
   int per_sm = 0;
@@ -376,6 +413,19 @@ int decode_common(void* out, const void* q, const void* k_cache, const void* v_c
     a.scores = score_out->scores;
     a.score_stride = score_out->stride;
   }
+  if (diff != nullptr) {
+    a.lambdas = diff->params->lambdas;
+    a.lambda_stride = diff->params->lambda_rows != 0 ? dims->num_q_heads : 0;
+    a.norm_weight = diff->params->norm_weight;
+    a.norm_eps = diff->params->norm_eps;
+    if (diff_scores) {
+      a.lse = reinterpret_cast<float*>(ws + plan.total);
+      a.logits = a.lse + align256(sizeof(float) * 2 * (size_t)dims->batch * dims->num_q_heads) / sizeof(float);
+      a.scores = const_cast<float*>(diff->scores);
+      a.scores_out = diff->scores_out;
+      a.score_stride = diff->stride;
+    }
+  }
   a.err = err;
   a.B = dims->batch;
   a.Hq = dims->num_q_heads;
@@ -422,10 +472,13 @@ int decode_common(void* out, const void* q, const void* k_cache, const void* v_c
   a.merge_trigger_early = (a.early != 0 && q8 == nullptr) ? 1 : 0;
   a.scale_log2 = scale * 1.4426950408889634f;
   a.timeout_ns = kWaitTimeoutNs;
-  const int wpr_log2 = merge_warps_log2(
-      dims, max_units, workers, a.min_units, a.min_busy_pct, a.tail_pct, a.chunk_min, a.cpw_cap,
-      (long long)info->sm_count * info->merge_ctas_per_sm[head_dim_index(dims->head_dim)] * kMergeWarps,
+  int wpr_log2 = merge_warps_log2(
+      &rows, max_units, workers, a.min_units, a.min_busy_pct, a.tail_pct, a.chunk_min, a.cpw_cap,
+      (long long)info->sm_count *
+          (diff != nullptr ? info->diff_merge_ctas_per_sm : info->merge_ctas_per_sm)[head_dim_index(dims->head_dim)] *
+          kMergeWarps,
       dense_q8 ? PKV_MERGE_PARTIALS_PER_WARP_Q8 : PKV_MERGE_PARTIALS_PER_WARP);
+  if (diff != nullptr) wpr_log2 = std::min(wpr_log2, 2);  // a head's two maps in one CTA
   return cuda_status(launch_decode(k, a, grid, smem, wpr_log2, static_cast<cudaStream_t>(stream)));
 }
 
@@ -487,6 +540,41 @@ int pkv_paged_decode_attention_f8(void* out, const void* q, const void* k_codes,
   const Q8Scales f8{k_scales, v_scales, true};
   return decode_common(out, q, k_codes, v_codes, block_tables, context_lens, nullptr, nullptr, 0, scale, 0, workspace,
                        workspace_bytes, dims, error_word, stream, false, nullptr, nullptr, nullptr, &f8, flags, rules);
+}
+
+size_t pkv_diff_decode_workspace_bytes(const pkv_dims* dims, int32_t score_stride) {
+  if (pkv_decode_workspace_bytes(dims) == 0 || score_stride < 0) return 0;
+  pkv_dims rows = *dims;
+  if (rows.num_q_heads >= (1 << 30)) return 0;
+  rows.num_q_heads *= 2;
+  return plan_workspace(&rows, (long long)kMaxWorkers * (1 + std::min(PKV_MAX_TAIL_CHUNKS, kMaxTailChunksLimit))).total +
+         diff_score_bytes(dims, score_stride);
+}
+
+int pkv_paged_diff_decode_attention(void* out, const void* q, const void* k_cache, const void* v_cache,
+                                    const int32_t* block_tables, const int32_t* context_lens, float scale,
+                                    const pkv_diff_params* params, const pkv_score_rules* rules, void* workspace,
+                                    size_t workspace_bytes, const pkv_dims* dims, uint32_t flags, int32_t* error_word,
+                                    void* stream) {
+  const DiffDecode diff{params};
+  return decode_common(out, q, k_cache, v_cache, block_tables, context_lens, nullptr, nullptr, 0, scale, 0, workspace,
+                       workspace_bytes, dims, error_word, stream, false, nullptr, nullptr, nullptr, nullptr, flags, rules,
+                       &diff);
+}
+
+int pkv_paged_diff_decode_attention_scores(void* out, const float* scores, float* scores_out, int32_t score_stride,
+                                           const void* q, const void* k_cache, const void* v_cache,
+                                           const int32_t* block_tables, const int32_t* context_lens, float scale,
+                                           const pkv_diff_params* params, const pkv_score_rules* rules,
+                                           void* workspace, size_t workspace_bytes, const pkv_dims* dims,
+                                           uint32_t flags, int32_t* error_word, void* stream) {
+  if (!scores || !scores_out) return PKV_ERR_NULL_POINTER;
+  if (score_stride <= 0) return PKV_ERR_DIMS;
+  if ((reinterpret_cast<uintptr_t>(scores) | reinterpret_cast<uintptr_t>(scores_out)) & 3u) return PKV_ERR_ALIGNMENT;
+  const DiffDecode diff{params, scores, scores_out, score_stride};
+  return decode_common(out, q, k_cache, v_cache, block_tables, context_lens, nullptr, nullptr, 0, scale, 0, workspace,
+                       workspace_bytes, dims, error_word, stream, false, nullptr, nullptr, nullptr, nullptr, flags, rules,
+                       &diff);
 }
 
 int pkv_kv_append_q8(void* k_codes, void* v_codes, float* k_scales, float* v_scales, const void* k,

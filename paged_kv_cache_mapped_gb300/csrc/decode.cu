@@ -59,6 +59,7 @@
 //  * Every wait is bounded (globaltimer); a timeout records PKV_DEV_WAIT_TIMEOUT, waits for
 //    the copies in flight and returns.  Bad block ids / kept indices are skipped and
 //    recorded, never dereferenced.
+#include <algorithm>
 #include <cmath>
 
 #include "kernels.h"
@@ -315,11 +316,14 @@ constexpr float kLog2e = 1.4426950408889634f;
 // SCORES (dense only): also keep every attended key's base-2 logit and write the log-sum-exp of
 // rows written out directly, for the score step (decode_score_kernel).
 // F8 (with Q8): the codes are E4M3 with a scale per block and kv head.  RULES (dense only): score rules.
-template <int D, bool SPARSE, bool SCORES, bool Q8, bool F8 = false, bool RULES = false>
+// DIFF (bf16, with RULES): differential attention; each head has two maps, and SCORES keeps the logits of both.
+template <int D, bool SPARSE, bool SCORES, bool Q8, bool F8 = false, bool RULES = false, bool DIFF = false>
 __global__ void __launch_bounds__(kDecodeWarps * 32, Q8 ? (F8 ? PKV_F8_MIN_CTAS : PKV_Q8_MIN_CTAS) : 0)
 decode_split_kernel(const __grid_constant__ DecodeArgs a) {
   static_assert(!(SPARSE && SCORES), "scores are emitted by the dense decode only");
-  static_assert(!(F8 && (SPARSE || SCORES || !Q8)) && !(RULES && (SPARSE || SCORES)), "dense decode only");
+  static_assert(!(F8 && (SPARSE || SCORES || !Q8)) && !(RULES && (SPARSE || (SCORES && !DIFF))), "dense decode only");
+  static_assert(!DIFF || (RULES && !Q8), "bf16 pools, with the rules' unit list");
+  constexpr int kMaps = DIFF ? 2 : 1;
   using GE = Geo<D, SPARSE, Q8, F8>;
   using WT = WarpTiles<D, SPARSE, Q8, F8>;
   using WB = WarpSlots<D, SPARSE, Q8, F8>;
@@ -727,6 +731,9 @@ decode_split_kernel(const __grid_constant__ DecodeArgs a) {
   float o[KS][4];        // O^T accumulator fragments: [m-tile][d row gq / gq+8, head h0 / h1]
   float mr0 = -INFINITY, mr1 = -INFINITY;  // running max (reference) of heads h0, h1
   float l0 = 0.f, l1 = 0.f;                // this lane's share of the running sums
+  // DIFF: the second map's accumulators, maximum and sums
+  float od[DIFF ? KS : 1][4];
+  float nr0 = -INFINITY, nr1 = -INFINITY, n0 = 0.f, n1 = 0.f;
   int seg_b = -1, seg_g = -1;
   int seg_slot = -1;  // partial slot of the current segment, -1: written out directly
   float* seg_logits = nullptr;  // scores mode: logit row of this lane's head h0 in the segment
@@ -764,6 +771,63 @@ decode_split_kernel(const __grid_constant__ DecodeArgs a) {
     for (int m = 4; m <= 16; m <<= 1) {
       l0 += __shfl_xor_sync(kFullMask, l0, m);
       l1 += __shfl_xor_sync(kFullMask, l1, m);
+    }
+    if constexpr (DIFF) {
+#pragma unroll
+      for (int m = 4; m <= 16; m <<= 1) {
+        n0 += __shfl_xor_sync(kFullMask, n0, m);
+        n1 += __shfl_xor_sync(kFullMask, n1, m);
+      }
+#pragma unroll
+      for (int hh = 0; hh < 2; ++hh) {
+        const int head = 2 * tq + hh;
+        const bool live = head < G;
+        const float l[2] = {hh ? l1 : l0, hh ? n1 : n0}, m[2] = {hh ? mr1 : mr0, hh ? nr1 : nr0};
+        const size_t row = (size_t)seg_b * a.Hq + (size_t)seg_g * G + head;
+        if (seg_slot >= 0) {
+          if (!live) continue;
+#pragma unroll
+          for (int w = 0; w < 2; ++w) {
+            const size_t e = ((size_t)seg_slot * G + head) * 2 + w;
+            float* dst = a.part_o + e * D + gq;
+#pragma unroll
+            for (int mt = 0; mt < KS; ++mt) {
+              dst[mt * 16] = w ? od[mt][hh] : o[mt][hh];
+              dst[mt * 16 + 8] = w ? od[mt][2 + hh] : o[mt][2 + hh];
+            }
+            if (gq == 0) a.part_ml[e] = make_float2(m[w], l[w]);
+          }
+          continue;
+        }
+        if constexpr (SCORES) {  // base 2
+          if (live && gq < 2) a.lse[row * 2 + gq] = (gq ? l[1] : l[0]) > 0.f ? (gq ? m[1] + log2f(l[1]) : m[0] + log2f(l[0])) : -INFINITY;
+        }
+        const float f1 = l[0] > 0.f ? 1.f / l[0] : 0.f;
+        const float f2 = live && l[1] > 0.f ? __ldg(a.lambdas + (size_t)seg_b * a.lambda_stride + seg_g * G + head) / l[1] : 0.f;
+        float ss = 0.f;
+#pragma unroll
+        for (int mt = 0; mt < KS; ++mt) {
+          o[mt][hh] = o[mt][hh] * f1 - od[mt][hh] * f2;
+          o[mt][2 + hh] = o[mt][2 + hh] * f1 - od[mt][2 + hh] * f2;
+          ss = fmaf(o[mt][hh], o[mt][hh], fmaf(o[mt][2 + hh], o[mt][2 + hh], ss));
+        }
+        float f = 1.f;
+        if (a.norm_weight != nullptr) {
+#pragma unroll
+          for (int s = 4; s <= 16; s <<= 1) ss += __shfl_xor_sync(kFullMask, ss, s);
+          f = rsqrtf(ss * (1.f / D) + a.norm_eps);
+        }
+        if (!live) continue;
+        __nv_bfloat16* dst = a.out + row * D + gq;
+#pragma unroll
+        for (int mt = 0; mt < KS; ++mt) {
+          const float w0 = a.norm_weight != nullptr ? __ldg(a.norm_weight + mt * 16 + gq) : 1.f;
+          const float w1 = a.norm_weight != nullptr ? __ldg(a.norm_weight + mt * 16 + 8 + gq) : 1.f;
+          dst[mt * 16] = __float2bfloat16_rn(o[mt][hh] * f * w0);
+          dst[mt * 16 + 8] = __float2bfloat16_rn(o[mt][2 + hh] * f * w1);
+        }
+      }
+      return;
     }
     // FP8: what one of o's units is in weights of 2^(logit - mr), 2^(vr - kF8Up - mr)
     auto unit = [&](int hh) {
@@ -827,7 +891,7 @@ decode_split_kernel(const __grid_constant__ DecodeArgs a) {
     // partial in slot 2 ridx (the segment holds the range's start) or 2 ridx + 1 (its end)
     seg_slot = (seg_begin >= u0 && seg_begin + nb <= u0 + nunits) ? -1 : 2 * ridx + (u0 >= seg_begin ? 0 : 1);
     if constexpr (SCORES)
-      seg_logits = a.logits + ((size_t)c.b * a.Hq + (size_t)c.g * G + 2 * tq) * a.score_stride;
+      seg_logits = a.logits + ((size_t)c.b * a.Hq + (size_t)c.g * G + 2 * tq) * kMaps * a.score_stride;
     if constexpr (RULES) {
       if (a.slopes != nullptr) {
         const float* sp = a.slopes + (size_t)c.g * G;
@@ -905,6 +969,14 @@ decode_split_kernel(const __grid_constant__ DecodeArgs a) {
       for (int i = 0; i < 4; ++i) o[mt][i] = 0.f;
     mr0 = mr1 = -INFINITY;
     l0 = l1 = 0.f;
+    if constexpr (DIFF) {
+#pragma unroll
+      for (int mt = 0; mt < KS; ++mt)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) od[mt][i] = 0.f;
+      nr0 = nr1 = -INFINITY;
+      n0 = n1 = 0.f;
+    }
     // prefetch q of the segment that follows, if this worker reaches it
     if (seg_begin + nb < u0 + nunits) {
       int nb2 = c.b, ng2 = c.g + 1;
@@ -983,6 +1055,7 @@ decode_split_kernel(const __grid_constant__ DecodeArgs a) {
     if (mask != 0u) {
       // -- S^T = K q^T: 16 tokens x 8 heads --------------------------------------------------
       float c[4] = {kbias[0], kbias[1], kbias[2], kbias[3]};  // zero but for INT8 pools
+      float cd[4] = {0.f, 0.f, 0.f, 0.f};  // DIFF: the second map's, from the second halves of q and K
       const uint32_t kbase = smem_u32(Wt.k[slot]);
       float fk0 = sl2, fk1 = sl2;  // logit factor of tokens gq and gq + 8
       if constexpr (F8) {
@@ -1021,7 +1094,7 @@ decode_split_kernel(const __grid_constant__ DecodeArgs a) {
         for (int ks = 0; ks < KS; ++ks) {
           uint32_t af[4];
           ldsm_x4(kbase + chunk_offset<D, SPARSE>(k_row, 2 * ks + k_half), af);
-          mma_bf16_m16n8k16(c, af, qb[2 * ks], qb[2 * ks + 1]);
+          mma_bf16_m16n8k16(DIFF && ks >= KS / 2 ? cd : c, af, qb[2 * ks], qb[2 * ks + 1]);
         }
       }
       // c[0] = (token gq, head h0), c[1] = (gq, h1), c[2] = (gq + 8, h0), c[3] = (gq + 8, h1)
@@ -1049,15 +1122,16 @@ decode_split_kernel(const __grid_constant__ DecodeArgs a) {
       const float s10 = (t1 && v0) ? x10 : -INFINITY;
       const float s11 = (t1 && v1) ? x11 : -INFINITY;
       if constexpr (SCORES) {  // keep the attended keys' logits for the score step
-        const int tok = (s_first[cc.b] + cc.j) * 16 + gq;
+        const int tok = block_of(cc.b, cc.j) * 16 + gq;
         float* lg = seg_logits + tok;
+        const size_t next = (size_t)kMaps * a.score_stride;
         if (tok < a.score_stride) {
           if (t0 && v0) lg[0] = s00;
-          if (t0 && v1) lg[a.score_stride] = s01;
+          if (t0 && v1) lg[next] = s01;
         }
         if (tok + 8 < a.score_stride) {
           if (t1 && v0) lg[8] = s10;
-          if (t1 && v1) lg[a.score_stride + 8] = s11;
+          if (t1 && v1) lg[next + 8] = s11;
         }
       }
       // lazy running max: move it only when this unit's max is well above it.  Each lane checks
@@ -1159,6 +1233,62 @@ decode_split_kernel(const __grid_constant__ DecodeArgs a) {
       }
       const uint32_t bh0 = movmatrix_trans(hA), bh1 = movmatrix_trans(hB);
       const uint32_t bl0 = Q8 ? 0u : movmatrix_trans(lA), bl1 = Q8 ? 0u : movmatrix_trans(lB);
+      uint32_t dh0 = 0u, dh1 = 0u, dl0 = 0u, dl1 = 0u;
+      if constexpr (DIFF) {  // the second map likewise
+        float y[4];  // tokens gq (heads h0, h1) and gq + 8
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          float x = cd[i] * sl2;
+          if (a.cap_log2 > 0.f) x = cap_logit(x, a.cap_log2, a.cap_in);
+          if (a.slopes != nullptr) {
+            const float far = (float)(s_len[cc.b] - 1 - block_of(cc.b, cc.j) * 16 - gq - (i & 2) * 4);
+            x = fmaf(-((i & 1) ? slope1 : slope0), far, x);
+          }
+          y[i] = ((i & 2) ? t1 : t0) && ((i & 1) ? v1 : v0) ? x : -INFINITY;
+          if constexpr (SCORES) {
+            const int tok = block_of(cc.b, cc.j) * 16 + gq + (i & 2) * 4;
+            if (tok < a.score_stride && ((i & 2) ? t1 : t0) && ((i & 1) ? v1 : v0))
+              seg_logits[(size_t)(2 * (i & 1) + 1) * a.score_stride + tok] = x;
+          }
+        }
+        float my0 = fmaxf(y[0], y[2]), my1 = fmaxf(y[1], y[3]);
+        if (__any_sync(kFullMask, my0 > nr0 + kRescaleSlack || my1 > nr1 + kRescaleSlack)) {
+#pragma unroll
+          for (int m = 4; m <= 16; m <<= 1) {
+            my0 = fmaxf(my0, __shfl_xor_sync(kFullMask, my0, m));
+            my1 = fmaxf(my1, __shfl_xor_sync(kFullMask, my1, m));
+          }
+          float al0 = 1.f, al1 = 1.f;
+          if (my0 > nr0 + kRescaleSlack) {
+            al0 = exp2f(nr0 - my0);
+            nr0 = my0;
+          }
+          if (my1 > nr1 + kRescaleSlack) {
+            al1 = exp2f(nr1 - my1);
+            nr1 = my1;
+          }
+          n0 *= al0;
+          n1 *= al1;
+#pragma unroll
+          for (int mt = 0; mt < KS; ++mt) {
+            od[mt][0] *= al0;
+            od[mt][1] *= al1;
+            od[mt][2] *= al0;
+            od[mt][3] *= al1;
+          }
+        }
+        const float ry0 = (nr0 == -INFINITY) ? 0.f : nr0;
+        const float ry1 = (nr1 == -INFINITY) ? 0.f : nr1;
+        const float w00 = exp2f(y[0] - ry0), w01 = exp2f(y[1] - ry1);
+        const float w10 = exp2f(y[2] - ry0), w11 = exp2f(y[3] - ry1);
+        n0 += w00 + w10;
+        n1 += w01 + w11;
+        const uint32_t wA = pack_bf16x2(w00, w01), wB = pack_bf16x2(w10, w11);
+        dh0 = movmatrix_trans(wA);
+        dh1 = movmatrix_trans(wB);
+        dl0 = movmatrix_trans(pack_bf16x2(w00 - bf16_lo_to_f32(wA), w01 - bf16_hi_to_f32(wA)));
+        dl1 = movmatrix_trans(pack_bf16x2(w10 - bf16_lo_to_f32(wB), w11 - bf16_hi_to_f32(wB)));
+      }
       if (!__all_sync(kFullMask, mbar_wait_bounded(&Wb.bar_v[slot], parity, a.timeout_ns))) {
         if (lane == 0) record_error(a.err, PKV_DEV_WAIT_TIMEOUT);
         aborted = true;
@@ -1245,6 +1375,10 @@ decode_split_kernel(const __grid_constant__ DecodeArgs a) {
           ldsm_x4_trans(vbase + chunk_offset<D, SPARSE>(v_row, 2 * mt + v_half), av);
           mma_bf16_m16n8k16(o[mt], av, bh0, bh1);
           mma_bf16_m16n8k16(o[mt], av, bl0, bl1);
+          if constexpr (DIFF) {
+            mma_bf16_m16n8k16(od[mt], av, dh0, dh1);
+            mma_bf16_m16n8k16(od[mt], av, dl0, dl1);
+          }
         }
       }
     } else if (!__all_sync(kFullMask, mbar_wait_bounded(&Wb.bar_v[slot], parity, a.timeout_ns))) {
@@ -1284,9 +1418,12 @@ decode_split_kernel(const __grid_constant__ DecodeArgs a) {
 // first warp combines the wpr results through shared memory.  Also writes the zero row of
 // empty sequences, checks that every tail chunk was taken exactly once and re-arms the
 // ticket counters for the next call.
-template <int D>
+// DIFF: a row is a map of a query head, the two of a head next to one another in one CTA (wpr <= 4), whose difference
+// (and norm) is written.
+template <int D, bool DIFF = false>
 __global__ void __launch_bounds__(kMergeWarps * 32)
 decode_merge_kernel(const DecodeArgs a, int group, int wpr_log2) {
+  constexpr int kMaps = DIFF ? 2 : 1;
   constexpr int EPW = D / 32;
   constexpr int W = kMergeWarps;
   __shared__ float s_acc[W][D];
@@ -1301,7 +1438,8 @@ decode_merge_kernel(const DecodeArgs a, int group, int wpr_log2) {
   const int lane = threadIdx.x & 31;
   const int wpr = 1 << wpr_log2;
   const int sub = warp & (wpr - 1);
-  const int row = blockIdx.x * (W >> wpr_log2) + (warp >> wpr_log2);
+  const int vrow = blockIdx.x * (W >> wpr_log2) + (warp >> wpr_log2);
+  const int row = vrow / kMaps;
   // What this row needs (uniform over its warps; no early exit before the block barrier):
   // nothing (written by the split kernel, or past the last row), a zero row, or a merge of
   // np partials.  The partition follows from the lengths (inputs the split kernel does not
@@ -1332,7 +1470,7 @@ decode_merge_kernel(const DecodeArgs a, int group, int wpr_log2) {
     slot0 = 2 * r0 + (range_start(part, rid0) < seg ? 1 : 0);
   };
   auto entry = [&](int i) -> size_t {
-    return (size_t)(i == 0 ? slot0 : 2 * (r0 + i)) * group + head;
+    return ((size_t)(i == 0 ? slot0 : 2 * (r0 + i)) * group + head) * kMaps + (DIFF ? vrow & 1 : 0);
   };
   if (a.B <= kMergeScanMaxBatch) {
     int before = 0, total = 0, nb = 0;  // units of the sequences before b, of all, of b
@@ -1431,20 +1569,58 @@ decode_merge_kernel(const DecodeArgs a, int group, int wpr_log2) {
 #pragma unroll
     for (int e = 0; e < EPW; ++e) s_acc[warp][lane * EPW + e] = acc[e];
     __syncthreads();
-    if (sub != 0) return;
+    if (!DIFF && sub != 0) return;
     float Mg = -INFINITY;
-    for (int w = 0; w < wpr; ++w) Mg = fmaxf(Mg, s_ml[warp + w].x);
+    const int lead = warp & ~(wpr - 1);  // (DIFF: every warp of a row goes on)
+    for (int w = 0; w < wpr; ++w) Mg = fmaxf(Mg, s_ml[lead + w].x);
     const float mref = (Mg == -INFINITY) ? 0.f : Mg;
     m_ref = mref;
     L = 0.f;
 #pragma unroll
     for (int e = 0; e < EPW; ++e) acc[e] = 0.f;
     for (int w = 0; w < wpr; ++w) {
-      const float f = exp2f(s_ml[warp + w].x - mref);  // 0 for a warp without partials
-      L += f * s_ml[warp + w].y;
+      const float f = exp2f(s_ml[lead + w].x - mref);  // 0 for a warp without partials
+      L += f * s_ml[lead + w].y;
 #pragma unroll
-      for (int e = 0; e < EPW; ++e) acc[e] += f * s_acc[warp + w][lane * EPW + e];
+      for (int e = 0; e < EPW; ++e) acc[e] += f * s_acc[lead + w][lane * EPW + e];
     }
+  }
+  if constexpr (DIFF) {
+    // the second map's row to its head's first map, through shared memory
+    const bool lead = sub == 0;
+    const float inv = L > 0.f ? 1.f / L : 0.f;
+    __syncthreads();
+    if (lead && (vrow & 1)) {
+#pragma unroll
+      for (int e = 0; e < EPW; ++e) s_acc[warp][lane * EPW + e] = acc[e] * inv;
+    }
+    __syncthreads();
+    if (!lead || (np == 0 && !zero_row)) return;
+    if (a.lse != nullptr && lane == 0) a.lse[vrow] = L > 0.f ? m_ref + log2f(L) : -INFINITY;  // scores mode: base 2
+    if (vrow & 1) return;
+    const float lam = __ldg(a.lambdas + (size_t)b * a.lambda_stride + (row - b * a.Hq));
+    float y[EPW], ss = 0.f;
+#pragma unroll
+    for (int e = 0; e < EPW; ++e) {
+      y[e] = acc[e] * inv - lam * s_acc[warp + wpr][lane * EPW + e];
+      ss = fmaf(y[e], y[e], ss);
+    }
+    if (zero_row) {  // (no key, whatever the factor)
+#pragma unroll
+      for (int e = 0; e < EPW; ++e) y[e] = 0.f;
+      ss = 0.f;
+    }
+    if (a.norm_weight != nullptr) {
+#pragma unroll
+      for (int s = 16; s > 0; s >>= 1) ss += __shfl_xor_sync(kFullMask, ss, s);
+      const float f = rsqrtf(ss * (1.f / D) + a.norm_eps);
+#pragma unroll
+      for (int e = 0; e < EPW; ++e) y[e] *= f * __ldg(a.norm_weight + lane * EPW + e);
+    }
+    __nv_bfloat16* dst = a.out + (size_t)row * D + lane * EPW;
+#pragma unroll
+    for (int e = 0; e < EPW; e += 2) *reinterpret_cast<uint32_t*>(dst + e) = pack_bf16x2(y[e], y[e + 1]);
+    return;
   }
   if (np == 0 && !zero_row) return;
   if (a.lse != nullptr && lane == 0)  // scores mode: the row's natural log-sum-exp
@@ -1514,13 +1690,50 @@ __global__ void __launch_bounds__(kScoreThreads) decode_score_kernel(const Decod
   }
 }
 
+// The score step of differential attention: a key's weight in a head is a_1 - lambda a_2, a_m its softmax
+// probability in map m, and
+//   scores_out[b, g, t] = scores[b, g, t] + sum_i |a_1 - lambda a_2|   over the query heads i of the kv head
+// for the t that the query sees; the other t < L are copied.  A CTA covers 256 keys of one (b, g), a thread one (the
+// logits of its 2 G rows are G pairs of independent loads).
+__global__ void __launch_bounds__(kScoreThreads) decode_diff_score_kernel(const DecodeArgs a, int group, int tiles) {
+  const int seg = blockIdx.x / tiles;  // b * Hkv + g
+  const int tile = blockIdx.x - seg * tiles;
+  const int b = seg / a.Hkv;
+  grid_dependency_wait();  // the logits and log-sum-exps of the decode
+  grid_launch_dependents();
+  const RuleUnits u = rule_units(a, b);  // (a bad length, reported by the split kernel, counts as 0)
+  const int t = tile * kScoreThreads + (int)threadIdx.x;
+  if (t >= u.s.len || t >= a.score_stride) return;
+  const size_t at = (size_t)seg * a.score_stride + t;
+  float sum = 0.f;
+  if (t >= u.s.lo || t < u.pre) {
+    const size_t row0 = (size_t)b * a.Hq + (size_t)(seg - b * a.Hkv) * group;
+    const float* lambdas = a.lambdas + (size_t)b * a.lambda_stride + (size_t)(seg - b * a.Hkv) * group;
+#pragma unroll 4
+    for (int i = 0; i < group; ++i) {
+      const float* src = a.logits + (row0 + i) * 2 * a.score_stride + t;
+      const float lse1 = a.lse[(row0 + i) * 2], lse2 = a.lse[(row0 + i) * 2 + 1];
+      const float w1 = lse1 == -INFINITY ? 0.f : exp2f(src[0] - lse1);
+      const float w2 = lse2 == -INFINITY ? 0.f : exp2f(src[a.score_stride] - lse2);
+      sum += fabsf(w1 - lambdas[i] * w2);
+    }
+  }
+  a.scores_out[at] = a.scores[at] + sum;
+}
+
 }  // namespace
 
 namespace {
 
 template <int D>
-DecodeKernel kernels_of(int group, bool sparse, bool scores, bool q8, bool f8, bool rules) {
+DecodeKernel kernels_of(int group, bool sparse, bool scores, bool q8, bool f8, bool rules, bool diff) {
   const void* split;
+  if (diff) {
+    split = scores ? (const void*)decode_split_kernel<D, false, true, false, false, true, true>
+                   : (const void*)decode_split_kernel<D, false, false, false, false, true, true>;
+    return DecodeKernel{split, (const void*)decode_merge_kernel<D, true>,
+                        scores ? (const void*)decode_diff_score_kernel : nullptr, D, group, sparse, scores, q8};
+  }
   if (f8)
     split = rules ? (const void*)decode_split_kernel<D, false, false, true, true, true>
                   : (const void*)decode_split_kernel<D, false, false, true, true, false>;
@@ -1540,11 +1753,12 @@ DecodeKernel kernels_of(int group, bool sparse, bool scores, bool q8, bool f8, b
 
 }  // namespace
 
-DecodeKernel decode_kernel(int head_dim, int group, bool sparse, bool scores, bool q8, bool f8, bool rules) {
+DecodeKernel decode_kernel(int head_dim, int group, bool sparse, bool scores, bool q8, bool f8, bool rules, bool diff) {
   const DecodeKernel none{nullptr, nullptr, nullptr, head_dim, group, sparse, scores, q8};
-  if (group < 1 || group > kMaxGroup || (sparse && scores) || ((f8 || rules) && (sparse || scores))) return none;
-  if (head_dim == 128) return kernels_of<128>(group, sparse, scores, q8, f8, rules);
-  if (head_dim == 64) return kernels_of<64>(group, sparse, scores, q8, f8, rules);
+  if (group < 1 || group > kMaxGroup || (sparse && scores) || ((f8 || rules) && (sparse || (scores && !diff)))) return none;
+  if (diff && (!rules || q8)) return none;
+  if (head_dim == 128) return kernels_of<128>(group, sparse, scores, q8, f8, rules, diff);
+  if (head_dim == 64) return kernels_of<64>(group, sparse, scores, q8, f8, rules, diff);
   return none;
 }
 
@@ -1565,12 +1779,18 @@ cudaError_t launch_decode(const DecodeKernel& k, const DecodeArgs& a, int grid, 
   int group = k.group;
   int wpr_log2 = merge_wpr_log2;
   void* merge_params[] = {&args, &group, &wpr_log2};
-  const long long rows = (long long)a.B * a.Hq;
+  const long long rows = (long long)a.B * a.Hq * (a.lambdas != nullptr ? 2 : 1);  // (a differential head's two maps)
   const int rows_per_cta = kMergeWarps >> merge_wpr_log2;
   const long long mgrid = (rows + rows_per_cta - 1) / rows_per_cta;
   if (mgrid == 0) return cudaSuccess;
   e = launch_pdl(k.merge, dim3((unsigned)mgrid), dim3(kMergeWarps * 32), 0, stream, merge_params);
   if (e != cudaSuccess || !k.scores) return e;
+  if (a.lambdas != nullptr) {  // all keys of the longest sequence
+    const long long span = std::min((long long)a.MB * 16, (long long)a.score_stride);
+    int tiles = (int)std::max(1ll, (span + kScoreThreads - 1) / kScoreThreads);
+    void* params[] = {&args, &group, &tiles};
+    return launch_pdl(k.score, dim3((unsigned)((long long)a.B * a.Hkv * tiles)), dim3(kScoreThreads), 0, stream, params);
+  }
   // score step: tiles of 256 keys over the longest attended range any sequence can have
   long long span = (long long)a.MB * 16;
   if (a.window > 0 && a.window < span) span = a.window;

@@ -8,6 +8,7 @@
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 
+#include "pkv_diff.h"
 #include "pkv_step.h"
 
 namespace pkv {
@@ -52,6 +53,11 @@ struct DecodeArgs {
   const int32_t* doc_starts;     // score rules: [B] or nullptr
   const int32_t* prefix_lens;    // score rules: [B] or nullptr
   float cap_log2, cap_in;        // score rules: cap * log2(e) (0: no cap) and 2 / cap
+  const float* lambdas;          // differential attention: [Hq] or [B, Hq] factors of the second map, else nullptr
+  int lambda_stride;             //   0 or Hq
+  const float* norm_weight;      //   [D] or nullptr
+  float norm_eps;
+  float* scores_out;             //   scores mode: [B, Hkv, score_stride] (logits and lse then have both maps of a head)
   int rules;                     // 1: score rules (the merge kernel derives the same units)
   int B, Hq, Hkv, NB, MB, max_kept, window;
   int workers;                   // worker warps of the split grid
@@ -195,7 +201,7 @@ struct DecodeKernel {
 // Returns a struct with split == nullptr when the combination is unsupported (scores mode
 // and INT8 pools exist for dense decode only, and not together).
 DecodeKernel decode_kernel(int head_dim, int group, bool sparse, bool scores = false, bool q8 = false,
-                           bool f8 = false, bool rules = false);
+                           bool f8 = false, bool rules = false, bool diff = false);
 size_t decode_smem_bytes(int head_dim, bool sparse, int batch, bool rules = false);
 // merge_wpr_log2: log2 of the merge warps per output row (0..3).
 cudaError_t launch_decode(const DecodeKernel& k, const DecodeArgs& a, int grid, size_t smem,
@@ -381,6 +387,15 @@ struct ScoreOutputs {
   int stride;
 };
 
+// Differential attention of a dense bf16 decode (with rules); scores: emitted too, lse and logits in the workspace.
+struct DiffDecode {
+  const struct pkv_diff_params* params;
+  const float* scores = nullptr;
+  float* scores_out = nullptr;
+  int stride = 0;
+};
+int check_diff(const struct pkv_diff_params* p);
+
 // INT8 pools of a dense decode (pkv_paged_decode_attention_q8); nullptr: bf16 pools.
 // f8: FP8 pools with a scale per block and kv head instead.
 struct Q8Scales {
@@ -395,6 +410,6 @@ int decode_common(void* out, const void* q, const void* k_cache, const void* v_c
                   void* workspace, size_t workspace_bytes, const struct pkv_dims* dims, int32_t* err,
                   void* stream, bool sparse, const void* k_new = nullptr, const void* v_new = nullptr,
                   const ScoreOutputs* score_out = nullptr, const Q8Scales* q8 = nullptr,
-                  uint32_t flags = 0, const struct pkv_score_rules* rules = nullptr);
+                  uint32_t flags = 0, const struct pkv_score_rules* rules = nullptr, const DiffDecode* diff = nullptr);
 
 }  // namespace pkv
