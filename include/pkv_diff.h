@@ -74,6 +74,23 @@ int pkv_paged_diff_decode_attention_scores(void* out, const float* scores, float
                                            size_t workspace_bytes, const pkv_dims* dims, uint32_t flags,
                                            int32_t* error_word, void* stream);
 
+/*
+ * pkv_diff_prefill_workspace_bytes -- bytes of device workspace for pkv_paged_diff_prefill_attention, as
+ * pkv_prefill_workspace_bytes (no preparation).  Returns 0 if the arguments are invalid.
+ */
+size_t pkv_diff_prefill_workspace_bytes(const pkv_dims* dims, int32_t total_tokens);
+
+/*
+ * pkv_paged_diff_prefill_attention -- many query tokens a sequence, causal: prompts, chunks, mixed steps.
+ *   params          : lambdas [Hq] or [total_tokens, Hq] (the packed rows).
+ *   other arguments, supported sizes, errors and the weights' precision : as pkv_paged_prefill_attention.
+ */
+int pkv_paged_diff_prefill_attention(void* out, const void* q, const void* k_cache, const void* v_cache,
+                                     const int32_t* block_tables, const int32_t* context_lens,
+                                     const int32_t* query_starts, int32_t total_tokens, float scale,
+                                     const pkv_diff_params* params, const pkv_score_rules* rules, void* workspace,
+                                     size_t workspace_bytes, const pkv_dims* dims, int32_t* error_word, void* stream);
+
 #ifdef __cplusplus
 }
 #endif

@@ -14,7 +14,8 @@ import ctypes
 import torch
 
 from ._lib import PkvDims, PkvError, check, header_constants, header_functions, load
-from .diff import diff_decode_workspace_bytes, paged_diff_decode_attention, paged_diff_decode_attention_scores
+from .diff import (diff_decode_workspace_bytes, diff_prefill_workspace_bytes, paged_diff_decode_attention,
+                   paged_diff_decode_attention_scores, paged_diff_prefill_attention)
 from .evict import evict_workspace_bytes, kv_evict, kv_evict_q8
 from .step import (kv_append_f8, kv_step_tables, paged_decode_attention_f8, paged_decode_attention_rules,
                    paged_prefill_attention, prefill_workspace_bytes)
@@ -33,6 +34,7 @@ __all__ = [
     "kv_step_tables", "kv_append_f8", "paged_decode_attention_rules", "paged_decode_attention_f8",
     "paged_prefill_attention", "prefill_workspace_bytes",
     "paged_diff_decode_attention", "paged_diff_decode_attention_scores", "diff_decode_workspace_bytes",
+    "paged_diff_prefill_attention", "diff_prefill_workspace_bytes",
     "kv_evict", "kv_evict_q8", "evict_workspace_bytes",
 ]
 

@@ -145,6 +145,8 @@ def load():
             "pkv_paged_diff_decode_attention": (I32, [P, P, P, P, P, P, F32, DP, R, P, SZ, D, U32, P, P]),
             "pkv_paged_diff_decode_attention_scores": (I32, [P, P, P, I32, P, P, P, P, P, F32, DP, R, P, SZ, D, U32, P,
                                                              P]),
+            "pkv_diff_prefill_workspace_bytes": (SZ, [D, I32]),
+            "pkv_paged_diff_prefill_attention": (I32, [P, P, P, P, P, P, P, I32, F32, DP, R, P, SZ, D, P, P]),
             "pkv_evict_workspace_bytes": (SZ, [D, ER]),
             "pkv_kv_evict": (I32, [P, P, P, P, P, ES, ER, P, P, P, P, SZ, D, P, P]),
             "pkv_kv_evict_q8": (I32, [P, P, P, P, P, P, P, ES, ER, P, P, P, P, SZ, D, P, P]),

@@ -804,18 +804,18 @@ decode_split_kernel(const __grid_constant__ DecodeArgs a) {
         }
         const float f1 = l[0] > 0.f ? 1.f / l[0] : 0.f;
         const float f2 = live && l[1] > 0.f ? __ldg(a.lambdas + (size_t)seg_b * a.lambda_stride + seg_g * G + head) / l[1] : 0.f;
-        float ss = 0.f;
+        SquareSum sq;
 #pragma unroll
         for (int mt = 0; mt < KS; ++mt) {
           o[mt][hh] = o[mt][hh] * f1 - od[mt][hh] * f2;
           o[mt][2 + hh] = o[mt][2 + hh] * f1 - od[mt][2 + hh] * f2;
-          ss = fmaf(o[mt][hh], o[mt][hh], fmaf(o[mt][2 + hh], o[mt][2 + hh], ss));
+          sq.add(o[mt][hh]);
+          sq.add(o[mt][2 + hh]);
         }
         float f = 1.f;
         if (a.norm_weight != nullptr) {
-#pragma unroll
-          for (int s = 4; s <= 16; s <<= 1) ss += __shfl_xor_sync(kFullMask, ss, s);
-          f = rsqrtf(ss * (1.f / D) + a.norm_eps);
+          sq.join(32, 4);
+          f = sq.factor(D, a.norm_eps);
         }
         if (!live) continue;
         __nv_bfloat16* dst = a.out + row * D + gq;
@@ -1599,21 +1599,16 @@ decode_merge_kernel(const DecodeArgs a, int group, int wpr_log2) {
     if (a.lse != nullptr && lane == 0) a.lse[vrow] = L > 0.f ? m_ref + log2f(L) : -INFINITY;  // scores mode: base 2
     if (vrow & 1) return;
     const float lam = __ldg(a.lambdas + (size_t)b * a.lambda_stride + (row - b * a.Hq));
-    float y[EPW], ss = 0.f;
+    float y[EPW];
+    SquareSum sq;
 #pragma unroll
     for (int e = 0; e < EPW; ++e) {
-      y[e] = acc[e] * inv - lam * s_acc[warp + wpr][lane * EPW + e];
-      ss = fmaf(y[e], y[e], ss);
-    }
-    if (zero_row) {  // (no key, whatever the factor)
-#pragma unroll
-      for (int e = 0; e < EPW; ++e) y[e] = 0.f;
-      ss = 0.f;
+      y[e] = zero_row ? 0.f : acc[e] * inv - lam * s_acc[warp + wpr][lane * EPW + e];  // (no key, whatever the factor)
+      sq.add(y[e]);
     }
     if (a.norm_weight != nullptr) {
-#pragma unroll
-      for (int s = 16; s > 0; s >>= 1) ss += __shfl_xor_sync(kFullMask, ss, s);
-      const float f = rsqrtf(ss * (1.f / D) + a.norm_eps);
+      sq.join(32);
+      const float f = sq.factor(D, a.norm_eps);
 #pragma unroll
       for (int e = 0; e < EPW; ++e) y[e] *= f * __ldg(a.norm_weight + lane * EPW + e);
     }

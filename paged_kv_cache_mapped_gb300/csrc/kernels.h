@@ -332,8 +332,12 @@ struct PrefillAttnArgs {
   float2* part_ml;               // partial rows: (running max in base 2, running sum)
   float* part_o;                 // partial rows, unnormalised [.., D]
   unsigned long long timeout_ns; // bound of every mbarrier wait
+  const float* lambdas;          // differential attention, as DecodeArgs: [Hq] or [T, Hq], else nullptr
+  int lambda_stride;
+  const float* norm_weight;
+  float norm_eps;
 };
-size_t prefill_attention_workspace(int B, int T, int Hq, int G, int D);
+size_t prefill_attention_workspace(int B, int T, int Hq, int G, int D, int maps);
 cudaError_t prefill_attention_device_setup();
 cudaError_t launch_prefill_attention(const PrefillAttnArgs& a, void* workspace, int head_dim, cudaStream_t stream);
 

@@ -83,10 +83,14 @@ constexpr float kSlack = 8.0f;       // the running maximum moves only when exce
 constexpr int kTwoTermTiles = 4;     // rows over at most this many key tiles take P as two bf16 terms (above)
 constexpr int kMinChunk = 4;         // key tiles of a share at least where items outnumber the CTAs
 
-template <int D, int NT>
+// DIFF: differential attention.  The two row tiles of an item are the two maps of the same 128 rows, from the
+// halves of one Q tile and of each K tile.
+template <int D, int NT, bool DIFF = false>
 struct Geo {
+  static_assert(!DIFF || NT == 2, "a row tile for each map");
   static constexpr int kHalves = D / 64;
   static constexpr int kTile = kHalves * kHalf;  // bytes of a Q, K or V tile
+  static constexpr int kQTiles = DIFF ? 1 : NT;
   static constexpr int kSlots = NT == 2 ? (D == 128 ? 4 : 8) : (D == 128 ? 2 : 5);
   static constexpr int kSoftmaxWarps = NT * 4;  // a row a thread
   // and a producer, two issuers (one for each row tile, or for each product of the one), the ticket taker
@@ -100,7 +104,7 @@ struct Geo {
   static constexpr int kSoftmaxRegs = NT == 2 ? 216 : 184, kOtherRegs = 72;
   static_assert(kSoftmaxWarps * 32 * kSoftmaxRegs + 128 * kOtherRegs <= kThreads * kLaunchRegs, "register split");
   static constexpr uint32_t kTmemCols = NT * (2 * kStep + D) <= 256 ? 256 : 512;
-  static constexpr size_t kSmem = 1024 + (size_t)(NT + kSlots) * kTile;
+  static constexpr size_t kSmem = 1024 + (size_t)(kQTiles + kSlots) * kTile;
 };
 
 // ------------------------------------------------------------------------------------ the plan
@@ -495,6 +499,139 @@ __device__ __noinline__ void exact_row(const PrefillAttnArgs& a, const Row& w, l
   if (part >= 0 && lane == 0) a.part_ml[part] = make_float2(m, l);
 }
 
+// exact_row of both maps of a differential row: writes the output row, or partial rows 2 part and 2 part + 1.
+template <int D>
+__device__ __noinline__ void exact_row_diff(const PrefillAttnArgs& a, const Row& w, long long part) {
+  constexpr int E = D / 32, H = D / 64;
+  const int lane = threadIdx.x & 31, sub = lane & 7;
+  const int key = (lane >> 3) + 4 * sub;  // of the 32: lanes 8 g .. 8 g + 7 read the rows of keys g + 4 n
+  float o[2][E], m[2] = {-INFINITY, -INFINITY}, l[2] = {0.f, 0.f};
+#pragma unroll
+  for (int e = 0; e < E; ++e) o[0][e] = o[1][e] = 0.f;
+  uint32_t q[H][4];
+#pragma unroll
+  for (int h = 0; h < H; ++h) {
+    const uint4 u = *reinterpret_cast<const uint4*>(a.q + ((size_t)w.r * a.Hq + w.h) * D + h * 64 + sub * 8);
+    q[h][0] = u.x; q[h][1] = u.y; q[h][2] = u.z; q[h][3] = u.w;
+  }
+  const float slope = a.slopes != nullptr ? a.slopes[w.h] * kLog2e : 0.f;
+  for (int en = w.e0; en < w.e1; en += 2) {
+    const int e = en + (key >> 4), c = key & 15;
+    const int blk = e < w.pre_units ? e : e + w.shift;
+    int phys = e < w.e1 ? a.block_tables[(size_t)w.b * a.MB + blk] : -1;
+    if (phys >= a.NB) phys = -1;
+    const bool see = phys >= 0 && ((seen_keys(w.i, w.lo, w.pre, blk) >> c) & 1u);
+    const uint32_t seen = __ballot_sync(kFullMask, see);
+    const long long row = ((long long)phys * a.Hkv + w.g) * 16 + c;
+    float x[2] = {0.f, 0.f};
+#pragma unroll 1
+    for (int n = 0; n < 8; ++n) {
+      const int from = (lane & 24) | n;
+      const long long at = __shfl_sync(kFullMask, row, from);
+      float y[H];
+#pragma unroll
+      for (int h = 0; h < H; ++h) {
+        const uint4 t = ((seen >> from) & 1u) ? *reinterpret_cast<const uint4*>(a.k_cache + at * D + h * 64 + sub * 8)
+                                              : make_uint4(0u, 0u, 0u, 0u);
+        const uint32_t ts[4] = {t.x, t.y, t.z, t.w};
+        y[h] = 0.f;
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+          y[h] = fmaf(bf16_lo_to_f32(q[h][k]), bf16_lo_to_f32(ts[k]), y[h]);
+          y[h] = fmaf(bf16_hi_to_f32(q[h][k]), bf16_hi_to_f32(ts[k]), y[h]);
+        }
+        y[h] += __shfl_xor_sync(kFullMask, y[h], 1);
+        y[h] += __shfl_xor_sync(kFullMask, y[h], 2);
+      }
+      // a map's half of the row is 64 elements, eight lanes, or 32, four of them
+      float y0, y1;
+      if constexpr (H == 2) {
+        y0 = y[0] + __shfl_xor_sync(kFullMask, y[0], 4);
+        y1 = y[1] + __shfl_xor_sync(kFullMask, y[1], 4);
+      } else {
+        const float other = __shfl_xor_sync(kFullMask, y[0], 4);
+        y0 = sub < 4 ? y[0] : other;
+        y1 = sub < 4 ? other : y[0];
+      }
+      if (n == sub) {
+        x[0] = y0;
+        x[1] = y1;
+      }
+    }
+    float p[2], keep[2];
+    bool nan = false;
+#pragma unroll
+    for (int k = 0; k < 2; ++k) {
+      float z = x[k] * a.scale_log2;
+      if (a.cap_log2 > 0.f) z = cap_logit(z, a.cap_log2, a.cap_in);
+      z -= slope * fabsf((float)(w.i - (blk * 16 + c)));
+      if (!see) z = -INFINITY;
+      float top = z;
+#pragma unroll
+      for (int s = 16; s > 0; s >>= 1) top = fmaxf(top, __shfl_xor_sync(kFullMask, top, s));
+      top = fmaxf(m[k], top);
+      const float ref = top == -INFINITY ? 0.f : top;
+      keep[k] = exp2f(m[k] - ref);
+      p[k] = exp2f(z - ref);
+      m[k] = top;
+      l[k] = l[k] * keep[k] + p[k];
+      nan |= l[k] != l[k];
+#pragma unroll
+      for (int j = 0; j < E; ++j) o[k][j] *= keep[k];
+    }
+    if (__any_sync(kFullMask, nan)) {
+      l[0] = l[1] = __int_as_float(0x7fffffff);
+      break;
+    }
+#pragma unroll 4
+    for (int s = 0; s < 32; ++s) {
+      const long long at = __shfl_sync(kFullMask, row, s);
+      const float p0 = __shfl_sync(kFullMask, p[0], s), p1 = __shfl_sync(kFullMask, p[1], s);
+      if (!((seen >> s) & 1u)) continue;
+      const uint32_t* src = reinterpret_cast<const uint32_t*>(a.v_cache + at * D + lane * E);
+#pragma unroll
+      for (int j = 0; j < E / 2; ++j) {
+        const uint32_t u = src[j];
+        o[0][2 * j] = fmaf(p0, bf16_lo_to_f32(u), o[0][2 * j]);
+        o[0][2 * j + 1] = fmaf(p0, bf16_hi_to_f32(u), o[0][2 * j + 1]);
+        o[1][2 * j] = fmaf(p1, bf16_lo_to_f32(u), o[1][2 * j]);
+        o[1][2 * j + 1] = fmaf(p1, bf16_hi_to_f32(u), o[1][2 * j + 1]);
+      }
+    }
+  }
+#pragma unroll
+  for (int k = 0; k < 2; ++k)
+#pragma unroll
+    for (int s = 16; s > 0; s >>= 1) l[k] += __shfl_xor_sync(kFullMask, l[k], s);
+  if (part >= 0) {
+#pragma unroll
+    for (int k = 0; k < 2; ++k) {
+#pragma unroll
+      for (int e = 0; e < E; ++e) a.part_o[(2 * part + k) * D + lane * E + e] = o[k][e];
+      if (lane == 0) a.part_ml[2 * part + k] = make_float2(m[k], l[k]);
+    }
+    return;
+  }
+  const float lam = a.lambdas[(size_t)w.r * a.lambda_stride + w.h];
+  const float f0 = l[0] > 0.f ? 1.f / l[0] : (l[0] == l[0] ? 0.f : l[0]);
+  const float f1 = l[1] > 0.f ? lam / l[1] : (l[1] == l[1] ? 0.f : l[1]);
+  float y[E];
+  SquareSum sq;
+#pragma unroll
+  for (int e = 0; e < E; ++e) {
+    y[e] = o[0][e] * f0 - o[1][e] * f1;
+    sq.add(y[e]);
+  }
+  sq.join(32);
+  const float f = a.norm_weight != nullptr ? sq.factor(D, a.norm_eps) : 1.f;
+#pragma unroll
+  for (int e = 0; e < E; ++e) {
+    const int c = lane * E + e;
+    const float g = a.norm_weight != nullptr ? f * a.norm_weight[c] : 1.f;
+    a.out[((size_t)w.r * a.Hq + w.h) * D + c] = __float2bfloat16_rn(y[e] * g);
+  }
+}
+
 // ------------------------------------------------------------------------------- the attention
 
 // One work item for one kv head, and the key list of its rows: the blocks of the prefix, then those of
@@ -518,7 +655,7 @@ struct Steps {
 };
 
 // p, q: the record of item it.
-__device__ __forceinline__ Item item_of(const PrefillAttnArgs& a, int it, int4 p, int4 q, int NT) {
+__device__ __forceinline__ Item item_of(const PrefillAttnArgs& a, int it, int4 p, int4 q, int NT, bool diff) {
   Item w;
   w.b = p.x;
   w.g = it % a.Hkv;
@@ -530,7 +667,7 @@ __device__ __forceinline__ Item item_of(const PrefillAttnArgs& a, int it, int4 p
   w.split = q.z & 0xffff;
   w.nsplit = q.z >> 16;
   w.part = q.w;
-  w.nx = NT == 2 && w.tokens > a.R ? 2 : 1;
+  w.nx = diff || (NT == 2 && w.tokens > a.R) ? 2 : 1;
   return w;
 }
 
@@ -556,30 +693,33 @@ __device__ __forceinline__ Steps steps_of(const PrefillAttnArgs& a, const Item& 
   return Steps{min(w.ns - 1, (e_last - e_base) >> 2), max(0, (e_first - e_base) >> 2)};
 }
 
-template <int D, int NT>
+template <int D, int NT, bool DIFF = false>
 struct Shared {
-  uint64_t q_full, kv_full[Geo<D, NT>::kSlots], kv_empty[Geo<D, NT>::kSlots];
+  uint64_t q_full, kv_full[Geo<D, NT, DIFF>::kSlots], kv_empty[Geo<D, NT, DIFF>::kSlots];
   uint64_t s_full[NT][2], p_full[NT][2], pv_done[NT][2];  // by buffer: S ready, P ready, P V added
   uint64_t drained[2];  // after a timeout: an issuer's MMAs have ended
   uint32_t tmem;
   int4 record[2];                       // of the next item
   int lo_least[NT], lo_most[NT], abort, next;  // interval starts of the row tiles' rows
+  float sum[DIFF ? 2 : 1][DIFF ? 128 : 1];     // DIFF: each map's sum of a row's weights
+  float2 squares[DIFF ? 2 : 1][DIFF ? 128 : 1];  // and half of each row's sum of squares
 };
 
 // Loads the item's Q tiles and its K and V tiles through the ring (one warp).  n_kv counts K and V tiles
 // since the kernel's start, n_q loaded items.
-template <int D, int NT>
-__device__ __forceinline__ void produce(const PrefillAttnArgs& a, Shared<D, NT>& sh, const Item& w, unsigned char* sq,
+template <int D, int NT, bool DIFF>
+__device__ __forceinline__ void produce(const PrefillAttnArgs& a, Shared<D, NT, DIFF>& sh, const Item& w, unsigned char* sq,
                                         uint32_t& n_kv, uint32_t n_q) {
-  using GE = Geo<D, NT>;
+  using GE = Geo<D, NT, DIFF>;
   constexpr int NS = GE::kSlots, H = GE::kHalves;
   const int lane = threadIdx.x & 31;
-  unsigned char* skv = sq + NT * GE::kTile;
+  unsigned char* skv = sq + GE::kQTiles * GE::kTile;
+  const int nq = DIFF ? 1 : w.nx;
   const uint64_t pol = l2_policy_evict_last();  // K and V tiles are read by every row tile of the sequence
   if (lane == 0) {
     const uint64_t pol_q = l2_policy_evict_first();
-    mbar_arrive_expect_tx(&sh.q_full, (uint32_t)(w.nx * H * 128 * a.G * a.R));
-    for (int y = 0; y < w.nx; ++y)
+    mbar_arrive_expect_tx(&sh.q_full, (uint32_t)(nq * H * 128 * a.G * a.R));
+    for (int y = 0; y < nq; ++y)
 #pragma unroll
       for (int h = 0; h < H; ++h)
         tma_load_3d(sq + y * GE::kTile + h * kHalf, &a.tmap_q, h * 64, w.g * a.G, w.row0 + y * a.R, &sh.q_full, pol_q);
@@ -654,12 +794,12 @@ __device__ __forceinline__ void produce(const PrefillAttnArgs& a, Shared<D, NT>&
 // 0.92; one for each product of each 0.75 against 0.72, its warps taking issue slots from the softmax).  With
 // one row tile and two CTAs an SM the products have an issuer each (64 tokens on 2000 keys each: 129 -> 112 us).
 // A ring tile is free once both row tiles have read it; a row tile that does not read it only says so.
-template <int D, int NT, bool QK, bool PV>
-__device__ __forceinline__ void issue_mmas(const PrefillAttnArgs& a, Shared<D, NT>& sh, const Item& w, unsigned char* sq,
+template <int D, int NT, bool DIFF, bool QK, bool PV>
+__device__ __forceinline__ void issue_mmas(const PrefillAttnArgs& a, Shared<D, NT, DIFF>& sh, const Item& w, unsigned char* sq,
                                            uint32_t tmem_any, uint32_t leader, int y, uint32_t& n_kv, uint32_t n_q,
                                            uint32_t& n_step) {
-  using GE = Geo<D, NT>;
-  using SH = Shared<D, NT>;
+  using GE = Geo<D, NT, DIFF>;
+  using SH = Shared<D, NT, DIFF>;
   constexpr int NS = GE::kSlots;
   constexpr uint32_t id_qk = umma_idesc_bf16(128, kStep), id_pv = umma_idesc_bf16_bmn(128, D);
   auto uniform = [](uint32_t v) { return __shfl_sync(kFullMask, v, 0); };
@@ -678,7 +818,7 @@ __device__ __forceinline__ void issue_mmas(const PrefillAttnArgs& a, Shared<D, N
   n_kv = kv_base + 2 * w.nt;
   bool ok = true;
   const int nt = (int)uniform((uint32_t)w.nt);
-  const Steps range = y < w.nx ? steps_of(a, w, y, sh.lo_least[y]) : Steps{-1, 0};
+  const Steps range = y < w.nx ? steps_of(a, w, DIFF ? 0 : y, sh.lo_least[y]) : Steps{-1, 0};
   const int hi = (int)uniform((uint32_t)range.hi), lo = (int)uniform((uint32_t)range.lo);
   auto pass = [&](int from, int to) {  // the loads [from, to) that this row tile does not read
     for (int i = from; i < to && ok; ++i)
@@ -695,15 +835,17 @@ __device__ __forceinline__ void issue_mmas(const PrefillAttnArgs& a, Shared<D, N
   const uint32_t step0 = uniform(n_step);
   const uint32_t s0 = uniform(tmem_any) + y * 2 * kStep, o = uniform(tmem_any) + NT * 2 * kStep + y * D;
   constexpr uint32_t kTile16 = GE::kTile / 16, kStep16 = kStep * 128 / 16;  // descriptors count 16 bytes
-  const uint32_t qa = umma_lo_k(base) + y * kTile16, k0 = umma_lo_k(base + NT * GE::kTile);
-  const uint32_t v0 = umma_lo_mn(base + NT * GE::kTile, kHalf);
+  // DIFF: map y's products are those of the y-th halves of the rows, 64 or 32 elements from element y D / 2 on
+  const uint32_t map16 = DIFF ? y * (D == 128 ? kHalf : 64) / 16 : 0u;
+  const uint32_t qa = umma_lo_k(base) + (DIFF ? map16 : y * kTile16), k0 = umma_lo_k(base + GE::kQTiles * GE::kTile) + map16;
+  const uint32_t v0 = umma_lo_mn(base + GE::kQTiles * GE::kTile, kHalf);
   auto k_tile = [&](int j) { return kv_base + 2u * (uint32_t)(nt - 1 - (j >> 1)); };
   // S of step j; its tile's K is awaited before the tile's first step and freed after the last
   auto wait_k = [&](int j) { return (j != hi && !(j & 1)) || wait_kv(k_tile(j)); };
   auto qk = [&](int j) {
     const uint32_t buf = (step0 + (uint32_t)(hi - j)) & 1u, kb = k0 + (k_tile(j) % NS) * kTile16 + (j & 1) * kStep16;
 #pragma unroll
-    for (int k = 0; k < D / 16; ++k) {
+    for (int k = 0; k < (DIFF ? D / 32 : D / 16); ++k) {
       const uint32_t off = (uint32_t)((k >> 2) * kHalf + (k & 3) * 32) / 16;
       umma_bf16_lo(leader, s0 + buf * kStep, qa + off, kb + off, id_qk, k > 0);
     }
@@ -945,18 +1087,155 @@ __device__ __forceinline__ float step_weights(const float (&v)[kStep], uint32_t 
   return t.x + t.y;
 }
 
+// The end of a differential item, by the 256 softmax threads: thread (x, r) has map x's maximum m and sum l of row r, and
+// both maps' O rows are in its lanes of tensor memory.  It takes half of the row's columns of both; or, of an item whose
+// keys are shared out, its own map's partial row.  ok: its waits ended.  Every thread passes the same barriers.
+template <int D>
+__device__ __forceinline__ void diff_rows(const PrefillAttnArgs& a, Shared<D, 2, true>& sh, const Item& w, uint32_t to, int x,
+                                          int r, bool valid, bool ok, float m, float l, int i, int lo, int prow, int h) {
+  constexpr int N = D / 2;
+  const int lane = threadIdx.x & 31;
+  const bool split = w.nsplit > 1, two = w.nt_all <= kTwoTermTiles;
+  const int e_base = w.ts * kTileBlocks;
+  const Steps range = steps_of(a, w, 0, sh.lo_least[x]);
+  const bool some = range.hi >= range.lo;
+  const long long part =
+      split ? (long long)w.part + ((long long)w.split * w.tokens + (prow - w.row0)) * a.Hq + h : 0;
+  sh.sum[x][r] = l;
+  tc_fence_before();
+  if (named_barrier_or(1, 256, !ok)) return;
+  tc_fence_after();
+  const float l0 = sh.sum[0][r], l1 = sh.sum[1][r];
+  bool bad = !(l <= 3.4028234e38f);
+  SquareSum sq;
+  const float lam = valid ? __ldg(a.lambdas + (size_t)prow * a.lambda_stride + h) : 0.f;
+  const float f0 = l0 > 0.f ? 1.f / l0 : 0.f, f1 = l1 > 0.f ? lam / l1 : 0.f;
+  // 16 columns of this thread's half of the difference; read twice, which costs less than the registers to keep them
+  auto columns = [&](int c, float (&y)[16]) {
+    float o[16];
+    __syncwarp();
+    if (some) {
+      tmem_ld_x16(to + x * N + 16 * c, y);
+      tmem_ld_x16(to + D + x * N + 16 * c, o);
+      tmem_wait_ld();
+    }
+#pragma unroll
+    for (int k = 0; k < 16; ++k) y[k] = some ? y[k] * f0 - o[k] * f1 : 0.f;
+  };
+  if (split) {
+#pragma unroll
+    for (int c = 0; c < D / 16; ++c) {
+      float o[16];
+      __syncwarp();
+      if (some) {
+        tmem_ld_x16(to + x * D + 16 * c, o);
+        tmem_wait_ld();
+      }
+#pragma unroll
+      for (int k = 0; k < 16; ++k) {
+        o[k] = some ? o[k] : 0.f;
+        bad |= !(fabsf(o[k]) <= 3.4028234e38f);
+      }
+      if (valid) {
+        float4* dst = reinterpret_cast<float4*>(a.part_o + (2 * part + x) * D + 16 * c);
+#pragma unroll
+        for (int k = 0; k < 4; ++k) dst[k] = make_float4(o[4 * k], o[4 * k + 1], o[4 * k + 2], o[4 * k + 3]);
+      }
+    }
+    if (valid) a.part_ml[2 * part + x] = make_float2(m, l);
+  } else {
+#pragma unroll
+    for (int c = 0; c < N / 16; ++c) {
+      float y[16];
+      columns(c, y);
+#pragma unroll
+      for (int k = 0; k < 16; ++k) {
+        bad |= !(fabsf(y[k]) <= 3.4028234e38f);
+        sq.add(y[k]);
+      }
+    }
+  }
+  // a row that is not finite says so in its half of the squares
+  sh.squares[x][r] = make_float2(bad ? __int_as_float(0x7fffffff) : sq.s, sq.b);
+  const bool any = named_barrier_or(1, 256, valid && bad);
+  const float2 s0 = sh.squares[0][r], s1 = sh.squares[1][r];
+  if (!split) {
+    sq.s = s0.x + s1.x;
+    sq.b = s0.y + s1.y;
+    const bool norm = a.norm_weight != nullptr;
+    const float f = norm ? sq.factor(D, a.norm_eps) : 1.f;
+    uint4* dst = reinterpret_cast<uint4*>(a.out + ((size_t)prow * a.Hq + h) * D + x * N);
+#pragma unroll
+    for (int c = 0; c < N / 16; ++c) {
+      float y[16];
+      columns(c, y);
+      if (!valid) continue;
+      if (norm) {
+#pragma unroll
+        for (int k = 0; k < 16; ++k) y[k] *= f * __ldg(a.norm_weight + x * N + 16 * c + k);
+      }
+#pragma unroll
+      for (int k = 0; k < 2; ++k)
+        dst[2 * c + k] = make_uint4(pack_bf16x2(y[8 * k], y[8 * k + 1]), pack_bf16x2(y[8 * k + 2], y[8 * k + 3]),
+                                    pack_bf16x2(y[8 * k + 4], y[8 * k + 5]), pack_bf16x2(y[8 * k + 6], y[8 * k + 7]));
+    }
+  }
+  if (!any) return;
+  // As at the end of softmax_rows: rows that may owe it to other than a V that they see are computed again, by the
+  // first map's threads, once every store of them has been made.
+  (void)named_barrier_or(1, 256, false);
+  const bool row_bad = valid && !(s0.x == s0.x && s1.x == s1.x);
+  uint32_t again = __ballot_sync(kFullMask, row_bad);
+  if (x != 0 || again == 0u) return;
+  const int full0 = max(0, (max(w.pre_units, ((sh.lo_most[x] + 15) >> 4) - w.shift) - e_base + kStepBlocks - 1) >> 2);
+  const int full1 = (((w.pos0 + 1) >> 4) - w.shift - e_base) >> 2, full_pre = ((w.pre >> 4) - e_base) >> 2;
+  Row row;
+  row.b = w.b;
+  row.g = w.g;
+  row.pre_units = w.pre_units;
+  row.shift = w.shift;
+  row.i = i;
+  row.lo = lo;
+  row.pre = valid ? w.pre : 0;
+  int found = 0;
+  for (int full = 0; full < 2; ++full) {
+    for (int j = range.hi; j >= range.lo && !two && !(full && (found & 1)); --j) {
+      if (((j >= full0 && j < full1) || j < full_pre) != (full != 0)) continue;
+      row.e0 = e_base + j * kStepBlocks;
+      row.e1 = min(row.e0 + kStepBlocks, w.nblk);
+      found |= non_finite_v<D>(a, row, w.L);
+    }
+  }
+  const bool owes = two || !(l0 <= 3.4028234e38f) || !(l1 <= 3.4028234e38f) || found != 1;
+  again = __ballot_sync(kFullMask, row_bad && owes);
+  while (again != 0u) {
+    const int src = __ffs(again) - 1;
+    again &= again - 1;
+    row.r = __shfl_sync(kFullMask, prow, src);
+    row.h = __shfl_sync(kFullMask, h, src);
+    row.i = __shfl_sync(kFullMask, i, src);
+    row.lo = __shfl_sync(kFullMask, lo, src);
+    row.pre = w.pre;
+    row.e0 = e_base;
+    row.e1 = min((w.ts + w.nt) * kTileBlocks, w.nblk);
+    exact_row_diff<D>(a, row, split ? __shfl_sync(kFullMask, part, src) : -1);
+  }
+}
+
 // The item's softmax and output for this thread's row r of row tile x: position i (-1: none), interval start
 // lo; prow and h name the output row.
 // MODE: the rules that need each key's own logit, 1 a cap and 2 a distance bias (or a scale that is not positive),
 // 4: asked of the arguments at each step.
-template <int D, int NT, int MODE>
-__device__ __forceinline__ void softmax_rows(const PrefillAttnArgs& a, Shared<D, NT>& sh, const Item& w,
+template <int D, int NT, bool DIFF, int MODE>
+__device__ __forceinline__ void softmax_rows(const PrefillAttnArgs& a, Shared<D, NT, DIFF>& sh, const Item& w,
                                              unsigned char* sq, uint32_t tmem, int x, int r, bool valid, int i,
-                                             int lo, int prow, int h, uint32_t n_kv, uint32_t& n_step) {
-  using GE = Geo<D, NT>;
+                                             int lo, int prow, int h, uint32_t n_kv, uint32_t& n_step, float& m, float& l,
+                                             bool& ok) {
+  using GE = Geo<D, NT, DIFF>;
   constexpr int NS = GE::kSlots, H = GE::kHalves, N = kStep;
   const int lane = threadIdx.x & 31;
-  unsigned char* skv = sq + NT * GE::kTile;
+  const int xt = DIFF ? 0 : x;  // the row tile's place among the item's tokens
+  unsigned char* skv = sq + GE::kQTiles * GE::kTile;
   const bool cap = MODE == 4 ? a.cap_log2 > 0.f : (MODE & 1) != 0;
   const bool bias = MODE == 4 ? a.slopes != nullptr || !(a.scale_log2 > 0.f) : (MODE & 2) != 0;
   const float slope2 = bias && valid && a.slopes != nullptr ? __ldg(a.slopes + h) * kLog2e : 0.f;
@@ -964,12 +1243,12 @@ __device__ __forceinline__ void softmax_rows(const PrefillAttnArgs& a, Shared<D,
   const bool two = w.nt_all <= kTwoTermTiles;
   // the cap as a polynomial of S: u = S ku, the logit cap_log2 u P(u^2)
   const float ku = a.scale_log2 * a.cap_in * 0.34657359f, ku_size = fabsf(ku) < 1e3f ? fabsf(ku) : INFINITY;
-  const Steps range = steps_of(a, w, x, sh.lo_least[x]);
+  const Steps range = steps_of(a, w, xt, sh.lo_least[x]);
   // steps whose keys all rows of the row tile see: a range of the interval's part of the list, and one of the
   // prefix's.  The list's position of entry e is 16 (e + shift) there.
   const int e_base = w.ts * kTileBlocks;
   int full0 = (max(w.pre_units, ((sh.lo_most[x] + 15) >> 4) - w.shift) - e_base + kStepBlocks - 1) >> 2;
-  const int full1 = (((w.pos0 + x * a.R + 1) >> 4) - w.shift - e_base) >> 2;  // whole blocks up to the first row's position
+  const int full1 = (((w.pos0 + xt * a.R + 1) >> 4) - w.shift - e_base) >> 2;  // whole blocks up to the first row's position
   full0 = max(full0, 0);
   const int full_pre = ((w.pre >> 4) - e_base) >> 2;
   static_assert(kStepBlocks == 4, "steps of four blocks");
@@ -981,8 +1260,9 @@ __device__ __forceinline__ void softmax_rows(const PrefillAttnArgs& a, Shared<D,
                             ? (e_last - e_base) >> 2 : -1;
   const uint32_t t_lane = tmem + ((uint32_t)(r & ~31) << 16);
   const uint32_t to_addr = t_lane + NT * 2 * kStep + x * D;
-  bool ok = true;
-  float m = -INFINITY, l = 0.f;
+  ok = true;
+  m = -INFINITY;
+  l = 0.f;
   float reach = kCapNear;  // of the polynomial tried for the cap
   for (int j = range.hi; j >= range.lo; --j) {
     const uint32_t buf = n_step & 1u;
@@ -1140,13 +1420,11 @@ __device__ __forceinline__ void softmax_rows(const PrefillAttnArgs& a, Shared<D,
     ok = __all_sync(kFullMask, mbar_wait_spin(&sh.pv_done[x][(n_step - 1) & 1u], ((n_step - 1) >> 1) & 1u, a.timeout_ns));
     tc_fence_after();
   }
-  if (!ok) {
-    if (lane == 0) {
-      record_error(a.err, PKV_DEV_WAIT_TIMEOUT);
-      sh.abort = 1;
-    }
-    return;
+  if (!ok && lane == 0) {
+    record_error(a.err, PKV_DEV_WAIT_TIMEOUT);
+    sh.abort = 1;
   }
+  if (DIFF || !ok) return;  // (diff_rows goes on from here)
   // ---- the rows out: bf16, or this share's unnormalised row with its maximum and sum
   const bool split = w.nsplit > 1;
   const long long part =
@@ -1218,13 +1496,13 @@ __device__ __forceinline__ void softmax_rows(const PrefillAttnArgs& a, Shared<D,
   }
 }
 
-template <int D, int NT>
-__global__ void __launch_bounds__(Geo<D, NT>::kThreads, Geo<D, NT>::kCtas)
+template <int D, int NT, bool DIFF = false>
+__global__ void __launch_bounds__(Geo<D, NT, DIFF>::kThreads, Geo<D, NT, DIFF>::kCtas)
 prefill_attention_kernel(const __grid_constant__ PrefillAttnArgs a) {
-  using GE = Geo<D, NT>;
+  using GE = Geo<D, NT, DIFF>;
   extern __shared__ unsigned char smem_raw[];
   unsigned char* sq = reinterpret_cast<unsigned char*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
-  __shared__ Shared<D, NT> sh;
+  __shared__ Shared<D, NT, DIFF> sh;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   if (threadIdx.x == 32) {
     prefetch_tensor_map(&a.tmap_q);
@@ -1274,7 +1552,7 @@ prefill_attention_kernel(const __grid_constant__ PrefillAttnArgs a) {
     uint32_t n_step = 0;
     const int mode = (a.cap_log2 > 0.f ? 1 : 0) | (a.slopes != nullptr || !(a.scale_log2 > 0.f) ? 2 : 0);
     for (int it = blockIdx.x; it < total; it = sh.next, rec0 = sh.record[0], rec1 = sh.record[1]) {
-      Item w = item_of(a, it, rec0, rec1, NT);
+      Item w = item_of(a, it, rec0, rec1, NT, DIFF);
       if (threadIdx.x == 0) {
         for (int y = 0; y < NT; ++y) {
           sh.lo_least[y] = 0x7fffffff;
@@ -1282,9 +1560,10 @@ prefill_attention_kernel(const __grid_constant__ PrefillAttnArgs a) {
         }
       }
       __syncthreads();
-      const bool valid = tok < a.R && x * a.R + tok < w.tokens;
-      const int prow = w.row0 + x * a.R + tok;
-      const int i = valid ? w.pos0 + x * a.R + tok : -1;
+      const int at = (DIFF ? 0 : x * a.R) + tok;
+      const bool valid = tok < a.R && at < w.tokens;
+      const int prow = w.row0 + at;
+      const int i = valid ? w.pos0 + at : -1;
       const int lo = valid ? interval_start(a, prow, i) : 0;
       const int least = __reduce_min_sync(kFullMask, valid ? lo : 0x7fffffff);
       const int most = __reduce_max_sync(kFullMask, lo);
@@ -1296,8 +1575,10 @@ prefill_attention_kernel(const __grid_constant__ PrefillAttnArgs a) {
       set_keys(w, min(sh.lo_least[0], sh.lo_least[NT - 1]));
       if (x < w.nx) {
         const int h = w.g * a.G + head;
+        float top, sum;
+        bool ok;
         auto rows = [&](auto m) {
-          softmax_rows<D, NT, decltype(m)::value>(a, sh, w, sq, tmem, x, r, valid, i, lo, prow, h, n_kv, n_step);
+          softmax_rows<D, NT, DIFF, decltype(m)::value>(a, sh, w, sq, tmem, x, r, valid, i, lo, prow, h, n_kv, n_step, top, sum, ok);
         };
         // a loop for each set of rules: one for all is 3 to 5 % slower with a cap (0.88 against 0.84 ms, a chunk
         // of 4096 on 16384 keys).  One row tile has the registers of half the threads: there the loop for all
@@ -1310,6 +1591,8 @@ prefill_attention_kernel(const __grid_constant__ PrefillAttnArgs a) {
           else if (mode == 2) rows(std::integral_constant<int, 2>{});
           else rows(std::integral_constant<int, 3>{});
         }
+        if constexpr (DIFF)
+          diff_rows<D>(a, sh, w, tmem + ((uint32_t)(r & ~31) << 16) + NT * 2 * kStep, x, r, valid, ok, top, sum, i, lo, prow, h);
       }
       n_kv += 2 * w.nt;
       tc_fence_before();
@@ -1321,21 +1604,21 @@ prefill_attention_kernel(const __grid_constant__ PrefillAttnArgs a) {
     uint32_t n_step = 0;
     const uint32_t leader = elect_one();
     for (int it = blockIdx.x; it < total; it = sh.next, rec0 = sh.record[0], rec1 = sh.record[1]) {
-      Item w = item_of(a, it, rec0, rec1, NT);
+      Item w = item_of(a, it, rec0, rec1, NT, DIFF);
       __syncthreads();
       __syncthreads();
       set_keys(w, min(sh.lo_least[0], sh.lo_least[NT - 1]));
       if (w.nt > 0) {
         if (warp == GE::kProducer) {
-          produce<D, NT>(a, sh, w, sq, n_kv, n_q);
+          produce<D, NT, DIFF>(a, sh, w, sq, n_kv, n_q);
         } else if (warp < GE::kTicket) {
           tc_fence_after();
           const int k = warp - GE::kIssuer;
           if constexpr (NT == 2) {
-            issue_mmas<D, NT, true, true>(a, sh, w, sq, tmem, leader, k, n_kv, n_q, n_step);
+            issue_mmas<D, NT, DIFF, true, true>(a, sh, w, sq, tmem, leader, k, n_kv, n_q, n_step);
           } else {
-            if (k == 0) issue_mmas<D, NT, true, false>(a, sh, w, sq, tmem, leader, 0, n_kv, n_q, n_step);
-            else issue_mmas<D, NT, false, true>(a, sh, w, sq, tmem, leader, 0, n_kv, n_q, n_step);
+            if (k == 0) issue_mmas<D, NT, DIFF, true, false>(a, sh, w, sq, tmem, leader, 0, n_kv, n_q, n_step);
+            else issue_mmas<D, NT, DIFF, false, true>(a, sh, w, sq, tmem, leader, 0, n_kv, n_q, n_step);
           }
         }
         ++n_q;
@@ -1362,10 +1645,11 @@ prefill_attention_kernel(const __grid_constant__ PrefillAttnArgs a) {
 // ------------------------------------------------------------------------------------ the merge
 
 // A warp a row of a split entry: lane k has the (maximum, sum) of shares k and k + 32, then the rows of all
-// shares are added, four loads in flight.
-template <int D>
+// shares are added, four loads in flight.  DIFF: the partial rows of a row's two maps stand next to one another, and
+// their difference (and norm) goes out.
+template <int D, bool DIFF = false>
 __global__ void __launch_bounds__(256) prefill_merge_kernel(const PrefillAttnArgs a, int per_item) {
-  constexpr int E = D / 32;
+  constexpr int E = D / 32, M = DIFF ? 2 : 1;
   const int lane = threadIdx.x & 31;
   grid_dependency_wait();
   grid_launch_dependents();
@@ -1378,12 +1662,15 @@ __global__ void __launch_bounds__(256) prefill_merge_kernel(const PrefillAttnArg
     const int per = split.y * a.Hq;
     if (in >= per) continue;
     const long long p0 = (long long)split.w + in;
+    float y[E] = {};
+#pragma unroll
+    for (int map = 0; map < M; ++map) {
     float2 ml[2];
     float m = -INFINITY;
 #pragma unroll
     for (int q = 0; q < 2; ++q) {
       const int sh = lane + 32 * q;
-      ml[q] = sh < split.z ? __ldcg(a.part_ml + p0 + (long long)sh * per) : make_float2(-INFINITY, 0.f);
+      ml[q] = sh < split.z ? __ldcg(a.part_ml + (p0 + (long long)sh * per) * M + map) : make_float2(-INFINITY, 0.f);
       m = fmaxf(m, ml[q].x);
     }
 #pragma unroll
@@ -1401,7 +1688,7 @@ __global__ void __launch_bounds__(256) prefill_merge_kernel(const PrefillAttnArg
 #pragma unroll 4
     for (int sh = 0; sh < split.z; ++sh) {
       const float f = __shfl_sync(kFullMask, sh < 32 ? w[0] : w[1], sh & 31);
-      const float* src = a.part_o + (p0 + (long long)sh * per) * D + lane * E;
+      const float* src = a.part_o + ((p0 + (long long)sh * per) * M + map) * D + lane * E;
       float x[E];
       if constexpr (E == 4) {
         const float4 t = __ldcg(reinterpret_cast<const float4*>(src));
@@ -1414,10 +1701,31 @@ __global__ void __launch_bounds__(256) prefill_merge_kernel(const PrefillAttnArg
       for (int e = 0; e < E; ++e) o[e] = f == 0.f ? o[e] : fmaf(f, x[e], o[e]);
     }
     const float inv = l > 0.f ? 1.f / l : (l == l ? 0.f : l);
+    if constexpr (DIFF) {
+      const int tok = in / a.Hq, h = in - tok * a.Hq;
+      float f = inv;
+      if (map == 1) f = l != 0.f ? -inv * __ldg(a.lambdas + (size_t)(split.x + tok) * a.lambda_stride + h) : 0.f;
+#pragma unroll
+      for (int e = 0; e < E; ++e) y[e] = map == 0 ? o[e] * f : fmaf(o[e], f, y[e]);
+    } else {
+#pragma unroll
+      for (int e = 0; e < E; ++e) y[e] = o[e] * inv;
+    }
+    }
+    if constexpr (DIFF) {
+      if (a.norm_weight != nullptr) {
+        SquareSum s;
+#pragma unroll
+        for (int e = 0; e < E; ++e) s.add(y[e]);
+        s.join(32);
+        const float f = s.factor(D, a.norm_eps);
+#pragma unroll
+        for (int e = 0; e < E; ++e) y[e] *= f * __ldg(a.norm_weight + lane * E + e);
+      }
+    }
     __nv_bfloat16* dst = a.out + ((long long)split.x * a.Hq + in) * D + lane * E;
 #pragma unroll
-    for (int e = 0; e < E; e += 2)
-      *reinterpret_cast<uint32_t*>(dst + e) = pack_bf16x2(o[e] * inv, o[e + 1] * inv);
+    for (int e = 0; e < E; e += 2) *reinterpret_cast<uint32_t*>(dst + e) = pack_bf16x2(y[e], y[e + 1]);
   }
 }
 
@@ -1434,10 +1742,10 @@ struct PrefillWorkspace {
 
 // head | int4[2] items | int4 split entries | float2 (m, l) | float o.  Entries: at most one per 128 rows, and one
 // more per sequence; items: those and the shares of split ones.
-PrefillWorkspace plan_prefill(long long B, long long T, int Hq, int G, int D) {
+PrefillWorkspace plan_prefill(long long B, long long T, int Hq, int G, int D, int maps) {
   PrefillWorkspace w{};
   const long long entries = T / (128 / G) + B;
-  const long long rows = std::min(kMaxPartRows, T * Hq * kMaxShares);
+  const long long rows = std::min(kMaxPartRows, T * Hq * kMaxShares * maps);
   w.items = 256;
   w.split = align256p(w.items + 2 * sizeof(int4) * (size_t)(entries + 4 * kMaxSms));
   w.ml = align256p(w.split + sizeof(int4) * (size_t)std::min<long long>(entries, 4 * kMaxSms));
@@ -1448,12 +1756,12 @@ PrefillWorkspace plan_prefill(long long B, long long T, int Hq, int G, int D) {
 
 size_t plan_smem_bytes(int B) { return sizeof(int) * (4 * (size_t)B + 1); }
 
-template <int D, int NT>
+template <int D, int NT, bool DIFF = false>
 cudaError_t launch_attention(const PrefillAttnArgs& a, cudaStream_t stream) {
-  using GE = Geo<D, NT>;
+  using GE = Geo<D, NT, DIFF>;
   PrefillAttnArgs args = a;
   args.slots = std::min(a.sms, kMaxSms) * GE::kCtas;
-  int per_item = NT * a.R;
+  int per_item = (DIFF ? 1 : NT) * a.R;
   void* plan_params[] = {&args, &per_item};
   // a whole call with a plan of 512 and of 1024 threads, us: one token 19.1, 20.0; 24 mixed sequences 28.1, 28.9; 300
   // sequences 39.1, 40.3; 1000 37.6, 36.5; 4000 114, 106 (256 threads: 19.3, 28.5, 41.2, 42.4, 140)
@@ -1462,21 +1770,21 @@ cudaError_t launch_attention(const PrefillAttnArgs& a, cudaStream_t stream) {
   if (e != cudaSuccess) return e;
   void* params[] = {&args};
   // a CTA for every slot: even one token's keys are cut into shares for all of them
-  e = launch_pdl((const void*)prefill_attention_kernel<D, NT>, dim3((unsigned)args.slots), dim3(GE::kThreads), GE::kSmem, stream, params);
+  e = launch_pdl((const void*)prefill_attention_kernel<D, NT, DIFF>, dim3((unsigned)args.slots), dim3(GE::kThreads), GE::kSmem, stream, params);
   if (e != cudaSuccess) return e;
   const long long entries = (long long)a.T / per_item + a.B;  // at most
   const long long warps = std::min(entries * std::min(per_item, a.T) * a.Hq, 8ll * 8 * a.sms);
-  return launch_pdl((const void*)prefill_merge_kernel<D>, dim3((unsigned)((warps + 7) / 8)), dim3(256), 0, stream, plan_params);
+  return launch_pdl((const void*)prefill_merge_kernel<D, DIFF>, dim3((unsigned)((warps + 7) / 8)), dim3(256), 0, stream, plan_params);
 }
 
-template <int D, int NT>
+template <int D, int NT, bool DIFF = false>
 cudaError_t setup_attention() {
-  return cudaFuncSetAttribute((const void*)prefill_attention_kernel<D, NT>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                              (int)Geo<D, NT>::kSmem);
+  return cudaFuncSetAttribute((const void*)prefill_attention_kernel<D, NT, DIFF>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                              (int)Geo<D, NT, DIFF>::kSmem);
 }
 }  // namespace
 
-size_t prefill_attention_workspace(int B, int T, int Hq, int G, int D) { return plan_prefill(B, T, Hq, G, D).total; }
+size_t prefill_attention_workspace(int B, int T, int Hq, int G, int D, int maps) { return plan_prefill(B, T, Hq, G, D, maps).total; }
 
 cudaError_t prefill_attention_device_setup() {
   cudaError_t e = cudaFuncSetAttribute((const void*)prefill_plan_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
@@ -1485,18 +1793,22 @@ cudaError_t prefill_attention_device_setup() {
   if (e == cudaSuccess) e = setup_attention<128, 2>();
   if (e == cudaSuccess) e = setup_attention<64, 1>();
   if (e == cudaSuccess) e = setup_attention<64, 2>();
+  if (e == cudaSuccess) e = setup_attention<128, 2, true>();
+  if (e == cudaSuccess) e = setup_attention<64, 2, true>();
   return e;
 }
 
 cudaError_t launch_prefill_attention(const PrefillAttnArgs& a, void* workspace, int head_dim, cudaStream_t stream) {
   PrefillAttnArgs args = a;
-  const PrefillWorkspace w = plan_prefill(a.B, a.T, a.Hq, a.G, head_dim);
+  const PrefillWorkspace w = plan_prefill(a.B, a.T, a.Hq, a.G, head_dim, a.lambdas != nullptr ? 2 : 1);
   unsigned char* ws = static_cast<unsigned char*>(workspace);
   args.plan_head = reinterpret_cast<int*>(ws);
   args.plan_items = reinterpret_cast<int4*>(ws + w.items);
   args.plan_split = reinterpret_cast<int4*>(ws + w.split);
   args.part_ml = reinterpret_cast<float2*>(ws + w.ml);
   args.part_o = reinterpret_cast<float*>(ws + w.o);
+  if (a.lambdas != nullptr)
+    return head_dim == 128 ? launch_attention<128, 2, true>(args, stream) : launch_attention<64, 2, true>(args, stream);
   // two row tiles an item when the sequences fill more than one on average (64 single tokens on 2000 keys, d 128:
   // 110 us with one, 149 with two; 8 x 16 on 5000 52 and 64; 4 x 2048 prompts 205 and 163; 4 x 512 on 4096 with
   // one head a kv head 62 and 56)
@@ -1527,17 +1839,25 @@ int check_prefill(const pkv_dims* dims, int32_t total_tokens) {
 
 extern "C" {
 
-size_t pkv_prefill_workspace_bytes(const pkv_dims* dims, int32_t total_tokens) {
+static size_t prefill_bytes(const pkv_dims* dims, int32_t total_tokens, int maps) {
   if (check_prefill(dims, total_tokens) != PKV_OK) return 0;
   return prefill_attention_workspace(dims->batch, total_tokens, dims->num_q_heads,
-                                     dims->num_q_heads / dims->num_kv_heads, dims->head_dim);
+                                     dims->num_q_heads / dims->num_kv_heads, dims->head_dim, maps);
 }
 
-int pkv_paged_prefill_attention(void* out, const void* q, const void* k_cache, const void* v_cache,
-                                const int32_t* block_tables, const int32_t* context_lens,
-                                const int32_t* query_starts, int32_t total_tokens, float scale,
-                                const pkv_score_rules* rules, void* workspace, size_t workspace_bytes,
-                                const pkv_dims* dims, int32_t* error_word, void* stream) {
+size_t pkv_prefill_workspace_bytes(const pkv_dims* dims, int32_t total_tokens) {
+  return prefill_bytes(dims, total_tokens, 1);
+}
+
+size_t pkv_diff_prefill_workspace_bytes(const pkv_dims* dims, int32_t total_tokens) {
+  return prefill_bytes(dims, total_tokens, 2);
+}
+
+static int prefill_common(void* out, const void* q, const void* k_cache, const void* v_cache,
+                          const int32_t* block_tables, const int32_t* context_lens, const int32_t* query_starts,
+                          int32_t total_tokens, float scale, const pkv_diff_params* diff, const pkv_score_rules* rules,
+                          void* workspace, size_t workspace_bytes, const pkv_dims* dims, int32_t* error_word,
+                          void* stream) {
   int st = check_prefill(dims, total_tokens);
   if (st != PKV_OK) return st;
   if (rules != nullptr) {
@@ -1546,7 +1866,7 @@ int pkv_paged_prefill_attention(void* out, const void* q, const void* k_cache, c
   }
   if (dims->batch == 0 || total_tokens == 0) return PKV_OK;
   if (!out || !q || !k_cache || !v_cache || !block_tables || !context_lens || !query_starts) return PKV_ERR_NULL_POINTER;
-  if (!workspace || workspace_bytes < pkv_prefill_workspace_bytes(dims, total_tokens)) return PKV_ERR_WORKSPACE;
+  if (!workspace || workspace_bytes < prefill_bytes(dims, total_tokens, diff != nullptr ? 2 : 1)) return PKV_ERR_WORKSPACE;
   if (!aligned16(out) || !aligned16(q) || !aligned16(k_cache) || !aligned16(v_cache) || !aligned16(workspace) ||
       ((reinterpret_cast<uintptr_t>(block_tables) | reinterpret_cast<uintptr_t>(context_lens) |
         reinterpret_cast<uintptr_t>(query_starts) | reinterpret_cast<uintptr_t>(error_word)) & 3u))
@@ -1589,7 +1909,33 @@ int pkv_paged_prefill_attention(void* out, const void* q, const void* k_cache, c
     a.cap_log2 = rules->softcap * kLog2e;
     a.cap_in = rules->softcap > 0.f ? 2.f / rules->softcap : 0.f;
   }
+  if (diff != nullptr) {
+    a.lambdas = diff->lambdas;
+    a.lambda_stride = diff->lambda_rows != 0 ? dims->num_q_heads : 0;
+    a.norm_weight = diff->norm_weight;
+    a.norm_eps = diff->norm_eps;
+  }
   return cuda_status(launch_prefill_attention(a, workspace, dims->head_dim, static_cast<cudaStream_t>(stream)));
+}
+
+int pkv_paged_prefill_attention(void* out, const void* q, const void* k_cache, const void* v_cache,
+                                const int32_t* block_tables, const int32_t* context_lens,
+                                const int32_t* query_starts, int32_t total_tokens, float scale,
+                                const pkv_score_rules* rules, void* workspace, size_t workspace_bytes,
+                                const pkv_dims* dims, int32_t* error_word, void* stream) {
+  return prefill_common(out, q, k_cache, v_cache, block_tables, context_lens, query_starts, total_tokens, scale, nullptr,
+                        rules, workspace, workspace_bytes, dims, error_word, stream);
+}
+
+int pkv_paged_diff_prefill_attention(void* out, const void* q, const void* k_cache, const void* v_cache,
+                                     const int32_t* block_tables, const int32_t* context_lens,
+                                     const int32_t* query_starts, int32_t total_tokens, float scale,
+                                     const pkv_diff_params* params, const pkv_score_rules* rules, void* workspace,
+                                     size_t workspace_bytes, const pkv_dims* dims, int32_t* error_word, void* stream) {
+  const int st = check_diff(params);
+  if (st != PKV_OK) return st;
+  return prefill_common(out, q, k_cache, v_cache, block_tables, context_lens, query_starts, total_tokens, scale, params,
+                        rules, workspace, workspace_bytes, dims, error_word, stream);
 }
 
 }  // extern "C"

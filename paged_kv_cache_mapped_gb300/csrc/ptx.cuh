@@ -499,6 +499,39 @@ __device__ __forceinline__ float ex2_approx(float x) {
   return y;
 }
 
+// Barrier number `id` of `threads` threads of the block; whether `p` holds in any of them.
+__device__ __forceinline__ bool named_barrier_or(int id, int threads, bool p) {
+  int any;
+  asm volatile(
+      "{\n\t.reg .pred a, b;\n\tsetp.ne.s32 a, %1, 0;\n\tbarrier.red.or.pred b, %2, %3, a;\n\tselp.s32 %0, 1, 0, b;\n\t}"
+      : "=r"(any)
+      : "r"((int)p), "r"(id), "r"(threads)
+      : "memory");
+  return any != 0;
+}
+
+// A row's sum of squares, and that of its values times 2^-80, for rows whose squares pass fp32.
+struct SquareSum {
+  float s = 0.f, b = 0.f;
+  __device__ __forceinline__ void add(float y) {
+    const float t = y * 8.271806125530277e-25f;  // 2^-80
+    s = fmaf(y, y, s);
+    b = fmaf(t, t, b);
+  }
+  // over the lanes whose numbers differ in bits of from .. n / 2
+  __device__ __forceinline__ void join(int n, int from = 1) {
+#pragma unroll
+    for (int o = from; o < n; o <<= 1) {
+      s += __shfl_xor_sync(kFullMask, s, o);
+      b += __shfl_xor_sync(kFullMask, b, o);
+    }
+  }
+  // 1 / sqrt(mean + eps) of n values
+  __device__ __forceinline__ float factor(int n, float eps) const {
+    return s <= 3.4028234e38f ? rsqrtf(s * (1.f / (float)n) + eps) : rsqrtf(b * (1.f / (float)n)) * 8.271806125530277e-25f;
+  }
+};
+
 // The largest i < n with start[i] <= x (start ascending, start[0] <= x: entry i has the items from start[i] on; of
 // equal starts the last one has them).
 __device__ __forceinline__ int owner_of(const int* start, int n, int x) {

@@ -96,3 +96,44 @@ def paged_diff_decode_attention_scores(q, k_cache, v_cache, block_tables, contex
     return _decode("pkv_paged_diff_decode_attention_scores", (sp, sop, stride), stride, q, k_cache, v_cache, block_tables,
                    context_lens, lambdas, scale, window, norm_weight, norm_eps, softcap, alibi_slopes, doc_starts, prefix_lens, out,
                    workspace, error_word, inputs_ready, stream)
+
+
+def diff_prefill_workspace_bytes(total_tokens, batch, num_q_heads, num_kv_heads, head_dim, num_blocks, max_blocks_per_seq) -> int:
+    """Workspace of paged_diff_prefill_attention for these sizes and at most total_tokens query rows."""
+    dims = _dims(batch, num_q_heads, num_kv_heads, head_dim, num_blocks, max_blocks_per_seq)
+    T = int(total_tokens)
+    n = int(load().pkv_diff_prefill_workspace_bytes(dims, T)) if 0 <= T < 2**31 else 0
+    if n == 0:
+        raise ValueError("invalid dims for paged prefill")
+    return n
+
+
+def paged_diff_prefill_attention(q, k_cache, v_cache, block_tables, context_lens, query_starts, lambdas, scale, window=0, *,
+                                 norm_weight=None, norm_eps=1e-5, softcap=0.0, alibi_slopes=None, doc_starts=None,
+                                 prefix_lens=None, out=None, workspace=None, error_word=None, stream=None):
+    """Differential attention of many query tokens per sequence, causal, over the paged cache: q [T, Hq, d] packs the
+    queries of every sequence as in paged_prefill_attention (query_starts int32 [B + 1]), heads, norm and rules are those of
+    paged_diff_decode_attention with lambdas fp32 [Hq] or [T, Hq] and doc_starts one int32 per packed row.  Returns
+    out [T, Hq, d]; rows from query_starts[B] on are left as they were (unset when `out` is made here)."""
+    nb, hkv, d, dev, kp, vp = _bf16_pools(k_cache, v_cache)
+    qp = _need(q, "q", torch.bfloat16, 3, dev)
+    bp = _need(block_tables, "block_tables", torch.int32, 2, dev)
+    lp = _need(context_lens, "context_lens", torch.int32, 1, dev)
+    sp = _need(query_starts, "query_starts", torch.int32, 1, dev)
+    err = _opt(error_word, "error_word", torch.int32, 1, dev)
+    T, hq, dq = q.shape
+    B, mb = block_tables.shape
+    if dq != d:
+        raise ValueError("q head_dim differs from the pools'")
+    if context_lens.shape[0] != B or query_starts.shape[0] != B + 1:
+        raise ValueError("context_lens must be [B] and query_starts [B + 1]")
+    params = _params(lambdas, norm_weight, norm_eps, T, hq, d, dev)
+    rules = _rules(softcap, window, alibi_slopes, doc_starts, prefix_lens, hq, T, B, dev)
+    dims = _dims(B, hq, hkv, d, nb, mb)
+    out, op = _give(out, "out", (T, hq, d), torch.bfloat16, q, dev, stream)
+    if workspace is None:
+        workspace = _new((int(load().pkv_diff_prefill_workspace_bytes(dims, T)),), torch.uint8, q, stream)
+    wp = _need(workspace, "workspace", torch.uint8, 1, dev)
+    _call("pkv_paged_diff_prefill_attention", dev, stream, op, qp, kp, vp, bp, lp, sp, T, scale, ctypes.byref(params),
+          ctypes.byref(rules), wp, workspace.numel(), dims, err)
+    return out
