@@ -20,6 +20,9 @@
 extern "C" {
 #endif
 
+/* Most cached tokens of a sequence that an eviction takes. */
+#define PKV_MAX_EVICT_TOKENS 262144
+
 /* What an eviction keeps: n_sink + k_top + n_recent tokens (the budget) of a sequence of more than
  * max(trigger, budget). */
 typedef struct pkv_evict_rules {
@@ -75,9 +78,11 @@ size_t pkv_evict_workspace_bytes(const pkv_dims* dims, const pkv_evict_rules* ru
  *                      free_count_out): nothing is pushed.  Layers that share one table pass it once, and
  *                      all but the last get context_lens_out other than context_lens.
  *   free_count_out   : [1] int32; may be free_count itself.
- *   dims             : uses batch (<= 4096), num_kv_heads, head_dim, block_size, num_blocks, max_blocks_per_seq.
- *   error_word       : PKV_DEV_BAD_CONTEXT_LEN (a length outside its table or past `stride`, dropped < 0 or a
- *                      length with it past 32 bits: the sequence is left alone, without copies), PKV_DEV_BAD_SCORE
+ *   dims             : uses batch (<= 4096), num_kv_heads, head_dim, block_size, num_blocks (< 2^27),
+ *                      max_blocks_per_seq.
+ *   error_word       : PKV_DEV_BAD_CONTEXT_LEN (a length outside its table, past `stride` or past
+ *                      PKV_MAX_EVICT_TOKENS, dropped < 0 or a length with it past 32 bits: the sequence is left alone,
+ *                      without copies), PKV_DEV_BAD_SCORE
  *                      (a NaN, which counts as the lowest score), PKV_DEV_BAD_BLOCK_ID (a block outside the pool
  *                      among those a row moves from or to -- the row is not moved -- or that would be pushed -- it
  *                      is not), PKV_DEV_NO_BLOCKS (a free count outside the stack: nothing is pushed; or a full

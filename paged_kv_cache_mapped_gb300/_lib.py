@@ -81,7 +81,7 @@ class PkvError(RuntimeError):
 def header_constants() -> dict:
     """#define NAME value pairs of the public headers (status and device-error codes, flags, limits)."""
     out = {}
-    for path in (HEADER, STEP_HEADER):
+    for path in (HEADER, STEP_HEADER, EVICT_HEADER):
         with open(path) as f:
             for m in re.finditer(r"^#define\s+(PKV_\w+)\s+([-+*() 0-9]+?)\s*(?:/\*.*)?$", f.read(), re.M):
                 out[m.group(1)] = int(eval(m.group(2), {"__builtins__": {}}, {}))  # integer literal arithmetic only

@@ -12,6 +12,8 @@
 //    rows to go there, scores and positions.
 //  * evict_move_kernel: the rows, many CTAs for each (sequence, kv head); one more CTA does the lengths and the
 //    free stack.
+#include <cooperative_groups.h>
+
 #include <algorithm>
 
 #include "kernels.h"
@@ -35,10 +37,10 @@ struct EvictArgs {
   int32_t* free_count_out;
   int32_t* err;
   int32_t* count;                // [B * Hkv] moves of each (sequence, kv head)
-  int2* moves;                   // [B * Hkv, budget] (slot from, slot to)
+  int4* moves;                   // [B * Hkv, budget] (from, to: block * 16 + offset, or -1; score bits, position)
+  int32_t* to_slot;              // [B * Hkv, budget] the slot that each goes to
   int B, Hkv, NB, MB;
   int n_sink, n_recent, budget, trigger;
-  int cached;                    // keys of a row that shared memory holds
   int splits;                    // CTAs that share the moves of one (sequence, kv head)
 };
 
@@ -54,7 +56,7 @@ __device__ __forceinline__ EvictSeq evict_seq(const EvictArgs& a, int b) {
   EvictSeq s;
   s.L = a.context_lens[b];
   s.dropped = a.st.dropped[b];
-  const bool bad = s.L < 0 || s.L > a.MB * 16 || s.L > a.st.stride || s.dropped < 0 || s.dropped > 0x7fffffff - s.L;
+  const bool bad = s.L < 0 || s.L > a.MB * 16 || s.L > a.st.stride || s.L > PKV_MAX_EVICT_TOKENS || s.dropped < 0 || s.dropped > 0x7fffffff - s.L;
   s.err = bad ? PKV_DEV_BAD_CONTEXT_LEN : 0;
   s.cut = !bad && s.L > a.trigger;
   return s;
@@ -86,13 +88,20 @@ __device__ __forceinline__ int block_sum_before(int v, int* sums, int* total) {
 //
 // Keys are the scores mapped to uint32 in their order (a protected token has the largest, a NaN the
 // smallest).  The key of the last place is found in rounds: a histogram of 2048 equal bins over the range of
-// keys that are left (their own least to greatest in the first round, so that the few exponents of real
-// scores fill many bins), then the bin that holds it, until at most a thread's worth of keys each
+// keys that are left (in the first round those of positive scores, from their own least to their greatest, so that
+// the few exponents of real scores fill many bins; the others only if the positive ones do not suffice), then the bin that holds it, until at most a thread's worth of keys each
 // is left, which are ranked against one another.  Three rounds at most end in a range of one key.
+// A row of few (sequence, kv head) pairs is shared by a cluster of CTAs, each with its part of the slots and
+// all with the sums of the others' histograms.
 
 constexpr int kEvictBins = 2048;
-constexpr int kEvictMaxThreads = 1024;
+constexpr int kEvictMinThreads = 256, kEvictMaxThreads = 1024;
+constexpr int kEvictBatch = 8;  // slots whose loads a thread has in flight
+constexpr int kMoveBatch = 4;   // likewise, moves
+constexpr int kEvictSlots = 32768;  // of a CTA at most: 32 words of 32 for each of 32 warps
+static_assert(PKV_MAX_EVICT_TOKENS == 8 * kEvictSlots, "a cluster of eight");
 constexpr uint32_t kProtectedKey = 0xffffffffu;
+constexpr uint32_t kZeroKey = 0x80000000u;  // of a score of 0
 
 __device__ __forceinline__ uint32_t order_key(float s) {
   if (s != s) return 0u;
@@ -101,21 +110,33 @@ __device__ __forceinline__ uint32_t order_key(float s) {
   return (u & 0x80000000u) ? ~u : (u | 0x80000000u);
 }
 
+struct EvictShared {
+  int hist[kEvictBins];
+  uint32_t list[kEvictMaxThreads];
+  int sums[33];
+  uint32_t least, most, key;  // least key of a positive score (less the key of zero), greatest unprotected one (plus 1)
+  int guarded, n, bin, above, in, total, ties, cut;
+  int equal, to, from;  // counts of this CTA's slots
+};
+
+template <bool CLUSTER>
 __global__ void __launch_bounds__(kEvictMaxThreads, 1) evict_select_kernel(const EvictArgs a) {
-  extern __shared__ uint32_t s_keys[];  // [cached]
-  __shared__ int s_hist[kEvictBins];
-  __shared__ uint32_t s_list[kEvictMaxThreads];
-  __shared__ int s_sums[33];
-  __shared__ uint32_t s_min, s_max;
-  __shared__ int s_protected, s_n, s_bin, s_above, s_in;
-  __shared__ uint32_t s_key;
-  __shared__ int s_ties;
+  namespace cg = cooperative_groups;
+  extern __shared__ uint32_t s_keys[];  // of this CTA's slots
+  __shared__ EvictShared sh;
+  cg::cluster_group cluster = cg::this_cluster();
+  const int ranks = CLUSTER ? (int)cluster.num_blocks() : 1, rank = CLUSTER ? (int)cluster.block_rank() : 0;
+  auto sync_all = [&] {
+    if constexpr (CLUSTER) cluster.sync();
+    else __syncthreads();
+  };
+  auto of_rank = [&](int r) { return CLUSTER ? cluster.map_shared_rank(&sh, r) : &sh; };
   const int tid = threadIdx.x, lane = tid & 31, T = blockDim.x;
-  const int bg = blockIdx.x, b = bg / a.Hkv;
+  const int bg = blockIdx.x / ranks, b = bg / a.Hkv;
   if (tid == 0) {
-    s_min = 0xffffffffu;
-    s_max = 0u;
-    s_protected = 0;
+    sh.least = 0xffffffffu;
+    sh.most = 0u;
+    sh.guarded = 0;
   }
   grid_dependency_wait();
   grid_launch_dependents();
@@ -125,175 +146,360 @@ __global__ void __launch_bounds__(kEvictMaxThreads, 1) evict_select_kernel(const
   float* scores_out = a.st.scores_out + (size_t)bg * a.st.stride;
   int32_t* pos_out = a.st.slot_pos_out + (size_t)bg * a.st.stride;
   if (!s.cut) {
-    if (tid == 0) {
+    if (tid == 0 && rank == 0) {
       a.count[bg] = 0;
       if (s.err != 0) record_error(a.err, s.err);
     }
     if (s.err == 0) {
-      for (int i = tid; i < s.L; i += T) {
-        if (scores_out != scores) scores_out[i] = scores[i];
-        if (pos_out != slot_pos) pos_out[i] = slot_pos[i];
-      }
+      if (scores_out != scores)
+        for (int i = rank * T + tid; i < s.L; i += ranks * T) scores_out[i] = scores[i];
+      if (pos_out != slot_pos)
+        for (int i = rank * T + tid; i < s.L; i += ranks * T) pos_out[i] = slot_pos[i];
     }
     return;
   }
   __syncthreads();
-  const int L = s.L, recent0 = L + s.dropped - a.n_recent;  // (n_recent <= budget < L)
-  auto position = [&](int i) {
-    const int p = slot_pos[i];
-    return p >= 0 ? p : i + s.dropped;
+  const int recent0 = s.L + s.dropped - a.n_recent;  // (n_recent <= budget < L)
+  // this CTA's slots
+  const int chunk = (s.L + ranks - 1) / ranks, first = min(rank * chunk, s.L), end = min(first + chunk, s.L), own = end - first;
+  auto place = [&](int p, int i) { return p >= 0 ? p : i + s.dropped; };
+  auto make_key = [&](int p, int i, float score) {
+    p = place(p, i);
+    return p < a.n_sink || p >= recent0 ? kProtectedKey : order_key(score);
   };
-  auto key_of = [&](int i) {
-    const int p = position(i);
-    return p < a.n_sink || p >= recent0 ? kProtectedKey : order_key(scores[i]);
-  };
-  auto key_at = [&](int i) { return i < a.cached ? s_keys[i] : key_of(i); };
 
   // ---- keys into shared memory; their range
-  uint32_t least = 0xffffffffu, most = 0u;
-  int prot = 0;
-  bool nan = false;
-  for (int i = tid; i < L; i += T) {
-    const uint32_t k = key_of(i);
-    if (i < a.cached) s_keys[i] = k;
-    nan |= k == 0u;
-    if (k == kProtectedKey) {
-      ++prot;
-    } else {
-      least = min(least, k);
-      most = max(most, k);
+  {
+    uint32_t least = 0xffffffffu, most = 0u;
+    int guarded = 0;
+    bool nan = false;
+    const float* sc = scores + first;
+    const int32_t* sp = slot_pos + first;
+    auto take = [&](int j, float x, int p) {
+      const uint32_t k = make_key(p, first + j, x);
+      s_keys[j] = k;
+      nan |= k == 0u;
+      guarded += k == kProtectedKey ? 1 : 0;
+      least = min(least, k - (kZeroKey + 1u));  // (keys up to that of zero wrap to the end)
+      most = max(most, k + 1u);                 // (the protected one wraps to 0)
+    };
+    int j0 = tid;
+    for (; j0 + (kEvictBatch - 1) * T < own; j0 += kEvictBatch * T) {
+      float x[kEvictBatch];
+      int p[kEvictBatch];
+#pragma unroll
+      for (int q = 0; q < kEvictBatch; ++q) {
+        x[q] = sc[j0 + q * T];
+        p[q] = sp[j0 + q * T];
+      }
+#pragma unroll
+      for (int q = 0; q < kEvictBatch; ++q) take(j0 + q * T, x[q], p[q]);
     }
+    if (j0 < own) {
+      float x[kEvictBatch];
+      int p[kEvictBatch];
+#pragma unroll
+      for (int q = 0; q < kEvictBatch; ++q) {
+        const int j = min(j0 + q * T, own - 1);
+        x[q] = sc[j];
+        p[q] = sp[j];
+      }
+#pragma unroll
+      for (int q = 0; q < kEvictBatch; ++q)
+        if (j0 + q * T < own) take(j0 + q * T, x[q], p[q]);
+    }
+    least = __reduce_min_sync(kFullMask, least);
+    most = __reduce_max_sync(kFullMask, most);
+    guarded = __reduce_add_sync(kFullMask, guarded);
+    if (lane == 0) {
+      atomicMin(&sh.least, least);
+      atomicMax(&sh.most, most);
+      atomicAdd(&sh.guarded, guarded);
+    }
+    if (nan) record_error(a.err, PKV_DEV_BAD_SCORE);
   }
-  least = __reduce_min_sync(kFullMask, least);
-  most = __reduce_max_sync(kFullMask, most);
-  prot = __reduce_add_sync(kFullMask, prot);
-  if (lane == 0) {
-    atomicMin(&s_min, least);
-    atomicMax(&s_max, most);
-    atomicAdd(&s_protected, prot);
+  sync_all();
+  uint32_t lo = 0xffffffffu, hi = 0u;
+  int need = a.budget;  // among the unprotected, fewer than they are
+  for (int r = 0; r < ranks; ++r) {
+    const EvictShared* o = of_rank(r);
+    lo = min(lo, o->least);
+    hi = max(hi, o->most);
+    need -= o->guarded;
   }
-  if (nan) record_error(a.err, PKV_DEV_BAD_SCORE);
-  __syncthreads();
+  hi -= 1u;
+  lo += kZeroKey + 1u;
 
-  // ---- the last place: keys above s_key stay, and the first s_ties of those equal to it
-  int need = a.budget - s_protected;  // among the unprotected, fewer than they are
+  // ---- the last place: keys above sh.key stay, and the first sh.ties of those equal to it, all of them unless sh.cut
   if (need <= 0) {
     if (tid == 0) {
-      s_key = kProtectedKey;
-      s_ties = a.budget;
+      sh.key = kProtectedKey;
+      sh.ties = a.budget;
+      sh.cut = need < 0 ? 1 : 0;
     }
   } else {
-    uint32_t lo = s_min, hi = s_max;
+    bool above_zero = true;
+    if (lo > hi || hi <= kZeroKey) {  // no score is positive
+      lo = 0u;
+      hi = kZeroKey;
+      above_zero = false;
+    }
     for (;;) {
       const uint32_t range = hi - lo;
-      if (range == 0u) {
+      if (range == 0u && !above_zero) {
         if (tid == 0) {
-          s_key = lo;
-          s_ties = need;
+          sh.key = lo;
+          sh.ties = need;
+          sh.cut = 1;
         }
         break;
       }
       const int shift = max(0, 32 - __clz(range) - 11);
-      for (int i = tid; i < kEvictBins; i += T) s_hist[i] = 0;
-      if (tid == 0) s_n = 0;
+      for (int i = tid; i < kEvictBins; i += T) sh.hist[i] = 0;
+      if (tid == 0) sh.n = 0;
       __syncthreads();
-      int at_lo = 0;  // the least key is often that of many (tokens without any weight)
-      for (int i = tid; i < L; i += T) {
-        const uint32_t k = key_at(i);
-        if (k == lo) ++at_lo;
-        else if (k > lo && k <= hi) atomicAdd(&s_hist[(k - lo) >> shift], 1);
+#pragma unroll 4
+      for (int j = tid; j < own; j += T) {
+        const uint32_t k = s_keys[j] - lo;
+        if (k <= range) atomicAdd(&sh.hist[k >> shift], 1);
       }
-      at_lo = __reduce_add_sync(kFullMask, at_lo);
-      if (lane == 0 && at_lo > 0) atomicAdd(&s_hist[0], at_lo);
-      __syncthreads();
+      sync_all();
+      // a thread's bins of the whole row, and the keys in the bins past them
       const int per = kEvictBins / T;  // (T divides it)
-      int sum = 0;
-      for (int q = 0; q < per; ++q) sum += s_hist[tid * per + q];
-      int total;
-      int above = block_sum_before(sum, s_sums, &total);
-      above = total - above - sum;  // keys in bins past this thread's
-      for (int q = per - 1; q >= 0; --q) {
-        const int h = s_hist[tid * per + q];
-        if (above < need && need <= above + h) {
-          s_bin = tid * per + q;
-          s_above = above;
-          s_in = h;
-        }
-        above += h;
+      int h[kEvictBins / kEvictMinThreads], sum = 0;
+#pragma unroll
+      for (int q = 0; q < kEvictBins / kEvictMinThreads; ++q) h[q] = 0;
+      for (int r = 0; r < ranks; ++r) {
+        const EvictShared* o = of_rank(r);
+#pragma unroll
+        for (int q = 0; q < kEvictBins / kEvictMinThreads; ++q)
+          if (q < per) h[q] += o->hist[tid * per + q];
       }
-      __syncthreads();
-      lo += (uint32_t)s_bin << shift;
-      hi = min(hi, lo + ((1u << shift) - 1u));
-      need -= s_above;
-      const int in = s_in;
-      if (in <= T && lo != hi) {
-        for (int i = tid; i < L; i += T) {
-          const uint32_t k = key_at(i);
-          if (k >= lo && k <= hi) s_list[atomicAdd(&s_n, 1)] = k;
+#pragma unroll
+      for (int q = 0; q < kEvictBins / kEvictMinThreads; ++q) sum += h[q];
+      int total;
+      int above = block_sum_before(sum, sh.sums, &total);
+      above = total - above - sum;
+      if (tid == 0) sh.total = total;
+#pragma unroll
+      for (int q = kEvictBins / kEvictMinThreads - 1; q >= 0; --q) {
+        if (q >= per) continue;
+        if (above < need && need <= above + h[q]) {
+          sh.bin = tid * per + q;
+          sh.above = above;
+          sh.in = h[q];
         }
-        __syncthreads();
-        if (tid < in) {
-          const uint32_t k = s_list[tid];
-          int more = 0, same = 0;
-          for (int i = 0; i < in; ++i) {
-            more += s_list[i] > k ? 1 : 0;
-            same += s_list[i] == k ? 1 : 0;
-          }
-          if (more < need && need <= more + same) {  // (every thread that has this key writes the same)
-            s_key = k;
-            s_ties = need - more;
+        above += h[q];
+      }
+      sync_all();  // (and the histograms have been read)
+      if (above_zero && sh.total < need) {  // all positive scores stay, and some of the others
+        need -= sh.total;
+        lo = 0u;
+        hi = kZeroKey;
+        above_zero = false;
+        continue;
+      }
+      above_zero = false;
+      lo += (uint32_t)sh.bin << shift;
+      hi = min(hi, lo + ((1u << shift) - 1u));
+      need -= sh.above;
+      const int in = sh.in;
+      if (in <= T && lo != hi) {
+        EvictShared* o = of_rank(0);
+        const uint32_t width = hi - lo;
+#pragma unroll 4
+        for (int j = tid; j < own; j += T) {
+          const uint32_t k = s_keys[j];
+          if (k - lo <= width) o->list[atomicAdd(&o->n, 1)] = k;
+        }
+        sync_all();
+        if (rank == 0) {  // a warp a key
+          for (int c = tid >> 5; c < in; c += T >> 5) {
+            const uint32_t k = sh.list[c];
+            int more = 0, same = 0;
+            for (int i = lane; i < in; i += 32) {
+              more += sh.list[i] > k ? 1 : 0;
+              same += sh.list[i] == k ? 1 : 0;
+            }
+            more = __reduce_add_sync(kFullMask, more);
+            same = __reduce_add_sync(kFullMask, same);
+            if (lane < ranks && more < need && need <= more + same) {  // (every warp that has this key writes the same)
+              EvictShared* to = of_rank(lane);
+              to->key = k;
+              to->ties = need - more;
+              to->cut = need < more + same ? 1 : 0;
+            }
           }
         }
         break;
       }
     }
   }
-  __syncthreads();
-  const uint32_t last = s_key;
-  const int ties = s_ties;
+  sync_all();
+  const uint32_t last = sh.key;
+  const int ties = sh.ties;
 
-  // ---- the moves: a thread has a run of slots (of an odd length, which spreads the banks)
-  const int run = ((L + T - 1) / T) | 1;
-  const int i0 = min(tid * run, L), i1 = min(i0 + run, L);
-  int equal = 0;
-  for (int i = i0; i < i1; ++i) equal += key_at(i) == last ? 1 : 0;
-  int total;
-  const int equal0 = block_sum_before(equal, s_sums, &total);
-  int2* moves = a.moves + (size_t)bg * a.budget;
-  int seen = equal0, to = 0, from = 0;
-  for (int i = i0; i < i1; ++i) {
-    const uint32_t k = key_at(i);
-    const bool keep = k > last || (k == last && seen < ties);
-    seen += k == last ? 1 : 0;
-    to += !keep && i < a.budget ? 1 : 0;
-    from += keep && i >= a.budget ? 1 : 0;
+  // ---- the moves: a warp has a run of up to 32 words of 32 slots, a word a lane
+  const int warp = tid >> 5, warps = T >> 5;
+  const int run = ((own + warps - 1) / warps + 31) & ~31;  // (at most 1024: kEvictSlots)
+  const int j0 = min(warp * run, own), j1 = min(j0 + run, own), n_words = (j1 - j0 + 31) >> 5;
+  const uint32_t below = (1u << lane) - 1u;
+  const bool cut = sh.cut != 0;
+  int before = 0;  // equal keys before this warp's slots, where only some of them stay
+  if (cut) {
+    int equal = 0, total;
+#pragma unroll 4
+    for (int j = j0 + lane; j < j1; j += 32) equal += s_keys[j] == last ? 1 : 0;
+    equal = __reduce_add_sync(kFullMask, equal);
+    before = block_sum_before(lane == 0 ? equal : 0, sh.sums, &total);
+    before = __shfl_sync(kFullMask, before, 0);
+    if constexpr (CLUSTER) {
+      if (tid == 0) sh.equal = total;
+      sync_all();
+      for (int r = 0; r < rank; ++r) before += of_rank(r)->equal;
+    }
   }
-  int n;
-  to = block_sum_before(to, s_sums, &total);
-  from = block_sum_before(from, s_sums, &n);
-  seen = equal0;
-  for (int i = i0; i < i1; ++i) {
-    const uint32_t k = key_at(i);
-    const bool keep = k > last || (k == last && seen < ties);
-    seen += k == last ? 1 : 0;
-    if (!keep && i < a.budget) moves[to++].y = i;
-    if (keep && i >= a.budget) moves[from++].x = i;
+  auto sum_to_lane = [&](int v) {  // over the lanes up to this one
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int t = __shfl_up_sync(kFullMask, v, o);
+      if (lane >= o) v += t;
+    }
+    return v;
+  };
+  uint32_t stay = 0u;  // the lane's word: slots that stay
+  if (!cut) {
+#pragma unroll 4
+    for (int t = 0; t < n_words; ++t) {
+      const int j = j0 + 32 * t + lane;
+      const uint32_t m = __ballot_sync(kFullMask, j < j1 && s_keys[min(j, own - 1)] >= last);
+      stay = lane == t ? m : stay;
+    }
+  } else {
+    uint32_t same = 0u;
+#pragma unroll 4
+    for (int t = 0; t < n_words; ++t) {
+      const int j = j0 + 32 * t + lane;
+      const uint32_t k = s_keys[min(j, own - 1)];
+      const uint32_t m = __ballot_sync(kFullMask, j < j1 && k > last), e = __ballot_sync(kFullMask, j < j1 && k == last);
+      stay = lane == t ? m : stay;
+      same = lane == t ? e : same;
+    }
+    int take = ties - (before + sum_to_lane(__popc(same)) - __popc(same));  // of this word's equal keys, the lowest
+    if (take <= 0) {
+      same = 0u;
+    } else if (take < __popc(same)) {
+      uint32_t rest = same;
+      for (; take > 0; --take) rest &= rest - 1u;
+      same &= ~rest;
+    }
+    stay |= same;
   }
-  if (tid == 0) a.count[bg] = n;
-
-  // ---- scores and positions: those that stay, those that move, then the slots behind
-  for (int i = tid; i < a.budget; i += T) {
-    if (scores_out != scores) scores_out[i] = scores[i];
-    pos_out[i] = position(i);
+  const int w0 = j0 + 32 * lane;  // the word's first slot
+  const int low = max(0, min(min(32, j1 - w0), a.budget - first - w0));
+  const uint32_t front = low == 32 ? kFullMask : (1u << low) - 1u;
+  const uint32_t gone = front & ~stay, late = stay & ~front;  // slots that are filled, slots that go there
+  const int to_upto = sum_to_lane(__popc(gone)), from_upto = sum_to_lane(__popc(late));
+  int to = __shfl_sync(kFullMask, to_upto, 31), from = __shfl_sync(kFullMask, from_upto, 31);
+  int n_to, n_from;
+  to = __shfl_sync(kFullMask, block_sum_before(lane == 0 ? to : 0, sh.sums, &n_to), 0);
+  from = __shfl_sync(kFullMask, block_sum_before(lane == 0 ? from : 0, sh.sums, &n_from), 0);
+  int to0 = 0, from0 = 0, n = n_from;  // places of this CTA's first ones, and all moves
+  if constexpr (CLUSTER) {
+    if (tid == 0) {
+      sh.to = n_to;
+      sh.from = n_from;
+    }
+    sync_all();
+    n = 0;
+    for (int r = 0; r < ranks; ++r) {
+      const EvictShared* o = of_rank(r);
+      if (r < rank) {
+        to0 += o->to;
+        from0 += o->from;
+      }
+      n += o->from;
+    }
+  }
+  if (tid == 0 && rank == 0) a.count[bg] = n;
+  // The CTA's slots as lists, in place of the keys; then all that the rows' kernel needs of them.  (That kernel joins
+  // the two lists: a CTA writes its own part of each and reads no other's.)
+  int* s_to = reinterpret_cast<int*>(s_keys);
+  int* s_from = s_to + n_to;  // (n_to + n_from <= own)
+  __syncthreads();            // the keys have been read
+#pragma unroll 2
+  for (int t = 0; t < n_words; ++t) {
+    const uint32_t g = __shfl_sync(kFullMask, gone, t), l = __shfl_sync(kFullMask, late, t);
+    const int g1 = __shfl_sync(kFullMask, to_upto, t), l1 = __shfl_sync(kFullMask, from_upto, t);
+    const int i = first + j0 + 32 * t + lane;
+    if ((g >> lane) & 1u) s_to[to + g1 - __popc(g & ~below)] = i;
+    if ((l >> lane) & 1u) s_from[from + l1 - __popc(l & ~below)] = i;
   }
   __syncthreads();
-  for (int j = tid; j < n; j += T) {
-    const int2 m = moves[j];
-    scores_out[m.y] = scores[m.x];
-    pos_out[m.y] = position(m.x);
+  const int32_t* bt = a.block_tables + (size_t)b * a.MB;
+  auto pool_slot = [&](int i, int blk) {
+    if (blk >= 0 && blk < a.NB) return blk * 16 + (i & 15);
+    record_error(a.err, PKV_DEV_BAD_BLOCK_ID);
+    return -1;
+  };
+  int4* moves = a.moves + (size_t)bg * a.budget;
+  int32_t* to_slot = a.to_slot + (size_t)bg * a.budget;
+  for (int m0 = tid; m0 < max(n_to, n_from); m0 += kMoveBatch * T) {
+    int i[kMoveBatch], j[kMoveBatch], blk_i[kMoveBatch], blk_j[kMoveBatch], p[kMoveBatch];
+    float x[kMoveBatch];
+#pragma unroll
+    for (int q = 0; q < kMoveBatch; ++q) {
+      const int m = m0 + q * T;
+      if (m < n_from) {
+        i[q] = s_from[m];
+        x[q] = scores[i[q]];
+        p[q] = slot_pos[i[q]];
+        blk_i[q] = bt[i[q] >> 4];
+      }
+      if (m < n_to) {
+        j[q] = s_to[m];
+        blk_j[q] = bt[j[q] >> 4];
+      }
+    }
+#pragma unroll
+    for (int q = 0; q < kMoveBatch; ++q) {
+      const int m = m0 + q * T;
+      if (m < n_from) {
+        int4* at = moves + from0 + m;
+        at->x = pool_slot(i[q], blk_i[q]);
+        at->z = __float_as_int(x[q]);
+        at->w = place(p[q], i[q]);
+      }
+      if (m < n_to) {
+        moves[to0 + m].y = pool_slot(j[q], blk_j[q]);
+        to_slot[to0 + m] = j[q];
+      }
+    }
   }
-  __syncthreads();
-  for (int i = a.budget + tid; i < L; i += T) {
+  // ---- scores and positions: of the slots below the budget (those that are filled get theirs with the rows), and past it
+  const int mid = min(end, a.budget);
+  for (int i0 = first + tid; i0 < mid; i0 += kEvictBatch * T) {
+    float x[kEvictBatch];
+    int p[kEvictBatch];
+#pragma unroll
+    for (int q = 0; q < kEvictBatch; ++q) {
+      const int i = i0 + q * T;
+      if (i < mid) {
+        x[q] = scores[i];
+        p[q] = slot_pos[i];
+      }
+    }
+#pragma unroll
+    for (int q = 0; q < kEvictBatch; ++q) {
+      const int i = i0 + q * T;
+      if (i < mid) {
+        scores_out[i] = x[q];
+        pos_out[i] = place(p[q], i);
+      }
+    }
+  }
+  sync_all();  // the moved slots' values, and (a cluster) the counts, have been read
+  for (int i = max(first, a.budget) + tid; i < end; i += T) {
     scores_out[i] = 0.f;
     pos_out[i] = -1;
   }
@@ -363,7 +569,7 @@ __device__ __forceinline__ void evict_tables(const EvictArgs& a) {
 // RB: bytes of a row; SCALES: INT8 pools.  A warp takes 2 KB of K rows and as much of V at a time: lanes find the rows,
 // then every lane has eight 16-byte loads in flight before it stores.
 template <int RB, bool SCALES>
-__global__ void __launch_bounds__(kMoveThreads) evict_move_kernel(const EvictArgs a) {
+__global__ void __launch_bounds__(kMoveThreads, 3) evict_move_kernel(const EvictArgs a) {
   constexpr int CPR = RB / 16, NR = 128 / CPR;  // 16-byte pieces of a row; rows of a warp at a time
   static_assert(NR <= 32 && NR * CPR == 4 * 32, "four pieces of K and of V a lane");
   grid_dependency_wait();
@@ -374,22 +580,22 @@ __global__ void __launch_bounds__(kMoveThreads) evict_move_kernel(const EvictArg
   }
   const int item = (int)blockIdx.x - 1;
   const int bg = item / a.splits, part = item - bg * a.splits;
-  const int b = bg / a.Hkv, g = bg - b * a.Hkv;
+  const int g = bg % a.Hkv;
   const int n = a.count[bg], lane = threadIdx.x & 31;
-  const int2* moves = a.moves + (size_t)bg * a.budget;
+  const int4* moves = a.moves + (size_t)bg * a.budget;
+  const int32_t* to_slot = a.to_slot + (size_t)bg * a.budget;
   constexpr int kWarps = kMoveThreads / 32;
   for (int j0 = (part * kWarps + (int)(threadIdx.x >> 5)) * NR; j0 < n; j0 += a.splits * kWarps * NR) {
     long long src = -1, dst = -1;  // pool rows of this lane's move
     if (lane < NR && j0 + lane < n) {
-      const int2 m = moves[j0 + lane];
-      const int32_t* bt = a.block_tables + (size_t)b * a.MB;
-      const int from = bt[m.x >> 4], to = bt[m.y >> 4];
-      if (from < 0 || from >= a.NB || to < 0 || to >= a.NB) {
-        record_error(a.err, PKV_DEV_BAD_BLOCK_ID);
-      } else {
-        src = ((long long)from * a.Hkv + g) * 16 + (m.x & 15);
-        dst = ((long long)to * a.Hkv + g) * 16 + (m.y & 15);
+      const int4 m = moves[j0 + lane];
+      const size_t slot = (size_t)bg * a.st.stride + to_slot[j0 + lane];
+      if (m.x >= 0 && m.y >= 0) {
+        src = ((long long)(m.x >> 4) * a.Hkv + g) * 16 + (m.x & 15);
+        dst = ((long long)(m.y >> 4) * a.Hkv + g) * 16 + (m.y & 15);
       }
+      a.st.scores_out[slot] = __int_as_float(m.z);
+      a.st.slot_pos_out[slot] = m.w;
     }
     uint4 kb[4], vb[4];
     long long at[4];
@@ -423,12 +629,37 @@ __global__ void __launch_bounds__(kMoveThreads) evict_move_kernel(const EvictArg
   }
 }
 
-// Keys that shared memory holds; a longer row's others are worked out again from memory at each pass.
-constexpr int kEvictCachedKeys = 49152;
+// CTAs of a row: as many as the SMs hold at once, of 4096 slots at least, and more where a CTA cannot have them all.
+// Threads: as many as leave all CTAs on the SMs at once (64 registers each), of eight slots at least.
+cudaError_t launch_select(const EvictArgs& a, int pairs, int longest, int sms, cudaStream_t stream) {
+  EvictArgs args = a;
+  int ranks = 1;
+  while (ranks < 8 && ((pairs * 2 * ranks <= sms && longest / (2 * ranks) >= 4096) || longest > ranks * kEvictSlots)) ranks *= 2;
+  const int most = (longest + ranks - 1) / ranks;
+  int threads = kEvictMinThreads;
+  while (threads < kEvictMaxThreads && most > 8 * threads &&
+         (pairs * ranks <= sms * (kEvictMaxThreads / (2 * threads)) || most > 32 * threads))
+    threads *= 2;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3((unsigned)pairs * (unsigned)ranks);
+  cfg.blockDim = dim3(threads);
+  cfg.dynamicSmemBytes = sizeof(uint32_t) * (size_t)most;
+  cfg.stream = stream;
+  cudaLaunchAttribute attr[2];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  attr[1].id = cudaLaunchAttributeClusterDimension;
+  attr[1].val.clusterDim.x = (unsigned)ranks;
+  attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = ranks > 1 ? 2 : 1;
+  void* params[] = {&args};
+  return cudaLaunchKernelExC(&cfg, ranks > 1 ? (const void*)evict_select_kernel<true> : (const void*)evict_select_kernel<false>, params);
+}
 
 size_t align256e(size_t x) { return (x + 255) & ~size_t(255); }
 
-// int32 counts | int2 moves
+// int32 counts | int4 moves | int32 slots
 size_t evict_moves_offset(const pkv_dims* d) {
   return align256e(sizeof(int32_t) * (size_t)d->batch * d->num_kv_heads);
 }
@@ -441,10 +672,10 @@ int check_evict(const pkv_dims* d, const pkv_evict_rules* r) {
   if (r->n_sink < 0 || r->k_top < 0 || r->n_recent < 0) return PKV_ERR_ARGUMENT;
   const long long budget = (long long)r->n_sink + r->k_top + r->n_recent;
   if (budget >= (1ll << 30)) return PKV_ERR_ARGUMENT;
-  // table entries, slots of one sequence, and (sequence, kv head) pairs are counted in 32 bits
+  // table entries, slots of one sequence and of the pool, and (sequence, kv head) pairs are counted in 32 bits
   if ((long long)d->batch * d->max_blocks_per_seq >= (1ll << 30) ||
       (long long)d->max_blocks_per_seq * PKV_BLOCK_SIZE >= (1ll << 30) ||
-      (long long)d->batch * d->num_kv_heads >= (1ll << 24))
+      (long long)d->batch * d->num_kv_heads >= (1ll << 24) || d->num_blocks >= (1 << 27))
     return PKV_ERR_DIMS;
   return PKV_OK;
 }
@@ -501,17 +732,14 @@ int evict_common(void* k, void* v, float* ks, float* vs, const int32_t* block_ta
   a.trigger = std::max(rules->trigger, a.budget);
   unsigned char* ws = static_cast<unsigned char*>(workspace);
   a.count = reinterpret_cast<int32_t*>(ws);
-  a.moves = reinterpret_cast<int2*>(ws + evict_moves_offset(dims));
-  const int longest = std::min(state->stride, a.MB * PKV_BLOCK_SIZE);  // cached tokens at most
+  a.moves = reinterpret_cast<int4*>(ws + evict_moves_offset(dims));
   const int pairs = a.B * a.Hkv;
+  a.to_slot = reinterpret_cast<int32_t*>(a.moves + (size_t)a.budget * pairs);
+  const int longest = std::min({state->stride, a.MB * PKV_BLOCK_SIZE, PKV_MAX_EVICT_TOKENS});  // cached tokens at most
   cudaStream_t cu = static_cast<cudaStream_t>(stream);
   const int RB = q8 ? dims->head_dim : 2 * dims->head_dim;
   if (pairs > 0) {
-    a.cached = std::min(longest, kEvictCachedKeys);
-    const int threads = longest > 4096 ? 1024 : longest > 1024 ? 512 : 256;
-    void* params[] = {&a};
-    const cudaError_t e = launch_pdl((const void*)evict_select_kernel, dim3((unsigned)pairs), dim3(threads),
-                                     sizeof(uint32_t) * (size_t)a.cached, cu, params);
+    const cudaError_t e = launch_select(a, pairs, longest, sms, cu);
     if (e != cudaSuccess) return cuda_status(e);
   }
   // CTAs for the rows of a pair: a warp's share each where that is not too many in all
@@ -528,8 +756,10 @@ int evict_common(void* k, void* v, float* ks, float* vs, const int32_t* block_ta
 }  // namespace
 
 cudaError_t evict_device_setup() {
-  return cudaFuncSetAttribute((const void*)evict_select_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                              (int)(sizeof(uint32_t) * kEvictCachedKeys));
+  const int bytes = (int)(sizeof(uint32_t) * kEvictSlots);
+  cudaError_t e = cudaFuncSetAttribute((const void*)evict_select_kernel<false>, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+  if (e == cudaSuccess) e = cudaFuncSetAttribute((const void*)evict_select_kernel<true>, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+  return e;
 }
 
 }  // namespace pkv
@@ -541,7 +771,7 @@ extern "C" {
 size_t pkv_evict_workspace_bytes(const pkv_dims* dims, const pkv_evict_rules* rules) {
   if (check_evict(dims, rules) != PKV_OK) return 0;
   const size_t budget = (size_t)rules->n_sink + rules->k_top + rules->n_recent;
-  return align256e(evict_moves_offset(dims) + sizeof(int2) * budget * dims->batch * dims->num_kv_heads + 1);
+  return align256e(evict_moves_offset(dims) + (sizeof(int4) + sizeof(int32_t)) * budget * dims->batch * dims->num_kv_heads + 1);
 }
 
 int pkv_kv_evict(void* k_cache, void* v_cache, const int32_t* block_tables, const int32_t* context_lens,

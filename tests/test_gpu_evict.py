@@ -157,6 +157,43 @@ def test_rows_past_shared_memory(q8):
 
 
 @pytest.mark.gpu
+@pytest.mark.parametrize("scores", ["exp", "few"])
+def test_the_longest_row(scores):
+    most = C["PKV_MAX_EVICT_TOKENS"]
+    s = _state([most], 1, 64, most // 16 + 3, 18, scores=scores)
+    _check(s, _call(s, 4, 70001, 77), 4, 70001, 77)
+
+
+@pytest.mark.gpu
+def test_a_row_past_the_longest_is_refused():
+    most = C["PKV_MAX_EVICT_TOKENS"]
+    s = _state([most + 1, 500], 1, 64, most // 16 + 3, 18)
+    err = pkv.new_error_word(DEV)
+    got = _call(s, 4, 300, 77, err=err)
+    assert pkv.read_error(err) == C["PKV_DEV_BAD_CONTEXT_LEN"]
+    assert got[1].tolist() == [most + 1, 381] and got[4].tolist() == [0, 119]
+    assert (got[2][0] == 77.0).all() and (got[3][0] == -77).all()
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("lens", [[300, 290], [2000, 1999, 1733], [30011]])
+def test_a_small_part_of_a_large_pool(lens):
+    """Block ids far past the lengths: the lists of moves hold slots of the sequence, then slots of the pool."""
+    s = _state(lens, 1, 64, max(lens) // 16 + 1, 21, extra=20000)
+    for rules in ((4, 30, 41), (0, 137, 0)):
+        _check(s, _call(s, *rules), *rules)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("lens", [[20000, 9001], [33000], [8192, 8191, 16400, 4000]])
+@pytest.mark.parametrize("scores", ["exp", "few", "zero", "odd"])
+def test_rows_shared_by_clusters(lens, scores):
+    s = _state(lens, 2, 64, max(lens) // 16 + 1, 19, scores=scores)
+    for rules in ((4, 2000, 500), (0, 7999, 0)):
+        _check(s, _call(s, *rules, inplace=True), *rules, inplace=True)
+
+
+@pytest.mark.gpu
 def test_many_sequences():
     rng = np.random.default_rng(6)
     lens = rng.integers(0, 90, 700).tolist()
@@ -439,7 +476,7 @@ def test_host_validation_codes(lib):
     assert call(r=rules(a=-1)) == call(r=rules(b=-1)) == call(r=rules(c=-1)) == C["PKV_ERR_ARGUMENT"]
     assert call(r=rules(b=2**30)) == call(r=rules(2**29, 2**29, 0)) == C["PKV_ERR_ARGUMENT"]
     assert call(d=dims(B=4097)) == call(d=dims(B=-1)) == call(d=dims(mb=1 << 28)) == call(d=dims(hkv=0)) == C["PKV_ERR_DIMS"]
-    assert call(d=dims(hkv=1 << 23)) == call(st=state(stride=-1)) == C["PKV_ERR_DIMS"]
+    assert call(d=dims(hkv=1 << 23)) == call(d=dims(nb=1 << 27)) == call(st=state(stride=-1)) == C["PKV_ERR_DIMS"]
     assert call(d=dims(bs=8)) == C["PKV_ERR_BLOCK_SIZE"] and call(d=dims(d=96)) == C["PKV_ERR_HEAD_DIM"]
     for kw in (dict(k=None), dict(bt=None), dict(count=None), dict(st=state(sc=None)), dict(st=state(po=None)), dict(st=state(gone=None))):
         assert call(**kw) == C["PKV_ERR_NULL_POINTER"], kw
