@@ -41,6 +41,7 @@ struct EvictArgs {
   int32_t* to_slot;              // [B * Hkv, budget] the slot that each goes to
   int B, Hkv, NB, MB;
   int n_sink, n_recent, budget, trigger;
+  int wide;                      // 1: rows of scores and slot_pos may be read four slots at a time
   int splits;                    // CTAs that share the moves of one (sequence, kv head)
 };
 
@@ -96,7 +97,7 @@ __device__ __forceinline__ int block_sum_before(int v, int* sums, int* total) {
 
 constexpr int kEvictBins = 2048;
 constexpr int kEvictMinThreads = 256, kEvictMaxThreads = 1024;
-constexpr int kEvictBatch = 8;  // slots whose loads a thread has in flight
+constexpr int kEvictBatch = 8, kEvictWide = 4;  // loads of slots, and of four of them, that a thread has in flight
 constexpr int kMoveBatch = 4;   // likewise, moves
 constexpr int kEvictSlots = 32768;  // of a CTA at most: 32 words of 32 for each of 32 warps
 static_assert(PKV_MAX_EVICT_TOKENS == 8 * kEvictSlots, "a cluster of eight");
@@ -122,7 +123,7 @@ struct EvictShared {
 template <bool CLUSTER>
 __global__ void __launch_bounds__(kEvictMaxThreads, 1) evict_select_kernel(const EvictArgs a) {
   namespace cg = cooperative_groups;
-  extern __shared__ uint32_t s_keys[];  // of this CTA's slots
+  extern __shared__ __align__(16) uint32_t s_keys[];  // of this CTA's slots, a multiple of four
   __shared__ EvictShared sh;
   cg::cluster_group cluster = cg::this_cluster();
   const int ranks = CLUSTER ? (int)cluster.num_blocks() : 1, rank = CLUSTER ? (int)cluster.block_rank() : 0;
@@ -161,7 +162,7 @@ __global__ void __launch_bounds__(kEvictMaxThreads, 1) evict_select_kernel(const
   __syncthreads();
   const int recent0 = s.L + s.dropped - a.n_recent;  // (n_recent <= budget < L)
   // this CTA's slots
-  const int chunk = (s.L + ranks - 1) / ranks, first = min(rank * chunk, s.L), end = min(first + chunk, s.L), own = end - first;
+  const int chunk = ((s.L + ranks - 1) / ranks + 3) & ~3, first = min(rank * chunk, s.L), end = min(first + chunk, s.L), own = end - first;
   auto place = [&](int p, int i) { return p >= 0 ? p : i + s.dropped; };
   auto make_key = [&](int p, int i, float score) {
     p = place(p, i);
@@ -177,36 +178,53 @@ __global__ void __launch_bounds__(kEvictMaxThreads, 1) evict_select_kernel(const
     const int32_t* sp = slot_pos + first;
     auto take = [&](int j, float x, int p) {
       const uint32_t k = make_key(p, first + j, x);
-      s_keys[j] = k;
       nan |= k == 0u;
       guarded += k == kProtectedKey ? 1 : 0;
       least = min(least, k - (kZeroKey + 1u));  // (keys up to that of zero wrap to the end)
       most = max(most, k + 1u);                 // (the protected one wraps to 0)
+      return k;
     };
-    int j0 = tid;
-    for (; j0 + (kEvictBatch - 1) * T < own; j0 += kEvictBatch * T) {
-      float x[kEvictBatch];
-      int p[kEvictBatch];
+    if (a.wide) {  // four slots a load (those past the end lie within the row)
+      for (int v0 = tid; v0 < (own + 3) >> 2; v0 += kEvictWide * T) {
+        float4 x[kEvictWide];
+        int4 p[kEvictWide];
 #pragma unroll
-      for (int q = 0; q < kEvictBatch; ++q) {
-        x[q] = sc[j0 + q * T];
-        p[q] = sp[j0 + q * T];
+        for (int q = 0; q < kEvictWide; ++q) {
+          const int v = v0 + q * T;
+          if (4 * v < own) {
+            x[q] = reinterpret_cast<const float4*>(sc)[v];
+            p[q] = reinterpret_cast<const int4*>(sp)[v];
+          }
+        }
+#pragma unroll
+        for (int q = 0; q < kEvictWide; ++q) {
+          const int j = 4 * (v0 + q * T);
+          if (j >= own) continue;
+          uint4 k;
+          k.x = take(j, x[q].x, p[q].x);
+          k.y = j + 1 < own ? take(j + 1, x[q].y, p[q].y) : kProtectedKey;
+          k.z = j + 2 < own ? take(j + 2, x[q].z, p[q].z) : kProtectedKey;
+          k.w = j + 3 < own ? take(j + 3, x[q].w, p[q].w) : kProtectedKey;
+          reinterpret_cast<uint4*>(s_keys)[j >> 2] = k;
+        }
       }
+    } else {
+      for (int j0 = tid; j0 < own; j0 += kEvictBatch * T) {
+        float x[kEvictBatch];
+        int p[kEvictBatch];
 #pragma unroll
-      for (int q = 0; q < kEvictBatch; ++q) take(j0 + q * T, x[q], p[q]);
-    }
-    if (j0 < own) {
-      float x[kEvictBatch];
-      int p[kEvictBatch];
+        for (int q = 0; q < kEvictBatch; ++q) {
+          if (j0 + q * T < own) {
+            x[q] = sc[j0 + q * T];
+            p[q] = sp[j0 + q * T];
+          }
+        }
 #pragma unroll
-      for (int q = 0; q < kEvictBatch; ++q) {
-        const int j = min(j0 + q * T, own - 1);
-        x[q] = sc[j];
-        p[q] = sp[j];
+        for (int q = 0; q < kEvictBatch; ++q)
+          if (j0 + q * T < own) s_keys[j0 + q * T] = take(j0 + q * T, x[q], p[q]);
       }
-#pragma unroll
-      for (int q = 0; q < kEvictBatch; ++q)
-        if (j0 + q * T < own) take(j0 + q * T, x[q], p[q]);
+      // (the passes below read four keys at a time; a protected one is not counted there)
+      if (tid < (-own & 3)) s_keys[own + tid] = kProtectedKey;
     }
     least = __reduce_min_sync(kFullMask, least);
     most = __reduce_max_sync(kFullMask, most);
@@ -258,10 +276,14 @@ __global__ void __launch_bounds__(kEvictMaxThreads, 1) evict_select_kernel(const
       for (int i = tid; i < kEvictBins; i += T) sh.hist[i] = 0;
       if (tid == 0) sh.n = 0;
       __syncthreads();
-#pragma unroll 4
-      for (int j = tid; j < own; j += T) {
-        const uint32_t k = s_keys[j] - lo;
-        if (k <= range) atomicAdd(&sh.hist[k >> shift], 1);
+      const uint4* keys4 = reinterpret_cast<const uint4*>(s_keys);
+#pragma unroll 2
+      for (int v = tid; v < (own + 3) >> 2; v += T) {
+        const uint4 k = keys4[v];
+        if (k.x - lo <= range) atomicAdd(&sh.hist[(k.x - lo) >> shift], 1);
+        if (k.y - lo <= range) atomicAdd(&sh.hist[(k.y - lo) >> shift], 1);
+        if (k.z - lo <= range) atomicAdd(&sh.hist[(k.z - lo) >> shift], 1);
+        if (k.w - lo <= range) atomicAdd(&sh.hist[(k.w - lo) >> shift], 1);
       }
       sync_all();
       // a thread's bins of the whole row, and the keys in the bins past them
@@ -269,11 +291,19 @@ __global__ void __launch_bounds__(kEvictMaxThreads, 1) evict_select_kernel(const
       int h[kEvictBins / kEvictMinThreads], sum = 0;
 #pragma unroll
       for (int q = 0; q < kEvictBins / kEvictMinThreads; ++q) h[q] = 0;
-      for (int r = 0; r < ranks; ++r) {
-        const EvictShared* o = of_rank(r);
+      if constexpr (CLUSTER) {
+#pragma unroll
+        for (int r = 0; r < 8; ++r) {
+          if (r >= ranks) break;
+          const EvictShared* o = of_rank(r);
+#pragma unroll
+          for (int q = 0; q < kEvictBins / kEvictMinThreads; ++q)
+            if (q < per) h[q] += o->hist[tid * per + q];
+        }
+      } else {
 #pragma unroll
         for (int q = 0; q < kEvictBins / kEvictMinThreads; ++q)
-          if (q < per) h[q] += o->hist[tid * per + q];
+          if (q < per) h[q] = sh.hist[tid * per + q];
       }
 #pragma unroll
       for (int q = 0; q < kEvictBins / kEvictMinThreads; ++q) sum += h[q];
@@ -307,10 +337,16 @@ __global__ void __launch_bounds__(kEvictMaxThreads, 1) evict_select_kernel(const
       if (in <= T && lo != hi) {
         EvictShared* o = of_rank(0);
         const uint32_t width = hi - lo;
-#pragma unroll 4
-        for (int j = tid; j < own; j += T) {
-          const uint32_t k = s_keys[j];
+        auto list = [&](uint32_t k) {
           if (k - lo <= width) o->list[atomicAdd(&o->n, 1)] = k;
+        };
+#pragma unroll 2
+        for (int v = tid; v < (own + 3) >> 2; v += T) {
+          const uint4 k = keys4[v];
+          list(k.x);
+          list(k.y);
+          list(k.z);
+          list(k.w);
         }
         sync_all();
         if (rank == 0) {  // a warp a key
@@ -569,7 +605,7 @@ __device__ __forceinline__ void evict_tables(const EvictArgs& a) {
 // RB: bytes of a row; SCALES: INT8 pools.  A warp takes 2 KB of K rows and as much of V at a time: lanes find the rows,
 // then every lane has eight 16-byte loads in flight before it stores.
 template <int RB, bool SCALES>
-__global__ void __launch_bounds__(kMoveThreads, 3) evict_move_kernel(const EvictArgs a) {
+__global__ void __launch_bounds__(kMoveThreads, 4) evict_move_kernel(const EvictArgs a) {
   constexpr int CPR = RB / 16, NR = 128 / CPR;  // 16-byte pieces of a row; rows of a warp at a time
   static_assert(NR <= 32 && NR * CPR == 4 * 32, "four pieces of K and of V a lane");
   grid_dependency_wait();
@@ -585,46 +621,58 @@ __global__ void __launch_bounds__(kMoveThreads, 3) evict_move_kernel(const Evict
   const int4* moves = a.moves + (size_t)bg * a.budget;
   const int32_t* to_slot = a.to_slot + (size_t)bg * a.budget;
   constexpr int kWarps = kMoveThreads / 32;
-  for (int j0 = (part * kWarps + (int)(threadIdx.x >> 5)) * NR; j0 < n; j0 += a.splits * kWarps * NR) {
-    long long src = -1, dst = -1;  // pool rows of this lane's move
-    if (lane < NR && j0 + lane < n) {
-      const int4 m = moves[j0 + lane];
-      const size_t slot = (size_t)bg * a.st.stride + to_slot[j0 + lane];
-      if (m.x >= 0 && m.y >= 0) {
-        src = ((long long)(m.x >> 4) * a.Hkv + g) * 16 + (m.x & 15);
-        dst = ((long long)(m.y >> 4) * a.Hkv + g) * 16 + (m.y & 15);
-      }
-      a.st.scores_out[slot] = __int_as_float(m.z);
-      a.st.slot_pos_out[slot] = m.w;
+  const int step = a.splits * kWarps * NR;
+  int j0 = (part * kWarps + (int)(threadIdx.x >> 5)) * NR;
+  // the lane's move of the NR at j (none: slots of -1), on its way while the rows before it are copied
+  int4 m;
+  int slot;
+  auto fetch = [&](int j) {
+    m = make_int4(-1, -1, 0, 0);
+    slot = -1;
+    if (lane < NR && j + lane < n) {
+      m = moves[j + lane];
+      slot = to_slot[j + lane];
+    }
+  };
+  // 16-byte piece c % CPR of the row of a slot
+  auto piece = [&](int s, int c) { return (((size_t)(s >> 4) * a.Hkv + g) * 16 + (s & 15)) * RB + (c % CPR) * 16; };
+  fetch(j0);
+  for (; j0 < n; j0 += step) {
+    const bool live = m.x >= 0 && m.y >= 0;
+    const int src = live ? m.x : -1, dst = m.y;
+    if (slot >= 0) {
+      a.st.scores_out[(size_t)bg * a.st.stride + slot] = __int_as_float(m.z);
+      a.st.slot_pos_out[(size_t)bg * a.st.stride + slot] = m.w;
     }
     uint4 kb[4], vb[4];
-    long long at[4];
     float ks = 0.f, vs = 0.f;
+    uint32_t have = 0u;
 #pragma unroll
     for (int q = 0; q < 4; ++q) {
-      const int c = q * 32 + lane;
-      const long long from = __shfl_sync(kFullMask, src, c / CPR);
-      at[q] = __shfl_sync(kFullMask, dst, c / CPR);
-      if (at[q] >= 0) {
-        kb[q] = reinterpret_cast<const uint4*>(a.k + from * RB)[c % CPR];
-        vb[q] = reinterpret_cast<const uint4*>(a.v + from * RB)[c % CPR];
+      const int c = q * 32 + lane, from = __shfl_sync(kFullMask, src, c / CPR);
+      if (from >= 0) {
+        have |= 1u << q;
+        kb[q] = __ldcs(reinterpret_cast<const uint4*>(a.k + piece(from, c)));
+        vb[q] = __ldcs(reinterpret_cast<const uint4*>(a.v + piece(from, c)));
       }
     }
     if (SCALES && src >= 0) {
-      ks = a.k_scales[src];
-      vs = a.v_scales[src];
+      ks = a.k_scales[piece(src, 0) / RB];
+      vs = a.v_scales[piece(src, 0) / RB];
     }
+    fetch(j0 + step);
+    // (stores that do not stay in L2: 32 rows of 4000 tokens 80.9 -> 76.9 us)
 #pragma unroll
     for (int q = 0; q < 4; ++q) {
-      const int c = q * 32 + lane;
-      if (at[q] >= 0) {
-        reinterpret_cast<uint4*>(a.k + at[q] * RB)[c % CPR] = kb[q];
-        reinterpret_cast<uint4*>(a.v + at[q] * RB)[c % CPR] = vb[q];
+      const int c = q * 32 + lane, to = __shfl_sync(kFullMask, dst, c / CPR);
+      if ((have >> q) & 1u) {
+        __stcs(reinterpret_cast<uint4*>(a.k + piece(to, c)), kb[q]);
+        __stcs(reinterpret_cast<uint4*>(a.v + piece(to, c)), vb[q]);
       }
     }
     if (SCALES && src >= 0) {
-      a.k_scales[dst] = ks;
-      a.v_scales[dst] = vs;
+      a.k_scales[piece(dst, 0) / RB] = ks;
+      a.v_scales[piece(dst, 0) / RB] = vs;
     }
   }
 }
@@ -635,7 +683,8 @@ cudaError_t launch_select(const EvictArgs& a, int pairs, int longest, int sms, c
   EvictArgs args = a;
   int ranks = 1;
   while (ranks < 8 && ((pairs * 2 * ranks <= sms && longest / (2 * ranks) >= 4096) || longest > ranks * kEvictSlots)) ranks *= 2;
-  const int most = (longest + ranks - 1) / ranks;
+  const int most = ((longest + ranks - 1) / ranks + 3) & ~3;
+  args.wide = (a.st.stride & 3) == 0 && ((reinterpret_cast<uintptr_t>(a.st.scores) | reinterpret_cast<uintptr_t>(a.st.slot_pos)) & 15u) == 0;
   int threads = kEvictMinThreads;
   while (threads < kEvictMaxThreads && most > 8 * threads &&
          (pairs * ranks <= sms * (kEvictMaxThreads / (2 * threads)) || most > 32 * threads))
@@ -745,7 +794,7 @@ int evict_common(void* k, void* v, float* ks, float* vs, const int32_t* block_ta
   // CTAs for the rows of a pair: a warp's share each where that is not too many in all
   const int per_cta = kMoveThreads / 32 * (128 * 16 / RB);
   const int most = std::max(0, std::min(a.budget, longest - a.budget));  // moves of a pair at most
-  const long long fill = pairs > 0 ? (64ll * sms + pairs - 1) / pairs : 1;
+  const long long fill = pairs > 0 ? (16ll * sms + pairs - 1) / pairs : 1;
   a.splits = (int)std::max(1ll, std::min<long long>((most + per_cta - 1) / per_cta, fill));
   const void* f = q8 ? (dims->head_dim == 128 ? (const void*)evict_move_kernel<128, true> : (const void*)evict_move_kernel<64, true>)
                      : (dims->head_dim == 128 ? (const void*)evict_move_kernel<256, false> : (const void*)evict_move_kernel<128, false>);

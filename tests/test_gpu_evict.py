@@ -194,6 +194,18 @@ def test_rows_shared_by_clusters(lens, scores):
 
 
 @pytest.mark.gpu
+@pytest.mark.parametrize("lens", [[300, 290], [2001, 1999], [20003, 17001]])
+@pytest.mark.parametrize("more", [0, 1, 2, 5])
+def test_rows_of_odd_length(lens, more):
+    """Rows of scores and positions that start anywhere."""
+    s = _state(lens, 2, 64, max(lens) // 16 + 2, 22)
+    for n in ("scores", "pos"):
+        s[n] = s[n][:, :, :max(lens) + more].copy()
+    for inplace in (False, True):
+        _check(s, _call(s, 4, 60, 41, inplace=inplace), 4, 60, 41, inplace=inplace)
+
+
+@pytest.mark.gpu
 def test_many_sequences():
     rng = np.random.default_rng(6)
     lens = rng.integers(0, 90, 700).tolist()
