@@ -21,14 +21,14 @@ constexpr int kNumHeadDims = 2;
 constexpr int kGroups[] = {1};  // every group size shares one kernel per (head_dim, mode)
 constexpr int kNumGroups = 1;
 
-constexpr int kNumModes = 11;
+constexpr int kNumModes = 13;
 
 struct DeviceInfo {
   bool ready = false;
   int sm_count = 0;
   size_t max_dyn_smem[2][kNumModes] = {};  // [head_dim index][mode: dense, sparse, dense + scores,
                                    //   dense INT8, INT8 + scores, sparse INT8, rules, FP8, FP8 + rules,
-                                   //   differential, differential + scores]:
+                                   //   differential of up to 4 heads a kv head, + scores, of more, + scores]:
                                    //   opt-in minus static shared memory
   int merge_ctas_per_sm[2] = {};   // [head_dim index]: resident merge CTAs per SM
   int diff_merge_ctas_per_sm[2] = {};  // likewise, of the differential form
@@ -64,7 +64,8 @@ const DeviceInfo* device_info(int* status) {
         for (int sp = 0; sp < kNumModes; ++sp) {
           const bool diff = sp >= 9;
           const DecodeKernel k =
-              decode_kernel(hd == 0 ? 128 : 64, kGroups[gi], sp == 1 || sp == 5, sp == 2 || sp == 4 || sp == 10,
+              decode_kernel(hd == 0 ? 128 : 64, sp >= 11 ? kMaxGroup : kGroups[gi], sp == 1 || sp == 5,
+                            sp == 2 || sp == 4 || sp == 10 || sp == 12,
                             sp >= 3 && sp != 6 && !diff, sp >= 7 && !diff, sp == 6 || sp == 8 || diff, diff);
           if (k.split == nullptr) continue;
           cudaFuncAttributes fa{};
@@ -362,7 +363,7 @@ int decode_common(void* out, const void* q, const void* k_cache, const void* v_c
   const DeviceInfo* info = device_info(&st);
   if (!info) return st;
   const size_t smem = decode_smem_bytes(dims->head_dim, sparse, dims->batch, rules != nullptr);
-  const int mode = diff ? (diff_scores ? 10 : 9) : f8 ? (rules ? 8 : 7) : rules ? 6 : sparse ? (q8 ? 5 : 1) : (q8 ? (score_out ? 4 : 3) : (score_out ? 2 : 0));
+  const int mode = diff ? (group <= 4 ? 9 : 11) + (diff_scores ? 1 : 0) : f8 ? (rules ? 8 : 7) : rules ? 6 : sparse ? (q8 ? 5 : 1) : (q8 ? (score_out ? 4 : 3) : (score_out ? 2 : 0));
   if (smem > info->max_dyn_smem[head_dim_index(dims->head_dim)][mode])
     return PKV_ERR_DIMS;
   int per_sm = 0;
@@ -454,11 +455,11 @@ int decode_common(void* out, const void* q, const void* k_cache, const void* v_c
   // score-emitting variant share one set, so their outputs agree bit for bit; the dense INT8
   // decode (issue-bound) and the gather form have their own.
   const bool dense_q8 = !sparse && q8 != nullptr;
-  a.min_units = std::max(sparse ? PKV_MIN_UNITS_SPARSE : dense_q8 ? PKV_MIN_UNITS_Q8 : PKV_MIN_UNITS, 1);
+  a.min_units = std::max(sparse ? PKV_MIN_UNITS_SPARSE : dense_q8 ? PKV_MIN_UNITS_Q8 : diff ? PKV_MIN_UNITS_DIFF : PKV_MIN_UNITS, 1);
   const int busy_pct = sparse ? (q8 != nullptr ? PKV_MIN_BUSY_PCT_SPARSE_Q8 : PKV_MIN_BUSY_PCT_SPARSE)
-                       : dense_q8 ? PKV_MIN_BUSY_PCT_Q8 : PKV_MIN_BUSY_PCT;
+                       : dense_q8 ? PKV_MIN_BUSY_PCT_Q8 : diff ? PKV_MIN_BUSY_PCT_DIFF : PKV_MIN_BUSY_PCT;
   a.min_busy_pct = std::min(std::max(busy_pct, 0), 100);
-  a.tail_pct = std::min(std::max(sparse ? PKV_TAIL_PCT_SPARSE : f8 ? PKV_TAIL_PCT_F8 : dense_q8 ? PKV_TAIL_PCT_Q8 : PKV_TAIL_PCT, 0), 50);
+  a.tail_pct = std::min(std::max(sparse ? PKV_TAIL_PCT_SPARSE : f8 ? PKV_TAIL_PCT_F8 : dense_q8 ? PKV_TAIL_PCT_Q8 : diff ? PKV_TAIL_PCT_DIFF : PKV_TAIL_PCT, 0), 50);
   a.chunk_min = std::max(dense_q8 ? PKV_CHUNK_MIN_Q8 : PKV_CHUNK_MIN, ring);  // never ends inside the tile ring
   a.cpw_cap = (int)std::min<long long>(std::min(PKV_MAX_TAIL_CHUNKS, kMaxTailChunksLimit),
                                        plan.ranges / workers - 1);

@@ -310,20 +310,29 @@ __device__ void make_partition(int32_t* p, int total, int nw, const DecodeArgs& 
     p[kPartOff + c] = cpw > 0 ? T - (int)((long long)T * ((1 << (cpw - c)) - 1) / ((1 << cpw) - 1)) : 0;
 }
 
+constexpr int kDiffPairs = 1, kDiffWide = 2;  // forms of the differential decode
+
 constexpr float kLn2 = 0.6931471805599453f;
 constexpr float kLog2e = 1.4426950408889634f;
 
 // SCORES (dense only): also keep every attended key's base-2 logit and write the log-sum-exp of
 // rows written out directly, for the score step (decode_score_kernel).
 // F8 (with Q8): the codes are E4M3 with a scale per block and kv head.  RULES (dense only): score rules.
-// DIFF (bf16, with RULES): differential attention; each head has two maps, and SCORES keeps the logits of both.
-template <int D, bool SPARSE, bool SCORES, bool Q8, bool F8 = false, bool RULES = false, bool DIFF = false>
-__global__ void __launch_bounds__(kDecodeWarps * 32, Q8 ? (F8 ? PKV_F8_MIN_CTAS : PKV_Q8_MIN_CTAS) : 0)
+// DIFF (bf16, with RULES): differential attention; each head has two maps, and SCORES keeps the logits of both.  Either way
+// the first half of a K row's k-steps goes into the first map's products and the second into the second's, so
+// nothing of one half enters the other map.
+//   kDiffPairs: up to four query heads a kv head.  Columns 2 j and 2 j + 1 of the fragments are the maps of head j, both
+//   with head j's q; a lane takes its even column from the products of the first half and its odd one from
+//   those of the second.  The softmax and the product with V are those of the plain form over eight heads.
+//   kDiffWide: up to eight; columns are heads, and each map has its own weights and outputs.
+template <int D, bool SPARSE, bool SCORES, bool Q8, bool F8 = false, bool RULES = false, int DIFF = 0>
+__global__ void __launch_bounds__(kDecodeWarps * 32, Q8 ? (F8 ? PKV_F8_MIN_CTAS : PKV_Q8_MIN_CTAS) : DIFF == kDiffWide ? PKV_DIFF_MIN_CTAS : 0)
 decode_split_kernel(const __grid_constant__ DecodeArgs a) {
   static_assert(!(SPARSE && SCORES), "scores are emitted by the dense decode only");
   static_assert(!(F8 && (SPARSE || SCORES || !Q8)) && !(RULES && (SPARSE || (SCORES && !DIFF))), "dense decode only");
   static_assert(!DIFF || (RULES && !Q8), "bf16 pools, with the rules' unit list");
   constexpr int kMaps = DIFF ? 2 : 1;
+  constexpr bool PAIRS = DIFF == kDiffPairs, WIDE = DIFF == kDiffWide;
   using GE = Geo<D, SPARSE, Q8, F8>;
   using WT = WarpTiles<D, SPARSE, Q8, F8>;
   using WB = WarpSlots<D, SPARSE, Q8, F8>;
@@ -507,7 +516,8 @@ decode_split_kernel(const __grid_constant__ DecodeArgs a) {
   // of int8 rows hands each lane its K bytes: four consecutive columns).
   uint32_t qraw[2 * KS];
   auto load_q = [&](int b, int g) {
-    if (gq < G) {
+    const int head = PAIRS ? gq >> 1 : gq;
+    if (head < G) {
       if constexpr (Q8) {
         const uint2* qw = reinterpret_cast<const uint2*>(a.q + ((size_t)b * a.Hq + (size_t)g * G + gq) * D);
 #pragma unroll
@@ -517,7 +527,7 @@ decode_split_kernel(const __grid_constant__ DecodeArgs a) {
           qraw[2 * ks + 1] = w.y;
         }
       } else {
-        const uint32_t* qw = reinterpret_cast<const uint32_t*>(a.q + ((size_t)b * a.Hq + (size_t)g * G + gq) * D);
+        const uint32_t* qw = reinterpret_cast<const uint32_t*>(a.q + ((size_t)b * a.Hq + (size_t)g * G + head) * D);
 #pragma unroll
         for (int ks = 0; ks < KS; ++ks) {
           qraw[2 * ks] = __ldg(qw + ks * 8 + tq);
@@ -731,8 +741,8 @@ decode_split_kernel(const __grid_constant__ DecodeArgs a) {
   float o[KS][4];        // O^T accumulator fragments: [m-tile][d row gq / gq+8, head h0 / h1]
   float mr0 = -INFINITY, mr1 = -INFINITY;  // running max (reference) of heads h0, h1
   float l0 = 0.f, l1 = 0.f;                // this lane's share of the running sums
-  // DIFF: the second map's accumulators, maximum and sums
-  float od[DIFF ? KS : 1][4];
+  // kDiffWide: the second map's accumulators, maximum and sums
+  float od[WIDE ? KS : 1][4];
   float nr0 = -INFINITY, nr1 = -INFINITY, n0 = 0.f, n1 = 0.f;
   int seg_b = -1, seg_g = -1;
   int seg_slot = -1;  // partial slot of the current segment, -1: written out directly
@@ -772,7 +782,54 @@ decode_split_kernel(const __grid_constant__ DecodeArgs a) {
       l0 += __shfl_xor_sync(kFullMask, l0, m);
       l1 += __shfl_xor_sync(kFullMask, l1, m);
     }
-    if constexpr (DIFF) {
+    if constexpr (PAIRS) {
+      const bool live = tq < G;
+      const size_t row = (size_t)seg_b * a.Hq + (size_t)seg_g * G + tq;
+      if (seg_slot >= 0) {
+        if (!live) return;
+#pragma unroll
+        for (int w = 0; w < 2; ++w) {
+          const size_t e = ((size_t)seg_slot * G + tq) * 2 + w;
+          float* dst = a.part_o + e * D + gq;
+#pragma unroll
+          for (int mt = 0; mt < KS; ++mt) {
+            dst[mt * 16] = o[mt][w];
+            dst[mt * 16 + 8] = o[mt][2 + w];
+          }
+          if (gq == 0) a.part_ml[e] = make_float2(w ? mr1 : mr0, w ? l1 : l0);
+        }
+        return;
+      }
+      if constexpr (SCORES) {  // base 2
+        if (live && gq < 2) a.lse[row * 2 + gq] = (gq ? l1 : l0) > 0.f ? (gq ? mr1 + log2f(l1) : mr0 + log2f(l0)) : -INFINITY;
+      }
+      const float f1 = l0 > 0.f ? 1.f / l0 : 0.f;
+      const float f2 = live && l1 > 0.f ? __ldg(a.lambdas + (size_t)seg_b * a.lambda_stride + seg_g * G + tq) / l1 : 0.f;
+      SquareSum sq;
+#pragma unroll
+      for (int mt = 0; mt < KS; ++mt) {
+        o[mt][0] = o[mt][0] * f1 - o[mt][1] * f2;
+        o[mt][2] = o[mt][2] * f1 - o[mt][3] * f2;
+        sq.add(o[mt][0]);
+        sq.add(o[mt][2]);
+      }
+      float f = 1.f;
+      if (a.norm_weight != nullptr) {
+        sq.join(32, 4);
+        f = sq.factor(D, a.norm_eps);
+      }
+      if (!live) return;
+      __nv_bfloat16* dst = a.out + row * D + gq;
+#pragma unroll
+      for (int mt = 0; mt < KS; ++mt) {
+        const float w0 = a.norm_weight != nullptr ? __ldg(a.norm_weight + mt * 16 + gq) : 1.f;
+        const float w1 = a.norm_weight != nullptr ? __ldg(a.norm_weight + mt * 16 + 8 + gq) : 1.f;
+        dst[mt * 16] = __float2bfloat16_rn(o[mt][0] * f * w0);
+        dst[mt * 16 + 8] = __float2bfloat16_rn(o[mt][2] * f * w1);
+      }
+      return;
+    }
+    if constexpr (WIDE) {
 #pragma unroll
       for (int m = 4; m <= 16; m <<= 1) {
         n0 += __shfl_xor_sync(kFullMask, n0, m);
@@ -891,12 +948,16 @@ decode_split_kernel(const __grid_constant__ DecodeArgs a) {
     // partial in slot 2 ridx (the segment holds the range's start) or 2 ridx + 1 (its end)
     seg_slot = (seg_begin >= u0 && seg_begin + nb <= u0 + nunits) ? -1 : 2 * ridx + (u0 >= seg_begin ? 0 : 1);
     if constexpr (SCORES)
-      seg_logits = a.logits + ((size_t)c.b * a.Hq + (size_t)c.g * G + 2 * tq) * kMaps * a.score_stride;
+      seg_logits = a.logits + ((size_t)c.b * a.Hq + (size_t)c.g * G + (PAIRS ? tq : 2 * tq)) * kMaps * a.score_stride;
     if constexpr (RULES) {
       if (a.slopes != nullptr) {
         const float* sp = a.slopes + (size_t)c.g * G;
-        slope0 = 2 * tq < G ? __ldg(sp + 2 * tq) * kLog2e : 0.f;
-        slope1 = 2 * tq + 1 < G ? __ldg(sp + 2 * tq + 1) * kLog2e : 0.f;
+        if constexpr (PAIRS) {
+          slope0 = slope1 = tq < G ? __ldg(sp + tq) * kLog2e : 0.f;
+        } else {
+          slope0 = 2 * tq < G ? __ldg(sp + 2 * tq) * kLog2e : 0.f;
+          slope1 = 2 * tq + 1 < G ? __ldg(sp + 2 * tq + 1) * kLog2e : 0.f;
+        }
       }
     }
     if constexpr (Q8) {
@@ -969,7 +1030,7 @@ decode_split_kernel(const __grid_constant__ DecodeArgs a) {
       for (int i = 0; i < 4; ++i) o[mt][i] = 0.f;
     mr0 = mr1 = -INFINITY;
     l0 = l1 = 0.f;
-    if constexpr (DIFF) {
+    if constexpr (WIDE) {
 #pragma unroll
       for (int mt = 0; mt < KS; ++mt)
 #pragma unroll
@@ -1100,8 +1161,12 @@ decode_split_kernel(const __grid_constant__ DecodeArgs a) {
       // c[0] = (token gq, head h0), c[1] = (gq, h1), c[2] = (gq + 8, h0), c[3] = (gq + 8, h1)
       const bool t0 = (mask >> gq) & 1u;
       const bool t1 = (mask >> (gq + 8)) & 1u;
-      const bool v0 = 2 * tq < G, v1 = 2 * tq + 1 < G;
+      const bool v0 = PAIRS ? tq < G : 2 * tq < G, v1 = PAIRS ? tq < G : 2 * tq + 1 < G;
       float x00 = c[0] * fk0, x01 = c[1] * fk0, x10 = c[2] * fk1, x11 = c[3] * fk1;  // base-2 logits
+      if constexpr (PAIRS) {
+        x01 = cd[1] * fk0;
+        x11 = cd[3] * fk1;
+      }
       if constexpr (RULES) {
         if (a.cap_log2 > 0.f) {
           x00 = cap_logit(x00, a.cap_log2, a.cap_in);
@@ -1124,7 +1189,7 @@ decode_split_kernel(const __grid_constant__ DecodeArgs a) {
       if constexpr (SCORES) {  // keep the attended keys' logits for the score step
         const int tok = block_of(cc.b, cc.j) * 16 + gq;
         float* lg = seg_logits + tok;
-        const size_t next = (size_t)kMaps * a.score_stride;
+        const size_t next = (size_t)(WIDE ? 2 : 1) * a.score_stride;
         if (tok < a.score_stride) {
           if (t0 && v0) lg[0] = s00;
           if (t0 && v1) lg[next] = s01;
@@ -1234,7 +1299,7 @@ decode_split_kernel(const __grid_constant__ DecodeArgs a) {
       const uint32_t bh0 = movmatrix_trans(hA), bh1 = movmatrix_trans(hB);
       const uint32_t bl0 = Q8 ? 0u : movmatrix_trans(lA), bl1 = Q8 ? 0u : movmatrix_trans(lB);
       uint32_t dh0 = 0u, dh1 = 0u, dl0 = 0u, dl1 = 0u;
-      if constexpr (DIFF) {  // the second map likewise
+      if constexpr (WIDE) {  // the second map likewise
         float y[4];  // tokens gq (heads h0, h1) and gq + 8
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
@@ -1375,7 +1440,7 @@ decode_split_kernel(const __grid_constant__ DecodeArgs a) {
           ldsm_x4_trans(vbase + chunk_offset<D, SPARSE>(v_row, 2 * mt + v_half), av);
           mma_bf16_m16n8k16(o[mt], av, bh0, bh1);
           mma_bf16_m16n8k16(o[mt], av, bl0, bl1);
-          if constexpr (DIFF) {
+          if constexpr (WIDE) {
             mma_bf16_m16n8k16(od[mt], av, dh0, dh1);
             mma_bf16_m16n8k16(od[mt], av, dl0, dl1);
           }
@@ -1423,7 +1488,7 @@ decode_split_kernel(const __grid_constant__ DecodeArgs a) {
 template <int D, bool DIFF = false>
 __global__ void __launch_bounds__(kMergeWarps * 32)
 decode_merge_kernel(const DecodeArgs a, int group, int wpr_log2) {
-  constexpr int kMaps = DIFF ? 2 : 1;
+  constexpr int kMaps = DIFF ? 2 : 1;  // rows of a query head
   constexpr int EPW = D / 32;
   constexpr int W = kMergeWarps;
   __shared__ float s_acc[W][D];
@@ -1688,8 +1753,9 @@ __global__ void __launch_bounds__(kScoreThreads) decode_score_kernel(const Decod
 // The score step of differential attention: a key's weight in a head is a_1 - lambda a_2, a_m its softmax
 // probability in map m, and
 //   scores_out[b, g, t] = scores[b, g, t] + sum_i |a_1 - lambda a_2|   over the query heads i of the kv head
-// for the t that the query sees; the other t < L are copied.  A CTA covers 256 keys of one (b, g), a thread one (the
-// logits of its 2 G rows are G pairs of independent loads).
+// for the t that the query sees; the other t < L are copied.  A CTA covers 1024 keys of one (b, g), a thread four, as
+// 16-byte loads and stores where the rows allow it (16-byte aligned arrays, score_stride % 4 == 0).  The logits
+// are what it reads: 8 bytes a key and head.
 __global__ void __launch_bounds__(kScoreThreads) decode_diff_score_kernel(const DecodeArgs a, int group, int tiles) {
   const int seg = blockIdx.x / tiles;  // b * Hkv + g
   const int tile = blockIdx.x - seg * tiles;
@@ -1697,23 +1763,51 @@ __global__ void __launch_bounds__(kScoreThreads) decode_diff_score_kernel(const 
   grid_dependency_wait();  // the logits and log-sum-exps of the decode
   grid_launch_dependents();
   const RuleUnits u = rule_units(a, b);  // (a bad length, reported by the split kernel, counts as 0)
-  const int t = tile * kScoreThreads + (int)threadIdx.x;
-  if (t >= u.s.len || t >= a.score_stride) return;
-  const size_t at = (size_t)seg * a.score_stride + t;
-  float sum = 0.f;
-  if (t >= u.s.lo || t < u.pre) {
-    const size_t row0 = (size_t)b * a.Hq + (size_t)(seg - b * a.Hkv) * group;
-    const float* lambdas = a.lambdas + (size_t)b * a.lambda_stride + (size_t)(seg - b * a.Hkv) * group;
+  const int end = min(u.s.len, a.score_stride);
+  const int t0 = tile * kScoreKeys + 4 * (int)threadIdx.x;
+  if (t0 >= end) return;
+  const size_t at = (size_t)seg * a.score_stride + t0, row0 = (size_t)b * a.Hq + (size_t)(seg - b * a.Hkv) * group;
+  const float* lambdas = a.lambdas + (size_t)b * a.lambda_stride + (size_t)(seg - b * a.Hkv) * group;
+  const bool vec = (a.score_stride & 3) == 0 && t0 + 4 <= end &&
+                   ((reinterpret_cast<uintptr_t>(a.scores) | reinterpret_cast<uintptr_t>(a.scores_out)) & 15u) == 0;
+  float sum[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll 4
-    for (int i = 0; i < group; ++i) {
-      const float* src = a.logits + (row0 + i) * 2 * a.score_stride + t;
-      const float lse1 = a.lse[(row0 + i) * 2], lse2 = a.lse[(row0 + i) * 2 + 1];
-      const float w1 = lse1 == -INFINITY ? 0.f : exp2f(src[0] - lse1);
-      const float w2 = lse2 == -INFINITY ? 0.f : exp2f(src[a.score_stride] - lse2);
-      sum += fabsf(w1 - lambdas[i] * w2);
+  for (int i = 0; i < group; ++i) {
+    const float lse1 = a.lse[(row0 + i) * 2], lse2 = a.lse[(row0 + i) * 2 + 1], lam = lambdas[i];
+    const float* src = a.logits + (row0 + i) * 2 * a.score_stride + t0;
+    float x[4], y[4];
+    if (vec) {
+      const float4 p = *reinterpret_cast<const float4*>(src), q = *reinterpret_cast<const float4*>(src + a.score_stride);
+      x[0] = p.x; x[1] = p.y; x[2] = p.z; x[3] = p.w;
+      y[0] = q.x; y[1] = q.y; y[2] = q.z; y[3] = q.w;
+    } else {
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        x[e] = t0 + e < end ? src[e] : 0.f;
+        y[e] = t0 + e < end ? src[a.score_stride + e] : 0.f;
+      }
+    }
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      const float w1 = lse1 == -INFINITY ? 0.f : exp2f(x[e] - lse1), w2 = lse2 == -INFINITY ? 0.f : exp2f(y[e] - lse2);
+      sum[e] += fabsf(w1 - lam * w2);
     }
   }
-  a.scores_out[at] = a.scores[at] + sum;
+  // (the logits of keys that the query does not see were not written)
+#pragma unroll
+  for (int e = 0; e < 4; ++e) sum[e] = t0 + e >= u.s.lo || t0 + e < u.pre ? sum[e] : 0.f;
+  if (vec) {
+    float4 o = *reinterpret_cast<const float4*>(a.scores + at);
+    o.x += sum[0];
+    o.y += sum[1];
+    o.z += sum[2];
+    o.w += sum[3];
+    *reinterpret_cast<float4*>(a.scores_out + at) = o;
+  } else {
+#pragma unroll
+    for (int e = 0; e < 4; ++e)
+      if (t0 + e < end) a.scores_out[at + e] = a.scores[at + e] + sum[e];
+  }
 }
 
 }  // namespace
@@ -1724,8 +1818,12 @@ template <int D>
 DecodeKernel kernels_of(int group, bool sparse, bool scores, bool q8, bool f8, bool rules, bool diff) {
   const void* split;
   if (diff) {
-    split = scores ? (const void*)decode_split_kernel<D, false, true, false, false, true, true>
-                   : (const void*)decode_split_kernel<D, false, false, false, false, true, true>;
+    if (group <= 4)
+      split = scores ? (const void*)decode_split_kernel<D, false, true, false, false, true, kDiffPairs>
+                     : (const void*)decode_split_kernel<D, false, false, false, false, true, kDiffPairs>;
+    else
+      split = scores ? (const void*)decode_split_kernel<D, false, true, false, false, true, kDiffWide>
+                     : (const void*)decode_split_kernel<D, false, false, false, false, true, kDiffWide>;
     return DecodeKernel{split, (const void*)decode_merge_kernel<D, true>,
                         scores ? (const void*)decode_diff_score_kernel : nullptr, D, group, sparse, scores, q8};
   }
@@ -1782,7 +1880,7 @@ cudaError_t launch_decode(const DecodeKernel& k, const DecodeArgs& a, int grid, 
   if (e != cudaSuccess || !k.scores) return e;
   if (a.lambdas != nullptr) {  // all keys of the longest sequence
     const long long span = std::min((long long)a.MB * 16, (long long)a.score_stride);
-    int tiles = (int)std::max(1ll, (span + kScoreThreads - 1) / kScoreThreads);
+    int tiles = (int)std::max(1ll, (span + kScoreKeys - 1) / kScoreKeys);
     void* params[] = {&args, &group, &tiles};
     return launch_pdl(k.score, dim3((unsigned)((long long)a.B * a.Hkv * tiles)), dim3(kScoreThreads), 0, stream, params);
   }

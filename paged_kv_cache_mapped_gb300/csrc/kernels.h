@@ -121,6 +121,10 @@ constexpr int kPartFields = kPartOff + kMaxTailChunksLimit + 1;
 #define PKV_F8_MIN_CTAS 12  // FP8 decode: the same bound (14: 53.6 us against 49.1 for 32 x ~4000 tokens)
 #endif
 
+#ifndef PKV_DIFF_MIN_CTAS
+#define PKV_DIFF_MIN_CTAS 0  // differential decode: the same bound
+#endif
+
 #ifndef PKV_MIN_UNITS
 #define PKV_MIN_UNITS 16  // lower bound of a worker slice, in 16-token units
 #endif
@@ -148,6 +152,15 @@ constexpr int kPartFields = kPartOff + kMaxTailChunksLimit + 1;
 // 49.0, 52.8 and 49.0 us).
 #ifndef PKV_TAIL_PCT_F8
 #define PKV_TAIL_PCT_F8 0
+#endif
+#ifndef PKV_MIN_UNITS_DIFF
+#define PKV_MIN_UNITS_DIFF 16
+#endif
+#ifndef PKV_MIN_BUSY_PCT_DIFF
+#define PKV_MIN_BUSY_PCT_DIFF 70
+#endif
+#ifndef PKV_TAIL_PCT_DIFF
+#define PKV_TAIL_PCT_DIFF 20
 #endif
 #ifndef PKV_CHUNK_MIN_Q8
 #define PKV_CHUNK_MIN_Q8 6
