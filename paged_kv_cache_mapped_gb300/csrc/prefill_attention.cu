@@ -918,6 +918,16 @@ __device__ __forceinline__ float row_max(const float (&v)[N]) {
   return fmaxf(fmax3(t[0], t[1], t[2]), t[3]);
 }
 
+// The same of v[at .. at + 31], in one chain: beside the other row tile's warp on the scheduler its latency costs less
+// than the instructions that join more (chunk of 4096 on 16384: 1321 us, with two chains 1341).
+template <bool ABS>
+__device__ __forceinline__ float half_max(const float (&v)[kStep], int at) {
+  float t = ABS ? 0.f : -INFINITY;
+#pragma unroll
+  for (int c = at; c < at + 32; c += 2) t = fmax3(t, ABS ? fabsf(v[c]) : v[c], ABS ? fabsf(v[c + 1]) : v[c + 1]);
+  return t;
+}
+
 // tanh(u) / u as a polynomial of u^2, of the least largest relative error on |u| <= kCapNear (degree 2, 1.1e-7)
 // and on |u| <= kCapFar (degree 5, 5.8e-8), found by Remez' exchange in 40 digits; as stored 1.2e-7 and 6.8e-8, in
 // fp32 steps 1.5e-7 and 1.1e-7.
@@ -1264,15 +1274,32 @@ __device__ __forceinline__ void softmax_rows(const PrefillAttnArgs& a, Shared<D,
   m = -INFINITY;
   l = 0.f;
   float reach = kCapNear;  // of the polynomial tried for the cap
+  float v[N];
+  auto wait_s = [&](uint32_t step) {
+    ok = __all_sync(kFullMask, mbar_wait_spin(&sh.s_full[x][step & 1u], (step >> 1) & 1u, a.timeout_ns));
+    if (ok) tc_fence_after();
+    return ok;
+  };
+  auto read_s = [&](uint32_t step, int c) {
+    tmem_ld_x32(t_lane + x * 2 * kStep + (step & 1u) * kStep + 32 * c, *reinterpret_cast<float(*)[32]>(v + 32 * c));
+  };
+  // DIFF: the second half of a step's S is read under the maximum of the first (chunk of 4096 on 16384: 1350 us with one
+  // wait for both, 1321).  Reading S of the next step under this one's weights costs: it is not there yet, the
+  // issuers being as slow as the softmax (1428; after the last weights 1371)
   for (int j = range.hi; j >= range.lo; --j) {
     const uint32_t buf = n_step & 1u;
     const uint32_t ts_addr = t_lane + x * 2 * kStep + buf * kStep;
-    ok = __all_sync(kFullMask, mbar_wait_spin(&sh.s_full[x][buf], (n_step >> 1) & 1u, a.timeout_ns));
-    if (!ok) break;
-    tc_fence_after();
-    float v[N];
-#pragma unroll
-    for (int c = 0; c < N / 32; ++c) tmem_ld_x32(ts_addr + 32 * c, *reinterpret_cast<float(*)[32]>(v + 32 * c));
+    float first_max = -INFINITY, first_size = 0.f;
+    if (!wait_s(n_step)) break;
+    read_s(n_step, 0);
+    if constexpr (DIFF) {
+      tmem_wait_ld();
+      read_s(n_step, 1);
+      if (MODE == 0) first_max = half_max<false>(v, 0);
+      else first_size = half_max<true>(v, 0);
+    } else {
+      read_s(n_step, 1);
+    }
     tmem_wait_ld();
     const int e0 = e_base + j * kStepBlocks;
     const bool full = (j >= full0 && j < full1) || j < full_pre;
@@ -1284,9 +1311,9 @@ __device__ __forceinline__ void softmax_rows(const PrefillAttnArgs& a, Shared<D,
     float mx = -INFINITY, base = 0.f;
     Logits y{a.scale_log2, 0.f, 0.f};
     if (fast && !cap && !bias) {
-      mx = row_max<false>(v) * a.scale_log2;
+      mx = (DIFF ? fmaxf(first_max, half_max<false>(v, 32)) : row_max<false>(v)) * a.scale_log2;
     } else if (fast) {
-      const float far = row_max<true>(v);
+      const float far = DIFF ? fmaxf(first_size, half_max<true>(v, 32)) : row_max<true>(v);
       const float size = far * fabsf(a.scale_log2);
       mx = size;
       if (bias && slope2 != 0.f) {
@@ -1496,7 +1523,11 @@ __device__ __forceinline__ void softmax_rows(const PrefillAttnArgs& a, Shared<D,
   }
 }
 
-template <int D, int NT, bool DIFF = false>
+// RULES: softmax_rows' MODE for the whole launch, or kAnyRules: by the arguments.  (A differential chunk of 4096 on 16384
+// keys takes 1350 us with its own kernel and 1395 with four loops in one, one loop's code being all that runs.)
+constexpr int kAnyRules = -1;
+
+template <int D, int NT, bool DIFF = false, int RULES = kAnyRules>
 __global__ void __launch_bounds__(Geo<D, NT, DIFF>::kThreads, Geo<D, NT, DIFF>::kCtas)
 prefill_attention_kernel(const __grid_constant__ PrefillAttnArgs a) {
   using GE = Geo<D, NT, DIFF>;
@@ -1583,7 +1614,9 @@ prefill_attention_kernel(const __grid_constant__ PrefillAttnArgs a) {
         // a loop for each set of rules: one for all is 3 to 5 % slower with a cap (0.88 against 0.84 ms, a chunk
         // of 4096 on 16384 keys).  One row tile has the registers of half the threads: there the loop for all
         // serves (64 tokens on 2000 keys 109 us, 114 with four loops, which spill)
-        if constexpr (NT == 1) {
+        if constexpr (RULES != kAnyRules) {
+          rows(std::integral_constant<int, RULES>{});
+        } else if constexpr (NT == 1) {
           rows(std::integral_constant<int, 4>{});
         } else {
           if (mode == 0) rows(std::integral_constant<int, 0>{});
@@ -1756,6 +1789,23 @@ PrefillWorkspace plan_prefill(long long B, long long T, int Hq, int G, int D, in
 
 size_t plan_smem_bytes(int B) { return sizeof(int) * (4 * (size_t)B + 1); }
 
+// The rules of a call that need each key's own logit, as softmax_rows' MODE.
+__host__ __device__ inline int rules_mode(const PrefillAttnArgs& a) {
+  return (a.cap_log2 > 0.f ? 1 : 0) | (a.slopes != nullptr || !(a.scale_log2 > 0.f) ? 2 : 0);
+}
+
+template <int D, int NT, bool DIFF>
+const void* attention_kernel(int mode) {
+  if constexpr (DIFF) {
+    return mode == 0   ? (const void*)prefill_attention_kernel<D, NT, true, 0>
+           : mode == 1 ? (const void*)prefill_attention_kernel<D, NT, true, 1>
+           : mode == 2 ? (const void*)prefill_attention_kernel<D, NT, true, 2>
+                       : (const void*)prefill_attention_kernel<D, NT, true, 3>;
+  } else {
+    return (const void*)prefill_attention_kernel<D, NT>;
+  }
+}
+
 template <int D, int NT, bool DIFF = false>
 cudaError_t launch_attention(const PrefillAttnArgs& a, cudaStream_t stream) {
   using GE = Geo<D, NT, DIFF>;
@@ -1770,7 +1820,7 @@ cudaError_t launch_attention(const PrefillAttnArgs& a, cudaStream_t stream) {
   if (e != cudaSuccess) return e;
   void* params[] = {&args};
   // a CTA for every slot: even one token's keys are cut into shares for all of them
-  e = launch_pdl((const void*)prefill_attention_kernel<D, NT, DIFF>, dim3((unsigned)args.slots), dim3(GE::kThreads), GE::kSmem, stream, params);
+  e = launch_pdl(attention_kernel<D, NT, DIFF>(rules_mode(a)), dim3((unsigned)args.slots), dim3(GE::kThreads), GE::kSmem, stream, params);
   if (e != cudaSuccess) return e;
   const long long entries = (long long)a.T / per_item + a.B;  // at most
   const long long warps = std::min(entries * std::min(per_item, a.T) * a.Hq, 8ll * 8 * a.sms);
@@ -1779,8 +1829,12 @@ cudaError_t launch_attention(const PrefillAttnArgs& a, cudaStream_t stream) {
 
 template <int D, int NT, bool DIFF = false>
 cudaError_t setup_attention() {
-  return cudaFuncSetAttribute((const void*)prefill_attention_kernel<D, NT, DIFF>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                              (int)Geo<D, NT, DIFF>::kSmem);
+  for (int mode = 0; mode < (DIFF ? 4 : 1); ++mode) {
+    const cudaError_t e = cudaFuncSetAttribute(attention_kernel<D, NT, DIFF>(mode), cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                               (int)Geo<D, NT, DIFF>::kSmem);
+    if (e != cudaSuccess) return e;
+  }
+  return cudaSuccess;
 }
 }  // namespace
 
