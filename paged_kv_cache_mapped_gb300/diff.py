@@ -4,28 +4,28 @@ marshalling only."""
 from __future__ import annotations
 
 import ctypes
-import math
 
 import torch
 
 from ._lib import PkvDiffParams, header_constants, load
-from .step import _bf16_pools, _call, _dims, _give, _need, _new, _opt, _rules
+from .step import _bf16_pools, _call, _dims, _give, _like, _need, _new, _opt, _rules
 
 _INPUTS_READY = header_constants()["PKV_DECODE_INPUTS_READY"]
 
 
 def _params(lambdas, norm_weight, norm_eps, rows, hq, d, dev):
-    per_row = isinstance(lambdas, torch.Tensor) and lambdas.dim() == 2
+    per_row = getattr(lambdas, "ndim", 0) == 2
     lp = _need(lambdas, "lambdas", torch.float32, 2 if per_row else 1, dev)
-    if tuple(lambdas.shape) != ((rows, hq) if per_row else (hq,)):
+    if lambdas.shape != ((rows, hq) if per_row else (hq,)):
         raise ValueError(f"lambdas must be [num_q_heads] or [rows of q, num_q_heads], got {tuple(lambdas.shape)}")
-    wp = _opt(norm_weight, "norm_weight", torch.float32, 1, dev)
+    wp = None
     if norm_weight is not None:
+        wp = _need(norm_weight, "norm_weight", torch.float32, 1, dev)
         if norm_weight.shape[0] != d:
             raise ValueError("norm_weight must be [head_dim]")
-        if not (math.isfinite(norm_eps) and ctypes.c_float(norm_eps).value > 0):
+        if not 1e-45 <= norm_eps < 3.4e38:  # (finite and positive in fp32)
             raise ValueError("norm_eps must be finite and positive")
-    return PkvDiffParams(lp, 1 if per_row else 0, float(norm_eps), wp)
+    return PkvDiffParams(lp, 1 if per_row else 0, norm_eps, wp)
 
 
 def diff_decode_workspace_bytes(batch, num_q_heads, num_kv_heads, head_dim, num_blocks, max_blocks_per_seq, *, score_stride=0) -> int:
@@ -45,7 +45,7 @@ def _decode(name, lead, stride, q, k_cache, v_cache, block_tables, context_lens,
     qp = _need(q, "q", torch.bfloat16, 3, dev)
     bp = _need(block_tables, "block_tables", torch.int32, 2, dev)
     lp = _need(context_lens, "context_lens", torch.int32, 1, dev)
-    err = _opt(error_word, "error_word", torch.int32, 1, dev)
+    err = None if error_word is None else _need(error_word, "error_word", torch.int32, 1, dev)
     B, hq, dq = q.shape
     rows, mb = block_tables.shape
     if dq != d:
@@ -57,7 +57,7 @@ def _decode(name, lead, stride, q, k_cache, v_cache, block_tables, context_lens,
     if softcap != 0 or window > 0 or alibi_slopes is not None or doc_starts is not None or prefix_lens is not None:
         rules = ctypes.byref(_rules(softcap, window, alibi_slopes, doc_starts, prefix_lens, hq, B, B, dev))
     dims = _dims(B, hq, hkv, d, nb, mb)
-    out, op = _give(out, "out", (B, hq, d), torch.bfloat16, q, dev, stream)
+    out, op = _like(out, "out", q, dev, stream)
     if workspace is None:
         workspace = _new((int(load().pkv_diff_decode_workspace_bytes(dims, stride)),), torch.uint8, q, stream, torch.zeros)
     wp = _need(workspace, "workspace", torch.uint8, 1, dev)
@@ -130,7 +130,7 @@ def paged_diff_prefill_attention(q, k_cache, v_cache, block_tables, context_lens
     params = _params(lambdas, norm_weight, norm_eps, T, hq, d, dev)
     rules = _rules(softcap, window, alibi_slopes, doc_starts, prefix_lens, hq, T, B, dev)
     dims = _dims(B, hq, hkv, d, nb, mb)
-    out, op = _give(out, "out", (T, hq, d), torch.bfloat16, q, dev, stream)
+    out, op = _like(out, "out", q, dev, stream)
     if workspace is None:
         workspace = _new((int(load().pkv_diff_prefill_workspace_bytes(dims, T)),), torch.uint8, q, stream)
     wp = _need(workspace, "workspace", torch.uint8, 1, dev)

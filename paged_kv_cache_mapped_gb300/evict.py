@@ -4,23 +4,25 @@ rest of the package: argument checks and marshalling only."""
 from __future__ import annotations
 
 import ctypes
+import functools
 
 import torch
 
 from ._lib import PkvEvictRules, PkvEvictState, load
-from .step import BLOCK_SIZE, _bf16_pools, _call, _dims, _give, _need, _new, _opt
+from .step import BLOCK_SIZE, _bf16_pools, _call, _dims, _give, _like, _need, _new
 
 
+@functools.lru_cache(maxsize=256)
 def _rules(n_sink, k_top, n_recent, trigger=0):
     for name, x in (("n_sink", n_sink), ("k_top", k_top), ("n_recent", n_recent)):
         if not 0 <= int(x) < 2**30:
             raise ValueError(f"{name} must be within [0, 2**30), got {x}")
-    return PkvEvictRules(int(n_sink), int(k_top), int(n_recent), max(0, min(int(trigger), 2**31 - 1)))
+    return ctypes.pointer(PkvEvictRules(int(n_sink), int(k_top), int(n_recent), max(0, min(int(trigger), 2**31 - 1))))
 
 
 def evict_workspace_bytes(batch, num_kv_heads, n_sink, k_top, n_recent) -> int:
     """Workspace of kv_evict and kv_evict_q8 for these sizes."""
-    n = int(load().pkv_evict_workspace_bytes(_dims(batch, 1, num_kv_heads, 128, 0, 0), ctypes.byref(_rules(n_sink, k_top, n_recent))))
+    n = int(load().pkv_evict_workspace_bytes(_dims(batch, 1, num_kv_heads, 128, 0, 0), _rules(n_sink, k_top, n_recent)))
     if n == 0:
         raise ValueError("invalid sizes for an eviction")
     return n
@@ -34,12 +36,12 @@ def _evict(name, pools, hkv, d, nb, dev, block_tables, context_lens, scores, slo
     sp = _need(scores, "scores", torch.float32, 3, dev)
     pp = _need(slot_pos, "slot_pos", torch.int32, 3, dev)
     dp = _need(dropped, "dropped", torch.int32, 1, dev)
-    err = _opt(error_word, "error_word", torch.int32, 1, dev)
+    err = None if error_word is None else _need(error_word, "error_word", torch.int32, 1, dev)
     B, mb = block_tables.shape
     stride = scores.shape[2]
     if context_lens.shape[0] != B or dropped.shape[0] != B:
         raise ValueError("context_lens / dropped batch differs from block_tables'")
-    if scores.shape[:2] != (B, hkv) or slot_pos.shape != scores.shape:
+    if scores.shape != (B, hkv, stride) or slot_pos.shape != scores.shape:
         raise ValueError("scores and slot_pos must have one shape [batch, num_kv_heads, slots]")
     if stride >= 2**31:
         raise ValueError(f"sizes must be within [0, 2**31), got {stride}")
@@ -47,8 +49,8 @@ def _evict(name, pools, hkv, d, nb, dev, block_tables, context_lens, scores, slo
         raise ValueError("free_blocks and free_count come together")
     rules = _rules(n_sink, k_top, n_recent, trigger)
     dims = _dims(B, 1, hkv, d, nb, mb)
-    lens_out, lp = _give(context_lens_out, "context_lens_out", (B,), torch.int32, block_tables, dev, stream)
-    gone_out, gp = _give(dropped_out, "dropped_out", (B,), torch.int32, block_tables, dev, stream)
+    lens_out, lp = _like(context_lens_out, "context_lens_out", context_lens, dev, stream)
+    gone_out, gp = _like(dropped_out, "dropped_out", dropped, dev, stream)
     sop = sp if scores_out is None else _give(scores_out, "scores_out", scores.shape, torch.float32, scores, dev, stream)[1]
     pop = pp if slot_pos_out is None else _give(slot_pos_out, "slot_pos_out", scores.shape, torch.int32, scores, dev, stream)[1]
     free = count = cp = count_out = None
@@ -57,13 +59,13 @@ def _evict(name, pools, hkv, d, nb, dev, block_tables, context_lens, scores, slo
         count = _need(free_count, "free_count", torch.int32, 1, dev)
         if free_blocks.shape[0] != nb or free_count.shape[0] != 1:
             raise ValueError("free_blocks must be [num_blocks] and free_count [1]")
-        count_out, cp = _give(free_count_out, "free_count_out", (1,), torch.int32, block_tables, dev, stream)
+        count_out, cp = _like(free_count_out, "free_count_out", free_count, dev, stream)
     if workspace is None:
-        n = int(load().pkv_evict_workspace_bytes(dims, ctypes.byref(rules)))
+        n = int(load().pkv_evict_workspace_bytes(dims, rules))
         workspace = _new((n,), torch.uint8, block_tables, stream)
     wp = _need(workspace, "workspace", torch.uint8, 1, dev)
     state = PkvEvictState(sp, sop, pp, pop, dp, gp, stride)
-    _call(name, dev, stream, *pools, bt, lens, lp, ctypes.byref(state), ctypes.byref(rules), free, count, cp, wp, workspace.numel(),
+    _call(name, dev, stream, *pools, bt, lens, lp, ctypes.byref(state), rules, free, count, cp, wp, workspace.numel(),
           dims, err)
     return lens_out, gone_out, count_out
 

@@ -87,6 +87,14 @@ def _give(t, name, shape, dtype, like, device, stream):
     return t, ptr
 
 
+def _like(t, name, like, device, stream):
+    """The output `t` of `like`'s shape and type after its checks, or a new one; with its address."""
+    if t is None and stream is None:
+        t = torch.empty_like(like)
+        return t, t.data_ptr()
+    return _give(t, name, like.shape, like.dtype, like, device, stream)
+
+
 def kv_step_tables(block_tables, context_lens, new_tokens, free_blocks, free_count, max_new_tokens, *,
                    context_lens_out=None, free_count_out=None, query_starts=None, slot_mapping=None, positions=None,
                    error_word=None, stream=None):

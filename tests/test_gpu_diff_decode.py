@@ -394,3 +394,46 @@ def test_binding_refusals():
     for x in (-1, 2**31, 2**32 + 4):
         with pytest.raises(ValueError):
             pkv.diff_decode_workspace_bytes(*ok, score_stride=x)
+
+
+@pytest.mark.gpu
+def test_binding_refuses_wrong_shapes_and_types():
+    c = _case([20, 33], 8, 2, 64, 15)
+    q, lens, lam, w = c["q"].to(DEV), torch.tensor(c["lens"], dtype=torch.int32, device=DEV), c["lam"].to(DEV), c["w"].to(DEV)
+    starts = torch.tensor([0, 1, 2], dtype=torch.int32, device=DEV)
+    sc = torch.zeros(2, 2, 48, device=DEV)
+
+    def decode(q=q, bt=c["bt"], lens=lens, lam=lam, **kw):
+        kw = dict(dict(norm_weight=w), **kw)
+        return pkv.paged_diff_decode_attention(q, *c["pools"], bt, lens, lam, 0.2, **kw)
+
+    def prefill(lam=lam, **kw):
+        return pkv.paged_diff_prefill_attention(q, *c["pools"], c["bt"], lens, starts, lam, 0.2, **dict(dict(norm_weight=w), **kw))
+
+    def scores(sc=sc, **kw):
+        return pkv.paged_diff_decode_attention_scores(q, *c["pools"], c["bt"], lens, lam, sc, 0.2, **kw)
+
+    for call in (decode, prefill):
+        for bad in (lam[:7], lam[None], torch.zeros(3, 8, device=DEV), torch.zeros(2, 7, device=DEV), torch.zeros(2, 2, 8, device=DEV)):
+            with pytest.raises(ValueError):
+                call(lam=bad)
+        for bad in (lam.double(), 0.5, None):
+            with pytest.raises(TypeError):
+                call(lam=bad)
+        for eps in (0.0, -1.0, float("nan"), float("inf"), 1e-50, 1e300):
+            with pytest.raises(ValueError, match="norm_eps"):
+                call(norm_eps=eps)
+        for kw in (dict(norm_weight=w[:32]), dict(out=torch.empty_like(q[:1])), dict(out=q.permute(1, 0, 2)), dict(softcap=-1.0),
+                   dict(alibi_slopes=lam[:3].clone()), dict(workspace=torch.zeros(16, dtype=torch.uint8))):
+            with pytest.raises(ValueError):
+                call(**kw)
+        with pytest.raises(pkv.PkvError):
+            call(workspace=torch.zeros(16, dtype=torch.uint8, device=DEV))
+    for kw in (dict(q=q[:, :, :32].contiguous()), dict(bt=c["bt"][:1]), dict(lens=lens[:1])):
+        with pytest.raises(ValueError):
+            decode(**kw)
+    for kw in (dict(sc=sc[:1]), dict(sc=sc[:, :1].contiguous()), dict(sc=sc[0]), dict(scores_out=sc[:, :, :40].contiguous()), dict(sc=sc.cpu())):
+        with pytest.raises(ValueError):
+            scores(**kw)
+    with pytest.raises(pkv.PkvError):   # rows of no slots
+        scores(sc=sc[:, :, :0].contiguous())

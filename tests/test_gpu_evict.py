@@ -520,3 +520,37 @@ def test_binding_refusals():
     for sizes in ((5000, 2), (2**32 + 1, 2), (-1, 2), (2, 0)):
         with pytest.raises(ValueError):
             pkv.evict_workspace_bytes(*sizes, 1, 1, 1)
+
+
+@pytest.mark.gpu
+def test_binding_refuses_wrong_shapes_and_types():
+    s = _state([40, 50], 2, 64, 4, 23)
+    pools = [_dev(p).view(torch.bfloat16) for p in s["pools"]]
+    t = dict(bt=_dev(s["bt"]), lens=_dev(s["lens"]), sc=_dev(s["scores"]), pos=_dev(s["pos"]), gone=_dev(s["dropped"]))
+    free, count = torch.zeros(s["nb"], dtype=torch.int32, device=DEV), torch.zeros(1, dtype=torch.int32, device=DEV)
+    before = [p.clone() for p in pools]
+
+    def call(n=(4, 10, 10), kw=None, **x):
+        a = dict(t, **x)
+        return pkv.kv_evict(*pools, a["bt"], a["lens"], a["sc"], a["pos"], a["gone"], *n, **(kw or {}))
+
+    for x in (dict(lens=t["lens"][:1]), dict(gone=t["gone"][:1]), dict(sc=t["sc"][:, :1].contiguous()), dict(sc=t["sc"][:1]),
+              dict(pos=t["pos"][:, :, :32].contiguous()), dict(bt=t["bt"].t()), dict(sc=t["sc"].cpu()), dict(bt=t["bt"][0])):
+        with pytest.raises(ValueError):
+            call(**x)
+    for x in (dict(sc=t["sc"].double()), dict(pos=t["pos"].long()), dict(lens=None)):
+        with pytest.raises(TypeError):
+            call(**x)
+    for kw in (dict(free_blocks=free), dict(free_count=count), dict(free_count_out=count), dict(free_blocks=free[:3], free_count=count),
+               dict(free_blocks=free, free_count=free), dict(scores_out=t["sc"][:1]), dict(context_lens_out=count),
+               dict(workspace=torch.zeros(16, dtype=torch.uint8))):
+        with pytest.raises(ValueError):
+            call(kw=kw)
+    with pytest.raises(pkv.PkvError):
+        call(kw=dict(workspace=torch.zeros(16, dtype=torch.uint8, device=DEV)))
+    for n in ((-1, 1, 1), (1, 2**30, 1)):
+        with pytest.raises(ValueError):
+            call(n)
+    with pytest.raises(pkv.PkvError):
+        call((2**29, 2**29, 2**29))
+    assert all(torch.equal(a.view(torch.int16), b.view(torch.int16)) for a, b in zip(pools, before))
