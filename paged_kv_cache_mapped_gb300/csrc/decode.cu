@@ -1755,7 +1755,8 @@ __global__ void __launch_bounds__(kScoreThreads) decode_score_kernel(const Decod
 //   scores_out[b, g, t] = scores[b, g, t] + sum_i |a_1 - lambda a_2|   over the query heads i of the kv head
 // for the t that the query sees; the other t < L are copied.  A CTA covers 1024 keys of one (b, g), a thread four, as
 // 16-byte loads and stores where the rows allow it (16-byte aligned arrays, score_stride % 4 == 0).  The logits
-// are what it reads: 8 bytes a key and head.
+// are what it reads: 8 bytes a key and head.  `tiles` CTAs a (b, g), which take its keys in turn: as many as fill the GPU,
+// where the tables' width would ask for far more.
 __global__ void __launch_bounds__(kScoreThreads) decode_diff_score_kernel(const DecodeArgs a, int group, int tiles) {
   const int seg = blockIdx.x / tiles;  // b * Hkv + g
   const int tile = blockIdx.x - seg * tiles;
@@ -1764,49 +1765,50 @@ __global__ void __launch_bounds__(kScoreThreads) decode_diff_score_kernel(const 
   grid_launch_dependents();
   const RuleUnits u = rule_units(a, b);  // (a bad length, reported by the split kernel, counts as 0)
   const int end = min(u.s.len, a.score_stride);
-  const int t0 = tile * kScoreKeys + 4 * (int)threadIdx.x;
-  if (t0 >= end) return;
-  const size_t at = (size_t)seg * a.score_stride + t0, row0 = (size_t)b * a.Hq + (size_t)(seg - b * a.Hkv) * group;
+  const size_t row0 = (size_t)b * a.Hq + (size_t)(seg - b * a.Hkv) * group;
   const float* lambdas = a.lambdas + (size_t)b * a.lambda_stride + (size_t)(seg - b * a.Hkv) * group;
-  const bool vec = (a.score_stride & 3) == 0 && t0 + 4 <= end &&
-                   ((reinterpret_cast<uintptr_t>(a.scores) | reinterpret_cast<uintptr_t>(a.scores_out)) & 15u) == 0;
-  float sum[4] = {0.f, 0.f, 0.f, 0.f};
+  for (int t0 = tile * kScoreKeys + 4 * (int)threadIdx.x; t0 < end; t0 += tiles * kScoreKeys) {
+    const size_t at = (size_t)seg * a.score_stride + t0;
+    const bool vec = (a.score_stride & 3) == 0 && t0 + 4 <= end &&
+                     ((reinterpret_cast<uintptr_t>(a.scores) | reinterpret_cast<uintptr_t>(a.scores_out)) & 15u) == 0;
+    float sum[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll 4
-  for (int i = 0; i < group; ++i) {
-    const float lse1 = a.lse[(row0 + i) * 2], lse2 = a.lse[(row0 + i) * 2 + 1], lam = lambdas[i];
-    const float* src = a.logits + (row0 + i) * 2 * a.score_stride + t0;
-    float x[4], y[4];
-    if (vec) {
-      const float4 p = *reinterpret_cast<const float4*>(src), q = *reinterpret_cast<const float4*>(src + a.score_stride);
-      x[0] = p.x; x[1] = p.y; x[2] = p.z; x[3] = p.w;
-      y[0] = q.x; y[1] = q.y; y[2] = q.z; y[3] = q.w;
-    } else {
+    for (int i = 0; i < group; ++i) {
+      const float lse1 = a.lse[(row0 + i) * 2], lse2 = a.lse[(row0 + i) * 2 + 1], lam = lambdas[i];
+      const float* src = a.logits + (row0 + i) * 2 * a.score_stride + t0;
+      float x[4], y[4];
+      if (vec) {
+        const float4 p = *reinterpret_cast<const float4*>(src), q = *reinterpret_cast<const float4*>(src + a.score_stride);
+        x[0] = p.x; x[1] = p.y; x[2] = p.z; x[3] = p.w;
+        y[0] = q.x; y[1] = q.y; y[2] = q.z; y[3] = q.w;
+      } else {
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          x[e] = t0 + e < end ? src[e] : 0.f;
+          y[e] = t0 + e < end ? src[a.score_stride + e] : 0.f;
+        }
+      }
 #pragma unroll
       for (int e = 0; e < 4; ++e) {
-        x[e] = t0 + e < end ? src[e] : 0.f;
-        y[e] = t0 + e < end ? src[a.score_stride + e] : 0.f;
+        const float w1 = lse1 == -INFINITY ? 0.f : exp2f(x[e] - lse1), w2 = lse2 == -INFINITY ? 0.f : exp2f(y[e] - lse2);
+        sum[e] += fabsf(w1 - lam * w2);
       }
     }
+    // (the logits of keys that the query does not see were not written)
 #pragma unroll
-    for (int e = 0; e < 4; ++e) {
-      const float w1 = lse1 == -INFINITY ? 0.f : exp2f(x[e] - lse1), w2 = lse2 == -INFINITY ? 0.f : exp2f(y[e] - lse2);
-      sum[e] += fabsf(w1 - lam * w2);
+    for (int e = 0; e < 4; ++e) sum[e] = t0 + e >= u.s.lo || t0 + e < u.pre ? sum[e] : 0.f;
+    if (vec) {
+      float4 o = *reinterpret_cast<const float4*>(a.scores + at);
+      o.x += sum[0];
+      o.y += sum[1];
+      o.z += sum[2];
+      o.w += sum[3];
+      *reinterpret_cast<float4*>(a.scores_out + at) = o;
+    } else {
+#pragma unroll
+      for (int e = 0; e < 4; ++e)
+        if (t0 + e < end) a.scores_out[at + e] = a.scores[at + e] + sum[e];
     }
-  }
-  // (the logits of keys that the query does not see were not written)
-#pragma unroll
-  for (int e = 0; e < 4; ++e) sum[e] = t0 + e >= u.s.lo || t0 + e < u.pre ? sum[e] : 0.f;
-  if (vec) {
-    float4 o = *reinterpret_cast<const float4*>(a.scores + at);
-    o.x += sum[0];
-    o.y += sum[1];
-    o.z += sum[2];
-    o.w += sum[3];
-    *reinterpret_cast<float4*>(a.scores_out + at) = o;
-  } else {
-#pragma unroll
-    for (int e = 0; e < 4; ++e)
-      if (t0 + e < end) a.scores_out[at + e] = a.scores[at + e] + sum[e];
   }
 }
 
@@ -1880,7 +1882,8 @@ cudaError_t launch_decode(const DecodeKernel& k, const DecodeArgs& a, int grid, 
   if (e != cudaSuccess || !k.scores) return e;
   if (a.lambdas != nullptr) {  // all keys of the longest sequence
     const long long span = std::min((long long)a.MB * 16, (long long)a.score_stride);
-    int tiles = (int)std::max(1ll, (span + kScoreKeys - 1) / kScoreKeys);
+    const long long fill = 4ll * grid / ((long long)a.B * a.Hkv);
+    int tiles = (int)std::max(1ll, std::min((span + kScoreKeys - 1) / kScoreKeys, fill));
     void* params[] = {&args, &group, &tiles};
     return launch_pdl(k.score, dim3((unsigned)((long long)a.B * a.Hkv * tiles)), dim3(kScoreThreads), 0, stream, params);
   }

@@ -120,11 +120,11 @@ struct EvictShared {
   int equal, to, from;  // counts of this CTA's slots
 };
 
+// One row, bg, by a CTA or a cluster, unless it shrinks from more than `upto` slots.  s_keys: keys of this CTA's slots, a
+// multiple of four.
 template <bool CLUSTER>
-__global__ void __launch_bounds__(kEvictMaxThreads, 1) evict_select_kernel(const EvictArgs a) {
+__device__ __forceinline__ void select_row(const EvictArgs& a, int bg, int upto, EvictShared& sh, uint32_t* s_keys) {
   namespace cg = cooperative_groups;
-  extern __shared__ __align__(16) uint32_t s_keys[];  // of this CTA's slots, a multiple of four
-  __shared__ EvictShared sh;
   cg::cluster_group cluster = cg::this_cluster();
   const int ranks = CLUSTER ? (int)cluster.num_blocks() : 1, rank = CLUSTER ? (int)cluster.block_rank() : 0;
   auto sync_all = [&] {
@@ -132,15 +132,7 @@ __global__ void __launch_bounds__(kEvictMaxThreads, 1) evict_select_kernel(const
     else __syncthreads();
   };
   auto of_rank = [&](int r) { return CLUSTER ? cluster.map_shared_rank(&sh, r) : &sh; };
-  const int tid = threadIdx.x, lane = tid & 31, T = blockDim.x;
-  const int bg = blockIdx.x / ranks, b = bg / a.Hkv;
-  if (tid == 0) {
-    sh.least = 0xffffffffu;
-    sh.most = 0u;
-    sh.guarded = 0;
-  }
-  grid_dependency_wait();
-  grid_launch_dependents();
+  const int tid = threadIdx.x, lane = tid & 31, T = blockDim.x, b = bg / a.Hkv;
   const EvictSeq s = evict_seq(a, b);
   const float* scores = a.st.scores + (size_t)bg * a.st.stride;
   const int32_t* slot_pos = a.st.slot_pos + (size_t)bg * a.st.stride;
@@ -158,6 +150,12 @@ __global__ void __launch_bounds__(kEvictMaxThreads, 1) evict_select_kernel(const
         for (int i = rank * T + tid; i < s.L; i += ranks * T) pos_out[i] = slot_pos[i];
     }
     return;
+  }
+  if (s.L > upto) return;
+  if (tid == 0) {
+    sh.least = 0xffffffffu;
+    sh.most = 0u;
+    sh.guarded = 0;
   }
   __syncthreads();
   const int recent0 = s.L + s.dropped - a.n_recent;  // (n_recent <= budget < L)
@@ -541,6 +539,33 @@ __global__ void __launch_bounds__(kEvictMaxThreads, 1) evict_select_kernel(const
   }
 }
 
+// A CTA or cluster a row; or, MANY, few clusters that take the rows of more than `above` slots in turn.  (Apart: in the loop
+// the compiler keeps the arguments in registers, which the CTA a row has no room for: 32 x 4000 tokens 72 us against 66.)
+template <bool CLUSTER, bool MANY>
+__global__ void __launch_bounds__(kEvictMaxThreads, 1) evict_select_kernel(const __grid_constant__ EvictArgs a, int above, int upto) {
+  extern __shared__ __align__(16) uint32_t s_keys[];
+  __shared__ EvictShared sh;
+  const int ranks = CLUSTER ? (int)cooperative_groups::this_cluster().num_blocks() : 1;
+  const int first = (int)blockIdx.x / ranks;
+  grid_dependency_wait();
+  grid_launch_dependents();
+  if constexpr (!MANY) {
+    select_row<CLUSTER>(a, first, upto, sh, s_keys);
+  } else {
+    const int pairs = a.B * a.Hkv, step = (int)gridDim.x / ranks, lane = threadIdx.x & 31;
+    for (int base = first; base < pairs; base += 32 * step) {  // (every warp looks at the same 32)
+      const int bg = base + lane * step;
+      bool mine = false;
+      if (bg < pairs) {
+        const EvictSeq s = evict_seq(a, bg / a.Hkv);
+        mine = s.cut && s.L > above;
+      }
+      for (uint32_t todo = __ballot_sync(kFullMask, mine); todo != 0u; todo &= todo - 1u)
+        select_row<CLUSTER>(a, base + (__ffs(todo) - 1) * step, upto, sh, s_keys);
+    }
+  }
+}
+
 // ------------------------------------------------------------------------------------ the rows
 
 constexpr int kMoveThreads = 256;
@@ -605,7 +630,7 @@ __device__ __forceinline__ void evict_tables(const EvictArgs& a) {
 // RB: bytes of a row; SCALES: INT8 pools.  A warp takes 2 KB of K rows and as much of V at a time: lanes find the rows,
 // then every lane has eight 16-byte loads in flight before it stores.
 template <int RB, bool SCALES>
-__global__ void __launch_bounds__(kMoveThreads, 4) evict_move_kernel(const EvictArgs a) {
+__global__ void __launch_bounds__(kMoveThreads, 4) evict_move_kernel(const __grid_constant__ EvictArgs a) {
   constexpr int CPR = RB / 16, NR = 128 / CPR;  // 16-byte pieces of a row; rows of a warp at a time
   static_assert(NR <= 32 && NR * CPR == 4 * 32, "four pieces of K and of V a lane");
   grid_dependency_wait();
@@ -677,33 +702,47 @@ __global__ void __launch_bounds__(kMoveThreads, 4) evict_move_kernel(const Evict
   }
 }
 
-// CTAs of a row: as many as the SMs hold at once, of 4096 slots at least, and more where a CTA cannot have them all.
+constexpr int kShortSlots = 16384;  // of a row that a CTA takes where there are many: three CTAs' keys an SM
+
+// `longest`: slots of a row at most, which the tables' width gives, not the sequences' lengths.  With few pairs a
+// launch has clusters of as many CTAs a row as the SMs hold at once, of 4096 slots at least (4 x 8 rows of 65536: select
+// kernel 203 us with a CTA a row, 35 with four).  With many and wide tables one launch has a CTA for each row of up to
+// kShortSlots, and another few clusters that take the longer ones in turn.
 // Threads: as many as leave all CTAs on the SMs at once (64 registers each), of eight slots at least.
 cudaError_t launch_select(const EvictArgs& a, int pairs, int longest, int sms, cudaStream_t stream) {
   EvictArgs args = a;
-  int ranks = 1;
-  while (ranks < 8 && ((pairs * 2 * ranks <= sms && longest / (2 * ranks) >= 4096) || longest > ranks * kEvictSlots)) ranks *= 2;
-  const int most = ((longest + ranks - 1) / ranks + 3) & ~3;
   args.wide = (a.st.stride & 3) == 0 && ((reinterpret_cast<uintptr_t>(a.st.scores) | reinterpret_cast<uintptr_t>(a.st.slot_pos)) & 15u) == 0;
-  int threads = kEvictMinThreads;
-  while (threads < kEvictMaxThreads && most > 8 * threads &&
-         (pairs * ranks <= sms * (kEvictMaxThreads / (2 * threads)) || most > 32 * threads))
-    threads *= 2;
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3((unsigned)pairs * (unsigned)ranks);
-  cfg.blockDim = dim3(threads);
-  cfg.dynamicSmemBytes = sizeof(uint32_t) * (size_t)most;
-  cfg.stream = stream;
-  cudaLaunchAttribute attr[2];
-  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr[0].val.programmaticStreamSerializationAllowed = 1;
-  attr[1].id = cudaLaunchAttributeClusterDimension;
-  attr[1].val.clusterDim.x = (unsigned)ranks;
-  attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
-  cfg.attrs = attr;
-  cfg.numAttrs = ranks > 1 ? 2 : 1;
-  void* params[] = {&args};
-  return cudaLaunchKernelExC(&cfg, ranks > 1 ? (const void*)evict_select_kernel<true> : (const void*)evict_select_kernel<false>, params);
+  auto launch = [&](const void* kernel, int ctas, int ranks, int slots, int above) {
+    const int most = ((slots + ranks - 1) / ranks + 3) & ~3;
+    int threads = kEvictMinThreads;
+    while (threads < kEvictMaxThreads && most > 8 * threads &&
+           (ctas <= sms * (kEvictMaxThreads / (2 * threads)) || most > 32 * threads))
+      threads *= 2;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3((unsigned)ctas);
+    cfg.blockDim = dim3(threads);
+    cfg.dynamicSmemBytes = sizeof(uint32_t) * (size_t)most;
+    cfg.stream = stream;
+    cudaLaunchAttribute attr[2];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    attr[1].id = cudaLaunchAttributeClusterDimension;
+    attr[1].val.clusterDim.x = (unsigned)ranks;
+    attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = ranks > 1 ? 2 : 1;
+    void* params[] = {&args, &above, &slots};
+    return cudaLaunchKernelExC(&cfg, kernel, params);
+  };
+  const void* one = (const void*)evict_select_kernel<false, false>;
+  int ranks = 1;
+  while (ranks < 8 && pairs * 2 * ranks <= sms && longest / (2 * ranks) >= 4096) ranks *= 2;
+  if (longest <= kShortSlots || (pairs * ranks <= sms && longest <= ranks * kEvictSlots))
+    return launch(ranks > 1 ? (const void*)evict_select_kernel<true, false> : one, pairs * ranks, ranks, longest, 0);
+  const cudaError_t e = launch(one, pairs, 1, kShortSlots, 0);
+  if (e != cudaSuccess) return e;
+  ranks = longest > 4 * kShortSlots ? 8 : longest > 2 * kShortSlots ? 4 : 2;
+  return launch((const void*)evict_select_kernel<true, true>, std::max(1, sms / ranks) * ranks, ranks, longest, kShortSlots);
 }
 
 size_t align256e(size_t x) { return (x + 255) & ~size_t(255); }
@@ -806,9 +845,12 @@ int evict_common(void* k, void* v, float* ks, float* vs, const int32_t* block_ta
 
 cudaError_t evict_device_setup() {
   const int bytes = (int)(sizeof(uint32_t) * kEvictSlots);
-  cudaError_t e = cudaFuncSetAttribute((const void*)evict_select_kernel<false>, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
-  if (e == cudaSuccess) e = cudaFuncSetAttribute((const void*)evict_select_kernel<true>, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
-  return e;
+  for (const void* f : {(const void*)evict_select_kernel<false, false>, (const void*)evict_select_kernel<true, false>,
+                        (const void*)evict_select_kernel<true, true>}) {
+    const cudaError_t e = cudaFuncSetAttribute(f, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+    if (e != cudaSuccess) return e;
+  }
+  return cudaSuccess;
 }
 
 }  // namespace pkv

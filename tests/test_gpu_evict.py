@@ -206,6 +206,19 @@ def test_rows_of_odd_length(lens, more):
 
 
 @pytest.mark.gpu
+@pytest.mark.parametrize("mb,long", [(1100, [17600, 16384, 16385, 17001]), (2600, [41000, 16390, 33000]), (5000, [80000, 70001, 16385])])
+@pytest.mark.parametrize("inplace", [False, True])
+def test_many_sequences_in_wide_tables(mb, long, inplace):
+    """More rows than CTAs at a time, most of them far shorter than the tables are wide, a few longer than one CTA takes."""
+    rng = np.random.default_rng(mb)
+    lens = rng.integers(0, 900, 82)
+    lens[rng.choice(82, len(long), replace=False)] = long
+    s = _state(lens.tolist(), 2, 64, mb, mb, scores="few" if inplace else "exp")
+    for rules in ((4, 300, 41), (0, 9000, 0)):
+        _check(s, _call(s, *rules, inplace=inplace), *rules, inplace=inplace)
+
+
+@pytest.mark.gpu
 def test_many_sequences():
     rng = np.random.default_rng(6)
     lens = rng.integers(0, 90, 700).tolist()
