@@ -455,11 +455,11 @@ int decode_common(void* out, const void* q, const void* k_cache, const void* v_c
   // score-emitting variant share one set, so their outputs agree bit for bit; the dense INT8
   // decode (issue-bound) and the gather form have their own.
   const bool dense_q8 = !sparse && q8 != nullptr;
-  a.min_units = std::max(sparse ? PKV_MIN_UNITS_SPARSE : dense_q8 ? PKV_MIN_UNITS_Q8 : diff ? PKV_MIN_UNITS_DIFF : PKV_MIN_UNITS, 1);
+  a.min_units = std::max(sparse ? PKV_MIN_UNITS_SPARSE : dense_q8 ? PKV_MIN_UNITS_Q8 : PKV_MIN_UNITS, 1);
   const int busy_pct = sparse ? (q8 != nullptr ? PKV_MIN_BUSY_PCT_SPARSE_Q8 : PKV_MIN_BUSY_PCT_SPARSE)
-                       : dense_q8 ? PKV_MIN_BUSY_PCT_Q8 : diff ? PKV_MIN_BUSY_PCT_DIFF : PKV_MIN_BUSY_PCT;
+                       : dense_q8 || diff != nullptr ? PKV_MIN_BUSY_PCT_Q8 : PKV_MIN_BUSY_PCT;
   a.min_busy_pct = std::min(std::max(busy_pct, 0), 100);
-  a.tail_pct = std::min(std::max(sparse ? PKV_TAIL_PCT_SPARSE : f8 ? PKV_TAIL_PCT_F8 : dense_q8 ? PKV_TAIL_PCT_Q8 : diff ? PKV_TAIL_PCT_DIFF : PKV_TAIL_PCT, 0), 50);
+  a.tail_pct = std::min(std::max(sparse ? PKV_TAIL_PCT_SPARSE : f8 ? PKV_TAIL_PCT_F8 : dense_q8 ? PKV_TAIL_PCT_Q8 : PKV_TAIL_PCT, 0), 50);
   a.chunk_min = std::max(dense_q8 ? PKV_CHUNK_MIN_Q8 : PKV_CHUNK_MIN, ring);  // never ends inside the tile ring
   a.cpw_cap = (int)std::min<long long>(std::min(PKV_MAX_TAIL_CHUNKS, kMaxTailChunksLimit),
                                        plan.ranges / workers - 1);

@@ -326,7 +326,7 @@ constexpr float kLog2e = 1.4426950408889634f;
 //   those of the second.  The softmax and the product with V are those of the plain form over eight heads.
 //   kDiffWide: up to eight; columns are heads, and each map has its own weights and outputs.
 template <int D, bool SPARSE, bool SCORES, bool Q8, bool F8 = false, bool RULES = false, int DIFF = 0>
-__global__ void __launch_bounds__(kDecodeWarps * 32, Q8 ? (F8 ? PKV_F8_MIN_CTAS : PKV_Q8_MIN_CTAS) : DIFF == kDiffWide ? PKV_DIFF_MIN_CTAS : 0)
+__global__ void __launch_bounds__(kDecodeWarps * 32, Q8 ? (F8 ? PKV_F8_MIN_CTAS : PKV_Q8_MIN_CTAS) : 0)
 decode_split_kernel(const __grid_constant__ DecodeArgs a) {
   static_assert(!(SPARSE && SCORES), "scores are emitted by the dense decode only");
   static_assert(!(F8 && (SPARSE || SCORES || !Q8)) && !(RULES && (SPARSE || (SCORES && !DIFF))), "dense decode only");

@@ -121,10 +121,6 @@ constexpr int kPartFields = kPartOff + kMaxTailChunksLimit + 1;
 #define PKV_F8_MIN_CTAS 12  // FP8 decode: the same bound (14: 53.6 us against 49.1 for 32 x ~4000 tokens)
 #endif
 
-#ifndef PKV_DIFF_MIN_CTAS
-#define PKV_DIFF_MIN_CTAS 0  // differential decode: the same bound
-#endif
-
 #ifndef PKV_MIN_UNITS
 #define PKV_MIN_UNITS 16  // lower bound of a worker slice, in 16-token units
 #endif
@@ -135,7 +131,8 @@ constexpr int kPartFields = kPartOff + kMaxTailChunksLimit + 1;
 // a slice (measured: the 28-layer qwen step over INT8 pools 0.913 -> 0.835 ms, the sparse step
 // over INT8 pools 1.098 -> 1.040 ms), while the bf16 decode keeps the floor (all workers busy
 // made the qwen step 0.911 -> 0.973 ms).  The score-emitting decode keeps the plain decode's
-// partition, so its output stays bit-identical to the plain call's.
+// partition, so its output stays bit-identical to the plain call's.  The differential decode, with two maps a unit,
+// keeps every worker busy too (64 sequences of ~630 tokens, 2 kv heads of 6: 27.8 -> 26.5 us; 32 x ~4000 as it was).
 #ifndef PKV_MIN_UNITS_Q8
 #define PKV_MIN_UNITS_Q8 16
 #endif
@@ -152,15 +149,6 @@ constexpr int kPartFields = kPartOff + kMaxTailChunksLimit + 1;
 // 49.0, 52.8 and 49.0 us).
 #ifndef PKV_TAIL_PCT_F8
 #define PKV_TAIL_PCT_F8 0
-#endif
-#ifndef PKV_MIN_UNITS_DIFF
-#define PKV_MIN_UNITS_DIFF 16
-#endif
-#ifndef PKV_MIN_BUSY_PCT_DIFF
-#define PKV_MIN_BUSY_PCT_DIFF 70
-#endif
-#ifndef PKV_TAIL_PCT_DIFF
-#define PKV_TAIL_PCT_DIFF 20
 #endif
 #ifndef PKV_CHUNK_MIN_Q8
 #define PKV_CHUNK_MIN_Q8 6
