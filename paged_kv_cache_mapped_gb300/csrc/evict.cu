@@ -41,7 +41,7 @@ struct EvictArgs {
   int32_t* to_slot;              // [B * Hkv, budget] the slot that each goes to
   int B, Hkv, NB, MB;
   int n_sink, n_recent, budget, trigger;
-  int wide;                      // 1: rows of scores and slot_pos may be read four slots at a time
+  int wide;                      // 1: rows of scores and slot_pos may be read and written four slots at a time
   int splits;                    // CTAs that share the moves of one (sequence, kv head)
 };
 
@@ -63,19 +63,20 @@ __device__ __forceinline__ EvictSeq evict_seq(const EvictArgs& a, int b) {
   return s;
 }
 
-// Exclusive sum over the block; the total in *total.  `sums` holds 33 ints; two barriers.
-__device__ __forceinline__ int block_sum_before(int v, int* sums, int* total) {
+// Exclusive sum over the block; the total in *total.  `sums` holds 33 ints; two barriers.  T: int or uint32_t.
+template <typename T>
+__device__ __forceinline__ T block_sum_before(T v, int* sums, T* total) {
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, warps = blockDim.x >> 5;
-  int x = v;
+  T x = v;
 #pragma unroll
   for (int o = 1; o < 32; o <<= 1) {
-    const int t = __shfl_up_sync(kFullMask, x, o);
+    const T t = __shfl_up_sync(kFullMask, x, o);
     if (lane >= o) x += t;
   }
   __syncthreads();  // the sums of the call before have been read
-  if (lane == 31) sums[warp] = x;
+  if (lane == 31) sums[warp] = (int)x;
   __syncthreads();
-  int mine = lane < warps ? sums[lane] : 0, before = lane < warp ? mine : 0;
+  T mine = lane < warps ? (T)sums[lane] : T(0), before = lane < warp ? mine : T(0);
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) {
     mine += __shfl_xor_sync(kFullMask, mine, o);
@@ -156,7 +157,9 @@ __device__ __forceinline__ void select_row(const EvictArgs& a, int bg, int upto,
     sh.least = 0xffffffffu;
     sh.most = 0u;
     sh.guarded = 0;
+    sh.n = 0;
   }
+  for (int i = tid; i < kEvictBins; i += T) sh.hist[i] = 0;
   __syncthreads();
   const int recent0 = s.L + s.dropped - a.n_recent;  // (n_recent <= budget < L)
   // this CTA's slots
@@ -167,13 +170,20 @@ __device__ __forceinline__ void select_row(const EvictArgs& a, int bg, int upto,
     return p < a.n_sink || p >= recent0 ? kProtectedKey : order_key(score);
   };
 
-  // ---- keys into shared memory; their range
+  // ---- keys into shared memory; their range.  Scores and positions of the slots below the budget go out at once (those
+  // that are filled get theirs with the rows); the ones past it are read again when what moves is known.
   {
+    const bool same_scores = scores_out == scores, same_pos = pos_out == slot_pos;
+    const int mid = min(end, a.budget) - first;
     uint32_t least = 0xffffffffu, most = 0u;
     int guarded = 0;
     bool nan = false;
     const float* sc = scores + first;
     const int32_t* sp = slot_pos + first;
+    auto keep = [&](int j, float x, int p) {
+      if (!same_scores) scores_out[first + j] = x;
+      if (!same_pos || p < 0) pos_out[first + j] = place(p, first + j);
+    };
     auto take = [&](int j, float x, int p) {
       const uint32_t k = make_key(p, first + j, x);
       nan |= k == 0u;
@@ -198,6 +208,16 @@ __device__ __forceinline__ void select_row(const EvictArgs& a, int bg, int upto,
         for (int q = 0; q < kEvictWide; ++q) {
           const int j = 4 * (v0 + q * T);
           if (j >= own) continue;
+          if (j + 3 < mid) {
+            if (!same_scores) reinterpret_cast<float4*>(scores_out + first)[j >> 2] = x[q];
+            const int i = first + j;
+            const int4 y = make_int4(place(p[q].x, i), place(p[q].y, i + 1), place(p[q].z, i + 2), place(p[q].w, i + 3));
+            if (!same_pos || (p[q].x | p[q].y | p[q].z | p[q].w) < 0) reinterpret_cast<int4*>(pos_out + first)[j >> 2] = y;
+          } else if (j < mid) {  // one to three of the four
+            keep(j, x[q].x, p[q].x);
+            if (j + 1 < mid) keep(j + 1, x[q].y, p[q].y);
+            if (j + 2 < mid) keep(j + 2, x[q].z, p[q].z);
+          }
           uint4 k;
           k.x = take(j, x[q].x, p[q].x);
           k.y = j + 1 < own ? take(j + 1, x[q].y, p[q].y) : kProtectedKey;
@@ -218,8 +238,11 @@ __device__ __forceinline__ void select_row(const EvictArgs& a, int bg, int upto,
           }
         }
 #pragma unroll
-        for (int q = 0; q < kEvictBatch; ++q)
-          if (j0 + q * T < own) s_keys[j0 + q * T] = take(j0 + q * T, x[q], p[q]);
+        for (int q = 0; q < kEvictBatch; ++q) {
+          const int j = j0 + q * T;
+          if (j < own) s_keys[j] = take(j, x[q], p[q]);
+          if (j < mid) keep(j, x[q], p[q]);
+        }
       }
       // (the passes below read four keys at a time; a protected one is not counted there)
       if (tid < (-own & 3)) s_keys[own + tid] = kProtectedKey;
@@ -254,7 +277,7 @@ __device__ __forceinline__ void select_row(const EvictArgs& a, int bg, int upto,
       sh.cut = need < 0 ? 1 : 0;
     }
   } else {
-    bool above_zero = true;
+    bool above_zero = true, clean = true;
     if (lo > hi || hi <= kZeroKey) {  // no score is positive
       lo = 0u;
       hi = kZeroKey;
@@ -271,9 +294,11 @@ __device__ __forceinline__ void select_row(const EvictArgs& a, int bg, int upto,
         break;
       }
       const int shift = max(0, 32 - __clz(range) - 11);
-      for (int i = tid; i < kEvictBins; i += T) sh.hist[i] = 0;
-      if (tid == 0) sh.n = 0;
-      __syncthreads();
+      if (!clean) {
+        for (int i = tid; i < kEvictBins; i += T) sh.hist[i] = 0;
+        __syncthreads();
+      }
+      clean = false;
       const uint4* keys4 = reinterpret_cast<const uint4*>(s_keys);
 #pragma unroll 2
       for (int v = tid; v < (own + 3) >> 2; v += T) {
@@ -433,11 +458,12 @@ __device__ __forceinline__ void select_row(const EvictArgs& a, int bg, int upto,
   const int low = max(0, min(min(32, j1 - w0), a.budget - first - w0));
   const uint32_t front = low == 32 ? kFullMask : (1u << low) - 1u;
   const uint32_t gone = front & ~stay, late = stay & ~front;  // slots that are filled, slots that go there
-  const int to_upto = sum_to_lane(__popc(gone)), from_upto = sum_to_lane(__popc(late));
-  int to = __shfl_sync(kFullMask, to_upto, 31), from = __shfl_sync(kFullMask, from_upto, 31);
-  int n_to, n_from;
-  to = __shfl_sync(kFullMask, block_sum_before(lane == 0 ? to : 0, sh.sums, &n_to), 0);
-  from = __shfl_sync(kFullMask, block_sum_before(lane == 0 ? from : 0, sh.sums, &n_from), 0);
+  // both counts in a word (together at most kEvictSlots)
+  const uint32_t upto_lane = (uint32_t)sum_to_lane(__popc(gone) | __popc(late) << 16);
+  uint32_t all;
+  const uint32_t of_warp = __shfl_sync(kFullMask, upto_lane, 31);
+  const uint32_t start = __shfl_sync(kFullMask, block_sum_before(lane == 0 ? of_warp : 0u, sh.sums, &all), 0);
+  const int to = (int)(start & 0xffffu), from = (int)(start >> 16), n_to = (int)(all & 0xffffu), n_from = (int)(all >> 16);
   int to0 = 0, from0 = 0, n = n_from;  // places of this CTA's first ones, and all moves
   if constexpr (CLUSTER) {
     if (tid == 0) {
@@ -464,7 +490,8 @@ __device__ __forceinline__ void select_row(const EvictArgs& a, int bg, int upto,
 #pragma unroll 2
   for (int t = 0; t < n_words; ++t) {
     const uint32_t g = __shfl_sync(kFullMask, gone, t), l = __shfl_sync(kFullMask, late, t);
-    const int g1 = __shfl_sync(kFullMask, to_upto, t), l1 = __shfl_sync(kFullMask, from_upto, t);
+    const uint32_t upto_word = __shfl_sync(kFullMask, upto_lane, t);
+    const int g1 = (int)(upto_word & 0xffffu), l1 = (int)(upto_word >> 16);
     const int i = first + j0 + 32 * t + lane;
     if ((g >> lane) & 1u) s_to[to + g1 - __popc(g & ~below)] = i;
     if ((l >> lane) & 1u) s_from[from + l1 - __popc(l & ~below)] = i;
@@ -507,28 +534,6 @@ __device__ __forceinline__ void select_row(const EvictArgs& a, int bg, int upto,
       if (m < n_to) {
         moves[to0 + m].y = pool_slot(j[q], blk_j[q]);
         to_slot[to0 + m] = j[q];
-      }
-    }
-  }
-  // ---- scores and positions: of the slots below the budget (those that are filled get theirs with the rows), and past it
-  const int mid = min(end, a.budget);
-  for (int i0 = first + tid; i0 < mid; i0 += kEvictBatch * T) {
-    float x[kEvictBatch];
-    int p[kEvictBatch];
-#pragma unroll
-    for (int q = 0; q < kEvictBatch; ++q) {
-      const int i = i0 + q * T;
-      if (i < mid) {
-        x[q] = scores[i];
-        p[q] = slot_pos[i];
-      }
-    }
-#pragma unroll
-    for (int q = 0; q < kEvictBatch; ++q) {
-      const int i = i0 + q * T;
-      if (i < mid) {
-        scores_out[i] = x[q];
-        pos_out[i] = place(p[q], i);
       }
     }
   }
@@ -711,7 +716,8 @@ constexpr int kShortSlots = 16384;  // of a row that a CTA takes where there are
 // Threads: as many as leave all CTAs on the SMs at once (64 registers each), of eight slots at least.
 cudaError_t launch_select(const EvictArgs& a, int pairs, int longest, int sms, cudaStream_t stream) {
   EvictArgs args = a;
-  args.wide = (a.st.stride & 3) == 0 && ((reinterpret_cast<uintptr_t>(a.st.scores) | reinterpret_cast<uintptr_t>(a.st.slot_pos)) & 15u) == 0;
+  args.wide = (a.st.stride & 3) == 0 && aligned16(a.st.scores) && aligned16(a.st.slot_pos) && aligned16(a.st.scores_out) &&
+              aligned16(a.st.slot_pos_out);
   auto launch = [&](const void* kernel, int ctas, int ranks, int slots, int above) {
     const int most = ((slots + ranks - 1) / ranks + 3) & ~3;
     int threads = kEvictMinThreads;
