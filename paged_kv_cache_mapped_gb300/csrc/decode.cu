@@ -1771,6 +1771,7 @@ __global__ void __launch_bounds__(kScoreThreads) decode_diff_score_kernel(const 
     const size_t at = (size_t)seg * a.score_stride + t0;
     const bool vec = (a.score_stride & 3) == 0 && t0 + 4 <= end &&
                      ((reinterpret_cast<uintptr_t>(a.scores) | reinterpret_cast<uintptr_t>(a.scores_out)) & 15u) == 0;
+    const int blk = a.block_tables[(size_t)b * a.MB + (t0 >> 4)];
     float sum[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll 4
     for (int i = 0; i < group; ++i) {
@@ -1794,9 +1795,10 @@ __global__ void __launch_bounds__(kScoreThreads) decode_diff_score_kernel(const 
         sum[e] += fabsf(w1 - lam * w2);
       }
     }
-    // (the logits of keys that the query does not see were not written)
+    // (the logits of keys that the query does not see, or whose block is bad, were not written)
+    const bool known = blk >= 0 && blk < a.NB;
 #pragma unroll
-    for (int e = 0; e < 4; ++e) sum[e] = t0 + e >= u.s.lo || t0 + e < u.pre ? sum[e] : 0.f;
+    for (int e = 0; e < 4; ++e) sum[e] = known && (t0 + e >= u.s.lo || t0 + e < u.pre) ? sum[e] : 0.f;
     if (vec) {
       float4 o = *reinterpret_cast<const float4*>(a.scores + at);
       o.x += sum[0];

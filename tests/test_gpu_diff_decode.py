@@ -259,6 +259,27 @@ def test_a_length_past_the_scores_and_bad_inputs():
 
 
 @pytest.mark.gpu
+@pytest.mark.parametrize("hq", [4, 12], ids=["pairs", "wide"])
+@pytest.mark.parametrize("stride", [320, 321])
+def test_keys_of_a_bad_block_get_no_weight(hq, stride):
+    """After a call on the same workspace whose keys there had weights: those scores stay, bit for bit."""
+    c = _case([300, 77], hq, 2, 64, 12, fill=0.0)
+    err = pkv.new_error_word(DEV)
+    ws = torch.zeros((pkv.diff_decode_workspace_bytes(2, hq, 2, 64, c["pools"][0].shape[0], c["bt"].shape[1], score_stride=stride),),
+                     dtype=torch.uint8, device=DEV)
+    before = torch.rand((2, 2, stride), device=DEV)
+    _call(c, scores=before.clone(), workspace=ws, error_word=err)
+    assert pkv.read_error(err) == 0
+    for x in (-1, c["pools"][0].shape[0]):
+        c["bt"][0, 3] = x
+        after = before.clone()
+        _call(c, scores=after, workspace=ws, error_word=err)
+        assert pkv.read_error(err, clear=True) == C["PKV_DEV_BAD_BLOCK_ID"]
+        assert torch.equal(after[0, :, 48:64], before[0, :, 48:64])
+        assert (after[0, :, :48] > before[0, :, :48]).all() and (after[0, :, 64:300] > before[0, :, 64:300]).all()
+
+
+@pytest.mark.gpu
 def test_inputs_ready_streams_graphs_and_one_workspace():
     cases = [_case([300, 2, 1000], 8, 2, 128, s) for s in (12, 13)]
     want = [_call(c) for c in cases]
