@@ -1216,7 +1216,8 @@ __device__ __forceinline__ void diff_rows(const PrefillAttnArgs& a, Shared<D, 2,
       found |= non_finite_v<D>(a, row, w.L);
     }
   }
-  const bool owes = two || !(l0 <= 3.4028234e38f) || !(l1 <= 3.4028234e38f) || found != 1;
+  const bool own = found == 0 && !split && !(fabsf(lam) <= 3.4028234e38f);  // it comes from lambda
+  const bool owes = two || !(l0 <= 3.4028234e38f) || !(l1 <= 3.4028234e38f) || (found != 1 && !own);
   again = __ballot_sync(kFullMask, row_bad && owes);
   while (again != 0u) {
     const int src = __ffs(again) - 1;
@@ -1523,6 +1524,11 @@ __device__ __forceinline__ void softmax_rows(const PrefillAttnArgs& a, Shared<D,
   }
 }
 
+// The rules of a call that need each key's own logit, as softmax_rows' MODE (0 to 3).
+__host__ __device__ inline int rules_mode(const PrefillAttnArgs& a) {
+  return (a.cap_log2 > 0.f ? 1 : 0) | (a.slopes != nullptr || !(a.scale_log2 > 0.f) ? 2 : 0);
+}
+
 // RULES: softmax_rows' MODE for the whole launch, or kAnyRules: by the arguments.  (A differential chunk of 4096 on 16384
 // keys takes 1350 us with its own kernel and 1395 with four loops in one, one loop's code being all that runs.)
 constexpr int kAnyRules = -1;
@@ -1581,7 +1587,7 @@ prefill_attention_kernel(const __grid_constant__ PrefillAttnArgs a) {
     const int x = warp >> 2, r = 32 * (warp & 3) + lane;
     const int tok = r / a.G, head = r - tok * a.G;
     uint32_t n_step = 0;
-    const int mode = (a.cap_log2 > 0.f ? 1 : 0) | (a.slopes != nullptr || !(a.scale_log2 > 0.f) ? 2 : 0);
+    const int mode = rules_mode(a);
     for (int it = blockIdx.x; it < total; it = sh.next, rec0 = sh.record[0], rec1 = sh.record[1]) {
       Item w = item_of(a, it, rec0, rec1, NT, DIFF);
       if (threadIdx.x == 0) {
@@ -1698,52 +1704,52 @@ __global__ void __launch_bounds__(256) prefill_merge_kernel(const PrefillAttnArg
     float y[E] = {};
 #pragma unroll
     for (int map = 0; map < M; ++map) {
-    float2 ml[2];
-    float m = -INFINITY;
+      float2 ml[2];
+      float m = -INFINITY;
 #pragma unroll
-    for (int q = 0; q < 2; ++q) {
-      const int sh = lane + 32 * q;
-      ml[q] = sh < split.z ? __ldcg(a.part_ml + (p0 + (long long)sh * per) * M + map) : make_float2(-INFINITY, 0.f);
-      m = fmaxf(m, ml[q].x);
-    }
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(kFullMask, m, o));
-    const float ref = m == -INFINITY ? 0.f : m;
-    float w[2], l = 0.f;
-#pragma unroll
-    for (int q = 0; q < 2; ++q) {
-      w[q] = exp2f(ml[q].x - ref);  // 0 for a share that saw nothing
-      l += w[q] * ml[q].y;
-    }
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) l += __shfl_xor_sync(kFullMask, l, o);
-    float o[E] = {};
-#pragma unroll 4
-    for (int sh = 0; sh < split.z; ++sh) {
-      const float f = __shfl_sync(kFullMask, sh < 32 ? w[0] : w[1], sh & 31);
-      const float* src = a.part_o + ((p0 + (long long)sh * per) * M + map) * D + lane * E;
-      float x[E];
-      if constexpr (E == 4) {
-        const float4 t = __ldcg(reinterpret_cast<const float4*>(src));
-        x[0] = t.x; x[1] = t.y; x[2] = t.z; x[3] = t.w;
-      } else {
-        const float2 t = __ldcg(reinterpret_cast<const float2*>(src));
-        x[0] = t.x; x[1] = t.y;
+      for (int q = 0; q < 2; ++q) {
+        const int sh = lane + 32 * q;
+        ml[q] = sh < split.z ? __ldcg(a.part_ml + (p0 + (long long)sh * per) * M + map) : make_float2(-INFINITY, 0.f);
+        m = fmaxf(m, ml[q].x);
       }
 #pragma unroll
-      for (int e = 0; e < E; ++e) o[e] = f == 0.f ? o[e] : fmaf(f, x[e], o[e]);
-    }
-    const float inv = l > 0.f ? 1.f / l : (l == l ? 0.f : l);
-    if constexpr (DIFF) {
-      const int tok = in / a.Hq, h = in - tok * a.Hq;
-      float f = inv;
-      if (map == 1) f = l != 0.f ? -inv * __ldg(a.lambdas + (size_t)(split.x + tok) * a.lambda_stride + h) : 0.f;
+      for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(kFullMask, m, o));
+      const float ref = m == -INFINITY ? 0.f : m;
+      float w[2], l = 0.f;
 #pragma unroll
-      for (int e = 0; e < E; ++e) y[e] = map == 0 ? o[e] * f : fmaf(o[e], f, y[e]);
-    } else {
+      for (int q = 0; q < 2; ++q) {
+        w[q] = exp2f(ml[q].x - ref);  // 0 for a share that saw nothing
+        l += w[q] * ml[q].y;
+      }
 #pragma unroll
-      for (int e = 0; e < E; ++e) y[e] = o[e] * inv;
-    }
+      for (int o = 16; o > 0; o >>= 1) l += __shfl_xor_sync(kFullMask, l, o);
+      float o[E] = {};
+#pragma unroll 4
+      for (int sh = 0; sh < split.z; ++sh) {
+        const float f = __shfl_sync(kFullMask, sh < 32 ? w[0] : w[1], sh & 31);
+        const float* src = a.part_o + ((p0 + (long long)sh * per) * M + map) * D + lane * E;
+        float x[E];
+        if constexpr (E == 4) {
+          const float4 t = __ldcg(reinterpret_cast<const float4*>(src));
+          x[0] = t.x; x[1] = t.y; x[2] = t.z; x[3] = t.w;
+        } else {
+          const float2 t = __ldcg(reinterpret_cast<const float2*>(src));
+          x[0] = t.x; x[1] = t.y;
+        }
+#pragma unroll
+        for (int e = 0; e < E; ++e) o[e] = f == 0.f ? o[e] : fmaf(f, x[e], o[e]);
+      }
+      const float inv = l > 0.f ? 1.f / l : (l == l ? 0.f : l);
+      if constexpr (DIFF) {
+        const int tok = in / a.Hq, h = in - tok * a.Hq;
+        float f = inv;
+        if (map == 1) f = l != 0.f ? -inv * __ldg(a.lambdas + (size_t)(split.x + tok) * a.lambda_stride + h) : 0.f;
+#pragma unroll
+        for (int e = 0; e < E; ++e) y[e] = map == 0 ? o[e] * f : fmaf(o[e], f, y[e]);
+      } else {
+#pragma unroll
+        for (int e = 0; e < E; ++e) y[e] = o[e] * inv;
+      }
     }
     if constexpr (DIFF) {
       if (a.norm_weight != nullptr) {
@@ -1788,11 +1794,6 @@ PrefillWorkspace plan_prefill(long long B, long long T, int Hq, int G, int D, in
 }
 
 size_t plan_smem_bytes(int B) { return sizeof(int) * (4 * (size_t)B + 1); }
-
-// The rules of a call that need each key's own logit, as softmax_rows' MODE.
-__host__ __device__ inline int rules_mode(const PrefillAttnArgs& a) {
-  return (a.cap_log2 > 0.f ? 1 : 0) | (a.slopes != nullptr || !(a.scale_log2 > 0.f) ? 2 : 0);
-}
 
 template <int D, int NT, bool DIFF>
 const void* attention_kernel(int mode) {

@@ -357,6 +357,27 @@ def test_other_streams_graph_and_steps_without_an_entry():
 
 
 @pytest.mark.gpu
+@pytest.mark.parametrize("bad", [float("nan"), float("inf")])
+def test_cost_of_a_factor_that_is_no_number(bad):
+    """A prompt of 4096 tokens, the factor of one head NaN or infinite: that head's rows are no numbers by right
+    and are not worked out twice, and the others are as ever."""
+    c = _case([4096], [4096], 8, 2, 128, 35, per_row=False)
+    ins = [c["q"].to(DEV), *c["pools"], c["bt"], torch.tensor([4096], dtype=torch.int32, device=DEV), torch.from_numpy(c["starts"]).to(DEV)]
+    lam = c["lam"].to(DEV)
+    want = pkv.paged_diff_prefill_attention(*ins, lam, c["scale"])
+    lam[3] = bad
+    a, b = torch.cuda.Event(enable_timing=True), torch.cuda.Event(enable_timing=True)
+    a.record()
+    got = pkv.paged_diff_prefill_attention(*ins, lam, c["scale"])
+    b.record()
+    torch.cuda.synchronize()
+    assert not torch.isfinite(got[:, 3]).any()
+    others = [0, 1, 2, 4, 5, 6, 7]
+    assert torch.equal(got[:, others], want[:, others])
+    assert a.elapsed_time(b) < 10.0
+
+
+@pytest.mark.gpu
 def test_device_errors():
     c = _case([100, 60, 40], [50, 60, 1], 4, 2, 128, 13)
     good = _call(c)
