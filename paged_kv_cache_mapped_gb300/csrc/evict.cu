@@ -112,8 +112,10 @@ __device__ __forceinline__ uint32_t order_key(float s) {
   return (u & 0x80000000u) ? ~u : (u | 0x80000000u);
 }
 
+static_assert(kEvictBins >= 2 * kEvictMaxThreads, "two bins a thread");
+
 struct EvictShared {
-  int hist[kEvictBins];
+  alignas(8) int hist[kEvictBins];
   uint32_t list[kEvictMaxThreads];
   int sums[33];
   uint32_t least, most, key;  // least key of a positive score (less the key of zero), greatest unprotected one (plus 1)
@@ -310,23 +312,22 @@ __device__ __forceinline__ void select_row(const EvictArgs& a, int bg, int upto,
       }
       sync_all();
       // a thread's bins of the whole row, and the keys in the bins past them
-      const int per = kEvictBins / T;  // (T divides it)
+      const int per = kEvictBins / T;  // two at least (T divides it)
       int h[kEvictBins / kEvictMinThreads], sum = 0;
 #pragma unroll
       for (int q = 0; q < kEvictBins / kEvictMinThreads; ++q) h[q] = 0;
-      if constexpr (CLUSTER) {
 #pragma unroll
-        for (int r = 0; r < 8; ++r) {
-          if (r >= ranks) break;
-          const EvictShared* o = of_rank(r);
+      for (int r = 0; r < (CLUSTER ? 8 : 1); ++r) {
+        if (r >= ranks) break;
+        const int2* o = reinterpret_cast<const int2*>(of_rank(r)->hist + tid * per);
 #pragma unroll
-          for (int q = 0; q < kEvictBins / kEvictMinThreads; ++q)
-            if (q < per) h[q] += o->hist[tid * per + q];
+        for (int q = 0; q < kEvictBins / kEvictMinThreads; q += 2) {
+          if (q < per) {
+            const int2 x = o[q >> 1];
+            h[q] += x.x;
+            h[q + 1] += x.y;
+          }
         }
-      } else {
-#pragma unroll
-        for (int q = 0; q < kEvictBins / kEvictMinThreads; ++q)
-          if (q < per) h[q] = sh.hist[tid * per + q];
       }
 #pragma unroll
       for (int q = 0; q < kEvictBins / kEvictMinThreads; ++q) sum += h[q];
@@ -480,6 +481,7 @@ __device__ __forceinline__ void select_row(const EvictArgs& a, int bg, int upto,
       }
       n += o->from;
     }
+    cluster_arrive();  // (the counts have been read; no CTA may leave before)
   }
   if (tid == 0 && rank == 0) a.count[bg] = n;
   // The CTA's slots as lists, in place of the keys; then all that the rows' kernel needs of them.  (That kernel joins
@@ -537,11 +539,21 @@ __device__ __forceinline__ void select_row(const EvictArgs& a, int bg, int upto,
       }
     }
   }
-  sync_all();  // the moved slots' values, and (a cluster) the counts, have been read
-  for (int i = max(first, a.budget) + tid; i < end; i += T) {
+  __syncthreads();  // the moved slots' values have been read
+  const int z0 = max(first, a.budget), z1 = a.wide ? min((z0 + 3) & ~3, end) : end, z2 = a.wide ? max(z1, end & ~3) : end;
+  for (int i = z0 + tid; i < z1; i += T) {
     scores_out[i] = 0.f;
     pos_out[i] = -1;
   }
+  for (int i = z1 + 4 * tid; i < z2; i += 4 * T) {
+    *reinterpret_cast<float4*>(scores_out + i) = make_float4(0.f, 0.f, 0.f, 0.f);
+    *reinterpret_cast<int4*>(pos_out + i) = make_int4(-1, -1, -1, -1);
+  }
+  for (int i = z2 + tid; i < end; i += T) {
+    scores_out[i] = 0.f;
+    pos_out[i] = -1;
+  }
+  if constexpr (CLUSTER) cluster_wait();
 }
 
 // A CTA or cluster a row; or, MANY, few clusters that take the rows of more than `above` slots in turn.  (Apart: in the loop

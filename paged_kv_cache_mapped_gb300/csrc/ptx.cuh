@@ -499,6 +499,10 @@ __device__ __forceinline__ float ex2_approx(float x) {
   return y;
 }
 
+// The cluster's barrier in two parts, for every thread of its CTAs.
+__device__ __forceinline__ void cluster_arrive() { asm volatile("barrier.cluster.arrive;" ::: "memory"); }
+__device__ __forceinline__ void cluster_wait() { asm volatile("barrier.cluster.wait;" ::: "memory"); }
+
 // Barrier number `id` of `threads` threads of the block; whether `p` holds in any of them.
 __device__ __forceinline__ bool named_barrier_or(int id, int threads, bool p) {
   int any;
