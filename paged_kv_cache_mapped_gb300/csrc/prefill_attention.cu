@@ -29,6 +29,15 @@
 // where a few keys or equal weights carry a row, and averages out where many unequal ones do.  Shorter rows, where few weights may carry the result, add the
 // remainder as a second term, which costs half as many MMAs again (all rows in two terms: chunk of 4096 on 16384
 // 937 us against 730; none: 24 mixed sequences 26.3 against 28.5).
+// Differential attention (DIFF): out = sum_t (a_1,t - lambda a_2,t) V_t and a norm, the maps from the halves of q and K.  An
+// item's two row tiles are the two maps of the same 128 rows, so a CTA's K and V tiles serve both, each map's S takes
+// half the products, and the difference is made from the two outputs in tensor memory at the item's end.  Twice the exponentials
+// and one and a half times the products of the plain form, and the same chain of a step bounds it: 4096 tokens on 16384 keys 1390 us
+// (1.04 PFLOP/s, 54 % of the measured bf16 rate; tensor pipe 50 %, issue 52 %, exponentials 30 %); 4 prompts of 3000, d 64, 8 heads with a
+// bias 112 us (tensor pipe 18 %, issue 46 %, exponentials 21 %); 24 mixed sequences 53 us, a chain of plan, loads, few steps and merge.
+// The maps' rounding errors add while their outputs subtract, so the nearest sixth of a longer row's steps takes two terms as well:
+// the error against 64 bits, in that of bf16 outputs alone, is 1.48 (chunk; no step 1.55, 1327 us; an eighth of them 1.50, 1379 us) and
+// 1.03 (prompts with the bias, whose weights lie near; no step 1.32, 109 us).
 // Non-finite V: a masked key's weight is 0, and 0 * NaN is NaN, so V rows past the sequence are cleared,
 // and an output row that owes a NaN to a masked key is computed again over what it sees.
 // Every wait is bounded; bad block ids are cleared tiles, recorded.
@@ -81,6 +90,7 @@ constexpr int kStepBlocks = kStep / 16;
 constexpr int kHalf = kKeys * 128;   // bytes of one 64-element half of a tile
 constexpr float kSlack = 8.0f;       // the running maximum moves only when exceeded by this (base 2)
 constexpr int kTwoTermTiles = 4;     // rows over at most this many key tiles take P as two bf16 terms (above)
+constexpr int kTwoTermShare = 6;     // of the other rows' steps, one in this many where maps are subtracted (above)
 constexpr int kMinChunk = 4;         // key tiles of a share at least where items outnumber the CTAs
 
 // DIFF: differential attention.  The two row tiles of an item are the two maps of the same 128 rows, from the
@@ -693,6 +703,13 @@ __device__ __forceinline__ Steps steps_of(const PrefillAttnArgs& a, const Item& 
   return Steps{min(w.ns - 1, (e_last - e_base) >> 2), max(0, (e_first - e_base) >> 2)};
 }
 
+// The step of this share from which on weights are two bf16 terms (see the header).
+template <bool DIFF>
+__device__ __forceinline__ int two_terms_from(const Item& w) {
+  if (w.nt_all <= kTwoTermTiles) return 0;
+  return DIFF ? 2 * (w.nt_all - w.ts) - (2 * w.nt_all + kTwoTermShare - 2) / kTwoTermShare : 0x7fffffff;
+}
+
 template <int D, int NT, bool DIFF = false>
 struct Shared {
   uint64_t q_full, kv_full[Geo<D, NT, DIFF>::kSlots], kv_empty[Geo<D, NT, DIFF>::kSlots];
@@ -831,7 +848,7 @@ __device__ __forceinline__ void issue_mmas(const PrefillAttnArgs& a, Shared<D, N
     pass(0, nt);
     return;
   }
-  const bool two = uniform((uint32_t)w.nt_all) <= (uint32_t)kTwoTermTiles;
+  const int two_from = (int)uniform((uint32_t)two_terms_from<DIFF>(w));
   const uint32_t step0 = uniform(n_step);
   const uint32_t s0 = uniform(tmem_any) + y * 2 * kStep, o = uniform(tmem_any) + NT * 2 * kStep + y * D;
   constexpr uint32_t kTile16 = GE::kTile / 16, kStep16 = kStep * 128 / 16;  // descriptors count 16 bytes
@@ -859,7 +876,7 @@ __device__ __forceinline__ void issue_mmas(const PrefillAttnArgs& a, Shared<D, N
 #pragma unroll
     for (int k = 0; k < kStep / 16; ++k)  // 32 keys' first terms, then their remainders, 16 columns each
       umma_bf16_ts_lo(leader, o, p + 32 * (k >> 1) + 8 * (k & 1), vb + k * 128, id_pv, k > 0 || j < hi);
-    if (two) {
+    if (j >= two_from) {
 #pragma unroll
       for (int k = 0; k < kStep / 16; ++k)
         umma_bf16_ts_lo(leader, o, p + 32 * (k >> 1) + 16 + 8 * (k & 1), vb + k * 128, id_pv, true);
@@ -1251,7 +1268,8 @@ __device__ __forceinline__ void softmax_rows(const PrefillAttnArgs& a, Shared<D,
   const bool bias = MODE == 4 ? a.slopes != nullptr || !(a.scale_log2 > 0.f) : (MODE & 2) != 0;
   const float slope2 = bias && valid && a.slopes != nullptr ? __ldg(a.slopes + h) * kLog2e : 0.f;
   const int pre = valid ? w.pre : 0;
-  const bool two = w.nt_all <= kTwoTermTiles;
+  const bool short_row = w.nt_all <= kTwoTermTiles;
+  const int two_from = two_terms_from<DIFF>(w);
   // the cap as a polynomial of S: u = S ku, the logit cap_log2 u P(u^2)
   const float ku = a.scale_log2 * a.cap_in * 0.34657359f, ku_size = fabsf(ku) < 1e3f ? fabsf(ku) : INFINITY;
   const Steps range = steps_of(a, w, xt, sh.lo_least[x]);
@@ -1308,6 +1326,7 @@ __device__ __forceinline__ void softmax_rows(const PrefillAttnArgs& a, Shared<D,
     // the logits: the step's nearest key lies within twice that below the bound, so where that is 2^80 or less
     // the bound serves as the maximum (the weights stay within fp32 and bf16 range), and the cap and the bias
     // are part of the exponent's FMAs
+    const bool two = j >= two_from;
     bool fast = full && !two;
     float mx = -INFINITY, base = 0.f;
     Logits y{a.scale_log2, 0.f, 0.f};
@@ -1499,14 +1518,14 @@ __device__ __forceinline__ void softmax_rows(const PrefillAttnArgs& a, Shared<D,
     row.pre = pre;
     int found = 0;
     for (int full = 0; full < 2; ++full) {  // (a masked key is in a step with a mask; in the others one key is enough)
-      for (int j = range.hi; j >= range.lo && !two && !(full && (found & 1)); --j) {
+      for (int j = range.hi; j >= range.lo && !short_row && !(full && (found & 1)); --j) {
         if (((j >= full0 && j < full1) || j < full_pre) != (full != 0)) continue;
         row.e0 = e_base + j * kStepBlocks;
         row.e1 = min(row.e0 + kStepBlocks, w.nblk);
         found |= non_finite_v<D>(a, row, w.L);
       }
     }
-    const bool owes = two || !(l <= 3.4028234e38f) || found != 1;
+    const bool owes = short_row || !(l <= 3.4028234e38f) || found != 1;
     again = __ballot_sync(kFullMask, valid && bad && owes);
     __syncwarp();  // the rows are stored by other lanes after this one's stores
     while (again != 0u) {
