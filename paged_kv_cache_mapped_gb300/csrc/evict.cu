@@ -12,6 +12,17 @@
 //    rows to go there, scores and positions.
 //  * evict_move_kernel: the rows, many CTAs for each (sequence, kv head); one more CTA does the lengths and the
 //    free stack.
+//
+// What has to move: 8 bytes a slot and kv head of scores and positions, as many written, and each moved row of K and
+// of V read and written.  What bounds it (calls in a graph):
+//  * 32 sequences of ~4000 bf16 tokens cut to 1540, 8 heads of 128: 65 us.  Profiled alone 16 for the selection and 51 for
+//    the rows, at 71 % of peak DRAM (whole 256-byte rows, reads and writes mixed).
+//  * 4 of 65536 cut to 8191: 81 us.  The kept rows behind the budget lie one or two in a block, and such single rows reach
+//    48 % of peak DRAM (53 us; CTAs for twice or three times the rows in flight change nothing; five resident ones an
+//    SM 77 us in all, but 66.3 for the case above).  The selection's 47000 cycles in a cluster of four are 9500 of loads and ten
+//    steps of 2500 to 4500 between barriers.
+//  * 64 of 1800 INT8 tokens, 270 moved a head: 18 us; 2 of 300: 11 us.  Two launches and a chain of latencies:
+//    lengths, slots, histogram, scan, list, rank, words, lists, moves, then count, moves, rows.
 #include <cooperative_groups.h>
 
 #include <algorithm>
@@ -91,8 +102,9 @@ __device__ __forceinline__ T block_sum_before(T v, int* sums, T* total) {
 // Keys are the scores mapped to uint32 in their order (a protected token has the largest, a NaN the
 // smallest).  The key of the last place is found in rounds: a histogram of 2048 equal bins over the range of
 // keys that are left (in the first round those of positive scores, from their own least to their greatest, so that
-// the few exponents of real scores fill many bins; the others only if the positive ones do not suffice), then the bin that holds it, until at most a thread's worth of keys each
-// is left, which are ranked against one another.  Three rounds at most end in a range of one key.
+// the few exponents of real scores fill many bins; the others only if the positive ones do not suffice), then the bin that
+// holds it, until at most a key a thread is left, which are ranked against one another.  32 bits are three rounds at most, and
+// one more where the positive ones did not suffice.
 // A row of few (sequence, kv head) pairs is shared by a cluster of CTAs, each with its part of the slots and
 // all with the sums of the others' histograms.
 
@@ -723,8 +735,9 @@ constexpr int kShortSlots = 16384;  // of a row that a CTA takes where there are
 
 // `longest`: slots of a row at most, which the tables' width gives, not the sequences' lengths.  With few pairs a
 // launch has clusters of as many CTAs a row as the SMs hold at once, of 4096 slots at least (4 x 8 rows of 65536: select
-// kernel 203 us with a CTA a row, 35 with four).  With many and wide tables one launch has a CTA for each row of up to
-// kShortSlots, and another few clusters that take the longer ones in turn.
+// kernel 203 us with a CTA a row, 33 with four).  With many and wide tables one launch has a CTA for each row of up to
+// kShortSlots, and another few clusters that take the longer ones in turn (256 sequences of 1800 INT8 tokens, 8 heads: 89 us in tables
+// of 1920 slots, 114 in ones of 131072).
 // Threads: as many as leave all CTAs on the SMs at once (64 registers each), of eight slots at least.
 cudaError_t launch_select(const EvictArgs& a, int pairs, int longest, int sms, cudaStream_t stream) {
   EvictArgs args = a;
