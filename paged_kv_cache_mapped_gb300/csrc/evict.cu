@@ -111,9 +111,10 @@ __device__ __forceinline__ T block_sum_before(T v, int* sums, T* total) {
 constexpr int kEvictBins = 2048;
 constexpr int kEvictMinThreads = 256, kEvictMaxThreads = 1024;
 constexpr int kEvictBatch = 8, kEvictWide = 4;  // loads of slots, and of four of them, that a thread has in flight
+constexpr int kEvictRanks = 8;  // CTAs of a cluster at most
 constexpr int kMoveBatch = 4;   // likewise, moves
 constexpr int kEvictSlots = 32768;  // of a CTA at most: 32 words of 32 for each of 32 warps
-static_assert(PKV_MAX_EVICT_TOKENS == 8 * kEvictSlots, "a cluster of eight");
+static_assert(PKV_MAX_EVICT_TOKENS == kEvictRanks * kEvictSlots, "the longest row");
 constexpr uint32_t kProtectedKey = 0xffffffffu;
 constexpr uint32_t kZeroKey = 0x80000000u;  // of a score of 0
 
@@ -126,19 +127,23 @@ __device__ __forceinline__ uint32_t order_key(float s) {
 
 static_assert(kEvictBins >= 2 * kEvictMaxThreads, "two bins a thread");
 
+template <bool CLUSTER>
 struct EvictShared {
   alignas(8) int hist[kEvictBins];
+  alignas(8) int all[CLUSTER ? kEvictBins : 2];  // the histogram of the row
   uint32_t list[kEvictMaxThreads];
   int sums[33];
   uint32_t least, most, key;  // least key of a positive score (less the key of zero), greatest unprotected one (plus 1)
   int guarded, n, bin, above, in, total, ties, cut;
-  int equal, to, from;  // counts of this CTA's slots
+  // what each CTA of the cluster found, written there by itself: as above, equal keys, places to fill and rows to go there
+  uint32_t leasts[kEvictRanks], mosts[kEvictRanks];
+  int guards[kEvictRanks], equals[kEvictRanks], tos[kEvictRanks], froms[kEvictRanks];
 };
 
 // One row, bg, by a CTA or a cluster, unless it shrinks from more than `upto` slots.  s_keys: keys of this CTA's slots, a
 // multiple of four.
 template <bool CLUSTER>
-__device__ __forceinline__ void select_row(const EvictArgs& a, int bg, int upto, EvictShared& sh, uint32_t* s_keys) {
+__device__ __forceinline__ void select_row(const EvictArgs& a, int bg, int upto, EvictShared<CLUSTER>& sh, uint32_t* s_keys) {
   namespace cg = cooperative_groups;
   cg::cluster_group cluster = cg::this_cluster();
   const int ranks = CLUSTER ? (int)cluster.num_blocks() : 1, rank = CLUSTER ? (int)cluster.block_rank() : 0;
@@ -167,6 +172,7 @@ __device__ __forceinline__ void select_row(const EvictArgs& a, int bg, int upto,
     return;
   }
   if (s.L > upto) return;
+  if constexpr (CLUSTER) cluster_arrive();  // (what is written to another CTA comes after it has begun)
   if (tid == 0) {
     sh.least = 0xffffffffu;
     sh.most = 0u;
@@ -271,14 +277,24 @@ __device__ __forceinline__ void select_row(const EvictArgs& a, int bg, int upto,
     }
     if (nan) record_error(a.err, PKV_DEV_BAD_SCORE);
   }
-  sync_all();
-  uint32_t lo = 0xffffffffu, hi = 0u;
-  int need = a.budget;  // among the unprotected, fewer than they are
-  for (int r = 0; r < ranks; ++r) {
-    const EvictShared* o = of_rank(r);
-    lo = min(lo, o->least);
-    hi = max(hi, o->most);
-    need -= o->guarded;
+  __syncthreads();
+  uint32_t lo = sh.least, hi = sh.most;
+  int need = a.budget - sh.guarded;  // among the unprotected, fewer than they are
+  if constexpr (CLUSTER) {
+    cluster_wait();
+    if (tid < ranks) {
+      auto* o = of_rank(tid);
+      o->leasts[rank] = lo;
+      o->mosts[rank] = hi;
+      o->guards[rank] = a.budget - need;
+    }
+    cluster.sync();
+    need = a.budget;
+    for (int r = 0; r < ranks; ++r) {
+      lo = min(lo, sh.leasts[r]);
+      hi = max(hi, sh.mosts[r]);
+      need -= sh.guards[r];
+    }
   }
   hi -= 1u;
   lo += kZeroKey + 1u;
@@ -323,23 +339,28 @@ __device__ __forceinline__ void select_row(const EvictArgs& a, int bg, int upto,
         if (k.w - lo <= range) atomicAdd(&sh.hist[(k.w - lo) >> shift], 1);
       }
       sync_all();
+      if constexpr (CLUSTER) {  // each CTA adds up its share of the bins, for all
+        const int share = kEvictBins / ranks;
+        for (int i = rank * share + tid; i < (rank + 1) * share; i += T) {
+          int n = 0;
+#pragma unroll
+          for (int r = 0; r < kEvictRanks; ++r)
+            if (r < ranks) n += of_rank(r)->hist[i];
+#pragma unroll
+          for (int r = 0; r < kEvictRanks; ++r)
+            if (r < ranks) of_rank(r)->all[i] = n;
+        }
+        cluster.sync();
+      }
       // a thread's bins of the whole row, and the keys in the bins past them
       const int per = kEvictBins / T;  // two at least (T divides it)
       int h[kEvictBins / kEvictMinThreads], sum = 0;
+      const int2* bins = reinterpret_cast<const int2*>((CLUSTER ? sh.all : sh.hist) + tid * per);
 #pragma unroll
-      for (int q = 0; q < kEvictBins / kEvictMinThreads; ++q) h[q] = 0;
-#pragma unroll
-      for (int r = 0; r < (CLUSTER ? 8 : 1); ++r) {
-        if (r >= ranks) break;
-        const int2* o = reinterpret_cast<const int2*>(of_rank(r)->hist + tid * per);
-#pragma unroll
-        for (int q = 0; q < kEvictBins / kEvictMinThreads; q += 2) {
-          if (q < per) {
-            const int2 x = o[q >> 1];
-            h[q] += x.x;
-            h[q + 1] += x.y;
-          }
-        }
+      for (int q = 0; q < kEvictBins / kEvictMinThreads; q += 2) {
+        const int2 x = q < per ? bins[q >> 1] : make_int2(0, 0);
+        h[q] = x.x;
+        h[q + 1] = x.y;
       }
 #pragma unroll
       for (int q = 0; q < kEvictBins / kEvictMinThreads; ++q) sum += h[q];
@@ -357,7 +378,7 @@ __device__ __forceinline__ void select_row(const EvictArgs& a, int bg, int upto,
         }
         above += h[q];
       }
-      sync_all();  // (and the histograms have been read)
+      __syncthreads();  // (and the histogram has been read)
       if (above_zero && sh.total < need) {  // all positive scores stay, and some of the others
         need -= sh.total;
         lo = 0u;
@@ -371,7 +392,7 @@ __device__ __forceinline__ void select_row(const EvictArgs& a, int bg, int upto,
       need -= sh.above;
       const int in = sh.in;
       if (in <= T && lo != hi) {
-        EvictShared* o = of_rank(0);
+        auto* o = of_rank(0);
         const uint32_t width = hi - lo;
         auto list = [&](uint32_t k) {
           if (k - lo <= width) o->list[atomicAdd(&o->n, 1)] = k;
@@ -396,7 +417,7 @@ __device__ __forceinline__ void select_row(const EvictArgs& a, int bg, int upto,
             more = __reduce_add_sync(kFullMask, more);
             same = __reduce_add_sync(kFullMask, same);
             if (lane < ranks && more < need && need <= more + same) {  // (every warp that has this key writes the same)
-              EvictShared* to = of_rank(lane);
+              auto* to = of_rank(lane);
               to->key = k;
               to->ties = need - more;
               to->cut = need < more + same ? 1 : 0;
@@ -426,9 +447,9 @@ __device__ __forceinline__ void select_row(const EvictArgs& a, int bg, int upto,
     before = block_sum_before(lane == 0 ? equal : 0, sh.sums, &total);
     before = __shfl_sync(kFullMask, before, 0);
     if constexpr (CLUSTER) {
-      if (tid == 0) sh.equal = total;
-      sync_all();
-      for (int r = 0; r < rank; ++r) before += of_rank(r)->equal;
+      if (tid < ranks) of_rank(tid)->equals[rank] = total;
+      cluster.sync();
+      for (int r = 0; r < rank; ++r) before += sh.equals[r];
     }
   }
   auto sum_to_lane = [&](int v) {  // over the lanes up to this one
@@ -479,21 +500,20 @@ __device__ __forceinline__ void select_row(const EvictArgs& a, int bg, int upto,
   const int to = (int)(start & 0xffffu), from = (int)(start >> 16), n_to = (int)(all & 0xffffu), n_from = (int)(all >> 16);
   int to0 = 0, from0 = 0, n = n_from;  // places of this CTA's first ones, and all moves
   if constexpr (CLUSTER) {
-    if (tid == 0) {
-      sh.to = n_to;
-      sh.from = n_from;
+    if (tid < ranks) {
+      auto* o = of_rank(tid);
+      o->tos[rank] = n_to;
+      o->froms[rank] = n_from;
     }
-    sync_all();
+    cluster.sync();  // the last: nothing of another CTA is read or written past it
     n = 0;
     for (int r = 0; r < ranks; ++r) {
-      const EvictShared* o = of_rank(r);
       if (r < rank) {
-        to0 += o->to;
-        from0 += o->from;
+        to0 += sh.tos[r];
+        from0 += sh.froms[r];
       }
-      n += o->from;
+      n += sh.froms[r];
     }
-    cluster_arrive();  // (the counts have been read; no CTA may leave before)
   }
   if (tid == 0 && rank == 0) a.count[bg] = n;
   // The CTA's slots as lists, in place of the keys; then all that the rows' kernel needs of them.  (That kernel joins
@@ -565,7 +585,6 @@ __device__ __forceinline__ void select_row(const EvictArgs& a, int bg, int upto,
     scores_out[i] = 0.f;
     pos_out[i] = -1;
   }
-  if constexpr (CLUSTER) cluster_wait();
 }
 
 // A CTA or cluster a row; or, MANY, few clusters that take the rows of more than `above` slots in turn.  (Apart: in the loop
@@ -573,7 +592,7 @@ __device__ __forceinline__ void select_row(const EvictArgs& a, int bg, int upto,
 template <bool CLUSTER, bool MANY>
 __global__ void __launch_bounds__(kEvictMaxThreads, 1) evict_select_kernel(const __grid_constant__ EvictArgs a, int above, int upto) {
   extern __shared__ __align__(16) uint32_t s_keys[];
-  __shared__ EvictShared sh;
+  __shared__ EvictShared<CLUSTER> sh;
   const int ranks = CLUSTER ? (int)cooperative_groups::this_cluster().num_blocks() : 1;
   const int first = (int)blockIdx.x / ranks;
   grid_dependency_wait();
