@@ -17,10 +17,10 @@
 // of V read and written.  What bounds it (calls in a graph):
 //  * 32 sequences of ~4000 bf16 tokens cut to 1540, 8 heads of 128: 65 us.  Profiled alone 16 for the selection and 51 for
 //    the rows, at 71 % of peak DRAM (whole 256-byte rows, reads and writes mixed).
-//  * 4 of 65536 cut to 8191: 81 us.  The kept rows behind the budget lie one or two in a block, and such single rows reach
+//  * 4 of 65536 cut to 8191: 78-81 us.  The kept rows behind the budget lie one or two in a block, and such single rows reach
 //    48 % of peak DRAM (53 us; CTAs for twice or three times the rows in flight change nothing; five resident ones an
-//    SM 77 us in all, but 66.3 for the case above).  The selection's 47000 cycles in a cluster of four are 9500 of loads and ten
-//    steps of 2500 to 4500 between barriers.
+//    SM 75-77 us in all, but 66.3 for the case above).  The selection's 45000 cycles in a cluster of four are 9500 of loads and ten
+//    steps of 2500 to 4500 between barriers.  One sequence of 32768: 27 us, of 200000: 63.
 //  * 64 of 1800 INT8 tokens, 270 moved a head: 18 us; 2 of 300: 11 us.  Two launches and a chain of latencies:
 //    lengths, slots, histogram, scan, list, rank, words, lists, moves, then count, moves, rows.
 #include <cooperative_groups.h>
