@@ -17,10 +17,10 @@
 // of V read and written.  What bounds it (calls in a graph):
 //  * 32 sequences of ~4000 bf16 tokens cut to 1540, 8 heads of 128: 65 us.  Profiled alone 16 for the selection and 51 for
 //    the rows, at 71 % of peak DRAM (whole 256-byte rows, reads and writes mixed).
-//  * 4 of 65536 cut to 8191: 78-81 us.  The kept rows behind the budget lie one or two in a block, and such single rows reach
-//    48 % of peak DRAM (53 us; CTAs for twice or three times the rows in flight change nothing; five resident ones an
-//    SM 75-77 us in all, but 66.3 for the case above).  The selection's 45000 cycles in a cluster of four are 9500 of loads and ten
-//    steps of 2500 to 4500 between barriers.  One sequence of 32768: 27 us, of 200000: 63.
+//  * 4 of 65536 cut to 8191: 74-77 us.  The kept rows behind the budget lie one or two in a block, and such single rows reach
+//    some 50 % of peak DRAM (CTAs for twice or three times the rows in flight change nothing).  The selection's 45000 cycles
+//    in a cluster of four are 9500 of loads and ten steps of 2500 to 4500 between barriers.  One sequence of 32768: 27 us, of
+//    200000: 61.
 //  * 64 of 1800 INT8 tokens, 270 moved a head: 18 us; 2 of 300: 11 us.  Two launches and a chain of latencies:
 //    lengths, slots, histogram, scan, list, rank, words, lists, moves, then count, moves, rows.
 #include <cooperative_groups.h>
@@ -676,9 +676,9 @@ __device__ __forceinline__ void evict_tables(const EvictArgs& a) {
 }
 
 // RB: bytes of a row; SCALES: INT8 pools.  A warp takes 2 KB of K rows and as much of V at a time: lanes find the rows,
-// then every lane has eight 16-byte loads in flight before it stores.
-template <int RB, bool SCALES>
-__global__ void __launch_bounds__(kMoveThreads, 4) evict_move_kernel(const __grid_constant__ EvictArgs a) {
+// then every lane has eight 16-byte loads in flight before it stores.  CTAS: resident an SM (a few spilled words with five).
+template <int RB, bool SCALES, int CTAS>
+__global__ void __launch_bounds__(kMoveThreads, CTAS) evict_move_kernel(const __grid_constant__ EvictArgs a) {
   constexpr int CPR = RB / 16, NR = 128 / CPR;  // 16-byte pieces of a row; rows of a warp at a time
   static_assert(NR <= 32 && NR * CPR == 4 * 32, "four pieces of K and of V a lane");
   grid_dependency_wait();
@@ -795,6 +795,16 @@ cudaError_t launch_select(const EvictArgs& a, int pairs, int longest, int sms, c
   return launch((const void*)evict_select_kernel<true, true>, std::max(1, sms / ranks) * ranks, ranks, longest, kShortSlots);
 }
 
+// bf16: five CTAs an SM where the kept rows behind the budget lie far apart, fewer than four of a block (4 sequences of 65536 cut
+// to 8191: 74-77 us, 78-81 with four), and four where they lie close (32 of ~4000 cut to 1540: 64.8 us, 66.4 with
+// five).  The tables' width stands for the lengths.  INT8: four (256 of 1800 in tables of 131072 slots, which say
+// far apart: 114 us, 118 with five).
+const void* move_kernel(bool q8, int head_dim, bool apart) {
+  if (q8) return head_dim == 128 ? (const void*)evict_move_kernel<128, true, 4> : (const void*)evict_move_kernel<64, true, 4>;
+  if (apart) return head_dim == 128 ? (const void*)evict_move_kernel<256, false, 5> : (const void*)evict_move_kernel<128, false, 5>;
+  return head_dim == 128 ? (const void*)evict_move_kernel<256, false, 4> : (const void*)evict_move_kernel<128, false, 4>;
+}
+
 size_t align256e(size_t x) { return (x + 255) & ~size_t(255); }
 
 // int32 counts | int4 moves | int32 slots
@@ -885,8 +895,7 @@ int evict_common(void* k, void* v, float* ks, float* vs, const int32_t* block_ta
   const int most = std::max(0, std::min(a.budget, longest - a.budget));  // moves of a pair at most
   const long long fill = pairs > 0 ? (16ll * sms + pairs - 1) / pairs : 1;
   a.splits = (int)std::max(1ll, std::min<long long>((most + per_cta - 1) / per_cta, fill));
-  const void* f = q8 ? (dims->head_dim == 128 ? (const void*)evict_move_kernel<128, true> : (const void*)evict_move_kernel<64, true>)
-                     : (dims->head_dim == 128 ? (const void*)evict_move_kernel<256, false> : (const void*)evict_move_kernel<128, false>);
+  const void* f = move_kernel(q8, dims->head_dim, longest > 4ll * a.budget);
   void* params[] = {&a};
   return cuda_status(launch_pdl(f, dim3(1 + (unsigned)pairs * (unsigned)a.splits), dim3(kMoveThreads), 0, cu, params));
 }
