@@ -32,11 +32,11 @@
 // Differential attention (DIFF): out = sum_t (a_1,t - lambda a_2,t) V_t and a norm, the maps from the halves of q and K.  An
 // item's two row tiles are the two maps of the same 128 rows, so a CTA's K and V tiles serve both, each map's S takes
 // half the products, and the difference is made from the two outputs in tensor memory at the item's end.  Twice the exponentials
-// and one and a half times the products of the plain form, and the same chain of a step bounds it: 4096 tokens on 16384 keys 1390 us
-// (1.04 PFLOP/s, 54 % of the measured bf16 rate; tensor pipe 50 %, issue 52 %, exponentials 30 %); 4 prompts of 3000, d 64, 8 heads with a
-// bias 112 us (tensor pipe 18 %, issue 46 %, exponentials 21 %); 24 mixed sequences 53 us, a chain of plan, loads, few steps and merge.
+// and one and a half times the products of the plain form, and the same chain of a step bounds it: 4096 tokens on 16384 keys 1355 us
+// (1.07 PFLOP/s, 56 % of the measured bf16 rate; tensor pipe 50 %, issue 52 %, exponentials 30 %); 4 prompts of 3000, d 64, 8 heads with a
+// bias 111 us (tensor pipe 18 %, issue 46 %, exponentials 21 %); 24 mixed sequences 52 us, a chain of plan, loads, few steps and merge.
 // The maps' rounding errors add while their outputs subtract, so the nearest sixth of a longer row's steps takes two terms as well:
-// the error against 64 bits, in that of bf16 outputs alone, is 1.48 (chunk; no step 1.55, 1327 us; an eighth of them 1.50, 1379 us) and
+// the error against 64 bits, in that of bf16 outputs alone, is 1.48 (chunk, then 1390 us; no step 1.55, 1327 us; an eighth of them 1.50, 1379 us) and
 // 1.03 (prompts with the bias, whose weights lie near; no step 1.32, 109 us).
 // Non-finite V: a masked key's weight is 0, and 0 * NaN is NaN, so V rows past the sequence are cleared,
 // and an output row that owes a NaN to a masked key is computed again over what it sees.
@@ -720,6 +720,8 @@ struct Shared {
   int lo_least[NT], lo_most[NT], abort, next;  // interval starts of the row tiles' rows
   float sum[DIFF ? 2 : 1][DIFF ? 128 : 1];     // DIFF: each map's sum of a row's weights
   float2 squares[DIFF ? 2 : 1][DIFF ? 128 : 1];  // and half of each row's sum of squares
+  alignas(16) float norm[DIFF ? D : 1];          // the norm's weights
+  int place[DIFF ? 128 : 1];                     // of each row: its head and its token among the item's, -1: none
 };
 
 // Loads the item's Q tiles and its K and V tiles through the ring (one warp).  n_kv counts K and V tiles
@@ -1117,17 +1119,24 @@ __device__ __forceinline__ float step_weights(const float (&v)[kStep], uint32_t 
 // The end of a differential item, by the 256 softmax threads: thread (x, r) has map x's maximum m and sum l of row r, and
 // both maps' O rows are in its lanes of tensor memory.  It takes half of the row's columns of both; or, of an item whose
 // keys are shared out, its own map's partial row.  ok: its waits ended.  Every thread passes the same barriers.
+// At d 128 the rows go out through the Q tile's place (stage), which no product reads any more, so that a warp's stores are
+// of whole rows, by loops that stay loops: unrolled ones that store 16 bytes a lane of 32 rows take 6500 cycles an item,
+// these 5800, a third of it the other map's last step (chunk of 4096 on 16384 1390 -> 1355 us, 24 mixed sequences 52.9 -> 51.7).
+// At d 64 that costs registers of the steps (4 prompts of 3000: 115.5 us; unrolled and straight 111).
 template <int D>
-__device__ __forceinline__ void diff_rows(const PrefillAttnArgs& a, Shared<D, 2, true>& sh, const Item& w, uint32_t to, int x,
-                                          int r, bool valid, bool ok, float m, float l, int i, int lo, int prow, int h) {
+__device__ __forceinline__ void diff_rows(const PrefillAttnArgs& a, Shared<D, 2, true>& sh, const Item& w, unsigned char* stage,
+                                          uint32_t to, int x, int r, bool valid, bool ok, float m, float l, int i, int lo, int prow,
+                                          int h) {
   constexpr int N = D / 2;
-  const int lane = threadIdx.x & 31;
+  constexpr bool kStage = D == 128;
+  constexpr int kTurns = kStage ? 1 : D / 16;
   const bool split = w.nsplit > 1, two = w.nt_all <= kTwoTermTiles;
   const int e_base = w.ts * kTileBlocks;
   const Steps range = steps_of(a, w, 0, sh.lo_least[x]);
   const bool some = range.hi >= range.lo;
   const long long part =
       split ? (long long)w.part + ((long long)w.split * w.tokens + (prow - w.row0)) * a.Hq + h : 0;
+  const float lam = valid ? __ldg(a.lambdas + (size_t)prow * a.lambda_stride + h) : 0.f;
   sh.sum[x][r] = l;
   tc_fence_before();
   if (named_barrier_or(1, 256, !ok)) return;
@@ -1135,7 +1144,6 @@ __device__ __forceinline__ void diff_rows(const PrefillAttnArgs& a, Shared<D, 2,
   const float l0 = sh.sum[0][r], l1 = sh.sum[1][r];
   bool bad = !(l <= 3.4028234e38f);
   SquareSum sq;
-  const float lam = valid ? __ldg(a.lambdas + (size_t)prow * a.lambda_stride + h) : 0.f;
   const float f0 = l0 > 0.f ? 1.f / l0 : 0.f, f1 = l1 > 0.f ? lam / l1 : 0.f;
   // 16 columns of this thread's half of the difference; read twice, which costs less than the registers to keep them
   auto columns = [&](int c, float (&y)[16]) {
@@ -1150,7 +1158,7 @@ __device__ __forceinline__ void diff_rows(const PrefillAttnArgs& a, Shared<D, 2,
     for (int k = 0; k < 16; ++k) y[k] = some ? y[k] * f0 - o[k] * f1 : 0.f;
   };
   if (split) {
-#pragma unroll
+#pragma unroll kTurns
     for (int c = 0; c < D / 16; ++c) {
       float o[16];
       __syncwarp();
@@ -1171,7 +1179,7 @@ __device__ __forceinline__ void diff_rows(const PrefillAttnArgs& a, Shared<D, 2,
     }
     if (valid) a.part_ml[2 * part + x] = make_float2(m, l);
   } else {
-#pragma unroll
+#pragma unroll kTurns
     for (int c = 0; c < N / 16; ++c) {
       float y[16];
       columns(c, y);
@@ -1181,6 +1189,7 @@ __device__ __forceinline__ void diff_rows(const PrefillAttnArgs& a, Shared<D, 2,
         sq.add(y[k]);
       }
     }
+    if (kStage && x == 0) sh.place[r] = valid ? (prow - w.row0) << 3 | (h - w.g * a.G) : -1;
   }
   // a row that is not finite says so in its half of the squares
   sh.squares[x][r] = make_float2(bad ? __int_as_float(0x7fffffff) : sq.s, sq.b);
@@ -1192,19 +1201,37 @@ __device__ __forceinline__ void diff_rows(const PrefillAttnArgs& a, Shared<D, 2,
     const bool norm = a.norm_weight != nullptr;
     const float f = norm ? sq.factor(D, a.norm_eps) : 1.f;
     uint4* dst = reinterpret_cast<uint4*>(a.out + ((size_t)prow * a.Hq + h) * D + x * N);
-#pragma unroll
+#pragma unroll kTurns
     for (int c = 0; c < N / 16; ++c) {
+      if (kStage && !some) break;
       float y[16];
       columns(c, y);
-      if (!valid) continue;
+      if (!kStage && !valid) continue;
       if (norm) {
 #pragma unroll
-        for (int k = 0; k < 16; ++k) y[k] *= f * __ldg(a.norm_weight + x * N + 16 * c + k);
+        for (int k = 0; k < 16; ++k) y[k] *= f * sh.norm[x * N + 16 * c + k];
       }
 #pragma unroll
-      for (int k = 0; k < 2; ++k)
-        dst[2 * c + k] = make_uint4(pack_bf16x2(y[8 * k], y[8 * k + 1]), pack_bf16x2(y[8 * k + 2], y[8 * k + 3]),
-                                    pack_bf16x2(y[8 * k + 4], y[8 * k + 5]), pack_bf16x2(y[8 * k + 6], y[8 * k + 7]));
+      for (int k = 0; k < 2; ++k) {
+        const uint4 u = make_uint4(pack_bf16x2(y[8 * k], y[8 * k + 1]), pack_bf16x2(y[8 * k + 2], y[8 * k + 3]),
+                                   pack_bf16x2(y[8 * k + 4], y[8 * k + 5]), pack_bf16x2(y[8 * k + 6], y[8 * k + 7]));
+        // a row's 16-byte piece lies at its number xor the row's (mod 8), for the banks
+        if constexpr (kStage) *reinterpret_cast<uint4*>(stage + r * 2 * D + ((x * (N / 8) + 2 * c + k) ^ (r & 7)) * 16) = u;
+        else dst[2 * c + k] = u;
+      }
+    }
+    if constexpr (kStage) {
+      (void)named_barrier_or(1, 256, false);
+      constexpr int kPieces = D / 8;  // of a row
+      const int thread = x * 128 + r, piece = thread % kPieces;
+#pragma unroll 2
+      for (int t = thread / kPieces; t < 128; t += 256 / kPieces) {
+        const int at = sh.place[t];
+        if (at < 0) continue;
+        const uint4 u = some ? *reinterpret_cast<const uint4*>(stage + t * 2 * D + (piece ^ (t & 7)) * 16) : make_uint4(0u, 0u, 0u, 0u);
+        *reinterpret_cast<uint4*>(a.out + ((size_t)(w.row0 + (at >> 3)) * a.Hq + w.g * a.G + (at & 7)) * D + piece * 8) = u;
+      }
+      fence_proxy_async_smem();  // (the next Q tile comes here)
     }
   }
   if (!any) return;
@@ -1597,6 +1624,9 @@ prefill_attention_kernel(const __grid_constant__ PrefillAttnArgs a) {
   const int4* first = a.plan_items + 2 * ((int)blockIdx.x / a.Hkv);
   int4 rec0 = first[0], rec1 = first[1];
   const int total = a.plan_head[0] * a.Hkv;
+  if constexpr (DIFF) {  // (read after the items' first barriers)
+    if (a.norm_weight != nullptr && threadIdx.x < D) sh.norm[threadIdx.x] = a.norm_weight[threadIdx.x];
+  }
   // Each role has the whole item loop, so that its registers are its own.  Three block barriers an item:
   // the shared minimum is reset, it is complete, every role has left the item.
   uint32_t n_kv = 0, n_q = 0;  // K and V tiles, and items with tiles, since the kernel's start (barrier phases)
@@ -1650,7 +1680,7 @@ prefill_attention_kernel(const __grid_constant__ PrefillAttnArgs a) {
           else rows(std::integral_constant<int, 3>{});
         }
         if constexpr (DIFF)
-          diff_rows<D>(a, sh, w, tmem + ((uint32_t)(r & ~31) << 16) + NT * 2 * kStep, x, r, valid, ok, top, sum, i, lo, prow, h);
+          diff_rows<D>(a, sh, w, sq, tmem + ((uint32_t)(r & ~31) << 16) + NT * 2 * kStep, x, r, valid, ok, top, sum, i, lo, prow, h);
       }
       n_kv += 2 * w.nt;
       tc_fence_before();
