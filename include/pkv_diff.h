@@ -65,7 +65,9 @@ int pkv_paged_diff_decode_attention(void* out, const void* q, const void* k_cach
  *                           scores[b, g, t]                                    for the other t < L_b.
  *   scores, scores_out : [B, Hkv, score_stride] fp32; may be the same array and may not overlap otherwise.  Entries
  *                        from L_b on are left as they were.  Keys from score_stride on get no score, and are reported
- *                        (PKV_DEV_BAD_CONTEXT_LEN).
+ *                        (PKV_DEV_BAD_CONTEXT_LEN).  A logit of NaN or +infinity makes a map's weights NaN, as the
+ *                        formula does: those of every key that the query sees.  Keys of a block outside the
+ *                        pool get no weight.
  */
 int pkv_paged_diff_decode_attention_scores(void* out, const float* scores, float* scores_out, int32_t score_stride,
                                            const void* q, const void* k_cache, const void* v_cache,

@@ -324,6 +324,10 @@ constexpr int kDiffPairs = 1, kDiffWide = 2;  // forms of the differential decod
 constexpr float kLn2 = 0.6931471805599453f;
 constexpr float kLog2e = 1.4426950408889634f;
 
+// Base-2 log-sum-exp of a row whose weights, relative to 2^m, sum to l: -infinity where it saw nothing (or only logits of
+// -infinity), NaN where a logit was NaN or +infinity, so that the score step gives no finite weight from such a row.
+__device__ __forceinline__ float row_lse2(float m, float l) { return l == 0.f ? -INFINITY : m + log2f(l); }
+
 // SCORES (dense only): also keep every attended key's base-2 logit and write the log-sum-exp of
 // rows written out directly, for the score step (decode_score_kernel).
 // F8 (with Q8): the codes are E4M3 with a scale per block and kv head.  RULES (dense only): score rules.
@@ -810,7 +814,7 @@ decode_split_kernel(const __grid_constant__ DecodeArgs a) {
         return;
       }
       if constexpr (SCORES) {  // base 2
-        if (live && gq < 2) a.lse[row * 2 + gq] = (gq ? l1 : l0) > 0.f ? (gq ? mr1 + log2f(l1) : mr0 + log2f(l0)) : -INFINITY;
+        if (live && gq < 2) a.lse[row * 2 + gq] = row_lse2(gq ? mr1 : mr0, gq ? l1 : l0);
       }
       const float f1 = l0 > 0.f ? 1.f / l0 : 0.f;
       const float f2 = live && l1 > 0.f ? __ldg(a.lambdas + (size_t)seg_b * a.lambda_stride + seg_g * G + tq) / l1 : 0.f;
@@ -866,7 +870,7 @@ decode_split_kernel(const __grid_constant__ DecodeArgs a) {
           continue;
         }
         if constexpr (SCORES) {  // base 2
-          if (live && gq < 2) a.lse[row * 2 + gq] = (gq ? l[1] : l[0]) > 0.f ? (gq ? m[1] + log2f(l[1]) : m[0] + log2f(l[0])) : -INFINITY;
+          if (live && gq < 2) a.lse[row * 2 + gq] = row_lse2(gq ? m[1] : m[0], gq ? l[1] : l[0]);
         }
         const float f1 = l[0] > 0.f ? 1.f / l[0] : 0.f;
         const float f2 = live && l[1] > 0.f ? __ldg(a.lambdas + (size_t)seg_b * a.lambda_stride + seg_g * G + head) / l[1] : 0.f;
@@ -1670,7 +1674,7 @@ decode_merge_kernel(const DecodeArgs a, int group, int wpr_log2) {
     }
     __syncthreads();
     if (!lead || (np == 0 && !zero_row)) return;
-    if (a.lse != nullptr && lane == 0) a.lse[vrow] = L > 0.f ? m_ref + log2f(L) : -INFINITY;  // scores mode: base 2
+    if (a.lse != nullptr && lane == 0) a.lse[vrow] = row_lse2(m_ref, L);  // scores mode: base 2
     if (vrow & 1) return;
     const float lam = __ldg(a.lambdas + (size_t)b * a.lambda_stride + (row - b * a.Hq));
     float y[EPW];
