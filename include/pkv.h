@@ -354,7 +354,8 @@ int pkv_prefill_window_scores(float* score_accum, int32_t score_stride, float* l
  * every attended key's logit (4 bytes per query head and key) and a light second kernel
  * turns them into probabilities, which reads far fewer bytes than reading K again.
  *   lse_out        : [B, Hq] fp32: natural log-sum-exp of each row's attended logits
- *                    (-infinity when nothing is attended).
+ *                    (-infinity when nothing is attended, NaN when a logit is NaN or +infinity; the
+ *                    scores of that row's attended keys are NaN then).
  *   score_accum    : [B, Hkv, score_stride] fp32, updated in place: for every attended
  *                    position t < score_stride of (b, kv head g),
  *                    score_accum[b][g][t] += sum over h in g's group of p_{b,h,t}.

@@ -913,7 +913,7 @@ decode_split_kernel(const __grid_constant__ DecodeArgs a) {
       const size_t row = (size_t)seg_b * a.Hq + (size_t)seg_g * G + head;
       if (seg_slot < 0) {
         if constexpr (SCORES) {  // the row's log-sum-exp: m is the reference l is relative to
-          if (gq == 0) a.lse[row] = l > 0.f ? (m + log2f(l)) * kLn2 : -INFINITY;
+          if (gq == 0) a.lse[row] = row_lse2(m, l) * kLn2;
         }
         const float inv = l > 0.f ? 1.f / l : 0.f;
         if constexpr (Q8) {  // accumulator rows gq, gq + 8 are columns 2gq, 2gq + 1 of each 16
@@ -1697,7 +1697,7 @@ decode_merge_kernel(const DecodeArgs a, int group, int wpr_log2) {
   }
   if (np == 0 && !zero_row) return;
   if (a.lse != nullptr && lane == 0)  // scores mode: the row's natural log-sum-exp
-    a.lse[row] = L > 0.f ? (m_ref + log2f(L)) * kLn2 : -INFINITY;
+    a.lse[row] = row_lse2(m_ref, L) * kLn2;
   __nv_bfloat16* dst = a.out + (size_t)row * D + lane * EPW;
   const float inv = L > 0.f ? 1.f / L : 0.f;  // a zero row has L = 0 and acc = 0
 #pragma unroll
