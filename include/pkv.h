@@ -359,7 +359,7 @@ int pkv_prefill_window_scores(float* score_accum, int32_t score_stride, float* l
  *   score_accum    : [B, Hkv, score_stride] fp32, updated in place: for every attended
  *                    position t < score_stride of (b, kv head g),
  *                    score_accum[b][g][t] += sum over h in g's group of p_{b,h,t}.
- *                    Other positions are left unchanged.
+ *                    Other positions are left unchanged, as are those of a block outside the pool.
  *   logits         : [B, Hq, score_stride] fp32 scratch, caller-owned; contents on return
  *                    unspecified.
  *   score_stride   : > 0; should be >= every L_b (max_blocks_per_seq * 16 always is): keys

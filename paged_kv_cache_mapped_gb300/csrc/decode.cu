@@ -1729,6 +1729,8 @@ __global__ void __launch_bounds__(kScoreThreads) decode_score_kernel(const Decod
   const int end = min(L, a.score_stride);
   const int t0 = (start & ~3) + tile * kScoreKeys + 4 * (int)threadIdx.x;  // keys t0 .. t0 + 3
   if (t0 >= end || t0 + 4 <= start) return;
+  const int blk = a.block_tables[(size_t)b * a.MB + (t0 >> 4)];  // of all four
+  if (blk < 0 || blk >= a.NB) return;  // (reported by the split kernel, which wrote no logits for these keys)
   const size_t row0 = (size_t)b * a.Hq + (size_t)g * group;
   float* dst = a.scores + (size_t)seg * a.score_stride + t0;
   const bool vec = (a.score_stride & 3) == 0 && t0 >= start && t0 + 4 <= end &&

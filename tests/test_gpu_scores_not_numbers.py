@@ -1,12 +1,14 @@
-"""The decode that emits scores (bf16 and INT8 pools) where a key's logit is no number: what the attended keys
-get, and that every other score stays."""
+"""The decode that emits scores (bf16 and INT8 pools) where a key's logit is no number, and where a block is outside the
+pool: what the attended keys get, and that every other score stays."""
 import pytest
 import torch
 
 import paged_kv_cache_mapped_gb300 as pkv
 from helpers import paged_from_contiguous, rand_bf16, rand_code_pool
+from paged_kv_cache_mapped_gb300 import header_constants
 
 pytestmark = pytest.mark.gpu
+C = header_constants()
 DEV = torch.device("cuda:0")
 LENS = {"whole rows": [9, 12, 16], "rows in shares": [2500, 700, 1900]}
 
@@ -55,3 +57,24 @@ def test_a_sum_that_is_no_number_reaches_the_scores(lens, hq, d, q8, where):
     assert torch.equal(got[0, 1], clean[0, 1]) and torch.equal(got[1:], clean[1:])
     assert torch.equal(again[0, g:], out[0, g:]) and torch.equal(again[1:], out[1:])
     assert torch.equal(lse2[0, g:], lse[0, g:]) and torch.equal(lse2[1:], lse[1:])
+
+
+@pytest.mark.parametrize("q8", [False, True])
+@pytest.mark.parametrize("window", [0, 250])
+@pytest.mark.parametrize("stride", [320, 321])
+def test_keys_of_a_bad_block_get_no_score(q8, window, stride):
+    """Over the logits of another call, whose keys there had weights: those scores stay, bit for bit."""
+    c = _case([300, 77], 8, 64, q8, 42)
+    err = pkv.new_error_word(DEV)
+    before, logits = torch.rand((2, 2, stride), device=DEV), torch.full((2, 8, stride), 1e3, device=DEV)
+    for x in (-1, c["pools"][0].shape[0]):
+        c["bt"][0, 5] = x
+        after = before.clone()
+        _, lse = _call(c, after, logits, window, err)
+        assert pkv.read_error(err, clear=True) == C["PKV_DEV_BAD_BLOCK_ID"] and torch.isfinite(lse).all()
+        start = max(0, 300 - window) if window else 0
+        assert torch.equal(after[0, :, 80:96], before[0, :, 80:96]) and torch.equal(after[0, :, :start], before[0, :, :start])
+        add = after - before
+        assert (add[0, :, start:80] > 0).all() and (add[0, :, 96:300] > 0).all() and (add[1, :, :77] > 0).all()
+        # each row's probabilities sum to 1: four heads a kv head, fp32 sums of 300 steps of at most half 2^-23 of 5
+        assert torch.allclose(add.sum(2), torch.full((2, 2), 4.0, device=DEV), rtol=0, atol=300 * 5 * 2.0 ** -24 + 1e-4)
