@@ -13,11 +13,17 @@ from .step import BLOCK_SIZE, _bf16_pools, _call, _dims, _give, _like, _need, _n
 
 
 @functools.lru_cache(maxsize=256)
+def _record(n_sink, k_top, n_recent, trigger):
+    return ctypes.pointer(PkvEvictRules(n_sink, k_top, n_recent, trigger))
+
+
 def _rules(n_sink, k_top, n_recent, trigger=0):
+    # (the record is kept by these numbers, not by the arguments: a tensor of one would be kept by its identity)
+    n_sink, k_top, n_recent = int(n_sink), int(k_top), int(n_recent)
     for name, x in (("n_sink", n_sink), ("k_top", k_top), ("n_recent", n_recent)):
-        if not 0 <= int(x) < 2**30:
+        if not 0 <= x < 2**30:
             raise ValueError(f"{name} must be within [0, 2**30), got {x}")
-    return ctypes.pointer(PkvEvictRules(int(n_sink), int(k_top), int(n_recent), max(0, min(int(trigger), 2**31 - 1))))
+    return _record(n_sink, k_top, n_recent, max(0, min(int(trigger), 2**31 - 1)))
 
 
 def evict_workspace_bytes(batch, num_kv_heads, n_sink, k_top, n_recent) -> int:
