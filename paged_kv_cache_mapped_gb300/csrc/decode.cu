@@ -832,11 +832,12 @@ decode_split_kernel(const __grid_constant__ DecodeArgs a) {
         f = sq.factor(D, a.norm_eps);
       }
       if (!live) return;
+      const bool norm = a.norm_weight != nullptr && (l0 != 0.f || l1 != 0.f);  // (no key: zero, whatever the norm's weights)
       __nv_bfloat16* dst = a.out + row * D + gq;
 #pragma unroll
       for (int mt = 0; mt < KS; ++mt) {
-        const float w0 = a.norm_weight != nullptr ? __ldg(a.norm_weight + mt * 16 + gq) : 1.f;
-        const float w1 = a.norm_weight != nullptr ? __ldg(a.norm_weight + mt * 16 + 8 + gq) : 1.f;
+        const float w0 = norm ? __ldg(a.norm_weight + mt * 16 + gq) : 1.f;
+        const float w1 = norm ? __ldg(a.norm_weight + mt * 16 + 8 + gq) : 1.f;
         dst[mt * 16] = __float2bfloat16_rn(o[mt][0] * f * w0);
         dst[mt * 16 + 8] = __float2bfloat16_rn(o[mt][2] * f * w1);
       }
@@ -888,11 +889,12 @@ decode_split_kernel(const __grid_constant__ DecodeArgs a) {
           f = sq.factor(D, a.norm_eps);
         }
         if (!live) continue;
+        const bool norm = a.norm_weight != nullptr && (l[0] != 0.f || l[1] != 0.f);  // (as above)
         __nv_bfloat16* dst = a.out + row * D + gq;
 #pragma unroll
         for (int mt = 0; mt < KS; ++mt) {
-          const float w0 = a.norm_weight != nullptr ? __ldg(a.norm_weight + mt * 16 + gq) : 1.f;
-          const float w1 = a.norm_weight != nullptr ? __ldg(a.norm_weight + mt * 16 + 8 + gq) : 1.f;
+          const float w0 = norm ? __ldg(a.norm_weight + mt * 16 + gq) : 1.f;
+          const float w1 = norm ? __ldg(a.norm_weight + mt * 16 + 8 + gq) : 1.f;
           dst[mt * 16] = __float2bfloat16_rn(o[mt][hh] * f * w0);
           dst[mt * 16 + 8] = __float2bfloat16_rn(o[mt][2 + hh] * f * w1);
         }
@@ -1671,20 +1673,23 @@ decode_merge_kernel(const DecodeArgs a, int group, int wpr_log2) {
     if (lead && (vrow & 1)) {
 #pragma unroll
       for (int e = 0; e < EPW; ++e) s_acc[warp][lane * EPW + e] = acc[e] * inv;
+      if (lane == 0) s_ml[warp].y = L;
     }
     __syncthreads();
     if (!lead || (np == 0 && !zero_row)) return;
     if (a.lse != nullptr && lane == 0) a.lse[vrow] = row_lse2(m_ref, L);  // scores mode: base 2
     if (vrow & 1) return;
-    const float lam = __ldg(a.lambdas + (size_t)b * a.lambda_stride + (row - b * a.Hq));
+    // a row that saw no key is zero, whatever the factor and the norm's weights
+    const float L2 = s_ml[warp + wpr].y;
+    const float lam = L2 != 0.f ? __ldg(a.lambdas + (size_t)b * a.lambda_stride + (row - b * a.Hq)) : 0.f;
     float y[EPW];
     SquareSum sq;
 #pragma unroll
     for (int e = 0; e < EPW; ++e) {
-      y[e] = zero_row ? 0.f : acc[e] * inv - lam * s_acc[warp + wpr][lane * EPW + e];  // (no key, whatever the factor)
+      y[e] = acc[e] * inv - lam * s_acc[warp + wpr][lane * EPW + e];
       sq.add(y[e]);
     }
-    if (a.norm_weight != nullptr) {
+    if (a.norm_weight != nullptr && (L != 0.f || L2 != 0.f)) {
       sq.join(32);
       const float f = sq.factor(D, a.norm_eps);
 #pragma unroll

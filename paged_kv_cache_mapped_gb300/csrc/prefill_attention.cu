@@ -633,11 +633,12 @@ __device__ __noinline__ void exact_row_diff(const PrefillAttnArgs& a, const Row&
     sq.add(y[e]);
   }
   sq.join(32);
-  const float f = a.norm_weight != nullptr ? sq.factor(D, a.norm_eps) : 1.f;
+  const bool norm = a.norm_weight != nullptr && (l[0] != 0.f || l[1] != 0.f);  // (no key: zero, whatever the norm's weights)
+  const float f = norm ? sq.factor(D, a.norm_eps) : 1.f;
 #pragma unroll
   for (int e = 0; e < E; ++e) {
     const int c = lane * E + e;
-    const float g = a.norm_weight != nullptr ? f * a.norm_weight[c] : 1.f;
+    const float g = norm ? f * a.norm_weight[c] : 1.f;
     a.out[((size_t)w.r * a.Hq + w.h) * D + c] = __float2bfloat16_rn(y[e] * g);
   }
 }
@@ -1198,7 +1199,7 @@ __device__ __forceinline__ void diff_rows(const PrefillAttnArgs& a, Shared<D, 2,
   if (!split) {
     sq.s = s0.x + s1.x;
     sq.b = s0.y + s1.y;
-    const bool norm = a.norm_weight != nullptr;
+    const bool norm = a.norm_weight != nullptr && (l0 != 0.f || l1 != 0.f);  // (no key: zero, whatever the norm's weights)
     const float f = norm ? sq.factor(D, a.norm_eps) : 1.f;
     uint4* dst = reinterpret_cast<uint4*>(a.out + ((size_t)prow * a.Hq + h) * D + x * N);
 #pragma unroll kTurns
@@ -1751,6 +1752,7 @@ __global__ void __launch_bounds__(256) prefill_merge_kernel(const PrefillAttnArg
     if (in >= per) continue;
     const long long p0 = (long long)split.w + in;
     float y[E] = {};
+    bool some = false;  // DIFF: the row saw a key
 #pragma unroll
     for (int map = 0; map < M; ++map) {
       float2 ml[2];
@@ -1791,6 +1793,7 @@ __global__ void __launch_bounds__(256) prefill_merge_kernel(const PrefillAttnArg
       const float inv = l > 0.f ? 1.f / l : (l == l ? 0.f : l);
       if constexpr (DIFF) {
         const int tok = in / a.Hq, h = in - tok * a.Hq;
+        some |= l != 0.f;
         float f = inv;
         if (map == 1) f = l != 0.f ? -inv * __ldg(a.lambdas + (size_t)(split.x + tok) * a.lambda_stride + h) : 0.f;
 #pragma unroll
@@ -1801,7 +1804,7 @@ __global__ void __launch_bounds__(256) prefill_merge_kernel(const PrefillAttnArg
       }
     }
     if constexpr (DIFF) {
-      if (a.norm_weight != nullptr) {
+      if (a.norm_weight != nullptr && some) {
         SquareSum s;
 #pragma unroll
         for (int e = 0; e < E; ++e) s.add(y[e]);

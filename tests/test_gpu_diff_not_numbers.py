@@ -1,10 +1,13 @@
-"""Differential attention where a sum is no number: a NaN or an infinite logit in one map of a key that the
-query sees reaches the scores of every key of its heads, and no others."""
+"""Differential attention where a sum or a parameter is no number: a NaN or an infinite logit in one map of a key that the
+query sees reaches the scores of every key of its heads, and no others; a row that sees no key is zero whatever the norm's
+weights and the factor."""
+import numpy as np
 import pytest
 import torch
 
 import paged_kv_cache_mapped_gb300 as pkv
 import test_gpu_diff_decode as decode
+import test_gpu_diff_prefill as prefill
 from paged_kv_cache_mapped_gb300 import header_constants
 
 C = header_constants()
@@ -56,3 +59,43 @@ def test_eviction_reports_the_scores_that_are_no_numbers():
     pkv.kv_evict(*c["pools"], c["bt"], torch.tensor(c["lens"], dtype=torch.int32, device=DEV), scores, pos,
                  torch.zeros(2, dtype=torch.int32, device=DEV), 2, 20, 10, error_word=err)
     assert pkv.read_error(err) == C["PKV_DEV_BAD_SCORE"]
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("hq", [4, 12], ids=["pairs", "wide"])
+@pytest.mark.parametrize("bad", [float("nan"), float("inf")])
+def test_rows_that_see_nothing_are_zero_whatever_the_norm(hq, d, bad):
+    """A weight of the norm that is no number makes that column of the rows that see a key none, and no other; a
+    factor that is no number besides leaves a row zero whose blocks are all outside the pool."""
+    lens, docs = [300, 40, 0, 2500, 33], [0, 41, 0, 2500, 0]
+    c = decode._case(lens, hq, 2, d, 33)
+    want = decode._call(c, doc_starts=docs).float()
+    c["w"][7] = bad
+    got = decode._call(c, doc_starts=docs).float()
+    others = [i for i in range(d) if i != 7]
+    assert not got[1:4].any() and torch.equal(got[:, :, others], want[:, :, others])
+    assert not torch.isfinite(got[[0, 4], :, 7]).any()
+    c["lam"][:] = bad
+    c["bt"][[0, 3]] = -1
+    err = pkv.new_error_word(DEV)
+    got = decode._call(c, error_word=err, doc_starts=[0, 41, 0, 0, 0]).float()
+    assert pkv.read_error(err) == C["PKV_DEV_BAD_BLOCK_ID"]
+    assert not got[:4].any() and not torch.isfinite(got[4]).any()
+    # of many tokens: some rows of an item see nothing, all rows of one, and shares of keys
+    for lens, new in (([100, 64], [100, 3]), ([3000, 700], [2, 200])):
+        c = prefill._case(lens, new, hq, 2, d, 34)
+        pos = np.concatenate([np.arange(L - n, L) for L, n in zip(lens, new)])
+        docs = np.where(np.arange(len(pos)) % 2 == 0, pos + 1, np.maximum(pos - 5, 0))
+        want = prefill._call(c, doc_starts=docs).float()
+        c["w"][7] = bad
+        got = prefill._call(c, doc_starts=docs).float()
+        assert not got[::2].any() and torch.equal(got[:, :, others], want[:, :, others])
+        assert not torch.isfinite(got[1::2, :, 7]).any()
+        assert not prefill._call(c, doc_starts=pos + 1).any()
+        # NaN in V rows past every row's keys, in the blocks that they share, has rows computed again
+        c["pools"][1][int(c["bt"][0, (lens[0] - 1) // 16]), :, (lens[0] - 1) % 16] = float("nan")
+        last = new[0] - 1
+        docs2 = np.where(np.arange(len(pos)) == last, pos + 1, docs)
+        got = prefill._call(c, doc_starts=docs2).float()
+        assert not got[::2].any() and not got[last].any()
