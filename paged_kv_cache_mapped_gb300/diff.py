@@ -8,7 +8,7 @@ import ctypes
 import torch
 
 from ._lib import PkvDiffParams, header_constants, load
-from .step import _bf16_pools, _call, _dims, _give, _like, _need, _new, _opt, _rules
+from .step import _bf16_pools, _call, _dims, _give, _like, _need, _new, _opt, _rules, _sizes
 
 _INPUTS_READY = header_constants()["PKV_DECODE_INPUTS_READY"]
 
@@ -31,7 +31,7 @@ def _params(lambdas, norm_weight, norm_eps, rows, hq, d, dev):
 def diff_decode_workspace_bytes(batch, num_q_heads, num_kv_heads, head_dim, num_blocks, max_blocks_per_seq, *, score_stride=0) -> int:
     """Workspace of paged_diff_decode_attention, or with the scores' row length of paged_diff_decode_attention_scores.
     Zero-filled before its first use."""
-    dims = _dims(batch, num_q_heads, num_kv_heads, head_dim, num_blocks, max_blocks_per_seq)
+    dims = _sizes(batch, num_q_heads, num_kv_heads, head_dim, num_blocks, max_blocks_per_seq)
     stride = int(score_stride)
     n = int(load().pkv_diff_decode_workspace_bytes(dims, stride)) if 0 <= stride < 2**31 else 0
     if n == 0:
@@ -100,7 +100,7 @@ def paged_diff_decode_attention_scores(q, k_cache, v_cache, block_tables, contex
 
 def diff_prefill_workspace_bytes(total_tokens, batch, num_q_heads, num_kv_heads, head_dim, num_blocks, max_blocks_per_seq) -> int:
     """Workspace of paged_diff_prefill_attention for these sizes and at most total_tokens query rows."""
-    dims = _dims(batch, num_q_heads, num_kv_heads, head_dim, num_blocks, max_blocks_per_seq)
+    dims = _sizes(batch, num_q_heads, num_kv_heads, head_dim, num_blocks, max_blocks_per_seq)
     T = int(total_tokens)
     n = int(load().pkv_diff_prefill_workspace_bytes(dims, T)) if 0 <= T < 2**31 else 0
     if n == 0:

@@ -9,7 +9,7 @@ import functools
 import torch
 
 from ._lib import PkvEvictRules, PkvEvictState, load
-from .step import BLOCK_SIZE, _bf16_pools, _call, _dims, _give, _like, _need, _new
+from .step import BLOCK_SIZE, _bf16_pools, _call, _dims, _give, _like, _need, _new, _sizes
 
 
 @functools.lru_cache(maxsize=256)
@@ -28,7 +28,7 @@ def _rules(n_sink, k_top, n_recent, trigger=0):
 
 def evict_workspace_bytes(batch, num_kv_heads, n_sink, k_top, n_recent) -> int:
     """Workspace of kv_evict and kv_evict_q8 for these sizes."""
-    n = int(load().pkv_evict_workspace_bytes(_dims(batch, 1, num_kv_heads, 128, 0, 0), _rules(n_sink, k_top, n_recent)))
+    n = int(load().pkv_evict_workspace_bytes(_sizes(batch, 1, num_kv_heads, 128, 0, 0), _rules(n_sink, k_top, n_recent)))
     if n == 0:
         raise ValueError("invalid sizes for an eviction")
     return n

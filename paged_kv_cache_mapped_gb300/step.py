@@ -6,6 +6,7 @@ from __future__ import annotations
 
 import ctypes
 import functools
+import operator
 
 import torch
 
@@ -65,6 +66,12 @@ def _dims(batch, hq, hkv, d, nb, mb):
             raise ValueError(f"sizes must be within [0, 2**31), got {x}")
     r = PkvDims(batch, hq, hkv, d, BLOCK_SIZE, nb, mb)
     return ctypes.pointer(r)
+
+
+def _sizes(*sizes):
+    """_dims of sizes that a caller names: the record is kept by the numbers (a tensor of one would be kept by its
+    identity, and count as it once was)."""
+    return _dims(*(operator.index(x) for x in sizes))
 
 
 def _new(shape, dtype, like, stream, make=torch.empty):
@@ -242,7 +249,7 @@ def paged_decode_attention_f8(q, k_codes, v_codes, k_scales, v_scales, block_tab
 
 def prefill_workspace_bytes(total_tokens, batch, num_q_heads, num_kv_heads, head_dim, num_blocks, max_blocks_per_seq) -> int:
     """Workspace of paged_prefill_attention for these sizes and at most total_tokens query rows."""
-    dims = _dims(batch, num_q_heads, num_kv_heads, head_dim, num_blocks, max_blocks_per_seq)
+    dims = _sizes(batch, num_q_heads, num_kv_heads, head_dim, num_blocks, max_blocks_per_seq)
     T = int(total_tokens)
     n = int(load().pkv_prefill_workspace_bytes(dims, T)) if 0 <= T < 2**31 else 0
     if n == 0:

@@ -4,7 +4,12 @@ import pytest
 import torch
 
 import paged_kv_cache_mapped_gb300 as pkv
-from paged_kv_cache_mapped_gb300 import evict
+from paged_kv_cache_mapped_gb300 import _build, evict
+
+
+@pytest.fixture(scope="module", autouse=True)
+def _built():
+    _build.build()
 
 
 def _values(*args):
