@@ -35,9 +35,12 @@
 // and one and a half times the products of the plain form, and the same chain of a step bounds it: 4096 tokens on 16384 keys 1355 us
 // (1.07 PFLOP/s, 56 % of the measured bf16 rate; tensor pipe 50 %, issue 52 %, exponentials 30 %); 4 prompts of 3000, d 64, 8 heads with a
 // bias 111 us (tensor pipe 18 %, issue 46 %, exponentials 21 %); 24 mixed sequences 52 us, a chain of plan, loads, few steps and merge.
-// The maps' rounding errors add while their outputs subtract, so the nearest sixth of a longer row's steps takes two terms as well:
-// the error against 64 bits, in that of bf16 outputs alone, is 1.48 (chunk, then 1390 us; no step 1.55, 1327 us; an eighth of them 1.50, 1379 us) and
-// 1.03 (prompts with the bias, whose weights lie near; no step 1.32, 109 us).
+// The maps' rounding errors add while their outputs subtract, so of a longer row's steps one in six, the nearest ones, takes two
+// terms as well.  That is for weights that lie near, where few may carry the row: prompts with the bias have an error against 64 bits,
+// in that of bf16 outputs alone, of 1.02 (no step in two terms 1.32, 109 us).  For keys in no order the one-term part of
+// the error falls only as the root of the steps left: 1.48 (chunk, 1390 us when it was measured; no step 1.55, 1327 us; an eighth
+// of them 1.50, 1379 us; all would cost some 25 %), 4 % of error for 5 % of time.  Which of the two a call is is not known before its scores,
+// so the share is one for all rules, and a sixth is no optimum of either.
 // Non-finite V: a masked key's weight is 0, and 0 * NaN is NaN, so V rows past the sequence are cleared,
 // and an output row that owes a NaN to a masked key is computed again over what it sees.
 // Every wait is bounded; bad block ids are cleared tiles, recorded.
@@ -704,11 +707,15 @@ __device__ __forceinline__ Steps steps_of(const PrefillAttnArgs& a, const Item& 
   return Steps{min(w.ns - 1, (e_last - e_base) >> 2), max(0, (e_first - e_base) >> 2)};
 }
 
-// The step of this share from which on weights are two bf16 terms (see the header).
+// The step of this share from which on weights are two bf16 terms (see the header).  DIFF: counted back from the step of
+// the first row's own position, so that every row of the item has them on the share's keys nearest to it, wherever
+// the item ends in its last tile.
 template <bool DIFF>
 __device__ __forceinline__ int two_terms_from(const Item& w) {
   if (w.nt_all <= kTwoTermTiles) return 0;
-  return DIFF ? 2 * (w.nt_all - w.ts) - (2 * w.nt_all + kTwoTermShare - 2) / kTwoTermShare : 0x7fffffff;
+  if constexpr (!DIFF) return 0x7fffffff;
+  const int own = ((w.pos0 >> 4) - w.shift) / kStepBlocks, steps = (w.nblk + kStepBlocks - 1) / kStepBlocks;
+  return own + 1 - (steps + kTwoTermShare - 1) / kTwoTermShare - w.ts * (kTileBlocks / kStepBlocks);
 }
 
 template <int D, int NT, bool DIFF = false>
