@@ -68,7 +68,8 @@ size_t pkv_evict_workspace_bytes(const pkv_dims* dims, const pkv_evict_rules* ru
  *      sequence that is left alone).
  *   5. Blocks ceil(budget / 16) .. ceil(L_b / 16) - 1 of the sequence are pushed on the free stack, in the order of
  *      (b, table entry).  block_tables itself is not changed.
- * The token that follows has position L_b + dropped[b], and attention without position rules over the
+ * The token that follows has position L_b + dropped[b] (pkv_kv_step_tables numbers slots: a model that wants a token's
+ * position adds dropped[b] to its `positions`), and attention without position rules over the
  * shrunk cache is that over the kept tokens (slots are in no order, so a window or a distance bias over slots has
  * no meaning).  No block of a shrinking sequence may belong to another one too.
  *   k_cache, v_cache : [NB, Hkv, 16, d] bf16, changed in place.
@@ -83,7 +84,7 @@ size_t pkv_evict_workspace_bytes(const pkv_dims* dims, const pkv_evict_rules* ru
  *   error_word       : PKV_DEV_BAD_CONTEXT_LEN (a length outside its table, past `stride` or past
  *                      PKV_MAX_EVICT_TOKENS, dropped < 0 or a length with it past 32 bits: the sequence is left alone,
  *                      without copies), PKV_DEV_BAD_SCORE
- *                      (a NaN, which counts as the lowest score), PKV_DEV_BAD_BLOCK_ID (a block outside the pool
+ *                      (a NaN of an unprotected token of a sequence that shrinks; it counts as the lowest score), PKV_DEV_BAD_BLOCK_ID (a block outside the pool
  *                      among those a row moves from or to -- the row is not moved -- or that would be pushed -- it
  *                      is not), PKV_DEV_NO_BLOCKS (a free count outside the stack: nothing is pushed; or a full
  *                      stack: the blocks past it are not pushed).

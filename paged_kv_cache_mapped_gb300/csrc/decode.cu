@@ -57,9 +57,9 @@
 //    the two maps of each fill columns that the plain form leaves empty, with no product more, and bytes bound
 //    it as they do that (32 of ~4000, 32 / 8 heads, d 128: 87 us, 6.1 TB/s, 78 % of peak DRAM; with eight
 //    columns of heads and second accumulators 90.3; 4 of 131072: 311 us, 6.9 TB/s).  Five to eight heads need
-//    those second accumulators: 210 registers, eight resident CTAs an SM instead of twelve (8 heads, 32 of
+//    those second accumulators: 214 registers, eight resident CTAs an SM instead of twelve (8 heads, 32 of
 //    ~4000: 91.4 us; held to twelve CTAs' registers 94.8; 6 heads on windows of 1000 keys, 64 sequences:
-//    22.4 us, the fixed cost of a call).  Weights added into scores write and read 8 bytes a key and head
+//    22.5-22.7 us, the fixed cost of a call).  Weights added into scores write and read 8 bytes a key and head
 //    (16 of ~4000: 56.2 us).
 //  * Online softmax ("How KV Sparsity...", section "2. Attention modification", Fig. 7:
 //    running max, running sum, rescale, divide at the end) in base 2 with log2(e) folded

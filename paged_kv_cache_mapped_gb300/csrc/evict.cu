@@ -588,7 +588,8 @@ __device__ __forceinline__ void select_row(const EvictArgs& a, int bg, int upto,
 }
 
 // A CTA or cluster a row; or, MANY, few clusters that take the rows of more than `above` slots in turn.  (Apart: in the loop
-// the compiler keeps the arguments in registers, which the CTA a row has no room for: 32 x 4000 tokens 72 us against 66.)
+// the compiler keeps the arguments in registers, which the CTA a row has no room for: 32 x 4000 tokens 72 us against 66.
+// Held to 64 registers, 1024 threads a CTA, MANY spills 172 bytes a thread, the clusters without it 12, the CTA a row none.)
 template <bool CLUSTER, bool MANY>
 __global__ void __launch_bounds__(kEvictMaxThreads, 1) evict_select_kernel(const __grid_constant__ EvictArgs a, int above, int upto) {
   extern __shared__ __align__(16) uint32_t s_keys[];
@@ -753,8 +754,8 @@ __global__ void __launch_bounds__(kMoveThreads, CTAS) evict_move_kernel(const __
 constexpr int kShortSlots = 16384;  // of a row that a CTA takes where there are many: three CTAs' keys an SM
 
 // `longest`: slots of a row at most, which the tables' width gives, not the sequences' lengths.  With few pairs a
-// launch has clusters of as many CTAs a row as the SMs hold at once, of 4096 slots at least (4 x 8 rows of 65536: select
-// kernel 203 us with a CTA a row, 33 with four).  With many and wide tables one launch has a CTA for each row of up to
+// launch has clusters of as many CTAs a row as the SMs hold at once, of 4096 slots at least (a call for 4 x 8 rows of 32768, the
+// longest that one CTA takes, cut to 4096: 51 us with a CTA a row, 45 with two, 40 with the four of this rule).  With many and wide tables one launch has a CTA for each row of up to
 // kShortSlots, and another few clusters that take the longer ones in turn (256 sequences of 1800 INT8 tokens, 8 heads: 89 us in tables
 // of 1920 slots, 114 in ones of 131072).
 // Threads: as many as leave all CTAs on the SMs at once (64 registers each), of eight slots at least.
@@ -797,7 +798,8 @@ cudaError_t launch_select(const EvictArgs& a, int pairs, int longest, int sms, c
 
 // bf16: five CTAs an SM where the kept rows behind the budget lie far apart, fewer than four of a block (4 sequences of 65536 cut
 // to 8191: 74-77 us, 78-81 with four), and four where they lie close (32 of ~4000 cut to 1540: 64.8 us, 66.4 with
-// five).  The tables' width stands for the lengths.  INT8: four (256 of 1800 in tables of 131072 slots, which say
+// five).  The border lies somewhere between these two points, and the tables' width stands for the lengths, which the host
+// does not know: short sequences in wide tables get five, which costs the 2 % above.  INT8: four (256 of 1800 in tables of 131072 slots, which say
 // far apart: 114 us, 118 with five).
 const void* move_kernel(bool q8, int head_dim, bool apart) {
   if (q8) return head_dim == 128 ? (const void*)evict_move_kernel<128, true, 4> : (const void*)evict_move_kernel<64, true, 4>;

@@ -32,14 +32,15 @@
 // Differential attention (DIFF): out = sum_t (a_1,t - lambda a_2,t) V_t and a norm, the maps from the halves of q and K.  An
 // item's two row tiles are the two maps of the same 128 rows, so a CTA's K and V tiles serve both, each map's S takes
 // half the products, and the difference is made from the two outputs in tensor memory at the item's end.  Twice the exponentials
-// and one and a half times the products of the plain form, and the same chain of a step bounds it: 4096 tokens on 16384 keys 1355 us
-// (1.07 PFLOP/s, 56 % of the measured bf16 rate; tensor pipe 50 %, issue 52 %, exponentials 30 %); 4 prompts of 3000, d 64, 8 heads with a
-// bias 111 us (tensor pipe 18 %, issue 46 %, exponentials 21 %); 24 mixed sequences 52 us, a chain of plan, loads, few steps and merge.
+// and one and a half times the products of the plain form, and the same chain of a step takes the time, no unit being full: 4096
+// tokens on 16384 keys 1353 us (6 d operations a visible key, head and row, as two softmaxes need: 1.07 PFLOP/s, 56 % of the measured
+// bf16 rate; 4 d, as one weight would: 0.71; tensor pipe 50 %, issue 52 %, exponentials 30 %); 4 prompts of 3000, d 64, 8 heads with a bias
+// 112-114 us (tensor pipe 18 %, issue 46 %, exponentials 21 %); 24 mixed sequences 52 us, a chain of plan, loads, few steps and merge.
 // The maps' rounding errors add while their outputs subtract, so of a longer row's steps one in six, the nearest ones, takes two
 // terms as well.  That is for weights that lie near, where few may carry the row: prompts with the bias have an error against 64 bits,
 // in that of bf16 outputs alone, of 1.02 (no step in two terms 1.32, 109 us).  For keys in no order the one-term part of
 // the error falls only as the root of the steps left: 1.48 (chunk, 1390 us when it was measured; no step 1.55, 1327 us; an eighth
-// of them 1.50, 1379 us; all would cost some 25 %), 4 % of error for 5 % of time.  Which of the two a call is is not known before its scores,
+// of them 1.50, 1379 us; all of them 1.00, 1707 us, and the prompts 133 us), 4 % of error for 5 % of time.  Which of the two a call is is not known before its scores,
 // so the share is one for all rules, and a sixth is no optimum of either.
 // Non-finite V: a masked key's weight is 0, and 0 * NaN is NaN, so V rows past the sequence are cleared,
 // and an output row that owes a NaN to a masked key is computed again over what it sees.
@@ -134,6 +135,8 @@ struct Geo {
 //  * P >= slots: entries above one and a half times the fair share W / slots are cut to that.  If there are
 //    none, the last P mod slots items, which would leave most CTAs idle for a whole item, are cut in s shares each (chunk of 4096 on 16384,
 //    512 items on 152 CTAs: 56 items in two shares, capped 0.99 -> 0.87 ms).
+// The constants were measured with the plain form.  The differential one, with two partial rows a row and other steps, is
+// planned with the same, not with its own.
 // The shares of split entries number at most 2 slots, which bounds the partial rows.  The list has the entries
 // with more than half of ktmax first, a sequence's last rows first within either part.
 struct Entry {

@@ -84,7 +84,8 @@ def kv_evict(k_cache, v_cache, block_tables, context_lens, scores, slot_pos, dro
     others of highest accumulated weight stay, and kept rows behind the budget move into the places of evicted ones.
     scores [B, Hkv, S] fp32 and slot_pos [B, Hkv, S] int32 (the position of each slot's token, -1: in order,
     slot + dropped[b]) go with them, in place unless scores_out / slot_pos_out are given.  dropped [B] int32
-    counts the tokens lost.  With free_blocks [NB] and free_count [1] (the stack of kv_step_tables) the blocks
+    counts the tokens lost; the positions of kv_step_tables are slots, to which dropped[b] adds up to a later token's own
+    position.  With free_blocks [NB] and free_count [1] (the stack of kv_step_tables) the blocks
     behind the budget are pushed.  Returns (context_lens_out [B], dropped_out [B], free_count_out [1] or None); the
     outputs may be the inputs themselves."""
     nb, hkv, d, dev, kp, vp = _bf16_pools(k_cache, v_cache)
